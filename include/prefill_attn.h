@@ -248,6 +248,152 @@ pa_status prefill_attn_varlen_ex(
     float scale, int causal, const pa_options *opts, pa_stream_t stream);
 
 /*
+ * prefill_attn_varlen_sinks -- windowed attention with sink tokens.
+ *
+ * prefill_attn_varlen_ex (causal = 1) under a sliding window W =
+ * pa_options.window >= 1, except that the first sink_tokens keys of each
+ * sequence stay visible: the query at absolute position p sees key j when
+ * j <= p and (j > p - W or j < sink_tokens).  sink_tokens = 0 is the plain
+ * window.  Every option of pa_options applies but wait_timeout_test.  Only the
+ * tiles of 128 keys that hold a visible key are read -- whole, so every row of
+ * [0, cache_offsets[b]) must hold finite values (and, in a paged cache, every
+ * table entry there must name a block of the pool), even rows that no query
+ * sees any more.  A few long rows are split along their keys and joined: then
+ * three kernels run instead of two, and the partial results (fp32, at most
+ * 64 MiB) live in the per-stream workspace.  Under graph capture the stream
+ * must already have run a call of at least these sizes.
+ */
+pa_status prefill_attn_varlen_sinks(
+    const void *q, const void *k, const void *v,
+    const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+    void *cache_k, void *cache_v, const int32_t *cache_offsets,
+    void *out, float *lse,
+    int num_seqs, int total_q, int max_cache_len,
+    int n_heads, int n_kv_heads, int head_dim,
+    float scale, int sink_tokens, const pa_options *opts, pa_stream_t stream);
+
+/*
+ * A prefix that every sequence of a call shares (a system prompt, a document):
+ * len tokens whose keys and values exist once.
+ *   contiguous cache: k and v [n_kv_heads, capacity, head_dim] bf16, 16-byte
+ *     aligned, rows [0, len) used (len <= capacity); with kv_quant = 1 int8
+ *     codes, and k_scale / v_scale fp32 [n_kv_heads, capacity].
+ *   paged cache (pa_options.block_table): block_table, a device array of int32
+ *     [ceil(len / block_size)], names the prefix's blocks in the call's own
+ *     pools (and scale pools); the other fields are ignored.
+ * Zero-initialise it and set struct_size = sizeof(pa_prefix).
+ */
+typedef struct pa_prefix {
+    uint32_t struct_size;
+    int32_t len;
+    const void *k;
+    const void *v;
+    int32_t capacity;
+    int32_t reserved;  /* must be 0 */
+    const float *k_scale;
+    const float *v_scale;
+    const int32_t *block_table;
+} pa_prefix;
+
+/*
+ * prefill_attn_varlen_prefix -- attention for a batch that shares a prefix.
+ *
+ * prefill_attn_varlen_ex where the keys of every sequence are the prefix's len
+ * tokens, then its own cache_offsets[b] cached tokens, then its new ones
+ * (causal among its own; the whole prefix is visible to every query).
+ * cu_seqlens_k, cache_offsets and max_cache_len count a sequence's OWN tokens
+ * only; the new K/V are written to its own cache at cache_offsets[b].  With
+ * rope_theta > 0 the new q and k are rotated to position len +
+ * cache_offsets[b] + i.  The prefix's K/V are read once for a block of the
+ * whole batch's queries, not once per sequence, and the two parts are joined
+ * by their log-sum-exp (partial results in fp32 in the per-stream workspace:
+ * up to 64 MiB, and at least two times total_q * n_heads * (head_dim + 1) * 4
+ * bytes).  Every option of pa_options applies but window and
+ * wait_timeout_test.  len = 0 is prefill_attn_varlen_ex.  A prefix block
+ * outside the pool rejects the whole call on the device
+ * (PA_DEVERR_METADATA, nothing written).  Under graph capture the stream must
+ * already have run a call of at least these sizes.
+ */
+pa_status prefill_attn_varlen_prefix(
+    const void *q, const void *k, const void *v,
+    const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+    void *cache_k, void *cache_v, const int32_t *cache_offsets,
+    void *out, float *lse,
+    int num_seqs, int total_q, int max_cache_len,
+    int n_heads, int n_kv_heads, int head_dim,
+    float scale, int causal, const pa_prefix *prefix, const pa_options *opts, pa_stream_t stream);
+
+/*
+ * prefill_attn_key_weights -- the attention weight that each key collects.
+ *
+ *   weights[row of key j of (b, h)]  (+)=  sum over the new queries i of b and
+ *       the query heads g of KV head h of exp(scale * q_{i,g} . k_j - lse_{i,g})
+ * over the queries that see key j.  With lse from the attention call of the
+ * same step the terms are that call's softmax probabilities.  Keys
+ * [0, cache_offsets[b]) are read from cache_k and their weights added to; the
+ * new tokens' keys are read from k and their weights set.  The call neither
+ * reads nor writes anything else, so it may run before or after the attention
+ * call has written the cache.
+ *
+ *   weights      one fp32 per cached (token, KV head): [num_seqs, n_kv_heads,
+ *                max_cache_len], or [num_blocks, n_kv_heads, block_size] with a
+ *                block_table; 4-byte aligned.
+ *   lse          [total_q, n_heads] fp32, not NULL.
+ *   sink_tokens  as in prefill_attn_varlen_sinks (needs a window); 0: none.
+ *   prefix_len   tokens of a shared prefix ahead of the sequences; it only moves
+ *                the rotary positions (the prefix's own keys get no weights).
+ *   opts         window, block_table, rope_theta, kv_quant with cache_k_scale
+ *                (cache_v_scale must be set too, and is not read).
+ * The sums are fp32, each key's by one thread block in a fixed order, so equal
+ * inputs give equal bits.  A sequence with inconsistent metadata is skipped
+ * (PA_DEVERR_METADATA).  Other arguments as in prefill_attn_varlen.
+ */
+pa_status prefill_attn_key_weights(
+    const void *q, const void *k,
+    const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+    const void *cache_k, const int32_t *cache_offsets,
+    const float *lse, float *weights,
+    int num_seqs, int total_q, int max_cache_len,
+    int n_heads, int n_kv_heads, int head_dim,
+    float scale, int causal, int sink_tokens, int prefix_len,
+    const pa_options *opts, pa_stream_t stream);
+
+/*
+ * prefill_attn_evict -- cuts each (sequence, KV head) of a cache back to
+ * `budget` tokens by weight, in place.
+ *
+ * A sequence of lengths[b] > budget cached tokens keeps its first sink_tokens,
+ * its last recent_tokens and, of those between, the budget - sink_tokens -
+ * recent_tokens with the largest weight (equal weights: the lowest position
+ * first; NaN ranks above every number).  Each KV head chooses for itself.  The
+ * kept rows of K and V (and the int8 cache's scales) move to positions 0 ..
+ * budget - 1 in their old order; rows from there on are left as they were.  A
+ * sequence of at most budget tokens keeps them all.
+ *
+ *   cache_k/v     as in prefill_attn_varlen (bf16), or int8 with kv_quant = 1 and
+ *                 both scales; pools with a block_table.  Sequences of a paged
+ *                 call must not share blocks.
+ *   weights       one fp32 per cached row, laid out as in prefill_attn_key_weights.
+ *   lengths       [num_seqs] int32: cached tokens.
+ *   kept_lengths  [num_seqs] int32 out: min(lengths[b], budget); must not
+ *                 overlap lengths.
+ *   kept_index    [num_seqs, n_kv_heads, budget] int32 out or NULL: the kept
+ *                 positions, ascending, -1 past the last.
+ *   kept_weights  out or NULL: the kept weights, moved like the rows; weights
+ *                 itself, or memory that does not overlap it.
+ * A sequence whose length is outside [0, max_cache_len], or that names a block
+ * outside the pool, is skipped (PA_DEVERR_METADATA, nothing of it written).
+ * Evicted caches keep their order but not their positions: a caller with
+ * rotary embeddings rotates later tokens itself (rope_theta = 0 in the calls).
+ */
+pa_status prefill_attn_evict(
+    void *cache_k, void *cache_v, const float *weights, const int32_t *lengths,
+    int32_t *kept_lengths, int32_t *kept_index, float *kept_weights,
+    int num_seqs, int max_cache_len, int n_kv_heads, int head_dim,
+    int budget, int sink_tokens, int recent_tokens,
+    const pa_options *opts, pa_stream_t stream);
+
+/*
  * prefill_attn_varlen_noalloc -- prefill_attn_varlen that allocates nothing.
  * The pages have no counterpart to this call; it exists for integration.
  *

@@ -31,6 +31,13 @@ class PaOptions(ctypes.Structure):
                 ("wait_timeout_test", ctypes.c_int32), ("schedule", ctypes.c_int32)]
 
 
+class PaPrefix(ctypes.Structure):
+    """pa_prefix of include/prefill_attn.h."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("len", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("capacity", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
+
+
 # Entry points declared in include/prefill_attn.h: name -> (restype, argtypes)
 _P, _I, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 _VARLEN_ARGS = [_P] * 10 + [_I] * 6 + [_F, _I, _P]
@@ -40,6 +47,11 @@ SIGNATURES = {
     "prefill_attn_varlen_validate": (_I, _VARLEN_ARGS),
     "prefill_attn_varlen_noalloc": (_I, _VARLEN_ARGS),
     "prefill_attn_varlen_ex": (_I, _VARLEN_EX_ARGS),
+    "prefill_attn_varlen_sinks": (_I, [_P] * 10 + [_I] * 6 + [_F, _I, ctypes.POINTER(PaOptions), _P]),
+    "prefill_attn_varlen_prefix": (_I, [_P] * 10 + [_I] * 6 + [_F, _I, ctypes.POINTER(PaPrefix),
+                                                              ctypes.POINTER(PaOptions), _P]),
+    "prefill_attn_key_weights": (_I, [_P] * 8 + [_I] * 6 + [_F, _I, _I, _I, ctypes.POINTER(PaOptions), _P]),
+    "prefill_attn_evict": (_I, [_P] * 7 + [_I] * 7 + [ctypes.POINTER(PaOptions), _P]),
     "prefill_attn_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_int32)]),
     "prefill_attn_release": (None, []),
     "prefill_attn_status_string": (ctypes.c_char_p, [_I]),
@@ -158,6 +170,23 @@ def make_options(window: int = 0, block_table=None, block_size: int = 0, num_blo
     return o
 
 
+def _cache_args(cache_k, block_table, cache_k_scale, cache_v_scale):
+    """Checks the cache options; returns (slot capacity of a paged cache or None, whether the cache is int8)."""
+    cap = None
+    if block_table is not None:
+        if block_table.dtype != torch.int32 or not block_table.is_cuda or not block_table.is_contiguous() \
+                or block_table.dim() != 2:
+            raise ValueError("block_table must be a contiguous 2-D CUDA int32 tensor")
+        cap = block_table.shape[1] * cache_k.shape[2]
+    quant = cache_k_scale is not None or cache_v_scale is not None
+    if quant:
+        for name, t in (("cache_k_scale", cache_k_scale), ("cache_v_scale", cache_v_scale)):
+            if t is None or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() \
+                    or tuple(t.shape) != tuple(cache_k.shape[:-1]):
+                raise ValueError(f"{name} must be a contiguous CUDA float32 tensor of shape cache.shape[:-1]")
+    return cap, quant
+
+
 def prefill_attn_varlen_ex(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse=None, *,
                            scale: Optional[float] = None, causal: bool = True, window: int = 0,
                            block_table=None, rope_theta: float = 0.0, cache_k_scale=None, cache_v_scale=None,
@@ -178,24 +207,182 @@ def prefill_attn_varlen_ex(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v
     splitting their KV tiles between the two slots, 2 two-tile units, 3
     two-tile units with single-tile ones split; 0 = the library's choice).
     """
-    cap = None
-    if block_table is not None:
-        if block_table.dtype != torch.int32 or not block_table.is_cuda or not block_table.is_contiguous() \
-                or block_table.dim() != 2:
-            raise ValueError("block_table must be a contiguous 2-D CUDA int32 tensor")
-        cap = block_table.shape[1] * cache_k.shape[2]
-    quant = cache_k_scale is not None or cache_v_scale is not None
-    if quant:
-        for name, t in (("cache_k_scale", cache_k_scale), ("cache_v_scale", cache_v_scale)):
-            if t is None or t.dtype != torch.float32 or not t.is_cuda or not t.is_contiguous() \
-                    or tuple(t.shape) != tuple(cache_k.shape[:-1]):
-                raise ValueError(f"{name} must be a contiguous CUDA float32 tensor of shape cache.shape[:-1]")
+    cap, quant = _cache_args(cache_k, block_table, cache_k_scale, cache_v_scale)
     args = _varlen_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse,
                         scale, causal, stream, max_cache_len=cap,
                         cache_dtype=torch.int8 if quant else torch.bfloat16)
     opts = make_options(window, block_table, cache_k.shape[2], cache_k.shape[0], rope_theta,
                         cache_k_scale, cache_v_scale, wait_timeout_test, schedule)
     _check(load().prefill_attn_varlen_ex(*args[:-1], ctypes.byref(opts), args[-1]))
+
+
+def _cuda_tensor(name, t, dtype, shape=None):
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _check_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table):
+    """Shapes that must agree (the long-context calls check them; v, cache_v, out and lse may be None)."""
+    if q.dim() != 3 or k.dim() != 3 or cache_k.dim() != 4:
+        raise ValueError("q/k/v are [total_q, heads, head_dim]; caches are [num_seqs, kv_heads, cap, head_dim]")
+    (t, h, d), hk, b = q.shape, k.shape[1], cache_offsets.numel()
+    slots = cache_k.shape[0] if block_table is not None else b
+    for name, x, shape in (("k", k, (t, hk, d)), ("v", v, (t, hk, d)), ("out", out, (t, h, d)), ("lse", lse, (t, h)),
+                           ("cache_k", cache_k, (slots, hk, cache_k.shape[2], d)), ("cache_v", cache_v, cache_k.shape),
+                           ("cu_seqlens_q", cu_seqlens_q, (b + 1,)), ("cu_seqlens_k", cu_seqlens_k, (b + 1,)),
+                           ("cache_offsets", cache_offsets, (b,))):
+        if x is not None and tuple(x.shape) != tuple(shape):
+            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    if block_table is not None and block_table.shape[0] != b:
+        raise ValueError(f"block_table must have {b} rows")
+    same_device(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table)
+
+
+def same_device(*tensors):
+    """Every tensor on one device, the current one (the library launches there)."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), not {t.device}")
+
+
+def prefill_attn_varlen_sinks(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse=None, *,
+                              window: int, sink_tokens: int, scale: Optional[float] = None, block_table=None,
+                              rope_theta: float = 0.0, cache_k_scale=None, cache_v_scale=None, schedule: int = 0,
+                              stream=None) -> None:
+    """Causal attention under a sliding window whose first `sink_tokens` keys stay visible.
+
+    The query at absolute position p sees key j when j <= p and (j > p - window or
+    j < sink_tokens).  Tensors and options as in prefill_attn_varlen_ex.
+    """
+    cap, quant = _cache_args(cache_k, block_table, cache_k_scale, cache_v_scale)
+    args = _varlen_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, scale, True,
+                        stream, max_cache_len=cap, cache_dtype=torch.int8 if quant else torch.bfloat16)
+    _check_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table)
+    opts = make_options(window, block_table, cache_k.shape[2], cache_k.shape[0], rope_theta, cache_k_scale,
+                        cache_v_scale, schedule=schedule)
+    _check(load().prefill_attn_varlen_sinks(*args[:-2], int(sink_tokens), ctypes.byref(opts), args[-1]))
+
+
+def prefill_attn_varlen_prefix(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse=None, *,
+                               prefix_k=None, prefix_v=None, prefix_len: Optional[int] = None, prefix_table=None,
+                               prefix_k_scale=None, prefix_v_scale=None, scale: Optional[float] = None,
+                               causal: bool = True, block_table=None, rope_theta: float = 0.0, cache_k_scale=None,
+                               cache_v_scale=None, schedule: int = 0, stream=None) -> None:
+    """Attention for a batch whose sequences all start with the same prefix, read once.
+
+    Contiguous cache: prefix_k / prefix_v [n_kv_heads, capacity, head_dim] hold the prefix's
+    keys and values in their first prefix_len rows (default: all of them), with fp32
+    prefix_k_scale / prefix_v_scale [n_kv_heads, capacity] for an int8 cache.  Paged cache:
+    prefix_table (int32 CUDA, one entry per block) names the prefix's blocks in the pools,
+    and prefix_len its tokens.  cu_seqlens_k and cache_offsets count each sequence's own
+    tokens, which follow the prefix.
+    """
+    cap, quant = _cache_args(cache_k, block_table, cache_k_scale, cache_v_scale)
+    dtype = torch.int8 if quant else torch.bfloat16
+    args = _varlen_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, scale, causal,
+                        stream, max_cache_len=cap, cache_dtype=dtype)
+    _check_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table)
+    pre = PaPrefix()
+    pre.struct_size = ctypes.sizeof(PaPrefix)
+    if block_table is not None:
+        if prefix_table is None or prefix_len is None:
+            raise ValueError("a paged cache needs prefix_table and prefix_len")
+        _cuda_tensor("prefix_table", prefix_table, torch.int32)
+        if prefix_len > prefix_table.numel() * cache_k.shape[2]:
+            raise ValueError("prefix_table has fewer blocks than prefix_len needs")
+        same_device(prefix_table)
+        pre.block_table = prefix_table.data_ptr()
+    else:
+        if prefix_k is None or prefix_v is None:
+            raise ValueError("a contiguous cache needs prefix_k and prefix_v")
+        _cuda_tensor("prefix_k", prefix_k, dtype)
+        if prefix_k.dim() != 3 or prefix_k.shape[0] != k.shape[1] or prefix_k.shape[2] != q.shape[2]:
+            raise ValueError("prefix_k is [n_kv_heads, capacity, head_dim]")
+        _cuda_tensor("prefix_v", prefix_v, dtype, prefix_k.shape)
+        same_device(prefix_k, prefix_v, prefix_k_scale, prefix_v_scale)
+        pre.k, pre.v, pre.capacity = prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_k.shape[1]
+        if prefix_len is None:
+            prefix_len = prefix_k.shape[1]
+        if quant:
+            for name, t in (("prefix_k_scale", prefix_k_scale), ("prefix_v_scale", prefix_v_scale)):
+                if t is None:
+                    raise ValueError(f"an int8 cache needs {name}")
+                _cuda_tensor(name, t, torch.float32, prefix_k.shape[:2])
+            pre.k_scale, pre.v_scale = prefix_k_scale.data_ptr(), prefix_v_scale.data_ptr()
+    pre.len = int(prefix_len)
+    opts = make_options(0, block_table, cache_k.shape[2], cache_k.shape[0], rope_theta, cache_k_scale, cache_v_scale,
+                        schedule=schedule)
+    _check(load().prefill_attn_varlen_prefix(*args[:-1], ctypes.byref(pre), ctypes.byref(opts), args[-1]))
+
+
+def prefill_attn_key_weights(q, k, cu_seqlens_q, cu_seqlens_k, cache_k, cache_offsets, lse, weights, *,
+                             scale: Optional[float] = None, causal: bool = True, window: int = 0, sink_tokens: int = 0,
+                             prefix_len: int = 0, block_table=None, rope_theta: float = 0.0, cache_k_scale=None,
+                             stream=None) -> None:
+    """Adds to `weights` the softmax probability that each cached key gets from the new queries.
+
+    weights: fp32, shape cache_k.shape[:-1].  Keys already cached are added to, the new tokens'
+    keys are set.  lse is what the attention call of the same step wrote; the other arguments
+    are those of that call (prefix_len: its shared prefix, for the rotary positions).
+    """
+    cap, quant = _cache_args(cache_k, block_table, cache_k_scale, cache_k_scale)
+    dtype = torch.int8 if quant else torch.bfloat16
+    for name, t, dt in (("q", q, torch.bfloat16), ("k", k, torch.bfloat16), ("cache_k", cache_k, dtype),
+                        ("cu_seqlens_q", cu_seqlens_q, torch.int32), ("cu_seqlens_k", cu_seqlens_k, torch.int32),
+                        ("cache_offsets", cache_offsets, torch.int32), ("lse", lse, torch.float32)):
+        _cuda_tensor(name, t, dt)
+    _check_shapes(q, k, None, cu_seqlens_q, cu_seqlens_k, cache_k, None, cache_offsets, None, lse, block_table)
+    _cuda_tensor("weights", weights, torch.float32, cache_k.shape[:-1])
+    same_device(weights, cache_k_scale)
+    total_q, n_heads, head_dim = q.shape
+    if scale is None:
+        scale = head_dim ** -0.5
+    opts = make_options(window, block_table, cache_k.shape[2], cache_k.shape[0], rope_theta, cache_k_scale,
+                        cache_k_scale)
+    _check(load().prefill_attn_key_weights(
+        q.data_ptr(), k.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cache_k.data_ptr(),
+        cache_offsets.data_ptr(), lse.data_ptr(), weights.data_ptr(), cache_offsets.numel(), total_q,
+        cache_k.shape[2] if cap is None else cap, n_heads, k.shape[1], head_dim, float(scale), int(bool(causal)),
+        int(sink_tokens), int(prefix_len), ctypes.byref(opts), _stream_handle(stream, q.get_device())))
+
+
+def prefill_attn_evict(cache_k, cache_v, weights, lengths, kept_lengths, kept_index=None, kept_weights=None, *,
+                       budget: int, sink_tokens: int = 0, recent_tokens: int = 0, block_table=None, cache_k_scale=None,
+                       cache_v_scale=None, stream=None) -> None:
+    """Cuts every (sequence, KV head) of the cache back to `budget` tokens by weight, in place.
+
+    The first sink_tokens and the last recent_tokens stay, the heaviest of the rest fill the
+    budget (ties: the lowest position); kept rows move to the front in their old order.
+    lengths / kept_lengths int32 [num_seqs]; kept_index int32 [num_seqs, n_kv_heads, budget] or
+    None; weights / kept_weights fp32 of shape cache_k.shape[:-1] (kept_weights may be weights).
+    """
+    cap, quant = _cache_args(cache_k, block_table, cache_k_scale, cache_v_scale)
+    dtype = torch.int8 if quant else torch.bfloat16
+    if cache_k.dim() != 4:
+        raise ValueError("caches are [num_seqs, kv_heads, cap, head_dim]")
+    b, hk = lengths.numel(), cache_k.shape[1]
+    _cuda_tensor("cache_k", cache_k, dtype, (b, *cache_k.shape[1:]) if block_table is None else None)
+    _cuda_tensor("cache_v", cache_v, dtype, cache_k.shape)
+    _cuda_tensor("weights", weights, torch.float32, cache_k.shape[:-1])
+    _cuda_tensor("lengths", lengths, torch.int32, (b,))
+    _cuda_tensor("kept_lengths", kept_lengths, torch.int32, (b,))
+    if block_table is not None and block_table.shape[0] != b:
+        raise ValueError(f"block_table must have {b} rows")
+    if kept_index is not None:
+        _cuda_tensor("kept_index", kept_index, torch.int32, (b, hk, budget))
+    if kept_weights is not None:
+        _cuda_tensor("kept_weights", kept_weights, torch.float32, cache_k.shape[:-1])
+    same_device(cache_k, cache_v, weights, lengths, kept_lengths, kept_index, kept_weights, block_table, cache_k_scale,
+                cache_v_scale)
+    opts = make_options(0, block_table, cache_k.shape[2], cache_k.shape[0], 0.0, cache_k_scale, cache_v_scale)
+    _check(load().prefill_attn_evict(
+        cache_k.data_ptr(), cache_v.data_ptr(), weights.data_ptr(), lengths.data_ptr(), kept_lengths.data_ptr(),
+        None if kept_index is None else kept_index.data_ptr(), None if kept_weights is None else kept_weights.data_ptr(),
+        b, cache_k.shape[2] if cap is None else cap, hk, cache_k.shape[3], int(budget), int(sink_tokens),
+        int(recent_tokens), ctypes.byref(opts), _stream_handle(stream, cache_k.get_device())))
 
 
 def prefill_attn_varlen_noalloc(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out,

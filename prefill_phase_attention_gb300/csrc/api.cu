@@ -45,10 +45,23 @@ struct Workspace {
     int max_seqs = 0;
     void* rope = nullptr;  // rotated q/k copies (grown on demand)
     size_t rope_bytes = 0;
+    void* aux = nullptr;   // lists and partial results of the long-context calls (grown on demand)
+    size_t aux_bytes = 0;
+    bool captured = false;  // a captured graph holds these addresses: outgrown blocks are kept, not freed
 };
 
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
+std::vector<std::pair<int, void*>> g_retired;  // (device, block) outgrown but held by a captured graph
+
+// Gives up a block of a workspace that has been replaced by a larger one.
+void drop_block(const Workspace& w, int dev, void* ptr, cudaStream_t st) {
+    if (!ptr) return;
+    if (w.captured)
+        g_retired.emplace_back(dev, ptr);
+    else
+        cudaFreeAsync(ptr, st);
+}
 
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
@@ -79,6 +92,7 @@ pa_status get_workspace(int dev, cudaStream_t st, int num_seqs, int max_units, W
     std::lock_guard<std::mutex> lock(g_mu);
     Workspace& w = g_ws[std::make_pair(dev, st)];
     if (w.ptr && w.max_seqs >= num_seqs && w.max_units >= max_units) {
+        if (!w.captured && capturing(st)) w.captured = true;
         *out = &w;
         return PA_OK;
     }
@@ -100,16 +114,19 @@ pa_status get_workspace(int dev, cudaStream_t st, int num_seqs, int max_units, W
         cudaFreeAsync(nw.ptr, st);
         return cuda_fail(e, "workspace init");
     }
-    if (w.ptr) cudaFreeAsync(w.ptr, st);
-    nw.rope = w.rope;  // the rotary scratch is grown on its own
+    drop_block(w, dev, w.ptr, st);
+    nw.captured = w.captured;
+    nw.rope = w.rope;  // the rotary and auxiliary scratch are grown on their own
     nw.rope_bytes = w.rope_bytes;
+    nw.aux = w.aux;
+    nw.aux_bytes = w.aux_bytes;
     w = nw;
     *out = &w;
     return PA_OK;
 }
 
 // Grows (stream-ordered) the rotated-q/k scratch of a workspace to `bytes`.
-pa_status get_rope_scratch(Workspace* w, cudaStream_t st, size_t bytes, void** out) {
+pa_status get_rope_scratch(Workspace* w, int dev, cudaStream_t st, size_t bytes, void** out) {
     std::lock_guard<std::mutex> lock(g_mu);
     if (w->rope_bytes < bytes && capturing(st))
         return fail(PA_ERR_UNSUPPORTED,
@@ -120,11 +137,31 @@ pa_status get_rope_scratch(Workspace* w, cudaStream_t st, size_t bytes, void** o
         void* nptr = nullptr;
         cudaError_t e = cudaMallocAsync(&nptr, bytes, st);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(rotary scratch)");
-        if (w->rope) cudaFreeAsync(w->rope, st);
+        drop_block(*w, dev, w->rope, st);
         w->rope = nptr;
         w->rope_bytes = bytes;
     }
     *out = w->rope;
+    return PA_OK;
+}
+
+// Grows (stream-ordered) the auxiliary scratch of a workspace to `bytes`.
+pa_status get_aux_scratch(Workspace* w, int dev, cudaStream_t st, size_t bytes, void** out) {
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (w->aux_bytes < bytes && capturing(st))
+        return fail(PA_ERR_UNSUPPORTED,
+                    "graph capture: the stream's auxiliary scratch would have to grow (%zu bytes); run a call of at "
+                    "least these sizes on this stream before capturing",
+                    bytes);
+    if (w->aux_bytes < bytes) {
+        void* nptr = nullptr;
+        cudaError_t e = cudaMallocAsync(&nptr, bytes, st);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(auxiliary scratch)");
+        drop_block(*w, dev, w->aux, st);
+        w->aux = nptr;
+        w->aux_bytes = bytes;
+    }
+    *out = w->aux;
     return PA_OK;
 }
 
@@ -304,66 +341,34 @@ struct Scratch {
     void* rope = nullptr;  // room for the rotated q and k when the rotary embedding is on
 };
 
-// Enqueues the scheduler and the attention kernel (arguments already checked).
-pa_status enqueue(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
-                  const int32_t* cu_seqlens_k, void* cache_k, void* cache_v, const int32_t* cache_offsets, void* out,
-                  float* lse, int num_seqs, int total_q, int max_cache_len, int n_heads, int n_kv_heads,
-                  int head_dim, float scale, int causal, const Options& o, const Scratch& scr, long long units_bound,
-                  int sched, int sms, cudaStream_t stream) {
-    const int slots = sched == 1 ? 1 : pa::kSlots;  // Q tiles per unit
-    const int group = n_heads / n_kv_heads;
-    pa::ScheduleArgs sa;
-    sa.cu_seqlens_q = cu_seqlens_q;
-    sa.cu_seqlens_k = cu_seqlens_k;
-    sa.cache_offsets = cache_offsets;
-    sa.hdr = scr.hdr;
-    sa.seqs = scr.seqs;
-    sa.units = scr.units;
-    sa.seq_scratch = scr.seq_scratch;
-    sa.seq_group = scr.seq_scratch + num_seqs;
-    sa.num_seqs = num_seqs;
-    sa.total_q = total_q;
-    sa.max_cache_len = max_cache_len;
-    sa.n_kv_heads = n_kv_heads;
-    sa.head_dim = head_dim;
-    sa.group = group;
-    sa.causal = causal;
-    sa.window = o.window;
-    sa.max_units = scr.max_units;
-    sa.num_ctas = (int)std::min<long long>(sms, units_bound);
-    sa.unit_slots = slots;
-    sa.block_table = o.block_table;
-    sa.block_size = o.block_size;
-    sa.max_blocks = o.max_blocks;
-    sa.num_blocks = o.num_blocks;
-    cudaError_t e = pa::launch_build_schedule(sa, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
+// Enqueues the rotary prologue; q and k then point at the rotated copies in `rope`.
+cudaError_t rotate(const void*& q, const void*& k, const int32_t* cu_seqlens_q, const pa::SeqInfo* seqs, void* rope,
+                   int total_q, int num_seqs, int n_heads, int n_kv_heads, int head_dim, float theta, int pos0,
+                   cudaStream_t stream) {
+    pa::RopeParams rp;
+    rp.q = static_cast<const __nv_bfloat16*>(q);
+    rp.k = static_cast<const __nv_bfloat16*>(k);
+    rp.q_rot = static_cast<__nv_bfloat16*>(rope);
+    rp.k_rot = rp.q_rot + (size_t)total_q * n_heads * head_dim;
+    rp.cu_seqlens_q = cu_seqlens_q;
+    rp.seqs = seqs;
+    rp.total_q = total_q;
+    rp.num_seqs = num_seqs;
+    rp.n_heads = n_heads;
+    rp.n_kv_heads = n_kv_heads;
+    rp.head_dim = head_dim;
+    rp.pos0 = pos0;
+    for (int i = 0; i < head_dim / 2; ++i)
+        rp.inv_freq[i] = 1.0f / std::pow(theta, (float)(2 * i) / (float)head_dim);
+    q = rp.q_rot;
+    k = rp.k_rot;
+    return pa::launch_rope(rp, stream);
+}
 
-    int launches = 2;
-    if (o.rope_theta > 0.f) {
-        // rotary prologue: attention then reads the rotated copies
-        pa::RopeParams rp;
-        rp.q = static_cast<const __nv_bfloat16*>(q);
-        rp.k = static_cast<const __nv_bfloat16*>(k);
-        rp.q_rot = static_cast<__nv_bfloat16*>(scr.rope);
-        rp.k_rot = rp.q_rot + (size_t)total_q * n_heads * head_dim;
-        rp.cu_seqlens_q = cu_seqlens_q;
-        rp.seqs = scr.seqs;
-        rp.total_q = total_q;
-        rp.num_seqs = num_seqs;
-        rp.n_heads = n_heads;
-        rp.n_kv_heads = n_kv_heads;
-        rp.head_dim = head_dim;
-        for (int i = 0; i < head_dim / 2; ++i)
-            rp.inv_freq[i] = 1.0f / std::pow(o.rope_theta, (float)(2 * i) / (float)head_dim);
-        e = pa::launch_rope(rp, stream);
-        if (e != cudaSuccess) return cuda_fail(e, "rotary prologue launch");
-        q = rp.q_rot;
-        k = rp.k_rot;
-        launches = 3;
-    }
-
-    pa::FwdParams p;
+// The attention kernel's parameters except its tensor maps.
+void fill_fwd(pa::FwdParams& p, const void* k, const void* v, void* cache_k, void* cache_v, void* out, float* lse,
+              const Scratch& scr, int max_cache_len, int n_heads, int n_kv_heads, float scale, int causal,
+              const Options& o, int sched) {
     p.k = static_cast<const __nv_bfloat16*>(k);
     p.v = static_cast<const __nv_bfloat16*>(v);
     p.cache_k = static_cast<__nv_bfloat16*>(cache_k);
@@ -375,7 +380,7 @@ pa_status enqueue(const void* q, const void* k, const void* v, const int32_t* cu
     p.units = scr.units;
     p.n_heads = n_heads;
     p.n_kv_heads = n_kv_heads;
-    p.group = group;
+    p.group = n_heads / n_kv_heads;
     p.max_cache_len = max_cache_len;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.causal = causal;
@@ -389,10 +394,63 @@ pa_status enqueue(const void* q, const void* k, const void* v, const int32_t* cu
     p.kv_quant = o.kv_quant;
     p.wait_timeout_test = o.wait_timeout_test;
     p.alt = sched != 2;
-    p.unit_slots = slots;
+    p.unit_slots = sched == 1 ? 1 : pa::kSlots;
     p.out_align32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     p.scale_k = o.scale_k;
     p.scale_v = o.scale_v;
+}
+
+void fill_schedule(pa::ScheduleArgs& sa, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                   const int32_t* cache_offsets, int num_seqs, int total_q, int max_cache_len, int n_heads,
+                   int n_kv_heads, int head_dim, int causal, const Options& o, const Scratch& scr, int slots, int ctas) {
+    sa.cu_seqlens_q = cu_seqlens_q;
+    sa.cu_seqlens_k = cu_seqlens_k;
+    sa.cache_offsets = cache_offsets;
+    sa.hdr = scr.hdr;
+    sa.seqs = scr.seqs;
+    sa.units = scr.units;
+    sa.seq_scratch = scr.seq_scratch;
+    sa.seq_group = scr.seq_scratch + num_seqs;
+    sa.num_seqs = num_seqs;
+    sa.total_q = total_q;
+    sa.max_cache_len = max_cache_len;
+    sa.n_kv_heads = n_kv_heads;
+    sa.head_dim = head_dim;
+    sa.group = n_heads / n_kv_heads;
+    sa.causal = causal;
+    sa.window = o.window;
+    sa.max_units = scr.max_units;
+    sa.num_ctas = ctas;
+    sa.unit_slots = slots;
+    sa.block_table = o.block_table;
+    sa.block_size = o.block_size;
+    sa.max_blocks = o.max_blocks;
+    sa.num_blocks = o.num_blocks;
+}
+
+// Enqueues the scheduler and the attention kernel (arguments already checked).
+pa_status enqueue(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                  const int32_t* cu_seqlens_k, void* cache_k, void* cache_v, const int32_t* cache_offsets, void* out,
+                  float* lse, int num_seqs, int total_q, int max_cache_len, int n_heads, int n_kv_heads,
+                  int head_dim, float scale, int causal, const Options& o, const Scratch& scr, long long units_bound,
+                  int sched, int sms, cudaStream_t stream) {
+    const int slots = sched == 1 ? 1 : pa::kSlots;  // Q tiles per unit
+    pa::ScheduleArgs sa;
+    fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, max_cache_len, n_heads, n_kv_heads,
+                  head_dim, causal, o, scr, slots, (int)std::min<long long>(sms, units_bound));
+    cudaError_t e = pa::launch_build_schedule(sa, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
+
+    int launches = 2;
+    if (o.rope_theta > 0.f) {
+        e = rotate(q, k, cu_seqlens_q, scr.seqs, scr.rope, total_q, num_seqs, n_heads, n_kv_heads, head_dim,
+                   o.rope_theta, 0, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "rotary prologue launch");
+        launches = 3;
+    }
+
+    pa::FwdParams p;
+    fill_fwd(p, k, v, cache_k, cache_v, out, lse, scr, max_cache_len, n_heads, n_kv_heads, scale, causal, o, sched);
     e = pa::encode_fwd_maps(p, q, total_q, num_seqs, head_dim, o.num_blocks);
     if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
     const int grid = (int)std::min<long long>(sms, units_bound);
@@ -479,7 +537,7 @@ pa_status prefill_attn_varlen_ex(const void* q, const void* k, const void* v, co
     Scratch scr{static_cast<pa::WorkspaceHeader*>(ws->ptr), ws_seqs(*ws), ws_units(*ws), ws->max_units,
                 ws_seq_scratch(*ws)};
     if (o.rope_theta > 0.f) {
-        s = get_rope_scratch(ws, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
+        s = get_rope_scratch(ws, dev, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
         if (s != PA_OK) return s;
     }
     return enqueue(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs, total_q,
@@ -560,7 +618,13 @@ void prefill_attn_release(void) {
         cudaSetDevice(kv.first.first);
         if (kv.second.ptr) cudaFree(kv.second.ptr);
         if (kv.second.rope) cudaFree(kv.second.rope);
+        if (kv.second.aux) cudaFree(kv.second.aux);
     }
+    for (auto& r : g_retired) {
+        cudaSetDevice(r.first);
+        cudaFree(r.second);
+    }
+    g_retired.clear();
     cudaSetDevice(cur);
     g_ws.clear();
 }
@@ -683,3 +747,433 @@ extern "C" pa_status prefill_attn_varlen_noalloc(const void* q, const void* k, c
                    max_cache_len, n_heads, n_kv_heads, head_dim, scale, causal, Options(), scr, units, sched, sms,
                    stream);
 }
+
+// ---------------------------------------------------------------------------
+// Long-context calls: sink tokens, a shared prefix, key weights, eviction.
+// ---------------------------------------------------------------------------
+namespace {
+
+// A prefix that every sequence of a call sees (pa_prefix, checked).
+struct Prefix {
+    int len = 0;
+    const void* k = nullptr;
+    const void* v = nullptr;
+    int capacity = 0;
+    const float* scale_k = nullptr;
+    const float* scale_v = nullptr;
+    const int32_t* block_table = nullptr;
+};
+
+pa_status read_prefix(const pa_prefix* prefix, const Options& o, Prefix* out) {
+    *out = Prefix();
+    if (!prefix) return fail(PA_ERR_INVALID_ARG, "prefix is NULL");
+    if (prefix->struct_size < sizeof(pa_prefix))
+        return fail(PA_ERR_INVALID_ARG, "pa_prefix.struct_size %u is too small", (unsigned)prefix->struct_size);
+    if (prefix->reserved != 0) return fail(PA_ERR_INVALID_ARG, "pa_prefix.reserved must be 0");
+    if (prefix->len < 0) return fail(PA_ERR_INVALID_ARG, "pa_prefix.len must be >= 0 (got %d)", prefix->len);
+    out->len = prefix->len;
+    if (prefix->len == 0) return PA_OK;  // nothing of it is read
+    if (o.block_table) {
+        if (!prefix->block_table) return fail(PA_ERR_INVALID_ARG, "a paged cache needs pa_prefix.block_table");
+        if (reinterpret_cast<uintptr_t>(prefix->block_table) & 3u)
+            return fail(PA_ERR_INVALID_ARG, "pa_prefix.block_table must be 4-byte aligned");
+        out->block_table = prefix->block_table;
+        return PA_OK;
+    }
+    if (!prefix->k || !prefix->v) return fail(PA_ERR_INVALID_ARG, "pa_prefix.k and pa_prefix.v must not be NULL");
+    if (!aligned16(prefix->k) || !aligned16(prefix->v))
+        return fail(PA_ERR_INVALID_ARG, "pa_prefix.k and pa_prefix.v must be 16-byte aligned");
+    if (prefix->capacity < prefix->len)
+        return fail(PA_ERR_INVALID_ARG, "pa_prefix.len (%d) exceeds its capacity (%d)", prefix->len, prefix->capacity);
+    if (o.kv_quant) {
+        if (!prefix->k_scale || !prefix->v_scale)
+            return fail(PA_ERR_INVALID_ARG, "kv_quant = 1 needs pa_prefix.k_scale and pa_prefix.v_scale");
+        if ((reinterpret_cast<uintptr_t>(prefix->k_scale) | reinterpret_cast<uintptr_t>(prefix->v_scale)) & 3u)
+            return fail(PA_ERR_INVALID_ARG, "prefix scales must be 4-byte aligned");
+        out->scale_k = prefix->k_scale;
+        out->scale_v = prefix->v_scale;
+    }
+    out->k = prefix->k;
+    out->v = prefix->v;
+    out->capacity = prefix->capacity;
+    return PA_OK;
+}
+
+// Slabs of partial results are bounded by this many bytes for a sequence's own
+// keys (a few long rows: up to kMaxPieces pieces) and again for the prefix's.
+constexpr long long kPartialBytes = 64ll << 20;
+constexpr int kMaxPieces = 32;
+constexpr int kMinPieceTiles = 4;
+constexpr int kPieceWaves = 2;
+
+pa_status check_unused(const Options& o, const char* what) {
+    if (o.schedule || o.wait_timeout_test)
+        return fail(PA_ERR_INVALID_ARG, "%s takes no schedule and no wait_timeout_test", what);
+    return PA_OK;
+}
+
+// Enqueues a long-context attention call (arguments already checked).
+pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                       const int32_t* cu_seqlens_k, void* cache_k, void* cache_v, const int32_t* cache_offsets,
+                       void* out, float* lse, int num_seqs, int total_q, int max_cache_len, int n_heads,
+                       int n_kv_heads, int head_dim, float scale, int causal, int sinks, const Prefix& pre,
+                       const Options& o, cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    pa_status s;
+    const int sms = sm_count(dev, &s);
+    if (s != PA_OK) return s;
+    const int sched = o.schedule ? o.schedule
+                                 : auto_schedule(total_q, num_seqs, n_heads, n_kv_heads, o.kv_quant != 0, sms);
+    const int slots = sched == 1 ? 1 : pa::kSlots;
+    const int tpu = slots * (pa::kBlockM / (n_heads / n_kv_heads));
+    const long long blocks = ((long long)total_q + tpu - 1) / tpu;
+    const long long own_units = (blocks + num_seqs) * n_kv_heads;
+    const long long pre_units = pre.len > 0 ? blocks * n_kv_heads : 0;
+    const long long target = (long long)kPieceWaves * sms;
+    const long long slab_rows = (long long)total_q * n_heads;
+    const long long slab_bytes = slab_rows * (head_dim + 1) * 4;
+    const int fit = (int)std::max(1ll, std::min((long long)kMaxPieces, kPartialBytes / slab_bytes));
+    const int max_pieces = fit;
+    int max_prefix_pieces = 0;
+    if (pre.len > 0)
+        max_prefix_pieces = (int)std::max(1ll, std::min((long long)kMaxPieces, std::min(kPartialBytes / slab_bytes,
+                                                                                       (target + pre_units - 1) / pre_units)));
+    const bool merge = pre.len > 0 || max_pieces > 1;
+    const long long slabs = merge ? max_pieces + max_prefix_pieces : 0;
+    // pieces per block: at most 1 + tiles / piece size, so a call has at most its
+    // blocks plus twice the wanted units (a causal sequence's blocks average at
+    // least half its longest one); twice that again is room to spare
+    const long long units =
+        std::min(own_units * max_pieces + pre_units * std::max(1, max_prefix_pieces), own_units + pre_units + 4 * target);
+    if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
+    Workspace* ws = nullptr;
+    s = get_workspace(dev, stream, num_seqs + 1, 0, &ws);
+    if (s != PA_OK) return s;
+    const size_t list_bytes = align_up((size_t)units * sizeof(pa::UnitX), 256);
+    const size_t seq_bytes = align_up(((size_t)num_seqs + 1) * sizeof(int), 256);
+    const size_t tok_bytes = merge ? align_up((size_t)total_q * sizeof(int), 256) : 0;
+    const size_t lse_bytes = align_up((size_t)(slabs * slab_rows) * sizeof(float), 256);
+    const size_t o_bytes = (size_t)(slabs * slab_rows) * head_dim * sizeof(float);
+    void* aux = nullptr;
+    s = get_aux_scratch(ws, dev, stream, list_bytes + seq_bytes + tok_bytes + lse_bytes + o_bytes, &aux);
+    if (s != PA_OK) return s;
+    char* at = static_cast<char*>(aux);
+    Scratch scr{static_cast<pa::WorkspaceHeader*>(ws->ptr), ws_seqs(*ws), nullptr, (int)units, ws_seq_scratch(*ws)};
+    if (o.rope_theta > 0.f) {
+        s = get_rope_scratch(ws, dev, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
+        if (s != PA_OK) return s;
+    }
+    const int grid = (int)std::min<long long>(sms, units);
+
+    pa::LongScheduleArgs sa;
+    fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, max_cache_len, n_heads, n_kv_heads,
+                  head_dim, causal, o, scr, slots, grid);
+    sa.seq_group = scr.seq_scratch + num_seqs + 1;
+    sa.xunits = reinterpret_cast<pa::UnitX*>(at);
+    sa.seq_pieces = reinterpret_cast<int*>(at + list_bytes);
+    sa.tok_pieces = merge ? reinterpret_cast<int*>(at + list_bytes + seq_bytes) : nullptr;
+    sa.sinks = sinks;
+    sa.prefix_len = pre.len;
+    sa.prefix_table = pre.block_table;
+    sa.max_pieces = max_pieces;
+    sa.max_prefix_pieces = max_prefix_pieces;
+    sa.target_units = (int)target;
+    sa.min_tiles = kMinPieceTiles;
+    e = pa::launch_build_long_schedule(sa, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
+    int launches = 2;
+    if (o.rope_theta > 0.f) {
+        e = rotate(q, k, cu_seqlens_q, scr.seqs, scr.rope, total_q, num_seqs, n_heads, n_kv_heads, head_dim,
+                   o.rope_theta, pre.len, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "rotary prologue launch");
+        ++launches;
+    }
+
+    pa::FwdParamsX p;
+    fill_fwd(p, k, v, cache_k, cache_v, out, lse, scr, max_cache_len, n_heads, n_kv_heads, scale, causal, o, sched);
+    p.xunits = sa.xunits;
+    p.num_seqs = num_seqs;
+    p.sinks = sinks;
+    p.prefix_len = pre.len;
+    p.prefix_cap = pre.capacity;
+    p.prefix_table = pre.block_table;
+    p.prefix_scale_k = pre.scale_k;
+    p.prefix_scale_v = pre.scale_v;
+    p.part_lse = reinterpret_cast<float*>(at + list_bytes + seq_bytes + tok_bytes);
+    p.part_o = reinterpret_cast<float*>(at + list_bytes + seq_bytes + tok_bytes + lse_bytes);
+    p.slab_rows = (size_t)slab_rows;
+    e = pa::encode_fwd_maps(p, q, total_q, num_seqs, head_dim, o.num_blocks);
+    if (e == cudaSuccess && pre.k) e = pa::encode_prefix_maps(p, head_dim, pre.k, pre.v);
+    if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
+    e = head_dim == 32   ? pa::launch_attn_long_d<32>(p, grid, stream)
+        : head_dim == 64 ? pa::launch_attn_long_d<64>(p, grid, stream)
+                         : pa::launch_attn_long_d<128>(p, grid, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+    if (merge) {
+        pa::MergeArgs ma{p.part_o, p.part_lse, sa.tok_pieces, pre.len > 0 ? sa.seq_pieces + num_seqs : nullptr,
+                         max_pieces, static_cast<__nv_bfloat16*>(out), lse, total_q, n_heads};
+        e = pa::launch_merge(ma, head_dim, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "merge launch");
+        ++launches;
+    }
+    g_last_launches = launches;
+    g_last_schedule = sched;
+    return PA_OK;
+}
+
+// Whether [a, a + a_bytes) and [b, b + b_bytes) overlap.
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + b_bytes && y < x + a_bytes;
+}
+
+int log2_of(int block_size) {
+    int l = 0;
+    while ((1 << l) < block_size) ++l;
+    return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status prefill_attn_varlen_sinks(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                                    const int32_t* cu_seqlens_k, void* cache_k, void* cache_v,
+                                    const int32_t* cache_offsets, void* out, float* lse, int num_seqs, int total_q,
+                                    int max_cache_len, int n_heads, int n_kv_heads, int head_dim, float scale,
+                                    int sink_tokens, const pa_options* opts, pa_stream_t stream_) {
+    g_last_error.clear();
+    g_last_launches = 0;
+    g_last_schedule = 0;
+    Options o;
+    pa_status s = read_options(opts, 1, &o);
+    if (s != PA_OK) return s;
+    if (o.window < 1) return fail(PA_ERR_INVALID_ARG, "sink tokens need a window (pa_options.window >= 1)");
+    if (sink_tokens < 0) return fail(PA_ERR_INVALID_ARG, "sink_tokens must be >= 0 (got %d)", sink_tokens);
+    if (o.wait_timeout_test) return fail(PA_ERR_INVALID_ARG, "wait_timeout_test is for prefill_attn_varlen_ex");
+    s = check_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs, total_q,
+                   max_cache_len, n_heads, n_kv_heads, head_dim, scale, 1, o.block_table != nullptr);
+    if (s != PA_OK) return s;
+    s = check_paged(o, max_cache_len, n_kv_heads);
+    if (s != PA_OK) return s;
+    if (num_seqs == 0 || total_q == 0) return PA_OK;
+    return enqueue_long(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs,
+                        total_q, max_cache_len, n_heads, n_kv_heads, head_dim, scale, 1, sink_tokens, Prefix(), o,
+                        reinterpret_cast<cudaStream_t>(stream_));
+}
+
+pa_status prefill_attn_varlen_prefix(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                                     const int32_t* cu_seqlens_k, void* cache_k, void* cache_v,
+                                     const int32_t* cache_offsets, void* out, float* lse, int num_seqs, int total_q,
+                                     int max_cache_len, int n_heads, int n_kv_heads, int head_dim, float scale,
+                                     int causal, const pa_prefix* prefix, const pa_options* opts,
+                                     pa_stream_t stream_) {
+    g_last_error.clear();
+    g_last_launches = 0;
+    g_last_schedule = 0;
+    Options o;
+    pa_status s = read_options(opts, causal, &o);
+    if (s != PA_OK) return s;
+    if (o.window) return fail(PA_ERR_INVALID_ARG, "a shared prefix takes no sliding window");
+    if (o.wait_timeout_test) return fail(PA_ERR_INVALID_ARG, "wait_timeout_test is for prefill_attn_varlen_ex");
+    s = check_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs, total_q,
+                   max_cache_len, n_heads, n_kv_heads, head_dim, scale, causal, o.block_table != nullptr);
+    if (s != PA_OK) return s;
+    s = check_paged(o, max_cache_len, n_kv_heads);
+    if (s != PA_OK) return s;
+    Prefix pre;
+    s = read_prefix(prefix, o, &pre);
+    if (s != PA_OK) return s;
+    if (num_seqs == 0 || total_q == 0) return PA_OK;
+    if (pre.k && (pre.k == out || pre.v == out || pre.k == cache_k || pre.k == cache_v || pre.v == cache_k ||
+                  pre.v == cache_v))
+        return fail(PA_ERR_INVALID_ARG, "the prefix must not alias out or the caches");
+    return enqueue_long(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs,
+                        total_q, max_cache_len, n_heads, n_kv_heads, head_dim, scale, causal, 0, pre, o,
+                        reinterpret_cast<cudaStream_t>(stream_));
+}
+
+pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* cu_seqlens_q,
+                                   const int32_t* cu_seqlens_k, const void* cache_k, const int32_t* cache_offsets,
+                                   const float* lse, float* weights, int num_seqs, int total_q, int max_cache_len,
+                                   int n_heads, int n_kv_heads, int head_dim, float scale, int causal,
+                                   int sink_tokens, int prefix_len, const pa_options* opts, pa_stream_t stream_) {
+    g_last_error.clear();
+    g_last_launches = 0;
+    g_last_schedule = 0;
+    Options o;
+    pa_status s = read_options(opts, causal, &o);
+    if (s != PA_OK) return s;
+    s = check_unused(o, "prefill_attn_key_weights");
+    if (s != PA_OK) return s;
+    if (sink_tokens < 0) return fail(PA_ERR_INVALID_ARG, "sink_tokens must be >= 0 (got %d)", sink_tokens);
+    if (sink_tokens > 0 && o.window < 1)
+        return fail(PA_ERR_INVALID_ARG, "sink tokens need a window (pa_options.window >= 1)");
+    if (prefix_len < 0) return fail(PA_ERR_INVALID_ARG, "prefix_len must be >= 0 (got %d)", prefix_len);
+    if (prefix_len > 0 && o.window) return fail(PA_ERR_INVALID_ARG, "a shared prefix takes no sliding window");
+    // v, cache_v and out have no part here: stand-ins that satisfy the shared checks
+    const void* none = reinterpret_cast<const void*>(uintptr_t(16));
+    if (num_seqs > 0 && total_q > 0) {
+        if (!lse) return fail(PA_ERR_INVALID_ARG, "lse is NULL");
+        if (!weights) return fail(PA_ERR_INVALID_ARG, "weights is NULL");
+        if (reinterpret_cast<uintptr_t>(weights) & 3u)
+            return fail(PA_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+        if (static_cast<const void*>(weights) == lse || static_cast<const void*>(weights) == q ||
+            static_cast<const void*>(weights) == k || static_cast<const void*>(weights) == cache_k)
+            return fail(PA_ERR_INVALID_ARG, "weights must not alias an input");
+    }
+    s = check_args(q, k, none, cu_seqlens_q, cu_seqlens_k, cache_k, reinterpret_cast<const void*>(uintptr_t(32)),
+                   cache_offsets, reinterpret_cast<const void*>(uintptr_t(48)), lse, num_seqs, total_q, max_cache_len,
+                   n_heads, n_kv_heads, head_dim, scale, causal, o.block_table != nullptr);
+    if (s != PA_OK) return s;
+    s = check_paged(o, max_cache_len, n_kv_heads);
+    if (s != PA_OK) return s;
+    if (num_seqs == 0 || total_q == 0) return PA_OK;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    const int sms = sm_count(dev, &s);
+    if (s != PA_OK) return s;
+    const long long units = unit_bound(total_q, num_seqs, n_heads, n_kv_heads, pa::kSlots);
+    if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
+    Workspace* ws = nullptr;
+    s = get_workspace(dev, stream, num_seqs, (int)units, &ws);
+    if (s != PA_OK) return s;
+    Scratch scr{static_cast<pa::WorkspaceHeader*>(ws->ptr), ws_seqs(*ws), ws_units(*ws), ws->max_units,
+                ws_seq_scratch(*ws)};
+    if (o.rope_theta > 0.f) {
+        s = get_rope_scratch(ws, dev, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
+        if (s != PA_OK) return s;
+    }
+    pa::ScheduleArgs sa;
+    fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, max_cache_len, n_heads, n_kv_heads,
+                  head_dim, causal, o, scr, pa::kSlots, sms);
+    e = pa::launch_build_schedule(sa, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
+    int launches = 2;
+    if (o.rope_theta > 0.f) {
+        e = rotate(q, k, cu_seqlens_q, scr.seqs, scr.rope, total_q, num_seqs, n_heads, n_kv_heads, head_dim,
+                   o.rope_theta, prefix_len, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "rotary prologue launch");
+        ++launches;
+    }
+    pa::KeyWeightsArgs a;
+    a.q = static_cast<const __nv_bfloat16*>(q);
+    a.k = static_cast<const __nv_bfloat16*>(k);
+    a.cache_k = cache_k;
+    a.scale_k = o.kv_quant ? o.scale_k : nullptr;
+    a.lse = lse;
+    a.weights = weights;
+    a.seqs = scr.seqs;
+    a.hdr = scr.hdr;
+    a.num_seqs = num_seqs;
+    a.total_q = total_q;
+    a.n_heads = n_heads;
+    a.n_kv_heads = n_kv_heads;
+    a.group = n_heads / n_kv_heads;
+    a.max_cache_len = max_cache_len;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.causal = causal;
+    a.window = o.window;
+    a.sinks = sink_tokens;
+    a.block_table = o.block_table;
+    a.block_log2 = log2_of(o.block_size);
+    a.max_blocks = o.max_blocks;
+    a.num_blocks = o.num_blocks;
+    e = pa::launch_key_weights(a, head_dim, sms, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "key weight launch");
+    g_last_launches = launches;
+    return PA_OK;
+}
+
+pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights, const int32_t* lengths,
+                             int32_t* kept_lengths, int32_t* kept_index, float* kept_weights, int num_seqs,
+                             int max_cache_len, int n_kv_heads, int head_dim, int budget, int sink_tokens,
+                             int recent_tokens, const pa_options* opts, pa_stream_t stream_) {
+    g_last_error.clear();
+    g_last_launches = 0;
+    g_last_schedule = 0;
+    Options o;
+    pa_status s = read_options(opts, 1, &o);
+    if (s != PA_OK) return s;
+    s = check_unused(o, "prefill_attn_evict");
+    if (s != PA_OK) return s;
+    if (o.window) return fail(PA_ERR_INVALID_ARG, "prefill_attn_evict takes no window");
+    if (o.rope_theta > 0.f) return fail(PA_ERR_INVALID_ARG, "prefill_attn_evict takes no rope_theta");
+    if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs must be >= 0 (got %d)", num_seqs);
+    if (max_cache_len < 1) return fail(PA_ERR_INVALID_ARG, "max_cache_len must be >= 1 (got %d)", max_cache_len);
+    if (n_kv_heads < 1) return fail(PA_ERR_INVALID_ARG, "n_kv_heads must be >= 1 (got %d)", n_kv_heads);
+    if (head_dim != 32 && head_dim != 64 && head_dim != 128)
+        return fail(PA_ERR_UNSUPPORTED, "head_dim must be 32, 64 or 128 (got %d)", head_dim);
+    if (budget < 1) return fail(PA_ERR_INVALID_ARG, "budget must be >= 1 (got %d)", budget);
+    if (sink_tokens < 0 || recent_tokens < 0 || (long long)sink_tokens + recent_tokens > budget)
+        return fail(PA_ERR_INVALID_ARG, "sink_tokens (%d) and recent_tokens (%d) must be >= 0 and fit the budget (%d)",
+                    sink_tokens, recent_tokens, budget);
+    s = check_paged(o, max_cache_len, n_kv_heads);
+    if (s != PA_OK) return s;
+    const long long heads = (long long)num_seqs * n_kv_heads;
+    if (heads >= (1LL << 24)) return fail(PA_ERR_UNSUPPORTED, "num_seqs * n_kv_heads must be < 2^24");
+    if (!o.block_table && heads * max_cache_len >= (1LL << 31))
+        return fail(PA_ERR_UNSUPPORTED, "num_seqs * n_kv_heads * max_cache_len must be < 2^31");
+    if (num_seqs == 0) return PA_OK;
+    const void* ptrs[] = {cache_k, cache_v, weights, lengths, kept_lengths};
+    const char* names[] = {"cache_k", "cache_v", "weights", "lengths", "kept_lengths"};
+    for (int i = 0; i < 5; ++i) {
+        if (!ptrs[i]) return fail(PA_ERR_INVALID_ARG, "%s is NULL", names[i]);
+        if (i < 2 ? !aligned16(ptrs[i]) : (reinterpret_cast<uintptr_t>(ptrs[i]) & 3u) != 0)
+            return fail(PA_ERR_INVALID_ARG, "%s must be %d-byte aligned", names[i], i < 2 ? 16 : 4);
+    }
+    if ((reinterpret_cast<uintptr_t>(kept_index) | reinterpret_cast<uintptr_t>(kept_weights)) & 3u)
+        return fail(PA_ERR_INVALID_ARG, "kept_index and kept_weights must be 4-byte aligned");
+    if (overlap(lengths, (size_t)num_seqs * 4, kept_lengths, (size_t)num_seqs * 4))
+        return fail(PA_ERR_INVALID_ARG, "kept_lengths must not overlap lengths");
+    const size_t rows = o.block_table ? (size_t)o.num_blocks * n_kv_heads * o.block_size : (size_t)heads * max_cache_len;
+    const size_t row_bytes = o.kv_quant ? head_dim : 2 * head_dim;
+    if (kept_weights && kept_weights != weights && overlap(weights, rows * 4, kept_weights, rows * 4))
+        return fail(PA_ERR_INVALID_ARG, "kept_weights must be weights itself or not overlap it");
+    if (overlap(cache_k, rows * row_bytes, cache_v, rows * row_bytes))
+        return fail(PA_ERR_INVALID_ARG, "cache_k and cache_v must not overlap");
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    Workspace* ws = nullptr;
+    s = get_workspace(dev, stream, 0, 0, &ws);
+    if (s != PA_OK) return s;
+    void* aux = nullptr;
+    if (!kept_index) {
+        s = get_aux_scratch(ws, dev, stream, (size_t)heads * budget * sizeof(int), &aux);
+        if (s != PA_OK) return s;
+    }
+    pa::EvictArgs a;
+    a.cache_k = cache_k;
+    a.cache_v = cache_v;
+    a.row_bytes = (int)row_bytes;
+    a.scale_k = o.kv_quant ? o.scale_k : nullptr;
+    a.scale_v = o.kv_quant ? o.scale_v : nullptr;
+    a.weights = weights;
+    a.kept_weights = kept_weights;
+    a.lengths = lengths;
+    a.kept_lengths = kept_lengths;
+    a.index = kept_index ? kept_index : static_cast<int*>(aux);
+    a.hdr = static_cast<pa::WorkspaceHeader*>(ws->ptr);
+    a.num_seqs = num_seqs;
+    a.n_kv_heads = n_kv_heads;
+    a.max_cache_len = max_cache_len;
+    a.budget = budget;
+    a.sinks = sink_tokens;
+    a.recent = recent_tokens;
+    a.block_table = o.block_table;
+    a.block_log2 = log2_of(o.block_size);
+    a.max_blocks = o.max_blocks;
+    a.num_blocks = o.num_blocks;
+    e = pa::launch_evict(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
+    g_last_launches = 2;
+    return PA_OK;
+}
+
+}  // extern "C"

@@ -53,6 +53,7 @@
 #include <climits>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -105,6 +106,7 @@ struct __align__(16) Ctrl {
     uint64_t mma_drain;
     uint64_t unit_full[2], unit_empty[2];
     UnitSlot slot[2];
+    int2 ext[2];  // long-context variant: UnitX::s0 and UnitX::slab of slot[]
     uint32_t tmem_base;
     int abort;
     union {
@@ -227,17 +229,62 @@ __device__ __forceinline__ bool paged_tail_tile(int j, int P, int np) {
 // work on its rows, slot 0 on the even tiles of the stream and slot 1 on the
 // odd ones, so that the two still ping-pong on the tensor pipe, and the two
 // partial results are merged in the epilogue.
+// Long-context variant (kExt): the unit's stream is a piece, from stream position
+// s0 on, of the tiles its query block needs -- the sink tiles [0, nsink), then
+// the window's; lo is then the gap between a window tile and its stream
+// position -- and pre marks a block of the whole batch's queries against the
+// shared prefix.
 struct UnitGeo {
     int lo, ntiles, np;
     int a[kSlots], b[kSlots];
     bool alt;
+    int s0, nsink;
+    bool pre;
 };
 
-template <bool kPaged, bool kAlt>
-__device__ __forceinline__ UnitGeo unit_geo(const Unit& u, const SeqInfo& s, int tps, int causal, int window,
+// Index in the sequence of tile j of the unit's stream.
+template <bool kExt>
+__device__ __forceinline__ int tile_at(const UnitGeo& g, int j) {
+    if constexpr (!kExt) return g.lo + j;
+    const int x = g.s0 + j;
+    return x < g.nsink ? x : x + g.lo;
+}
+
+template <bool kPaged, bool kAlt, bool kExt, class Params>
+__device__ __forceinline__ UnitGeo unit_geo(const Unit& u, const SeqInfo& s, int s0, int tps, const Params& p,
                                             int unit_slots) {
     const int nslots = kAlt ? unit_slots : kSlots;  // Q tiles of a unit
+    const int causal = p.causal, window = p.window;
     UnitGeo g;
+    if constexpr (kExt) {
+        g.np = prefix_tiles(s.P);
+        g.pre = u.b == p.num_seqs;
+        g.s0 = s0;
+        g.ntiles = u.ntiles;
+        const StreamGeo all = stream_geo(s.n, s.P, u.q0, min(u.q0 + nslots * tps, s.n), causal, window, p.sinks, g.pre,
+                                         kPaged);
+        g.nsink = all.nsink;
+        g.lo = all.lo - all.nsink;
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            const int qs = u.q0 + i * tps;
+            g.a[i] = g.b[i] = 0;
+            if (i < nslots && qs < s.n) {
+                // with sink tokens every slot visits the stream from its start
+                const StreamGeo t = stream_geo(s.n, s.P, qs, min(qs + tps, s.n), causal, window, p.sinks, g.pre, kPaged);
+                const int a = max(p.sinks > 0 ? 0 : t.lo - all.lo, s0) - s0;
+                const int b = min(t.hi - all.lo + all.nsink, s0 + u.ntiles) - s0;
+                if (a < b) {
+                    g.a[i] = a;
+                    g.b[i] = b;
+                }
+            }
+        }
+        g.alt = kAlt && u.q0 + tps >= min(u.q0 + nslots * tps, s.n) && g.ntiles >= 2;
+        return g;
+    }
+    g.s0 = g.nsink = 0;
+    g.pre = false;
     g.np = prefix_tiles(s.P);
     const TileSpan all = query_tiles(s.n, s.P, u.q0, min(u.q0 + nslots * tps, s.n), causal, window, kPaged);
     g.lo = all.lo;
@@ -443,14 +490,14 @@ __device__ __noinline__ void quant_tile_rows(const uint8_t* tile, int8_t* codes,
 
 // Contiguous cache, one KV ring (K or V): waits for the stage, then
 // TMA-loads tile j (index in the sequence) of unit u from the cache (prefix
-// tiles) or from the new tokens' k/v.  Out of line: the K and the V loader
+// tiles; z = its [slot, head] plane) or from the new tokens' k/v.  Out of line: the K and the V loader
 // share one copy of this code, which keeps the kernel's hot code within the
 // instruction caches.
 template <int D, bool kQuant>
 __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, WorkspaceHeader* hdr, uint8_t* ring,
                                           int stages, uint64_t* full, uint64_t* empty, const CUtensorMap* tm_cache,
                                           const CUtensorMap* tm_new, int* last_parity, uint32_t t, int j,
-                                          const Unit& u, const SeqInfo& s, int np) {
+                                          const Unit& u, const SeqInfo& s, int np, int z) {
     using C = Cfg<D>;
     const int st = t % stages;
     const uint32_t ph = (t / stages) & 1;
@@ -460,8 +507,7 @@ __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, Work
         // int8 codes of the prefix tile into the stage's upper half (one box of
         // 128 rows x D bytes), expanded to bf16 by the cache writer
         mbar_arrive_expect_tx(&full[st], kBlockN * D);
-        tma_load_3d(ring + st * C::kTileBytes + C::kTileBytes / 2, tm_cache, &full[st], 0, kb,
-                    u.b * p.n_kv_heads + u.kvh);
+        tma_load_3d(ring + st * C::kTileBytes + C::kTileBytes / 2, tm_cache, &full[st], 0, kb, z);
         last_parity[st] = (int)ph;
         return true;
     }
@@ -469,7 +515,7 @@ __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, Work
     for (int c = 0; c < C::kChunks; ++c) {
         uint8_t* dst = ring + st * C::kTileBytes + c * C::kChunkBytes;
         if (j < np)
-            tma_load_3d(dst, tm_cache, &full[st], c * C::kChunkCols, kb, u.b * p.n_kv_heads + u.kvh);
+            tma_load_3d(dst, tm_cache, &full[st], c * C::kChunkCols, kb, z);
         else
             tma_load_3d(dst, tm_new, &full[st], c * C::kChunkCols, u.kvh, s.q_start + kb - s.P);
     }
@@ -477,8 +523,28 @@ __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, Work
     return true;
 }
 
-template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false>
-__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ FwdParams p) {
+// Claims the next unit that has tiles (the scheduler leaves holes in the list
+// where a query block has fewer tiles than its sequence has pieces).
+__device__ __forceinline__ void claim_unit_ext(const FwdParamsX& p, WorkspaceHeader* hdr, int num_units, UnitSlot& us,
+                                               int2& ext) {
+    us.u.b = -1;
+    for (int idx = atomicAdd(&hdr->counter, 1); idx < num_units; idx = atomicAdd(&hdr->counter, 1)) {
+        const UnitX x = p.xunits[idx];
+        if (x.u.ntiles == 0) continue;
+        us.u = x.u;
+        us.s = p.seqs[x.u.b];
+        ext = make_int2(x.s0, x.slab);
+        return;
+    }
+}
+
+// kExt: the long-context variant (sink tokens, a prefix the batch shares, units
+// whose tiles are split between CTAs).
+template <bool kExt>
+using KernelParams = std::conditional_t<kExt, FwdParamsX, FwdParams>;
+
+template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
+__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ KernelParams<kExt> p) {
     using C = Cfg<D>;
     static_assert(!(kAlt && kQuant), "the merge exchange shares storage with the int8 scale ring");
     // K stages in use.  With an int8 cache the K writer publishes each tile's row
@@ -544,6 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         prefetch_tmap(&p.tm_v);
         prefetch_tmap(&p.tm_ck);
         prefetch_tmap(&p.tm_cv);
+        if constexpr (kExt) {
+            if (p.prefix_len > 0 && !kPaged) {
+                prefetch_tmap(&p.tm_pk);
+                prefetch_tmap(&p.tm_pv);
+            }
+        }
     }
     if (!misaligned && warp == 1) {
         tmem_alloc(&ctl->tmem_base, 512);
@@ -643,13 +715,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         if (gleader) {
                             ok = wait_bar(&ctl->unit_empty[sl], ((u_it >> 1) & 1) ^ 1, ctl, hdr);
                             if (ok) {
-                                const int idx = atomicAdd(&hdr->counter, 1);
                                 UnitSlot us;
-                                if (idx < num_units) {
-                                    us.u = p.units[idx];
-                                    us.s = p.seqs[us.u.b];
+                                if constexpr (kExt) {
+                                    claim_unit_ext(p, hdr, num_units, us, ctl->ext[sl]);
                                 } else {
-                                    us.u.b = -1;
+                                    const int idx = atomicAdd(&hdr->counter, 1);
+                                    if (idx < num_units) {
+                                        us.u = p.units[idx];
+                                        us.s = p.seqs[us.u.b];
+                                    } else {
+                                        us.u.b = -1;
+                                    }
                                 }
                                 ctl->slot[sl] = us;
                                 mbar_arrive(&ctl->unit_full[sl]);
@@ -667,6 +743,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     __syncwarp(gmask);  // the slot written by lane 0 (K) / acquired by lane 16 (V) is visible
                     u = ctl->slot[sl].u;
                     s = ctl->slot[sl].s;
+                    const int s0 = kExt ? ctl->ext[sl].x : 0;
                     __syncwarp(gmask);
                     if (is_v && gleader) mbar_arrive(&ctl->unit_empty[sl]);
                     if (u.b < 0) {
@@ -692,15 +769,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         break;
                     }
                     ++u_it;
-                    ug = unit_geo<true, kAlt>(u, s, tps, p.causal, p.window, unit_slots);
+                    ug = unit_geo<true, kAlt, kExt>(u, s, s0, tps, p, unit_slots);
                     tab = p.block_table + (size_t)u.b * p.max_blocks;
+                    if constexpr (kExt)
+                        if (ug.pre) tab = p.prefix_table;
                     j = 0;
                     ntl = ug.ntiles;
-                    if (ntl > 0) fetch_ids(ug.lo, id0, id1);
+                    if (ntl > 0) fetch_ids(tile_at<kExt>(ug, 0), id0, id1);
                 }
                 if (!done) {
-                    const int jj = ug.lo + j;
-                    if (j + 1 < ntl) fetch_ids(jj + 1, nid0, nid1);  // in flight during this tile
+                    const int jj = tile_at<kExt>(ug, j);
+                    if (j + 1 < ntl) fetch_ids(tile_at<kExt>(ug, j + 1), nid0, nid1);  // in flight during this tile
                     const bool ok = gleader ? wait_bar(&empty[st], ph ^ 1, ctl, hdr) : true;
                     if (!__shfl_sync(gmask, ok, src)) {
                         done = true;
@@ -779,13 +858,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             for (int u_it = 0;; ++u_it) {
                 const int sl = u_it & 1;
                 if (!wait_bar(&ctl->unit_empty[sl], ((u_it >> 1) & 1) ^ 1, ctl, hdr)) break;
-                const int idx = atomicAdd(&hdr->counter, 1);
                 UnitSlot us;
-                if (idx < num_units) {
-                    us.u = p.units[idx];
-                    us.s = p.seqs[us.u.b];
+                if constexpr (kExt) {
+                    claim_unit_ext(p, hdr, num_units, us, ctl->ext[sl]);
                 } else {
-                    us.u.b = -1;
+                    const int idx = atomicAdd(&hdr->counter, 1);
+                    if (idx < num_units) {
+                        us.u = p.units[idx];
+                        us.s = p.seqs[us.u.b];
+                    } else {
+                        us.u.b = -1;
+                    }
                 }
                 ctl->slot[sl] = us;
                 mbar_arrive(&ctl->unit_full[sl]);
@@ -801,11 +884,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         tma_load_3d(q_smem + i * C::kTileBytes + c * C::kChunkBytes, &p.tm_q, &ctl->q_full,
                                     c * C::kChunkCols, u.kvh * G, s.q_start + u.q0 + i * tps);
                 last_q_parity[0] = u_it & 1;
-                const UnitGeo ug = unit_geo<kPaged, kAlt>(u, s, tps, p.causal, p.window, unit_slots);
+                const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(u, s, kExt ? ctl->ext[sl].x : 0, tps, p, unit_slots);
+                const CUtensorMap* tm_c = &p.tm_ck;
+                int z = u.b * p.n_kv_heads + u.kvh;
+                if constexpr (kExt)
+                    if (ug.pre) tm_c = &p.tm_pk, z = u.kvh;
                 bool ok = true;
                 for (int j = 0; j < ug.ntiles && ok; ++j, ++t)
-                    ok = load_kv_tile<D, kQuant>(p, ctl, hdr, k_smem, kStK, ctl->k_full, ctl->k_empty, &p.tm_ck,
-                                                 &p.tm_k, last_k_parity, t, ug.lo + j, u, s, ug.np);
+                    ok = load_kv_tile<D, kQuant>(p, ctl, hdr, k_smem, kStK, ctl->k_full, ctl->k_empty, tm_c, &p.tm_k,
+                                                 last_k_parity, t, tile_at<kExt>(ug, j), u, s, ug.np, z);
                 if (!ok) break;
             }
             if (aborted(ctl)) {
@@ -821,13 +908,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 const int sl = u_it & 1;
                 if (!wait_bar(&ctl->unit_full[sl], (u_it >> 1) & 1, ctl, hdr)) break;
                 const UnitSlot us = ctl->slot[sl];
+                const int s0 = kExt ? ctl->ext[sl].x : 0;
                 mbar_arrive(&ctl->unit_empty[sl]);
                 if (us.u.b < 0) break;
-                const UnitGeo ug = unit_geo<kPaged, kAlt>(us.u, us.s, tps, p.causal, p.window, unit_slots);
+                const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(us.u, us.s, s0, tps, p, unit_slots);
+                const CUtensorMap* tm_c = &p.tm_cv;
+                int z = us.u.b * p.n_kv_heads + us.u.kvh;
+                if constexpr (kExt)
+                    if (ug.pre) tm_c = &p.tm_pv, z = us.u.kvh;
                 bool ok = true;
                 for (int j = 0; j < ug.ntiles && ok; ++j, ++t)
-                    ok = load_kv_tile<D, kQuant>(p, ctl, hdr, v_smem, C::kStagesV, ctl->v_full, ctl->v_empty, &p.tm_cv,
-                                                 &p.tm_v, last_v_parity, t, ug.lo + j, us.u, us.s, ug.np);
+                    ok = load_kv_tile<D, kQuant>(p, ctl, hdr, v_smem, C::kStagesV, ctl->v_full, ctl->v_empty, tm_c,
+                                                 &p.tm_v, last_v_parity, t, tile_at<kExt>(ug, j), us.u, us.s, ug.np, z);
                 if (!ok) break;
             }
             if (aborted(ctl)) drain(ctl->v_full, last_v_parity, C::kStagesV);
@@ -909,10 +1001,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             if (!warp_wait(&ctl->unit_full[sl], (u_it >> 1) & 1, ctl, hdr)) break;
             const Unit u = ctl->slot[sl].u;
             const SeqInfo s = ctl->slot[sl].s;
+            const int s0 = kExt ? ctl->ext[sl].x : 0;
             __syncwarp();
             if (leader) mbar_arrive(&ctl->unit_empty[sl]);
             if (u.b < 0) break;
-            const UnitGeo ug = unit_geo<kPaged, kAlt>(u, s, tps, p.causal, p.window, unit_slots);
+            const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(u, s, s0, tps, p, unit_slots);
+            auto at = [&](int j) { return tile_at<kExt>(ug, j); };
             const int ntiles = ug.ntiles;
             if (!warp_wait(&ctl->q_full, u_it & 1, ctl, hdr)) break;
             if constexpr (kAlt) if (ug.alt) {
@@ -928,13 +1022,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 };
                 // slot i takes the tiles j with j % 2 == i, both from Q tile 0:
                 // S_0(0), S_1(1), then per tile j: PV_i(j), S_i(j + 2)
-                if (!wait_k(t, ug.lo, ug.np)) break;
+                if (!wait_k(t, at(0), ug.np)) break;
                 tc_fence_after();
-                issue_s(0, t, 0, ug.lo < ug.np);
+                issue_s(0, t, 0, at(0) < ug.np);
                 commit(&ctl->k_empty[t % kStK]);
-                if (!wait_k(t + 1, ug.lo + 1, ug.np)) break;
+                if (!wait_k(t + 1, at(1), ug.np)) break;
                 tc_fence_after();
-                issue_s(1, t + 1, 0, ug.lo + 1 < ug.np);
+                issue_s(1, t + 1, 0, at(1) < ug.np);
                 commit(&ctl->k_empty[(t + 1) % kStK]);
                 if (ntiles == 2) commit(&ctl->q_empty);
                 for (int j = 0; j < ntiles && ok; ++j) {
@@ -942,13 +1036,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     const int i = j & 1, kth = j >> 1;
                     if (!warp_wait(&ctl->p_full[i], (ns[i] + kth) & 1, ctl, hdr)) { ok = false; break; }
                     if (kth == 0 && !warp_wait(&ctl->o_empty[i], (no[i] & 1) ^ 1, ctl, hdr)) { ok = false; break; }
-                    if (!wait_v(tj, ug.lo + j)) { ok = false; break; }
+                    if (!wait_v(tj, at(j))) { ok = false; break; }
                     tc_fence_after();
-                    issue_pv(i, tj, kth == 0, ug.lo + j < ug.np);
+                    issue_pv(i, tj, kth == 0, at(j) < ug.np);
                     if (j + 2 < ntiles) {
-                        if (!wait_k(tj + 2, ug.lo + j + 2, ug.np)) { ok = false; break; }
+                        if (!wait_k(tj + 2, at(j + 2), ug.np)) { ok = false; break; }
                         tc_fence_after();
-                        issue_s(i, tj + 2, 0, ug.lo + j + 2 < ug.np);
+                        issue_s(i, tj + 2, 0, at(j + 2) < ug.np);
                         commit(&ctl->k_empty[(tj + 2) % kStK]);
                         if (j + 3 == ntiles) commit(&ctl->q_empty);
                     }
@@ -962,10 +1056,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 continue;
             }
             // prologue: S of tile 0 for the slots that start there
-            if (!wait_k(t, ug.lo, ug.np)) break;
+            if (!wait_k(t, at(0), ug.np)) break;
             tc_fence_after();
             for (int i = 0; i < kSlots; ++i)
-                if (ug.a[i] == 0 && ug.b[i] > 0) issue_s(i, t, i, ug.lo < ug.np);
+                if (ug.a[i] == 0 && ug.b[i] > 0) issue_s(i, t, i, at(0) < ug.np);
             commit(&ctl->k_empty[t % kStK]);
             if (ntiles == 1) commit(&ctl->q_empty);
             for (int j = 0; j < ntiles && ok; ++j) {
@@ -979,12 +1073,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         if (!v_ready) {
                             const int vst = tj % C::kStagesV;
                             bool got;
-                            if (kQuant && ug.lo + j < ug.np) {
+                            if (kQuant && at(j) < ug.np) {
                                 // int8 prefix tile (a paged tail included: its rows past P
                                 // get scale 0 in the expansion)
                                 got = warp_wait(&ctl->v_conv[vst], (vcpar >> vst) & 1, ctl, hdr);
                                 vcpar ^= 1u << vst;
-                            } else if (kPaged && paged_tail_tile(ug.lo + j, s.P, ug.np)) {
+                            } else if (kPaged && paged_tail_tile(at(j), s.P, ug.np)) {
                                 got = warp_wait(&ctl->v_fix[vst], (fixpar >> vst) & 1, ctl, hdr);
                                 fixpar ^= 1u << vst;
                             } else {
@@ -997,19 +1091,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                             v_ready = true;
                         }
                         tc_fence_after();
-                        issue_pv(i, tj, j == ug.a[i], ug.lo + j < ug.np);
+                        issue_pv(i, tj, j == ug.a[i], at(j) < ug.np);
                     }
                     if (j + 1 >= ug.a[i] && j + 1 < ug.b[i]) {
                         // S_i(j+1) overwrites P_i(j): issued after PV_i(j) on the in-order tensor pipe
                         if (!k_ready) {
-                            if (!wait_k(tj + 1, ug.lo + j + 1, ug.np)) {
+                            if (!wait_k(tj + 1, at(j + 1), ug.np)) {
                                 ok = false;
                                 break;
                             }
                             k_ready = true;
                             tc_fence_after();
                         }
-                        issue_s(i, tj + 1, i, ug.lo + j + 1 < ug.np);
+                        issue_s(i, tj + 1, i, at(j + 1) < ug.np);
                     }
                 }
                 if (!ok) break;
@@ -1051,15 +1145,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             const int sl = u_it & 1;
             if (!warp_wait(&ctl->unit_full[sl], (u_it >> 1) & 1, ctl, hdr)) break;
             const UnitSlot us = ctl->slot[sl];
+            const int s0 = kExt ? ctl->ext[sl].x : 0;
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->unit_empty[sl]);
             if (us.u.b < 0) break;
-            const UnitGeo ug = unit_geo<kPaged, kAlt>(us.u, us.s, tps, p.causal, p.window, unit_slots);
+            const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(us.u, us.s, s0, tps, p, unit_slots);
             const int np = ug.np;
             const int q_end = min(us.u.q0 + unit_slots * tps, us.s.n);
             bool ok = true;
             for (int jr = 0; jr < ug.ntiles; ++jr, ++t) {
-                const int j = ug.lo + jr;  // tile index in the sequence
+                const int j = tile_at<kExt>(ug, jr);  // tile index in the sequence
                 const int st = t % stages;
                 if (kQuant && j < np) {
                     // int8 prefix tile: expand the codes for the MMA.  V rows
@@ -1072,6 +1167,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         // row scales through the block table; rows from P on (rest of the
                         // last block, stale rows) get scale 0 and so expand to zeros
                         const int32_t* tab = p.block_table + (size_t)us.u.b * p.max_blocks;
+                        if constexpr (kExt)
+                            if (ug.pre) tab = p.prefix_table;
                         const int bmask = (1 << p.block_log2) - 1;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
@@ -1086,6 +1183,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         }
                     } else {
                         const float* srow = scales + ((size_t)us.u.b * p.n_kv_heads + us.u.kvh) * p.max_cache_len;
+                        if constexpr (kExt)
+                            if (ug.pre)
+                                srow = (is_k ? p.prefix_scale_k : p.prefix_scale_v) + (size_t)us.u.kvh * p.prefix_cap;
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const int row = kb + 32 * q + lane;  // rows below 0 are zero-filled codes
@@ -1201,16 +1301,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             const int sl = u_it & 1;
             if (!warp_wait(&ctl->unit_full[sl], (u_it >> 1) & 1, ctl, hdr)) break;
             const UnitSlot us = ctl->slot[sl];
+            const int2 ext = kExt ? ctl->ext[sl] : make_int2(0, -1);
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->unit_empty[sl]);
             if (us.u.b < 0) break;
             const Unit u = us.u;
             const SeqInfo s = us.s;
-            const UnitGeo ug = unit_geo<kPaged, kAlt>(u, s, tps, p.causal, p.window, unit_slots);
+            const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(u, s, ext.x, tps, p, unit_slots);
             bool alt = false;
             if constexpr (kAlt) alt = ug.alt;
             const int np = ug.np;
-            const int Lk = s.P + s.n;
+            const int Lk = kExt && ug.pre ? s.P : s.P + s.n;
+            const bool causal = p.causal && !(kExt && ug.pre);
             // rows of each slot (alt: both slots hold slot 0's rows)
             int tok[kSlots], row_hi[kSlots], slot_hi[kSlots], row_lo[kSlots], slot_lo[kSlots];
             bool valid[kSlots];
@@ -1220,11 +1322,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 const int qe = min(qs + tps, s.n);
                 tok[i] = qs + r / G;
                 valid[i] = r < tps * G && tok[i] < s.n;
-                row_hi[i] = p.causal ? min(s.P + tok[i] + 1, Lk) : Lk;  // keys [0, row_hi) visible
-                slot_hi[i] = p.causal ? min(s.P + qs + 1, Lk) : Lk;    // smallest row_hi of the slot
+                row_hi[i] = causal ? min(s.P + tok[i] + 1, Lk) : Lk;  // keys [0, row_hi) visible
+                slot_hi[i] = causal ? min(s.P + qs + 1, Lk) : Lk;    // smallest row_hi of the slot
                 // sliding window: keys [row_lo, row_hi); slot_lo = largest row_lo of the slot
-                row_lo[i] = (p.causal && p.window > 0) ? s.P + tok[i] - p.window + 1 : INT_MIN / 2;
-                slot_lo[i] = (p.causal && p.window > 0) ? s.P + qe - p.window : INT_MIN / 2;
+                row_lo[i] = (causal && p.window > 0) ? s.P + tok[i] - p.window + 1 : INT_MIN / 2;
+                slot_lo[i] = (causal && p.window > 0) ? s.P + qe - p.window : INT_MIN / 2;
             }
             const int hrow = u.kvh * G + r % G;
             float m[kSlots] = {-INFINITY, -INFINITY}, l[kSlots] = {0.f, 0.f};
@@ -1254,16 +1356,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                             sv[32 + c] = __uint_as_float(r1[c]);
                         }
                     }
-                    const int jt = ug.lo + j;  // tile index in the sequence
+                    const int jt = tile_at<kExt>(ug, j);  // tile index in the sequence
                     const int kb = tile_key_base<kPaged>(jt, s.P, np);
                     // paged: the last prefix tile holds prefix keys only below P
                     const bool tail = kPaged && jt < np && kb + kBlockN > s.P;
                     if (kb < 0 || kb + kBlockN > slot_hi[i] || kb < slot_lo[i] || tail) {
                         const int lo = max(-kb, row_lo[i] - kb) - half * kHalfCols;
                         const int hi = (tail ? min(row_hi[i], s.P) : row_hi[i]) - kb - half * kHalfCols;
+                        if constexpr (kExt) {
+                            // sink tokens stay visible below the window: columns [lo0, sink)
+                            const int lo0 = -kb - half * kHalfCols, sink = max(p.sinks, 0) + lo0;
 #pragma unroll
-                        for (int c = 0; c < kHalfCols; ++c)
-                            if (c < lo || c >= hi) sv[c] = -INFINITY;
+                            for (int c = 0; c < kHalfCols; ++c)
+                                if (c < lo0 || c >= hi || (c < lo && c >= sink)) sv[c] = -INFINITY;
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < kHalfCols; ++c)
+                                if (c < lo || c >= hi) sv[c] = -INFINITY;
+                        }
                     }
                     // row max of the warp's columns: four chains of three-input maxima
                     float mx0 = fmaxf(sv[0], sv[1]), mx1 = fmaxf(sv[2], sv[3]);
@@ -1362,6 +1472,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             bool done = false;
             for (int e = 0; e < kSlots && !done; ++e) {
                 // alt: one merged output (e = 0 only); else slot e, if it had tiles
+                if constexpr (kExt) {
+                    // no tile of this piece is the slot's: an empty partial result
+                    if (!alt && e < unit_slots && cnt[e] == 0 && valid[e] && half == 0 && ext.y >= 0)
+                        p.part_lse[(size_t)ext.y * p.slab_rows + (size_t)(s.q_start + tok[e]) * p.n_heads + hrow] =
+                            -INFINITY;
+                }
                 if (alt ? e > 0 : cnt[e] == 0) continue;
                 float lt[kSlots], mm = -INFINITY;
 #pragma unroll
@@ -1387,7 +1503,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     w[i] = c;
                     lsum += lt[i] * c;
                 }
-                const float inv_l = 1.f / lsum;
+                // a piece of the tiles may hold no key of the row: weight 0, lse -inf
+                const float inv_l = kExt && lsum == 0.f ? 0.f : 1.f / lsum;
                 const int orow_slot = alt ? 0 : e;
                 const bool v_ok = valid[orow_slot];
                 const size_t row = (size_t)(s.q_start + tok[orow_slot]) * p.n_heads + hrow;
@@ -1410,7 +1527,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 #pragma unroll
                         for (int q = 0; q < kW; ++q) o[q] = fmaf(__uint_as_float(ob[q]), wi, o[q]);
                     }
-                    if (v_ok) {
+                    if constexpr (kExt) {
+                        if (v_ok && ext.y >= 0) {
+                            float* po = p.part_o + ((size_t)ext.y * p.slab_rows + row) * D + half * kHalfD + c;
+#pragma unroll
+                            for (int g = 0; g < kW; g += 8) {
+                                uint32_t pw[8];
+#pragma unroll
+                                for (int k = 0; k < 8; ++k) pw[k] = __float_as_uint(o[g + k]);
+                                st_global_v8(po + g, pw);
+                            }
+                        }
+                    }
+                    if (v_ok && (!kExt || ext.y < 0)) {
 #pragma unroll
                         for (int g = 0; g < kW / 16; ++g) {
                             uint32_t pw[8];
@@ -1425,7 +1554,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         }
                     }
                 }
-                if (v_ok && half == 0 && p.lse) p.lse[row] = (mm + lg2(lsum)) * 0.69314718055994530942f;
+                if constexpr (kExt) {
+                    if (v_ok && half == 0 && ext.y >= 0)
+                        p.part_lse[(size_t)ext.y * p.slab_rows + row] = mm + lg2(lsum);
+                }
+                if (v_ok && half == 0 && p.lse && (!kExt || ext.y < 0)) p.lse[row] = (mm + lg2(lsum)) * 0.69314718055994530942f;
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
@@ -1454,27 +1587,34 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             const int sl = u_it & 1;
             if (!warp_wait(&ctl->unit_full[sl], (u_it >> 1) & 1, ctl, hdr)) break;
             const UnitSlot us = ctl->slot[sl];
+            const int2 ext = kExt ? ctl->ext[sl] : make_int2(0, -1);
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->unit_empty[sl]);
             if (us.u.b < 0) break;
             const Unit u = us.u;
             const SeqInfo s = us.s;
-            const UnitGeo ug = unit_geo<kPaged, false>(u, s, tps, p.causal, p.window, unit_slots);
+            const UnitGeo ug = unit_geo<kPaged, false, kExt>(u, s, ext.x, tps, p, unit_slots);
             const int nt = ug.b[slot] - ug.a[slot];  // tiles of this slot: [a, b) of the stream
             const uint32_t tg0 = tg;
             tg += ug.ntiles;
-            if (nt == 0) continue;
             const int qs = u.q0 + slot * tps;
-            const int qe = min(qs + tps, s.n);
             const int tok = qs + r / G;
             const int h = u.kvh * G + r % G;
             const bool valid = r < tps * G && tok < s.n;
-            const int Lk = s.P + s.n;
-            const int row_hi = p.causal ? min(s.P + tok + 1, Lk) : Lk;  // keys [0, row_hi) visible
-            const int slot_hi = p.causal ? min(s.P + qs + 1, Lk) : Lk;  // smallest row_hi of the slot
+            if constexpr (kExt) {
+                // no tile of this piece is the slot's: an empty partial result
+                if (nt == 0 && valid && ext.y >= 0)
+                    p.part_lse[(size_t)ext.y * p.slab_rows + (size_t)(s.q_start + tok) * p.n_heads + h] = -INFINITY;
+            }
+            if (nt == 0) continue;
+            const int qe = min(qs + tps, s.n);
+            const int Lk = kExt && ug.pre ? s.P : s.P + s.n;
+            const bool causal = p.causal && !(kExt && ug.pre);
+            const int row_hi = causal ? min(s.P + tok + 1, Lk) : Lk;  // keys [0, row_hi) visible
+            const int slot_hi = causal ? min(s.P + qs + 1, Lk) : Lk;  // smallest row_hi of the slot
             // sliding window: keys [row_lo, row_hi) visible; slot_lo = largest row_lo of the slot
-            const int row_lo = (p.causal && p.window > 0) ? s.P + tok - p.window + 1 : INT_MIN / 2;
-            const int slot_lo = (p.causal && p.window > 0) ? s.P + qe - p.window : INT_MIN / 2;
+            const int row_lo = (causal && p.window > 0) ? s.P + tok - p.window + 1 : INT_MIN / 2;
+            const int slot_lo = (causal && p.window > 0) ? s.P + qe - p.window : INT_MIN / 2;
             const int np = ug.np;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
@@ -1504,7 +1644,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     }
                 }
                 const int jrel = ug.a[slot] + j;  // tile index in the unit's stream
-                const int jt = ug.lo + jrel;  // tile index in the sequence
+                const int jt = tile_at<kExt>(ug, jrel);  // tile index in the sequence
                 if (kQuant && jt < np) {
                     // int8 prefix tile: S holds q . code; scale column c by its row's scale
                     const uint32_t tc = tg0 + jrel;
@@ -1526,9 +1666,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 const bool tail = kPaged && jt < np && kb + kBlockN > s.P;
                 if (kb < 0 || kb + kBlockN > slot_hi || kb < slot_lo || tail) {
                     const int lo = max(-kb, row_lo - kb), hi = (tail ? min(row_hi, s.P) : row_hi) - kb;
+                    if constexpr (kExt) {
+                        // sink tokens stay visible below the window: columns [-kb, sink)
+                        const int sink = max(p.sinks, 0) - kb;
 #pragma unroll
-                    for (int c = 0; c < kBlockN; ++c)
-                        if (c < lo || c >= hi) sv[c] = -INFINITY;
+                        for (int c = 0; c < kBlockN; ++c)
+                            if (c < -kb || c >= hi || (c < lo && c >= sink)) sv[c] = -INFINITY;
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kBlockN; ++c)
+                            if (c < lo || c >= hi) sv[c] = -INFINITY;
+                    }
                 }
                 // row max: four chains of three-input maxima
                 float mx0 = fmaxf(sv[0], sv[1]), mx1 = fmaxf(sv[2], sv[3]);
@@ -1600,7 +1748,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             // epilogue: O of the slot is final once the PV of its last tile is done
             if (!warp_wait(&ctl->pv_done[slot], (ns + nt - 1) & 1, ctl, hdr)) break;
             tc_fence_after();
-            const float inv_l = 1.f / l;
+            const float inv_l = kExt && l == 0.f ? 0.f : 1.f / l;
             const size_t row = (size_t)(s.q_start + tok) * p.n_heads + h;
             uint4* dst = reinterpret_cast<uint4*>(p.out + row * D);
 #pragma unroll
@@ -1609,7 +1757,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 tmem_ld32(o_col + c, o);
                 tmem_wait_ld();
                 reg_fence(o);
-                if (valid) {
+                if constexpr (kExt) {
+                    if (valid && ext.y >= 0) {
+                        float* po = p.part_o + ((size_t)ext.y * p.slab_rows + row) * D + c;
+#pragma unroll
+                        for (int g = 0; g < 32; g += 8) {
+                            uint32_t w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(__uint_as_float(o[g + k]) * inv_l);
+                            st_global_v8(po + g, w);
+                        }
+                    }
+                }
+                if (valid && (!kExt || ext.y < 0)) {
                     // whole 32-byte sectors per store when out allows it: the lanes
                     // of a warp write 32 different rows, so each store is 32 pieces
 #pragma unroll
@@ -1628,7 +1788,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     }
                 }
             }
-            if (valid && p.lse) p.lse[row] = (m + lg2(l)) * 0.69314718055994530942f;
+            if constexpr (kExt) {
+                if (valid && ext.y >= 0) p.part_lse[(size_t)ext.y * p.slab_rows + row] = m + lg2(l);
+            }
+            if (valid && p.lse && (!kExt || ext.y < 0)) p.lse[row] = (m + lg2(l)) * 0.69314718055994530942f;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->o_empty[slot]);
@@ -1642,6 +1805,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
+#ifndef PA_ATTN_LONG
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -1688,17 +1852,18 @@ cudaError_t encode_pool_by_block(CUtensorMap* m, const void* ptr, uint64_t bs, u
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false>
-cudaError_t launch_d(const FwdParams& p, int grid, cudaStream_t st) {
+#endif  // PA_ATTN_LONG
+
+template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
+cudaError_t launch_d(const KernelParams<kExt>& p, int grid, cudaStream_t st) {
     constexpr int kSmem = smem_bytes<D>();
     static_assert(kSmem <= 232448, "shared memory budget");
     static int configured_for[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && !configured_for[dev]) {
-        cudaError_t e =
-            cudaFuncSetAttribute(attn_fwd_kernel<D, kPaged, kQuant, kAlt, kHook>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmem);
+        cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<D, kPaged, kQuant, kAlt, kHook, kExt>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         configured_for[dev] = 1;
     }
@@ -1714,11 +1879,12 @@ cudaError_t launch_d(const FwdParams& p, int grid, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, kPaged, kQuant, kAlt, kHook>, p);
+    return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, kPaged, kQuant, kAlt, kHook, kExt>, p);
 }
 
 }  // namespace
 
+#ifndef PA_ATTN_LONG
 cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_seqs, int head_dim, int num_blocks) {
     const uint32_t cc = head_dim >= 64 ? 64 : 32;
     const CUtensorMapSwizzle sw = head_dim >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -1771,6 +1937,22 @@ cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_se
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+// Tensor maps of a contiguous shared prefix [Hk, prefix_cap, D] (a paged one is read through tm_ck / tm_cv).
+cudaError_t encode_prefix_maps(FwdParamsX& p, int head_dim, const void* prefix_k, const void* prefix_v) {
+    const uint32_t cc = head_dim >= 64 ? 64 : 32;
+    const CUtensorMapSwizzle sw = p.kv_quant        ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                  : head_dim >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                                   : CU_TENSOR_MAP_SWIZZLE_64B;
+    const CUtensorMapDataType dt = p.kv_quant ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint64_t D = head_dim, row = p.kv_quant ? D : 2 * D, cap = p.prefix_cap;
+    const uint32_t box = p.kv_quant ? (uint32_t)head_dim : cc;
+    const cudaError_t e = encode3d(&p.tm_pk, prefix_k, D, cap, p.n_kv_heads, row, cap * row, box, kBlockN, 1, sw,
+                                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, dt);
+    if (e != cudaSuccess) return e;
+    return encode3d(&p.tm_pv, prefix_v, D, cap, p.n_kv_heads, row, cap * row, box, kBlockN, 1, sw,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, dt);
+}
+
 template <int D>
 cudaError_t launch_dim(const FwdParams& p, int grid, cudaStream_t st) {
     static_assert(D == 32 || D == 64 || D == 128, "head_dim");
@@ -1794,5 +1976,21 @@ cudaError_t launch_attn_fwd(const FwdParams& p, int head_dim, int grid, cudaStre
         default: return cudaErrorInvalidValue;
     }
 }
+#else
+// attn_long_*.cu include this file with PA_ATTN_LONG = the head_dim they compile
+// the long-context variant for (one translation unit each, built in parallel).
+template <>
+cudaError_t launch_attn_long_d<PA_ATTN_LONG>(const FwdParamsX& p, int grid, cudaStream_t st) {
+    constexpr int D = PA_ATTN_LONG;
+    if (p.block_table) {
+        if (p.kv_quant) return launch_d<D, true, true, false, false, true>(p, grid, st);
+        return p.alt ? launch_d<D, true, false, true, false, true>(p, grid, st)
+                     : launch_d<D, true, false, false, false, true>(p, grid, st);
+    }
+    if (p.kv_quant) return launch_d<D, false, true, false, false, true>(p, grid, st);
+    return p.alt ? launch_d<D, false, false, true, false, true>(p, grid, st)
+                 : launch_d<D, false, false, false, false, true>(p, grid, st);
+}
+#endif  // PA_ATTN_LONG
 
 }  // namespace pa

@@ -36,6 +36,16 @@ struct Unit {
     int ntiles;  // KV tiles the unit visits (its cost; the later slot visits all of them)
 };
 
+// Work unit of the long-context variant: tiles [s0, s0 + u.ntiles) of the
+// stream of its query block.  slab >= 0: a partial result goes to that slab
+// and a merge follows; -1: the unit writes its rows of out itself.  u.b =
+// num_seqs: a block of the whole batch's tokens against the shared prefix.
+struct UnitX {
+    Unit u;
+    int s0;
+    int slab;
+};
+
 // Device workspace header; SeqInfo[num_seqs] and Unit[max_units] follow it.
 struct WorkspaceHeader {
     int error;       // PA_DEVERR_* bits, sticky until read by prefill_attn_device_status
@@ -102,6 +112,34 @@ __host__ __device__ inline TileSpan query_tiles(int n, int P, int qs, int qe, in
     t.lo = key_tile(klo, P, paged);
     t.hi = key_tile(khi - 1, P, paged) + 1;
     return t;
+}
+
+// The tiles of query tokens [qs, qe) when the first `sinks` keys stay visible
+// below the window: sink tiles [0, nsink), then [lo, hi), lo >= nsink (nsink is
+// 0 when the window reaches tile 0).  pre: the tokens see a shared prefix of P
+// keys whole, and nothing else.
+struct StreamGeo {
+    int nsink, lo, hi;
+};
+
+__host__ __device__ inline StreamGeo stream_geo(int n, int P, int qs, int qe, int causal, int window, int sinks,
+                                                bool pre, bool paged) {
+    StreamGeo g;
+    g.nsink = 0;
+    if (pre) {
+        g.lo = 0;
+        g.hi = prefix_tiles(P);
+        return g;
+    }
+    const TileSpan t = query_tiles(n, P, qs, qe, causal, window, paged);
+    g.lo = t.lo;
+    g.hi = t.hi;
+    if (sinks > 0 && t.lo > 0) {
+        const int last = (causal ? P + qe : P + n) - 1;  // last visible key
+        const int ns = key_tile(sinks - 1 < last ? sinks - 1 : last, P, paged) + 1;
+        g.nsink = ns < t.lo ? ns : t.lo;
+    }
+    return g;
 }
 
 // KV tiles a work unit streams (its cost): tokens [q0, min(q0 + tokens, n)).

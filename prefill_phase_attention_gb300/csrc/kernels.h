@@ -20,6 +20,7 @@ struct RopeParams {
     const int32_t* cu_seqlens_q;
     const SeqInfo* seqs;
     int total_q, num_seqs, n_heads, n_kv_heads, head_dim;
+    int pos0;            // position of a sequence's first cached token (tokens of a shared prefix)
     float inv_freq[64];  // inv_freq[i] = 1 / base^(2i / d), i < d/2
 };
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
@@ -78,5 +79,99 @@ struct FwdParams {
 // num_blocks: blocks in the pool when p.block_table is set (else unused).
 cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_seqs, int head_dim, int num_blocks);
 cudaError_t launch_attn_fwd(const FwdParams& p, int head_dim, int grid, cudaStream_t st);
+
+// Parameters of the long-context variant: sink tokens, a prefix the batch
+// shares, and units whose tiles are split between CTAs (pieces).
+struct FwdParamsX : FwdParams {
+    CUtensorMap tm_pk;  // contiguous shared prefix [Hk, prefix_cap, D] viewed (D, cap, Hk), box as tm_ck
+    CUtensorMap tm_pv;
+    const UnitX* xunits;          // instead of `units`
+    int num_seqs;                 // Unit::b of a prefix unit (its SeqInfo: all tokens, P = prefix_len)
+    int sinks;                    // sink tokens (0: none)
+    int prefix_len;               // tokens of the shared prefix (0: none)
+    int prefix_cap;               // rows per head of a contiguous prefix
+    const int32_t* prefix_table;  // blocks of a paged prefix
+    const float* prefix_scale_k;  // int8 contiguous prefix: fp32 scale of each row
+    const float* prefix_scale_v;
+    // partial results: slab s holds rows [s * slab_rows, ...), one per (token, head):
+    // normalised fp32 output and log2-sum-exp2 over the keys of the piece
+    float* part_o;
+    float* part_lse;
+    size_t slab_rows;             // total_q * n_heads
+};
+cudaError_t encode_prefix_maps(FwdParamsX& p, int head_dim, const void* prefix_k, const void* prefix_v);
+template <int D>
+cudaError_t launch_attn_long_d(const FwdParamsX& p, int grid, cudaStream_t st);
+template <>
+cudaError_t launch_attn_long_d<32>(const FwdParamsX& p, int grid, cudaStream_t st);
+template <>
+cudaError_t launch_attn_long_d<64>(const FwdParamsX& p, int grid, cudaStream_t st);
+template <>
+cudaError_t launch_attn_long_d<128>(const FwdParamsX& p, int grid, cudaStream_t st);
+
+// Scheduler of the long-context variant.
+struct LongScheduleArgs : ScheduleArgs {
+    UnitX* xunits;
+    int* seq_pieces;  // [num_seqs + 1] pieces each query block of the sequence is cut into (last: the prefix's)
+    int* tok_pieces;  // [total_q] slabs that the merge joins for a token (0: none); nullptr: no merge
+    int sinks;
+    int prefix_len;
+    const int32_t* prefix_table;
+    int max_pieces, max_prefix_pieces;  // slabs the workspace has for each
+    int target_units;  // units wanted in flight (a multiple of the CTAs)
+    int min_tiles;     // no piece smaller than this is cut
+};
+cudaError_t launch_build_long_schedule(const LongScheduleArgs& a, cudaStream_t stream);
+
+// Joins the partial results of every (token, head): the token's own slabs
+// [0, tok_pieces) and the prefix's [prefix_slab, prefix_slab + *prefix_pieces).
+struct MergeArgs {
+    const float* part_o;
+    const float* part_lse;
+    const int* tok_pieces;
+    const int* prefix_pieces;  // nullptr: no prefix
+    int prefix_slab;
+    __nv_bfloat16* out;
+    float* lse;
+    int total_q, n_heads;
+};
+cudaError_t launch_merge(const MergeArgs& a, int head_dim, cudaStream_t stream);
+
+// Weight each cached key collects from the new queries.
+struct KeyWeightsArgs {
+    const __nv_bfloat16* q;  // [T, H, d]
+    const __nv_bfloat16* k;  // [T, Hk, d]
+    const void* cache_k;     // bf16 rows, or int8 codes with scale_k
+    const float* scale_k;
+    const float* lse;        // [T, H]
+    float* weights;          // one per cache row
+    const SeqInfo* seqs;
+    WorkspaceHeader* hdr;
+    int num_seqs, total_q, n_heads, n_kv_heads, group, max_cache_len;
+    float scale_log2;
+    int causal, window, sinks;
+    const int32_t* block_table;
+    int block_log2, max_blocks, num_blocks;
+};
+cudaError_t launch_key_weights(const KeyWeightsArgs& a, int head_dim, int sms, cudaStream_t stream);
+
+// Eviction by weight, in place.
+struct EvictArgs {
+    void* cache_k;
+    void* cache_v;
+    int row_bytes;  // of one cached key or value
+    float* scale_k;
+    float* scale_v;
+    const float* weights;
+    float* kept_weights;
+    const int32_t* lengths;
+    int32_t* kept_lengths;
+    int32_t* index;  // [num_seqs, n_kv_heads, budget] kept positions, -1 past the last
+    WorkspaceHeader* hdr;
+    int num_seqs, n_kv_heads, max_cache_len, budget, sinks, recent;
+    const int32_t* block_table;
+    int block_log2, max_blocks, num_blocks;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 
 }  // namespace pa

@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
             }
             const SeqInfo si = p.seqs[lo];  // sanitised by the scheduler (n = 0 when rejected)
             if (t >= si.q_start && t < (long long)si.q_start + si.n) {
-                const float angle = __fmul_rn((float)(si.P + (int)(t - si.q_start)), p.inv_freq[i]);
+                const float angle = __fmul_rn((float)(p.pos0 + si.P + (int)(t - si.q_start)), p.inv_freq[i]);
                 sincosf(angle, &s, &c);
             }
         }

@@ -1,0 +1,294 @@
+// schedule_long.cu -- tile scheduler and merge of the long-context variant.
+//
+// The list is laid out as in schedule.cu (sequences by descending cost, KV
+// heads in L2-sized groups, blocks last to first), with two additions:
+//  - a prefix that the batch shares is one more sequence, whose query blocks
+//    are cut from the whole batch's tokens and see the prefix's tiles only;
+//  - query blocks with many tiles are cut into pieces along the keys, so that
+//    a few long rows still fill the GPU.  The pieces of a block write partial
+//    results (fp32 output and log-sum-exp) into slabs that merge_kernel joins.
+//
+// Piece size: the whole call's tiles over target_units, at least min_tiles.
+// All blocks of a sequence get the same number of pieces (that of its longest
+// block); a block with fewer tiles than pieces leaves holes in the list.
+#include <cuda_bf16.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "prefill_attn.h"
+#include "ptx.cuh"
+#include "schedule.cuh"
+
+namespace pa {
+
+namespace {
+
+__global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_constant__ LongScheduleArgs a) {
+    __shared__ int hist[kCostBins];
+    __shared__ int warp_sums[32];
+    __shared__ unsigned long long s_total;
+    __shared__ SeqInfo s_seqs[kSmemSeqs];
+    __shared__ int s_scratch[kSmemSeqs], s_group[kSmemSeqs], s_pieces[kSmemSeqs];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nthr = blockDim.x, nwarps = nthr >> 5;
+    const int tpu = a.unit_slots * (kBlockM / a.group);  // query tokens per unit
+    const bool shared_prefix = a.prefix_len > 0;
+    const int nseq = a.num_seqs + (shared_prefix ? 1 : 0);
+    griddep_launch();
+    const bool small = nseq <= kSmemSeqs;
+    SeqInfo* const seqs = small ? s_seqs : a.seqs;
+    int* const seq_scratch = small ? s_scratch : a.seq_scratch;
+    int* const seq_group = small ? s_group : a.seq_group;
+    int* const pieces = small ? s_pieces : a.seq_pieces;
+
+    for (int i = tid; i < kCostBins; i += nthr) hist[i] = 0;
+    if (tid == 0) s_total = 0;
+
+    // every block that a sequence (or the prefix) touches must be one of the pool's
+    const bool paged = a.block_table != nullptr;
+    bool bad_prefix = false;
+    if (paged) {
+        for (int b = warp; b < a.num_seqs; b += nwarps) {
+            const long long lk = (long long)a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
+            const long long used = lk > 0 ? (lk + a.block_size - 1) / a.block_size : 0;
+            const int nb = used < a.max_blocks ? (int)used : a.max_blocks;
+            bool bad = false;
+            for (int L = lane; L < nb; L += 32) {
+                const int blk = a.block_table[(size_t)b * a.max_blocks + L];
+                bad |= blk < 0 || blk >= a.num_blocks;
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            if (lane == 0) seqs[b].pad = bad ? 1 : 0;
+        }
+        if (shared_prefix) {
+            const int nb = (a.prefix_len + a.block_size - 1) / a.block_size;
+            for (int L = tid; L < nb; L += nthr) bad_prefix |= a.prefix_table[L] < 0 || a.prefix_table[L] >= a.num_blocks;
+        }
+        __threadfence_block();
+        bad_prefix = __syncthreads_or(bad_prefix);
+    }
+
+    // Pass 1: sanitise each sequence; number its query blocks.
+    int blocks_before = 0;
+    for (int b0 = 0; b0 < nseq; b0 += nthr) {
+        const int b = b0 + tid;
+        SeqInfo si{0, 0, 0, 0};
+        if (b < a.num_seqs) {
+            const int q_start = a.cu_seqlens_q[b];
+            const int q_end = a.cu_seqlens_q[b + 1];
+            const int lk = a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
+            const int P = a.cache_offsets[b];
+            const long long n = (long long)q_end - q_start;
+            const bool ok = q_start >= 0 && n >= 0 && (long long)q_end <= a.total_q && P >= 0 &&
+                            (long long)lk == (long long)P + n && (long long)P + n <= a.max_cache_len &&
+                            (b > 0 || q_start == 0) && !(paged && seqs[b].pad != 0) && !bad_prefix;
+            if (!ok) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
+            si.q_start = ok ? q_start : 0;
+            si.n = ok ? (int)n : 0;
+            si.P = ok ? P : 0;
+        } else if (b == a.num_seqs && shared_prefix && !bad_prefix) {
+            const int end = a.cu_seqlens_q[a.num_seqs];
+            si.n = end < 0 ? 0 : (end < a.total_q ? end : a.total_q);
+            si.P = a.prefix_len;
+        }
+        const int nblk = (si.n + tpu - 1) / tpu;
+        int chunk_total;
+        const int excl = block_exclusive_scan(nblk, warp_sums, &chunk_total);
+        si.pad = blocks_before + excl;
+        if (b < nseq) {
+            a.seqs[b] = si;
+            if (small) s_seqs[b] = si;
+        }
+        blocks_before += chunk_total;
+    }
+    const int total_blocks = blocks_before;
+    if (a.tok_pieces)
+        for (int t = tid; t < a.total_q; t += nthr) a.tok_pieces[t] = 0;
+    __threadfence_block();
+    __syncthreads();
+
+    // tiles of the stream of query block blk of sequence si
+    auto block_tiles = [&](const SeqInfo& si, int blk, bool pre) {
+        const int q0 = blk * tpu, qe = q0 + tpu < si.n ? q0 + tpu : si.n;
+        const StreamGeo g = stream_geo(si.n, si.P, q0, qe, a.causal, a.window, a.sinks, pre, paged);
+        return g.nsink + g.hi - g.lo;
+    };
+
+    // Pass 2 (one warp per sequence): its tiles per head and its longest block.
+    for (int b = warp; b < nseq; b += nwarps) {
+        const SeqInfo si = seqs[b];
+        const int nblk = (si.n + tpu - 1) / tpu;
+        long long c = 0;
+        int mx = 0;
+        for (int i = lane; i < nblk; i += 32) {
+            const int t = block_tiles(si, i, b == a.num_seqs);
+            c += t;
+            mx = max(mx, t);
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            c += __shfl_xor_sync(0xffffffffu, c, o);
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
+        if (lane == 0) {
+            seq_scratch[b] = (int)(c < 0x7fffffffll ? c : 0x7fffffffll);
+            seq_group[b] = mx;
+            if (c > 0) atomicAdd(&s_total, (unsigned long long)c * a.n_kv_heads);
+        }
+    }
+    __threadfence_block();
+    __syncthreads();
+
+    // Pieces per block, the sequence's cost bin and its KV-head group.
+    const long long piece =
+        max((long long)a.min_tiles, (long long)((s_total + a.target_units - 1) / (unsigned)a.target_units));
+    for (int b = tid; b < nseq; b += nthr) {
+        const SeqInfo si = seqs[b];
+        const int nblk = (si.n + tpu - 1) / tpu;
+        const int c = seq_scratch[b], mx = seq_group[b];
+        const bool pre = b == a.num_seqs;
+        int p = (int)((mx + piece - 1) / piece);
+        p = max(1, min(p, pre ? a.max_prefix_pieces : a.max_pieces));
+        pieces[b] = p;
+        a.seq_pieces[b] = p;
+        if (nblk > 0) {
+            const int bin = cost_bin((long long)c * a.n_kv_heads / p);
+            seq_scratch[b] = bin;
+            seq_group[b] = kv_head_group(si, a.head_dim, a.n_kv_heads, a.num_ctas, c, (mx + p - 1) / p);
+            atomicAdd(&hist[bin], nblk * a.n_kv_heads * p);
+        }
+    }
+    __threadfence_block();
+    __syncthreads();
+
+    // Exclusive scan in descending cost order.
+    static_assert(kCostBins == 2 * 1024, "scan assumes two bins per thread");
+    const int r0 = kCostBins - 1 - 2 * tid;
+    const int h0 = hist[r0], h1 = hist[r0 - 1];
+    int total;
+    const int excl = block_exclusive_scan(h0 + h1, warp_sums, &total);
+    hist[r0] = excl;
+    hist[r0 - 1] = excl + h0;
+    if (tid == 0) {
+        a.hdr->num_units = total < a.max_units ? total : a.max_units;
+        a.hdr->counter = 0;
+        a.hdr->max_units = a.max_units;
+        if (total > a.max_units) atomicOr(&a.hdr->error, PA_DEVERR_OVERFLOW);
+    }
+    __syncthreads();
+
+    // Pass 3: each sequence claims its range of the list ...
+    for (int b = tid; b < nseq; b += nthr) {
+        const int nblk = (seqs[b].n + tpu - 1) / tpu;
+        if (nblk > 0) seq_scratch[b] = atomicAdd(&hist[seq_scratch[b]], nblk * a.n_kv_heads * pieces[b]);
+    }
+    __threadfence_block();
+    __syncthreads();
+
+    // ... and its units go there.
+    const int total_units = total_blocks * a.n_kv_heads;
+    for (int w = tid; w < total_units; w += nthr) {
+        const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
+        const int b = block_owner(seqs, nseq, i);
+        const bool pre = b == a.num_seqs;
+        const SeqInfo si = seqs[b];
+        const int blk = i - si.pad;
+        const int nblk = (si.n + tpu - 1) / tpu;
+        const int hg = seq_group[b];
+        const int g0 = kvh - kvh % hg;
+        const int gsize = min(hg, a.n_kv_heads - g0);
+        const int p = pieces[b];
+        const int pos = seq_scratch[b] + (g0 * nblk + (nblk - 1 - blk) * gsize + (kvh - g0)) * p;
+        const int c = block_tiles(si, blk, pre);
+        const int pb = min(p, c);  // pieces of this block
+        const bool partial = shared_prefix || p > 1;
+        for (int k = 0; k < p; ++k) {
+            if (pos + k >= a.max_units) break;
+            UnitX x;
+            x.u.b = b;
+            x.u.kvh = kvh;
+            x.u.q0 = blk * tpu;
+            x.s0 = k < pb ? (int)((long long)c * k / pb) : 0;
+            x.u.ntiles = k < pb ? (int)((long long)c * (k + 1) / pb) - x.s0 : 0;
+            x.slab = partial ? (pre ? a.max_pieces : 0) + k : -1;
+            a.xunits[pos + k] = x;
+        }
+    }
+    if (!a.tok_pieces) return;
+    const int span = min(tpu, a.total_q);  // tokens of a block
+    for (int w = tid; w < total_blocks * span; w += nthr) {
+        const int i = w / span, off = w % span;
+        const int b = block_owner(seqs, nseq, i);
+        const SeqInfo si = seqs[b];
+        const int blk = i - si.pad, tok = blk * tpu + off;
+        if (b == a.num_seqs || tok >= si.n) continue;
+        const int p = pieces[b];
+        if (shared_prefix || p > 1) a.tok_pieces[si.q_start + tok] = min(p, block_tiles(si, blk, false));
+    }
+}
+
+// One row (token, head) per D / 4 lanes; the row's slabs are read 4 at a time.
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ MergeArgs a) {
+    constexpr int kLanes = D / 4;
+    griddep_wait();
+    const long long rows = (long long)a.total_q * a.n_heads;
+    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+    if (row >= rows) return;
+    const int c = threadIdx.x % kLanes * 4;
+    const int own = a.tok_pieces[row / a.n_heads];
+    if (own == 0) return;  // not this call's, or written by its unit
+    const int n = own + (a.prefix_pieces ? *a.prefix_pieces : 0);
+    auto slab = [&](int i) { return (size_t)(i < own ? i : a.prefix_slab + i - own) * rows + row; };
+    float m = -INFINITY;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, a.part_lse[slab(i)]);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const size_t s = slab(i);
+        const float l = a.part_lse[s];
+        const float4 o = *reinterpret_cast<const float4*>(a.part_o + s * D + c);
+        const float w = l == -INFINITY ? 0.f : exp2f(l - m);
+        if (w == 0.f) continue;  // an empty piece: its output was not written
+        sum += w;
+        acc.x = fmaf(w, o.x, acc.x);
+        acc.y = fmaf(w, o.y, acc.y);
+        acc.z = fmaf(w, o.z, acc.z);
+        acc.w = fmaf(w, o.w, acc.w);
+    }
+    const float inv = 1.f / sum;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+    uint2 packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    *reinterpret_cast<uint2*>(a.out + row * D + c) = packed;
+    if (c == 0 && a.lse) a.lse[row] = (m + log2f(sum)) * 0.69314718055994530942f;
+}
+
+}  // namespace
+
+cudaError_t launch_build_long_schedule(const LongScheduleArgs& a, cudaStream_t stream) {
+    build_long_schedule_kernel<<<1, 1024, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_merge(const MergeArgs& a, int head_dim, cudaStream_t stream) {
+    const long long threads = (long long)a.total_q * a.n_heads * (head_dim / 4);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((threads + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    switch (head_dim) {
+        case 32: return cudaLaunchKernelEx(&cfg, merge_kernel<32>, a);
+        case 64: return cudaLaunchKernelEx(&cfg, merge_kernel<64>, a);
+        default: return cudaLaunchKernelEx(&cfg, merge_kernel<128>, a);
+    }
+}
+
+}  // namespace pa

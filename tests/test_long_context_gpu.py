@@ -1,0 +1,441 @@
+"""GPU tests of the long-context calls: windowed attention with sink tokens, a
+prefix that the batch shares, key weights and eviction, each against its plain
+64-bit form (tests/long_reference.py, where the tolerances are derived)."""
+import math
+
+import pytest
+import torch
+
+from prefill_phase_attention_gb300 import binding
+from tests import long_reference as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from prefill_phase_attention_gb300 import build
+    build.build()
+    binding.load()
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need CUDA")
+
+
+class Call:
+    """Inputs of one call on the CPU, their GPU copies, and the outputs in guarded buffers."""
+
+    GUARD = 2048
+
+    def __init__(self, seed, new, lens, d=64, hk=2, group=2, block=0, int8=False, prefix=0, slack=3):
+        g = torch.Generator().manual_seed(seed)
+        self.new, self.lens, self.hk, self.group, self.d = new, lens, hk, group, d
+        cap = max(p + n for p, n in zip(lens, new)) + slack
+        self.cache = R.Cache(g, lens, cap, hk, d, block, int8, prefix)
+        t = sum(new)
+        self.q = torch.randn((t, hk * group, d), generator=g).to(torch.bfloat16)
+        self.k = torch.randn((t, hk, d), generator=g).to(torch.bfloat16)
+        self.v = torch.randn((t, hk, d), generator=g).to(torch.bfloat16)
+        self.cu = R.cumulative(new)
+        self.scale = d ** -0.5
+        self.weights = torch.rand(self.cache.shape[:-1], generator=g)
+        cu_k = R.cumulative([p + n for p, n in zip(lens, new)])
+        i32 = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
+        self.meta = (i32(self.cu), i32(cu_k))
+        self.offsets = i32(lens)
+        self.dev = [x.cuda() for x in (self.q, self.k, self.v)]
+        self.data = [self.guarded(x) for x in self.cache.data]
+        self.sc = [None if x is None else self.guarded(x) for x in self.cache.scale]
+        self.out = self.guarded(torch.full(self.q.shape, math.nan, dtype=torch.bfloat16))
+        self.lse = self.guarded(torch.full((t, hk * group), math.nan))
+        c = self.cache
+        self.opts = dict(block_table=None if c.table is None else c.table.cuda())
+        self.scales = dict(cache_k_scale=self.sc[0][1] if self.sc[0] else None,
+                           cache_v_scale=self.sc[1][1] if self.sc[1] else None)
+        self.pre = {}
+        if prefix and block:
+            self.pre = dict(prefix_table=c.prefix_table.cuda(), prefix_len=prefix)
+        elif prefix:
+            up = lambda x: None if x is None else x.cuda()  # noqa: E731
+            self.pre = dict(prefix_k=up(c.pre_data[0]), prefix_v=up(c.pre_data[1]), prefix_len=prefix,
+                            prefix_k_scale=up(c.pre_scale[0]), prefix_v_scale=up(c.pre_scale[1]))
+
+    def guarded(self, x):
+        """(buffer with bands on both sides, the view that holds x)."""
+        n = x.numel()
+        buf = torch.empty(n + 2 * self.GUARD, dtype=x.dtype, device="cuda")
+        R.bits(buf).fill_(0x5a)
+        view = buf[self.GUARD:self.GUARD + n].view(x.shape)
+        view.copy_(x)
+        return buf, view
+
+    def guards(self):
+        for buf, _ in self.data + [x for x in self.sc if x] + [self.out, self.lse]:
+            b = R.bits(buf)
+            assert (b[:self.GUARD] == 0x5a).all() and (b[-self.GUARD:] == 0x5a).all(), "write outside a buffer"
+
+    def tensors(self):
+        return (*self.dev, *self.meta, self.data[0][1], self.data[1][1], self.offsets, self.out[1], self.lse[1])
+
+    def sinks(self, window, sinks, theta=0.0, **kw):
+        binding.prefill_attn_varlen_sinks(*self.tensors(), window=window, sink_tokens=sinks, scale=self.scale,
+                                          rope_theta=theta, **self.opts, **self.scales, **kw)
+
+    def prefix(self, causal=True, theta=0.0, **kw):
+        binding.prefill_attn_varlen_prefix(*self.tensors(), scale=self.scale, causal=causal, rope_theta=theta,
+                                           **self.opts, **self.scales, **self.pre, **kw)
+
+    def check(self, theta=0.0, skipped=(), **kw):
+        """out, lse and the caches against the plain form; sequences in `skipped` were left alone."""
+        torch.cuda.synchronize()
+        self.guards()
+        ref, lse, mag = R.attention(self.cache, self.q, self.k, self.v, self.new, self.scale, theta=theta, **kw)
+        got, got_lse = self.out[1].cpu().double(), self.lse[1].cpu().double()
+        rows = torch.ones(len(self.q), dtype=torch.bool)
+        for b in skipped:
+            rows[self.cu[b]:self.cu[b + 1]] = False
+        assert got[~rows].isnan().all() and got_lse[~rows].isnan().all(), "rows of a skipped sequence were written"
+        # a rotated q or k may differ from the plain rotation by a bf16 rounding: 2^-8 of each product
+        score = R.SCORE + (2 * R.BF16 if theta else 0.0)
+        tol = R.BF16 * (mag * (2 if self.cache.int8 else 1) + ref.abs()) + score * mag + 1e-6
+        err = (got - ref).abs()[rows]
+        assert (err <= tol[rows]).all(), f"out off by {err.max():.3e}, {(err / tol[rows]).max():.2f} of the tolerance"
+        err = (got_lse - lse).abs()[rows]
+        assert (err <= score).all(), f"lse off by {err.max():.3e}"
+        if theta:
+            return
+        for w, new in ((0, self.k), (1, self.v)):
+            cu = list(self.cu)
+            data, scale = self.cache.written(w, new, cu) if not skipped else (None, None)
+            if data is None:
+                continue
+            assert torch.equal(R.bits(self.data[w][1].cpu()), R.bits(data)), "cache differs"
+            if scale is not None:
+                assert torch.equal(R.bits(self.sc[w][1].cpu()), R.bits(scale)), "cache scales differ"
+
+
+def ok():
+    assert binding.prefill_attn_device_status() == 0
+
+
+# --------------------------------------------------------------------------- sink tokens
+
+@pytest.mark.parametrize("block", [0, 16, 128])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d,group", [(32, 1), (64, 4), (128, 2)])
+def test_sinks_decode_and_chunks(d, group, int8, block):
+    """Decode rows, short chunks, an empty sequence and a fresh one; sinks of one token and of several tiles."""
+    new, lens = [1, 5, 0, 1, 33, 2], [700, 0, 40, 128, 390, 1]
+    for i, (window, sinks) in enumerate([(1, 1), (64, 4), (200, 130), (257, 300), (4000, 7)]):
+        c = Call(10 + i, new, lens, d, 2, group, block, int8)
+        c.sinks(window, sinks)
+        c.check(window=window, sinks=sinks)
+    ok()
+
+
+@pytest.mark.parametrize("schedule", [0, 1, 2, 3])
+@pytest.mark.parametrize("block", [0, 64])
+@pytest.mark.parametrize("d,group", [(64, 1), (128, 8)])
+def test_sinks_prompts(d, group, block, schedule):
+    """Prompts longer than the window: tiles between the sinks and the window are skipped."""
+    c = Call(30, [900, 131, 1], [0, 517, 64], d, 1, group, block)
+    c.sinks(150, 5, schedule=schedule)
+    c.check(window=150, sinks=5)
+    ok()
+
+
+@pytest.mark.parametrize("window,sinks", [(2500, 4), (6000, 200), (100, 129)])
+@pytest.mark.parametrize("block,int8", [(0, False), (16, False), (0, True)])
+def test_sinks_one_long_row_is_split(block, int8, window, sinks):
+    """One decode row over many tiles: its keys are split between CTAs and joined."""
+    c = Call(40, [1], [4099], 128, 2, 4, block, int8)
+    c.sinks(window, sinks)
+    assert binding.prefill_attn_last_launch_count() == 3
+    c.check(window=window, sinks=sinks)
+    ok()
+
+
+def test_sinks_zero_is_the_plain_window():
+    c = Call(50, [1, 70], [300, 200], 64, 2, 2)
+    c.sinks(90, 0)
+    c.check(window=90)
+    ok()
+
+
+@pytest.mark.parametrize("block", [0, 32])
+def test_sinks_rotary(block):
+    c = Call(51, [3, 40], [300, 0], 64, 2, 2, block)
+    c.sinks(90, 4, theta=1e4)
+    c.check(theta=1e4, window=90, sinks=4)
+    ok()
+
+
+# --------------------------------------------------------------------------- shared prefix
+
+@pytest.mark.parametrize("block", [0, 16, 256])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d,group", [(32, 4), (64, 1), (128, 8)])
+def test_prefix_of_every_length(d, group, int8, block):
+    """Prefixes that end inside, at and past a tile; decode rows, chunks, empty and fresh sequences."""
+    new, lens = [1, 4, 0, 1, 20, 1], [0, 130, 9, 300, 0, 128]
+    for i, prefix in enumerate([1, 127, 128, 129, 700]):
+        c = Call(60 + i, new, lens, d, 2, group, block, int8, prefix)
+        c.prefix()
+        c.check()
+    ok()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("schedule", [0, 1, 2, 3])
+def test_prefix_with_prompts(causal, schedule):
+    c = Call(70, [300, 1, 129], [0, 70, 5], 128, 2, 2, prefix=389)
+    c.prefix(causal=causal, schedule=schedule)
+    c.check(causal=causal)
+    ok()
+
+
+@pytest.mark.parametrize("block", [0, 16])
+def test_prefix_split_between_many_blocks(block):
+    """A long prefix under a few rows: pieces, and a long own context cut into pieces as well."""
+    c = Call(71, [1, 1, 2], [3000, 1, 0], 128, 1, 4, block, prefix=6001)
+    c.prefix()
+    c.check()
+    ok()
+
+
+def test_prefix_of_nothing_is_the_plain_call():
+    c = Call(72, [1, 30], [200, 0], 64, 2, 2)
+    one = torch.zeros((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    c.pre = dict(prefix_k=one, prefix_v=one.clone(), prefix_len=0)
+    c.prefix()
+    c.check()
+    ok()
+
+
+@pytest.mark.parametrize("block", [0, 32])
+def test_prefix_rotary_counts_from_the_prefix(block):
+    c = Call(73, [2, 17], [100, 0], 64, 2, 2, block, prefix=150)
+    c.prefix(theta=1e4)
+    c.check(theta=1e4)
+    ok()
+
+
+def test_prefix_bad_block_rejects_the_call():
+    c = Call(74, [1, 3], [20, 0], 64, 2, 2, 16, prefix=40)
+    c.pre["prefix_table"][1] = 10 ** 6
+    before = [x[1].clone() for x in c.data]
+    c.prefix()
+    torch.cuda.synchronize()
+    assert binding.prefill_attn_device_status() & binding.DEVERR_METADATA
+    assert c.out[1].isnan().all() and c.lse[1].isnan().all()
+    assert all(torch.equal(R.bits(a), R.bits(b[1])) for a, b in zip(before, c.data))
+
+
+@pytest.mark.parametrize("call", ["sinks", "prefix"])
+def test_inconsistent_sequence_is_skipped(call):
+    c = Call(75, [1, 3, 2], [20, 7, 200], 64, 2, 2, prefix=40 if call == "prefix" else 0)
+    c.offsets[1] = 8  # disagrees with cu_seqlens_k
+    before = [x[1][1].clone() for x in c.data]
+    if call == "sinks":
+        c.sinks(64, 4)
+        c.check(skipped=[1], window=64, sinks=4)
+    else:
+        c.prefix()
+        c.check(skipped=[1])
+    assert binding.prefill_attn_device_status() & binding.DEVERR_METADATA
+    assert all(torch.equal(R.bits(a), R.bits(b[1][1])) for a, b in zip(before, c.data))
+
+
+# --------------------------------------------------------------------------- key weights
+
+def weigh(c, lse=None, causal=True, window=0, sinks=0, theta=0.0, **kw):
+    """Runs the call on c's weights and compares every row of them."""
+    if lse is None:
+        lse = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale, causal, window, sinks, theta)[1].float()
+    buf, w = c.guarded(c.weights)
+    binding.prefill_attn_key_weights(c.dev[0], c.dev[1], *c.meta, c.data[0][1], c.offsets, lse.cuda(), w, scale=c.scale,
+                                     causal=causal, window=window, sink_tokens=sinks, rope_theta=theta,
+                                     prefix_len=c.cache.prefix, cache_k_scale=c.scales["cache_k_scale"], **c.opts, **kw)
+    torch.cuda.synchronize()
+    b = R.bits(buf)
+    assert (b[:c.GUARD] == 0x5a).all() and (b[-c.GUARD:] == 0x5a).all(), "write outside weights"
+    ref = R.key_weights(c.cache, c.q, c.k, c.new, lse, c.scale, c.weights, causal, window, sinks, theta)
+    got = w.cpu().double()
+    same = ref == c.weights.double()  # rows no key of this call has: untouched, bit for bit
+    assert torch.equal(got[same], ref[same])
+    # 2^-11 of a term for its score; n fp32 additions of terms of one sign: n 2^-24 of the sum
+    tol = (R.SCORE + (2 * R.BF16 if theta else 0.0) + max(c.new) * c.group * 2.0 ** -24) * ref.abs() + 1e-6
+    err = (got - ref).abs()
+    assert (err <= tol).all(), f"weights off by {err.max():.3e}, {(err / tol).max():.2f} of the tolerance"
+    return w
+
+
+@pytest.mark.parametrize("block", [0, 16, 256])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d,group", [(32, 4), (64, 1), (128, 8)])
+def test_key_weights(d, group, int8, block):
+    c = Call(80, [1, 5, 0, 1, 150, 2], [700, 0, 40, 128, 390, 1], d, 2, group, block, int8)
+    weigh(c)
+    weigh(c, window=100, sinks=3)
+    ok()
+
+
+@pytest.mark.parametrize("group,causal", [(1, True), (3, True), (4, False), (128, True)])
+def test_key_weights_of_prompts(group, causal):
+    new = [513, 128, 1, 200] if group < 128 else [9, 1]
+    lens = [0, 129, 0, 5] if group < 128 else [0, 140]
+    c = Call(81, new, lens, 128, 1, group)
+    weigh(c, causal=causal)
+    ok()
+
+
+def test_key_weights_are_probabilities():
+    """The weights that a fresh prompt's keys collect sum to its number of queries times heads."""
+    c = Call(82, [333], [0], 64, 2, 2)
+    w = weigh(c)
+    total = w[0, :, :333].double().sum(-1).cpu()
+    assert (total - 333 * 2).abs().max() <= 333 * 2 * R.SCORE
+
+
+def test_key_weights_rotary_and_prefix():
+    c = Call(83, [3, 40], [120, 0], 64, 2, 2, prefix=77)
+    lse = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale, theta=1e4)[1].float()
+    weigh(c, lse, theta=1e4)
+    ok()
+
+
+def test_key_weights_twice_gives_equal_bits():
+    c = Call(84, [200, 1], [100, 900], 128, 2, 4)
+    lse = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale)[1].float()
+    assert torch.equal(weigh(c, lse), weigh(c, lse))
+
+
+# --------------------------------------------------------------------------- eviction
+
+def evict(c, weights, budget, sinks, recent, lens=None, index=True, kept="new", bad=()):
+    lens = c.lens if lens is None else lens
+    dev = torch.tensor(lens, dtype=torch.int32).cuda()
+    new = torch.full_like(dev, -7)
+    buf, w = c.guarded(weights)
+    kw = w if kept == "same" else torch.full_like(w, 9.0) if kept == "new" else None
+    idx = torch.full((len(lens), c.hk, budget), -9, dtype=torch.int32, device="cuda") if index else None
+    binding.prefill_attn_evict(c.data[0][1], c.data[1][1], w, dev, new, idx, kw, budget=budget, sink_tokens=sinks,
+                               recent_tokens=recent, **c.opts, **c.scales)
+    torch.cuda.synchronize()
+    c.guards()
+    want = [[x.clone() for x in c.cache.data], [None if x is None else x.clone() for x in c.cache.scale]]
+    want_w = weights.clone() if kept == "same" else torch.full_like(weights, 9.0)
+    for b, n in enumerate(lens):
+        if b in bad:
+            assert new[b] == -7 and (idx is None or (idx[b] == -9).all())
+            continue
+        m = min(n, budget)
+        assert int(new[b]) == m
+        for h in range(c.hk):
+            slot, row = c.cache.at(b, torch.arange(n))
+            keep = R.evicted(weights[slot, h, row], budget, sinks, recent)
+            if idx is not None:
+                assert torch.equal(idx[b, h, :m].cpu().long(), keep), f"sequence {b}, head {h}"
+                assert (idx[b, h, m:] == -1).all()
+            want_w[slot[:m], h, row[:m]] = weights[slot[keep], h, row[keep]]
+            for w_ in range(2):
+                want[0][w_][slot[:m], h, row[:m]] = c.cache.data[w_][slot[keep], h, row[keep]]
+                if c.cache.int8:
+                    want[1][w_][slot[:m], h, row[:m]] = c.cache.scale[w_][slot[keep], h, row[keep]]
+    for w_ in range(2):
+        assert torch.equal(R.bits(c.data[w_][1].cpu()), R.bits(want[0][w_])), "cache differs"
+        if c.cache.int8:
+            assert torch.equal(R.bits(c.sc[w_][1].cpu()), R.bits(want[1][w_])), "scales differ"
+    if kw is not None:
+        assert torch.equal(R.bits(kw.cpu()), R.bits(want_w)), "kept weights differ"
+    if kept != "same":
+        assert torch.equal(R.bits(w.cpu()), R.bits(weights)), "weights were changed"
+
+
+def weights_for(c, seed, kind):
+    g = torch.Generator().manual_seed(seed)
+    w = torch.rand(c.cache.shape[:-1], generator=g)
+    if kind == "ties":
+        w = (w * 4).floor() / 4
+    if kind == "special":
+        for x in (math.nan, math.inf, -math.inf, 0.0, -0.0, -1.5, 1e-42):
+            w[torch.rand(w.shape, generator=g) < 0.08] = x
+    return w
+
+
+@pytest.mark.parametrize("block", [0, 8, 256])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_evict(d, int8, block):
+    """Every length class: empty, one token, below, at and just above the budget, far above it."""
+    lens = [0, 1, 90, 100, 101, 733, 2100]
+    for i, (kind, sinks, recent) in enumerate([("plain", 4, 16), ("ties", 0, 0), ("special", 3, 97), ("special", 1, 5)]):
+        c = Call(90 + i, [0] * len(lens), lens, d, 3, 1, block, int8)
+        evict(c, weights_for(c, i, kind), 100, sinks, recent, kept=["new", "same", "new", "none"][i], index=i != 1)
+    ok()
+
+
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (1, 1, 0), (1, 0, 1), (2049, 4, 1000), (4999, 0, 3)])
+def test_evict_extremes(budget, sinks, recent):
+    c = Call(95, [0, 0], [5000, 3000], 64, 2, 1)
+    evict(c, weights_for(c, 1, "ties"), budget, sinks, recent)
+    ok()
+
+
+def test_evict_equal_weights_keeps_the_first():
+    c = Call(96, [0], [1500], 64, 1, 1)
+    evict(c, torch.zeros(c.cache.shape[:-1]), 600, 2, 10)
+    ok()
+
+
+def test_evict_skips_a_bad_length_and_a_bad_block():
+    c = Call(97, [0] * 3, [200, 300, 250], 64, 2, 1, 16)
+    c.opts["block_table"][1, 3] = -1
+    evict(c, weights_for(c, 2, "plain"), 100, 2, 10, bad=(1,))
+    assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+    c = Call(98, [0] * 3, [200, 300, 250], 64, 2, 1)
+    evict(c, weights_for(c, 2, "plain"), 100, 2, 10, lens=[200, 10 ** 6, 250], bad=(1,))
+    assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+    evict(Call(98, [0] * 3, [200, 300, 250], 64, 2, 1), weights_for(c, 2, "plain"), 100, 2, 10, lens=[200, -4, 250],
+          bad=(1,))
+    assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+
+
+# --------------------------------------------------------------------------- together
+
+@pytest.mark.parametrize("block", [0, 16])
+def test_prefill_weigh_evict_decode(block):
+    """A prompt is prefilled, its keys weighed, the cache cut back, and a token decoded over what is left."""
+    d, hk, group, n, budget = 64, 2, 4, 300, 120
+    c = Call(100, [n, n - 61], [0, 0], d, hk, group, block)
+    binding.prefill_attn_varlen_ex(*c.tensors(), scale=c.scale, **c.opts)
+    c.check()
+    lse = c.lse[1].cpu()
+    w = weigh(c, lse)
+    before = w.cpu()
+    lens = torch.tensor(c.new, dtype=torch.int32).cuda()
+    kept, index = torch.empty_like(lens), torch.empty((2, hk, budget), dtype=torch.int32, device="cuda")
+    binding.prefill_attn_evict(c.data[0][1], c.data[1][1], w, lens, kept, index, w, budget=budget, sink_tokens=4,
+                               recent_tokens=32, **c.opts)
+    assert kept.tolist() == [budget, budget]
+    # the token that follows sees the kept keys and itself
+    g = torch.Generator().manual_seed(5)
+    q1 = torch.randn((2, hk * group, d), generator=g).to(torch.bfloat16)
+    k1, v1 = (torch.randn((2, hk, d), generator=g).to(torch.bfloat16) for _ in range(2))
+    out, cu = torch.empty_like(q1).cuda(), torch.tensor([0, 1, 2], dtype=torch.int32).cuda()
+    cu_k = torch.tensor([0, budget + 1, 2 * budget + 2], dtype=torch.int32).cuda()
+    binding.prefill_attn_varlen_ex(q1.cuda(), k1.cuda(), v1.cuda(), cu, cu_k, c.data[0][1], c.data[1][1], kept, out,
+                                   scale=c.scale, **c.opts)
+    got = out.cpu().double()
+    for b in range(2):
+        t = slice(c.cu[b], c.cu[b + 1])
+        for h in range(hk * group):
+            keep = index[b, h // group].cpu().long()
+            slot, row = c.cache.at(b, torch.arange(c.new[b]))
+            assert torch.equal(keep, R.evicted(before[slot, h // group, row], budget, 4, 32))
+            keys = torch.cat([c.k[t][keep, h // group], k1[b:b + 1, h // group]]).double()
+            vals = torch.cat([c.v[t][keep, h // group], v1[b:b + 1, h // group]]).double()
+            p = torch.softmax(keys @ q1[b, h].double() * c.scale, 0)
+            ref, mag = p @ vals, p @ vals.abs()
+            tol = R.BF16 * (mag + ref.abs()) + R.SCORE * mag + 1e-6
+            assert ((got[b, h] - ref).abs() <= tol).all()
+    ok()
