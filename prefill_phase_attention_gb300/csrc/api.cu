@@ -929,6 +929,10 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
     return x < y + b_bytes && y < x + a_bytes;
 }
 
+// A window or sink count past the cache's capacity says the same as the
+// capacity; clamped so that position arithmetic stays within 32 bits.
+int clamp_span(int tokens, int max_cache_len) { return std::min(tokens, max_cache_len); }
+
 int log2_of(int block_size) {
     int l = 0;
     while ((1 << l) < block_size) ++l;
@@ -959,8 +963,10 @@ pa_status prefill_attn_varlen_sinks(const void* q, const void* k, const void* v,
     s = check_paged(o, max_cache_len, n_kv_heads);
     if (s != PA_OK) return s;
     if (num_seqs == 0 || total_q == 0) return PA_OK;
+    o.window = clamp_span(o.window, max_cache_len);
     return enqueue_long(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs,
-                        total_q, max_cache_len, n_heads, n_kv_heads, head_dim, scale, 1, sink_tokens, Prefix(), o,
+                        total_q, max_cache_len, n_heads, n_kv_heads, head_dim, scale, 1,
+                        clamp_span(sink_tokens, max_cache_len), Prefix(), o,
                         reinterpret_cast<cudaStream_t>(stream_));
 }
 
@@ -1037,7 +1043,12 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     const int sms = sm_count(dev, &s);
     if (s != PA_OK) return s;
-    const long long units = unit_bound(total_q, num_seqs, n_heads, n_kv_heads, pa::kSlots);
+    o.window = clamp_span(o.window, max_cache_len);
+    sink_tokens = clamp_span(sink_tokens, max_cache_len);
+    // units of at least two key tiles (or the sequence's last); prefix and new
+    // keys are cut apart, so a sequence has at most one tile more than its rows need
+    const long long tiles = ((long long)max_cache_len + pa::kBlockN - 1) / pa::kBlockN + 1;
+    const long long units = (long long)num_seqs * n_kv_heads * ((tiles + 1) / 2);
     if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
     Workspace* ws = nullptr;
     s = get_workspace(dev, stream, num_seqs, (int)units, &ws);
@@ -1048,10 +1059,12 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
         s = get_rope_scratch(ws, dev, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
         if (s != PA_OK) return s;
     }
-    pa::ScheduleArgs sa;
+    const int grid = (int)std::min<long long>(sms, units);
+    pa::KeyScheduleArgs sa;
     fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, max_cache_len, n_heads, n_kv_heads,
-                  head_dim, causal, o, scr, pa::kSlots, sms);
-    e = pa::launch_build_schedule(sa, stream);
+                  head_dim, causal, o, scr, pa::kSlots, grid);
+    sa.sinks = sink_tokens;
+    e = pa::launch_build_key_schedule(sa, stream);
     if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
     int launches = 2;
     if (o.rope_theta > 0.f) {
@@ -1060,30 +1073,14 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
         if (e != cudaSuccess) return cuda_fail(e, "rotary prologue launch");
         ++launches;
     }
-    pa::KeyWeightsArgs a;
-    a.q = static_cast<const __nv_bfloat16*>(q);
-    a.k = static_cast<const __nv_bfloat16*>(k);
-    a.cache_k = cache_k;
-    a.scale_k = o.kv_quant ? o.scale_k : nullptr;
-    a.lse = lse;
-    a.weights = weights;
-    a.seqs = scr.seqs;
-    a.hdr = scr.hdr;
-    a.num_seqs = num_seqs;
-    a.total_q = total_q;
-    a.n_heads = n_heads;
-    a.n_kv_heads = n_kv_heads;
-    a.group = n_heads / n_kv_heads;
-    a.max_cache_len = max_cache_len;
-    a.scale_log2 = scale * 1.4426950408889634f;
-    a.causal = causal;
-    a.window = o.window;
-    a.sinks = sink_tokens;
-    a.block_table = o.block_table;
-    a.block_log2 = log2_of(o.block_size);
-    a.max_blocks = o.max_blocks;
-    a.num_blocks = o.num_blocks;
-    e = pa::launch_key_weights(a, head_dim, sms, stream);
+    pa::KeyWeightsParams p;
+    fill_fwd(p, k, k, const_cast<void*>(cache_k), const_cast<void*>(cache_k), nullptr, const_cast<float*>(lse), scr,
+             max_cache_len, n_heads, n_kv_heads, scale, causal, o, 2);
+    p.weights = weights;
+    p.sinks = sink_tokens;
+    e = pa::encode_fwd_maps(p, q, total_q, num_seqs, head_dim, o.num_blocks);
+    if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
+    e = pa::launch_key_weights(p, head_dim, grid, stream);
     if (e != cudaSuccess) return cuda_fail(e, "key weight launch");
     g_last_launches = launches;
     return PA_OK;

@@ -138,22 +138,17 @@ struct MergeArgs {
 cudaError_t launch_merge(const MergeArgs& a, int head_dim, cudaStream_t stream);
 
 // Weight each cached key collects from the new queries.
-struct KeyWeightsArgs {
-    const __nv_bfloat16* q;  // [T, H, d]
-    const __nv_bfloat16* k;  // [T, Hk, d]
-    const void* cache_k;     // bf16 rows, or int8 codes with scale_k
-    const float* scale_k;
-    const float* lse;        // [T, H]
-    float* weights;          // one per cache row
-    const SeqInfo* seqs;
-    WorkspaceHeader* hdr;
-    int num_seqs, total_q, n_heads, n_kv_heads, group, max_cache_len;
-    float scale_log2;
-    int causal, window, sinks;
-    const int32_t* block_table;
-    int block_log2, max_blocks, num_blocks;
+struct KeyScheduleArgs : ScheduleArgs {
+    int sinks;
 };
-cudaError_t launch_key_weights(const KeyWeightsArgs& a, int head_dim, int sms, cudaStream_t stream);
+// units: Unit{sequence, KV head, first key tile of the sequence's stream, key tiles}.
+cudaError_t launch_build_key_schedule(const KeyScheduleArgs& a, cudaStream_t stream);
+// The attention kernel's parameters and tensor maps (its v, cache_v and out unused).
+struct KeyWeightsParams : FwdParams {
+    float* weights;  // one per cache row
+    int sinks;
+};
+cudaError_t launch_key_weights(const KeyWeightsParams& p, int head_dim, int grid, cudaStream_t stream);
 
 // Eviction by weight, in place.
 struct EvictArgs {

@@ -125,7 +125,7 @@ def ok():
 def test_sinks_decode_and_chunks(d, group, int8, block):
     """Decode rows, short chunks, an empty sequence and a fresh one; sinks of one token and of several tiles."""
     new, lens = [1, 5, 0, 1, 33, 2], [700, 0, 40, 128, 390, 1]
-    for i, (window, sinks) in enumerate([(1, 1), (64, 4), (200, 130), (257, 300), (4000, 7)]):
+    for i, (window, sinks) in enumerate([(1, 1), (64, 4), (200, 130), (257, 300), (4000, 7), (2 ** 31 - 1, 2 ** 31 - 1)]):
         c = Call(10 + i, new, lens, d, 2, group, block, int8)
         c.sinks(window, sinks)
         c.check(window=window, sinks=sinks)
@@ -276,6 +276,7 @@ def test_key_weights(d, group, int8, block):
     c = Call(80, [1, 5, 0, 1, 150, 2], [700, 0, 40, 128, 390, 1], d, 2, group, block, int8)
     weigh(c)
     weigh(c, window=100, sinks=3)
+    weigh(c, window=2 ** 31 - 1, sinks=2 ** 31 - 1)
     ok()
 
 
