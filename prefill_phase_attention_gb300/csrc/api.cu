@@ -1149,6 +1149,7 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     a.cache_k = cache_k;
     a.cache_v = cache_v;
     a.row_bytes = (int)row_bytes;
+    a.part_bytes = 0;
     a.scale_k = o.kv_quant ? o.scale_k : nullptr;
     a.scale_v = o.kv_quant ? o.scale_v : nullptr;
     a.weights = weights;
@@ -1169,7 +1170,7 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     a.num_blocks = o.num_blocks;
     e = pa::launch_evict(a, stream);
     if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
-    g_last_launches = 2;
+    g_last_launches = 1;
     return PA_OK;
 }
 

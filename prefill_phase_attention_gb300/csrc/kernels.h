@@ -154,7 +154,8 @@ cudaError_t launch_key_weights(const KeyWeightsParams& p, int head_dim, int grid
 struct EvictArgs {
     void* cache_k;
     void* cache_v;
-    int row_bytes;  // of one cached key or value
+    int row_bytes;   // of one cached key or value
+    int part_bytes;  // of it that one CTA moves (set by launch_evict)
     float* scale_k;
     float* scale_v;
     const float* weights;

@@ -376,9 +376,19 @@ def test_evict(d, int8, block):
 
 
 @pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 0), (1, 1, 0), (1, 0, 1), (2049, 4, 1000), (4999, 0, 3)])
-def test_evict_extremes(budget, sinks, recent):
-    c = Call(95, [0, 0], [5000, 3000], 64, 2, 1)
-    evict(c, weights_for(c, 1, "ties"), budget, sinks, recent)
+@pytest.mark.parametrize("kept", ["new", "same"])
+def test_evict_extremes(budget, sinks, recent, kept):
+    """Lengths on both sides of what one CTA selects alone (4096 tokens)."""
+    c = Call(95, [0] * 4, [5000, 3000, 4096, 4097], 64, 2, 1)
+    evict(c, weights_for(c, 1, "ties"), budget, sinks, recent, kept=kept)
+    ok()
+
+
+@pytest.mark.parametrize("int8,block", [(False, 0), (True, 0), (False, 16)])
+def test_evict_long_sequences(int8, block):
+    """Shares of a cluster's CTAs past what their threads hold in registers."""
+    c = Call(94, [0, 0], [40001, 16500], 32, 1, 1, block, int8)
+    evict(c, weights_for(c, 3, "special"), 9001, 4, 100, kept="same")
     ok()
 
 
