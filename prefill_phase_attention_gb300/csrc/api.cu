@@ -1079,6 +1079,7 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
     p.weights = weights;
     p.sinks = sink_tokens;
     e = pa::encode_fwd_maps(p, q, total_q, num_seqs, head_dim, o.num_blocks);
+    if (e == cudaSuccess) e = pa::encode_one_token_map(p, q, total_q, head_dim);
     if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
     e = pa::launch_key_weights(p, head_dim, grid, stream);
     if (e != cudaSuccess) return cuda_fail(e, "key weight launch");
@@ -1137,6 +1138,8 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    const int sms = sm_count(dev, &s);
+    if (s != PA_OK) return s;
     Workspace* ws = nullptr;
     s = get_workspace(dev, stream, 0, 0, &ws);
     if (s != PA_OK) return s;
@@ -1168,9 +1171,10 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     a.block_log2 = log2_of(o.block_size);
     a.max_blocks = o.max_blocks;
     a.num_blocks = o.num_blocks;
-    e = pa::launch_evict(a, stream);
+    int launches = 0;
+    e = pa::launch_evict(a, sms, &launches, stream);
     if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
-    g_last_launches = 1;
+    g_last_launches = launches;
     return PA_OK;
 }
 

@@ -1953,6 +1953,14 @@ cudaError_t encode_prefix_maps(FwdParamsX& p, int head_dim, const void* prefix_k
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, dt);
 }
 
+cudaError_t encode_one_token_map(KeyWeightsParams& p, const void* q, int total_q, int head_dim) {
+    const uint32_t cc = head_dim >= 64 ? 64 : 32;
+    const CUtensorMapSwizzle sw = head_dim >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const uint64_t D = head_dim, H = p.n_heads;
+    return encode3d(&p.tm_q1, q, D, H, (uint64_t)total_q, D * 2, H * D * 2, cc, (uint32_t)p.group, 1, sw,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+}
+
 template <int D>
 cudaError_t launch_dim(const FwdParams& p, int grid, cudaStream_t st) {
     static_assert(D == 32 || D == 64 || D == 128, "head_dim");

@@ -7,21 +7,25 @@
 // to positions 0 .. budget - 1 in their old order, in place.  L <= budget keeps
 // every token.
 //
-// One launch, one cluster of 2, 4 or 8 CTAs per (sequence, head): each CTA
-// moves one column part (64 bytes where the row has them) of K or of V, and
-// together they choose the tokens:
-//  - the m-th largest weight by a radix select, 8 bits of the weight's
-//    order-preserving integer image per pass; up to kSoloTokens tokens every
-//    CTA does it alone (a few thousand weights cost less than a cluster
-//    barrier), beyond that each CTA takes its share of the positions and the
-//    histograms are added through distributed shared memory;
-//  - one pass over the positions then lists the kept ones in order (in shared
-//    memory, or in global memory for the cluster).
-// The move copies row list[j] to row j in increasing j, a chunk of rows in
-// registers at a time.  list[j] >= j, so a chunk may be written once all of ITS
-// sources are read: later chunks read at or past their own start, and the next
-// chunk's loads are already in flight while this one is stored.  Column parts
-// never touch one another's bytes, so no CTA waits for another here.
+// Choosing: the m-th largest weight by a radix select, 8 bits of the weight's
+// order-preserving integer image per pass.  One CTA does it alone while its
+// threads can hold the weights in registers; beyond that the CTAs of a cluster
+// each take a share of the positions and add their histograms through
+// distributed shared memory.  One pass over the positions then lists the kept
+// ones in order.
+//
+// Moving: row list[j] to row j in increasing j, a chunk of rows in registers at
+// a time.  list[j] >= j, so a chunk may be written once all of ITS sources are
+// read: later chunks read at or past their own start, and the next chunk's
+// loads are already in flight while this one is stored.  A CTA moves one column
+// part (64 bytes where the row has them) of K or of V; parts never touch one
+// another's bytes, so no CTA waits for another.
+//
+// Two forms, picked by the launch's size.  A launch whose CTAs all run at once
+// is bound by latency: evict_kernel does both in one launch, a cluster of 2, 4
+// or 8 CTAs (its column parts) per (sequence, head).  A larger one is bound by
+// HBM, and a CTA that selects moves no bytes: select_kernel runs first, one CTA
+// of 1024 threads (or a cluster) per (sequence, head), then move_kernel.
 #include <cooperative_groups.h>
 
 #include <cstdint>
@@ -29,6 +33,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "prefill_attn.h"
+#include "ptx.cuh"
 
 namespace pa {
 
@@ -36,30 +41,44 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
-constexpr int kVec = 4;            // 16-byte pieces per thread and chunk of the move
-constexpr int kHeld = 8;           // weights a thread keeps in registers between passes
-constexpr int kSoloTokens = kThreads * kHeld;
+constexpr int kVec = 4;  // 16-byte pieces per thread and chunk of the move
+// one-launch form: threads, weights a thread holds (so tokens a CTA selects from alone)
+constexpr int kFusedThreads = 512, kFusedHeld = 8;
+// two-launch form
+constexpr int kSelectThreads = 512, kSelectHeld = 16, kMoveThreads = 256;
+constexpr int kScalars = 8;  // weights or scales a thread moves per chunk
+// Weights crowd into a few digits: a histogram has this many copies, one per
+// lane & 7, a bank apart, so that a warp's equal digits do not queue up.
+constexpr int kCopies = 8;
 
 // Order-preserving image of a weight: larger weight, larger integer; -0 equals
 // +0 and every NaN is the largest value.
 __device__ __forceinline__ uint32_t rank_bits(float w) {
-    uint32_t u = __float_as_uint(w);
-    if ((u & 0x7fffffffu) > 0x7f800000u) return 0xffffffffu;
-    if (u == 0x80000000u) u = 0;
-    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+    const uint32_t u = __float_as_uint(__fadd_rn(w, 0.f));  // -0 + 0 = +0
+    return w != w ? 0xffffffffu : u ^ ((uint32_t)((int)u >> 31) | 0x80000000u);
 }
 
-// Cache row (over [slots or blocks, heads, rows]) of position pos of (b, h).
-__device__ __forceinline__ size_t cache_row(const EvictArgs& a, int b, int h, int pos) {
-    if (!a.block_table) return ((size_t)b * a.n_kv_heads + h) * a.max_cache_len + pos;
-    const int blk = __ldg(a.block_table + (size_t)b * a.max_blocks + (pos >> a.block_log2));
-    return (((size_t)blk * a.n_kv_heads + h) << a.block_log2) + (pos & ((1 << a.block_log2) - 1));
-}
+// Cache rows (over [slots or blocks, heads, rows]) of the positions of one (b, h).
+struct Rows {
+    const int32_t* table;  // nullptr: contiguous, rows base + pos
+    size_t base;
+    int log2, n_kv_heads, h;
+    __device__ __forceinline__ Rows(const EvictArgs& a, int b, int head)
+        : table(a.block_table ? a.block_table + (size_t)b * a.max_blocks : nullptr),
+          base(((size_t)b * a.n_kv_heads + head) * a.max_cache_len),
+          log2(a.block_log2),
+          n_kv_heads(a.n_kv_heads),
+          h(head) {}
+    __device__ __forceinline__ size_t operator()(int pos) const {
+        if (!table) return base + pos;
+        const int head_block = __ldg(table + (pos >> log2)) * n_kv_heads + h;
+        return ((size_t)head_block << log2) + (pos & ((1 << log2) - 1));
+    }
+};
 
 // Length of sequence b, or -1 when it is inconsistent or one of its blocks lies
 // outside the pool (every CTA of the sequence comes to the same verdict).
+template <int kThreads>
 __device__ int checked_length(const EvictArgs& a, int b) {
     const int len = a.lengths[b];
     bool bad = len < 0 || len > a.max_cache_len;
@@ -75,86 +94,114 @@ __device__ int checked_length(const EvictArgs& a, int b) {
     return __syncthreads_or(bad) ? -1 : len;
 }
 
+template <int kThreads, int kHeld>
 struct Shared {
-    int hist[4][256];  // one per pass: no barrier between reading one and clearing the next
+    int copies[kCopies][257];
+    int hist[4][256];  // this CTA's, one per pass: no barrier between the cluster's reads and the next pass
     int sums[256];
-    int counts[2][kHeld * kWarps];  // certain and equal positions per block and warp, then ahead of them
-    int total[2];        // ... of this CTA's share
-    int total_batch[2];  // ... of a batch
+    int warp_counts[2][kThreads / 32];  // certain and equal positions per warp, then ahead of the warp
+    int total[2];                       // ... of this CTA's share
+    int batch[2];                       // ... of a batch
     uint32_t digit;
     int need;
-    int list[kSoloTokens];  // kept positions (one CTA alone)
+    uint32_t ranks[kThreads * (kHeld + 1)];  // a batch of rank_bits, one padding word per thread
 };
 
 // Moves a scalar per row (weights, row scales): dst row j = src row list[j].
-__device__ void move_scalars(const EvictArgs& a, int b, int h, const float* src, float* dst, const int* list, int count) {
-    for (int j0 = 0; j0 < count; j0 += kThreads * kHeld) {
-        float x[kHeld];
+template <int kThreads>
+__device__ void move_scalars(const Rows& rows, const float* src, float* dst, const int* list, int count) {
+    for (int j0 = 0; j0 < count; j0 += kThreads * kScalars) {
+        float x[kScalars];
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
+        for (int i = 0; i < kScalars; ++i) {
             const int j = j0 + i * kThreads + threadIdx.x;
-            if (j < count) x[i] = src[cache_row(a, b, h, list[j])];
+            if (j < count) x[i] = src[rows(list[j])];
         }
         __syncthreads();  // in place: this chunk's sources are read
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
+        for (int i = 0; i < kScalars; ++i) {
             const int j = j0 + i * kThreads + threadIdx.x;
-            if (j < count) dst[cache_row(a, b, h, j)] = x[i];
+            if (j < count) dst[rows(j)] = x[i];
         }
     }
 }
 
-__global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constant__ EvictArgs a) {
-    __shared__ Shared sh;
-    cg::cluster_group cluster = cg::this_cluster();
+// Lists the kept positions of (b, h) into `list`, ascending: this CTA's share of
+// [0, len) when the cluster works together (coop), all of them otherwise.  Ends
+// with a barrier of the CTA; a cluster's list is whole after a cluster barrier.
+template <int kThreads, int kHeld>
+__device__ __forceinline__ void select_tokens(const EvictArgs& a, Shared<kThreads, kHeld>& sh,
+                                              const cg::cluster_group& cluster, int b, int h, int len, bool coop,
+                                              int* list) {
+    constexpr int kWarps = kThreads / 32;
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
-    const int bh = blockIdx.x / ranks;
-    const int h = bh % a.n_kv_heads, b = bh / a.n_kv_heads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int len = checked_length(a, b);
-    if (len < 0) {
-        if (tid == 0 && rank == 0 && h == 0) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
-        return;
-    }
-    const bool coop = len > kSoloTokens;
     const int parts = coop ? ranks : 1, part = coop ? rank : 0;
-    const int count = min(len, a.budget);
     const bool all = len <= a.budget;
     const int lo = a.sinks, hi = len - a.recent;  // the tokens that compete (when !all)
     int need = all ? 0 : a.budget - a.sinks - a.recent;
-    // this CTA's positions: [p_lo, p_hi), thread t at p_lo + t, + kThreads, ...
+    // This CTA's positions [p_lo, p_hi), in batches; thread t has kHeld
+    // consecutive ones of a batch in registers, read coalesced and handed over
+    // through shared memory.  A rank of 0 (below every weight's) stands for a
+    // position that does not compete.
     const int share = ((len + parts - 1) / parts + 31) & ~31;
     const int p_lo = min(len, part * share), p_hi = min(len, p_lo + share);
+    constexpr int kBatch = kThreads * kHeld;
+    const bool compete = need > 0;
+    const Rows rows(a, b, h);
     uint32_t held[kHeld];
     uint32_t threshold = 0;
-    int* const list = coop ? a.index + (size_t)bh * a.budget : sh.list;
-
-    if (need > 0) {
+    auto load_batch = [&](int p0) {
+        __syncthreads();
+        // positions [lo, last) compete
+        const unsigned span = compete ? (unsigned)max(0, min(p_hi, hi) - lo) : 0u;
+        if (!rows.table) {
+            const float* w = a.weights + rows.base + p0;
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int x = i * kThreads + tid;
+                sh.ranks[x + x / kHeld] = (unsigned)(p0 + x - lo) < span ? rank_bits(w[x]) : 0;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int x = i * kThreads + tid;
+                sh.ranks[x + x / kHeld] = (unsigned)(p0 + x - lo) < span ? rank_bits(a.weights[rows(p0 + x)]) : 0;
+            }
+        }
+        __syncthreads();
 #pragma unroll
         for (int i = 0; i < kHeld; ++i) {
-            const int p = p_lo + i * kThreads + tid;
-            held[i] = p >= lo && p < min(p_hi, hi) ? rank_bits(a.weights[cache_row(a, b, h, p)]) : 0;
+            const int x = tid * kHeld + i;
+            held[i] = x < p_hi - p0 ? sh.ranks[tid * (kHeld + 1) + i] : 0;
         }
-        for (int i = tid; i < 4 * 256; i += kThreads) (&sh.hist[0][0])[i] = 0;
-        __syncthreads();
+    };
+    const bool one_batch = p_hi - p_lo <= kBatch;
+    load_batch(p_lo);
+
+    if (compete) {
+        int* const my_copy = sh.copies[lane & (kCopies - 1)];
         for (int pass = 0; pass < 4; ++pass) {
             const int shift = 24 - 8 * pass;
             const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
+            for (int i = tid; i < kCopies * 257; i += kThreads) (&sh.copies[0][0])[i] = 0;
+            __syncthreads();
+            for (int p0 = p_lo; p0 < p_hi; p0 += kBatch) {
+                if (!one_batch && (pass > 0 || p0 > p_lo)) load_batch(p0);
+                if (p0 + warp * 32 * kHeld >= p_hi) continue;  // nothing of the batch is this warp's
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                const int p = p_lo + i * kThreads + tid;
-                if (p >= lo && p < min(p_hi, hi) && (held[i] & mask) == threshold)
-                    atomicAdd(&sh.hist[pass][(held[i] >> shift) & 255], 1);
+                for (int i = 0; i < kHeld; ++i)
+                    // (ranks of 0 are the lowest: the digits chosen from above never reach them)
+                    if ((held[i] & mask) == threshold) atomicAdd(&my_copy[(held[i] >> shift) & 255], 1);
             }
-#pragma unroll 4
-            for (int p = p_lo + kHeld * kThreads + tid; p < min(p_hi, hi); p += kThreads) {
-                const uint32_t r = rank_bits(a.weights[cache_row(a, b, h, p)]);
-                if (p >= lo && (r & mask) == threshold) atomicAdd(&sh.hist[pass][(r >> shift) & 255], 1);
+            __syncthreads();
+            if (tid < 256) {
+                int sum = 0;
+#pragma unroll
+                for (int c = 0; c < kCopies; ++c) sum += sh.copies[c][tid];
+                sh.hist[pass][tid] = sum;
             }
-            if (coop)
-                cluster.sync();
-            else
-                __syncthreads();
+            if (coop) cluster.sync();
             // bin `tid` over the cluster; then how many weights lie in higher bins
             int mine = 0;
             if (tid < 256) {
@@ -185,43 +232,45 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
             need = sh.need;
         }
     }
-    // `need` is now how many weights equal to the threshold stay.
-    const bool compete = !all && a.budget > a.sinks + a.recent;
-    // 1: the position stays for certain, 2: its weight equals the threshold
-    auto state = [&](int p, uint32_t r) -> int {
-        if (p >= p_hi) return 0;
-        if (all || p < lo || p >= hi) return 1;
-        return !compete ? 0 : r > threshold ? 1 : r == threshold ? 2 : 0;
-    };
-    // a batch of kHeld blocks of kThreads positions from p0; the first is in `held`
-    auto load_batch = [&](int p0) {
+    // `need` is now how many weights equal to the threshold stay.  Of a thread's
+    // positions: bit i of `certain` / `equal`: it stays for certain / its weight
+    // equals the threshold.
+    uint32_t certain = 0, equal = 0;
+    auto classify = [&](int p0) {
+        const int p = p0 + tid * kHeld;
+        certain = equal = 0;
+        if (p0 + warp * 32 * kHeld >= p_hi) return;
+        if (compete) {  // a rank of 0 is neither above the threshold nor equal to it
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const int p = p0 + i * kThreads + tid;
-            if (compete && p >= lo && p < min(p_hi, hi)) held[i] = rank_bits(a.weights[cache_row(a, b, h, p)]);
+            for (int i = 0; i < kHeld; ++i) {
+                certain |= held[i] > threshold ? 1u << i : 0u;
+                equal |= held[i] == threshold ? 1u << i : 0u;
+            }
+        }
+        if (all || p < lo || p + kHeld > hi) {  // some are forced, or past the share
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i)
+                if (p + i < p_hi && (all || p + i < lo || p + i >= hi)) certain |= 1u << i;
         }
     };
     int before = 0, equal_before = 0;  // kept positions and equal weights ahead of the batch
     if (coop) {
-        int certain = 0, equal = 0;
-        for (int p0 = p_lo; p0 < p_hi; p0 += kHeld * kThreads) {
-            if (p0 > p_lo) load_batch(p0);
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                const int s = state(p0 + i * kThreads + tid, held[i]);
-                certain += s == 1;
-                equal += s == 2;
-            }
+        int c = 0, e = 0;
+        for (int p0 = p_lo; p0 < p_hi; p0 += kBatch) {
+            if (!one_batch) load_batch(p0);
+            classify(p0);
+            c += __popc(certain);
+            e += __popc(equal);
         }
         for (int o = 16; o > 0; o >>= 1) {
-            certain += __shfl_xor_sync(0xffffffffu, certain, o);
-            equal += __shfl_xor_sync(0xffffffffu, equal, o);
+            c += __shfl_xor_sync(0xffffffffu, c, o);
+            e += __shfl_xor_sync(0xffffffffu, e, o);
         }
-        if (lane == 0) sh.counts[0][warp] = certain, sh.counts[1][warp] = equal;
+        if (lane == 0) sh.warp_counts[0][warp] = c, sh.warp_counts[1][warp] = e;
         __syncthreads();
         if (tid < 2) {
             int sum = 0;
-            for (int w = 0; w < kWarps; ++w) sum += sh.counts[tid][w];
+            for (int w = 0; w < kWarps; ++w) sum += sh.warp_counts[tid][w];
             sh.total[tid] = sum;
         }
         cluster.sync();
@@ -230,72 +279,74 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
             equal_before += *cluster.map_shared_rank(&sh.total[1], r);
         }
         before += min(equal_before, need);
-        if (p_hi - p_lo > kHeld * kThreads) load_batch(p_lo);
     }
-    // the kept positions, in order: warp w's part of block i comes after every
-    // part of an earlier block and the earlier warps' parts of its own
-    static_assert(kHeld * kWarps == 128, "four parts per lane of the scan");
-    for (int p0 = p_lo; p0 < p_hi; p0 += kHeld * kThreads) {
-        if (p0 > p_lo) load_batch(p0);
-        int st[kHeld];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            st[i] = state(p0 + i * kThreads + tid, held[i]);
-            const unsigned cm = __ballot_sync(0xffffffffu, st[i] == 1), em = __ballot_sync(0xffffffffu, st[i] == 2);
-            if (lane == 0) sh.counts[0][i * kWarps + warp] = __popc(cm), sh.counts[1][i * kWarps + warp] = __popc(em);
+    for (int p0 = p_lo; p0 < p_hi; p0 += kBatch) {
+        if (!one_batch) load_batch(p0);
+        if (!one_batch || !coop) classify(p0);
+        const int c = __popc(certain), e = __popc(equal);
+        int c_inc = c, e_inc = e;  // inclusive over the warp
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, c_inc, o), y = __shfl_up_sync(0xffffffffu, e_inc, o);
+            if (lane >= o) c_inc += x, e_inc += y;
         }
         __syncthreads();
-        if (warp < 2) {  // warp 0 scans the certain ones, warp 1 the equal ones
-            int c[4], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[i] = sum;
-                sum += sh.counts[warp][lane * 4 + i];
-            }
-            int inc = sum;
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane == 31) sh.warp_counts[0][warp] = c_inc, sh.warp_counts[1][warp] = e_inc;
+        __syncthreads();
+        if (warp < 2 && lane < kWarps) {  // warp 0 scans the certain ones, warp 1 the equal ones
+            const unsigned active = (unsigned)((1ull << kWarps) - 1);
+            const int x = sh.warp_counts[warp][lane];
+            int inc = x;
+            for (int o = 1; o < kWarps; o <<= 1) {
+                const int y = __shfl_up_sync(active, inc, o);
                 if (lane >= o) inc += y;
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sh.counts[warp][lane * 4 + i] = inc - sum + c[i];
-            if (lane == 31) sh.total_batch[warp] = inc;
+            sh.warp_counts[warp][lane] = inc - x;
+            if (lane == kWarps - 1) sh.batch[warp] = inc;
         }
         __syncthreads();
+        int eq = equal_before + sh.warp_counts[1][warp] + e_inc - e;  // equal weights ahead of this thread
+        int pos = before + sh.warp_counts[0][warp] + c_inc - c + min(eq, need) - min(equal_before, need);
+        // the first need - eq of its equal weights stay
+        uint32_t keep = certain;
+        for (uint32_t left = equal; left != 0 && eq < need; left &= left - 1, ++eq) keep |= left & -left;
 #pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            const unsigned cm = __ballot_sync(0xffffffffu, st[i] == 1), em = __ballot_sync(0xffffffffu, st[i] == 2);
-            const unsigned below = (1u << lane) - 1;
-            const int certain = sh.counts[0][i * kWarps + warp] + __popc(cm & below);
-            const int equal = equal_before + sh.counts[1][i * kWarps + warp] + __popc(em & below);
-            // kept ahead of p: the certain ones, and the equal ones that stay
-            if (st[i] == 1 || (st[i] == 2 && equal < need))
-                list[before + certain + min(equal, need) - min(equal_before, need)] = p0 + i * kThreads + tid;
-        }
-        before += sh.total_batch[0] + min(equal_before + sh.total_batch[1], need) - min(equal_before, need);
-        equal_before += sh.total_batch[1];
+        for (int i = 0; i < kHeld; ++i)
+            if ((keep >> i) & 1) list[pos++] = p0 + tid * kHeld + i;
+        before += sh.batch[0] + min(equal_before + sh.batch[1], need) - min(equal_before, need);
+        equal_before += sh.batch[1];
     }
     __syncthreads();
-    if (coop)
-        cluster.sync();  // the list is whole, and every CTA has read the weights it needs
-    else if (a.kept_weights == a.weights)
-        cluster.sync();
-    if (!coop && rank == 0)
-        for (int i = tid; i < count; i += kThreads) a.index[(size_t)bh * a.budget + i] = list[i];
-    if (rank == ranks - 1)
-        for (int i = count + tid; i < a.budget; i += kThreads) a.index[(size_t)bh * a.budget + i] = -1;
-    if (tid == 0 && rank == 0 && h == 0) a.kept_lengths[b] = count;
-    if (rank == ranks - 1 && a.kept_weights && !(all && a.kept_weights == a.weights))
-        move_scalars(a, b, h, a.weights, a.kept_weights, list, count);
-    if (all) return;
-    if (a.scale_k && rank < 2) {
-        float* scale = rank ? a.scale_v : a.scale_k;
-        move_scalars(a, b, h, scale, scale, list, count);
-    }
+}
 
-    // K on even ranks, V on odd ones; column part rank / 2
-    uint8_t* const cache = static_cast<uint8_t*>(rank & 1 ? a.cache_v : a.cache_k) + (rank >> 1) * a.part_bytes;
+// What goes with the rows: the -1s past the last kept position, the length, the
+// kept weights and the row scales (K's by `scale_k_here`, V's by `scale_v_here`).
+template <int kThreads, int kHeld>
+__device__ __forceinline__ void finish(const EvictArgs& a, int b, int h, int len, const int* list, bool lead,
+                                       bool weights_here, bool scale_k_here, bool scale_v_here) {
+    const int count = min(len, a.budget), tid = threadIdx.x;
+    const bool all = len <= a.budget;
+    const Rows rows(a, b, h);
+    if (lead) {
+        int* const index = a.index + ((size_t)b * a.n_kv_heads + h) * a.budget;
+        if (list != index)
+            for (int i = tid; i < count; i += kThreads) index[i] = list[i];
+        for (int i = count + tid; i < a.budget; i += kThreads) index[i] = -1;
+        if (tid == 0 && h == 0) a.kept_lengths[b] = count;
+    }
+    if (weights_here && a.kept_weights && !(all && a.kept_weights == a.weights))
+        move_scalars<kThreads>(rows, a.weights, a.kept_weights, list, count);
+    if (all || !a.scale_k) return;
+    if (scale_k_here) move_scalars<kThreads>(rows, a.scale_k, a.scale_k, list, count);
+    if (scale_v_here) move_scalars<kThreads>(rows, a.scale_v, a.scale_v, list, count);
+}
+
+// Moves column part `part` of the kept rows of K (which = 0) or V (1).
+template <int kThreads>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, int b, int h, int count, int which, int part,
+                                          const int* list) {
+    const int tid = threadIdx.x;
+    const Rows row_of(a, b, h);
+    uint8_t* const cache = static_cast<uint8_t*>(which ? a.cache_v : a.cache_k) + part * a.part_bytes;
     const int log_pieces = a.part_bytes == 64 ? 2 : a.part_bytes == 32 ? 1 : 3;  // 16-byte pieces of a part
     const int rows = (kThreads * kVec) >> log_pieces;                           // of a chunk
     const int piece = tid & ((1 << log_pieces) - 1), row0 = tid >> log_pieces, step = kThreads >> log_pieces;
@@ -311,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
             if (src[i] >= 0)
-                x[i] = *reinterpret_cast<const uint4*>(cache + cache_row(a, b, h, src[i]) * a.row_bytes + piece * 16);
+                x[i] = *reinterpret_cast<const uint4*>(cache + row_of(src[i]) * a.row_bytes + piece * 16);
     };
     uint4 x[kVec], y[kVec];
     int src[kVec], next[kVec];
@@ -324,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
 #pragma unroll
         for (int i = 0; i < kVec; ++i)
             if (src[i] >= 0)
-                *reinterpret_cast<uint4*>(cache + cache_row(a, b, h, j0 + row0 + i * step) * a.row_bytes + piece * 16) = x[i];
+                *reinterpret_cast<uint4*>(cache + row_of(j0 + row0 + i * step) * a.row_bytes + piece * 16) = x[i];
 #pragma unroll
         for (int i = 0; i < kVec; ++i) {
             x[i] = y[i];
@@ -333,23 +384,90 @@ __global__ void __launch_bounds__(kThreads, 2) evict_kernel(const __grid_constan
     }
 }
 
+__global__ void __launch_bounds__(kFusedThreads, 2) evict_kernel(const __grid_constant__ EvictArgs a) {
+    __shared__ Shared<kFusedThreads, kFusedHeld> sh;
+    __shared__ int s_list[kFusedThreads * kFusedHeld];
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int bh = blockIdx.x / ranks, h = bh % a.n_kv_heads, b = bh / a.n_kv_heads;
+    const int len = checked_length<kFusedThreads>(a, b);
+    if (len < 0) {
+        if (threadIdx.x == 0 && rank == 0 && h == 0) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
+        return;
+    }
+    const bool coop = len > kFusedThreads * kFusedHeld;
+    int* const list = coop ? a.index + (size_t)bh * a.budget : s_list;
+    select_tokens(a, sh, cluster, b, h, len, coop, list);
+    // the list is whole, and every CTA has read the weights it needs
+    if (coop || a.kept_weights == a.weights) cluster.sync();
+    finish<kFusedThreads, kFusedHeld>(a, b, h, len, list, rank == 0, rank == ranks - 1, rank == 0, rank == 1);
+    if (len > a.budget) move_rows<kFusedThreads>(a, b, h, a.budget, rank & 1, rank >> 1, list);
+}
+
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_constant__ EvictArgs a) {
+    __shared__ Shared<kSelectThreads, kSelectHeld> sh;
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+    const int bh = blockIdx.x / ranks, h = bh % a.n_kv_heads, b = bh / a.n_kv_heads;
+    griddep_launch();
+    const int len = checked_length<kSelectThreads>(a, b);
+    if (len < 0) {
+        if (threadIdx.x == 0 && rank == 0 && h == 0) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
+        return;
+    }
+    const bool coop = ranks > 1 && len > kSelectThreads * kSelectHeld;
+    int* const list = a.index + (size_t)bh * a.budget;
+    if (coop || rank == 0) select_tokens(a, sh, cluster, b, h, len, coop, list);
+    if (ranks > 1) cluster.sync();
+    // with one CTA it does everything; else the weights and scales are shared out
+    finish<kSelectThreads, kSelectHeld>(a, b, h, len, list, rank == 0, rank == 0, rank == min(1, ranks - 1),
+                                        rank == min(2, ranks - 1));
+}
+
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a, int log_parts) {
+    const int part = blockIdx.x & ((1 << log_parts) - 1), which = (blockIdx.x >> log_parts) & 1;
+    const int bh = blockIdx.x >> (log_parts + 1), h = bh % a.n_kv_heads, b = bh / a.n_kv_heads;
+    const int len = checked_length<kMoveThreads>(a, b);
+    griddep_wait();
+    if (len > a.budget) move_rows<kMoveThreads>(a, b, h, a.budget, which, part, a.index + (size_t)bh * a.budget);
+}
+
 }  // namespace
 
-cudaError_t launch_evict(const EvictArgs& args, cudaStream_t stream) {
+// `sms`: SMs of the device; *launches: kernels enqueued.
+cudaError_t launch_evict(const EvictArgs& args, int sms, int* launches, cudaStream_t stream) {
     EvictArgs a = args;
     a.part_bytes = a.row_bytes < 64 ? a.row_bytes : 64;
-    const int ranks = 2 * (a.row_bytes / a.part_bytes);
+    const int parts = a.row_bytes / a.part_bytes, heads = a.num_seqs * a.n_kv_heads;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(ranks * a.num_seqs * a.n_kv_heads));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ranks;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel, a);
+    cfg.stream = stream;
+    if (2ll * parts * heads <= 2ll * sms) {
+        attr[0].val.clusterDim.x = (unsigned)(2 * parts);
+        cfg.gridDim = dim3((unsigned)(2 * parts * heads));
+        cfg.blockDim = dim3(kFusedThreads);
+        *launches = 1;
+        return cudaLaunchKernelEx(&cfg, evict_kernel, a);
+    }
+    int ranks = 1;
+    while (ranks < 8 && a.max_cache_len > ranks * kSelectThreads * kSelectHeld) ranks *= 2;
+    attr[0].val.clusterDim.x = (unsigned)ranks;
+    cfg.gridDim = dim3((unsigned)(ranks * heads));
+    cfg.blockDim = dim3(kSelectThreads);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, a);
+    if (e != cudaSuccess) return e;
+    int log_parts = 0;
+    while ((1 << log_parts) < parts) ++log_parts;
+    cfg.gridDim = dim3((unsigned)(2 * parts * heads));
+    cfg.blockDim = dim3(kMoveThreads);
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    *launches = 2;
+    return cudaLaunchKernelEx(&cfg, move_kernel, a, log_parts);
 }
 
 }  // namespace pa

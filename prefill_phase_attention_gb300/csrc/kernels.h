@@ -145,9 +145,11 @@ struct KeyScheduleArgs : ScheduleArgs {
 cudaError_t launch_build_key_schedule(const KeyScheduleArgs& a, cudaStream_t stream);
 // The attention kernel's parameters and tensor maps (its v, cache_v and out unused).
 struct KeyWeightsParams : FwdParams {
+    CUtensorMap tm_q1;  // q viewed as tm_q, box (C, G, 1): one token's heads
     float* weights;  // one per cache row
     int sinks;
 };
+cudaError_t encode_one_token_map(KeyWeightsParams& p, const void* q, int total_q, int head_dim);
 cudaError_t launch_key_weights(const KeyWeightsParams& p, int head_dim, int grid, cudaStream_t stream);
 
 // Eviction by weight, in place.
@@ -168,6 +170,6 @@ struct EvictArgs {
     const int32_t* block_table;
     int block_log2, max_blocks, num_blocks;
 };
-cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_evict(const EvictArgs& a, int sms, int* launches, cudaStream_t stream);
 
 }  // namespace pa

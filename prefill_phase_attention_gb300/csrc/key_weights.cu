@@ -44,7 +44,7 @@ namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr int kThreads = 384;
-constexpr int kMaxRun = 16;  // key tiles of a unit of a one-Q-tile sequence, at most
+constexpr int kMaxRun = 8;   // key tiles of a unit of a one-Q-tile sequence, at most
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
     __threadfence_block();
     __syncthreads();
     // sanitise; the tiles of the sequences whose queries fit one Q tile set the
-    // length of their units: about four units per CTA
+    // length of their units: about eight units per CTA
     for (int b = tid; b < a.num_seqs; b += nthr) {
         const int q_start = a.cu_seqlens_q[b], q_end = a.cu_seqlens_q[b + 1];
         const int lk = a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
     }
     __threadfence_block();
     __syncthreads();
-    const unsigned long long per = s_total / (4u * (unsigned)a.num_ctas);
+    const unsigned long long per = s_total / (8u * (unsigned)a.num_ctas);
     const int run = per >= kMaxRun ? kMaxRun : (per < 2 ? 2 : (int)per & ~1);
     // units per sequence and head, numbered (SeqInfo::pad), and cost bins
     int before = 0;
@@ -281,15 +281,20 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
         if (a.seq_group[b] > 0) a.seq_scratch[b] = atomicAdd(&hist[a.seq_scratch[b]], a.seq_group[b] * a.n_kv_heads);
     __threadfence_block();
     __syncthreads();
-    // a sequence's units head by head, first keys first (under a causal mask the
-    // most expensive ones)
+    // a sequence's units: its KV heads in groups whose queries fit the L2 budget,
+    // and within a group the first keys first (under a causal mask the most
+    // expensive ones) with the group's heads adjacent
     for (int w = tid; w < before * a.n_kv_heads; w += nthr) {
         const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
         const int b = block_owner(a.seqs, a.num_seqs, i);
         const SeqInfo si = a.seqs[b];
         const SeqGeo g = seq_geo(si, tps, a.causal, a.window, a.sinks, paged);
         const int len = g.nq == 1 ? run : 2, x = i - si.pad;
-        const int pos = a.seq_scratch[b] + kvh * a.seq_group[b] + x;
+        const float head_bytes = (float)si.n * a.group * a.head_dim * 2;
+        const float fit = floorf((float)kL2GroupBytes / fmaxf(head_bytes, 1.f));
+        const int hg = fit >= (float)a.n_kv_heads ? a.n_kv_heads : (fit < 1.f ? 1 : (int)fit);
+        const int g0 = kvh - kvh % hg, gsize = min(hg, a.n_kv_heads - g0);
+        const int pos = a.seq_scratch[b] + g0 * a.seq_group[b] + x * gsize + (kvh - g0);
         if (pos < a.max_units) a.units[pos] = Unit{b, kvh, x * len, min(len, g.tiles - x * len)};
     }
 }
@@ -330,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         ctl->abort = 0;
         fence_mbar_init();
         prefetch_tmap(&p.tm_q);
+        prefetch_tmap(&p.tm_q1);
         prefetch_tmap(&p.tm_k);
         prefetch_tmap(&p.tm_ck);
     }
@@ -379,6 +385,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         for (int u_it = 0;; ++u_it) {
             const int sl = u_it & 1;
             if (!warp_wait(&ctl->unit_empty[sl], ((u_it >> 1) & 1) ^ 1, ctl, hdr)) break;
+            // claim late: only when the ring has room for the unit's first tile,
+            // so that the longest-first list still evens out the CTAs at its end
+            if (!warp_wait(&ctl->k_empty[t % C::kStagesK], ((t / C::kStagesK) & 1) ^ 1, ctl, hdr)) break;
             if (lane == 0) {
                 const int idx = atomicAdd(&hdr->counter, 1);
                 UnitSlot us;
@@ -549,6 +558,12 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         // ------------------------------- Q tiles (warp 2) and their lse (warp 3)
         uint32_t lq = 0, lp_set = 0, lp_par = 0;
         bool ok = true;
+        int col_tok[4], col_head[4];  // token and head in group of this lane's columns
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            col_tok[i] = (lane + 32 * i) / G;
+            col_head[i] = (lane + 32 * i) % G;
+        }
         UnitSlot us;
         for (int u_it = 0; ok && next_unit(u_it, us); ++u_it) {
             const SeqInfo s = us.s;
@@ -560,35 +575,44 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
                 qr = pair_queries(key_tile_at<kPaged>(g, s, us.u.q0),
                                   key_tile_at<kPaged>(g, s, us.u.q0 + (two ? 1 : 0)), two, s, g.nq, tps, p.causal,
                                   p.window, p.sinks);
+            float l[4];
+            auto load_lse = [&](int qi) {
+                const int q0 = qi * tps, qe = min(q0 + tps, s.n);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int tok = q0 + col_tok[i];
+                    // a column of no query adds exp2(-inf) = 0
+                    l[i] = tok < qe && col_tok[i] < tps
+                               ? -kLog2e * __ldg(p.lse + (size_t)(s.q_start + tok) * p.n_heads + us.u.kvh * G + col_head[i])
+                               : -INFINITY;
+                }
+            };
+            if (warp == 3 && qr.lo < qr.hi) load_lse(qr.lo);
             for (int qi = qr.lo; qi < qr.hi; ++qi, ++lq) {
                 const int st = lq % C::kStagesQ;
                 const uint32_t ph = (lq / C::kStagesQ) & 1;
-                const int q0 = qi * tps, qe = min(q0 + tps, s.n);
+                const int q0 = qi * tps;
                 if (warp == 2) {
                     if (!warp_wait(&ctl->q_empty[st], ph ^ 1, ctl, hdr)) { ok = false; break; }
-                    if (lane == 0) mbar_arrive_expect_tx(&ctl->q_full[st], G * tps * C::kRowBytes * C::kChunks);
+                    // a decode row's Q tile is one token's heads: the rest of the
+                    // stage keeps what it held, in columns that no sum takes
+                    const bool one = s.n == 1;
+                    if (lane == 0)
+                        mbar_arrive_expect_tx(&ctl->q_full[st], G * (one ? 1 : tps) * C::kRowBytes * C::kChunks);
                     __syncwarp();
                     if (lane < C::kChunks)
-                        tma_load_3d(q_smem + st * C::kTileBytes + lane * C::kChunkBytes, &p.tm_q, &ctl->q_full[st],
+                        tma_load_3d(q_smem + st * C::kTileBytes + lane * C::kChunkBytes, one ? &p.tm_q1 : &p.tm_q, &ctl->q_full[st],
                                     lane * C::kChunkCols, us.u.kvh * G, s.q_start + q0);
                     __syncwarp();
                     lp_set |= 1u << st;
                     lp_par = (lp_par & ~(1u << st)) | (ph << st);
                 } else {
-                    float l[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = lane + 32 * i, tok = q0 + c / G;
-                        // a column of no query adds exp2(-inf) = 0
-                        l[i] = tok < qe && c < tps * G
-                                   ? -kLog2e * __ldg(p.lse + (size_t)(s.q_start + tok) * p.n_heads + us.u.kvh * G + c % G)
-                                   : -INFINITY;
-                    }
                     if (!warp_wait(&ctl->l_empty[st], ph ^ 1, ctl, hdr)) { ok = false; break; }
 #pragma unroll
                     for (int i = 0; i < 4; ++i) ctl->neg_lse[st][lane + 32 * i] = l[i];
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->l_full[st]);
+                    if (qi + 1 < qr.hi) load_lse(qi + 1);  // on its way during the next wait
                 }
             }
         }
@@ -687,27 +711,30 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
                         const float4* nl = reinterpret_cast<const float4*>(ctl->neg_lse[qst]);
                         float2 a0 = make_float2(0.f, 0.f), a1 = a0;
                         if (whole) {
+                            // 32 columns are summed while the next 32 are on their way
+                            uint32_t v[2][32];
+                            tmem_ld32(col, v[0]);
 #pragma unroll
-                            for (int c = 0; c < kBlockN; c += 64) {
-                                uint32_t v0[32], v1[32];
-                                tmem_ld32(col + c, v0);
-                                tmem_ld32(col + c + 32, v1);
+                            for (int c = 0; c < kBlockN; c += 32) {
+                                uint32_t (&x)[32] = v[(c / 32) & 1];
                                 tmem_wait_ld();
-                                reg_fence(v0);
-                                reg_fence(v1);
-                                if (c + 64 == kBlockN) {  // everything of the buffer is in registers
+                                reg_fence(x);
+                                if (c + 32 < kBlockN) {
+                                    tmem_ld32(col + c + 32, v[(c / 32 + 1) & 1]);
+                                } else {  // everything of the buffer is in registers
                                     tc_fence_before();
                                     __syncwarp();
                                     if (lane == 0) mbar_arrive(&ctl->s_empty[slot][buf]);
                                 }
 #pragma unroll
-                                for (int e = 0; e < 64; e += 4) {
+                                for (int e = 0; e < 32; e += 4) {
                                     const float4 l = nl[(c + e) / 4];
-                                    const uint32_t* v = e < 32 ? v0 + e : v1 + e - 32;
-                                    const float2 s0 = __ffma2_rn(
-                                        make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), mul2, make_float2(l.x, l.y));
-                                    const float2 s1 = __ffma2_rn(
-                                        make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), mul2, make_float2(l.z, l.w));
+                                    const float2 s0 =
+                                        __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2,
+                                                   make_float2(l.x, l.y));
+                                    const float2 s1 =
+                                        __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), mul2,
+                                                   make_float2(l.z, l.w));
                                     a0 = __fadd2_rn(a0, make_float2(ex2(s0.x), ex2(s0.y)));
                                     a1 = __fadd2_rn(a1, make_float2(ex2(s1.x), ex2(s1.y)));
                                 }
