@@ -255,10 +255,12 @@ pa_status prefill_attn_varlen_ex(
  * sequence stay visible: the query at absolute position p sees key j when
  * j <= p and (j > p - W or j < sink_tokens).  sink_tokens = 0 is the plain
  * window.  Every option of pa_options applies but wait_timeout_test.  Only the
- * tiles of 128 keys that hold a visible key are read -- whole, so every row of
- * [0, cache_offsets[b]) must hold finite values (and, in a paged cache, every
- * table entry there must name a block of the pool), even rows that no query
- * sees any more.  A few long rows are split along their keys and joined: then
+ * tiles of 128 keys that hold a visible key are read -- whole, so rows of
+ * [0, cache_offsets[b]) next to visible ones must hold finite values.  In a
+ * paged cache tiles start at multiples of 128 positions, and only the table
+ * entries of the sink tiles, of the tiles from the oldest query's window on and
+ * of the new tokens must name a block of the pool: the blocks in between may
+ * have been given back.  A few long rows are split along their keys and joined: then
  * three kernels run instead of two, and the partial results (fp32, at most
  * 64 MiB) live in the per-stream workspace.  Under graph capture the stream
  * must already have run a call of at least these sizes.

@@ -216,36 +216,96 @@ def prefill_attn_varlen_ex(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v
     _check(load().prefill_attn_varlen_ex(*args[:-1], ctypes.byref(opts), args[-1]))
 
 
-def _cuda_tensor(name, t, dtype, shape=None):
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+# The long-context calls are often a few microseconds of GPU work: their checks
+# are one pass over (name, tensor, dtype, elements) with as few attribute reads
+# as they need.  The shapes of q, k and the caches are checked as such; the other
+# tensors are dense in the layout their documentation states, so that their
+# element count says whether they fit.
+_BF16, _I8, _F32, _I32 = torch.bfloat16, torch.int8, torch.float32, torch.int32
 
 
-def _check_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table):
-    """Shapes that must agree (the long-context calls check them; v, cache_v, out and lse may be None)."""
-    if q.dim() != 3 or k.dim() != 3 or cache_k.dim() != 4:
-        raise ValueError("q/k/v are [total_q, heads, head_dim]; caches are [num_seqs, kv_heads, cap, head_dim]")
-    (t, h, d), hk, b = q.shape, k.shape[1], cache_offsets.numel()
-    slots = cache_k.shape[0] if block_table is not None else b
-    for name, x, shape in (("k", k, (t, hk, d)), ("v", v, (t, hk, d)), ("out", out, (t, h, d)), ("lse", lse, (t, h)),
-                           ("cache_k", cache_k, (slots, hk, cache_k.shape[2], d)), ("cache_v", cache_v, cache_k.shape),
-                           ("cu_seqlens_q", cu_seqlens_q, (b + 1,)), ("cu_seqlens_k", cu_seqlens_k, (b + 1,)),
-                           ("cache_offsets", cache_offsets, (b,))):
-        if x is not None and tuple(x.shape) != tuple(shape):
-            raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
-    if block_table is not None and block_table.shape[0] != b:
-        raise ValueError(f"block_table must have {b} rows")
-    same_device(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table)
+def _check_tensors(device: int, *specs) -> None:
+    """Each spec (name, tensor or None, dtype, elements): contiguous, CUDA, on `device`, of that type and size."""
+    for name, t, dtype, n in specs:
+        if t is not None and (t.dtype is not dtype or t.get_device() != device or t.numel() != n or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements on cuda:{device}, "
+                             f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def same_device(*tensors):
-    """Every tensor on one device, the current one (the library launches there)."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"every tensor must be on the current device (cuda:{dev}), not {t.device}")
+def _current_device(q) -> int:
+    """The index of q's device, which must be the current one (the library launches there)."""
+    device = q.get_device()
+    if device < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on cuda:{device}, but the current device is cuda:{torch._C._cuda_getDevice()}")
+    return device
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_on(stream, device: int) -> int:
+    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream_handle(stream, device)
+
+
+def _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d):
+    """Checks a call's cache tensors; returns (slot capacity, whether the cache is int8, rows of the cache)."""
+    if cache_k.dim() != 4:
+        raise ValueError("caches are [num_seqs, kv_heads, cap, head_dim], or [num_blocks, kv_heads, block_size, head_dim]")
+    n, ck_heads, rows, ck_dim = cache_k.shape
+    if ck_heads != hk or ck_dim != d or (block_table is None and n != b):
+        raise ValueError(f"cache_k has shape {tuple(cache_k.shape)}: {hk} KV heads of {d}"
+                         + ("" if block_table is not None else f" in {b} slots") + " are wanted")
+    dtype, quant, cap, total = _BF16, False, rows, n * hk * rows
+    if block_table is not None:
+        if block_table.dim() != 2 or block_table.shape[0] != b:
+            raise ValueError(f"block_table must be [{b}, max_blocks_per_seq]")
+        cap = block_table.shape[1] * rows
+        _check_tensors(device, ("block_table", block_table, _I32, block_table.numel()))
+    if cache_k_scale is not None or cache_v_scale is not None:
+        if cache_k_scale is None or cache_v_scale is None:
+            raise ValueError("an int8 cache needs both cache_k_scale and cache_v_scale")
+        dtype, quant = _I8, True
+        _check_tensors(device, ("cache_k_scale", cache_k_scale, _F32, total), ("cache_v_scale", cache_v_scale, _F32, total))
+    _check_tensors(device, ("cache_k", cache_k, dtype, total * d), ("cache_v", cache_v, dtype, total * d))
+    return cap, quant, total
+
+
+def _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table,
+                    cache_k_scale, cache_v_scale):
+    """Checks the tensors of a long-context call; returns (device, cache capacity, whether it is int8, cache rows)."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q/k/v are [total_q, heads, head_dim]")
+    device = _current_device(q)
+    (t, h, d), (kt, hk, kd), b = q.shape, k.shape, cache_offsets.numel()
+    if kt != t or kd != d:
+        raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+    nq, nk = t * h * d, t * hk * d
+    _check_tensors(device, ("q", q, _BF16, nq), ("k", k, _BF16, nk), ("v", v, _BF16, nk), ("out", out, _BF16, nq),
+                   ("lse", lse, _F32, t * h), ("cu_seqlens_q", cu_seqlens_q, _I32, b + 1),
+                   ("cu_seqlens_k", cu_seqlens_k, _I32, b + 1), ("cache_offsets", cache_offsets, _I32, b))
+    return device, *_cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d)
+
+
+def _pointers(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, cap, scale):
+    t, h, d = q.shape
+    return (q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(),
+            cache_k.data_ptr(), cache_v.data_ptr(), cache_offsets.data_ptr(), out.data_ptr(), _ptr(lse),
+            cache_offsets.numel(), t, cap, h, k.shape[1], d, d ** -0.5 if scale is None else scale)
+
+
+def _options(cache_k, block_table, cache_k_scale, cache_v_scale, window=0, rope_theta=0.0, schedule=0):
+    """pa_options by position (struct_size, window, block_table, block_size, max_blocks_per_seq, num_blocks, ...)."""
+    paged, quant = block_table is not None, cache_k_scale is not None
+    return PaOptions(_OPTIONS_SIZE, window, block_table.data_ptr() if paged else None,
+                     cache_k.shape[2] if paged else 0, block_table.shape[1] if paged else 0,
+                     cache_k.shape[0] if paged else 0, 0, rope_theta, 0, 1 if quant else 0, 0,
+                     cache_k_scale.data_ptr() if quant else None, cache_v_scale.data_ptr() if quant else None, 0, schedule)
+
+
+_OPTIONS_SIZE, _PREFIX_SIZE = ctypes.sizeof(PaOptions), ctypes.sizeof(PaPrefix)
 
 
 def prefill_attn_varlen_sinks(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse=None, *,
@@ -257,13 +317,12 @@ def prefill_attn_varlen_sinks(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cach
     The query at absolute position p sees key j when j <= p and (j > p - window or
     j < sink_tokens).  Tensors and options as in prefill_attn_varlen_ex.
     """
-    cap, quant = _cache_args(cache_k, block_table, cache_k_scale, cache_v_scale)
-    args = _varlen_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, scale, True,
-                        stream, max_cache_len=cap, cache_dtype=torch.int8 if quant else torch.bfloat16)
-    _check_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table)
-    opts = make_options(window, block_table, cache_k.shape[2], cache_k.shape[0], rope_theta, cache_k_scale,
-                        cache_v_scale, schedule=schedule)
-    _check(load().prefill_attn_varlen_sinks(*args[:-2], int(sink_tokens), ctypes.byref(opts), args[-1]))
+    device, cap, _, _ = _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse,
+                                        block_table, cache_k_scale, cache_v_scale)
+    _check((_lib or load()).prefill_attn_varlen_sinks(
+        *_pointers(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, cap, scale),
+        sink_tokens, _options(cache_k, block_table, cache_k_scale, cache_v_scale, window, rope_theta, schedule),
+        _stream_on(stream, device)))
 
 
 def prefill_attn_varlen_prefix(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse=None, *,
@@ -280,29 +339,25 @@ def prefill_attn_varlen_prefix(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cac
     and prefix_len its tokens.  cu_seqlens_k and cache_offsets count each sequence's own
     tokens, which follow the prefix.
     """
-    cap, quant = _cache_args(cache_k, block_table, cache_k_scale, cache_v_scale)
-    dtype = torch.int8 if quant else torch.bfloat16
-    args = _varlen_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, scale, causal,
-                        stream, max_cache_len=cap, cache_dtype=dtype)
-    _check_shapes(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table)
+    device, cap, quant, _ = _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out,
+                                            lse, block_table, cache_k_scale, cache_v_scale)
     pre = PaPrefix()
-    pre.struct_size = ctypes.sizeof(PaPrefix)
+    pre.struct_size = _PREFIX_SIZE
     if block_table is not None:
         if prefix_table is None or prefix_len is None:
             raise ValueError("a paged cache needs prefix_table and prefix_len")
-        _cuda_tensor("prefix_table", prefix_table, torch.int32)
+        _check_tensors(device, ("prefix_table", prefix_table, _I32, prefix_table.numel()))
         if prefix_len > prefix_table.numel() * cache_k.shape[2]:
             raise ValueError("prefix_table has fewer blocks than prefix_len needs")
-        same_device(prefix_table)
         pre.block_table = prefix_table.data_ptr()
     else:
         if prefix_k is None or prefix_v is None:
             raise ValueError("a contiguous cache needs prefix_k and prefix_v")
-        _cuda_tensor("prefix_k", prefix_k, dtype)
         if prefix_k.dim() != 3 or prefix_k.shape[0] != k.shape[1] or prefix_k.shape[2] != q.shape[2]:
             raise ValueError("prefix_k is [n_kv_heads, capacity, head_dim]")
-        _cuda_tensor("prefix_v", prefix_v, dtype, prefix_k.shape)
-        same_device(prefix_k, prefix_v, prefix_k_scale, prefix_v_scale)
+        rows, dtype = prefix_k.shape[0] * prefix_k.shape[1], _I8 if quant else _BF16
+        _check_tensors(device, ("prefix_k", prefix_k, dtype, rows * prefix_k.shape[2]),
+                       ("prefix_v", prefix_v, dtype, rows * prefix_k.shape[2]))
         pre.k, pre.v, pre.capacity = prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_k.shape[1]
         if prefix_len is None:
             prefix_len = prefix_k.shape[1]
@@ -310,12 +365,13 @@ def prefill_attn_varlen_prefix(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cac
             for name, t in (("prefix_k_scale", prefix_k_scale), ("prefix_v_scale", prefix_v_scale)):
                 if t is None:
                     raise ValueError(f"an int8 cache needs {name}")
-                _cuda_tensor(name, t, torch.float32, prefix_k.shape[:2])
+                _check_tensors(device, (name, t, _F32, rows))
             pre.k_scale, pre.v_scale = prefix_k_scale.data_ptr(), prefix_v_scale.data_ptr()
-    pre.len = int(prefix_len)
-    opts = make_options(0, block_table, cache_k.shape[2], cache_k.shape[0], rope_theta, cache_k_scale, cache_v_scale,
-                        schedule=schedule)
-    _check(load().prefill_attn_varlen_prefix(*args[:-1], ctypes.byref(pre), ctypes.byref(opts), args[-1]))
+    pre.len = prefix_len
+    _check((_lib or load()).prefill_attn_varlen_prefix(
+        *_pointers(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, cap, scale),
+        1 if causal else 0, pre, _options(cache_k, block_table, cache_k_scale, cache_v_scale, 0, rope_theta, schedule),
+        _stream_on(stream, device)))
 
 
 def prefill_attn_key_weights(q, k, cu_seqlens_q, cu_seqlens_k, cache_k, cache_offsets, lse, weights, *,
@@ -328,25 +384,18 @@ def prefill_attn_key_weights(q, k, cu_seqlens_q, cu_seqlens_k, cache_k, cache_of
     keys are set.  lse is what the attention call of the same step wrote; the other arguments
     are those of that call (prefix_len: its shared prefix, for the rotary positions).
     """
-    cap, quant = _cache_args(cache_k, block_table, cache_k_scale, cache_k_scale)
-    dtype = torch.int8 if quant else torch.bfloat16
-    for name, t, dt in (("q", q, torch.bfloat16), ("k", k, torch.bfloat16), ("cache_k", cache_k, dtype),
-                        ("cu_seqlens_q", cu_seqlens_q, torch.int32), ("cu_seqlens_k", cu_seqlens_k, torch.int32),
-                        ("cache_offsets", cache_offsets, torch.int32), ("lse", lse, torch.float32)):
-        _cuda_tensor(name, t, dt)
-    _check_shapes(q, k, None, cu_seqlens_q, cu_seqlens_k, cache_k, None, cache_offsets, None, lse, block_table)
-    _cuda_tensor("weights", weights, torch.float32, cache_k.shape[:-1])
-    same_device(weights, cache_k_scale)
-    total_q, n_heads, head_dim = q.shape
-    if scale is None:
-        scale = head_dim ** -0.5
-    opts = make_options(window, block_table, cache_k.shape[2], cache_k.shape[0], rope_theta, cache_k_scale,
-                        cache_k_scale)
-    _check(load().prefill_attn_key_weights(
+    if lse is None:
+        raise ValueError("prefill_attn_key_weights needs lse")
+    device, cap, _, rows = _attention_args(q, k, None, cu_seqlens_q, cu_seqlens_k, cache_k, None, cache_offsets, None, lse,
+                                           block_table, cache_k_scale, cache_k_scale)
+    _check_tensors(device, ("weights", weights, _F32, rows))
+    t, h, d = q.shape
+    hk, b = k.shape[1], cache_offsets.numel()
+    _check((_lib or load()).prefill_attn_key_weights(
         q.data_ptr(), k.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cache_k.data_ptr(),
-        cache_offsets.data_ptr(), lse.data_ptr(), weights.data_ptr(), cache_offsets.numel(), total_q,
-        cache_k.shape[2] if cap is None else cap, n_heads, k.shape[1], head_dim, float(scale), int(bool(causal)),
-        int(sink_tokens), int(prefix_len), ctypes.byref(opts), _stream_handle(stream, q.get_device())))
+        cache_offsets.data_ptr(), lse.data_ptr(), weights.data_ptr(), b, t, cap, h, hk, d,
+        d ** -0.5 if scale is None else scale, 1 if causal else 0, sink_tokens, prefix_len,
+        _options(cache_k, block_table, cache_k_scale, cache_k_scale, window, rope_theta), _stream_on(stream, device)))
 
 
 def prefill_attn_evict(cache_k, cache_v, weights, lengths, kept_lengths, kept_index=None, kept_weights=None, *,
@@ -359,30 +408,18 @@ def prefill_attn_evict(cache_k, cache_v, weights, lengths, kept_lengths, kept_in
     lengths / kept_lengths int32 [num_seqs]; kept_index int32 [num_seqs, n_kv_heads, budget] or
     None; weights / kept_weights fp32 of shape cache_k.shape[:-1] (kept_weights may be weights).
     """
-    cap, quant = _cache_args(cache_k, block_table, cache_k_scale, cache_v_scale)
-    dtype = torch.int8 if quant else torch.bfloat16
+    device = _current_device(cache_k)
     if cache_k.dim() != 4:
         raise ValueError("caches are [num_seqs, kv_heads, cap, head_dim]")
-    b, hk = lengths.numel(), cache_k.shape[1]
-    _cuda_tensor("cache_k", cache_k, dtype, (b, *cache_k.shape[1:]) if block_table is None else None)
-    _cuda_tensor("cache_v", cache_v, dtype, cache_k.shape)
-    _cuda_tensor("weights", weights, torch.float32, cache_k.shape[:-1])
-    _cuda_tensor("lengths", lengths, torch.int32, (b,))
-    _cuda_tensor("kept_lengths", kept_lengths, torch.int32, (b,))
-    if block_table is not None and block_table.shape[0] != b:
-        raise ValueError(f"block_table must have {b} rows")
-    if kept_index is not None:
-        _cuda_tensor("kept_index", kept_index, torch.int32, (b, hk, budget))
-    if kept_weights is not None:
-        _cuda_tensor("kept_weights", kept_weights, torch.float32, cache_k.shape[:-1])
-    same_device(cache_k, cache_v, weights, lengths, kept_lengths, kept_index, kept_weights, block_table, cache_k_scale,
-                cache_v_scale)
-    opts = make_options(0, block_table, cache_k.shape[2], cache_k.shape[0], 0.0, cache_k_scale, cache_v_scale)
-    _check(load().prefill_attn_evict(
+    b, (_, hk, _, d) = lengths.numel(), cache_k.shape
+    cap, _, rows = _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d)
+    _check_tensors(device, ("weights", weights, _F32, rows), ("lengths", lengths, _I32, b),
+                   ("kept_lengths", kept_lengths, _I32, b), ("kept_index", kept_index, _I32, b * hk * budget),
+                   ("kept_weights", kept_weights, _F32, rows))
+    _check((_lib or load()).prefill_attn_evict(
         cache_k.data_ptr(), cache_v.data_ptr(), weights.data_ptr(), lengths.data_ptr(), kept_lengths.data_ptr(),
-        None if kept_index is None else kept_index.data_ptr(), None if kept_weights is None else kept_weights.data_ptr(),
-        b, cache_k.shape[2] if cap is None else cap, hk, cache_k.shape[3], int(budget), int(sink_tokens),
-        int(recent_tokens), ctypes.byref(opts), _stream_handle(stream, cache_k.get_device())))
+        _ptr(kept_index), _ptr(kept_weights), b, cap, hk, d, budget, sink_tokens, recent_tokens,
+        _options(cache_k, block_table, cache_k_scale, cache_v_scale), _stream_on(stream, device)))
 
 
 def prefill_attn_varlen_noalloc(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out,

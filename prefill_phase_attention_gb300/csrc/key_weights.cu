@@ -188,46 +188,63 @@ __device__ __forceinline__ QRange pair_queries(const KeyTile& k0, const KeyTile&
     return r;
 }
 
+// Key tiles of a unit of a sequence whose queries fit one Q tile: about eight
+// units per CTA of the `total` tiles of all of them.
+__device__ __forceinline__ int run_length(unsigned long long total, int num_ctas) {
+    const unsigned long long per = total / (8u * (unsigned)num_ctas);
+    return per >= kMaxRun ? kMaxRun : (per < 2 ? 2 : (int)per & ~1);
+}
+
+// Writes unit x of sequence b and KV head kvh (its tiles in units of len).  A
+// sequence's units: its KV heads in groups whose queries fit the L2 budget, and
+// within a group the first keys first (under a causal mask the most expensive
+// ones) with the group's heads adjacent.
+__device__ __forceinline__ void emit_keys(const KeyScheduleArgs& a, const SeqInfo& si, int b, int x, int kvh, int tiles,
+                                          int len, int units, int first) {
+    const float head_bytes = (float)si.n * a.group * a.head_dim * 2;
+    const float fit = floorf((float)kL2GroupBytes / fmaxf(head_bytes, 1.f));
+    const int hg = fit >= (float)a.n_kv_heads ? a.n_kv_heads : (fit < 1.f ? 1 : (int)fit);
+    const int g0 = kvh - kvh % hg, gsize = min(hg, a.n_kv_heads - g0);
+    const int pos = first + g0 * units + x * gsize + (kvh - g0);
+    if (pos < a.max_units) a.units[pos] = Unit{b, kvh, x * len, min(len, tiles - x * len)};
+}
+
 __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_constant__ KeyScheduleArgs a) {
     __shared__ int hist[kCostBins];
     __shared__ int warp_sums[32];
     __shared__ unsigned long long s_total;
+    __shared__ SeqInfo s_seqs[kSmemSeqs];
+    __shared__ int s_first[kSmemSeqs], s_units[kSmemSeqs];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nthr = blockDim.x, nwarps = nthr >> 5;
     const int tps = kBlockM / a.group;
     griddep_launch();
+    const bool small = a.num_seqs <= kSmemSeqs;
+    SeqInfo* const seqs = small ? s_seqs : a.seqs;
+    int* const seq_first = small ? s_first : a.seq_scratch;  // cost bin, then first unit of the sequence
+    int* const seq_units = small ? s_units : a.seq_group;    // units per head
     for (int i = tid; i < kCostBins; i += nthr) hist[i] = 0;
     if (tid == 0) s_total = 0;
     const bool paged = a.block_table != nullptr;
-    if (paged) {
-        for (int b = warp; b < a.num_seqs; b += nwarps) {
-            const long long lk = (long long)a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
-            const long long used = lk > 0 ? (lk + a.block_size - 1) / a.block_size : 0;
-            const int nb = used < a.max_blocks ? (int)used : a.max_blocks;
-            bool bad = false;
-            for (int L = lane; L < nb; L += 32) {
-                const int blk = a.block_table[(size_t)b * a.max_blocks + L];
-                bad |= blk < 0 || blk >= a.num_blocks;
-            }
-            bad = __any_sync(0xffffffffu, bad);
-            if (lane == 0) a.seqs[b].pad = bad ? 1 : 0;
-        }
-    }
+    for (int b = tid; b < a.num_seqs; b += nthr) seqs[b] = checked_sequence(a, b);
     __threadfence_block();
     __syncthreads();
-    // sanitise; the tiles of the sequences whose queries fit one Q tile set the
-    // length of their units: about eight units per CTA
+    if (paged) {
+        for (int b = warp; b < a.num_seqs; b += nwarps) {
+            const bool bad = bad_visible_blocks(a.block_table + (size_t)b * a.max_blocks, seqs[b], a.block_size,
+                                                a.num_blocks, a.causal, a.window, a.sinks, lane);
+            if (bad && lane == 0) seqs[b].n = -1;
+        }
+        __threadfence_block();
+        __syncthreads();
+    }
     for (int b = tid; b < a.num_seqs; b += nthr) {
-        const int q_start = a.cu_seqlens_q[b], q_end = a.cu_seqlens_q[b + 1];
-        const int lk = a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
-        const int P = a.cache_offsets[b];
-        const long long n = (long long)q_end - q_start;
-        const bool ok = q_start >= 0 && n >= 0 && (long long)q_end <= a.total_q && P >= 0 &&
-                        (long long)lk == (long long)P + n && (long long)P + n <= a.max_cache_len &&
-                        (b > 0 || q_start == 0) && !(paged && a.seqs[b].pad != 0);
-        if (!ok) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
-        SeqInfo si{ok ? q_start : 0, ok ? (int)n : 0, ok ? P : 0, 0};
-        a.seqs[b] = si;
+        SeqInfo si = seqs[b];
+        if (si.n < 0) {
+            atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
+            si = SeqInfo{0, 0, 0, 0};
+            seqs[b] = si;
+        }
         if (si.n > 0) {
             const SeqGeo g = seq_geo(si, tps, a.causal, a.window, a.sinks, paged);
             if (g.nq == 1) atomicAdd(&s_total, (unsigned long long)g.tiles * a.n_kv_heads);
@@ -235,27 +252,30 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
     }
     __threadfence_block();
     __syncthreads();
-    const unsigned long long per = s_total / (8u * (unsigned)a.num_ctas);
-    const int run = per >= kMaxRun ? kMaxRun : (per < 2 ? 2 : (int)per & ~1);
+    const int run = run_length(s_total, a.num_ctas);
     // units per sequence and head, numbered (SeqInfo::pad), and cost bins
     int before = 0;
     for (int b0 = 0; b0 < a.num_seqs; b0 += nthr) {
         const int b = b0 + tid;
         int units = 0;
+        SeqInfo si{0, 0, 0, 0};
         SeqGeo g{};
-        if (b < a.num_seqs && a.seqs[b].n > 0) {
-            g = seq_geo(a.seqs[b], tps, a.causal, a.window, a.sinks, paged);
+        if (b < a.num_seqs) si = seqs[b];
+        if (si.n > 0) {
+            g = seq_geo(si, tps, a.causal, a.window, a.sinks, paged);
             const int len = g.nq == 1 ? run : 2;
             units = (g.tiles + len - 1) / len;
         }
         int chunk_total;
         const int excl = block_exclusive_scan(units, warp_sums, &chunk_total);
         if (b < a.num_seqs) {
-            a.seqs[b].pad = before + excl;
-            a.seq_group[b] = units;
+            si.pad = before + excl;
+            a.seqs[b] = si;
+            if (small) s_seqs[b] = si;
+            seq_units[b] = units;
             if (units > 0) {
                 const int bin = cost_bin((long long)g.tiles * g.nq * a.n_kv_heads);
-                a.seq_scratch[b] = bin;
+                seq_first[b] = bin;
                 atomicAdd(&hist[bin], units * a.n_kv_heads);
             }
         }
@@ -278,24 +298,45 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
     }
     __syncthreads();
     for (int b = tid; b < a.num_seqs; b += nthr)
-        if (a.seq_group[b] > 0) a.seq_scratch[b] = atomicAdd(&hist[a.seq_scratch[b]], a.seq_group[b] * a.n_kv_heads);
+        if (seq_units[b] > 0) seq_first[b] = atomicAdd(&hist[seq_first[b]], seq_units[b] * a.n_kv_heads);
     __threadfence_block();
     __syncthreads();
-    // a sequence's units: its KV heads in groups whose queries fit the L2 budget,
-    // and within a group the first keys first (under a causal mask the most
-    // expensive ones) with the group's heads adjacent
     for (int w = tid; w < before * a.n_kv_heads; w += nthr) {
         const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
-        const int b = block_owner(a.seqs, a.num_seqs, i);
-        const SeqInfo si = a.seqs[b];
+        const int b = block_owner(seqs, a.num_seqs, i);
+        const SeqInfo si = seqs[b];
         const SeqGeo g = seq_geo(si, tps, a.causal, a.window, a.sinks, paged);
-        const int len = g.nq == 1 ? run : 2, x = i - si.pad;
-        const float head_bytes = (float)si.n * a.group * a.head_dim * 2;
-        const float fit = floorf((float)kL2GroupBytes / fmaxf(head_bytes, 1.f));
-        const int hg = fit >= (float)a.n_kv_heads ? a.n_kv_heads : (fit < 1.f ? 1 : (int)fit);
-        const int g0 = kvh - kvh % hg, gsize = min(hg, a.n_kv_heads - g0);
-        const int pos = a.seq_scratch[b] + g0 * a.seq_group[b] + x * gsize + (kvh - g0);
-        if (pos < a.max_units) a.units[pos] = Unit{b, kvh, x * len, min(len, g.tiles - x * len)};
+        emit_keys(a, si, b, i - si.pad, kvh, g.tiles, g.nq == 1 ? run : 2, seq_units[b], seq_first[b]);
+    }
+}
+
+// The same for a few sequences (kFewSeqs): see schedule.cuh.
+__global__ void __launch_bounds__(kFewThreads) build_key_schedule_few_kernel(const __grid_constant__ KeyScheduleArgs a) {
+    __shared__ FewSeqs f;
+    __shared__ int s_tiles[kFewSeqs], s_len[kFewSeqs];
+    const int tid = threadIdx.x, tps = kBlockM / a.group;
+    const bool paged = a.block_table != nullptr;
+    griddep_launch();
+    load_few(a, f, a.sinks, nullptr, 0);
+    SeqGeo g{};
+    if (tid < a.num_seqs && f.seqs[tid].n > 0) {
+        g = seq_geo(f.seqs[tid], tps, a.causal, a.window, a.sinks, paged);
+        if (g.nq == 1) atomicAdd(&f.total, (unsigned long long)g.tiles * a.n_kv_heads);
+    }
+    __syncthreads();
+    if (tid < a.num_seqs) {
+        const int len = g.nq == 1 ? run_length(f.total, a.num_ctas) : 2;
+        s_tiles[tid] = g.tiles;
+        s_len[tid] = len;
+        f.blocks[tid] = f.units[tid] = (g.tiles + len - 1) / len;
+        f.cost[tid] = (float)g.tiles * (float)g.nq;
+    }
+    __syncthreads();
+    const int blocks = rank_few(a, f, a.num_seqs);
+    for (int w = tid; w < blocks * a.n_kv_heads; w += kFewThreads) {
+        const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
+        const int b = block_owner(f.seqs, a.num_seqs, i);
+        emit_keys(a, f.seqs[b], b, i - f.seqs[b].pad, kvh, s_tiles[b], s_len[b], f.units[b], f.first[b]);
     }
 }
 
@@ -382,12 +423,15 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     if (warp == 0) {
         // ------------------------------------------------- unit fetch, K tiles
         uint32_t t = 0, lp_set = 0, lp_par = 0;
+        bool short_units = true;
         for (int u_it = 0;; ++u_it) {
             const int sl = u_it & 1;
             if (!warp_wait(&ctl->unit_empty[sl], ((u_it >> 1) & 1) ^ 1, ctl, hdr)) break;
             // claim late: only when the ring has room for the unit's first tile,
             // so that the longest-first list still evens out the CTAs at its end
-            if (!warp_wait(&ctl->k_empty[t % C::kStagesK], ((t / C::kStagesK) & 1) ^ 1, ctl, hdr)) break;
+            // (not for decode rows, whose units are short and alike: there the
+            // claim's latency would show)
+            if (!short_units && !warp_wait(&ctl->k_empty[t % C::kStagesK], ((t / C::kStagesK) & 1) ^ 1, ctl, hdr)) break;
             if (lane == 0) {
                 const int idx = atomicAdd(&hdr->counter, 1);
                 UnitSlot us;
@@ -404,6 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             if (u.b < 0) break;
             const SeqInfo s = ctl->slot[sl].s;
             const SeqGeo g = geo(s);
+            short_units = g.nq == 1;
             bool ok = true;
             for (int x = u.q0; x < u.q0 + u.ntiles; ++x, ++t) {
                 const KeyTile k = key_tile_at<kPaged>(g, s, x);
@@ -821,7 +866,10 @@ cudaError_t launch_dim(const KeyWeightsParams& p, int grid, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_build_key_schedule(const KeyScheduleArgs& a, cudaStream_t stream) {
-    build_key_schedule_kernel<<<1, 1024, 0, stream>>>(a);
+    if (a.num_seqs <= kFewSeqs)
+        build_key_schedule_few_kernel<<<1, kFewThreads, 0, stream>>>(a);
+    else
+        build_key_schedule_kernel<<<1, 1024, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -4,6 +4,8 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "kernels.h"
+#include "prefill_attn.h"
 
 namespace pa {
 
@@ -80,6 +82,159 @@ __device__ __forceinline__ int kv_head_group(const SeqInfo& si, int head_dim, in
     float g = floorf((float)kL2GroupBytes / fmaxf(head_bytes, 1.f));
     if (head_cost > 0) g = fmaxf(g, ceilf((float)num_ctas * (float)longest / (float)head_cost));
     return g >= (float)n_kv_heads ? n_kv_heads : (g < 1.f ? 1 : (int)g);
+}
+
+// Whether entries [lo, hi) of a sequence's block table name a block outside the
+// pool (one warp; 16 loads of a lane in flight).
+__device__ __forceinline__ bool bad_blocks(const int32_t* table, int lo, int hi, int num_blocks, int lane) {
+    bool bad = false;
+    for (int L = lo + lane; L < hi; L += 32 * 16) {
+        int blk[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) blk[i] = L + 32 * i < hi ? __ldg(table + L + 32 * i) : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) bad |= (unsigned)blk[i] >= (unsigned)num_blocks;
+    }
+    return __any_sync(0xffffffffu, bad);
+}
+
+// The same for the blocks that a sequence's queries touch: those of its sink
+// tiles, and those from its window's first tile to its last new token (one warp).
+__device__ __forceinline__ bool bad_visible_blocks(const int32_t* table, const SeqInfo& si, int block_size,
+                                                   int num_blocks, int causal, int window, int sinks, int lane) {
+    if (si.n == 0) return false;
+    const StreamGeo g = stream_geo(si.n, si.P, 0, si.n, causal, window, sinks, false, true);
+    const int sink_end = min(g.nsink * kBlockN, si.P);
+    const int first = g.lo < prefix_tiles(si.P) ? g.lo * kBlockN : si.P;
+    return bad_blocks(table, 0, (sink_end + block_size - 1) / block_size, num_blocks, lane) |
+           bad_blocks(table, first / block_size, (si.P + si.n - 1) / block_size + 1, num_blocks, lane);
+}
+
+// Sequence b of a call as its device metadata states it; n = -1 when that is inconsistent.
+__device__ __forceinline__ SeqInfo checked_sequence(const ScheduleArgs& a, int b) {
+    const int q_start = a.cu_seqlens_q[b], q_end = a.cu_seqlens_q[b + 1];
+    const int lk = a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
+    const int P = a.cache_offsets[b];
+    const long long n = (long long)q_end - q_start;
+    const bool ok = q_start >= 0 && n >= 0 && (long long)q_end <= a.total_q && P >= 0 &&
+                    (long long)lk == (long long)P + n && (long long)P + n <= a.max_cache_len && (b > 0 || q_start == 0);
+    return ok ? SeqInfo{q_start, (int)n, P, 0} : SeqInfo{0, -1, 0, 0};
+}
+
+// ---- batches of up to kFewSeqs sequences (the shared prefix among them) ----
+//
+// The counting sort of the general schedulers costs a one-CTA kernel most of its
+// time (its passes run 32 warps through ~2000 instructions each; measured 8 us
+// for one sequence and 19 us for 64 paged ones, against 4 and 6 us here).  A few
+// sequences are ranked by comparing each with every other instead, one thread
+// per sequence, in shared memory.
+constexpr int kFewSeqs = 256;
+constexpr int kFewThreads = 512;
+
+struct FewSeqs {
+    SeqInfo seqs[kFewSeqs];  // pad: index of the sequence's first block
+    float cost[kFewSeqs];
+    int blocks[kFewSeqs];    // schedulable blocks per head
+    int units[kFewSeqs];     // units per head (0: none)
+    int first[kFewSeqs];     // its first unit in the list
+    int group[kFewSeqs];     // KV heads that run together
+    int spans[kFewSeqs][2];  // table entries [0, x) and [y, end) to check: x, y
+    int max_chunks;
+    unsigned long long total;
+};
+
+// Loads and checks the sequences (and the prefix's table); f.seqs[b].n is 0 for a
+// rejected one.  Ends with a barrier.  Returns whether the prefix is usable.
+__device__ __forceinline__ bool load_few(const ScheduleArgs& a, FewSeqs& f, int sinks, const int32_t* prefix_table,
+                                         int prefix_len) {
+    constexpr int kChunk = 16;  // table entries of a thread in flight
+    const int tid = threadIdx.x;
+    bool bad = false, prefix_ok = true;
+    if (tid == 0) f.max_chunks = 0, f.total = 0;
+    if (a.block_table) {
+        __syncthreads();
+        if (tid < a.num_seqs) {
+            const SeqInfo si = checked_sequence(a, tid);
+            f.seqs[tid] = si;
+            int x = 0, y = 0, end = 0;
+            if (si.n > 0) {
+                const StreamGeo g = stream_geo(si.n, si.P, 0, si.n, a.causal, a.window, sinks, false, true);
+                x = (min(g.nsink * kBlockN, si.P) + a.block_size - 1) / a.block_size;
+                y = (g.lo < prefix_tiles(si.P) ? g.lo * kBlockN : si.P) / a.block_size;
+                end = (si.P + si.n - 1) / a.block_size + 1;
+            }
+            x = min(x, y);  // the two ranges as one: entry i stands for i < x ? i : i - x + y
+            f.spans[tid][0] = x;
+            f.spans[tid][1] = y;
+            f.blocks[tid] = end - y + x;  // entries to check
+            atomicMax(&f.max_chunks, (end - y + x + kChunk - 1) / kChunk);
+        }
+        __syncthreads();
+        const int chunks = f.max_chunks;
+        for (int w = tid; w < a.num_seqs * chunks; w += kFewThreads) {
+            const int b = w / chunks, i0 = w % chunks * kChunk;
+            const int n = f.blocks[b], x = f.spans[b][0], shift = f.spans[b][1] - x;
+            const int32_t* row = a.block_table + (size_t)b * a.max_blocks;
+            int blk[kChunk];
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i) blk[i] = i0 + i < n ? __ldg(row + i0 + i + (i0 + i < x ? 0 : shift)) : 0;
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+                if ((unsigned)blk[i] >= (unsigned)a.num_blocks) f.seqs[b].n = -1;  // (several threads, one value)
+        }
+        if (prefix_len > 0) {
+            const int nb = (prefix_len + a.block_size - 1) / a.block_size;
+#pragma unroll 8
+            for (int i = tid; i < nb; i += kFewThreads) bad |= (unsigned)__ldg(prefix_table + i) >= (unsigned)a.num_blocks;
+        }
+        prefix_ok = !__syncthreads_or(bad);
+    }
+    if (tid < a.num_seqs) {
+        SeqInfo si = a.block_table ? f.seqs[tid] : checked_sequence(a, tid);
+        if (si.n < 0 || !prefix_ok) {
+            atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
+            si = SeqInfo{0, 0, 0, 0};
+        }
+        f.seqs[tid] = si;
+    } else if (tid == a.num_seqs && prefix_len > 0) {
+        const int end = a.cu_seqlens_q[a.num_seqs];
+        const int n = !prefix_ok || end < 0 ? 0 : (end < a.total_q ? end : a.total_q);
+        f.seqs[tid] = SeqInfo{0, n, prefix_len, 0};
+    }
+    __syncthreads();
+    return prefix_ok;
+}
+
+// From f.cost, f.blocks and f.units: each sequence's place in the list (by
+// descending cost, then index), the first-block numbers, and the header.
+// Returns the blocks of all sequences.  Ends with a barrier.
+__device__ __forceinline__ int rank_few(const ScheduleArgs& a, FewSeqs& f, int nseq) {
+    const int tid = threadIdx.x;
+    if (tid < nseq) {
+        const float mine = f.cost[tid];
+        int first = 0, pad = 0, total = 0;
+#pragma unroll 8
+        for (int b = 0; b < nseq; ++b) {
+            const float c = f.cost[b];
+            const int u = f.units[b], n = f.blocks[b];
+            first += c > mine || (c == mine && b < tid) ? u : 0;
+            pad += b < tid ? n : 0;
+            total += u;
+        }
+        f.first[tid] = first * a.n_kv_heads;
+        f.seqs[tid].pad = pad;
+        a.seqs[tid] = f.seqs[tid];
+        if (tid == nseq - 1) {
+            f.max_chunks = pad + f.blocks[tid];
+            total *= a.n_kv_heads;
+            a.hdr->num_units = total < a.max_units ? total : a.max_units;
+            a.hdr->counter = 0;
+            a.hdr->max_units = a.max_units;
+            if (total > a.max_units) atomicOr(&a.hdr->error, PA_DEVERR_OVERFLOW);
+        }
+    }
+    __syncthreads();
+    return f.max_chunks;
 }
 
 }  // namespace pa

@@ -25,6 +25,28 @@ namespace pa {
 
 namespace {
 
+// Writes the units of query block blk of sequence b and KV head kvh: the block's
+// c tiles in its sequence's p pieces.
+__device__ __forceinline__ void emit_block(const LongScheduleArgs& a, const SeqInfo& si, int b, int blk, int kvh,
+                                           int nblk, int hg, int p, int first, int tpu, int c) {
+    const bool pre = b == a.num_seqs, partial = a.prefix_len > 0 || p > 1;
+    const int g0 = kvh - kvh % hg, gsize = min(hg, a.n_kv_heads - g0);
+    const int pos = first + (g0 * nblk + (nblk - 1 - blk) * gsize + (kvh - g0)) * p;
+    const int pb = min(p, c);  // pieces of this block
+    for (int k = 0, s0 = 0; k < p && pos + k < a.max_units; ++k) {
+        // c < 2^24 tiles and k <= 32 pieces: the product fits 32 bits
+        const int s1 = k < pb ? (int)((unsigned)c * (unsigned)(k + 1) / (unsigned)pb) : s0;
+        UnitX x;
+        x.u = Unit{b, kvh, blk * tpu, s1 - s0};
+        x.s0 = s0;
+        x.slab = partial ? (pre ? a.max_pieces : 0) + k : -1;
+        a.xunits[pos + k] = x;
+        s0 = s1;
+    }
+    if (a.tok_pieces && partial && !pre && kvh == 0)
+        for (int t = blk * tpu; t < min(si.n, (blk + 1) * tpu); ++t) a.tok_pieces[si.q_start + t] = pb;
+}
+
 __global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_constant__ LongScheduleArgs a) {
     __shared__ int hist[kCostBins];
     __shared__ int warp_sums[32];
@@ -46,48 +68,36 @@ __global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_
     for (int i = tid; i < kCostBins; i += nthr) hist[i] = 0;
     if (tid == 0) s_total = 0;
 
-    // every block that a sequence (or the prefix) touches must be one of the pool's
+    // Pass 1: sanitise each sequence (its metadata, then its table's blocks; a
+    // bad block of the prefix rejects them all); number its query blocks.
     const bool paged = a.block_table != nullptr;
+    for (int b = tid; b < a.num_seqs; b += nthr) seqs[b] = checked_sequence(a, b);
     bool bad_prefix = false;
     if (paged) {
+        __threadfence_block();
+        __syncthreads();
         for (int b = warp; b < a.num_seqs; b += nwarps) {
-            const long long lk = (long long)a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
-            const long long used = lk > 0 ? (lk + a.block_size - 1) / a.block_size : 0;
-            const int nb = used < a.max_blocks ? (int)used : a.max_blocks;
-            bool bad = false;
-            for (int L = lane; L < nb; L += 32) {
-                const int blk = a.block_table[(size_t)b * a.max_blocks + L];
-                bad |= blk < 0 || blk >= a.num_blocks;
-            }
-            bad = __any_sync(0xffffffffu, bad);
-            if (lane == 0) seqs[b].pad = bad ? 1 : 0;
+            const bool bad = bad_visible_blocks(a.block_table + (size_t)b * a.max_blocks, seqs[b], a.block_size,
+                                                a.num_blocks, a.causal, a.window, a.sinks, lane);
+            if (bad && lane == 0) seqs[b].n = -1;
         }
         if (shared_prefix) {
-            const int nb = (a.prefix_len + a.block_size - 1) / a.block_size;
-            for (int L = tid; L < nb; L += nthr) bad_prefix |= a.prefix_table[L] < 0 || a.prefix_table[L] >= a.num_blocks;
+            const int nb = (a.prefix_len + a.block_size - 1) / a.block_size, part = (nb + nwarps - 1) / nwarps;
+            bad_prefix = bad_blocks(a.prefix_table, warp * part, min(nb, (warp + 1) * part), a.num_blocks, lane);
         }
         __threadfence_block();
         bad_prefix = __syncthreads_or(bad_prefix);
     }
-
-    // Pass 1: sanitise each sequence; number its query blocks.
     int blocks_before = 0;
     for (int b0 = 0; b0 < nseq; b0 += nthr) {
         const int b = b0 + tid;
         SeqInfo si{0, 0, 0, 0};
         if (b < a.num_seqs) {
-            const int q_start = a.cu_seqlens_q[b];
-            const int q_end = a.cu_seqlens_q[b + 1];
-            const int lk = a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
-            const int P = a.cache_offsets[b];
-            const long long n = (long long)q_end - q_start;
-            const bool ok = q_start >= 0 && n >= 0 && (long long)q_end <= a.total_q && P >= 0 &&
-                            (long long)lk == (long long)P + n && (long long)P + n <= a.max_cache_len &&
-                            (b > 0 || q_start == 0) && !(paged && seqs[b].pad != 0) && !bad_prefix;
-            if (!ok) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
-            si.q_start = ok ? q_start : 0;
-            si.n = ok ? (int)n : 0;
-            si.P = ok ? P : 0;
+            si = seqs[b];
+            if (si.n < 0 || bad_prefix) {
+                atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
+                si = SeqInfo{0, 0, 0, 0};
+            }
         } else if (b == a.num_seqs && shared_prefix && !bad_prefix) {
             const int end = a.cu_seqlens_q[a.num_seqs];
             si.n = end < 0 ? 0 : (end < a.total_q ? end : a.total_q);
@@ -191,40 +201,89 @@ __global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_
     for (int w = tid; w < total_units; w += nthr) {
         const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
         const int b = block_owner(seqs, nseq, i);
-        const bool pre = b == a.num_seqs;
         const SeqInfo si = seqs[b];
-        const int blk = i - si.pad;
+        emit_block(a, si, b, i - si.pad, kvh, (si.n + tpu - 1) / tpu, seq_group[b], pieces[b], seq_scratch[b], tpu,
+                   block_tiles(si, i - si.pad, b == a.num_seqs));
+    }
+}
+
+// The same for a few sequences (kFewSeqs): see schedule.cuh.
+__global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(const __grid_constant__ LongScheduleArgs a) {
+    __shared__ FewSeqs f;
+    __shared__ int s_max[kFewSeqs], s_tiles[kFewSeqs], s_pieces[kFewSeqs];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tpu = a.unit_slots * (kBlockM / a.group);
+    const bool shared_prefix = a.prefix_len > 0, paged = a.block_table != nullptr;
+    const int nseq = a.num_seqs + (shared_prefix ? 1 : 0);
+    griddep_launch();
+    if (a.tok_pieces)
+        for (int t = tid; t < a.total_q; t += kFewThreads) a.tok_pieces[t] = 0;
+    load_few(a, f, a.sinks, a.prefix_table, a.prefix_len);
+    auto block_tiles = [&](const SeqInfo& si, int blk, bool pre) {
+        const int q0 = blk * tpu, qe = q0 + tpu < si.n ? q0 + tpu : si.n;
+        const StreamGeo g = stream_geo(si.n, si.P, q0, qe, a.causal, a.window, a.sinks, pre, paged);
+        return g.nsink + g.hi - g.lo;
+    };
+    // tiles per head and longest block: by one thread, or by a warp where there are many blocks
+    constexpr int kThreadBlocks = 4;
+    if (tid < nseq) {
+        const SeqInfo si = f.seqs[tid];
         const int nblk = (si.n + tpu - 1) / tpu;
-        const int hg = seq_group[b];
-        const int g0 = kvh - kvh % hg;
-        const int gsize = min(hg, a.n_kv_heads - g0);
-        const int p = pieces[b];
-        const int pos = seq_scratch[b] + (g0 * nblk + (nblk - 1 - blk) * gsize + (kvh - g0)) * p;
-        const int c = block_tiles(si, blk, pre);
-        const int pb = min(p, c);  // pieces of this block
-        const bool partial = shared_prefix || p > 1;
-        for (int k = 0; k < p; ++k) {
-            if (pos + k >= a.max_units) break;
-            UnitX x;
-            x.u.b = b;
-            x.u.kvh = kvh;
-            x.u.q0 = blk * tpu;
-            x.s0 = k < pb ? (int)((long long)c * k / pb) : 0;
-            x.u.ntiles = k < pb ? (int)((long long)c * (k + 1) / pb) - x.s0 : 0;
-            x.slab = partial ? (pre ? a.max_pieces : 0) + k : -1;
-            a.xunits[pos + k] = x;
+        f.blocks[tid] = nblk;
+        if (nblk <= kThreadBlocks) {
+            int c = 0, mx = 0;
+            for (int i = 0; i < nblk; ++i) {
+                const int t = block_tiles(si, i, tid == a.num_seqs);
+                c += t;
+                mx = max(mx, t);
+            }
+            s_tiles[tid] = c;
+            s_max[tid] = mx;
+            if (c > 0) atomicAdd(&f.total, (unsigned long long)c * a.n_kv_heads);
         }
     }
-    if (!a.tok_pieces) return;
-    const int span = min(tpu, a.total_q);  // tokens of a block
-    for (int w = tid; w < total_blocks * span; w += nthr) {
-        const int i = w / span, off = w % span;
-        const int b = block_owner(seqs, nseq, i);
-        const SeqInfo si = seqs[b];
-        const int blk = i - si.pad, tok = blk * tpu + off;
-        if (b == a.num_seqs || tok >= si.n) continue;
-        const int p = pieces[b];
-        if (shared_prefix || p > 1) a.tok_pieces[si.q_start + tok] = min(p, block_tiles(si, blk, false));
+    __syncthreads();
+    for (int b = warp; b < nseq; b += kFewThreads / 32) {
+        const int nblk = f.blocks[b];
+        if (nblk <= kThreadBlocks) continue;
+        const SeqInfo si = f.seqs[b];
+        int c = 0, mx = 0;
+        for (int i = lane; i < nblk; i += 32) {
+            const int t = block_tiles(si, i, b == a.num_seqs);
+            c += t;
+            mx = max(mx, t);
+        }
+        for (int o = 16; o > 0; o >>= 1) {
+            c += __shfl_xor_sync(0xffffffffu, c, o);
+            mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        }
+        if (lane == 0) {
+            s_tiles[b] = c;
+            s_max[b] = mx;
+            atomicAdd(&f.total, (unsigned long long)c * a.n_kv_heads);
+        }
+    }
+    __syncthreads();
+    if (tid < nseq) {
+        const unsigned long long per = (f.total + a.target_units - 1) / (unsigned)a.target_units;
+        const int piece = max(a.min_tiles, (int)(per < 0x7fffffffull ? per : 0x7fffffffull));
+        const int c = s_tiles[tid], mx = s_max[tid];
+        int p = (mx + piece - 1) / piece;
+        p = max(1, min(p, tid == a.num_seqs ? a.max_prefix_pieces : a.max_pieces));
+        s_pieces[tid] = p;
+        a.seq_pieces[tid] = p;
+        f.units[tid] = f.blocks[tid] * p;
+        f.cost[tid] = (float)c / (float)p;
+        f.group[tid] =
+            kv_head_group(f.seqs[tid], a.head_dim, a.n_kv_heads, a.num_ctas, (long long)c, (mx + p - 1) / p);
+    }
+    __syncthreads();
+    const int total_blocks = rank_few(a, f, nseq);
+    for (int w = tid; w < total_blocks * a.n_kv_heads; w += kFewThreads) {
+        const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
+        const int b = block_owner(f.seqs, nseq, i);
+        emit_block(a, f.seqs[b], b, i - f.seqs[b].pad, kvh, f.blocks[b], f.group[b], s_pieces[b], f.first[b], tpu,
+                   block_tiles(f.seqs[b], i - f.seqs[b].pad, b == a.num_seqs));
     }
 }
 
@@ -269,7 +328,10 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Merg
 }  // namespace
 
 cudaError_t launch_build_long_schedule(const LongScheduleArgs& a, cudaStream_t stream) {
-    build_long_schedule_kernel<<<1, 1024, 0, stream>>>(a);
+    if (a.num_seqs + (a.prefix_len > 0 ? 1 : 0) <= kFewSeqs)
+        build_long_schedule_few_kernel<<<1, kFewThreads, 0, stream>>>(a);
+    else
+        build_long_schedule_kernel<<<1, 1024, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

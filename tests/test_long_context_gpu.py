@@ -450,3 +450,41 @@ def test_prefill_weigh_evict_decode(block):
             tol = R.BF16 * (mag + ref.abs()) + R.SCORE * mag + 1e-6
             assert ((got[b, h] - ref).abs() <= tol).all()
     ok()
+
+
+def test_sinks_blocks_between_sinks_and_window_may_be_gone():
+    """A streaming server gives back the blocks that no query sees: their table entries may hold anything."""
+    c = Call(52, [1, 3], [1000, 700], 64, 2, 2, 16)
+    # window 100 over 1000: tiles from position 896 on; over 700 (oldest query at 700): from 512 on
+    c.opts["block_table"][0, 8:56] = -1
+    c.opts["block_table"][1, 8:32] = 10 ** 6
+    c.sinks(100, 4)
+    c.check(window=100, sinks=4)
+    ok()
+    lse = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale, window=100, sinks=4)[1].float()
+    weigh(c, lse, window=100, sinks=4)
+    ok()
+
+
+@pytest.mark.parametrize("block", [0, 16])
+@pytest.mark.parametrize("seqs", [256, 257, 1300])
+def test_many_sequences(seqs, block):
+    """Both sides of the batch size up to which a few sequences are ranked directly (256, the prefix counted)."""
+    new = [(i * 7) % 3 for i in range(seqs)]
+    lens = [(i * 37) % 150 for i in range(seqs)]
+    c = Call(110, new, lens, 32, 1, 2, block)
+    c.sinks(40, 3)
+    c.check(window=40, sinks=3)
+    weigh(c)
+    c = Call(111, new, lens, 32, 1, 2, block, prefix=70)
+    c.prefix()
+    c.check()
+    ok()
+
+
+def test_many_sequences_with_a_bad_block():
+    c = Call(112, [1] * 300, [(i * 11) % 60 for i in range(300)], 32, 1, 1, 16)
+    c.opts["block_table"][299, 0] = -1
+    c.sinks(40, 3)
+    c.check(skipped=[299], window=40, sinks=3)
+    assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
