@@ -13,19 +13,29 @@
 // holds no key of the sequence (before its first key, past its last one, stale
 // rows of a cache block) only ever affects its own lane, which is not written.
 //
-// One persistent CTA per SM, 384 threads:
-//   warp 0          fetches units, loads K tiles into a ring of four;
-//   warp 1          tcgen05 issuer: per Q tile, S^T of both slots (two key tiles
-//                   share every Q tile), two TMEM buffers per slot;
-//   warp 2          loads Q tiles (rows = (token, head in group)) into a ring;
-//   warp 3          stages -lse * log2(e) of the Q tile's rows;
-//   warps 4-7, 8-11 slot 0 and slot 1: sum of exp2 over the columns, one key per
-//                   thread; an int8 key tile is first expanded by its slot's
-//                   warps (exact codes; the row scale multiplies the scores).
-// A unit is a pair of key tiles against every Q tile that sees one of them; for
-// a sequence whose queries fit one Q tile (decode rows) it is a longer run of
-// key tiles, and the Q tile is loaded once.  Every wait is bounded in time, as
-// in the attention kernel.
+// One persistent CTA per SM, 640 threads:
+//   warp 0      fetches units, loads their K and Q tiles (rows = (token, head in
+//               group)) into one ring of stages;
+//   warps 1, 2  tcgen05 issuers (one's waits hide behind the other's MMAs);
+//   warp 3      stages -lse * log2(e) of the Q tile's rows;
+//   warps 4-19  four groups of four warps, an S buffer of 128 TMEM columns each:
+//               the sums of exp2 over the columns, one key per thread.
+//
+// A wide unit is up to four key tiles against every Q tile that sees one of them:
+// each Q tile brought into shared memory then feeds four MMAs (loading it for two
+// key tiles at a time, the Q tiles alone -- with neither MMAs nor exponentials --
+// took 164 of 270 us on an 8192-token prompt of 32 heads).  With four tiles, each
+// group has a tile of its own; with one or two, two groups take a tile's Q tiles
+// in turn and add their sums at the end.  Where four-tile units would leave SMs
+// idle the scheduler cuts units of two.
+//
+// A sequence whose queries fit one Q tile (decode rows) has units that are longer
+// runs of key tiles against that one Q tile, the tiles in turn to the groups; what
+// bounds them is HBM.
+//
+// An int8 key tile is expanded in place by its group first (exact codes; the row
+// scale multiplies the scores).  Every wait is bounded in time, as in the
+// attention kernel.
 #include <cuda_bf16.h>
 
 #include <climits>
@@ -43,8 +53,10 @@ using namespace ptx;
 namespace {
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
-constexpr int kThreads = 384;
+constexpr int kThreads = 640;
+constexpr int kLse = 3;      // Q tiles whose lse is staged
 constexpr int kMaxRun = 8;   // key tiles of a unit of a one-Q-tile sequence, at most
+constexpr int kGroups = 4;   // groups of sum warps = S buffers = key tiles of a wide unit, at most
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D>
@@ -57,8 +69,7 @@ struct Cfg {
     static constexpr SmemSwizzle kSw = D >= 64 ? kSwizzle128B : kSwizzle64B;
     static constexpr int kSbo = 8 * kRowBytes;
     static constexpr int kGrpSbo = kChunks * kSbo;  // paged, two chunks: staged block by block
-    static constexpr int kStagesK = 4;
-    static constexpr int kStagesQ = D == 128 ? 3 : 4;
+    static constexpr int kStages = 7;
 };
 
 struct UnitSlot {
@@ -67,21 +78,49 @@ struct UnitSlot {
 };
 
 struct __align__(16) Ctrl {
-    uint64_t k_full[4], k_empty[4], k_conv[4];
-    uint64_t q_full[4], q_empty[4], l_full[4], l_empty[4];
-    uint64_t s_full[2][2], s_empty[2][2];
+    uint64_t full[7], empty[7];  // per ring stage
+    uint64_t l_full[kLse], l_empty[kLse];
+    uint64_t s_full[kGroups], s_empty[kGroups];  // S buffers
+    uint64_t read[kGroups], conv[kGroups];       // int8 key tile of a group: codes read, tile expanded
+    uint64_t pair_full[2], pair_empty[2];        // two groups on one tile: the second one's sums
     uint64_t mma_drain;
     uint64_t unit_full[2], unit_empty[2];
     UnitSlot slot[2];
     uint32_t tmem_base;
     int abort;
-    alignas(16) float neg_lse[4][128];  // -lse * log2(e) of the Q tile's rows
+    alignas(16) float neg_lse[kLse][128];  // -lse * log2(e) of the Q tile's rows
+    float pair[2][128];                    // two groups on one tile: the second one's sums
+};
+
+// The ring's stages in the order every role takes them: next() skips the stages
+// of the resident tiles (the last unit's too while this unit's are chosen, if
+// that leaves one).
+struct Ring {
+    int n, st = -1;
+    uint32_t held = 0, before = 0, phase = 0;
+    __device__ __forceinline__ explicit Ring(int stages) : n(stages) {}
+    __device__ __forceinline__ void unit() {
+        before = held;
+        held = 0;
+    }
+    // The next tile's stage; `parity` of its use.
+    __device__ __forceinline__ int next(bool resident, uint32_t& parity) {
+        const uint32_t both = held | before;
+        const uint32_t skip = resident && both != (1u << n) - 1 ? both : held;
+        do {
+            st = st + 1 == n ? 0 : st + 1;
+        } while ((skip >> st) & 1);
+        if (resident) held |= 1u << st;
+        parity = (phase >> st) & 1;
+        phase ^= 1u << st;
+        return st;
+    }
 };
 
 template <int D>
 constexpr int smem_bytes() {
     using C = Cfg<D>;
-    constexpr int n = C::kTileBytes * (C::kStagesK + C::kStagesQ) + (int)sizeof(Ctrl);
+    constexpr int n = C::kTileBytes * C::kStages + (int)sizeof(Ctrl);
     return n > 120 * 1024 ? n : 120 * 1024;  // one CTA per SM: it holds all 512 TMEM columns
 }
 
@@ -123,8 +162,17 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// Barrier of one slot's four warps.
-__device__ __forceinline__ void slot_sync(int slot) { asm volatile("bar.sync %0, 128;" ::"r"(slot + 1) : "memory"); }
+// Four int8 codes (a word) as two words of bf16 pairs, exactly: code + 128 is
+// the low mantissa byte of 2^23 + (code + 128).
+__device__ __forceinline__ void expand4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+    const uint32_t x = codes ^ 0x80808080u;
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = __uint_as_float(__byte_perm(x, 0x4B000000u, 0x7540u + e)) - 8388736.0f;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    lo = *reinterpret_cast<const uint32_t*>(&a);
+    hi = *reinterpret_cast<const uint32_t*>(&b);
+}
 
 // The key tiles a sequence's new queries see: stream positions [0, tiles), and
 // the Q tiles of its queries.
@@ -171,21 +219,27 @@ __device__ __forceinline__ bool tile_seen(const KeyTile& k, int P, int qs, int q
     return window == 0 || P + qs - (k.hi - 1) < window || k.lo < sinks;
 }
 
-// Q tiles [lo, hi) that see a tile of the pair (k1.hi == 0: a pair of one).
+// Q tiles [lo, hi) that see one of the key tiles first .. last of a unit.
 struct QRange {
     int lo, hi;
 };
 
-__device__ __forceinline__ QRange pair_queries(const KeyTile& k0, const KeyTile& k1, bool two, const SeqInfo& s, int nq,
+__device__ __forceinline__ QRange unit_queries(const KeyTile& first, const KeyTile& last, const SeqInfo& s, int nq,
                                                int tps, int causal, int window, int sinks) {
     QRange r{0, nq};
     if (!causal) return r;
-    if (k0.lo > s.P) r.lo = (k0.lo - s.P) / tps;
-    if (window > 0 && k0.lo >= sinks) {
-        const int last = window + (two ? k1.hi : k0.hi) - 2 - s.P;  // last token that sees the pair's last key
-        r.hi = last < 0 ? 0 : min(nq, last / tps + 1);
+    if (first.lo > s.P) r.lo = (first.lo - s.P) / tps;
+    if (window > 0 && first.lo >= sinks) {
+        const int tok = window + last.hi - 2 - s.P;  // last token that sees the last key
+        r.hi = tok < 0 ? 0 : min(nq, tok / tps + 1);
     }
     return r;
+}
+
+// Key tiles of a unit of several Q tiles: four, or two where four would make fewer
+// units than two per CTA (wide_tiles: the key tiles x KV heads of such sequences).
+__device__ __forceinline__ int wide_length(unsigned long long wide_tiles, int num_ctas) {
+    return wide_tiles >= 2ull * kGroups * (unsigned)num_ctas ? kGroups : 2;
 }
 
 // Key tiles of a unit of a sequence whose queries fit one Q tile: about eight
@@ -201,9 +255,12 @@ __device__ __forceinline__ int run_length(unsigned long long total, int num_ctas
 // ones) with the group's heads adjacent.
 __device__ __forceinline__ void emit_keys(const KeyScheduleArgs& a, const SeqInfo& si, int b, int x, int kvh, int tiles,
                                           int len, int units, int first) {
+    // groups of one size, and none so small that its longest unit outlasts the
+    // rest of it (a causal sequence's units average half its longest)
     const float head_bytes = (float)si.n * a.group * a.head_dim * 2;
-    const float fit = floorf((float)kL2GroupBytes / fmaxf(head_bytes, 1.f));
-    const int hg = fit >= (float)a.n_kv_heads ? a.n_kv_heads : (fit < 1.f ? 1 : (int)fit);
+    const float fit = fmaxf(floorf((float)kL2GroupBytes / fmaxf(head_bytes, 1.f)), 2.f * (float)a.num_ctas / (float)units);
+    const int groups = fit >= (float)a.n_kv_heads ? 1 : (a.n_kv_heads + (int)fit - 1) / max(1, (int)fit);
+    const int hg = (a.n_kv_heads + groups - 1) / groups;
     const int g0 = kvh - kvh % hg, gsize = min(hg, a.n_kv_heads - g0);
     const int pos = first + g0 * units + x * gsize + (kvh - g0);
     if (pos < a.max_units) a.units[pos] = Unit{b, kvh, x * len, min(len, tiles - x * len)};
@@ -212,7 +269,7 @@ __device__ __forceinline__ void emit_keys(const KeyScheduleArgs& a, const SeqInf
 __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_constant__ KeyScheduleArgs a) {
     __shared__ int hist[kCostBins];
     __shared__ int warp_sums[32];
-    __shared__ unsigned long long s_total;
+    __shared__ unsigned long long s_total, s_wide;
     __shared__ SeqInfo s_seqs[kSmemSeqs];
     __shared__ int s_first[kSmemSeqs], s_units[kSmemSeqs];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -224,7 +281,7 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
     int* const seq_first = small ? s_first : a.seq_scratch;  // cost bin, then first unit of the sequence
     int* const seq_units = small ? s_units : a.seq_group;    // units per head
     for (int i = tid; i < kCostBins; i += nthr) hist[i] = 0;
-    if (tid == 0) s_total = 0;
+    if (tid == 0) s_total = s_wide = 0;
     const bool paged = a.block_table != nullptr;
     for (int b = tid; b < a.num_seqs; b += nthr) seqs[b] = checked_sequence(a, b);
     __threadfence_block();
@@ -247,12 +304,12 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
         }
         if (si.n > 0) {
             const SeqGeo g = seq_geo(si, tps, a.causal, a.window, a.sinks, paged);
-            if (g.nq == 1) atomicAdd(&s_total, (unsigned long long)g.tiles * a.n_kv_heads);
+            atomicAdd(g.nq == 1 ? &s_total : &s_wide, (unsigned long long)g.tiles * a.n_kv_heads);
         }
     }
     __threadfence_block();
     __syncthreads();
-    const int run = run_length(s_total, a.num_ctas);
+    const int run = run_length(s_total, a.num_ctas), wide = wide_length(s_wide, a.num_ctas);
     // units per sequence and head, numbered (SeqInfo::pad), and cost bins
     int before = 0;
     for (int b0 = 0; b0 < a.num_seqs; b0 += nthr) {
@@ -263,7 +320,7 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
         if (b < a.num_seqs) si = seqs[b];
         if (si.n > 0) {
             g = seq_geo(si, tps, a.causal, a.window, a.sinks, paged);
-            const int len = g.nq == 1 ? run : 2;
+            const int len = g.nq == 1 ? run : wide;
             units = (g.tiles + len - 1) / len;
         }
         int chunk_total;
@@ -306,7 +363,7 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
         const int b = block_owner(seqs, a.num_seqs, i);
         const SeqInfo si = seqs[b];
         const SeqGeo g = seq_geo(si, tps, a.causal, a.window, a.sinks, paged);
-        emit_keys(a, si, b, i - si.pad, kvh, g.tiles, g.nq == 1 ? run : 2, seq_units[b], seq_first[b]);
+        emit_keys(a, si, b, i - si.pad, kvh, g.tiles, g.nq == 1 ? run : wide, seq_units[b], seq_first[b]);
     }
 }
 
@@ -314,18 +371,20 @@ __global__ void __launch_bounds__(1024) build_key_schedule_kernel(const __grid_c
 __global__ void __launch_bounds__(kFewThreads) build_key_schedule_few_kernel(const __grid_constant__ KeyScheduleArgs a) {
     __shared__ FewSeqs f;
     __shared__ int s_tiles[kFewSeqs], s_len[kFewSeqs];
+    __shared__ unsigned long long s_wide;
     const int tid = threadIdx.x, tps = kBlockM / a.group;
     const bool paged = a.block_table != nullptr;
     griddep_launch();
+    if (tid == 0) s_wide = 0;
     load_few(a, f, a.sinks, nullptr, 0);
     SeqGeo g{};
     if (tid < a.num_seqs && f.seqs[tid].n > 0) {
         g = seq_geo(f.seqs[tid], tps, a.causal, a.window, a.sinks, paged);
-        if (g.nq == 1) atomicAdd(&f.total, (unsigned long long)g.tiles * a.n_kv_heads);
+        atomicAdd(g.nq == 1 ? &f.total : &s_wide, (unsigned long long)g.tiles * a.n_kv_heads);
     }
     __syncthreads();
     if (tid < a.num_seqs) {
-        const int len = g.nq == 1 ? run_length(f.total, a.num_ctas) : 2;
+        const int len = g.nq == 1 ? run_length(f.total, a.num_ctas) : wide_length(s_wide, a.num_ctas);
         s_tiles[tid] = g.tiles;
         s_len[tid] = len;
         f.blocks[tid] = f.units[tid] = (g.tiles + len - 1) / len;
@@ -346,32 +405,35 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     constexpr bool kGrp = kPaged && !kQuant && C::kChunks == 2;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const bool misaligned = (smem_u32(smem_raw) & 1023u) != 0;
-    uint8_t* k_smem = smem_raw;
-    uint8_t* q_smem = k_smem + C::kStagesK * C::kTileBytes;
-    Ctrl* ctl = reinterpret_cast<Ctrl*>(q_smem + C::kStagesQ * C::kTileBytes);
+    uint8_t* const ring_smem = smem_raw;
+    Ctrl* ctl = reinterpret_cast<Ctrl*>(ring_smem + C::kStages * C::kTileBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     WorkspaceHeader* hdr = p.hdr;
     const int G = p.group, tps = kBlockM / G;
 
     if (!misaligned && threadIdx.x == 0) {
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&ctl->k_full[i], 1);
-            mbar_init(&ctl->k_empty[i], 1);  // MMA commit
-            mbar_init(&ctl->k_conv[i], 4);   // the slot's four warps
-            mbar_init(&ctl->q_full[i], 1);
-            mbar_init(&ctl->q_empty[i], 1);  // MMA commit
-            mbar_init(&ctl->l_full[i], 1);
-            mbar_init(&ctl->l_empty[i], 8);  // the sum warps
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&ctl->full[i], 1);
+            mbar_init(&ctl->empty[i], 2);  // the issuers: a commit, or an arrival
         }
-        for (int s = 0; s < 2; ++s)
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&ctl->s_full[s][i], 1);
-                mbar_init(&ctl->s_empty[s][i], 4);
-            }
-        mbar_init(&ctl->mma_drain, 1);
+        for (int i = 0; i < kLse; ++i) {
+            mbar_init(&ctl->l_full[i], 1);
+            mbar_init(&ctl->l_empty[i], 16);  // the sum warps
+        }
+        for (int i = 0; i < kGroups; ++i) {
+            mbar_init(&ctl->s_full[i], 1);
+            mbar_init(&ctl->s_empty[i], 4);  // the group's warps
+            mbar_init(&ctl->read[i], 4);
+            mbar_init(&ctl->conv[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl->pair_full[i], 4);
+            mbar_init(&ctl->pair_empty[i], 4);
+        }
+        mbar_init(&ctl->mma_drain, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ctl->unit_full[i], 1);
-            mbar_init(&ctl->unit_empty[i], 11);  // every warp but the fetching one
+            mbar_init(&ctl->unit_empty[i], kThreads / 32 - 1);  // every warp but the fetching one
         }
         ctl->abort = 0;
         fence_mbar_init();
@@ -383,12 +445,6 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
     if (!misaligned && warp == 1) {
         tmem_alloc(&ctl->tmem_base, 512);
         tmem_relinquish();
-    }
-    // Q rows [tps * G, 128) belong to no token and no copy fills them
-    if (!misaligned && tps * G < kBlockM) {
-        for (int i = threadIdx.x; i < C::kStagesQ * C::kTileBytes / 16; i += kThreads)
-            reinterpret_cast<uint4*>(q_smem)[i] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
     }
     griddep_wait();
     if (misaligned) {
@@ -418,20 +474,32 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         if (lane == 0) mbar_arrive(&ctl->unit_empty[sl]);
         return us.u.b >= 0;
     };
+    // The Q tiles of a wide unit.
+    auto queries = [&](const SeqGeo& g, const SeqInfo& s, const Unit& u) {
+        return unit_queries(key_tile_at<kPaged>(g, s, u.q0), key_tile_at<kPaged>(g, s, u.q0 + u.ntiles - 1), s, g.nq, tps,
+                            p.causal, p.window, p.sinks);
+    };
+    auto seen = [&](const KeyTile& k, const SeqInfo& s, int q0, int qe) {
+        return tile_seen(k, s.P, q0, qe, p.causal, p.window, p.sinks);
+    };
     auto geo = [&](const SeqInfo& s) { return seq_geo(s, tps, p.causal, p.window, p.sinks, kPaged); };
 
     if (warp == 0) {
-        // ------------------------------------------------- unit fetch, K tiles
-        uint32_t t = 0, lp_set = 0, lp_par = 0;
-        bool short_units = true;
+        // ---------------------------------------------- unit fetch, K and Q tiles
+        Ring ring(C::kStages);
+        uint32_t lp_set = 0, lp_par = 0;
+        // waits for the next tile's stage to be free
+        auto take = [&](bool resident, int& st) -> bool {
+            uint32_t par;
+            st = ring.next(resident, par);
+            if (!warp_wait(&ctl->empty[st], par ^ 1, ctl, hdr)) return false;
+            lp_set |= 1u << st;
+            lp_par = (lp_par & ~(1u << st)) | (par << st);
+            return true;
+        };
         for (int u_it = 0;; ++u_it) {
             const int sl = u_it & 1;
             if (!warp_wait(&ctl->unit_empty[sl], ((u_it >> 1) & 1) ^ 1, ctl, hdr)) break;
-            // claim late: only when the ring has room for the unit's first tile,
-            // so that the longest-first list still evens out the CTAs at its end
-            // (not for decode rows, whose units are short and alike: there the
-            // claim's latency would show)
-            if (!short_units && !warp_wait(&ctl->k_empty[t % C::kStagesK], ((t / C::kStagesK) & 1) ^ 1, ctl, hdr)) break;
             if (lane == 0) {
                 const int idx = atomicAdd(&hdr->counter, 1);
                 UnitSlot us;
@@ -448,13 +516,25 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             if (u.b < 0) break;
             const SeqInfo s = ctl->slot[sl].s;
             const SeqGeo g = geo(s);
-            short_units = g.nq == 1;
-            bool ok = true;
-            for (int x = u.q0; x < u.q0 + u.ntiles; ++x, ++t) {
+            const bool single = g.nq == 1;
+            ring.unit();
+            auto load_q = [&](int qi) -> bool {
+                // a decode row's Q tile is one token's heads; rows that no copy
+                // fills are columns that no sum takes
+                const bool one = s.n == 1;
+                int st;
+                if (!take(single, st)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(&ctl->full[st], G * (one ? 1 : tps) * C::kRowBytes * C::kChunks);
+                __syncwarp();
+                if (lane < C::kChunks)
+                    tma_load_3d(ring_smem + st * C::kTileBytes + lane * C::kChunkBytes, one ? &p.tm_q1 : &p.tm_q,
+                                &ctl->full[st], lane * C::kChunkCols, u.kvh * G, s.q_start + qi * tps);
+                __syncwarp();
+                return true;
+            };
+            bool ok = !single || load_q(0);
+            for (int x = u.q0; x < u.q0 + u.ntiles && ok; ++x) {
                 const KeyTile k = key_tile_at<kPaged>(g, s, x);
-                const int st = t % C::kStagesK;
-                const uint32_t ph = (t / C::kStagesK) & 1;
-                uint8_t* stage = k_smem + st * C::kTileBytes;
                 const bool pre = k.jt < g.np;
                 // paged prefix tile: this lane's block, fetched before the wait
                 const int br = p.box_rows;
@@ -462,136 +542,164 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
                 int blk = 0;
                 if (kPaged && lane < boxes)
                     blk = __ldg(p.block_table + (size_t)u.b * p.max_blocks + ((k.kb + lane * br) >> p.block_log2));
-                if (!warp_wait(&ctl->k_empty[st], ph ^ 1, ctl, hdr)) {
+                int st;
+                if (!take(!single, st)) {
                     ok = false;
                     break;
                 }
+                uint8_t* stage = ring_smem + st * C::kTileBytes;
+                uint64_t* full = &ctl->full[st];
                 uint32_t bytes = C::kTileBytes;
                 if (pre && kPaged) bytes = boxes * br * (kQuant ? D : C::kRowBytes * C::kChunks);
                 else if (pre && kQuant) bytes = kBlockN * D;
-                if (lane == 0) mbar_arrive_expect_tx(&ctl->k_full[st], bytes);
+                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
                 if (!pre) {
                     if (lane < C::kChunks)
-                        tma_load_3d(stage + lane * C::kChunkBytes, &p.tm_k, &ctl->k_full[st], lane * C::kChunkCols, u.kvh,
+                        tma_load_3d(stage + lane * C::kChunkBytes, &p.tm_k, full, lane * C::kChunkCols, u.kvh,
                                     s.q_start + k.kb - s.P);
                 } else if (kPaged) {
                     if (lane < boxes) {
                         const int row = (k.kb + lane * br) & ((1 << p.block_log2) - 1), z = blk * p.n_kv_heads + u.kvh;
                         if constexpr (kQuant) {
-                            tma_load_3d(stage + C::kTileBytes / 2 + lane * br * D, &p.tm_ck, &ctl->k_full[st], 0, row, z);
+                            tma_load_3d(stage + C::kTileBytes / 2 + lane * br * D, &p.tm_ck, full, 0, row, z);
                         } else if constexpr (kGrp) {
-                            tma_load_5d(stage + lane * br * C::kRowBytes * C::kChunks, &p.tm_ck, &ctl->k_full[st], 0, 0, 0,
-                                        row >> 3, z);
+                            tma_load_5d(stage + lane * br * C::kRowBytes * C::kChunks, &p.tm_ck, full, 0, 0, 0, row >> 3, z);
                         } else {
-                            tma_load_3d(stage + lane * br * C::kRowBytes, &p.tm_ck, &ctl->k_full[st], 0, row, z);
+                            tma_load_3d(stage + lane * br * C::kRowBytes, &p.tm_ck, full, 0, row, z);
                         }
                     }
                 } else {
                     const int z = u.b * p.n_kv_heads + u.kvh;
                     if constexpr (kQuant) {
-                        if (lane == 0) tma_load_3d(stage + C::kTileBytes / 2, &p.tm_ck, &ctl->k_full[st], 0, k.kb, z);
+                        if (lane == 0) tma_load_3d(stage + C::kTileBytes / 2, &p.tm_ck, full, 0, k.kb, z);
                     } else if (lane < C::kChunks) {
-                        tma_load_3d(stage + lane * C::kChunkBytes, &p.tm_ck, &ctl->k_full[st], lane * C::kChunkCols, k.kb, z);
+                        tma_load_3d(stage + lane * C::kChunkBytes, &p.tm_ck, full, lane * C::kChunkCols, k.kb, z);
                     }
                 }
                 __syncwarp();
-                lp_set |= 1u << st;
-                lp_par = (lp_par & ~(1u << st)) | (ph << st);
+            }
+            if (ok && !single) {
+                const QRange qr = queries(g, s, u);
+                for (int qi = qr.lo; qi < qr.hi && ok; ++qi) ok = load_q(qi);
             }
             if (!ok) break;
         }
-        if (lane == 0 && aborted(ctl)) drain(ctl->k_full, lp_set, lp_par, C::kStagesK);
-    } else if (warp == 1) {
-        // ---------------------------------------------------------- MMA issuer
+        if (lane == 0 && aborted(ctl)) drain(ctl->full, lp_set, lp_par, C::kStages);
+    } else if (warp == 1 || warp == 2) {
+        // --------------------------------------------------------- MMA issuers
+        // Issuer me serves the S buffers me and me + 2.  Each stage's release takes
+        // both: a commit by the one whose MMAs read it (both for a Q tile), an
+        // arrival by the other -- which waits for the tile all the same, lest it
+        // arrive for the stage's next use in this one's place.
+        const int me = warp - 1;
         const bool leader = elect_one();
-        const uint32_t k_addr = smem_u32(k_smem), q_addr = smem_u32(q_smem);
-        const uint64_t k_desc = smem_desc(k_addr, 16, C::kSbo, C::kSw);
-        const uint64_t k_desc_g = smem_desc(k_addr, 16, C::kGrpSbo, C::kSw);
-        const uint64_t q_desc = smem_desc(q_addr, 16, C::kSbo, C::kSw);
-        uint32_t t = 0, lq = 0;       // K tiles and Q tiles consumed so far
-        uint32_t ns[2] = {0, 0};      // S^T tiles issued per slot
-        uint32_t cpar = 0;            // parity of k_conv per stage
+        const uint32_t addr = smem_u32(ring_smem);
+        const uint64_t desc = smem_desc(addr, 16, C::kSbo, C::kSw);
+        const uint64_t desc_g = smem_desc(addr, 16, C::kGrpSbo, C::kSw);  // staged block by block
+        Ring ring(C::kStages);
+        uint32_t used[2] = {0, 0};   // uses so far of S buffers me, me + 2
+        uint32_t nconv[2] = {0, 0};  // tiles expanded by those groups
+        uint32_t nn = 0;             // tiles of one-Q-tile units so far
         bool ok = true;
+        // S^T of the key tile at stage kst and the Q tile at stage qst into buffer buf
+        auto issue = [&](int buf, int kst, bool grp, int qst, int cols) -> bool {
+            uint32_t& n = used[buf >> 1];
+            if (!warp_wait(&ctl->s_empty[buf], (n & 1) ^ 1, ctl, hdr)) return false;
+            ++n;
+            tc_fence_after();
+            // columns in use, rounded up to what an M = 128 MMA takes
+            const uint32_t idesc = idesc_bf16_f32(kBlockM, 0, 0, 0) | ((uint32_t)((cols + 15) / 16) * 2 << 17);
+            if (leader) {
+                const uint64_t kd = (grp ? desc_g : desc) + ((kst * C::kTileBytes) >> 4);
+                const uint64_t qd = desc + ((qst * C::kTileBytes) >> 4);
+                const uint32_t kcs = grp ? C::kSbo : C::kChunkBytes;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t ch = (kk * 16) / C::kChunkCols, in = ((kk * 16) % C::kChunkCols) * 2;
+                    mma_ss(tmem + buf * 128, kd + ((ch * kcs + in) >> 4), qd + ((ch * C::kChunkBytes + in) >> 4), idesc,
+                           kk > 0 ? 1u : 0u);
+                }
+                mma_commit(&ctl->s_full[buf]);
+            }
+            __syncwarp();
+            return true;
+        };
+        // the key tile of group grp at stage st: landed, and expanded if it was codes
+        auto wait_key = [&](int grp, bool codes, int st, uint32_t par) -> bool {
+            if (!(kQuant && codes)) return warp_wait(&ctl->full[st], par, ctl, hdr);
+            const bool got = warp_wait(&ctl->conv[grp], nconv[grp >> 1] & 1, ctl, hdr);
+            ++nconv[grp >> 1];
+            return got;
+        };
+        auto release = [&](int st, bool mine) {
+            if (leader) {
+                if (mine)
+                    mma_commit(&ctl->empty[st]);
+                else
+                    mbar_arrive(&ctl->empty[st]);
+            }
+            __syncwarp();
+        };
         UnitSlot us;
         for (int u_it = 0; ok && next_unit(u_it, us); ++u_it) {
             const SeqInfo s = us.s;
             const SeqGeo g = geo(s);
-            const bool single = g.nq == 1;
-            if (single && !warp_wait(&ctl->q_full[lq % C::kStagesQ], (lq / C::kStagesQ) & 1, ctl, hdr)) break;
-            for (int x = us.u.q0; x < us.u.q0 + us.u.ntiles && ok; x += 2) {
-                const bool two = x + 1 < us.u.q0 + us.u.ntiles;
-                const KeyTile kt[2] = {key_tile_at<kPaged>(g, s, x), key_tile_at<kPaged>(g, s, two ? x + 1 : x)};
-                const QRange qr = single ? QRange{0, 1}
-                                         : pair_queries(kt[0], kt[1], two, s, g.nq, tps, p.causal, p.window, p.sinks);
-                bool ready[2] = {false, false};
-                auto wait_k = [&](int i) -> bool {
-                    const int st = (t + i) % C::kStagesK;
-                    if (kQuant && kt[i].jt < g.np) {
-                        const bool got = warp_wait(&ctl->k_conv[st], (cpar >> st) & 1, ctl, hdr);
-                        cpar ^= 1u << st;
-                        return got;
-                    }
-                    return warp_wait(&ctl->k_full[st], ((t + i) / C::kStagesK) & 1, ctl, hdr);
-                };
-                for (int qi = qr.lo; qi < qr.hi && ok; ++qi) {
-                    const int qst = lq % C::kStagesQ;
-                    const int q0 = qi * tps, qe = min(q0 + tps, s.n);
-                    if (!single && !warp_wait(&ctl->q_full[qst], (lq / C::kStagesQ) & 1, ctl, hdr)) { ok = false; break; }
-                    // columns in use, rounded up to what an M = 128 MMA takes
-                    const uint32_t n16 = (uint32_t)((qe - q0) * G + 15) / 16;
-                    const uint32_t idesc = (idesc_bf16_f32(kBlockM, 0, 0, 0)) | (n16 * 2 << 17);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (i == 1 && !two) continue;
-                        if (!tile_seen(kt[i], s.P, q0, qe, p.causal, p.window, p.sinks)) continue;
-                        if (!ready[i]) {
-                            if (!wait_k(i)) { ok = false; break; }
-                            ready[i] = true;
-                        }
-                        const int buf = ns[i] & 1;
-                        if (!warp_wait(&ctl->s_empty[i][buf], ((ns[i] >> 1) & 1) ^ 1, ctl, hdr)) { ok = false; break; }
-                        tc_fence_after();
-                        if (leader) {
-                            const uint32_t koff = ((t + i) % C::kStagesK) * C::kTileBytes, qoff = qst * C::kTileBytes;
-                            const bool grp = kGrp && kt[i].jt < g.np;
-                            const uint64_t kd = grp ? k_desc_g : k_desc;
-                            const uint32_t kcs = grp ? C::kSbo : C::kChunkBytes;
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t ch = (kk * 16) / C::kChunkCols, in = ((kk * 16) % C::kChunkCols) * 2;
-                                mma_ss(tmem + (i * 2 + buf) * 128, kd + ((koff + ch * kcs + in) >> 4),
-                                       q_desc + ((qoff + ch * C::kChunkBytes + in) >> 4), idesc, kk > 0 ? 1u : 0u);
-                            }
-                            mma_commit(&ctl->s_full[i][buf]);
-                        }
-                        __syncwarp();
-                        ++ns[i];
-                    }
-                    if (!ok) break;
-                    if (!single) {
-                        if (leader) mma_commit(&ctl->q_empty[qst]);
-                        __syncwarp();
-                        ++lq;
-                    }
+            ring.unit();
+            uint32_t par;
+            if (g.nq == 1) {
+                const int qst = ring.next(true, par);
+                if (!warp_wait(&ctl->full[qst], par, ctl, hdr)) break;
+                for (int x = us.u.q0; x < us.u.q0 + us.u.ntiles && ok; ++x, ++nn) {
+                    const int kst = ring.next(false, par), grp = nn & 3;
+                    const KeyTile k = key_tile_at<kPaged>(g, s, x);
+                    const bool mine = (grp & 1) == me;
+                    ok = mine ? wait_key(grp, k.jt < g.np, kst, par) && issue(grp, kst, kGrp && k.jt < g.np, qst, s.n * G)
+                              : warp_wait(&ctl->full[kst], par, ctl, hdr);
+                    if (ok) release(kst, mine);
                 }
-                if (!ok) break;
-                // a tile no query saw was still loaded (and expanded): take its turn
-                for (int i = 0; i < (two ? 2 : 1) && ok; ++i) {
-                    if (!ready[i]) ok = wait_k(i);
-                    if (ok && leader) mma_commit(&ctl->k_empty[(t + i) % C::kStagesK]);
-                    __syncwarp();
+                if (ok) release(qst, true);
+                continue;
+            }
+            const int nt = us.u.ntiles;
+            const bool four = nt > 2;
+            const QRange qr = queries(g, s, us.u);
+            int kst[kGroups];
+            KeyTile kt[2];  // of this issuer: tiles me and me + 2
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                kst[i] = 0;
+                if (i >= nt) continue;
+                kst[i] = ring.next(true, par);
+                const KeyTile k = key_tile_at<kPaged>(g, s, us.u.q0 + i);
+                if ((i & 1) == me) {
+                    kt[i >> 1] = k;
+                    ok = ok && wait_key(i, k.jt < g.np, kst[i], par);
+                } else {
+                    ok = ok && warp_wait(&ctl->full[kst[i]], par, ctl, hdr);
                 }
-                t += two ? 2 : 1;
+            }
+            for (int qi = qr.lo; qi < qr.hi && ok; ++qi) {
+                const int q0 = qi * tps, qe = min(q0 + tps, s.n);
+                const int qst = ring.next(false, par);
+                if (!warp_wait(&ctl->full[qst], par, ctl, hdr)) { ok = false; break; }
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int t = me + 2 * i;  // tile of the unit
+                    if (t >= nt || !seen(kt[i], s, q0, qe) || !ok) continue;
+                    ok = issue(four ? t : t + 2 * (qi & 1), i ? (me ? kst[3] : kst[2]) : (me ? kst[1] : kst[0]), kGrp && kt[i].jt < g.np, qst,
+                               (qe - q0) * G);
+                    any = true;
+                }
+                if (ok) release(qst, any);
             }
             if (!ok) break;
-            if (single) {
-                if (leader) mma_commit(&ctl->q_empty[lq % C::kStagesQ]);
-                __syncwarp();
-                ++lq;
-            }
+#pragma unroll
+            for (int i = 0; i < kGroups; ++i)
+                if (i < nt) release(kst[i], (i & 1) == me);
         }
-        // every MMA this warp issued has finished before TMEM is released
+        // every MMA the issuers put in has finished before TMEM is released
         if (leader) {
             mma_commit(&ctl->mma_drain);
             const uint64_t t0 = globaltimer_ns();
@@ -599,9 +707,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             }
         }
         __syncwarp();
-    } else if (warp == 2 || warp == 3) {
-        // ------------------------------- Q tiles (warp 2) and their lse (warp 3)
-        uint32_t lq = 0, lp_set = 0, lp_par = 0;
+    } else if (warp == 3) {
+        // --------------------------------------------------- lse of the Q tiles
+        uint32_t lq = 0;
         bool ok = true;
         int col_tok[4], col_head[4];  // token and head in group of this lane's columns
 #pragma unroll
@@ -613,13 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         for (int u_it = 0; ok && next_unit(u_it, us); ++u_it) {
             const SeqInfo s = us.s;
             const SeqGeo g = geo(s);
-            const bool single = g.nq == 1;
-            const bool two = us.u.ntiles > 1;
-            QRange qr{0, 1};
-            if (!single)
-                qr = pair_queries(key_tile_at<kPaged>(g, s, us.u.q0),
-                                  key_tile_at<kPaged>(g, s, us.u.q0 + (two ? 1 : 0)), two, s, g.nq, tps, p.causal,
-                                  p.window, p.sinks);
+            const QRange qr = g.nq > 1 ? queries(g, s, us.u) : QRange{0, 1};
             float l[4];
             auto load_lse = [&](int qi) {
                 const int q0 = qi * tps, qe = min(q0 + tps, s.n);
@@ -632,196 +734,231 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
                                : -INFINITY;
                 }
             };
-            if (warp == 3 && qr.lo < qr.hi) load_lse(qr.lo);
+            if (qr.lo < qr.hi) load_lse(qr.lo);
             for (int qi = qr.lo; qi < qr.hi; ++qi, ++lq) {
-                const int st = lq % C::kStagesQ;
-                const uint32_t ph = (lq / C::kStagesQ) & 1;
-                const int q0 = qi * tps;
-                if (warp == 2) {
-                    if (!warp_wait(&ctl->q_empty[st], ph ^ 1, ctl, hdr)) { ok = false; break; }
-                    // a decode row's Q tile is one token's heads: the rest of the
-                    // stage keeps what it held, in columns that no sum takes
-                    const bool one = s.n == 1;
-                    if (lane == 0)
-                        mbar_arrive_expect_tx(&ctl->q_full[st], G * (one ? 1 : tps) * C::kRowBytes * C::kChunks);
-                    __syncwarp();
-                    if (lane < C::kChunks)
-                        tma_load_3d(q_smem + st * C::kTileBytes + lane * C::kChunkBytes, one ? &p.tm_q1 : &p.tm_q, &ctl->q_full[st],
-                                    lane * C::kChunkCols, us.u.kvh * G, s.q_start + q0);
-                    __syncwarp();
-                    lp_set |= 1u << st;
-                    lp_par = (lp_par & ~(1u << st)) | (ph << st);
-                } else {
-                    if (!warp_wait(&ctl->l_empty[st], ph ^ 1, ctl, hdr)) { ok = false; break; }
+                const int st = lq % kLse;
+                if (!warp_wait(&ctl->l_empty[st], ((lq / kLse) & 1) ^ 1, ctl, hdr)) { ok = false; break; }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ctl->neg_lse[st][lane + 32 * i] = l[i];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->l_full[st]);
-                    if (qi + 1 < qr.hi) load_lse(qi + 1);  // on its way during the next wait
-                }
+                for (int i = 0; i < 4; ++i) ctl->neg_lse[st][lane + 32 * i] = l[i];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->l_full[st]);
+                if (qi + 1 < qr.hi) load_lse(qi + 1);  // on its way during the next wait
             }
         }
-        if (warp == 2 && lane == 0 && aborted(ctl)) drain(ctl->q_full, lp_set, lp_par, C::kStagesQ);
     } else {
         // ------------------------------------------------------------ the sums
-        const int slot = (warp - 4) >> 2, sp = warp & 3;
+        const int group = (warp - 4) >> 2, sp = warp & 3;
         const int r = sp * 32 + lane;  // row of the key tile == TMEM lane
-        const uint32_t lane_off = (uint32_t)(sp * 32) << 16;
-        uint32_t t = 0, lq = 0, ns = 0;
+        const uint32_t col = tmem + ((uint32_t)(sp * 32) << 16) + group * 128;
+        Ring ring(C::kStages);
+        uint32_t lq = 0, ns = 0, nn = 0;  // Q tiles; S tiles of this group; tiles of one-Q-tile units (of every group)
+        uint32_t npair = 0, nread = 0;    // exchanges between two groups; tiles expanded
         bool ok = true;
+        // where the weight (and the scale) of key j of a tile of (b, kvh) lies
+        auto weight_row = [&](const Unit& u, int j) -> size_t {
+            if (kPaged) {
+                const int blk = __ldg(p.block_table + (size_t)u.b * p.max_blocks + (j >> p.block_log2));
+                return (((size_t)blk * p.n_kv_heads + u.kvh) << p.block_log2) + (j & ((1 << p.block_log2) - 1));
+            }
+            return ((size_t)u.b * p.n_kv_heads + u.kvh) * p.max_cache_len + j;
+        };
+        // Expands the codes (upper half of stage st) into the swizzled bf16 tile: the
+        // group's warps read all of them before any writes.
+        auto expand = [&](int st, uint32_t par) -> bool {
+            uint8_t* stage = ring_smem + st * C::kTileBytes;
+            if (!warp_wait(&ctl->full[st], par, ctl, hdr)) return false;
+            constexpr int kPieces = D / 8;  // 8 codes each, per thread
+            uint2 c[kPieces];
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                c[i] = *reinterpret_cast<const uint2*>(stage + C::kTileBytes / 2 + (r + 128 * i) * 8);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->read[group]);
+            if (!warp_wait(&ctl->read[group], nread & 1, ctl, hdr)) return false;
+            ++nread;
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+                const int idx = r + 128 * i, kr = idx / (D / 8), gr = idx % (D / 8);
+                const int ch = gr / (C::kChunkCols / 8), gg = gr % (C::kChunkCols / 8);
+                const int phys = D >= 64 ? (gg ^ (kr & 7)) : (gg ^ ((kr >> 1) & 3));
+                uint4 o;
+                expand4(c[i].x, o.x, o.y);
+                expand4(c[i].y, o.z, o.w);
+                *reinterpret_cast<uint4*>(stage + ch * C::kChunkBytes + kr * C::kRowBytes + phys * 16) = o;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->conv[group]);
+            return true;
+        };
+        // Adds to `total` the exp2s of this group's next S tile: n columns, of which
+        // this thread's key takes [lo, hi).
+        auto add_tile = [&](const float* nl, int n, int lo, int hi, bool has, float mul, float& total) -> bool {
+            if (!warp_wait(&ctl->s_full[group], ns & 1, ctl, hdr)) return false;
+            ++ns;
+            tc_fence_after();
+            float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+            if (__all_sync(0xffffffffu, n == kBlockN && (!has || (lo <= 0 && hi >= n)))) {
+                // 32 columns are summed while the next 32 are on their way
+                const float2 mul2 = make_float2(mul, mul);
+                uint32_t v[2][32];
+                tmem_ld32(col, v[0]);
+#pragma unroll
+                for (int c = 0; c < kBlockN; c += 32) {
+                    uint32_t (&x)[32] = v[(c / 32) & 1];
+                    tmem_wait_ld();
+                    reg_fence(x);
+                    if (c + 32 < kBlockN) {
+                        tmem_ld32(col + c + 32, v[(c / 32 + 1) & 1]);
+                    } else {  // everything of the buffer is in registers
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&ctl->s_empty[group]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 l = *reinterpret_cast<const float4*>(nl + c + e);
+                        const float2 s0 = __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2,
+                                                     make_float2(l.x, l.y));
+                        const float2 s1 = __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])),
+                                                     mul2, make_float2(l.z, l.w));
+                        a0 = __fadd2_rn(a0, make_float2(ex2(s0.x), ex2(s0.y)));
+                        a1 = __fadd2_rn(a1, make_float2(ex2(s1.x), ex2(s1.y)));
+                    }
+                }
+            } else {
+                for (int c = 0; c < n; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(col + c, v);
+                    tmem_wait_ld();
+                    reg_fence(v);
+                    const int m = min(32, n - c);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        if (e >= m) break;
+                        const float2 l = *reinterpret_cast<const float2*>(nl + c + e);
+                        const float x0 = ex2(fmaf(__uint_as_float(v[e]), mul, l.x));
+                        const float x1 = ex2(fmaf(__uint_as_float(v[e + 1]), mul, l.y));
+                        a0.x += c + e >= lo && c + e < hi ? x0 : 0.f;
+                        a0.y += c + e + 1 >= lo && c + e + 1 < hi ? x1 : 0.f;
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->s_empty[group]);
+            }
+            total += (a0.x + a1.x) + (a0.y + a1.y);
+            return true;
+        };
+        // columns [lo, hi) of the queries that see key j (columns are in token order)
+        auto columns = [&](const SeqInfo& s, int j, int q0, int cols, int& lo, int& hi) {
+            lo = 0;
+            hi = cols;
+            if (p.causal) {
+                lo = max(0, j - s.P - q0) * G;
+                if (p.window > 0 && j >= p.sinks) hi = min(hi, (p.window + j - s.P - q0) * G);
+            }
+        };
+        // key j's weight row, old weight and score factor; false: the row holds no key
+        auto fetch = [&](const Unit& u, const SeqGeo& g, const KeyTile& k, size_t& row, float& old, float& mul) -> bool {
+            const int j = k.kb + r;
+            old = 0.f;
+            mul = p.scale_log2;
+            if (j < k.lo || j >= k.hi) return false;
+            row = weight_row(u, j);
+            if (k.jt < g.np) {
+                old = p.weights[row];
+                if (kQuant) mul *= __ldg(p.scale_k + row);
+            }
+            return true;
+        };
         UnitSlot us;
         for (int u_it = 0; ok && next_unit(u_it, us); ++u_it) {
             const SeqInfo s = us.s;
+            const Unit u = us.u;
             const SeqGeo g = geo(s);
-            const bool single = g.nq == 1;
-            if (single && !warp_wait(&ctl->l_full[lq % C::kStagesQ], (lq / C::kStagesQ) & 1, ctl, hdr)) break;
-            for (int x = us.u.q0; x < us.u.q0 + us.u.ntiles && ok; x += 2) {
-                const bool two = x + 1 < us.u.q0 + us.u.ntiles;
-                const bool mine = slot == 0 || two;
-                const KeyTile k0 = key_tile_at<kPaged>(g, s, x), k1 = key_tile_at<kPaged>(g, s, two ? x + 1 : x);
-                const KeyTile k = slot ? k1 : k0;
-                const QRange qr =
-                    single ? QRange{0, 1} : pair_queries(k0, k1, two, s, g.nq, tps, p.causal, p.window, p.sinks);
-                // this thread's key: its weight's row, its old weight
-                const int j = k.kb + r;
-                const bool has = mine && j >= k.lo && j < k.hi;
-                const bool pre = k.jt < g.np;
-                float* w = nullptr;
-                float old = 0.f, mul = p.scale_log2;
-                if (has) {
-                    size_t row;
-                    if (kPaged) {
-                        const int blk = __ldg(p.block_table + (size_t)us.u.b * p.max_blocks + (j >> p.block_log2));
-                        row = (((size_t)blk * p.n_kv_heads + us.u.kvh) << p.block_log2) + (j & ((1 << p.block_log2) - 1));
-                    } else {
-                        row = ((size_t)us.u.b * p.n_kv_heads + us.u.kvh) * p.max_cache_len + j;
-                    }
-                    w = p.weights + row;
-                    if (pre) old = *w;
-                    if (kQuant && pre) mul *= __ldg(p.scale_k + row);
-                }
-                if (kQuant && mine && pre) {
-                    // expand the codes (upper half of the stage) into the swizzled
-                    // bf16 tile: all of them are read before any is overwritten
-                    const int st = (t + slot) % C::kStagesK;
-                    uint8_t* stage = k_smem + st * C::kTileBytes;
-                    if (!warp_wait(&ctl->k_full[st], ((t + slot) / C::kStagesK) & 1, ctl, hdr)) { ok = false; break; }
-                    constexpr int kPieces = 128 * D / 8 / 128;  // 8 codes each, per thread
-                    const int i0 = sp * 32 + lane;
-                    uint2 c[kPieces];
-#pragma unroll
-                    for (int i = 0; i < kPieces; ++i)
-                        c[i] = *reinterpret_cast<const uint2*>(stage + C::kTileBytes / 2 + (i0 + 128 * i) * 8);
-                    slot_sync(slot);
-#pragma unroll
-                    for (int i = 0; i < kPieces; ++i) {
-                        const int idx = i0 + 128 * i, row = idx / (D / 8), gr = idx % (D / 8);
-                        const int ch = gr / (C::kChunkCols / 8), gg = gr % (C::kChunkCols / 8);
-                        const int phys = D >= 64 ? (gg ^ (row & 7)) : (gg ^ ((row >> 1) & 3));
-                        uint32_t o[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t wd = e < 2 ? c[i].x : c[i].y;
-                            const int sh = (e & 1) * 16;
-                            const __nv_bfloat162 v =
-                                __floats2bfloat162_rn((float)(int8_t)(wd >> sh), (float)(int8_t)(wd >> (sh + 8)));
-                            o[e] = *reinterpret_cast<const uint32_t*>(&v);
-                        }
-                        *reinterpret_cast<uint4*>(stage + ch * C::kChunkBytes + row * C::kRowBytes + phys * 16) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->k_conv[st]);
-                }
-                const float2 mul2 = make_float2(mul, mul);
-                float total = 0.f;
-                for (int qi = qr.lo; qi < qr.hi; ++qi) {
-                    const int qst = lq % C::kStagesQ;
-                    const int q0 = qi * tps, qe = min(q0 + tps, s.n);
-                    if (!single && !warp_wait(&ctl->l_full[qst], (lq / C::kStagesQ) & 1, ctl, hdr)) { ok = false; break; }
-                    if (mine && tile_seen(k, s.P, q0, qe, p.causal, p.window, p.sinks)) {
-                        const int buf = ns & 1;
-                        if (!warp_wait(&ctl->s_full[slot][buf], (ns >> 1) & 1, ctl, hdr)) { ok = false; break; }
-                        tc_fence_after();
-                        const int cols = (qe - q0) * G;
-                        // columns [clo, chi) of this key's queries (columns are in token order)
-                        int clo = 0, chi = cols;
-                        if (p.causal) {
-                            clo = max(0, j - s.P - q0) * G;
-                            if (p.window > 0 && j >= p.sinks) chi = min(chi, (p.window + j - s.P - q0) * G);
-                        }
-                        const bool whole = __all_sync(0xffffffffu, cols == kBlockN && (!has || (clo == 0 && chi == cols)));
-                        const uint32_t col = tmem + lane_off + (slot * 2 + buf) * 128;
-                        const float4* nl = reinterpret_cast<const float4*>(ctl->neg_lse[qst]);
-                        float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-                        if (whole) {
-                            // 32 columns are summed while the next 32 are on their way
-                            uint32_t v[2][32];
-                            tmem_ld32(col, v[0]);
-#pragma unroll
-                            for (int c = 0; c < kBlockN; c += 32) {
-                                uint32_t (&x)[32] = v[(c / 32) & 1];
-                                tmem_wait_ld();
-                                reg_fence(x);
-                                if (c + 32 < kBlockN) {
-                                    tmem_ld32(col + c + 32, v[(c / 32 + 1) & 1]);
-                                } else {  // everything of the buffer is in registers
-                                    tc_fence_before();
-                                    __syncwarp();
-                                    if (lane == 0) mbar_arrive(&ctl->s_empty[slot][buf]);
-                                }
-#pragma unroll
-                                for (int e = 0; e < 32; e += 4) {
-                                    const float4 l = nl[(c + e) / 4];
-                                    const float2 s0 =
-                                        __ffma2_rn(make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), mul2,
-                                                   make_float2(l.x, l.y));
-                                    const float2 s1 =
-                                        __ffma2_rn(make_float2(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])), mul2,
-                                                   make_float2(l.z, l.w));
-                                    a0 = __fadd2_rn(a0, make_float2(ex2(s0.x), ex2(s0.y)));
-                                    a1 = __fadd2_rn(a1, make_float2(ex2(s1.x), ex2(s1.y)));
-                                }
-                            }
-                        } else {
-                            for (int c = 0; c < cols; c += 32) {
-                                uint32_t v[32];
-                                tmem_ld32(col + c, v);
-                                tmem_wait_ld();
-                                reg_fence(v);
-#pragma unroll
-                                for (int e = 0; e < 32; e += 2) {
-                                    const float2 l = reinterpret_cast<const float2*>(nl)[(c + e) / 2];
-                                    const float x0 = ex2(fmaf(__uint_as_float(v[e]), mul, l.x));
-                                    const float x1 = ex2(fmaf(__uint_as_float(v[e + 1]), mul, l.y));
-                                    a0.x += c + e >= clo && c + e < chi ? x0 : 0.f;
-                                    a0.y += c + e + 1 >= clo && c + e + 1 < chi ? x1 : 0.f;
-                                }
-                            }
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&ctl->s_empty[slot][buf]);
-                        }
-                        total += (a0.x + a1.x) + (a0.y + a1.y);
-                        ++ns;
-                    }
-                    if (!single) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&ctl->l_empty[qst]);
-                        ++lq;
-                    }
+            uint32_t par;
+            ring.unit();
+            if (g.nq == 1) {
+                // every fourth tile is this group's; its next tile's weights are
+                // fetched one tile ahead
+                ring.next(true, par);
+                if (!warp_wait(&ctl->l_full[lq % kLse], (lq / kLse) & 1, ctl, hdr)) break;
+                const float* nl = ctl->neg_lse[lq % kLse];
+                const int end = u.q0 + u.ntiles;
+                int mine = u.q0 + (int)((group - nn) & 3);
+                size_t row = 0, next_row = 0;
+                float old = 0.f, next_old = 0.f, mul = 0.f, next_mul = 0.f;
+                bool has = mine < end && fetch(u, g, key_tile_at<kPaged>(g, s, mine), row, old, mul), next_has = false;
+                for (int x = u.q0; x < end; ++x, ++nn) {
+                    const int kst = ring.next(false, par);
+                    if (x != mine) continue;
+                    mine += 4;
+                    next_has = mine < end && fetch(u, g, key_tile_at<kPaged>(g, s, mine), next_row, next_old, next_mul);
+                    const KeyTile k = key_tile_at<kPaged>(g, s, x);
+                    if (kQuant && k.jt < g.np && !expand(kst, par)) { ok = false; break; }
+                    int lo, hi;
+                    columns(s, k.kb + r, 0, s.n * G, lo, hi);
+                    float total = 0.f;
+                    if (!add_tile(nl, s.n * G, lo, hi, has, mul, total)) { ok = false; break; }
+                    if (has) p.weights[row] = old + total;
+                    row = next_row;
+                    has = next_has;
+                    old = next_old;
+                    mul = next_mul;
                 }
                 if (!ok) break;
-                if (has) *w = old + total;
-                t += two ? 2 : 1;
-            }
-            if (!ok) break;
-            if (single) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->l_empty[lq % C::kStagesQ]);
+                if (lane == 0) mbar_arrive(&ctl->l_empty[lq % kLse]);
+                ++lq;
+                continue;
+            }
+            const int nt = u.ntiles;
+            const bool four = nt > 2;
+            const int t = four ? group : group & 1, turn = group >> 1;  // this group's tile; its Q tiles' parity (if two)
+            const bool here = t < nt;
+            const QRange qr = queries(g, s, u);
+            const KeyTile k = key_tile_at<kPaged>(g, s, u.q0 + (here ? t : 0));
+            size_t row = 0;
+            float old = 0.f, mul = 0.f, total = 0.f;
+            const bool has = here && fetch(u, g, k, row, old, mul);
+            for (int i = 0; i < nt; ++i) {
+                const int st = ring.next(true, par);
+                if (kQuant && i == t && (four || turn == 0) && k.jt < g.np && !expand(st, par)) { ok = false; break; }
+            }
+            for (int qi = qr.lo; qi < qr.hi && ok; ++qi) {
+                const int q0 = qi * tps, qe = min(q0 + tps, s.n), cols = (qe - q0) * G;
+                ring.next(false, par);
+                if (here && (four || (qi & 1) == turn) && seen(k, s, q0, qe)) {
+                    if (!warp_wait(&ctl->l_full[lq % kLse], (lq / kLse) & 1, ctl, hdr)) { ok = false; break; }
+                    int lo, hi;
+                    columns(s, k.kb + r, q0, cols, lo, hi);
+                    if (!add_tile(ctl->neg_lse[lq % kLse], cols, lo, hi, has, mul, total)) { ok = false; break; }
+                } else if (!warp_wait(&ctl->l_full[lq % kLse], (lq / kLse) & 1, ctl, hdr)) {
+                    ok = false;
+                    break;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->l_empty[lq % kLse]);
                 ++lq;
             }
+            if (!ok) break;
+            if (!four && here) {
+                // the second group's sums join the first one's (bounded waits, both ways)
+                if (turn) {
+                    if (!warp_wait(&ctl->pair_empty[t], (npair & 1) ^ 1, ctl, hdr)) break;
+                    ctl->pair[t][r] = total;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->pair_full[t]);
+                } else {
+                    if (!warp_wait(&ctl->pair_full[t], npair & 1, ctl, hdr)) break;
+                    total += ctl->pair[t][r];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->pair_empty[t]);
+                }
+                ++npair;
+            }
+            if (has && (four || turn == 0)) p.weights[row] = old + total;
         }
     }
 

@@ -488,3 +488,15 @@ def test_many_sequences_with_a_bad_block():
     c.sinks(40, 3)
     c.check(skipped=[299], window=40, sinks=3)
     assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+
+
+@pytest.mark.parametrize("block,int8", [(0, False), (0, True), (32, False), (32, True)])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_key_weights_of_mixed_queries(d, block, int8):
+    """Sequences of one query row to several Q tiles of them (16, 17 and 32 tokens of 4 heads: 64, 68 and 128 rows),
+    many of each, so that a CTA takes units of both kinds in turn."""
+    new = [1, 17, 16, 200, 1, 32, 33, 3] * 12
+    lens = [(i * 131) % 700 for i in range(len(new))]
+    c = Call(120, new, lens, d, 2, 4, block, int8)
+    weigh(c)
+    ok()
