@@ -802,7 +802,7 @@ pa_status read_prefix(const pa_prefix* prefix, const Options& o, Prefix* out) {
 // Slabs of partial results are bounded by this many bytes for a sequence's own
 // keys (a few long rows: up to kMaxPieces pieces) and again for the prefix's.
 constexpr long long kPartialBytes = 64ll << 20;
-constexpr int kMaxPieces = 32;
+using pa::kMaxPieces;
 constexpr int kMinPieceTiles = 4;
 constexpr int kPieceWaves = 2;
 

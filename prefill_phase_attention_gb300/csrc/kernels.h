@@ -123,6 +123,10 @@ struct LongScheduleArgs : ScheduleArgs {
 };
 cudaError_t launch_build_long_schedule(const LongScheduleArgs& a, cudaStream_t stream);
 
+// Slabs of a row that the merge joins, at most: a sequence's own pieces and the prefix's.
+constexpr int kMaxPieces = 32;
+constexpr int kMaxSlabs = 2 * kMaxPieces;
+
 // Joins the partial results of every (token, head): the token's own slabs
 // [0, tok_pieces) and the prefix's [prefix_slab, prefix_slab + *prefix_pieces).
 struct MergeArgs {

@@ -287,42 +287,62 @@ __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(co
     }
 }
 
-// One row (token, head) per D / 4 lanes; the row's slabs are read 4 at a time.
+// One row (token, head) per D / 4 lanes.  The lanes fetch the row's log-sum-exps
+// together (one load deep, whatever the number of slabs) and share their weights
+// by shuffles; the slabs' outputs are then fetched eight at a time.  The launch is
+// bound by these latencies for a few rows and by L2 for many (the slabs were just
+// written).
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ MergeArgs a) {
     constexpr int kLanes = D / 4;
     griddep_wait();
     const long long rows = (long long)a.total_q * a.n_heads;
-    const long long row = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
-    if (row >= rows) return;
-    const int c = threadIdx.x % kLanes * 4;
-    const int own = a.tok_pieces[row / a.n_heads];
-    if (own == 0) return;  // not this call's, or written by its unit
-    const int n = own + (a.prefix_pieces ? *a.prefix_pieces : 0);
+    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+    const int l = threadIdx.x % kLanes;
+    const unsigned lanes = kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1) << (threadIdx.x % 32 / kLanes * kLanes);
+    const bool in = at < rows;
+    const long long row = in ? at : 0;
+    const int own = in ? a.tok_pieces[row / a.n_heads] : 0;
+    if (own == 0) return;  // not this call's, or written by its unit (the row's lanes agree)
+    const int n = own + (a.prefix_pieces ? __ldg(a.prefix_pieces) : 0);
     auto slab = [&](int i) { return (size_t)(i < own ? i : a.prefix_slab + i - own) * rows + row; };
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, a.part_lse[slab(i)]);
+    // lane l holds slabs l, l + kLanes, ...; at most kMaxSlabs in all
+    constexpr int kHeld = (kMaxSlabs + kLanes - 1) / kLanes;
+    float w[kHeld], m = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        w[h] = h * kLanes + l < n ? a.part_lse[slab(h * kLanes + l)] : -INFINITY;
+        m = fmaxf(m, w[h]);
+    }
+    for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        w[h] = w[h] == -INFINITY ? 0.f : exp2f(w[h] - m);  // 0: an empty piece, its output was not written
+        sum += w[h];
+    }
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const size_t s = slab(i);
-        const float l = a.part_lse[s];
-        const float4 o = *reinterpret_cast<const float4*>(a.part_o + s * D + c);
-        const float w = l == -INFINITY ? 0.f : exp2f(l - m);
-        if (w == 0.f) continue;  // an empty piece: its output was not written
-        sum += w;
-        acc.x = fmaf(w, o.x, acc.x);
-        acc.y = fmaf(w, o.y, acc.y);
-        acc.z = fmaf(w, o.z, acc.z);
-        acc.w = fmaf(w, o.w, acc.w);
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+        if (h * kLanes >= n) break;
+        const int k = min(kLanes, n - h * kLanes);
+#pragma unroll 8
+        for (int i = 0; i < k; ++i) {
+            const float wi = __shfl_sync(lanes, w[h], i, kLanes);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (wi != 0.f) o = *reinterpret_cast<const float4*>(a.part_o + slab(h * kLanes + i) * D + 4 * l);
+            acc.x = fmaf(wi, o.x, acc.x);
+            acc.y = fmaf(wi, o.y, acc.y);
+            acc.z = fmaf(wi, o.z, acc.z);
+            acc.w = fmaf(wi, o.w, acc.w);
+        }
     }
     const float inv = 1.f / sum;
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
     const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    uint2 packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    *reinterpret_cast<uint2*>(a.out + row * D + c) = packed;
-    if (c == 0 && a.lse) a.lse[row] = (m + log2f(sum)) * 0.69314718055994530942f;
+    const uint2 packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+    *reinterpret_cast<uint2*>(a.out + row * D + 4 * l) = packed;
+    if (l == 0 && a.lse) a.lse[row] = (m + log2f(sum)) * 0.69314718055994530942f;
 }
 
 }  // namespace
