@@ -309,8 +309,8 @@ typedef struct pa_prefix {
  * cache_offsets[b] + i.  The prefix's K/V are read once for a block of the
  * whole batch's queries, not once per sequence, and the two parts are joined
  * by their log-sum-exp (partial results in fp32 in the per-stream workspace:
- * up to 64 MiB, and at least two times total_q * n_heads * (head_dim + 1) * 4
- * bytes).  Every option of pa_options applies but window and
+ * up to 64 MiB for the own part and 256 MiB for the prefix's, and at least
+ * total_q * n_heads * (head_dim + 1) * 4 bytes for each).  Every option of pa_options applies but window and
  * wait_timeout_test.  len = 0 is prefill_attn_varlen_ex.  A prefix block
  * outside the pool rejects the whole call on the device
  * (PA_DEVERR_METADATA, nothing written).  Under graph capture the stream must

@@ -799,9 +799,9 @@ pa_status read_prefix(const pa_prefix* prefix, const Options& o, Prefix* out) {
     return PA_OK;
 }
 
-// Slabs of partial results are bounded by this many bytes for a sequence's own
-// keys (a few long rows: up to kMaxPieces pieces) and again for the prefix's.
-constexpr long long kPartialBytes = 64ll << 20;
+// Slabs of partial results are bounded by this many bytes for the sequences' own
+// keys (a few long rows: up to kMaxPieces pieces) and for the prefix's.
+constexpr long long kPartialBytes = 64ll << 20, kPrefixPartialBytes = 256ll << 20;
 using pa::kMaxPieces;
 constexpr int kMinPieceTiles = 4;
 constexpr int kPieceWaves = 2;
@@ -836,10 +836,13 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     const long long slab_bytes = slab_rows * (head_dim + 1) * 4;
     const int fit = (int)std::max(1ll, std::min((long long)kMaxPieces, kPartialBytes / slab_bytes));
     const int max_pieces = fit;
+    // a prefix of fewer units than wanted is cut to make as many; of one with more
+    // than CTAs only the units of the last round are, into at most four
     int max_prefix_pieces = 0;
-    if (pre.len > 0)
-        max_prefix_pieces = (int)std::max(1ll, std::min((long long)kMaxPieces, std::min(kPartialBytes / slab_bytes,
-                                                                                       (target + pre_units - 1) / pre_units)));
+    if (pre.len > 0) {
+        const long long want = pre_units > sms ? 4 : std::min((long long)kMaxPieces, (target + pre_units - 1) / pre_units);
+        max_prefix_pieces = (int)std::max(1ll, std::min(want, kPrefixPartialBytes / slab_bytes));
+    }
     const bool merge = pre.len > 0 || max_pieces > 1;
     const long long slabs = merge ? max_pieces + max_prefix_pieces : 0;
     // pieces per block: at most 1 + tiles / piece size, so a call has at most its
@@ -852,7 +855,7 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     s = get_workspace(dev, stream, num_seqs + 1, 0, &ws);
     if (s != PA_OK) return s;
     const size_t list_bytes = align_up((size_t)units * sizeof(pa::UnitX), 256);
-    const size_t seq_bytes = align_up(((size_t)num_seqs + 1) * sizeof(int), 256);
+    const size_t seq_bytes = align_up(((size_t)num_seqs + 1 + pre_units) * sizeof(int), 256);
     const size_t tok_bytes = merge ? align_up((size_t)total_q * sizeof(int), 256) : 0;
     const size_t lse_bytes = align_up((size_t)(slabs * slab_rows) * sizeof(float), 256);
     const size_t o_bytes = (size_t)(slabs * slab_rows) * head_dim * sizeof(float);
@@ -873,6 +876,7 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     sa.seq_group = scr.seq_scratch + num_seqs + 1;
     sa.xunits = reinterpret_cast<pa::UnitX*>(at);
     sa.seq_pieces = reinterpret_cast<int*>(at + list_bytes);
+    sa.pre_pieces = sa.seq_pieces + num_seqs + 1;
     sa.tok_pieces = merge ? reinterpret_cast<int*>(at + list_bytes + seq_bytes) : nullptr;
     sa.sinks = sinks;
     sa.prefix_len = pre.len;
@@ -912,8 +916,8 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
                          : pa::launch_attn_long_d<128>(p, grid, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
     if (merge) {
-        pa::MergeArgs ma{p.part_o, p.part_lse, sa.tok_pieces, pre.len > 0 ? sa.seq_pieces + num_seqs : nullptr,
-                         max_pieces, static_cast<__nv_bfloat16*>(out), lse, total_q, n_heads};
+        pa::MergeArgs ma{p.part_o, p.part_lse, sa.tok_pieces, pre.len > 0 ? sa.pre_pieces : nullptr, tpu,
+                         n_heads / n_kv_heads, max_pieces, static_cast<__nv_bfloat16*>(out), lse, total_q, n_heads};
         e = pa::launch_merge(ma, head_dim, stream);
         if (e != cudaSuccess) return cuda_fail(e, "merge launch");
         ++launches;

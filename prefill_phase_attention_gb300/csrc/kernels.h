@@ -112,7 +112,8 @@ cudaError_t launch_attn_long_d<128>(const FwdParamsX& p, int grid, cudaStream_t 
 // Scheduler of the long-context variant.
 struct LongScheduleArgs : ScheduleArgs {
     UnitX* xunits;
-    int* seq_pieces;  // [num_seqs + 1] pieces each query block of the sequence is cut into (last: the prefix's)
+    int* seq_pieces;  // [num_seqs + 1] scheduler scratch: pieces of each sequence's query blocks
+    int* pre_pieces;  // [query blocks of the whole batch][n_kv_heads] pieces of each prefix unit
     int* tok_pieces;  // [total_q] slabs that the merge joins for a token (0: none); nullptr: no merge
     int sinks;
     int prefix_len;
@@ -128,12 +129,13 @@ constexpr int kMaxPieces = 32;
 constexpr int kMaxSlabs = 2 * kMaxPieces;
 
 // Joins the partial results of every (token, head): the token's own slabs
-// [0, tok_pieces) and the prefix's [prefix_slab, prefix_slab + *prefix_pieces).
+// [0, tok_pieces) and its prefix unit's, from prefix_slab on.
 struct MergeArgs {
     const float* part_o;
     const float* part_lse;
     const int* tok_pieces;
-    const int* prefix_pieces;  // nullptr: no prefix
+    const int* pre_pieces;  // [token / tokens_per_block][n_kv_heads]; nullptr: no prefix
+    int tokens_per_block, group;
     int prefix_slab;
     __nv_bfloat16* out;
     float* lse;

@@ -387,7 +387,8 @@ __global__ void __launch_bounds__(kFewThreads) build_key_schedule_few_kernel(con
         const int len = g.nq == 1 ? run_length(f.total, a.num_ctas) : wide_length(s_wide, a.num_ctas);
         s_tiles[tid] = g.tiles;
         s_len[tid] = len;
-        f.blocks[tid] = f.units[tid] = (g.tiles + len - 1) / len;
+        f.blocks[tid] = (g.tiles + len - 1) / len;
+        f.units[tid] = f.blocks[tid] * a.n_kv_heads;
         f.cost[tid] = (float)g.tiles * (float)g.nq;
     }
     __syncthreads();
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kFewThreads) build_key_schedule_few_kernel(con
     for (int w = tid; w < blocks * a.n_kv_heads; w += kFewThreads) {
         const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
         const int b = block_owner(f.seqs, a.num_seqs, i);
-        emit_keys(a, f.seqs[b], b, i - f.seqs[b].pad, kvh, s_tiles[b], s_len[b], f.units[b], f.first[b]);
+        emit_keys(a, f.seqs[b], b, i - f.seqs[b].pad, kvh, s_tiles[b], s_len[b], f.blocks[b], f.first[b]);
     }
 }
 

@@ -135,7 +135,7 @@ struct FewSeqs {
     SeqInfo seqs[kFewSeqs];  // pad: index of the sequence's first block
     float cost[kFewSeqs];
     int blocks[kFewSeqs];    // schedulable blocks per head
-    int units[kFewSeqs];     // units per head (0: none)
+    int units[kFewSeqs];     // units in all
     int first[kFewSeqs];     // its first unit in the list
     int group[kFewSeqs];     // KV heads that run together
     int spans[kFewSeqs][2];  // table entries [0, x) and [y, end) to check: x, y
@@ -221,12 +221,11 @@ __device__ __forceinline__ int rank_few(const ScheduleArgs& a, FewSeqs& f, int n
             pad += b < tid ? n : 0;
             total += u;
         }
-        f.first[tid] = first * a.n_kv_heads;
+        f.first[tid] = first;
         f.seqs[tid].pad = pad;
         a.seqs[tid] = f.seqs[tid];
         if (tid == nseq - 1) {
             f.max_chunks = pad + f.blocks[tid];
-            total *= a.n_kv_heads;
             a.hdr->num_units = total < a.max_units ? total : a.max_units;
             a.hdr->counter = 0;
             a.hdr->max_units = a.max_units;

@@ -10,7 +10,11 @@
 //
 // Piece size: the whole call's tiles over target_units, at least min_tiles.
 // All blocks of a sequence get the same number of pieces (that of its longest
-// block); a block with fewer tiles than pieces leaves holes in the list.
+// block); a block with fewer tiles than pieces leaves holes in the list.  Of a
+// prefix with more units than CTAs, whole rounds of units stay uncut and only the
+// rest is cut, so that the last round is short (16 questions over an 8191-token
+// prefix, 256 units of 64 tiles on 152 CTAs: 112 tiles for the busiest CTA where
+// halves of every unit made it 128, for about the same partial results).
 #include <cuda_bf16.h>
 
 #include <cstdint>
@@ -26,12 +30,15 @@ namespace pa {
 namespace {
 
 // Writes the units of query block blk of sequence b and KV head kvh: the block's
-// c tiles in its sequence's p pieces.
+// c tiles in its sequence's p pieces, or in one where the block is among the
+// sequence's first `whole` ones.
 __device__ __forceinline__ void emit_block(const LongScheduleArgs& a, const SeqInfo& si, int b, int blk, int kvh,
-                                           int nblk, int hg, int p, int first, int tpu, int c) {
+                                           int nblk, int hg, int p, int whole, int first, int tpu, int c) {
     const bool pre = b == a.num_seqs, partial = a.prefix_len > 0 || p > 1;
     const int g0 = kvh - kvh % hg, gsize = min(hg, a.n_kv_heads - g0);
-    const int pos = first + (g0 * nblk + (nblk - 1 - blk) * gsize + (kvh - g0)) * p;
+    const int rank = g0 * nblk + (nblk - 1 - blk) * gsize + (kvh - g0);
+    const int pos = first + (rank < whole ? rank : whole + (rank - whole) * p);
+    if (rank < whole) p = 1;
     const int pb = min(p, c);  // pieces of this block
     for (int k = 0, s0 = 0; k < p && pos + k < a.max_units; ++k) {
         // c < 2^24 tiles and k <= 32 pieces: the product fits 32 bits
@@ -43,8 +50,23 @@ __device__ __forceinline__ void emit_block(const LongScheduleArgs& a, const SeqI
         a.xunits[pos + k] = x;
         s0 = s1;
     }
+    if (pre) a.pre_pieces[blk * a.n_kv_heads + kvh] = pb;
     if (a.tok_pieces && partial && !pre && kvh == 0)
         for (int t = blk * tpu; t < min(si.n, (blk + 1) * tpu); ++t) a.tok_pieces[si.q_start + t] = pb;
+}
+
+// How a prefix of U units of `tiles` each (U > CTAs) is cut: `whole` units stay
+// uncut, the others get the pieces that make their rounds shortest (a piece
+// costs about one tile more: its start, its partial results).
+__device__ __forceinline__ int cut_rest(int units, int tiles, int num_ctas, int max_pieces, int min_tiles, int* whole) {
+    *whole = units / num_ctas * num_ctas;
+    const int rest = units - *whole;
+    int best = 1, best_cost = 0x7fffffff;
+    for (int p = 1; p <= max_pieces && (p == 1 || tiles >= p * min_tiles); ++p) {
+        const int cost = (rest * p + num_ctas - 1) / num_ctas * ((tiles + p - 1) / p + 1);
+        if (cost < best_cost) best = p, best_cost = cost;
+    }
+    return best;
 }
 
 __global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_constant__ LongScheduleArgs a) {
@@ -161,7 +183,6 @@ __global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_
         int p = (int)((mx + piece - 1) / piece);
         p = max(1, min(p, pre ? a.max_prefix_pieces : a.max_pieces));
         pieces[b] = p;
-        a.seq_pieces[b] = p;
         if (nblk > 0) {
             const int bin = cost_bin((long long)c * a.n_kv_heads / p);
             seq_scratch[b] = bin;
@@ -202,7 +223,7 @@ __global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_
         const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
         const int b = block_owner(seqs, nseq, i);
         const SeqInfo si = seqs[b];
-        emit_block(a, si, b, i - si.pad, kvh, (si.n + tpu - 1) / tpu, seq_group[b], pieces[b], seq_scratch[b], tpu,
+        emit_block(a, si, b, i - si.pad, kvh, (si.n + tpu - 1) / tpu, seq_group[b], pieces[b], 0, seq_scratch[b], tpu,
                    block_tiles(si, i - si.pad, b == a.num_seqs));
     }
 }
@@ -210,7 +231,7 @@ __global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_
 // The same for a few sequences (kFewSeqs): see schedule.cuh.
 __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(const __grid_constant__ LongScheduleArgs a) {
     __shared__ FewSeqs f;
-    __shared__ int s_max[kFewSeqs], s_tiles[kFewSeqs], s_pieces[kFewSeqs];
+    __shared__ int s_max[kFewSeqs], s_tiles[kFewSeqs], s_pieces[kFewSeqs], s_whole;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tpu = a.unit_slots * (kBlockM / a.group);
     const bool shared_prefix = a.prefix_len > 0, paged = a.block_table != nullptr;
@@ -270,9 +291,14 @@ __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(co
         const int c = s_tiles[tid], mx = s_max[tid];
         int p = (mx + piece - 1) / piece;
         p = max(1, min(p, tid == a.num_seqs ? a.max_prefix_pieces : a.max_pieces));
+        const int units = f.blocks[tid] * a.n_kv_heads;
+        int whole = 0;
+        if (tid == a.num_seqs) {
+            if (units > a.num_ctas) p = cut_rest(units, mx, a.num_ctas, a.max_prefix_pieces, a.min_tiles, &whole);
+            s_whole = whole;
+        }
         s_pieces[tid] = p;
-        a.seq_pieces[tid] = p;
-        f.units[tid] = f.blocks[tid] * p;
+        f.units[tid] = whole + (units - whole) * p;
         f.cost[tid] = (float)c / (float)p;
         f.group[tid] =
             kv_head_group(f.seqs[tid], a.head_dim, a.n_kv_heads, a.num_ctas, (long long)c, (mx + p - 1) / p);
@@ -282,7 +308,8 @@ __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(co
     for (int w = tid; w < total_blocks * a.n_kv_heads; w += kFewThreads) {
         const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
         const int b = block_owner(f.seqs, nseq, i);
-        emit_block(a, f.seqs[b], b, i - f.seqs[b].pad, kvh, f.blocks[b], f.group[b], s_pieces[b], f.first[b], tpu,
+        emit_block(a, f.seqs[b], b, i - f.seqs[b].pad, kvh, f.blocks[b], f.group[b], s_pieces[b],
+                   b == a.num_seqs ? s_whole : 0, f.first[b], tpu,
                    block_tiles(f.seqs[b], i - f.seqs[b].pad, b == a.num_seqs));
     }
 }
@@ -304,7 +331,9 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Merg
     const long long row = in ? at : 0;
     const int own = in ? a.tok_pieces[row / a.n_heads] : 0;
     if (own == 0) return;  // not this call's, or written by its unit (the row's lanes agree)
-    const int n = own + (a.prefix_pieces ? __ldg(a.prefix_pieces) : 0);
+    int n = own;
+    if (a.pre_pieces)
+        n += __ldg(a.pre_pieces + row / a.n_heads / a.tokens_per_block * (a.n_heads / a.group) + row % a.n_heads / a.group);
     auto slab = [&](int i) { return (size_t)(i < own ? i : a.prefix_slab + i - own) * rows + row; };
     // lane l holds slabs l, l + kLanes, ...; at most kMaxSlabs in all
     constexpr int kHeld = (kMaxSlabs + kLanes - 1) / kLanes;
