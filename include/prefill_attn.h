@@ -50,6 +50,10 @@
  *     sizes and pointers of the capture; the device metadata (cu_seqlens_*,
  *     cache_offsets) and the data in the buffers are read at replay time, so
  *     they may change between replays within those sizes.
+ *     Graphs captured on one stream share that stream's workspace, so their
+ *     replays must not overlap each other or the stream's own calls.  A
+ *     workspace that a captured call uses is kept until prefill_attn_release()
+ *     even when a later call outgrows it.
  *     prefill_attn_varlen_noalloc allocates nothing at all.
  */
 #ifndef PREFILL_ATTN_H

@@ -247,7 +247,11 @@ def _ptr(t):
 
 
 def _stream_on(stream, device: int) -> int:
-    return _raw_stream(device) if stream is None and _raw_stream is not None else _stream_handle(stream, device)
+    if stream is None:
+        return _raw_stream(device) if _raw_stream is not None else _stream_handle(None, device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the tensors on cuda:{device}")
+    return stream.cuda_stream
 
 
 def _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d):

@@ -48,6 +48,7 @@ struct Workspace {
     void* aux = nullptr;   // lists and partial results of the long-context calls (grown on demand)
     size_t aux_bytes = 0;
     bool captured = false;  // a captured graph holds these addresses: outgrown blocks are kept, not freed
+    std::vector<void*> old_headers;  // headers of outgrown blocks that a graph may still write errors to
 };
 
 std::mutex g_mu;
@@ -114,8 +115,10 @@ pa_status get_workspace(int dev, cudaStream_t st, int num_seqs, int max_units, W
         cudaFreeAsync(nw.ptr, st);
         return cuda_fail(e, "workspace init");
     }
-    drop_block(w, dev, w.ptr, st);
     nw.captured = w.captured;
+    nw.old_headers = w.old_headers;
+    if (w.captured && w.ptr) nw.old_headers.push_back(w.ptr);
+    drop_block(w, dev, w.ptr, st);
     nw.rope = w.rope;  // the rotary and auxiliary scratch are grown on their own
     nw.rope_bytes = w.rope_bytes;
     nw.aux = w.aux;
@@ -588,11 +591,14 @@ pa_status prefill_attn_device_status(pa_stream_t stream_, int32_t* flags) {
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
-    void* words[2] = {nullptr, noalloc_scratch_if_set_up()};  // workspace, allocation-free scratch
+    std::vector<void*> words = {noalloc_scratch_if_set_up()};  // and the workspace, outgrown ones that graphs use included
     {
         std::lock_guard<std::mutex> lock(g_mu);
         auto it = g_ws.find(std::make_pair(dev, stream));
-        if (it != g_ws.end()) words[0] = it->second.ptr;
+        if (it != g_ws.end()) {
+            words.push_back(it->second.ptr);
+            words.insert(words.end(), it->second.old_headers.begin(), it->second.old_headers.end());
+        }
     }
     int32_t word = 0;
     for (void* ptr : words) {

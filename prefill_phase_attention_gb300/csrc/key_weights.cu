@@ -799,8 +799,10 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             ++ns;
             tc_fence_after();
             float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-            if (__all_sync(0xffffffffu, n == kBlockN && (!has || (lo <= 0 && hi >= n)))) {
-                // 32 columns are summed while the next 32 are on their way
+            if (__all_sync(0xffffffffu, n > kBlockN - 32 && (!has || (lo <= 0 && hi >= n)))) {
+                // 32 columns are summed while the next 32 are on their way; of the
+                // last 32, those past n (a group that does not divide 128) become 0,
+                // and their lse is infinite
                 const float2 mul2 = make_float2(mul, mul);
                 uint32_t v[2][32];
                 tmem_ld32(col, v[0]);
@@ -815,6 +817,11 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&ctl->s_empty[group]);
+                        if (n < kBlockN) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (c + e >= n) x[e] = 0;
+                        }
                     }
 #pragma unroll
                     for (int e = 0; e < 32; e += 4) {

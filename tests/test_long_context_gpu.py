@@ -500,3 +500,183 @@ def test_key_weights_of_mixed_queries(d, block, int8):
     c = Call(120, new, lens, d, 2, 4, block, int8)
     weigh(c)
     ok()
+
+
+@pytest.mark.parametrize("group", [3, 5, 7, 48])
+def test_key_weights_of_groups_that_do_not_divide_a_tile(group):
+    """126, 125, 126 and 96 rows in a Q tile; the queries' tails are cut at other places than tokens of 128 rows."""
+    c = Call(121, [300, 64, 1], [5, 200, 90], 64, 1, group)
+    weigh(c)
+    ok()
+
+
+def test_prefix_with_more_units_than_ctas():
+    """Whole rounds of prefix units stay uncut, the last round is cut into pieces."""
+    c = Call(122, [300, 1, 601], [0, 70, 5], 32, 64, 1, prefix=1111)
+    c.prefix()
+    c.check()
+    ok()
+
+
+# --------------------------------------------------------------------------- streams, graphs, large caches
+
+def run_all(c, d, st=None):
+    """Every long-context call once, on stream st, on the tensors in d; returns what they wrote."""
+    kw = dict(scale=c.scale, stream=st, **c.opts)
+    args = (d["q"], d["k"], d["v"], *c.meta, d["ck"], d["cv"], c.offsets)
+    binding.prefill_attn_varlen_sinks(*args, d["out"], d["lse"], window=90, sink_tokens=4, **kw)
+    binding.prefill_attn_varlen_prefix(*args, d["out2"], d["lse2"], **c.pre, **kw)
+    binding.prefill_attn_key_weights(d["q"], d["k"], *c.meta, d["ck"], c.offsets, d["lse"], d["w"], window=90, sink_tokens=4, **kw)
+    binding.prefill_attn_evict(d["ck"], d["cv"], d["w"], c.offsets, d["kept"], d["index"], d["kw"], budget=60, sink_tokens=4,
+                               recent_tokens=8, stream=st, **c.opts)
+
+
+def tensors(c):
+    d = dict(zip("qkv", (x.clone() for x in c.dev)))
+    d.update(ck=c.cache.data[0].cuda(), cv=c.cache.data[1].cuda(), w=c.weights.cuda(), kw=c.weights.cuda() * 0)
+    d.update(out=torch.zeros_like(d["q"]), out2=torch.zeros_like(d["q"]), kept=torch.zeros_like(c.offsets))
+    d.update(lse=torch.zeros(d["q"].shape[:2], device="cuda"), lse2=torch.zeros(d["q"].shape[:2], device="cuda"))
+    d.update(index=torch.zeros((len(c.lens), c.hk, 60), dtype=torch.int32, device="cuda"))
+    return d
+
+
+def same(a, b):
+    for name in a:
+        assert torch.equal(R.bits(a[name]), R.bits(b[name])), name
+
+
+@pytest.mark.parametrize("block", [0, 16])
+def test_graph_replay_gives_the_bits_of_an_eager_call(block):
+    """The calls captured once and replayed on other data, between eager calls that outgrow the workspace."""
+    st = torch.cuda.Stream()
+    mk = lambda seed: Call(seed, [1, 40, 0, 3], [300, 10, 5, 128], 64, 2, 2, block, prefix=200)  # noqa: E731
+    c, other = mk(130), mk(131)
+    held, start = tensors(c), tensors(c)
+    with torch.cuda.stream(st):
+        run_all(c, tensors(c), st)  # sizes the workspace
+    st.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        run_all(c, held, st)
+    want = tensors(c)
+    run_all(c, want)  # eager, on the default stream's own workspace
+    for _ in range(2):
+        for name in start:
+            held[name].copy_(start[name])
+        g.replay()
+        torch.cuda.synchronize()
+        same(held, want)
+        # larger calls on the graph's stream: its workspace is outgrown, not freed
+        big = Call(132, [1] * 90, [200 + i for i in range(90)], 64, 2, 2, block, prefix=900)
+        with torch.cuda.stream(st):
+            big.sinks(100, 4, stream=st)
+            big.prefix(stream=st)
+        st.synchronize()
+        big.check()
+    if not block:  # other data in the captured buffers (a paged call's table would be another)
+        for k, t in c.pre.items():
+            if torch.is_tensor(t):
+                t.copy_(other.pre[k])
+        want = tensors(other)
+        for name, t in tensors(other).items():
+            held[name].copy_(t)
+        run_all(c, want)
+        g.replay()
+        torch.cuda.synchronize()
+        same(held, want)
+    with torch.cuda.stream(st):
+        assert binding.prefill_attn_device_status(st) == 0
+    ok()
+
+
+@pytest.mark.filterwarnings("ignore:The CUDA Graph is empty")
+@pytest.mark.parametrize("call", ["sinks", "prefix", "weights"])
+def test_capture_on_a_fresh_stream_is_refused(call):
+    c = Call(133, [1, 40], [300, 10], 64, 2, 2, prefix=100 if call == "prefix" else 0)
+    d = tensors(c)
+    st = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with pytest.raises(binding.PrefillAttnError) as err:
+        with torch.cuda.graph(g, stream=st):
+            if call == "weights":
+                binding.prefill_attn_key_weights(d["q"], d["k"], *c.meta, d["ck"], c.offsets, d["lse"], d["w"], stream=st)
+            else:
+                getattr(c, call)(*((64, 4) if call == "sinks" else ()), stream=st)
+    assert err.value.status == 2 and "graph capture" in str(err.value)
+    if call != "weights":
+        getattr(c, call)(*((64, 4) if call == "sinks" else ()), stream=st)
+        torch.cuda.synchronize()
+        c.check(**(dict(window=64, sinks=4) if call == "sinks" else {}))
+
+
+def test_two_streams_at_once():
+    """Calls on two streams have workspaces of their own."""
+    cs = [Call(134 + i, [1, 50], [2000, 30], 128, 2, 4, prefix=300) for i in range(2)]
+    wants = [tensors(c) for c in cs]
+    for c, w in zip(cs, wants):
+        run_all(c, w)
+    torch.cuda.synchronize()
+    got, sts = [tensors(c) for c in cs], [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for c, d, st in zip(cs, got, sts):
+        with torch.cuda.stream(st):
+            run_all(c, d, st)
+    torch.cuda.synchronize()
+    for d, w in zip(got, wants):
+        same(d, w)
+
+
+def large_caches(c):
+    """c's caches inside ones of more than 2^32 bytes, in use at the far end: (K, V, place, back); place(t, x) copies
+    x to where a tensor of the large caches' rows has it, back(t) is that part of t."""
+    hk, d = c.hk, c.d
+    if c.cache.block:
+        first = 8400  # blocks ahead of the ones in use
+        shape = (first + c.cache.shape[0], hk, c.cache.block, d)
+        c.opts["block_table"] = c.opts["block_table"] + first
+        back = lambda t: t[first:]  # noqa: E731
+    else:
+        shape, cap = (2, hk, 1_100_000, d), c.cache.shape[2]
+        back = lambda t: t[:, :, :cap]  # noqa: E731
+    assert math.prod(shape) * 2 > 2 ** 32
+    place = lambda t, x: back(t).copy_(x)  # noqa: E731
+    big = [torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for t, x in zip(big, c.cache.data):
+        place(t, x.cuda())
+    return *big, place, back
+
+
+@pytest.mark.parametrize("block,prefix", [(0, 0), (256, 0), (0, 150)])
+def test_caches_past_four_gigabytes(block, prefix):
+    """The last slot (or the last blocks) of a cache lies more than 2^32 bytes from its start."""
+    new, lens = [3, 1], [700, 300]
+    c = Call(140, new, lens, 128, 8, 2, block, prefix=prefix)
+    ck, cv, place, back = large_caches(c)
+    args = (*c.dev, *c.meta, ck, cv, c.offsets, c.out[1], c.lse[1])
+    if prefix:
+        binding.prefill_attn_varlen_prefix(*args, scale=c.scale, **c.opts, **c.pre)
+    else:
+        binding.prefill_attn_varlen_sinks(*args, window=90, sink_tokens=4, scale=c.scale, **c.opts)
+    for own, big in zip(c.data, (ck, cv)):
+        own[1].copy_(back(big))
+    c.check(**({} if prefix else dict(window=90, sinks=4)))
+    if prefix:
+        return
+    weights = torch.zeros(ck.shape[:-1], device="cuda")
+    place(weights, c.weights.cuda())
+    lse = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale)[1].float()
+    binding.prefill_attn_key_weights(c.dev[0], c.dev[1], *c.meta, ck, c.offsets, lse.cuda(), weights, scale=c.scale, **c.opts)
+    ref = R.key_weights(c.cache, c.q, c.k, c.new, lse, c.scale, c.weights)
+    assert ((back(weights).cpu().double() - ref).abs() <= R.SCORE * 2 * ref.abs() + 1e-6).all()
+    kept, index = torch.zeros_like(c.offsets), torch.zeros((2, c.hk, 200), dtype=torch.int32, device="cuda")
+    now = back(weights).cpu()
+    binding.prefill_attn_evict(ck, cv, weights, c.offsets, kept, index, weights, budget=200, sink_tokens=4,
+                               recent_tokens=16, **c.opts)
+    moved = back(cv).cpu()
+    for b, n in enumerate(lens):
+        slot, row = c.cache.at(b, torch.arange(n))
+        for h in (0, c.hk - 1):
+            keep = R.evicted(now[slot, h, row], 200, 4, 16)
+            assert torch.equal(index[b, h].cpu().long(), keep)
+            assert torch.equal(R.bits(moved[slot[:200], h, row[:200]]), R.bits(c.cache.data[1][slot[keep], h, row[keep]]))
+    ok()
