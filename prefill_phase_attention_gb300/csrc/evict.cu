@@ -25,7 +25,7 @@
 // is bound by latency: evict_kernel does both in one launch, a cluster of 2, 4
 // or 8 CTAs (its column parts) per (sequence, head).  A larger one is bound by
 // HBM, and a CTA that selects moves no bytes: select_kernel runs first, one CTA
-// of 1024 threads (or a cluster) per (sequence, head), then move_kernel.
+// (or a cluster) per (sequence, head), then move_kernel.
 #include <cooperative_groups.h>
 
 #include <cstdint>
@@ -41,11 +41,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVec = 4;  // 16-byte pieces per thread and chunk of the move
+constexpr int kVec = 2;  // 16-byte pieces per thread and chunk of the move
 // one-launch form: threads, weights a thread holds (so tokens a CTA selects from alone)
 constexpr int kFusedThreads = 512, kFusedHeld = 8;
-// two-launch form
-constexpr int kSelectThreads = 512, kSelectHeld = 16, kMoveThreads = 256;
+// two-launch form: select CTAs of 256 threads for caches of up to 8192 tokens a
+// slot, of 512 for longer ones (64 sequences of 700-4099 tokens in int8 pages:
+// 72.8 us with 256, 81.6 with 512; 16 of 16384 tokens: 120.7 and 116.7)
+constexpr int kSelectHeld = 16, kMoveThreads = 256;
 constexpr int kScalars = 8;  // weights or scales a thread moves per chunk
 // Weights crowd into a few digits: a histogram has this many copies, one per
 // lane & 7, a bank apart, so that a warp's equal digits do not queue up.
@@ -404,7 +406,8 @@ __global__ void __launch_bounds__(kFusedThreads, 2) evict_kernel(const __grid_co
     if (len > a.budget) move_rows<kFusedThreads>(a, b, h, a.budget, rank & 1, rank >> 1, list);
 }
 
-__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_constant__ EvictArgs a) {
+template <int kSelectThreads>
+__global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) select_kernel(const __grid_constant__ EvictArgs a) {
     __shared__ Shared<kSelectThreads, kSelectHeld> sh;
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -424,7 +427,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_
                                         rank == min(2, ranks - 1));
 }
 
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a, int log_parts) {
+__global__ void __launch_bounds__(kMoveThreads, 7) move_kernel(const __grid_constant__ EvictArgs a, int log_parts) {
     const int part = blockIdx.x & ((1 << log_parts) - 1), which = (blockIdx.x >> log_parts) & 1;
     const int bh = blockIdx.x >> (log_parts + 1), h = bh % a.n_kv_heads, b = bh / a.n_kv_heads;
     const int len = checked_length<kMoveThreads>(a, b);
@@ -453,12 +456,13 @@ cudaError_t launch_evict(const EvictArgs& args, int sms, int* launches, cudaStre
         *launches = 1;
         return cudaLaunchKernelEx(&cfg, evict_kernel, a);
     }
+    const int threads = a.max_cache_len <= 2 * 256 * kSelectHeld ? 256 : 512;
     int ranks = 1;
-    while (ranks < 8 && a.max_cache_len > ranks * kSelectThreads * kSelectHeld) ranks *= 2;
+    while (ranks < 8 && a.max_cache_len > ranks * threads * kSelectHeld) ranks *= 2;
     attr[0].val.clusterDim.x = (unsigned)ranks;
     cfg.gridDim = dim3((unsigned)(ranks * heads));
-    cfg.blockDim = dim3(kSelectThreads);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, a);
+    cfg.blockDim = dim3((unsigned)threads);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, threads == 256 ? select_kernel<256> : select_kernel<512>, a);
     if (e != cudaSuccess) return e;
     int log_parts = 0;
     while ((1 << log_parts) < parts) ++log_parts;
