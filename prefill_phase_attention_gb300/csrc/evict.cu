@@ -43,7 +43,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kVec = 2;  // 16-byte pieces per thread and chunk of the move
 // one-launch form: threads, weights a thread holds (so tokens a CTA selects from alone)
-constexpr int kFusedThreads = 512, kFusedHeld = 8;
+constexpr int kFusedThreads = 256, kFusedHeld = 8;
 // two-launch form: select CTAs of 256 threads for caches of up to 8192 tokens a
 // slot, of 512 for longer ones (64 sequences of 700-4099 tokens in int8 pages:
 // 72.8 us with 256, 81.6 with 512; 16 of 16384 tokens: 120.7 and 116.7)
@@ -386,7 +386,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int b, int h, int 
     }
 }
 
-__global__ void __launch_bounds__(kFusedThreads, 2) evict_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kFusedThreads, 4) evict_kernel(const __grid_constant__ EvictArgs a) {
     __shared__ Shared<kFusedThreads, kFusedHeld> sh;
     __shared__ int s_list[kFusedThreads * kFusedHeld];
     const cg::cluster_group cluster = cg::this_cluster();

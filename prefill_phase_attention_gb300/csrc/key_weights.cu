@@ -55,7 +55,7 @@ namespace {
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
 constexpr int kThreads = 640;
 constexpr int kLse = 3;      // Q tiles whose lse is staged
-constexpr int kMaxRun = 8;   // key tiles of a unit of a one-Q-tile sequence, at most
+constexpr int kMaxRun = 32;  // key tiles of a unit of a one-Q-tile sequence, at most
 constexpr int kGroups = 4;   // groups of sum warps = S buffers = key tiles of a wide unit, at most
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -212,13 +212,6 @@ __device__ __forceinline__ KeyTile key_tile_at(const SeqGeo& g, const SeqInfo& s
     return k;
 }
 
-// Whether some query of tokens [qs, qe) sees some key of the tile.
-__device__ __forceinline__ bool tile_seen(const KeyTile& k, int P, int qs, int qe, int causal, int window, int sinks) {
-    if (!causal) return true;
-    if (P + qe - 1 < k.lo) return false;
-    return window == 0 || P + qs - (k.hi - 1) < window || k.lo < sinks;
-}
-
 // Q tiles [lo, hi) that see one of the key tiles first .. last of a unit.
 struct QRange {
     int lo, hi;
@@ -236,16 +229,27 @@ __device__ __forceinline__ QRange unit_queries(const KeyTile& first, const KeyTi
     return r;
 }
 
+// Q tiles [lo, hi) all of whose 128 columns count for every key of the tile.
+__device__ __forceinline__ QRange full_queries(const KeyTile& k, const SeqInfo& s, int tps, int group, int causal,
+                                               int window, int sinks) {
+    QRange r{0, tps * group > kBlockN - 32 ? s.n / tps : 0};
+    if (!causal) return r;
+    if (k.hi - 1 > s.P) r.lo = (k.hi - 1 - s.P + tps - 1) / tps;
+    if (window > 0 && k.hi > sinks) r.hi = min(r.hi, max(0, window + k.lo - s.P) / tps);
+    return r;
+}
+
 // Key tiles of a unit of several Q tiles: four, or two where four would make fewer
 // units than two per CTA (wide_tiles: the key tiles x KV heads of such sequences).
 __device__ __forceinline__ int wide_length(unsigned long long wide_tiles, int num_ctas) {
     return wide_tiles >= 2ull * kGroups * (unsigned)num_ctas ? kGroups : 2;
 }
 
-// Key tiles of a unit of a sequence whose queries fit one Q tile: about eight
-// units per CTA of the `total` tiles of all of them.
+// Key tiles of a unit of a sequence whose queries fit one Q tile: about three
+// units per CTA of the `total` tiles of all of them (64 decode rows over 256-4096
+// cached tokens: 55.0 us; 55.9 with four, 60.9 with eight, 56.4 with two).
 __device__ __forceinline__ int run_length(unsigned long long total, int num_ctas) {
-    const unsigned long long per = total / (8u * (unsigned)num_ctas);
+    const unsigned long long per = total / (3u * (unsigned)num_ctas);
     return per >= kMaxRun ? kMaxRun : (per < 2 ? 2 : (int)per & ~1);
 }
 
@@ -480,8 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         return unit_queries(key_tile_at<kPaged>(g, s, u.q0), key_tile_at<kPaged>(g, s, u.q0 + u.ntiles - 1), s, g.nq, tps,
                             p.causal, p.window, p.sinks);
     };
-    auto seen = [&](const KeyTile& k, const SeqInfo& s, int q0, int qe) {
-        return tile_seen(k, s.P, q0, qe, p.causal, p.window, p.sinks);
+    // The Q tiles that see one key tile.
+    auto seen_by = [&](const SeqGeo& g, const SeqInfo& s, const KeyTile& k) {
+        return unit_queries(k, k, s, g.nq, tps, p.causal, p.window, p.sinks);
     };
     auto geo = [&](const SeqInfo& s) { return seq_geo(s, tps, p.causal, p.window, p.sinks, kPaged); };
 
@@ -599,15 +604,14 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         const uint64_t desc = smem_desc(addr, 16, C::kSbo, C::kSw);
         const uint64_t desc_g = smem_desc(addr, 16, C::kGrpSbo, C::kSw);  // staged block by block
         Ring ring(C::kStages);
-        uint32_t used[2] = {0, 0};   // uses so far of S buffers me, me + 2
-        uint32_t nconv[2] = {0, 0};  // tiles expanded by those groups
+        uint32_t used = 0;   // bit i: parity of the uses so far of S buffer me + 2 i
+        uint32_t convs = 0;  // bit i: parity of the tiles expanded by group me + 2 i
         uint32_t nn = 0;             // tiles of one-Q-tile units so far
         bool ok = true;
         // S^T of the key tile at stage kst and the Q tile at stage qst into buffer buf
         auto issue = [&](int buf, int kst, bool grp, int qst, int cols) -> bool {
-            uint32_t& n = used[buf >> 1];
-            if (!warp_wait(&ctl->s_empty[buf], (n & 1) ^ 1, ctl, hdr)) return false;
-            ++n;
+            if (!warp_wait(&ctl->s_empty[buf], ((used >> (buf >> 1)) & 1) ^ 1, ctl, hdr)) return false;
+            used ^= 1u << (buf >> 1);
             tc_fence_after();
             // columns in use, rounded up to what an M = 128 MMA takes
             const uint32_t idesc = idesc_bf16_f32(kBlockM, 0, 0, 0) | ((uint32_t)((cols + 15) / 16) * 2 << 17);
@@ -629,8 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         // the key tile of group grp at stage st: landed, and expanded if it was codes
         auto wait_key = [&](int grp, bool codes, int st, uint32_t par) -> bool {
             if (!(kQuant && codes)) return warp_wait(&ctl->full[st], par, ctl, hdr);
-            const bool got = warp_wait(&ctl->conv[grp], nconv[grp >> 1] & 1, ctl, hdr);
-            ++nconv[grp >> 1];
+            const bool got = warp_wait(&ctl->conv[grp], (convs >> (grp >> 1)) & 1, ctl, hdr);
+            convs ^= 1u << (grp >> 1);
             return got;
         };
         auto release = [&](int st, bool mine) {
@@ -665,32 +669,33 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             const int nt = us.u.ntiles;
             const bool four = nt > 2;
             const QRange qr = queries(g, s, us.u);
-            int kst[kGroups];
-            KeyTile kt[2];  // of this issuer: tiles me and me + 2
+            int kst[kGroups], st[2] = {0, 0};  // stages of the unit's tiles, of this issuer's tiles me and me + 2
+            QRange mine[2] = {{0, 0}, {0, 0}};  // the Q tiles that see those
+            bool grp[2] = {false, false};
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
                 kst[i] = 0;
                 if (i >= nt) continue;
                 kst[i] = ring.next(true, par);
-                const KeyTile k = key_tile_at<kPaged>(g, s, us.u.q0 + i);
                 if ((i & 1) == me) {
-                    kt[i >> 1] = k;
+                    const KeyTile k = key_tile_at<kPaged>(g, s, us.u.q0 + i);
+                    st[i >> 1] = kst[i];
+                    mine[i >> 1] = seen_by(g, s, k);
+                    grp[i >> 1] = kGrp && k.jt < g.np;
                     ok = ok && wait_key(i, k.jt < g.np, kst[i], par);
                 } else {
                     ok = ok && warp_wait(&ctl->full[kst[i]], par, ctl, hdr);
                 }
             }
             for (int qi = qr.lo; qi < qr.hi && ok; ++qi) {
-                const int q0 = qi * tps, qe = min(q0 + tps, s.n);
+                const int cols = min(tps, s.n - qi * tps) * G;
                 const int qst = ring.next(false, par);
                 if (!warp_wait(&ctl->full[qst], par, ctl, hdr)) { ok = false; break; }
                 bool any = false;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int t = me + 2 * i;  // tile of the unit
-                    if (t >= nt || !seen(kt[i], s, q0, qe) || !ok) continue;
-                    ok = issue(four ? t : t + 2 * (qi & 1), i ? (me ? kst[3] : kst[2]) : (me ? kst[1] : kst[0]), kGrp && kt[i].jt < g.np, qst,
-                               (qe - q0) * G);
+                    if (qi < mine[i].lo || qi >= mine[i].hi || !ok) continue;
+                    ok = issue(four ? me + 2 * i : me + 2 * (qi & 1), st[i], grp[i], qst, cols);
                     any = true;
                 }
                 if (ok) release(qst, any);
@@ -752,9 +757,19 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
         const int r = sp * 32 + lane;  // row of the key tile == TMEM lane
         const uint32_t col = tmem + ((uint32_t)(sp * 32) << 16) + group * 128;
         Ring ring(C::kStages);
-        uint32_t lq = 0, ns = 0, nn = 0;  // Q tiles; S tiles of this group; tiles of one-Q-tile units (of every group)
+        int lst = 0;                      // lse stage of the Q tile, and the parity of its use
+        uint32_t lpar = 0, ns = 0, nn = 0;  // ns: S tiles of this group; nn: tiles of one-Q-tile units (of every group)
         uint32_t npair = 0, nread = 0;    // exchanges between two groups; tiles expanded
         bool ok = true;
+        // done with the Q tile's lse
+        auto next_lse = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->l_empty[lst]);
+            if (++lst == kLse) {
+                lst = 0;
+                lpar ^= 1;
+            }
+        };
         // where the weight (and the scale) of key j of a tile of (b, kvh) lies
         auto weight_row = [&](const Unit& u, int j) -> size_t {
             if (kPaged) {
@@ -792,14 +807,14 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             if (lane == 0) mbar_arrive(&ctl->conv[group]);
             return true;
         };
-        // Adds to `total` the exp2s of this group's next S tile: n columns, of which
-        // this thread's key takes [lo, hi).
-        auto add_tile = [&](const float* nl, int n, int lo, int hi, bool has, float mul, float& total) -> bool {
+        // Adds to `total` the exp2s of this group's next S tile: n columns, all of
+        // them (whole), or of which this thread's key takes [lo, hi).
+        auto add_tile = [&](const float* nl, int n, bool whole, int lo, int hi, float mul, float& total) -> bool {
             if (!warp_wait(&ctl->s_full[group], ns & 1, ctl, hdr)) return false;
             ++ns;
             tc_fence_after();
             float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-            if (__all_sync(0xffffffffu, n > kBlockN - 32 && (!has || (lo <= 0 && hi >= n)))) {
+            if (whole) {
                 // 32 columns are summed while the next 32 are on their way; of the
                 // last 32, those past n (a group that does not divide 128) become 0,
                 // and their lse is infinite
@@ -886,20 +901,20 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             const Unit u = us.u;
             const SeqGeo g = geo(s);
             uint32_t par;
-            ring.unit();
+            if (kQuant) ring.unit();
             if (g.nq == 1) {
                 // every fourth tile is this group's; its next tile's weights are
                 // fetched one tile ahead
-                ring.next(true, par);
-                if (!warp_wait(&ctl->l_full[lq % kLse], (lq / kLse) & 1, ctl, hdr)) break;
-                const float* nl = ctl->neg_lse[lq % kLse];
+                if (kQuant) ring.next(true, par);
+                if (!warp_wait(&ctl->l_full[lst], lpar, ctl, hdr)) break;
+                const float* nl = ctl->neg_lse[lst];
                 const int end = u.q0 + u.ntiles;
                 int mine = u.q0 + (int)((group - nn) & 3);
                 size_t row = 0, next_row = 0;
                 float old = 0.f, next_old = 0.f, mul = 0.f, next_mul = 0.f;
                 bool has = mine < end && fetch(u, g, key_tile_at<kPaged>(g, s, mine), row, old, mul), next_has = false;
                 for (int x = u.q0; x < end; ++x, ++nn) {
-                    const int kst = ring.next(false, par);
+                    const int kst = kQuant ? ring.next(false, par) : 0;
                     if (x != mine) continue;
                     mine += 4;
                     next_has = mine < end && fetch(u, g, key_tile_at<kPaged>(g, s, mine), next_row, next_old, next_mul);
@@ -908,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
                     int lo, hi;
                     columns(s, k.kb + r, 0, s.n * G, lo, hi);
                     float total = 0.f;
-                    if (!add_tile(nl, s.n * G, lo, hi, has, mul, total)) { ok = false; break; }
+                    if (!add_tile(nl, s.n * G, false, lo, hi, mul, total)) { ok = false; break; }
                     if (has) p.weights[row] = old + total;
                     row = next_row;
                     has = next_has;
@@ -916,9 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
                     mul = next_mul;
                 }
                 if (!ok) break;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->l_empty[lq % kLse]);
-                ++lq;
+                next_lse();
                 continue;
             }
             const int nt = u.ntiles;
@@ -930,25 +943,27 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             size_t row = 0;
             float old = 0.f, mul = 0.f, total = 0.f;
             const bool has = here && fetch(u, g, k, row, old, mul);
-            for (int i = 0; i < nt; ++i) {
-                const int st = ring.next(true, par);
-                if (kQuant && i == t && (four || turn == 0) && k.jt < g.np && !expand(st, par)) { ok = false; break; }
-            }
-            for (int qi = qr.lo; qi < qr.hi && ok; ++qi) {
-                const int q0 = qi * tps, qe = min(q0 + tps, s.n), cols = (qe - q0) * G;
-                ring.next(false, par);
-                if (here && (four || (qi & 1) == turn) && seen(k, s, q0, qe)) {
-                    if (!warp_wait(&ctl->l_full[lq % kLse], (lq / kLse) & 1, ctl, hdr)) { ok = false; break; }
-                    int lo, hi;
-                    columns(s, k.kb + r, q0, cols, lo, hi);
-                    if (!add_tile(ctl->neg_lse[lq % kLse], cols, lo, hi, has, mul, total)) { ok = false; break; }
-                } else if (!warp_wait(&ctl->l_full[lq % kLse], (lq / kLse) & 1, ctl, hdr)) {
-                    ok = false;
-                    break;
+            if (kQuant) {
+                for (int i = 0; i < nt; ++i) {
+                    const int st = ring.next(true, par);
+                    if (i == t && (four || turn == 0) && k.jt < g.np && !expand(st, par)) { ok = false; break; }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->l_empty[lq % kLse]);
-                ++lq;
+            }
+            const QRange mine = here ? seen_by(g, s, k) : QRange{0, 0};
+            const QRange full = full_queries(k, s, tps, G, p.causal, p.window, p.sinks);
+            for (int qi = qr.lo; qi < qr.hi && ok; ++qi) {
+                if (kQuant) ring.next(false, par);
+                ok = warp_wait(&ctl->l_full[lst], lpar, ctl, hdr);
+                if (!ok) break;
+                if (qi >= mine.lo && qi < mine.hi && (four || (qi & 1) == turn)) {
+                    const int q0 = qi * tps, cols = min(tps, s.n - q0) * G;
+                    int lo = 0, hi = 0;
+                    const bool whole = qi >= full.lo && qi < full.hi;
+                    if (!whole) columns(s, k.kb + r, q0, cols, lo, hi);
+                    ok = add_tile(ctl->neg_lse[lst], cols, whole, lo, hi, mul, total);
+                    if (!ok) break;
+                }
+                next_lse();
             }
             if (!ok) break;
             if (!four && here) {
