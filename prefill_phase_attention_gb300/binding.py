@@ -300,6 +300,13 @@ def _pointers(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offse
             cache_offsets.numel(), t, cap, h, k.shape[1], d, d ** -0.5 if scale is None else scale)
 
 
+def _int32(**values) -> None:
+    """The C calls take 32-bit integers, and ctypes cuts larger ones off without a word."""
+    for name, v in values.items():
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
 def _options(cache_k, block_table, cache_k_scale, cache_v_scale, window=0, rope_theta=0.0, schedule=0):
     """pa_options by position (struct_size, window, block_table, block_size, max_blocks_per_seq, num_blocks, ...)."""
     paged, quant = block_table is not None, cache_k_scale is not None
@@ -321,6 +328,7 @@ def prefill_attn_varlen_sinks(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cach
     The query at absolute position p sees key j when j <= p and (j > p - window or
     j < sink_tokens).  Tensors and options as in prefill_attn_varlen_ex.
     """
+    _int32(window=window, sink_tokens=sink_tokens)
     device, cap, _, _ = _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse,
                                         block_table, cache_k_scale, cache_v_scale)
     _check((_lib or load()).prefill_attn_varlen_sinks(
@@ -371,6 +379,7 @@ def prefill_attn_varlen_prefix(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cac
                     raise ValueError(f"an int8 cache needs {name}")
                 _check_tensors(device, (name, t, _F32, rows))
             pre.k_scale, pre.v_scale = prefix_k_scale.data_ptr(), prefix_v_scale.data_ptr()
+    _int32(prefix_len=prefix_len)
     pre.len = prefix_len
     _check((_lib or load()).prefill_attn_varlen_prefix(
         *_pointers(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, cap, scale),
@@ -390,6 +399,7 @@ def prefill_attn_key_weights(q, k, cu_seqlens_q, cu_seqlens_k, cache_k, cache_of
     """
     if lse is None:
         raise ValueError("prefill_attn_key_weights needs lse")
+    _int32(window=window, sink_tokens=sink_tokens, prefix_len=prefix_len)
     device, cap, _, rows = _attention_args(q, k, None, cu_seqlens_q, cu_seqlens_k, cache_k, None, cache_offsets, None, lse,
                                            block_table, cache_k_scale, cache_k_scale)
     _check_tensors(device, ("weights", weights, _F32, rows))
@@ -412,6 +422,7 @@ def prefill_attn_evict(cache_k, cache_v, weights, lengths, kept_lengths, kept_in
     lengths / kept_lengths int32 [num_seqs]; kept_index int32 [num_seqs, n_kv_heads, budget] or
     None; weights / kept_weights fp32 of shape cache_k.shape[:-1] (kept_weights may be weights).
     """
+    _int32(budget=budget, sink_tokens=sink_tokens, recent_tokens=recent_tokens)
     device = _current_device(cache_k)
     if cache_k.dim() != 4:
         raise ValueError("caches are [num_seqs, kv_heads, cap, head_dim]")

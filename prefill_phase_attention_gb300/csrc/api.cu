@@ -1140,6 +1140,12 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
         return fail(PA_ERR_INVALID_ARG, "kept_lengths must not overlap lengths");
     const size_t rows = o.block_table ? (size_t)o.num_blocks * n_kv_heads * o.block_size : (size_t)heads * max_cache_len;
     const size_t row_bytes = o.kv_quant ? head_dim : 2 * head_dim;
+    const size_t index_bytes = (size_t)heads * budget * sizeof(int);
+    if (kept_index && (overlap(kept_index, index_bytes, weights, rows * 4) ||
+                       overlap(kept_index, index_bytes, lengths, (size_t)num_seqs * 4) ||
+                       overlap(kept_index, index_bytes, kept_lengths, (size_t)num_seqs * 4) ||
+                       (kept_weights && overlap(kept_index, index_bytes, kept_weights, rows * 4))))
+        return fail(PA_ERR_INVALID_ARG, "kept_index must not overlap the weights or the lengths");
     if (kept_weights && kept_weights != weights && overlap(weights, rows * 4, kept_weights, rows * 4))
         return fail(PA_ERR_INVALID_ARG, "kept_weights must be weights itself or not overlap it");
     if (overlap(cache_k, rows * row_bytes, cache_v, rows * row_bytes))
@@ -1155,7 +1161,7 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     if (s != PA_OK) return s;
     void* aux = nullptr;
     if (!kept_index) {
-        s = get_aux_scratch(ws, dev, stream, (size_t)heads * budget * sizeof(int), &aux);
+        s = get_aux_scratch(ws, dev, stream, index_bytes, &aux);
         if (s != PA_OK) return s;
     }
     pa::EvictArgs a;

@@ -137,6 +137,8 @@ def test_key_weights_refusals(lib, kw, status, msg):
     (dict(new=1 << 20), 1, "kept_lengths must not overlap"),
     (dict(kept_w=(1 << 24) + 4), 1, "kept_weights must be"),
     (dict(index=2), 1, "4-byte"),
+    (dict(index=(1 << 24) + 8), 1, "kept_index must not overlap"),
+    (dict(index=1 << 21), 1, "kept_index must not overlap"),
     (dict(cv=1 << 25), 1, "cache_k and cache_v"),
     (dict(o=dict(window=4)), 1, "window"),
     (dict(o=dict(rope_theta=1e4)), 1, "rope_theta"),
@@ -170,3 +172,13 @@ def test_bindings_refuse_cpu_tensors(lib):
         binding.prefill_attn_key_weights(x, x, i, i, x[None], i[:1], w[0], w)
     with pytest.raises(ValueError):
         binding.prefill_attn_evict(x[None], x[None], w, i[:1], i[:1].clone(), budget=2)
+
+
+def test_bindings_refuse_integers_past_32_bits(lib):
+    """ctypes would cut them off: 2^32 + 5 tokens of budget would become 5."""
+    x = torch.zeros(4, 2, 32, dtype=torch.bfloat16)
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="sink_tokens"):
+        binding.prefill_attn_varlen_sinks(x, x, x, i, i, x[None], x[None], i[:1], x, window=4, sink_tokens=1 << 32)
+    with pytest.raises(ValueError, match="budget"):
+        binding.prefill_attn_evict(x[None], x[None], torch.zeros(1, 4, 2), i[:1], i[:1].clone(), budget=(1 << 32) + 5)

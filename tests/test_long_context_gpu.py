@@ -680,3 +680,21 @@ def test_caches_past_four_gigabytes(block, prefix):
             assert torch.equal(index[b, h].cpu().long(), keep)
             assert torch.equal(R.bits(moved[slot[:200], h, row[:200]]), R.bits(c.cache.data[1][slot[keep], h, row[keep]]))
     ok()
+
+
+@pytest.mark.parametrize("call", ["sinks", "prefix"])
+def test_without_lse(call):
+    """lse is optional, whether units write out themselves or a merge does."""
+    c = Call(150, [1, 40], [2000, 10], 64, 2, 2, prefix=300 if call == "prefix" else 0)
+    args = c.tensors()[:-1]
+    if call == "sinks":
+        binding.prefill_attn_varlen_sinks(*args, window=1500, sink_tokens=4, scale=c.scale)
+    else:
+        binding.prefill_attn_varlen_prefix(*args, scale=c.scale, **c.pre)
+    torch.cuda.synchronize()
+    kw = dict(window=1500, sinks=4) if call == "sinks" else {}
+    ref, lse, _ = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale, **kw)
+    assert c.lse[1].isnan().all()
+    c.lse[1].copy_(lse)
+    c.check(**kw)
+    ok()
