@@ -216,11 +216,12 @@ def prefill_attn_varlen_ex(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v
     _check(load().prefill_attn_varlen_ex(*args[:-1], ctypes.byref(opts), args[-1]))
 
 
-# The long-context calls are often a few microseconds of GPU work: their checks
-# are one pass over (name, tensor, dtype, elements) with as few attribute reads
-# as they need.  The shapes of q, k and the caches are checked as such; the other
-# tensors are dense in the layout their documentation states, so that their
-# element count says whether they fit.
+# The long-context calls are often a few microseconds of GPU work, so their checks
+# read as few attributes as they need, as one expression where every call goes
+# through (0.3 us a tensor on the GPU's host; _check_tensors then names the
+# tensor that failed).  The shapes of q, k and the caches are checked as such;
+# the other tensors are dense in the layout their documentation states, so that
+# their element count says whether they fit.
 _BF16, _I8, _F32, _I32 = torch.bfloat16, torch.int8, torch.float32, torch.int32
 
 
@@ -273,7 +274,10 @@ def _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_
             raise ValueError("an int8 cache needs both cache_k_scale and cache_v_scale")
         dtype, quant = _I8, True
         _check_tensors(device, ("cache_k_scale", cache_k_scale, _F32, total), ("cache_v_scale", cache_v_scale, _F32, total))
-    _check_tensors(device, ("cache_k", cache_k, dtype, total * d), ("cache_v", cache_v, dtype, total * d))
+    cv = cache_k if cache_v is None else cache_v
+    if not (cache_k.dtype is dtype and cache_k.is_contiguous() and cache_k.get_device() == device
+            and cv.dtype is dtype and cv.numel() == total * d and cv.is_contiguous() and cv.get_device() == device):
+        _check_tensors(device, ("cache_k", cache_k, dtype, total * d), ("cache_v", cache_v, dtype, total * d))
     return cap, quant, total
 
 
@@ -287,9 +291,20 @@ def _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache
     if kt != t or kd != d:
         raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
     nq, nk = t * h * d, t * hk * d
-    _check_tensors(device, ("q", q, _BF16, nq), ("k", k, _BF16, nk), ("v", v, _BF16, nk), ("out", out, _BF16, nq),
-                   ("lse", lse, _F32, t * h), ("cu_seqlens_q", cu_seqlens_q, _I32, b + 1),
-                   ("cu_seqlens_k", cu_seqlens_k, _I32, b + 1), ("cache_offsets", cache_offsets, _I32, b))
+    vv, oo = k if v is None else v, q if out is None else out
+    if not (q.dtype is _BF16 and k.dtype is _BF16 and q.is_contiguous() and k.is_contiguous() and k.get_device() == device
+            and vv.dtype is _BF16 and vv.numel() == nk and vv.is_contiguous() and vv.get_device() == device
+            and oo.dtype is _BF16 and oo.numel() == nq and oo.is_contiguous() and oo.get_device() == device
+            and (lse is None or lse.dtype is _F32 and lse.numel() == t * h and lse.is_contiguous()
+                 and lse.get_device() == device)
+            and cu_seqlens_q.dtype is _I32 and cu_seqlens_q.numel() == b + 1 and cu_seqlens_q.is_contiguous()
+            and cu_seqlens_q.get_device() == device
+            and cu_seqlens_k.dtype is _I32 and cu_seqlens_k.numel() == b + 1 and cu_seqlens_k.is_contiguous()
+            and cu_seqlens_k.get_device() == device
+            and cache_offsets.dtype is _I32 and cache_offsets.is_contiguous() and cache_offsets.get_device() == device):
+        _check_tensors(device, ("q", q, _BF16, nq), ("k", k, _BF16, nk), ("v", v, _BF16, nk), ("out", out, _BF16, nq),
+                       ("lse", lse, _F32, t * h), ("cu_seqlens_q", cu_seqlens_q, _I32, b + 1),
+                       ("cu_seqlens_k", cu_seqlens_k, _I32, b + 1), ("cache_offsets", cache_offsets, _I32, b))
     return device, *_cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d)
 
 
@@ -303,7 +318,7 @@ def _pointers(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offse
 def _int32(**values) -> None:
     """The C calls take 32-bit integers, and ctypes cuts larger ones off without a word."""
     for name, v in values.items():
-        if not -0x80000000 <= v <= 0x7fffffff:
+        if v > 0x7fffffff or v < -0x80000000:
             raise ValueError(f"{name} = {v} does not fit 32 bits")
 
 

@@ -3,6 +3,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -810,6 +811,7 @@ pa_status read_prefix(const pa_prefix* prefix, const Options& o, Prefix* out) {
 constexpr long long kPartialBytes = 64ll << 20, kPrefixPartialBytes = 256ll << 20;
 using pa::kMaxPieces;
 constexpr int kMinPieceTiles = 4;
+constexpr int kUncutTiles = 8;
 constexpr int kPieceWaves = 2;
 
 pa_status check_unused(const Options& o, const char* what) {
@@ -841,7 +843,10 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     const long long slab_rows = (long long)total_q * n_heads;
     const long long slab_bytes = slab_rows * (head_dim + 1) * 4;
     const int fit = (int)std::max(1ll, std::min((long long)kMaxPieces, kPartialBytes / slab_bytes));
-    const int max_pieces = fit;
+    // a row under a short window is not cut: its few tiles cost less than the merge's
+    // launch (one row, window 256: 13.6 us whole, 14.7 in two pieces; 16 and 20 from Python)
+    const long long most_tiles = o.window ? ((long long)o.window + sinks) / pa::kBlockN + 3 : LLONG_MAX;
+    const int max_pieces = most_tiles <= kUncutTiles ? 1 : fit;
     // a prefix of fewer units than wanted is cut to make as many; of one with more
     // than CTAs only the units of the last round are, into at most four
     int max_prefix_pieces = 0;
@@ -889,7 +894,6 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     sa.prefix_table = pre.block_table;
     sa.max_pieces = max_pieces;
     sa.max_prefix_pieces = max_prefix_pieces;
-    sa.target_units = (int)target;
     sa.min_tiles = kMinPieceTiles;
     e = pa::launch_build_long_schedule(sa, stream);
     if (e != cudaSuccess) return cuda_fail(e, "schedule launch");

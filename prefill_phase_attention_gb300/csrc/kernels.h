@@ -119,8 +119,7 @@ struct LongScheduleArgs : ScheduleArgs {
     int prefix_len;
     const int32_t* prefix_table;
     int max_pieces, max_prefix_pieces;  // slabs the workspace has for each
-    int target_units;  // units wanted in flight (a multiple of the CTAs)
-    int min_tiles;     // no piece smaller than this is cut
+    int min_tiles;  // no piece smaller than this is cut
 };
 cudaError_t launch_build_long_schedule(const LongScheduleArgs& a, cudaStream_t stream);
 

@@ -8,7 +8,12 @@
 //    a few long rows still fill the GPU.  The pieces of a block write partial
 //    results (fp32 output and log-sum-exp) into slabs that merge_kernel joins.
 //
-// Piece size: the whole call's tiles over target_units, at least min_tiles.
+// Piece size (piece_tiles): with fewer units than CTAs, what makes one round of
+// pieces; else the whole call's tiles over twice the CTAs; at least min_tiles.  A
+// sequence that would gain less than kCutGain tiles by it is not cut, unless the
+// call merges anyway.  (One decode row of 8 KV heads, graph: 10 tiles whole 18.5
+// us, in pieces of 4 15.4; 34 tiles 38.1 and 20.1.  Eight rows: 10 tiles whole
+// 19.5, in pieces of 4, which are more than a round, 25.7.)
 // All blocks of a sequence get the same number of pieces (that of its longest
 // block); a block with fewer tiles than pieces leaves holes in the list.  Of a
 // prefix with more units than CTAs, whole rounds of units stay uncut and only the
@@ -29,6 +34,20 @@
 namespace pa {
 
 namespace {
+
+constexpr int kCutGain = 4;
+
+__device__ __forceinline__ int piece_tiles(unsigned long long tiles, unsigned long long units, int num_ctas, int min_tiles) {
+    const unsigned long long over = units < (unsigned)num_ctas ? num_ctas - units / 2 : 2ull * (unsigned)num_ctas;
+    const unsigned long long piece = (tiles + over - 1) / over;
+    return max(min_tiles, (int)(piece < 0x7fffffffull ? piece : 0x7fffffffull));
+}
+
+// Pieces of a sequence whose longest block has mx tiles.
+__device__ __forceinline__ int pieces_of(int mx, int piece, bool merged_anyway, int most) {
+    if (!merged_anyway && mx <= piece + kCutGain) return 1;
+    return max(1, min((mx + piece - 1) / piece, most));
+}
 
 // Writes the units of query block blk of sequence b and KV head kvh: the block's
 // c tiles in its sequence's p pieces, or in one where the block is among the
@@ -174,15 +193,13 @@ __global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_
     __syncthreads();
 
     // Pieces per block, the sequence's cost bin and its KV-head group.
-    const long long piece =
-        max((long long)a.min_tiles, (long long)((s_total + a.target_units - 1) / (unsigned)a.target_units));
+    const int piece = piece_tiles(s_total, (unsigned long long)total_blocks * a.n_kv_heads, a.num_ctas, a.min_tiles);
     for (int b = tid; b < nseq; b += nthr) {
         const SeqInfo si = seqs[b];
         const int nblk = (si.n + tpu - 1) / tpu;
         const int c = seq_scratch[b], mx = seq_group[b];
         const bool pre = b == a.num_seqs;
-        int p = (int)((mx + piece - 1) / piece);
-        p = max(1, min(p, pre ? a.max_prefix_pieces : a.max_pieces));
+        const int p = pieces_of(mx, piece, shared_prefix, pre ? a.max_prefix_pieces : a.max_pieces);
         pieces[b] = p;
         if (nblk > 0) {
             const int bin = cost_bin((long long)c * a.n_kv_heads / p);
@@ -232,7 +249,7 @@ __global__ void __launch_bounds__(1024) build_long_schedule_kernel(const __grid_
 // The same for a few sequences (kFewSeqs): see schedule.cuh.
 __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(const __grid_constant__ LongScheduleArgs a) {
     __shared__ FewSeqs f;
-    __shared__ int s_max[kFewSeqs], s_tiles[kFewSeqs], s_pieces[kFewSeqs], s_whole;
+    __shared__ int s_max[kFewSeqs], s_tiles[kFewSeqs], s_pieces[kFewSeqs], s_whole, s_units;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tpu = a.unit_slots * (kBlockM / a.group);
     const bool shared_prefix = a.prefix_len > 0, paged = a.block_table != nullptr;
@@ -248,10 +265,13 @@ __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(co
     };
     // tiles per head and longest block: by one thread, or by a warp where there are many blocks
     constexpr int kThreadBlocks = 4;
+    if (tid == 0) s_units = 0;
+    __syncthreads();
     if (tid < nseq) {
         const SeqInfo si = f.seqs[tid];
         const int nblk = (si.n + tpu - 1) / tpu;
         f.blocks[tid] = nblk;
+        atomicAdd(&s_units, nblk * a.n_kv_heads);
         if (nblk <= kThreadBlocks) {
             int c = 0, mx = 0;
             for (int i = 0; i < nblk; ++i) {
@@ -287,11 +307,9 @@ __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(co
     }
     __syncthreads();
     if (tid < nseq) {
-        const unsigned long long per = (f.total + a.target_units - 1) / (unsigned)a.target_units;
-        const int piece = max(a.min_tiles, (int)(per < 0x7fffffffull ? per : 0x7fffffffull));
+        const int piece = piece_tiles(f.total, (unsigned)s_units, a.num_ctas, a.min_tiles);
         const int c = s_tiles[tid], mx = s_max[tid];
-        int p = (mx + piece - 1) / piece;
-        p = max(1, min(p, tid == a.num_seqs ? a.max_prefix_pieces : a.max_pieces));
+        int p = pieces_of(mx, piece, shared_prefix, tid == a.num_seqs ? a.max_prefix_pieces : a.max_pieces);
         const int units = f.blocks[tid] * a.n_kv_heads;
         int whole = 0;
         if (tid == a.num_seqs) {

@@ -149,7 +149,8 @@ def test_sinks_one_long_row_is_split(block, int8, window, sinks):
     """One decode row over many tiles: its keys are split between CTAs and joined."""
     c = Call(40, [1], [4099], 128, 2, 4, block, int8)
     c.sinks(window, sinks)
-    assert binding.prefill_attn_last_launch_count() == 3
+    # (a window of at most 8 tiles is not: it runs without the merge)
+    assert binding.prefill_attn_last_launch_count() == (3 if (window + sinks) // 128 + 3 > 8 else 2)
     c.check(window=window, sinks=sinks)
     ok()
 
