@@ -812,6 +812,7 @@ constexpr long long kPartialBytes = 64ll << 20, kPrefixPartialBytes = 256ll << 2
 using pa::kMaxPieces;
 constexpr int kMinPieceTiles = 4;
 constexpr int kUncutTiles = 8;
+constexpr int kDirectSeqs = 64;
 constexpr int kPieceWaves = 2;
 
 pa_status check_unused(const Options& o, const char* what) {
@@ -895,9 +896,16 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     sa.max_pieces = max_pieces;
     sa.max_prefix_pieces = max_prefix_pieces;
     sa.min_tiles = kMinPieceTiles;
-    e = pa::launch_build_long_schedule(sa, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
-    int launches = 2;
+    // Few sequences with at most one unit per SM before cutting (so at most a few
+    // pieces per CTA): the attention kernel's CTAs plan for themselves, which saves
+    // the scheduler's launch.  The rotary prologue needs the scheduler's sequences.
+    const bool direct = num_seqs < kDirectSeqs && own_units + pre_units <= grid && o.rope_theta == 0.f;
+    int launches = 1;
+    if (!direct) {
+        e = pa::launch_build_long_schedule(sa, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
+        ++launches;
+    }
     if (o.rope_theta > 0.f) {
         e = rotate(q, k, cu_seqlens_q, scr.seqs, scr.rope, total_q, num_seqs, n_heads, n_kv_heads, head_dim,
                    o.rope_theta, pre.len, stream);
@@ -918,6 +926,8 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     p.part_lse = reinterpret_cast<float*>(at + list_bytes + seq_bytes + tok_bytes);
     p.part_o = reinterpret_cast<float*>(at + list_bytes + seq_bytes + tok_bytes + lse_bytes);
     p.slab_rows = (size_t)slab_rows;
+    p.direct = direct;
+    p.plan = sa;
     e = pa::encode_fwd_maps(p, q, total_q, num_seqs, head_dim, o.num_blocks);
     if (e == cudaSuccess && pre.k) e = pa::encode_prefix_maps(p, head_dim, pre.k, pre.v);
     if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");

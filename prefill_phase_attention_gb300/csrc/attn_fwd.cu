@@ -59,6 +59,7 @@
 #include "kernels.h"
 #include "prefill_attn.h"
 #include "ptx.cuh"
+#include "schedule_long.cuh"
 
 namespace pa {
 using namespace ptx;
@@ -124,10 +125,10 @@ struct __align__(16) Ctrl {
 // kernel checks), control block after them.  At least 120 KB so that a second
 // CTA never lands on an SM (each CTA holds all 512 TMEM columns).
 template <int D>
-constexpr int smem_bytes() {
+constexpr int smem_bytes(int more = 0) {
     using C = Cfg<D>;
-    return (C::kTileBytes * (kSlots + C::kStagesK + C::kStagesV) + (int)sizeof(Ctrl)) > 120 * 1024
-               ? C::kTileBytes * (kSlots + C::kStagesK + C::kStagesV) + (int)sizeof(Ctrl)
+    return (C::kTileBytes * (kSlots + C::kStagesK + C::kStagesV) + (int)sizeof(Ctrl)) + more > 120 * 1024
+               ? C::kTileBytes * (kSlots + C::kStagesK + C::kStagesV) + (int)sizeof(Ctrl) + more
                : 120 * 1024;
 }
 
@@ -523,11 +524,32 @@ __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, Work
     return true;
 }
 
+// A CTA's own units when it plans for itself (FwdParamsX::direct), in list
+// order; u.b < 0: none.  The host takes this path only where a CTA gets a few.
+constexpr int kOwnUnits = 8;
+struct OwnUnits {
+    UnitX x[kOwnUnits];
+    SeqInfo s[kOwnUnits];
+    int next;
+};
+
 // Claims the next unit that has tiles (the scheduler leaves holes in the list
 // where a query block has fewer tiles than its sequence has pieces).
-__device__ __forceinline__ void claim_unit_ext(const FwdParamsX& p, WorkspaceHeader* hdr, int num_units, UnitSlot& us,
-                                               int2& ext) {
+__device__ __forceinline__ void claim_unit_ext(const FwdParamsX& p, WorkspaceHeader* hdr, int num_units, OwnUnits* own,
+                                               UnitSlot& us, int2& ext) {
     us.u.b = -1;
+    if (p.direct) {
+        for (int i = own->next; i < kOwnUnits; ++i) {
+            if (own->x[i].u.b < 0) continue;
+            us.u = own->x[i].u;
+            us.s = own->s[i];
+            ext = make_int2(own->x[i].s0, own->x[i].slab);
+            own->next = i + 1;
+            return;
+        }
+        own->next = kOwnUnits;
+        return;
+    }
     for (int idx = atomicAdd(&hdr->counter, 1); idx < num_units; idx = atomicAdd(&hdr->counter, 1)) {
         const UnitX x = p.xunits[idx];
         if (x.u.ntiles == 0) continue;
@@ -565,6 +587,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     uint8_t* k_smem = q_smem + kSlots * C::kTileBytes;       // [kStagesK] tiles
     uint8_t* v_smem = k_smem + C::kStagesK * C::kTileBytes;  // [kStagesV] tiles
     Ctrl* ctl = reinterpret_cast<Ctrl*>(v_smem + C::kStagesV * C::kTileBytes);
+    OwnUnits* own = reinterpret_cast<OwnUnits*>(ctl + 1);  // kExt
+    bool direct = false;
+    if constexpr (kExt) direct = p.direct != 0;
 
     const int warp = threadIdx.x / 32;
     const int lane = threadIdx.x % 32;
@@ -628,6 +653,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         if (threadIdx.x == 0) atomicOr(&p.hdr->error, PA_DEVERR_SMEM_ALIGN);
         return;
     }
+    if constexpr (kExt) {
+        if (direct) {
+            // the plan lives in the tiles' shared memory until the first copies
+            if (threadIdx.x < kOwnUnits) own->x[threadIdx.x].u.b = -1;
+            if (threadIdx.x == 0) own->next = 0;
+            __syncthreads();
+            const int ctas = (int)gridDim.x, me = (int)blockIdx.x;
+            plan_few(p.plan, *reinterpret_cast<LongPlan*>(smem_raw), me == 0, false,
+                     [&](int pos, const UnitX& x, const SeqInfo& si) {
+                         if (pos % ctas != me || x.u.ntiles == 0) return;
+                         if (pos / ctas >= kOwnUnits) {
+                             atomicOr(&p.hdr->error, PA_DEVERR_OVERFLOW);
+                             return;
+                         }
+                         own->x[pos / ctas] = x;
+                         own->s[pos / ctas] = si;
+                     });
+            fence_proxy_async_smem();
+        }
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -673,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         uint64_t* empty = is_v ? ctl->v_empty : ctl->k_empty;
         const CUtensorMap* tm_cache = is_v ? &p.tm_cv : &p.tm_ck;
         const CUtensorMap* tm_new = is_v ? &p.tm_v : &p.tm_k;
-        const int num_units = hdr->num_units;
+        const int num_units = kExt && direct ? 0 : hdr->num_units;
         const int br = p.box_rows;
         const int br_log2 = min(p.block_log2, 7);  // box_rows = 1 << br_log2
         const int bmask = (1 << p.block_log2) - 1;
@@ -717,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                             if (ok) {
                                 UnitSlot us;
                                 if constexpr (kExt) {
-                                    claim_unit_ext(p, hdr, num_units, us, ctl->ext[sl]);
+                                    claim_unit_ext(p, hdr, num_units, own, us, ctl->ext[sl]);
                                 } else {
                                     const int idx = atomicAdd(&hdr->counter, 1);
                                     if (idx < num_units) {
@@ -851,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     } else if (warp == 0) {
         if (lane == 0) {
             // ----------------------------------------- unit fetch, Q and K loads
-            const int num_units = hdr->num_units;
+            const int num_units = kExt && direct ? 0 : hdr->num_units;
             uint32_t t = 0;
             int last_q_parity[1] = {-1};
             int last_k_parity[4] = {-1, -1, -1, -1};
@@ -860,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 if (!wait_bar(&ctl->unit_empty[sl], ((u_it >> 1) & 1) ^ 1, ctl, hdr)) break;
                 UnitSlot us;
                 if constexpr (kExt) {
-                    claim_unit_ext(p, hdr, num_units, us, ctl->ext[sl]);
+                    claim_unit_ext(p, hdr, num_units, own, us, ctl->ext[sl]);
                 } else {
                     const int idx = atomicAdd(&hdr->counter, 1);
                     if (idx < num_units) {
@@ -1856,7 +1901,7 @@ cudaError_t encode_pool_by_block(CUtensorMap* m, const void* ptr, uint64_t bs, u
 
 template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
 cudaError_t launch_d(const KernelParams<kExt>& p, int grid, cudaStream_t st) {
-    constexpr int kSmem = smem_bytes<D>();
+    constexpr int kSmem = smem_bytes<D>(kExt ? (int)sizeof(OwnUnits) : 0);
     static_assert(kSmem <= 232448, "shared memory budget");
     static int configured_for[64] = {0};
     int dev = 0;

@@ -80,6 +80,20 @@ struct FwdParams {
 cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_seqs, int head_dim, int num_blocks);
 cudaError_t launch_attn_fwd(const FwdParams& p, int head_dim, int grid, cudaStream_t st);
 
+// Scheduler of the long-context variant.
+struct LongScheduleArgs : ScheduleArgs {
+    UnitX* xunits;
+    int* seq_pieces;  // [num_seqs + 1] scheduler scratch: pieces of each sequence's query blocks
+    int* pre_pieces;  // [query blocks of the whole batch][n_kv_heads] pieces of each prefix unit
+    int* tok_pieces;  // [total_q] slabs that the merge joins for a token (0: none); nullptr: no merge
+    int sinks;
+    int prefix_len;
+    const int32_t* prefix_table;
+    int max_pieces, max_prefix_pieces;  // slabs the workspace has for each
+    int min_tiles;  // no piece smaller than this is cut
+};
+cudaError_t launch_build_long_schedule(const LongScheduleArgs& a, cudaStream_t stream);
+
 // Parameters of the long-context variant: sink tokens, a prefix the batch
 // shares, and units whose tiles are split between CTAs (pieces).
 struct FwdParamsX : FwdParams {
@@ -98,6 +112,10 @@ struct FwdParamsX : FwdParams {
     float* part_o;
     float* part_lse;
     size_t slab_rows;             // total_q * n_heads
+    // a few sequences of few units: no scheduler ran, every CTA plans for itself and
+    // takes the units whose list position is its own modulo the grid
+    int direct;
+    LongScheduleArgs plan;
 };
 cudaError_t encode_prefix_maps(FwdParamsX& p, int head_dim, const void* prefix_k, const void* prefix_v);
 template <int D>
@@ -108,20 +126,6 @@ template <>
 cudaError_t launch_attn_long_d<64>(const FwdParamsX& p, int grid, cudaStream_t st);
 template <>
 cudaError_t launch_attn_long_d<128>(const FwdParamsX& p, int grid, cudaStream_t st);
-
-// Scheduler of the long-context variant.
-struct LongScheduleArgs : ScheduleArgs {
-    UnitX* xunits;
-    int* seq_pieces;  // [num_seqs + 1] scheduler scratch: pieces of each sequence's query blocks
-    int* pre_pieces;  // [query blocks of the whole batch][n_kv_heads] pieces of each prefix unit
-    int* tok_pieces;  // [total_q] slabs that the merge joins for a token (0: none); nullptr: no merge
-    int sinks;
-    int prefix_len;
-    const int32_t* prefix_table;
-    int max_pieces, max_prefix_pieces;  // slabs the workspace has for each
-    int min_tiles;  // no piece smaller than this is cut
-};
-cudaError_t launch_build_long_schedule(const LongScheduleArgs& a, cudaStream_t stream);
 
 // Slabs of a row that the merge joins, at most: a sequence's own pieces and the prefix's.
 constexpr int kMaxPieces = 32;

@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(kFewThreads) build_key_schedule_few_kernel(con
     const bool paged = a.block_table != nullptr;
     griddep_launch();
     if (tid == 0) s_wide = 0;
-    load_few(a, f, a.sinks, nullptr, 0);
+    load_few(a, f, a.sinks, nullptr, 0, true);
     SeqGeo g{};
     if (tid < a.num_seqs && f.seqs[tid].n > 0) {
         g = seq_geo(f.seqs[tid], tps, a.causal, a.window, a.sinks, paged);
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kFewThreads) build_key_schedule_few_kernel(con
         f.cost[tid] = (float)g.tiles * (float)g.nq;
     }
     __syncthreads();
-    const int blocks = rank_few(a, f, a.num_seqs);
+    const int blocks = rank_few(a, f, a.num_seqs, true);
     for (int w = tid; w < blocks * a.n_kv_heads; w += kFewThreads) {
         const int i = w / a.n_kv_heads, kvh = w % a.n_kv_heads;
         const int b = block_owner(f.seqs, a.num_seqs, i);

@@ -144,9 +144,10 @@ struct FewSeqs {
 };
 
 // Loads and checks the sequences (and the prefix's table); f.seqs[b].n is 0 for a
-// rejected one.  Ends with a barrier.  Returns whether the prefix is usable.
+// rejected one (which the lead CTA reports).  Ends with a barrier.  Returns
+// whether the prefix is usable.
 __device__ __forceinline__ bool load_few(const ScheduleArgs& a, FewSeqs& f, int sinks, const int32_t* prefix_table,
-                                         int prefix_len) {
+                                         int prefix_len, bool lead) {
     constexpr int kChunk = 16;  // table entries of a thread in flight
     const int tid = threadIdx.x;
     bool bad = false, prefix_ok = true;
@@ -171,7 +172,7 @@ __device__ __forceinline__ bool load_few(const ScheduleArgs& a, FewSeqs& f, int 
         }
         __syncthreads();
         const int chunks = f.max_chunks;
-        for (int w = tid; w < a.num_seqs * chunks; w += kFewThreads) {
+        for (int w = tid; w < a.num_seqs * chunks; w += blockDim.x) {
             const int b = w / chunks, i0 = w % chunks * kChunk;
             const int n = f.blocks[b], x = f.spans[b][0], shift = f.spans[b][1] - x;
             const int32_t* row = a.block_table + (size_t)b * a.max_blocks;
@@ -185,14 +186,14 @@ __device__ __forceinline__ bool load_few(const ScheduleArgs& a, FewSeqs& f, int 
         if (prefix_len > 0) {
             const int nb = (prefix_len + a.block_size - 1) / a.block_size;
 #pragma unroll 8
-            for (int i = tid; i < nb; i += kFewThreads) bad |= (unsigned)__ldg(prefix_table + i) >= (unsigned)a.num_blocks;
+            for (int i = tid; i < nb; i += blockDim.x) bad |= (unsigned)__ldg(prefix_table + i) >= (unsigned)a.num_blocks;
         }
         prefix_ok = !__syncthreads_or(bad);
     }
     if (tid < a.num_seqs) {
         SeqInfo si = a.block_table ? f.seqs[tid] : checked_sequence(a, tid);
         if (si.n < 0 || !prefix_ok) {
-            atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
+            if (lead) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
             si = SeqInfo{0, 0, 0, 0};
         }
         f.seqs[tid] = si;
@@ -206,9 +207,10 @@ __device__ __forceinline__ bool load_few(const ScheduleArgs& a, FewSeqs& f, int 
 }
 
 // From f.cost, f.blocks and f.units: each sequence's place in the list (by
-// descending cost, then index), the first-block numbers, and the header.
+// descending cost, then index) and the first-block numbers; where a list is
+// `shared` between CTAs, its header and the sequences for the other kernels.
 // Returns the blocks of all sequences.  Ends with a barrier.
-__device__ __forceinline__ int rank_few(const ScheduleArgs& a, FewSeqs& f, int nseq) {
+__device__ __forceinline__ int rank_few(const ScheduleArgs& a, FewSeqs& f, int nseq, bool shared) {
     const int tid = threadIdx.x;
     if (tid < nseq) {
         const float mine = f.cost[tid];
@@ -223,9 +225,9 @@ __device__ __forceinline__ int rank_few(const ScheduleArgs& a, FewSeqs& f, int n
         }
         f.first[tid] = first;
         f.seqs[tid].pad = pad;
-        a.seqs[tid] = f.seqs[tid];
-        if (tid == nseq - 1) {
-            f.max_chunks = pad + f.blocks[tid];
+        if (tid == nseq - 1) f.max_chunks = pad + f.blocks[tid];
+        if (shared) a.seqs[tid] = f.seqs[tid];
+        if (shared && tid == nseq - 1) {
             a.hdr->num_units = total < a.max_units ? total : a.max_units;
             a.hdr->counter = 0;
             a.hdr->max_units = a.max_units;

@@ -149,8 +149,8 @@ def test_sinks_one_long_row_is_split(block, int8, window, sinks):
     """One decode row over many tiles: its keys are split between CTAs and joined."""
     c = Call(40, [1], [4099], 128, 2, 4, block, int8)
     c.sinks(window, sinks)
-    # (a window of at most 8 tiles is not: it runs without the merge)
-    assert binding.prefill_attn_last_launch_count() == (3 if (window + sinks) // 128 + 3 > 8 else 2)
+    # (a window of at most 8 tiles is not: it runs without the merge; neither needs a scheduler of its own)
+    assert binding.prefill_attn_last_launch_count() == (2 if (window + sinks) // 128 + 3 > 8 else 1)
     c.check(window=window, sinks=sinks)
     ok()
 
@@ -698,4 +698,18 @@ def test_without_lse(call):
     assert c.lse[1].isnan().all()
     c.lse[1].copy_(lse)
     c.check(**kw)
+    ok()
+
+
+@pytest.mark.parametrize("seqs", [9, 10, 18, 19, 63, 64])
+def test_planned_by_the_kernel_or_by_the_scheduler(seqs):
+    """Both sides of the sizes up to which the attention kernel plans for itself (a unit per SM at most, 63 sequences)."""
+    hk = 8 if seqs < 40 else 1
+    lens = [(i * 977) % 2500 for i in range(seqs)]
+    c = Call(160, [1] * seqs, lens, 64, hk, 4, prefix=1500)
+    c.prefix()
+    c.check()
+    c = Call(161, [1 + i % 3 for i in range(seqs)], lens, 64, hk, 4, 32)
+    c.sinks(1200, 4)
+    c.check(window=1200, sinks=4)
     ok()
