@@ -264,10 +264,10 @@ pa_status prefill_attn_varlen_ex(
  * paged cache tiles start at multiples of 128 positions, and only the table
  * entries of the sink tiles, of the tiles from the oldest query's window on and
  * of the new tokens must name a block of the pool: the blocks in between may
- * have been given back.  A few long rows are split along their keys and joined: then
- * three kernels run instead of two, and the partial results (fp32, at most
- * 64 MiB) live in the per-stream workspace.  Under graph capture the stream
- * must already have run a call of at least these sizes.
+ * have been given back.  A few long rows are split along their keys and joined
+ * by one more kernel; the partial results (fp32, at most 64 MiB) live in the
+ * per-stream workspace.  Under graph capture the stream must already have run a
+ * call of at least these sizes.  max_cache_len is at most 2^30.
  */
 pa_status prefill_attn_varlen_sinks(
     const void *q, const void *k, const void *v,
@@ -314,9 +314,10 @@ typedef struct pa_prefix {
  * whole batch's queries, not once per sequence, and the two parts are joined
  * by their log-sum-exp (partial results in fp32 in the per-stream workspace:
  * up to 64 MiB for the own part and 256 MiB for the prefix's, and at least
- * total_q * n_heads * (head_dim + 1) * 4 bytes for each).  Every option of pa_options applies but window and
- * wait_timeout_test.  len = 0 is prefill_attn_varlen_ex.  A prefix block
- * outside the pool rejects the whole call on the device
+ * total_q * n_heads * (head_dim + 1) * 4 bytes for each).  Every option of
+ * pa_options applies but window and wait_timeout_test.  len = 0 is
+ * prefill_attn_varlen_ex.  len and max_cache_len are at most 2^30.  A prefix
+ * block outside the pool rejects the whole call on the device
  * (PA_DEVERR_METADATA, nothing written).  Under graph capture the stream must
  * already have run a call of at least these sizes.
  */
@@ -351,8 +352,11 @@ pa_status prefill_attn_varlen_prefix(
  *   opts         window, block_table, rope_theta, kv_quant with cache_k_scale
  *                (cache_v_scale must be set too, and is not read).
  * The sums are fp32, each key's by one thread block in a fixed order, so equal
- * inputs give equal bits.  A sequence with inconsistent metadata is skipped
- * (PA_DEVERR_METADATA).  Other arguments as in prefill_attn_varlen.
+ * inputs give equal bits.  Sequences of a paged call must not share blocks that
+ * hold cached keys their queries see: such a block's weights would be added to
+ * by several thread blocks at once.  A sequence with inconsistent metadata is
+ * skipped (PA_DEVERR_METADATA).  max_cache_len and prefix_len are at most 2^30.
+ * Other arguments as in prefill_attn_varlen.
  */
 pa_status prefill_attn_key_weights(
     const void *q, const void *k,
@@ -389,6 +393,7 @@ pa_status prefill_attn_key_weights(
  *                 itself, or memory that does not overlap it.
  * A sequence whose length is outside [0, max_cache_len], or that names a block
  * outside the pool, is skipped (PA_DEVERR_METADATA, nothing of it written).
+ * max_cache_len is at most 2^30.
  * Evicted caches keep their order but not their positions: a caller with
  * rotary embeddings rotates later tokens itself (rope_theta = 0 in the calls).
  */

@@ -411,6 +411,7 @@ def prefill_attn_key_weights(q, k, cu_seqlens_q, cu_seqlens_k, cache_k, cache_of
     weights: fp32, shape cache_k.shape[:-1].  Keys already cached are added to, the new tokens'
     keys are set.  lse is what the attention call of the same step wrote; the other arguments
     are those of that call (prefix_len: its shared prefix, for the rotary positions).
+    Sequences must not share blocks of a paged cache.
     """
     if lse is None:
         raise ValueError("prefill_attn_key_weights needs lse")

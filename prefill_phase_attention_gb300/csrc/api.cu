@@ -953,8 +953,18 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
     return x < y + b_bytes && y < x + a_bytes;
 }
 
-// A window or sink count past the cache's capacity says the same as the
-// capacity; clamped so that position arithmetic stays within 32 bits.
+// The kernels' position arithmetic stays within 32 bits: positions and spans are
+// at most kMaxTokens each, so the sum of two fits.  A window or sink count past
+// the cache's capacity says the same as the capacity.
+constexpr int kMaxTokens = 1 << 30;
+
+pa_status check_capacity(int max_cache_len, int prefix_len) {
+    if (max_cache_len > kMaxTokens || prefix_len > kMaxTokens)
+        return fail(PA_ERR_UNSUPPORTED, "max_cache_len (%d) and the prefix (%d tokens) must be at most 2^30",
+                    max_cache_len, prefix_len);
+    return PA_OK;
+}
+
 int clamp_span(int tokens, int max_cache_len) { return std::min(tokens, max_cache_len); }
 
 int log2_of(int block_size) {
@@ -986,6 +996,8 @@ pa_status prefill_attn_varlen_sinks(const void* q, const void* k, const void* v,
     if (s != PA_OK) return s;
     s = check_paged(o, max_cache_len, n_kv_heads);
     if (s != PA_OK) return s;
+    s = check_capacity(max_cache_len, 0);
+    if (s != PA_OK) return s;
     if (num_seqs == 0 || total_q == 0) return PA_OK;
     o.window = clamp_span(o.window, max_cache_len);
     return enqueue_long(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs,
@@ -1015,6 +1027,8 @@ pa_status prefill_attn_varlen_prefix(const void* q, const void* k, const void* v
     if (s != PA_OK) return s;
     Prefix pre;
     s = read_prefix(prefix, o, &pre);
+    if (s != PA_OK) return s;
+    s = check_capacity(max_cache_len, pre.len);
     if (s != PA_OK) return s;
     if (num_seqs == 0 || total_q == 0) return PA_OK;
     if (pre.k && (pre.k == out || pre.v == out || pre.k == cache_k || pre.k == cache_v || pre.v == cache_k ||
@@ -1059,6 +1073,8 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
                    n_heads, n_kv_heads, head_dim, scale, causal, o.block_table != nullptr);
     if (s != PA_OK) return s;
     s = check_paged(o, max_cache_len, n_kv_heads);
+    if (s != PA_OK) return s;
+    s = check_capacity(max_cache_len, prefix_len);
     if (s != PA_OK) return s;
     if (num_seqs == 0 || total_q == 0) return PA_OK;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
@@ -1135,6 +1151,8 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
         return fail(PA_ERR_INVALID_ARG, "sink_tokens (%d) and recent_tokens (%d) must be >= 0 and fit the budget (%d)",
                     sink_tokens, recent_tokens, budget);
     s = check_paged(o, max_cache_len, n_kv_heads);
+    if (s != PA_OK) return s;
+    s = check_capacity(max_cache_len, 0);
     if (s != PA_OK) return s;
     const long long heads = (long long)num_seqs * n_kv_heads;
     if (heads >= (1LL << 24)) return fail(PA_ERR_UNSUPPORTED, "num_seqs * n_kv_heads must be < 2^24");

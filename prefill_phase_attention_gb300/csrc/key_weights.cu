@@ -223,7 +223,7 @@ __device__ __forceinline__ QRange unit_queries(const KeyTile& first, const KeyTi
     if (!causal) return r;
     if (first.lo > s.P) r.lo = (first.lo - s.P) / tps;
     if (window > 0 && first.lo >= sinks) {
-        const int tok = window + last.hi - 2 - s.P;  // last token that sees the last key
+        const int tok = window + (last.hi - 2 - s.P);  // last token that sees the last key
         r.hi = tok < 0 ? 0 : min(nq, tok / tps + 1);
     }
     return r;
@@ -235,7 +235,7 @@ __device__ __forceinline__ QRange full_queries(const KeyTile& k, const SeqInfo& 
     QRange r{0, tps * group > kBlockN - 32 ? s.n / tps : 0};
     if (!causal) return r;
     if (k.hi - 1 > s.P) r.lo = (k.hi - 1 - s.P + tps - 1) / tps;
-    if (window > 0 && k.hi > sinks) r.hi = min(r.hi, max(0, window + k.lo - s.P) / tps);
+    if (window > 0 && k.hi > sinks) r.hi = min(r.hi, max(0, window + (k.lo - s.P)) / tps);
     return r;
 }
 
@@ -879,7 +879,9 @@ __global__ void __launch_bounds__(kThreads, 1) key_weights_kernel(const __grid_c
             hi = cols;
             if (p.causal) {
                 lo = max(0, j - s.P - q0) * G;
-                if (p.window > 0 && j >= p.sinks) hi = min(hi, (p.window + j - s.P - q0) * G);
+                // (clamped to a tile's tokens: a window times G may pass 32 bits)
+                if (p.window > 0 && j >= p.sinks)
+                    hi = min(hi, max(0, min(p.window + (j - s.P - q0), kBlockM)) * G);
             }
         };
         // key j's weight row, old weight and score factor; false: the row holds no key

@@ -171,8 +171,8 @@ __device__ __forceinline__ bool load_few(const ScheduleArgs& a, FewSeqs& f, int 
             atomicMax(&f.max_chunks, (end - y + x + kChunk - 1) / kChunk);
         }
         __syncthreads();
-        const int chunks = f.max_chunks;
-        for (int w = tid; w < a.num_seqs * chunks; w += blockDim.x) {
+        const unsigned chunks = (unsigned)f.max_chunks;  // < 2^23, of at most 2^8 sequences
+        for (unsigned w = tid; w < a.num_seqs * chunks; w += blockDim.x) {
             const int b = w / chunks, i0 = w % chunks * kChunk;
             const int n = f.blocks[b], x = f.spans[b][0], shift = f.spans[b][1] - x;
             const int32_t* row = a.block_table + (size_t)b * a.max_blocks;

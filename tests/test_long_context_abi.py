@@ -52,6 +52,7 @@ def attention_args(kw):
     (dict(out=16), 1, "alias"),
     (dict(o=dict(PAGED, block_size=16)), 1, "max_cache_len"),
     (dict(o=dict(QUANT, schedule=1)), 1, "schedule 1 needs"),
+    (dict(cap=2 ** 30 + 1, H=1, Hk=1), 2, "2^30"),
 ])
 def test_sinks_refusals(lib, kw, status, msg):
     opts = kw["opts"] if "opts" in kw else ctypes.byref(options(kw.get("window", 4), **kw.get("o", {})))
@@ -75,6 +76,9 @@ def test_sinks_refusals(lib, kw, status, msg):
     (dict(o=dict(wait_timeout_test=1)), 1, "wait_timeout_test"),
     (dict(d=40), 2, "head_dim"),
     (dict(causal=2), 1, "causal"),
+    (dict(cap=2 ** 30 + 1, H=1, Hk=1), 2, "2^30"),
+    (dict(p=dict(len=2 ** 30 + 1, capacity=2 ** 30 + 1)), 2, "2^30"),
+    (dict(o=dict(PAGED), p=dict(len=2 ** 30 + 1, block_table=256)), 2, "2^30"),
 ])
 def test_prefix_refusals(lib, kw, status, msg):
     p = binding.PaPrefix(ctypes.sizeof(binding.PaPrefix), 5, 160, 176, 8, 0, None, None, None)
@@ -111,6 +115,8 @@ def test_prefix_layout_matches_header():
     (dict(k=33), 1, "aligned"),
     (dict(o=dict(kv_quant=1, cache_k_scale=512)), 1, "cache_v_scale"),
     (dict(o=dict(PAGED, block_size=12)), 2, "power of two"),
+    (dict(k=256, cap=2 ** 30 + 1, H=1, Hk=1), 2, "2^30"),
+    (dict(k=256, prefix=2 ** 30 + 1), 2, "2^30"),
 ])
 def test_key_weights_refusals(lib, kw, status, msg):
     a = dict(q=16, k=32, cu_q=64, cu_k=80, ck=96, off=128, lse=144, weights=160, num_seqs=1, total_q=4, cap=8, H=4, Hk=2,
@@ -130,6 +136,7 @@ def test_key_weights_refusals(lib, kw, status, msg):
     (dict(d=16), 2, "head_dim"),
     (dict(num_seqs=2 ** 23, Hk=2), 2, "2^24"),
     (dict(num_seqs=2 ** 20, cap=2 ** 12), 2, "2^31"),
+    (dict(num_seqs=1, Hk=1, cap=2 ** 30 + 1), 2, "2^30"),
     (dict(ck=None), 1, "cache_k is NULL"),
     (dict(cv=40), 1, "16-byte"),
     (dict(weights=None), 1, "weights is NULL"),

@@ -511,6 +511,74 @@ def test_key_weights_of_groups_that_do_not_divide_a_tile(group):
     ok()
 
 
+@pytest.mark.parametrize("block", [0, 16])
+@pytest.mark.parametrize("group", [3, 7, 48, 128])
+def test_attention_groups_that_do_not_divide_a_tile(group, block):
+    """Query blocks of 42, 18, 2 tokens and of one, whole and in pieces (the merge numbers tokens by block)."""
+    new, lens = [45, 1, 4], [5, 1500, 90]
+    c = Call(123, new, lens, 64, 1, group, block)
+    c.sinks(1200, 4)
+    c.check(window=1200, sinks=4)
+    c = Call(124, new, lens, 64, 1, group, block, prefix=777)
+    c.prefix()
+    c.check()
+    ok()
+
+
+@pytest.mark.parametrize("call", ["sinks", "prefix", "weights"])
+@pytest.mark.parametrize("new,lens", [([1, 3], [900, 40]), ([1] * 70, list(range(70)))])
+def test_rows_behind_the_last_sequence_stay(call, new, lens):
+    """A batch padded to a larger total_q: the rows behind are left as they were, and reach no result."""
+    c = Call(125, new, lens, 64, 2, 2, prefix=300 if call == "prefix" else 0)
+    t, more = sum(new), 140
+    big = [torch.cat([x, torch.full((more, *x.shape[1:]), 3.0, dtype=x.dtype, device="cuda")]) for x in c.dev]
+    out = torch.full_like(big[0], math.nan)
+    lse = torch.full(big[0].shape[:2], math.nan, device="cuda")
+    c.dev, c.out, c.lse = big, (c.out[0], out), (c.lse[0], lse)
+    if call == "weights":
+        w = weigh_padded(c, t)
+        assert torch.equal(w, weigh_padded(c, t))
+        return
+    c.sinks(64, 4) if call == "sinks" else c.prefix()
+    torch.cuda.synchronize()
+    assert out[t:].isnan().all() and lse[t:].isnan().all()
+    c.out, c.lse = (c.out[0], out[:t]), (c.lse[0], lse[:t])
+    c.check(**(dict(window=64, sinks=4) if call == "sinks" else {}))
+    ok()
+
+
+def weigh_padded(c, t):
+    """Key weights of a padded batch whose first t rows are the sequences'."""
+    lse = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale)[1].float()
+    w = c.weights.cuda()
+    padded = torch.cat([lse, torch.full((len(c.dev[0]) - t, lse.shape[1]), -5.0)]).cuda()
+    binding.prefill_attn_key_weights(c.dev[0], c.dev[1], *c.meta, c.data[0][1], c.offsets, padded, w, scale=c.scale)
+    ref = R.key_weights(c.cache, c.q, c.k, c.new, lse, c.scale, c.weights)
+    tol = (R.SCORE + max(c.new) * c.group * 2.0 ** -24) * ref.abs() + 1e-6
+    assert ((w.cpu().double() - ref).abs() <= tol).all()
+    ok()
+    return w
+
+
+def test_key_weights_under_a_window_of_millions_of_tokens():
+    """A window times the heads of a group passes 32 bits; it sees the few tokens of these sequences all the same."""
+    c = Call(126, [1, 2, 1], [300, 10, 0], 32, 1, 128)
+    lse = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale)[1].float().cuda()
+    cap, used = (1 << 24) + 64, c.weights.shape[-1]
+    keys = torch.zeros((3, 1, cap, 32), dtype=torch.bfloat16, device="cuda")
+    keys[:, :, :used] = c.data[0][1]
+    got = {}
+    for window in (0, 1 << 24):
+        w = torch.zeros((3, 1, cap), device="cuda")
+        binding.prefill_attn_key_weights(c.dev[0], c.dev[1], *c.meta, keys, c.offsets, lse, w, scale=c.scale, window=window)
+        got[window] = w
+    assert torch.equal(got[0], got[1 << 24])
+    ref = R.key_weights(c.cache, c.q, c.k, c.new, lse.cpu(), c.scale, torch.zeros_like(c.weights))
+    tol = (R.SCORE + 2 * 128 * 2.0 ** -24) * ref.abs() + 1e-6
+    assert ((got[0][:, :, :used].cpu().double() - ref).abs() <= tol).all()
+    ok()
+
+
 def test_prefix_with_more_units_than_ctas():
     """Whole rounds of prefix units stay uncut, the last round is cut into pieces."""
     c = Call(122, [300, 1, 601], [0, 70, 5], 32, 64, 1, prefix=1111)
