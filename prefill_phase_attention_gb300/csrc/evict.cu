@@ -8,7 +8,8 @@
 // every token.
 //
 // Choosing: the m-th largest weight by a radix select, 8 bits of the weight's
-// order-preserving integer image per pass.  One CTA does it alone while its
+// order-preserving integer image per pass, until few enough weights share the
+// digits chosen so far to be compared with one another.  One CTA does it alone while its
 // threads can hold the weights in registers; beyond that the CTAs of a cluster
 // each take a share of the positions and add their histograms through
 // distributed shared memory.  One pass over the positions then lists the kept
@@ -52,6 +53,10 @@ constexpr int kScalars = 8;  // weights or scales a thread moves per chunk
 // Weights crowd into a few digits: a histogram has this many copies, one per
 // lane & 7, a bank apart, so that a warp's equal digits do not queue up.
 constexpr int kCopies = 8;
+// Once the bin that holds the m-th largest weight has at most this many, they are
+// compared with one another instead of by further passes: after two of the four,
+// for weights that are not nearly all alike.
+constexpr int kCandidates = 128;
 
 // Order-preserving image of a weight: larger weight, larger integer; -0 equals
 // +0 and every NaN is the largest value.
@@ -98,14 +103,15 @@ __device__ int checked_length(const EvictArgs& a, int b) {
 
 template <int kThreads, int kHeld>
 struct Shared {
-    int copies[kCopies][257];
+    uint32_t copies[kCopies][257];
     int hist[4][256];  // this CTA's, one per pass: no barrier between the cluster's reads and the next pass
     int sums[256];
     int warp_counts[2][kThreads / 32];  // certain and equal positions per warp, then ahead of the warp
     int total[2];                       // ... of this CTA's share
     int batch[2];                       // ... of a batch
     uint32_t digit;
-    int need;
+    int need, inside;                   // wanted from the chosen bin; weights in it
+    int found;                          // candidates of this CTA's share
     uint32_t ranks[kThreads * (kHeld + 1)];  // a batch of rank_bits, one padding word per thread
 };
 
@@ -182,10 +188,12 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& a, Shared<kThread
     load_batch(p_lo);
 
     if (compete) {
-        int* const my_copy = sh.copies[lane & (kCopies - 1)];
-        for (int pass = 0; pass < 4; ++pass) {
+        uint32_t* const my_copy = sh.copies[lane & (kCopies - 1)];
+        if (tid == 0) sh.found = 0;
+        uint32_t mask = 0;  // the digits chosen so far
+        int inside = len;   // weights that share them
+        for (int pass = 0; pass < 4 && inside > kCandidates; ++pass) {
             const int shift = 24 - 8 * pass;
-            const uint32_t mask = pass == 0 ? 0u : 0xffffffffu << (shift + 8);
             for (int i = tid; i < kCopies * 257; i += kThreads) (&sh.copies[0][0])[i] = 0;
             __syncthreads();
             for (int p0 = p_lo; p0 < p_hi; p0 += kBatch) {
@@ -194,13 +202,13 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& a, Shared<kThread
 #pragma unroll
                 for (int i = 0; i < kHeld; ++i)
                     // (ranks of 0 are the lowest: the digits chosen from above never reach them)
-                    if ((held[i] & mask) == threshold) atomicAdd(&my_copy[(held[i] >> shift) & 255], 1);
+                    if ((held[i] & mask) == threshold) atomicAdd(&my_copy[(held[i] >> shift) & 255], 1u);
             }
             __syncthreads();
             if (tid < 256) {
                 int sum = 0;
 #pragma unroll
-                for (int c = 0; c < kCopies; ++c) sum += sh.copies[c][tid];
+                for (int c = 0; c < kCopies; ++c) sum += (int)sh.copies[c][tid];
                 sh.hist[pass][tid] = sum;
             }
             if (coop) cluster.sync();
@@ -227,10 +235,54 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& a, Shared<kThread
                 if (above < need && above + mine >= need) {
                     sh.digit = (uint32_t)tid;
                     sh.need = need - above;  // of this bin's
+                    sh.inside = mine;
                 }
             }
             __syncthreads();
             threshold |= sh.digit << shift;
+            mask |= 255u << shift;
+            need = sh.need;
+            inside = sh.inside;
+        }
+        if (mask != 0xffffffffu) {
+            // the candidates of this CTA's share and of the cluster, where histograms were
+            uint32_t *const own = sh.copies[0], *const every = sh.copies[1];
+            __syncthreads();  // (sh.found)
+            for (int p0 = p_lo; p0 < p_hi; p0 += kBatch) {
+                if (!one_batch) load_batch(p0);
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i)
+                    if (held[i] != 0 && (held[i] & mask) == threshold) own[atomicAdd(&sh.found, 1)] = held[i];
+            }
+            __syncthreads();
+            const uint32_t* among = own;
+            int n = sh.found;
+            if (coop) {
+                cluster.sync();
+                n = 0;
+                for (int r = 0; r < ranks; ++r) {
+                    const int m = *cluster.map_shared_rank(&sh.found, r);
+                    if (tid < m) every[n + tid] = *cluster.map_shared_rank(&own[tid], r);
+                    n += m;
+                }
+                __syncthreads();
+                among = every;
+            }
+            if (tid < n) {
+                const uint32_t mine = among[tid];
+                int above = 0, alike = 0;
+#pragma unroll 8
+                for (int i = 0; i < n; ++i) {
+                    above += among[i] > mine;
+                    alike += among[i] == mine;
+                }
+                if (above < need && above + alike >= need) {  // (equal ones write the same)
+                    sh.digit = mine;
+                    sh.need = need - above;
+                }
+            }
+            __syncthreads();
+            threshold = sh.digit;
             need = sh.need;
         }
     }

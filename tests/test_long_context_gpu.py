@@ -393,6 +393,18 @@ def test_evict_long_sequences(int8, block):
     ok()
 
 
+@pytest.mark.parametrize("heads", [1, 200])
+@pytest.mark.parametrize("spread", [1, 7, 10, 14, 18, 25])
+def test_evict_weights_that_share_leading_bits(spread, heads):
+    """Weights within 2^spread steps of fp32 of one another: the choice is made after every possible number of
+    digits, and with more and fewer equal weights than are compared at once; one launch, and two."""
+    c = Call(93, [0] * 6, [129, 133, 700, 2049, 5000, 9000] if heads == 1 else [129, 133, 135, 300, 700, 1200], 32, heads, 1)
+    g = torch.Generator().manual_seed(spread)
+    steps = torch.randint(0, 2 ** spread, c.cache.shape[:-1], generator=g, dtype=torch.int32)
+    evict(c, (steps + 0x3f800000).view(torch.float32), 128, 3, 20)
+    ok()
+
+
 def test_evict_equal_weights_keeps_the_first():
     c = Call(96, [0], [1500], 64, 1, 1)
     evict(c, torch.zeros(c.cache.shape[:-1]), 600, 2, 10)
