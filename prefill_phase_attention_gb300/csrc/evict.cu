@@ -49,7 +49,6 @@ constexpr int kFusedThreads = 256, kFusedHeld = 8;
 // slot, of 512 for longer ones (64 sequences of 700-4099 tokens in int8 pages:
 // 72.8 us with 256, 81.6 with 512; 16 of 16384 tokens: 120.7 and 116.7)
 constexpr int kSelectHeld = 16, kMoveThreads = 256;
-constexpr int kScalars = 8;  // weights or scales a thread moves per chunk
 // Weights crowd into a few digits: a histogram has this many copies, one per
 // lane & 7, a bank apart, so that a warp's equal digits do not queue up.
 constexpr int kCopies = 8;
@@ -115,19 +114,20 @@ struct Shared {
     uint32_t ranks[kThreads * (kHeld + 1)];  // a batch of rank_bits, one padding word per thread
 };
 
-// Moves a scalar per row (weights, row scales): dst row j = src row list[j].
-template <int kThreads>
-__device__ void move_scalars(const Rows& rows, const float* src, float* dst, const int* list, int count) {
-    for (int j0 = 0; j0 < count; j0 += kThreads * kScalars) {
-        float x[kScalars];
+// Moves a scalar per row (weights, row scales), kPerThread of a thread at a time:
+// dst row j = src row list[j].
+template <int kThreads, int kPerThread>
+__device__ __forceinline__ void move_scalars(const Rows& rows, const float* src, float* dst, const int* list, int count) {
+    for (int j0 = 0; j0 < count; j0 += kThreads * kPerThread) {
+        float x[kPerThread];
 #pragma unroll
-        for (int i = 0; i < kScalars; ++i) {
+        for (int i = 0; i < kPerThread; ++i) {
             const int j = j0 + i * kThreads + threadIdx.x;
             if (j < count) x[i] = src[rows(list[j])];
         }
         __syncthreads();  // in place: this chunk's sources are read
 #pragma unroll
-        for (int i = 0; i < kScalars; ++i) {
+        for (int i = 0; i < kPerThread; ++i) {
             const int j = j0 + i * kThreads + threadIdx.x;
             if (j < count) dst[rows(j)] = x[i];
         }
@@ -372,26 +372,25 @@ __device__ __forceinline__ void select_tokens(const EvictArgs& a, Shared<kThread
     __syncthreads();
 }
 
-// What goes with the rows: the -1s past the last kept position, the length, the
-// kept weights and the row scales (K's by `scale_k_here`, V's by `scale_v_here`).
-template <int kThreads, int kHeld>
-__device__ __forceinline__ void finish(const EvictArgs& a, int b, int h, int len, const int* list, bool lead,
-                                       bool weights_here, bool scale_k_here, bool scale_v_here) {
-    const int count = min(len, a.budget), tid = threadIdx.x;
+// The list where the caller wants it (with the -1s past the last kept position),
+// and the length.
+template <int kThreads>
+__device__ __forceinline__ void write_index(const EvictArgs& a, int b, int h, int count, const int* list) {
+    int* const index = a.index + ((size_t)b * a.n_kv_heads + h) * a.budget;
+    if (list != index)
+        for (int i = threadIdx.x; i < count; i += kThreads) index[i] = list[i];
+    for (int i = count + threadIdx.x; i < a.budget; i += kThreads) index[i] = -1;
+    if (threadIdx.x == 0 && h == 0) a.kept_lengths[b] = count;
+}
+
+// What goes with the rows: the kept weights (which = 0), K's (1) or V's row scales (2).
+template <int kThreads, int kPerThread>
+__device__ __forceinline__ void move_companions(const EvictArgs& a, int b, int h, int len, const int* list, int which) {
     const bool all = len <= a.budget;
-    const Rows rows(a, b, h);
-    if (lead) {
-        int* const index = a.index + ((size_t)b * a.n_kv_heads + h) * a.budget;
-        if (list != index)
-            for (int i = tid; i < count; i += kThreads) index[i] = list[i];
-        for (int i = count + tid; i < a.budget; i += kThreads) index[i] = -1;
-        if (tid == 0 && h == 0) a.kept_lengths[b] = count;
-    }
-    if (weights_here && a.kept_weights && !(all && a.kept_weights == a.weights))
-        move_scalars<kThreads>(rows, a.weights, a.kept_weights, list, count);
-    if (all || !a.scale_k) return;
-    if (scale_k_here) move_scalars<kThreads>(rows, a.scale_k, a.scale_k, list, count);
-    if (scale_v_here) move_scalars<kThreads>(rows, a.scale_v, a.scale_v, list, count);
+    const float* const src = which == 0 ? a.weights : which == 1 ? a.scale_k : a.scale_v;
+    float* const dst = which == 0 ? a.kept_weights : which == 1 ? a.scale_k : a.scale_v;
+    if (!dst || (all && dst == src)) return;
+    move_scalars<kThreads, kPerThread>(Rows(a, b, h), src, dst, list, min(len, a.budget));
 }
 
 // Moves column part `part` of the kept rows of K (which = 0) or V (1).
@@ -454,7 +453,9 @@ __global__ void __launch_bounds__(kFusedThreads, 4) evict_kernel(const __grid_co
     select_tokens(a, sh, cluster, b, h, len, coop, list);
     // the list is whole, and every CTA has read the weights it needs
     if (coop || a.kept_weights == a.weights) cluster.sync();
-    finish<kFusedThreads, kFusedHeld>(a, b, h, len, list, rank == 0, rank == ranks - 1, rank == 0, rank == 1);
+    if (rank == 0) write_index<kFusedThreads>(a, b, h, min(len, a.budget), list);
+    if (rank == ranks - 1) move_companions<kFusedThreads, 8>(a, b, h, len, list, 0);
+    if (rank < 2) move_companions<kFusedThreads, 8>(a, b, h, len, list, 1 + rank);
     if (len > a.budget) move_rows<kFusedThreads>(a, b, h, a.budget, rank & 1, rank >> 1, list);
 }
 
@@ -474,17 +475,34 @@ __global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) select_
     int* const list = a.index + (size_t)bh * a.budget;
     if (coop || rank == 0) select_tokens(a, sh, cluster, b, h, len, coop, list);
     if (ranks > 1) cluster.sync();
-    // with one CTA it does everything; else the weights and scales are shared out
-    finish<kSelectThreads, kSelectHeld>(a, b, h, len, list, rank == 0, rank == 0, rank == min(1, ranks - 1),
-                                        rank == min(2, ranks - 1));
+    if (rank == 0) write_index<kSelectThreads>(a, b, h, min(len, a.budget), list);
 }
 
-__global__ void __launch_bounds__(kMoveThreads, 7) move_kernel(const __grid_constant__ EvictArgs a, int log_parts) {
-    const int part = blockIdx.x & ((1 << log_parts) - 1), which = (blockIdx.x >> log_parts) & 1;
-    const int bh = blockIdx.x >> (log_parts + 1), h = bh % a.n_kv_heads, b = bh / a.n_kv_heads;
+// (out of line: inlined, it makes the movers' registers spill, which cost 30 us of 45)
+__device__ __noinline__ void move_companions_of_movers(const EvictArgs& a, int b, int h, int len, const int* list,
+                                                       int which) {
+    move_companions<kMoveThreads, 4>(a, b, h, len, list, which);
+}
+
+// CTAs first for the column parts of K and V, of all heads, then for what goes with
+// them (weights, K's scales, V's; `others` of the three).  (The select kernel moving
+// these itself: 64 sequences in int8 pages 74.3 us a call against 62.7, 16 of 16384
+// tokens 116.5 against 110.7.)
+__global__ void __launch_bounds__(kMoveThreads, 7) move_kernel(const __grid_constant__ EvictArgs a, int parts, int others) {
+    const int heads = a.num_seqs * a.n_kv_heads, movers = 2 * parts * heads;
+    const bool mover = (int)blockIdx.x < movers;
+    const int x = mover ? blockIdx.x : blockIdx.x - movers, per = mover ? 2 * parts : others;
+    const int bh = x / per, what = x % per, h = bh % a.n_kv_heads, b = bh / a.n_kv_heads;
     const int len = checked_length<kMoveThreads>(a, b);
     griddep_wait();
-    if (len > a.budget) move_rows<kMoveThreads>(a, b, h, a.budget, which, part, a.index + (size_t)bh * a.budget);
+    const int* const list = a.index + (size_t)bh * a.budget;
+    if (!mover) {
+        // (every weight has been read: they may move in place)
+        const int first = a.kept_weights ? 0 : 1;
+        if (len >= 0) move_companions_of_movers(a, b, h, len, list, what + first);
+    } else if (len > a.budget) {
+        move_rows<kMoveThreads>(a, b, h, a.budget, what / parts, what % parts, list);
+    }
 }
 
 }  // namespace
@@ -516,14 +534,13 @@ cudaError_t launch_evict(const EvictArgs& args, int sms, int* launches, cudaStre
     cfg.blockDim = dim3((unsigned)threads);
     cudaError_t e = cudaLaunchKernelEx(&cfg, threads == 256 ? select_kernel<256> : select_kernel<512>, a);
     if (e != cudaSuccess) return e;
-    int log_parts = 0;
-    while ((1 << log_parts) < parts) ++log_parts;
-    cfg.gridDim = dim3((unsigned)(2 * parts * heads));
+    const int others = (a.kept_weights ? 1 : 0) + (a.scale_k ? 2 : 0);
+    cfg.gridDim = dim3((unsigned)((2 * parts + others) * heads));
     cfg.blockDim = dim3(kMoveThreads);
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     *launches = 2;
-    return cudaLaunchKernelEx(&cfg, move_kernel, a, log_parts);
+    return cudaLaunchKernelEx(&cfg, move_kernel, a, parts, others);
 }
 
 }  // namespace pa
