@@ -251,6 +251,17 @@ __device__ __forceinline__ int tile_at(const UnitGeo& g, int j) {
     return x < g.nsink ? x : x + g.lo;
 }
 
+// Bits 0 .. 31 set below x.
+__device__ __forceinline__ uint32_t bits_below(int x) { return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1; }
+
+// Which of 32 columns a query sees: [zero, sink) and [lo, hi), below hi and from
+// `zero` (the sequence's first key) on.  One bit test per column is cheaper than
+// comparisons with four bounds (16384 tokens, 32 heads, window 4096 and 4 sinks:
+// 860 us with those, 800 so).
+__device__ __forceinline__ uint32_t visible(int zero, int sink, int lo, int hi) {
+    return bits_below(hi) & ~bits_below(zero) & (bits_below(sink) | ~bits_below(lo));
+}
+
 template <bool kPaged, bool kAlt, bool kExt, class Params>
 __device__ __forceinline__ UnitGeo unit_geo(const Unit& u, const SeqInfo& s, int s0, int tps, const Params& p,
                                             int unit_slots) {
@@ -1410,10 +1421,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         const int hi = (tail ? min(row_hi[i], s.P) : row_hi[i]) - kb - half * kHalfCols;
                         if constexpr (kExt) {
                             // sink tokens stay visible below the window: columns [lo0, sink)
-                            const int lo0 = -kb - half * kHalfCols, sink = max(p.sinks, 0) + lo0;
+                            const int lo0 = -kb - half * kHalfCols, sink = p.sinks + lo0;
 #pragma unroll
-                            for (int c = 0; c < kHalfCols; ++c)
-                                if (c < lo0 || c >= hi || (c < lo && c >= sink)) sv[c] = -INFINITY;
+                            for (int c = 0; c < kHalfCols; c += 32) {
+                                const uint32_t seen = visible(lo0 - c, sink - c, lo - c, hi - c);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (!(seen >> e & 1)) sv[c + e] = -INFINITY;
+                            }
                         } else {
 #pragma unroll
                             for (int c = 0; c < kHalfCols; ++c)
@@ -1713,10 +1728,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     const int lo = max(-kb, row_lo - kb), hi = (tail ? min(row_hi, s.P) : row_hi) - kb;
                     if constexpr (kExt) {
                         // sink tokens stay visible below the window: columns [-kb, sink)
-                        const int sink = max(p.sinks, 0) - kb;
+                        const int sink = p.sinks - kb;
 #pragma unroll
-                        for (int c = 0; c < kBlockN; ++c)
-                            if (c < -kb || c >= hi || (c < lo && c >= sink)) sv[c] = -INFINITY;
+                        for (int c = 0; c < kBlockN; c += 32) {
+                            const uint32_t seen = visible(-kb - c, sink - c, lo - c, hi - c);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(seen >> e & 1)) sv[c + e] = -INFINITY;
+                        }
                     } else {
 #pragma unroll
                         for (int c = 0; c < kBlockN; ++c)
