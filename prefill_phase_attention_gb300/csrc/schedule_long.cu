@@ -182,25 +182,33 @@ __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(co
 
 // One row (token, head) per D / 4 lanes.  The lanes fetch the row's log-sum-exps
 // together (one load deep, whatever the number of slabs) and share their weights
-// by shuffles; the slabs' outputs are then fetched eight at a time.  The launch is
-// bound by these latencies for a few rows and by L2 for many (the slabs were just
-// written).
+// by shuffles; the slabs' outputs are fetched eight at a time, the first eight
+// while the log-sum-exps are on their way.  The launch is bound by these latencies
+// for a few rows and by L2 for many (the slabs were just written).
 template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ MergeArgs a) {
-    constexpr int kLanes = D / 4;
+    constexpr int kLanes = D / 4, kAtOnce = 8;
     griddep_wait();
     const long long rows = (long long)a.total_q * a.n_heads;
     const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
     const int l = threadIdx.x % kLanes;
     const unsigned lanes = kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1) << (threadIdx.x % 32 / kLanes * kLanes);
-    const bool in = at < rows;
-    const long long row = in ? at : 0;
-    const int own = in ? a.tok_pieces[row / a.n_heads] : 0;
-    if (own == 0) return;  // not this call's, or written by its unit (the row's lanes agree)
+    if (at >= rows) return;
+    const long long row = at;
+    const int token = (int)(row / a.n_heads), head = (int)(row % a.n_heads);
+    const int own = a.tok_pieces[token];
     int n = own;
-    if (a.pre_pieces)
-        n += __ldg(a.pre_pieces + row / a.n_heads / a.tokens_per_block * (a.n_heads / a.group) + row % a.n_heads / a.group);
+    if (a.pre_pieces) n += a.pre_pieces[token / a.tokens_per_block * (a.n_heads / a.group) + head / a.group];
+    if (own == 0) return;  // not this call's, or written by its unit (the row's lanes agree)
     auto slab = [&](int i) { return (size_t)(i < own ? i : a.prefix_slab + i - own) * rows + row; };
+    // (an empty piece's output was not written: whatever it holds gets no part)
+    float4 o[kAtOnce];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            if (i0 + i < n) o[i] = *reinterpret_cast<const float4*>(a.part_o + slab(i0 + i) * D + 4 * l);
+    };
+    fetch(0);
     // lane l holds slabs l, l + kLanes, ...; at most kMaxSlabs in all
     constexpr int kHeld = (kMaxSlabs + kLanes - 1) / kLanes;
     float w[kHeld], m = -INFINITY, sum = 0.f;
@@ -209,27 +217,27 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Merg
         w[h] = h * kLanes + l < n ? a.part_lse[slab(h * kLanes + l)] : -INFINITY;
         m = fmaxf(m, w[h]);
     }
-    for (int o = kLanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
+    for (int x = kLanes / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, x));
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
-        w[h] = w[h] == -INFINITY ? 0.f : exp2f(w[h] - m);  // 0: an empty piece, its output was not written
+        w[h] = w[h] == -INFINITY ? 0.f : exp2f(w[h] - m);
         sum += w[h];
     }
-    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(lanes, sum, o);
+    for (int x = kLanes / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(lanes, sum, x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    static_assert(kLanes % kAtOnce == 0, "the slabs fetched at once have their weights in one register");
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-        if (h * kLanes >= n) break;
-        const int k = min(kLanes, n - h * kLanes);
-#pragma unroll 8
-        for (int i = 0; i < k; ++i) {
-            const float wi = __shfl_sync(lanes, w[h], i, kLanes);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (wi != 0.f) o = *reinterpret_cast<const float4*>(a.part_o + slab(h * kLanes + i) * D + 4 * l);
-            acc.x = fmaf(wi, o.x, acc.x);
-            acc.y = fmaf(wi, o.y, acc.y);
-            acc.z = fmaf(wi, o.z, acc.z);
-            acc.w = fmaf(wi, o.w, acc.w);
+    for (int i0 = 0; i0 < kMaxSlabs; i0 += kAtOnce) {
+        if (i0 >= n) break;
+        if (i0 > 0) fetch(i0);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const float wi = __shfl_sync(lanes, w[i0 / kLanes], (i0 + i) % kLanes, kLanes);
+            if (i0 + i >= n || wi == 0.f) continue;
+            acc.x = fmaf(wi, o[i].x, acc.x);
+            acc.y = fmaf(wi, o[i].y, acc.y);
+            acc.z = fmaf(wi, o[i].z, acc.z);
+            acc.w = fmaf(wi, o[i].w, acc.w);
         }
     }
     const float inv = 1.f / sum;
