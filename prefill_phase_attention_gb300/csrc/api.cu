@@ -938,7 +938,7 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     if (merge) {
         pa::MergeArgs ma{p.part_o, p.part_lse, sa.tok_pieces, pre.len > 0 ? sa.pre_pieces : nullptr, tpu,
                          n_heads / n_kv_heads, max_pieces, static_cast<__nv_bfloat16*>(out), lse, total_q, n_heads};
-        e = pa::launch_merge(ma, head_dim, stream);
+        e = pa::launch_merge(ma, head_dim, sms, stream);
         if (e != cudaSuccess) return cuda_fail(e, "merge launch");
         ++launches;
     }

@@ -144,7 +144,7 @@ struct MergeArgs {
     float* lse;
     int total_q, n_heads;
 };
-cudaError_t launch_merge(const MergeArgs& a, int head_dim, cudaStream_t stream);
+cudaError_t launch_merge(const MergeArgs& a, int head_dim, int sms, cudaStream_t stream);
 
 // Weight each cached key collects from the new queries.
 struct KeyScheduleArgs : ScheduleArgs {

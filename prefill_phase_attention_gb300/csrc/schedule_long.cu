@@ -185,67 +185,76 @@ __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(co
 // by shuffles; the slabs' outputs are fetched eight at a time, the first eight
 // while the log-sum-exps are on their way.  The launch is bound by these latencies
 // for a few rows and by L2 for many (the slabs were just written).
-template <int D>
+template <int D, int kRows>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ MergeArgs a) {
-    constexpr int kLanes = D / 4, kAtOnce = 8;
+    constexpr int kLanes = D / 4, kAtOnce = kRows == 1 ? 8 : 4, kGroups = 256 / kLanes;
     griddep_wait();
     const long long rows = (long long)a.total_q * a.n_heads;
-    const long long at = ((long long)blockIdx.x * 256 + threadIdx.x) / kLanes;
+    const long long first = (long long)blockIdx.x * (kRows * kGroups) + threadIdx.x / kLanes;
     const int l = threadIdx.x % kLanes;
     const unsigned lanes = kLanes == 32 ? 0xffffffffu : ((1u << kLanes) - 1) << (threadIdx.x % 32 / kLanes * kLanes);
-    if (at >= rows) return;
-    const long long row = at;
-    const int token = (int)(row / a.n_heads), head = (int)(row % a.n_heads);
-    const int own = a.tok_pieces[token];
-    int n = own;
-    if (a.pre_pieces) n += a.pre_pieces[token / a.tokens_per_block * (a.n_heads / a.group) + head / a.group];
-    if (own == 0) return;  // not this call's, or written by its unit (the row's lanes agree)
-    auto slab = [&](int i) { return (size_t)(i < own ? i : a.prefix_slab + i - own) * rows + row; };
-    // (an empty piece's output was not written: whatever it holds gets no part)
-    float4 o[kAtOnce];
-    auto fetch = [&](int i0) {
+    int owns[kRows], all[kRows];  // slabs of the row: its token's own ones, and with its prefix unit's
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i)
-            if (i0 + i < n) o[i] = *reinterpret_cast<const float4*>(a.part_o + slab(i0 + i) * D + 4 * l);
-    };
-    fetch(0);
-    // lane l holds slabs l, l + kLanes, ...; at most kMaxSlabs in all
-    constexpr int kHeld = (kMaxSlabs + kLanes - 1) / kLanes;
-    float w[kHeld], m = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-        w[h] = h * kLanes + l < n ? a.part_lse[slab(h * kLanes + l)] : -INFINITY;
-        m = fmaxf(m, w[h]);
+    for (int k = 0; k < kRows; ++k) {
+        const long long row = first + k * kGroups;
+        owns[k] = all[k] = 0;
+        if (row >= rows) continue;
+        const int token = (int)(row / a.n_heads), head = (int)(row % a.n_heads);
+        owns[k] = a.tok_pieces[token];
+        if (a.pre_pieces) all[k] = a.pre_pieces[token / a.tokens_per_block * (a.n_heads / a.group) + head / a.group];
     }
-    for (int x = kLanes / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, x));
 #pragma unroll
-    for (int h = 0; h < kHeld; ++h) {
-        w[h] = w[h] == -INFINITY ? 0.f : exp2f(w[h] - m);
-        sum += w[h];
-    }
-    for (int x = kLanes / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(lanes, sum, x);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    static_assert(kLanes % kAtOnce == 0, "the slabs fetched at once have their weights in one register");
+    for (int k = 0; k < kRows; ++k) {
+        const long long row = first + k * kGroups;
+        const int own = owns[k], n = own + all[k];
+        if (own == 0) continue;  // not this call's, or written by its unit (the row's lanes agree)
+        auto slab = [&](int i) { return (size_t)(i < own ? i : a.prefix_slab + i - own) * rows + row; };
+        // (an empty piece's output was not written: whatever it holds gets no part)
+        float4 o[kAtOnce];
+        auto fetch = [&](int i0) {
 #pragma unroll
-    for (int i0 = 0; i0 < kMaxSlabs; i0 += kAtOnce) {
-        if (i0 >= n) break;
-        if (i0 > 0) fetch(i0);
+            for (int i = 0; i < kAtOnce; ++i)
+                if (i0 + i < n) o[i] = *reinterpret_cast<const float4*>(a.part_o + slab(i0 + i) * D + 4 * l);
+        };
+        fetch(0);
+        // lane l holds slabs l, l + kLanes, ...; at most kMaxSlabs in all
+        constexpr int kHeld = (kMaxSlabs + kLanes - 1) / kLanes;
+        float w[kHeld], m = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < kAtOnce; ++i) {
-            const float wi = __shfl_sync(lanes, w[i0 / kLanes], (i0 + i) % kLanes, kLanes);
-            if (i0 + i >= n || wi == 0.f) continue;
-            acc.x = fmaf(wi, o[i].x, acc.x);
-            acc.y = fmaf(wi, o[i].y, acc.y);
-            acc.z = fmaf(wi, o[i].z, acc.z);
-            acc.w = fmaf(wi, o[i].w, acc.w);
+        for (int h = 0; h < kHeld; ++h) {
+            w[h] = h * kLanes + l < n ? a.part_lse[slab(h * kLanes + l)] : -INFINITY;
+            m = fmaxf(m, w[h]);
         }
+        for (int x = kLanes / 2; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, x));
+#pragma unroll
+        for (int h = 0; h < kHeld; ++h) {
+            w[h] = w[h] == -INFINITY ? 0.f : exp2f(w[h] - m);
+            sum += w[h];
+        }
+        for (int x = kLanes / 2; x > 0; x >>= 1) sum += __shfl_xor_sync(lanes, sum, x);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        static_assert(kLanes % kAtOnce == 0, "the slabs fetched at once have their weights in one register");
+#pragma unroll
+        for (int i0 = 0; i0 < kMaxSlabs; i0 += kAtOnce) {
+            if (i0 >= n) break;
+            if (i0 > 0) fetch(i0);
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const float wi = __shfl_sync(lanes, w[i0 / kLanes], (i0 + i) % kLanes, kLanes);
+                if (i0 + i >= n || wi == 0.f) continue;
+                acc.x = fmaf(wi, o[i].x, acc.x);
+                acc.y = fmaf(wi, o[i].y, acc.y);
+                acc.z = fmaf(wi, o[i].z, acc.z);
+                acc.w = fmaf(wi, o[i].w, acc.w);
+            }
+        }
+        const float inv = 1.f / sum;
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        const uint2 packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        *reinterpret_cast<uint2*>(a.out + row * D + 4 * l) = packed;
+        if (l == 0 && a.lse) a.lse[row] = (m + log2f(sum)) * 0.69314718055994530942f;
     }
-    const float inv = 1.f / sum;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-    const uint2 packed = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-    *reinterpret_cast<uint2*>(a.out + row * D + 4 * l) = packed;
-    if (l == 0 && a.lse) a.lse[row] = (m + log2f(sum)) * 0.69314718055994530942f;
 }
 
 }  // namespace
@@ -258,10 +267,11 @@ cudaError_t launch_build_long_schedule(const LongScheduleArgs& a, cudaStream_t s
     return cudaGetLastError();
 }
 
-cudaError_t launch_merge(const MergeArgs& a, int head_dim, cudaStream_t stream) {
-    const long long threads = (long long)a.total_q * a.n_heads * (head_dim / 4);
+cudaError_t launch_merge(const MergeArgs& a, int head_dim, int sms, cudaStream_t stream) {
+    const long long threads = (long long)a.total_q * a.n_heads * (head_dim / 4), ctas = (threads + 255) / 256;
+    const bool many = ctas >= 8ll * sms;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((threads + 255) / 256));
+    cfg.gridDim = dim3((unsigned)(many ? (ctas + 3) / 4 : ctas));
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -270,9 +280,9 @@ cudaError_t launch_merge(const MergeArgs& a, int head_dim, cudaStream_t stream) 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     switch (head_dim) {
-        case 32: return cudaLaunchKernelEx(&cfg, merge_kernel<32>, a);
-        case 64: return cudaLaunchKernelEx(&cfg, merge_kernel<64>, a);
-        default: return cudaLaunchKernelEx(&cfg, merge_kernel<128>, a);
+        case 32: return cudaLaunchKernelEx(&cfg, many ? merge_kernel<32, 4> : merge_kernel<32, 1>, a);
+        case 64: return cudaLaunchKernelEx(&cfg, many ? merge_kernel<64, 4> : merge_kernel<64, 1>, a);
+        default: return cudaLaunchKernelEx(&cfg, many ? merge_kernel<128, 4> : merge_kernel<128, 1>, a);
     }
 }
 
