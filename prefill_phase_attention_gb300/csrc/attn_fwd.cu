@@ -230,26 +230,31 @@ __device__ __forceinline__ bool paged_tail_tile(int j, int P, int np) {
 // work on its rows, slot 0 on the even tiles of the stream and slot 1 on the
 // odd ones, so that the two still ping-pong on the tensor pipe, and the two
 // partial results are merged in the epilogue.
+struct UnitGeo {
+    int lo, ntiles, np;
+    int a[kSlots], b[kSlots];
+    bool alt;
+};
+
 // Long-context variant (kExt): the unit's stream is a piece, from stream position
 // s0 on, of the tiles its query block needs -- the sink tiles [0, nsink), then
 // the window's; lo is then the gap between a window tile and its stream
 // position -- and pre marks a block of the whole batch's queries against the
 // shared prefix.
-struct UnitGeo {
-    int lo, ntiles, np;
-    int a[kSlots], b[kSlots];
-    bool alt;
+struct UnitGeoX : UnitGeo {
     int s0, nsink;
     bool pre;
 };
 
 // Index in the sequence of tile j of the unit's stream.
-template <bool kExt>
-__device__ __forceinline__ int tile_at(const UnitGeo& g, int j) {
-    if constexpr (!kExt) return g.lo + j;
+__device__ __forceinline__ int tile_at(const UnitGeo& g, int j) { return g.lo + j; }
+__device__ __forceinline__ int tile_at(const UnitGeoX& g, int j) {
     const int x = g.s0 + j;
     return x < g.nsink ? x : x + g.lo;
 }
+
+__device__ __forceinline__ bool of_prefix(const UnitGeo&) { return false; }
+__device__ __forceinline__ bool of_prefix(const UnitGeoX& g) { return g.pre; }
 
 // Bits 0 .. 31 set below x.
 __device__ __forceinline__ uint32_t bits_below(int x) { return x >= 32 ? 0xffffffffu : x <= 0 ? 0u : (1u << x) - 1; }
@@ -262,41 +267,11 @@ __device__ __forceinline__ uint32_t visible(int zero, int sink, int lo, int hi) 
     return bits_below(hi) & ~bits_below(zero) & (bits_below(sink) | ~bits_below(lo));
 }
 
-template <bool kPaged, bool kAlt, bool kExt, class Params>
-__device__ __forceinline__ UnitGeo unit_geo(const Unit& u, const SeqInfo& s, int s0, int tps, const Params& p,
+template <bool kPaged, bool kAlt>
+__device__ __forceinline__ UnitGeo unit_geo(const Unit& u, const SeqInfo& s, int tps, int causal, int window,
                                             int unit_slots) {
     const int nslots = kAlt ? unit_slots : kSlots;  // Q tiles of a unit
-    const int causal = p.causal, window = p.window;
     UnitGeo g;
-    if constexpr (kExt) {
-        g.np = prefix_tiles(s.P);
-        g.pre = u.b == p.num_seqs;
-        g.s0 = s0;
-        g.ntiles = u.ntiles;
-        const StreamGeo all = stream_geo(s.n, s.P, u.q0, min(u.q0 + nslots * tps, s.n), causal, window, p.sinks, g.pre,
-                                         kPaged);
-        g.nsink = all.nsink;
-        g.lo = all.lo - all.nsink;
-#pragma unroll
-        for (int i = 0; i < kSlots; ++i) {
-            const int qs = u.q0 + i * tps;
-            g.a[i] = g.b[i] = 0;
-            if (i < nslots && qs < s.n) {
-                // with sink tokens every slot visits the stream from its start
-                const StreamGeo t = stream_geo(s.n, s.P, qs, min(qs + tps, s.n), causal, window, p.sinks, g.pre, kPaged);
-                const int a = max(p.sinks > 0 ? 0 : t.lo - all.lo, s0) - s0;
-                const int b = min(t.hi - all.lo + all.nsink, s0 + u.ntiles) - s0;
-                if (a < b) {
-                    g.a[i] = a;
-                    g.b[i] = b;
-                }
-            }
-        }
-        g.alt = kAlt && u.q0 + tps >= min(u.q0 + nslots * tps, s.n) && g.ntiles >= 2;
-        return g;
-    }
-    g.s0 = g.nsink = 0;
-    g.pre = false;
     g.np = prefix_tiles(s.P);
     const TileSpan all = query_tiles(s.n, s.P, u.q0, min(u.q0 + nslots * tps, s.n), causal, window, kPaged);
     g.lo = all.lo;
@@ -309,6 +284,39 @@ __device__ __forceinline__ UnitGeo unit_geo(const Unit& u, const SeqInfo& s, int
             const TileSpan t = query_tiles(s.n, s.P, qs, min(qs + tps, s.n), causal, window, kPaged);
             g.a[i] = t.lo - g.lo;
             g.b[i] = t.hi - g.lo;
+        }
+    }
+    g.alt = kAlt && u.q0 + tps >= min(u.q0 + nslots * tps, s.n) && g.ntiles >= 2;
+    return g;
+}
+
+// The same of the long-context variant (s0: UnitX::s0).
+template <bool kPaged, bool kAlt>
+__device__ __forceinline__ UnitGeoX unit_geo(const Unit& u, const SeqInfo& s, int s0, int tps, const FwdParamsX& p,
+                                            int unit_slots) {
+    const int nslots = kAlt ? unit_slots : kSlots;
+    UnitGeoX g;
+    g.np = prefix_tiles(s.P);
+    g.pre = u.b == p.num_seqs;
+    g.s0 = s0;
+    g.ntiles = u.ntiles;
+    const StreamGeo all = stream_geo(s.n, s.P, u.q0, min(u.q0 + nslots * tps, s.n), p.causal, p.window, p.sinks, g.pre,
+                                     kPaged);
+    g.nsink = all.nsink;
+    g.lo = all.lo - all.nsink;
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) {
+        const int qs = u.q0 + i * tps;
+        g.a[i] = g.b[i] = 0;
+        if (i < nslots && qs < s.n) {
+            // with sink tokens every slot visits the stream from its start
+            const StreamGeo t = stream_geo(s.n, s.P, qs, min(qs + tps, s.n), p.causal, p.window, p.sinks, g.pre, kPaged);
+            const int a = max(p.sinks > 0 ? 0 : t.lo - all.lo, s0) - s0;
+            const int b = min(t.hi - all.lo + all.nsink, s0 + u.ntiles) - s0;
+            if (a < b) {
+                g.a[i] = a;
+                g.b[i] = b;
+            }
         }
     }
     g.alt = kAlt && u.q0 + tps >= min(u.q0 + nslots * tps, s.n) && g.ntiles >= 2;
@@ -699,6 +707,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         }
     };
 
+    auto geo = [&](auto alt, const Unit& u, const SeqInfo& s, int s0) {
+        if constexpr (kExt)
+            return unit_geo<kPaged, decltype(alt)::value>(u, s, s0, tps, p, unit_slots);
+        else
+            return unit_geo<kPaged, decltype(alt)::value>(u, s, tps, p.causal, p.window, unit_slots);
+    };
+
     // Test hook (a kernel of its own, so that the product kernels' code is not
     // touched by it): the first CTA's producer thread waits on a barrier
     // nothing completes, so that the timeout path (error word, abort, drains,
@@ -741,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         int u_it = 0;            // units this group has taken so far
         Unit u{};                // the group's current unit ...
         SeqInfo s{};
-        UnitGeo ug{};
+        std::conditional_t<kExt, UnitGeoX, UnitGeo> ug{};
         const int32_t* tab = p.block_table;
         int j = 0, ntl = 0;      // ... its next tile and its tile count
         bool done = false;       // end of the unit list met (or a wait failed)
@@ -825,17 +840,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         break;
                     }
                     ++u_it;
-                    ug = unit_geo<true, kAlt, kExt>(u, s, s0, tps, p, unit_slots);
+                    ug = geo(std::bool_constant<kAlt>(), u, s, s0);
                     tab = p.block_table + (size_t)u.b * p.max_blocks;
                     if constexpr (kExt)
                         if (ug.pre) tab = p.prefix_table;
                     j = 0;
                     ntl = ug.ntiles;
-                    if (ntl > 0) fetch_ids(tile_at<kExt>(ug, 0), id0, id1);
+                    if (ntl > 0) fetch_ids(tile_at(ug, 0), id0, id1);
                 }
                 if (!done) {
-                    const int jj = tile_at<kExt>(ug, j);
-                    if (j + 1 < ntl) fetch_ids(tile_at<kExt>(ug, j + 1), nid0, nid1);  // in flight during this tile
+                    const int jj = tile_at(ug, j);
+                    if (j + 1 < ntl) fetch_ids(tile_at(ug, j + 1), nid0, nid1);  // in flight during this tile
                     const bool ok = gleader ? wait_bar(&empty[st], ph ^ 1, ctl, hdr) : true;
                     if (!__shfl_sync(gmask, ok, src)) {
                         done = true;
@@ -940,7 +955,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         tma_load_3d(q_smem + i * C::kTileBytes + c * C::kChunkBytes, &p.tm_q, &ctl->q_full,
                                     c * C::kChunkCols, u.kvh * G, s.q_start + u.q0 + i * tps);
                 last_q_parity[0] = u_it & 1;
-                const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(u, s, kExt ? ctl->ext[sl].x : 0, tps, p, unit_slots);
+                const auto ug = geo(std::bool_constant<kAlt>(), u, s, kExt ? ctl->ext[sl].x : 0);
                 const CUtensorMap* tm_c = &p.tm_ck;
                 int z = u.b * p.n_kv_heads + u.kvh;
                 if constexpr (kExt)
@@ -948,7 +963,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 bool ok = true;
                 for (int j = 0; j < ug.ntiles && ok; ++j, ++t)
                     ok = load_kv_tile<D, kQuant>(p, ctl, hdr, k_smem, kStK, ctl->k_full, ctl->k_empty, tm_c, &p.tm_k,
-                                                 last_k_parity, t, tile_at<kExt>(ug, j), u, s, ug.np, z);
+                                                 last_k_parity, t, tile_at(ug, j), u, s, ug.np, z);
                 if (!ok) break;
             }
             if (aborted(ctl)) {
@@ -967,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 const int s0 = kExt ? ctl->ext[sl].x : 0;
                 mbar_arrive(&ctl->unit_empty[sl]);
                 if (us.u.b < 0) break;
-                const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(us.u, us.s, s0, tps, p, unit_slots);
+                const auto ug = geo(std::bool_constant<kAlt>(), us.u, us.s, s0);
                 const CUtensorMap* tm_c = &p.tm_cv;
                 int z = us.u.b * p.n_kv_heads + us.u.kvh;
                 if constexpr (kExt)
@@ -975,7 +990,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 bool ok = true;
                 for (int j = 0; j < ug.ntiles && ok; ++j, ++t)
                     ok = load_kv_tile<D, kQuant>(p, ctl, hdr, v_smem, C::kStagesV, ctl->v_full, ctl->v_empty, tm_c,
-                                                 &p.tm_v, last_v_parity, t, tile_at<kExt>(ug, j), us.u, us.s, ug.np, z);
+                                                 &p.tm_v, last_v_parity, t, tile_at(ug, j), us.u, us.s, ug.np, z);
                 if (!ok) break;
             }
             if (aborted(ctl)) drain(ctl->v_full, last_v_parity, C::kStagesV);
@@ -1061,8 +1076,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             __syncwarp();
             if (leader) mbar_arrive(&ctl->unit_empty[sl]);
             if (u.b < 0) break;
-            const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(u, s, s0, tps, p, unit_slots);
-            auto at = [&](int j) { return tile_at<kExt>(ug, j); };
+            const auto ug = geo(std::bool_constant<kAlt>(), u, s, s0);
+            auto at = [&](int j) { return tile_at(ug, j); };
             const int ntiles = ug.ntiles;
             if (!warp_wait(&ctl->q_full, u_it & 1, ctl, hdr)) break;
             if constexpr (kAlt) if (ug.alt) {
@@ -1205,12 +1220,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->unit_empty[sl]);
             if (us.u.b < 0) break;
-            const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(us.u, us.s, s0, tps, p, unit_slots);
+            const auto ug = geo(std::bool_constant<kAlt>(), us.u, us.s, s0);
             const int np = ug.np;
             const int q_end = min(us.u.q0 + unit_slots * tps, us.s.n);
             bool ok = true;
             for (int jr = 0; jr < ug.ntiles; ++jr, ++t) {
-                const int j = tile_at<kExt>(ug, jr);  // tile index in the sequence
+                const int j = tile_at(ug, jr);  // tile index in the sequence
                 const int st = t % stages;
                 if (kQuant && j < np) {
                     // int8 prefix tile: expand the codes for the MMA.  V rows
@@ -1363,12 +1378,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             if (us.u.b < 0) break;
             const Unit u = us.u;
             const SeqInfo s = us.s;
-            const UnitGeo ug = unit_geo<kPaged, kAlt, kExt>(u, s, ext.x, tps, p, unit_slots);
+            const auto ug = geo(std::bool_constant<kAlt>(), u, s, ext.x);
             bool alt = false;
             if constexpr (kAlt) alt = ug.alt;
             const int np = ug.np;
-            const int Lk = kExt && ug.pre ? s.P : s.P + s.n;
-            const bool causal = p.causal && !(kExt && ug.pre);
+            const int Lk = of_prefix(ug) ? s.P : s.P + s.n;
+            const bool causal = p.causal && !of_prefix(ug);
             // rows of each slot (alt: both slots hold slot 0's rows)
             int tok[kSlots], row_hi[kSlots], slot_hi[kSlots], row_lo[kSlots], slot_lo[kSlots];
             bool valid[kSlots];
@@ -1412,7 +1427,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                             sv[32 + c] = __uint_as_float(r1[c]);
                         }
                     }
-                    const int jt = tile_at<kExt>(ug, j);  // tile index in the sequence
+                    const int jt = tile_at(ug, j);  // tile index in the sequence
                     const int kb = tile_key_base<kPaged>(jt, s.P, np);
                     // paged: the last prefix tile holds prefix keys only below P
                     const bool tail = kPaged && jt < np && kb + kBlockN > s.P;
@@ -1653,7 +1668,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             if (us.u.b < 0) break;
             const Unit u = us.u;
             const SeqInfo s = us.s;
-            const UnitGeo ug = unit_geo<kPaged, false, kExt>(u, s, ext.x, tps, p, unit_slots);
+            const auto ug = geo(std::bool_constant<false>(), u, s, ext.x);
             const int nt = ug.b[slot] - ug.a[slot];  // tiles of this slot: [a, b) of the stream
             const uint32_t tg0 = tg;
             tg += ug.ntiles;
@@ -1668,8 +1683,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             }
             if (nt == 0) continue;
             const int qe = min(qs + tps, s.n);
-            const int Lk = kExt && ug.pre ? s.P : s.P + s.n;
-            const bool causal = p.causal && !(kExt && ug.pre);
+            const int Lk = of_prefix(ug) ? s.P : s.P + s.n;
+            const bool causal = p.causal && !of_prefix(ug);
             const int row_hi = causal ? min(s.P + tok + 1, Lk) : Lk;  // keys [0, row_hi) visible
             const int slot_hi = causal ? min(s.P + qs + 1, Lk) : Lk;  // smallest row_hi of the slot
             // sliding window: keys [row_lo, row_hi) visible; slot_lo = largest row_lo of the slot
@@ -1704,7 +1719,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     }
                 }
                 const int jrel = ug.a[slot] + j;  // tile index in the unit's stream
-                const int jt = tile_at<kExt>(ug, jrel);  // tile index in the sequence
+                const int jt = tile_at(ug, jrel);  // tile index in the sequence
                 if (kQuant && jt < np) {
                     // int8 prefix tile: S holds q . code; scale column c by its row's scale
                     const uint32_t tc = tg0 + jrel;
