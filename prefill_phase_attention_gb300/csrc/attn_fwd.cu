@@ -44,6 +44,10 @@
 // (decode rows, short launches of one-tile units); there the softmax is
 // column-split: the two warps of a sub-partition take half of every row's
 // columns for both slots.
+// The long-context variant (kExt; compiled by attn_long_*.cu) serves windows with
+// sink tokens and batches that share a prefix.  Its units are pieces of a query
+// block's tiles (UnitX); a piece writes fp32 partial results, which merge_kernel
+// joins.  Few units: no scheduler runs, every CTA plans for itself first.
 // Every wait is bounded in time; on timeout the CTA records PA_DEVERR_TIMEOUT,
 // drains its in-flight copies and MMAs, frees TMEM and returns.
 #include <cuda.h>

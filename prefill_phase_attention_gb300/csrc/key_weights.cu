@@ -36,6 +36,12 @@
 // An int8 key tile is expanded in place by its group first (exact codes; the row
 // scale multiplies the scores).  Every wait is bounded in time, as in the
 // attention kernel.
+//
+// Measured (graph): 8192 tokens, 32 heads, D = 128: 208 us, 1.32 PFLOP/s; the
+// tensor pipe and the exponentials are each in use 58 % of the time, for a group
+// waits for its MMA and the MMA for the group's S buffer (all 512 TMEM columns are
+// in use).  64 decode rows over 256-4096 cached tokens: 55 us, 6.1 TB/s in the
+// kernel.
 #include <cuda_bf16.h>
 
 #include <climits>

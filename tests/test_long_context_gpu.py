@@ -143,6 +143,17 @@ def test_sinks_prompts(d, group, block, schedule):
     ok()
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 1), (1, 128), (127, 129), (128, 128), (129, 256), (300, 257), (257, 500), (640, 5)])
+@pytest.mark.parametrize("block,int8", [(0, False), (16, False), (0, True), (16, True)])
+def test_sinks_of_several_tiles_under_prompts(block, int8, window, sinks):
+    """Units of two query tiles on every side of where the window leaves the sink tiles."""
+    for group, lens in ((1, [0, 77, 640]), (4, [128, 0, 333])):
+        c = Call(31, [1030, 257, 700], lens, 64, 1, group, block, int8)
+        c.sinks(window, sinks, schedule=2)
+        c.check(window=window, sinks=sinks)
+    ok()
+
+
 @pytest.mark.parametrize("window,sinks", [(2500, 4), (6000, 200), (100, 129)])
 @pytest.mark.parametrize("block,int8", [(0, False), (16, False), (0, True)])
 def test_sinks_one_long_row_is_split(block, int8, window, sinks):
