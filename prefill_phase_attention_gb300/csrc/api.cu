@@ -845,7 +845,7 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     const long long slab_bytes = slab_rows * (head_dim + 1) * 4;
     const int fit = (int)std::max(1ll, std::min((long long)kMaxPieces, kPartialBytes / slab_bytes));
     // a row under a short window is not cut: its few tiles cost less than the merge's
-    // launch (one row, window 256: 13.6 us whole, 14.7 in two pieces; 16 and 20 from Python)
+    // launch (one row, window 256: 11.4 us whole, 12.9 in two pieces; 14 and 16 from Python)
     const long long most_tiles = o.window ? ((long long)o.window + sinks) / pa::kBlockN + 3 : LLONG_MAX;
     const int max_pieces = most_tiles <= kUncutTiles ? 1 : fit;
     // a prefix of fewer units than wanted is cut to make as many; of one with more

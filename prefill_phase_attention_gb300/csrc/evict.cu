@@ -26,9 +26,10 @@
 // is bound by latency: evict_kernel does both in one launch, a cluster of 2, 4
 // or 8 CTAs (its column parts) per (sequence, head).  A larger one is bound by
 // HBM, and a CTA that selects moves no bytes: select_kernel runs first, one CTA
-// (or a cluster) per (sequence, head), then move_kernel.  Measured (graph): 4
-// sequences of about 510 tokens, 8 heads, to 384: 7.7 us; 16 of 16384 to 4096: 111
-// us (select 19, move 85 at 6.3 TB/s).
+// (or a cluster) per (sequence, head), then move_kernel.  Measured (graph, 8 heads):
+// 4 sequences of about 510 tokens to 384 7.8 us in one launch, 10.1 in two; 16 of
+// 16384 to 4096 133 and 110 (select 19, move 85 at 6.3 TB/s); 64 of 700-4099 to
+// 1024 in int8 pages 97 and 62.6.
 #include <cooperative_groups.h>
 
 #include <cstdint>
@@ -47,10 +48,9 @@ namespace cg = cooperative_groups;
 constexpr int kVec = 2;  // 16-byte pieces per thread and chunk of the move
 // one-launch form: threads, weights a thread holds (so tokens a CTA selects from alone)
 constexpr int kFusedThreads = 256, kFusedHeld = 8;
-// two-launch form: select CTAs of 256 threads for caches of up to 8192 tokens a
-// slot, of 512 for longer ones (64 sequences of 700-4099 tokens in int8 pages:
-// 72.8 us with 256, 81.6 with 512; 16 of 16384 tokens: 120.7 and 116.7)
-constexpr int kSelectHeld = 16, kMoveThreads = 256;
+// two-launch form (select CTAs of 512 threads: 70.0 us against 62.6 for 64 sequences
+// of 700-4099 tokens in int8 pages, within 1 % for 16 of 16384, 32768 and 65536)
+constexpr int kSelectThreads = 256, kSelectHeld = 16, kMoveThreads = 256;
 // Weights crowd into a few digits: a histogram has this many copies, one per
 // lane & 7, a bank apart, so that a warp's equal digits do not queue up.
 constexpr int kCopies = 8;
@@ -461,8 +461,7 @@ __global__ void __launch_bounds__(kFusedThreads, 4) evict_kernel(const __grid_co
     if (len > a.budget) move_rows<kFusedThreads>(a, b, h, a.budget, rank & 1, rank >> 1, list);
 }
 
-template <int kSelectThreads>
-__global__ void __launch_bounds__(kSelectThreads, 1024 / kSelectThreads) select_kernel(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kSelectThreads, 4) select_kernel(const __grid_constant__ EvictArgs a) {
     __shared__ Shared<kSelectThreads, kSelectHeld> sh;
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
@@ -528,13 +527,12 @@ cudaError_t launch_evict(const EvictArgs& args, int sms, int* launches, cudaStre
         *launches = 1;
         return cudaLaunchKernelEx(&cfg, evict_kernel, a);
     }
-    const int threads = a.max_cache_len <= 2 * 256 * kSelectHeld ? 256 : 512;
     int ranks = 1;
-    while (ranks < 8 && a.max_cache_len > ranks * threads * kSelectHeld) ranks *= 2;
+    while (ranks < 8 && a.max_cache_len > ranks * kSelectThreads * kSelectHeld) ranks *= 2;
     attr[0].val.clusterDim.x = (unsigned)ranks;
     cfg.gridDim = dim3((unsigned)(ranks * heads));
-    cfg.blockDim = dim3((unsigned)threads);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, threads == 256 ? select_kernel<256> : select_kernel<512>, a);
+    cfg.blockDim = dim3(kSelectThreads);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, a);
     if (e != cudaSuccess) return e;
     const int others = (a.kept_weights ? 1 : 0) + (a.scale_k ? 2 : 0);
     cfg.gridDim = dim3((unsigned)((2 * parts + others) * heads));

@@ -185,9 +185,10 @@ __global__ void __launch_bounds__(kFewThreads) build_long_schedule_few_kernel(co
 // by shuffles; the slabs' outputs are fetched eight at a time, the first eight
 // while the log-sum-exps are on their way.  The launch is bound by these latencies
 // for a few rows and by L2 for many (the slabs were just written); many rows go
-// four to a lane group, their slab counts looked up together (59000 rows of 3.5
-// slabs on average, D = 128, cold caches: 35 us with one row each, 30 with four;
-// 37 with the first slabs of all four fetched ahead, at 80 registers).
+// four to a lane group, their slab counts looked up together.  (59000 rows of 3.5
+// slabs on average, D = 128, cold caches: 35 us with one row each, 30 with four, 37
+// with the first slabs of all four fetched ahead, at 80 registers; the whole call of
+// 2048 rows 134 with one, 141 with four.)
 template <int D, int kRows>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ MergeArgs a) {
     constexpr int kLanes = D / 4, kAtOnce = kRows == 1 ? 8 : 4, kGroups = 256 / kLanes;

@@ -14,9 +14,9 @@
 // Piece size (piece_tiles): with fewer units than CTAs, what makes one round of
 // pieces; else the whole call's tiles over twice the CTAs; at least min_tiles.  A
 // sequence that would gain less than kCutGain tiles by it is not cut, unless the
-// call merges anyway.  (One decode row of 8 KV heads, graph: 10 tiles whole 18.5
-// us, in pieces of 4 15.4; 34 tiles 38.1 and 20.1.  Eight rows: 10 tiles whole
-// 19.5, in pieces of 4, which are more than a round, 25.7.)
+// call merges anyway.  (Decode rows of 8 KV heads, graph: one row of 10 tiles whole
+// 16.3 us, in pieces of 4 14.8; of 34 tiles 36.3 and 17.5; eight rows of 34 tiles
+// 40.4 and 34.2.)
 // All blocks of a sequence get the same number of pieces (that of its longest
 // block); a block with fewer tiles than pieces leaves holes in the list.  Of a
 // prefix with more units than CTAs, whole rounds of units stay uncut and only the

@@ -416,6 +416,15 @@ def test_evict_weights_that_share_leading_bits(spread, heads):
     ok()
 
 
+@pytest.mark.parametrize("lens,block,kept", [([9000, 4097], 0, "same"), ([8193, 300], 16, "new"), ([33500, 4096], 0, "same")])
+def test_evict_of_many_long_heads(lens, block, kept):
+    """Two launches, the select by clusters: shares that a CTA's threads hold at once, and longer ones."""
+    c = Call(92, [0, 0], lens, 32, 77, 1, block)
+    evict(c, weights_for(c, 4, "ties" if block else "special"), 1000, 4, 100, kept=kept)
+    assert binding.prefill_attn_last_launch_count() == 2
+    ok()
+
+
 def test_evict_equal_weights_keeps_the_first():
     c = Call(96, [0], [1500], 64, 1, 1)
     evict(c, torch.zeros(c.cache.shape[:-1]), 600, 2, 10)
