@@ -73,7 +73,7 @@ typedef enum {
     PA_OK = 0,
     PA_ERR_INVALID_ARG = 1,     /* a host-checkable argument is wrong */
     PA_ERR_UNSUPPORTED = 2,     /* valid, but outside what this build implements */
-    PA_ERR_CUDA = 3,            /* a CUDA runtime/driver call failed */
+    PA_ERR_CUDA = 3,            /* a CUDA runtime/driver call failed, or host memory ran out */
     PA_ERR_DEVICE_TIMEOUT = 4,  /* a kernel gave up waiting (bounded wait) */
     PA_ERR_DEVICE_METADATA = 5, /* device metadata was inconsistent; sequences skipped */
     PA_ERR_DEVICE_LAYOUT = 6    /* a kernel found its shared-memory window misaligned; it computed nothing */

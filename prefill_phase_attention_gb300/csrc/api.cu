@@ -9,9 +9,10 @@
 #include <cstdio>
 #include <cstring>
 #include <algorithm>
+#include <exception>
 #include <map>
 #include <mutex>
-#include <string>
+#include <new>
 #include <utility>
 #include <vector>
 
@@ -21,22 +22,34 @@
 
 namespace {
 
-thread_local std::string g_last_error;
+thread_local char g_last_error[512];
 thread_local int g_last_launches = 0;
 thread_local int g_last_schedule = 0;
 
 pa_status fail(pa_status s, const char* fmt, ...) {
-    char buf[512];
     va_list ap;
     va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
+    vsnprintf(g_last_error, sizeof g_last_error, fmt, ap);
     va_end(ap);
-    g_last_error = buf;
     return s;
 }
 
 pa_status cuda_fail(cudaError_t e, const char* what) {
     return fail(PA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
+}
+
+// The status of the exception being handled.  Every C entry ends with it: an
+// exception that left one would end the caller's process.
+pa_status caught() noexcept {
+    try {
+        throw;
+    } catch (const std::bad_alloc&) {
+        return fail(PA_ERR_CUDA, "out of host memory");
+    } catch (const std::exception& e) {
+        return fail(PA_ERR_CUDA, "%s", e.what());
+    } catch (...) {
+        return fail(PA_ERR_CUDA, "unknown exception");
+    }
 }
 
 struct Workspace {
@@ -55,6 +68,12 @@ struct Workspace {
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 std::vector<std::pair<int, void*>> g_retired;  // (device, block) outgrown but held by a captured graph
+
+// Room in g_retired for one more block, made before the block that replaces it is
+// allocated: nothing throws in between.
+void prepare_drop(const Workspace& w) {
+    if (w.captured) g_retired.reserve(g_retired.size() + 1);
+}
 
 // Gives up a block of a workspace that has been replaced by a larger one.
 void drop_block(const Workspace& w, int dev, void* ptr, cudaStream_t st) {
@@ -107,6 +126,10 @@ pa_status get_workspace(int dev, cudaStream_t st, int num_seqs, int max_units, W
     nw.max_seqs = std::max(num_seqs, std::max(w.max_seqs, 64));
     nw.max_units = std::max(max_units, std::max(w.max_units, 4096));
     nw.bytes = ws_bytes(nw.max_seqs, nw.max_units);
+    nw.captured = w.captured;
+    nw.old_headers = w.old_headers;
+    if (w.captured && w.ptr) nw.old_headers.push_back(w.ptr);
+    prepare_drop(w);
     cudaError_t e = cudaMallocAsync(&nw.ptr, nw.bytes, st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(workspace)");
     e = cudaMemsetAsync(nw.ptr, 0, sizeof(pa::WorkspaceHeader), st);
@@ -116,15 +139,12 @@ pa_status get_workspace(int dev, cudaStream_t st, int num_seqs, int max_units, W
         cudaFreeAsync(nw.ptr, st);
         return cuda_fail(e, "workspace init");
     }
-    nw.captured = w.captured;
-    nw.old_headers = w.old_headers;
-    if (w.captured && w.ptr) nw.old_headers.push_back(w.ptr);
     drop_block(w, dev, w.ptr, st);
     nw.rope = w.rope;  // the rotary and auxiliary scratch are grown on their own
     nw.rope_bytes = w.rope_bytes;
     nw.aux = w.aux;
     nw.aux_bytes = w.aux_bytes;
-    w = nw;
+    w = std::move(nw);
     *out = &w;
     return PA_OK;
 }
@@ -138,6 +158,7 @@ pa_status get_rope_scratch(Workspace* w, int dev, cudaStream_t st, size_t bytes,
                     "rope_theta of at least these sizes on this stream before capturing",
                     bytes);
     if (w->rope_bytes < bytes) {
+        prepare_drop(*w);
         void* nptr = nullptr;
         cudaError_t e = cudaMallocAsync(&nptr, bytes, st);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(rotary scratch)");
@@ -158,6 +179,7 @@ pa_status get_aux_scratch(Workspace* w, int dev, cudaStream_t st, size_t bytes, 
                     "least these sizes on this stream before capturing",
                     bytes);
     if (w->aux_bytes < bytes) {
+        prepare_drop(*w);
         void* nptr = nullptr;
         cudaError_t e = cudaMallocAsync(&nptr, bytes, st);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(auxiliary scratch)");
@@ -483,7 +505,7 @@ const char* prefill_attn_status_string(pa_status s) {
     return "PA_ERR_UNKNOWN";
 }
 
-const char* prefill_attn_last_error(void) { return g_last_error.c_str(); }
+const char* prefill_attn_last_error(void) { return g_last_error; }
 
 int prefill_attn_last_launch_count(void) { return g_last_launches; }
 
@@ -510,8 +532,8 @@ pa_status prefill_attn_varlen_ex(const void* q, const void* k, const void* v, co
                                  const int32_t* cu_seqlens_k, void* cache_k, void* cache_v,
                                  const int32_t* cache_offsets, void* out, float* lse, int num_seqs, int total_q,
                                  int max_cache_len, int n_heads, int n_kv_heads, int head_dim, float scale,
-                                 int causal, const pa_options* opts, pa_stream_t stream_) {
-    g_last_error.clear();
+                                 int causal, const pa_options* opts, pa_stream_t stream_) try {
+    g_last_error[0] = 0;
     g_last_launches = 0;
     g_last_schedule = 0;
     Options o;
@@ -547,19 +569,21 @@ pa_status prefill_attn_varlen_ex(const void* q, const void* k, const void* v, co
     return enqueue(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs, total_q,
                    max_cache_len, n_heads, n_kv_heads, head_dim, scale, causal, o, scr, max_units_ll, sched, sms,
                    stream);
+} catch (...) {
+    return caught();
 }
 
 pa_status prefill_attn_varlen_validate(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
                                        const int32_t* cu_seqlens_k, void* cache_k, void* cache_v,
                                        const int32_t* cache_offsets, void* out, float* lse, int num_seqs,
                                        int total_q, int max_cache_len, int n_heads, int n_kv_heads, int head_dim,
-                                       float scale, int causal, pa_stream_t stream_) {
-    g_last_error.clear();
+                                       float scale, int causal, pa_stream_t stream_) try {
+    g_last_error[0] = 0;
     pa_status s = check_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse,
                              num_seqs, total_q, max_cache_len, n_heads, n_kv_heads, head_dim, scale, causal);
     if (s != PA_OK || num_seqs == 0) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    std::vector<int32_t> cq(num_seqs + 1), ck(num_seqs + 1), of(num_seqs);
+    std::vector<int32_t> cq((size_t)num_seqs + 1), ck((size_t)num_seqs + 1), of(num_seqs);
     cudaError_t e = cudaMemcpyAsync(cq.data(), cu_seqlens_q, cq.size() * 4, cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess) e = cudaMemcpyAsync(ck.data(), cu_seqlens_k, ck.size() * 4, cudaMemcpyDeviceToHost, stream);
     if (e == cudaSuccess) e = cudaMemcpyAsync(of.data(), cache_offsets, of.size() * 4, cudaMemcpyDeviceToHost, stream);
@@ -581,10 +605,12 @@ pa_status prefill_attn_varlen_validate(const void* q, const void* k, const void*
                         (long long)of[b] + n, max_cache_len);
     }
     return PA_OK;
+} catch (...) {
+    return caught();
 }
 
-pa_status prefill_attn_device_status(pa_stream_t stream_, int32_t* flags) {
-    g_last_error.clear();
+pa_status prefill_attn_device_status(pa_stream_t stream_, int32_t* flags) try {
+    g_last_error[0] = 0;
     if (flags) *flags = 0;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     int dev = 0;
@@ -615,9 +641,11 @@ pa_status prefill_attn_device_status(pa_stream_t stream_, int32_t* flags) {
     if (word & PA_DEVERR_TIMEOUT) return fail(PA_ERR_DEVICE_TIMEOUT, "device error word 0x%x", word);
     if (word & PA_DEVERR_SMEM_ALIGN) return fail(PA_ERR_DEVICE_LAYOUT, "device error word 0x%x", word);
     return fail(PA_ERR_DEVICE_METADATA, "device error word 0x%x", word);
+} catch (...) {
+    return caught();
 }
 
-void prefill_attn_release(void) {
+void prefill_attn_release(void) try {
     std::lock_guard<std::mutex> lock(g_mu);
     int cur = 0;
     cudaGetDevice(&cur);
@@ -634,6 +662,7 @@ void prefill_attn_release(void) {
     g_retired.clear();
     cudaSetDevice(cur);
     g_ws.clear();
+} catch (...) {
 }
 
 
@@ -719,8 +748,8 @@ extern "C" pa_status prefill_attn_varlen_noalloc(const void* q, const void* k, c
                                                  void* cache_k, void* cache_v, const int32_t* cache_offsets,
                                                  void* out, float* lse, int num_seqs, int total_q,
                                                  int max_cache_len, int n_heads, int n_kv_heads, int head_dim,
-                                                 float scale, int causal, pa_stream_t stream_) {
-    g_last_error.clear();
+                                                 float scale, int causal, pa_stream_t stream_) try {
+    g_last_error[0] = 0;
     g_last_launches = 0;
     g_last_schedule = 0;
     pa_status s = check_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse,
@@ -753,6 +782,8 @@ extern "C" pa_status prefill_attn_varlen_noalloc(const void* q, const void* k, c
     return enqueue(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs, total_q,
                    max_cache_len, n_heads, n_kv_heads, head_dim, scale, causal, Options(), scr, units, sched, sms,
                    stream);
+} catch (...) {
+    return caught();
 }
 
 // ---------------------------------------------------------------------------
@@ -981,8 +1012,8 @@ pa_status prefill_attn_varlen_sinks(const void* q, const void* k, const void* v,
                                     const int32_t* cu_seqlens_k, void* cache_k, void* cache_v,
                                     const int32_t* cache_offsets, void* out, float* lse, int num_seqs, int total_q,
                                     int max_cache_len, int n_heads, int n_kv_heads, int head_dim, float scale,
-                                    int sink_tokens, const pa_options* opts, pa_stream_t stream_) {
-    g_last_error.clear();
+                                    int sink_tokens, const pa_options* opts, pa_stream_t stream_) try {
+    g_last_error[0] = 0;
     g_last_launches = 0;
     g_last_schedule = 0;
     Options o;
@@ -1004,6 +1035,8 @@ pa_status prefill_attn_varlen_sinks(const void* q, const void* k, const void* v,
                         total_q, max_cache_len, n_heads, n_kv_heads, head_dim, scale, 1,
                         clamp_span(sink_tokens, max_cache_len), Prefix(), o,
                         reinterpret_cast<cudaStream_t>(stream_));
+} catch (...) {
+    return caught();
 }
 
 pa_status prefill_attn_varlen_prefix(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
@@ -1011,8 +1044,8 @@ pa_status prefill_attn_varlen_prefix(const void* q, const void* k, const void* v
                                      const int32_t* cache_offsets, void* out, float* lse, int num_seqs, int total_q,
                                      int max_cache_len, int n_heads, int n_kv_heads, int head_dim, float scale,
                                      int causal, const pa_prefix* prefix, const pa_options* opts,
-                                     pa_stream_t stream_) {
-    g_last_error.clear();
+                                     pa_stream_t stream_) try {
+    g_last_error[0] = 0;
     g_last_launches = 0;
     g_last_schedule = 0;
     Options o;
@@ -1037,14 +1070,16 @@ pa_status prefill_attn_varlen_prefix(const void* q, const void* k, const void* v
     return enqueue_long(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs,
                         total_q, max_cache_len, n_heads, n_kv_heads, head_dim, scale, causal, 0, pre, o,
                         reinterpret_cast<cudaStream_t>(stream_));
+} catch (...) {
+    return caught();
 }
 
 pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* cu_seqlens_q,
                                    const int32_t* cu_seqlens_k, const void* cache_k, const int32_t* cache_offsets,
                                    const float* lse, float* weights, int num_seqs, int total_q, int max_cache_len,
                                    int n_heads, int n_kv_heads, int head_dim, float scale, int causal,
-                                   int sink_tokens, int prefix_len, const pa_options* opts, pa_stream_t stream_) {
-    g_last_error.clear();
+                                   int sink_tokens, int prefix_len, const pa_options* opts, pa_stream_t stream_) try {
+    g_last_error[0] = 0;
     g_last_launches = 0;
     g_last_schedule = 0;
     Options o;
@@ -1125,13 +1160,15 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
     if (e != cudaSuccess) return cuda_fail(e, "key weight launch");
     g_last_launches = launches;
     return PA_OK;
+} catch (...) {
+    return caught();
 }
 
 pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights, const int32_t* lengths,
                              int32_t* kept_lengths, int32_t* kept_index, float* kept_weights, int num_seqs,
                              int max_cache_len, int n_kv_heads, int head_dim, int budget, int sink_tokens,
-                             int recent_tokens, const pa_options* opts, pa_stream_t stream_) {
-    g_last_error.clear();
+                             int recent_tokens, const pa_options* opts, pa_stream_t stream_) try {
+    g_last_error[0] = 0;
     g_last_launches = 0;
     g_last_schedule = 0;
     Options o;
@@ -1224,6 +1261,8 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
     g_last_launches = launches;
     return PA_OK;
+} catch (...) {
+    return caught();
 }
 
 }  // extern "C"
