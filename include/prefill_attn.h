@@ -41,6 +41,9 @@
  *   - out must not alias q, k or v; the caches must not alias k or v.
  *   - Inputs are assumed finite.  Cache entries outside [0, P_b) of each slot are
  *     never read, so an uninitialised cache is fine.
+ *   - Threads: calls may come from any host thread.  Calls on one stream at once
+ *     are enqueued one after the other (prefill_attn_varlen_noalloc leaves that to
+ *     the caller); prefill_attn_release must not run beside another call.
  *   - CUDA graphs: prefill_attn_varlen / _ex calls enqueue only kernels and
  *     device copies, so they may be captured into a graph, on a stream that
  *     already ran a call (outside the capture) with at least the same

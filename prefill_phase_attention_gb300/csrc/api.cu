@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <exception>
 #include <map>
+#include <memory>
 #include <mutex>
 #include <new>
 #include <utility>
@@ -53,6 +54,7 @@ pa_status caught() noexcept {
 }
 
 struct Workspace {
+    std::shared_ptr<std::mutex> mu;  // see StreamLock
     void* ptr = nullptr;
     size_t bytes = 0;
     int max_units = 0;
@@ -68,6 +70,23 @@ struct Workspace {
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
 std::vector<std::pair<int, void*>> g_retired;  // (device, block) outgrown but held by a captured graph
+
+// Held by a call from its first look at its stream's workspace to its last launch.
+// A call's kernels hand data to one another through that workspace, and a call may
+// replace its blocks: two host threads that call on one stream must not mix their
+// launches.  (The lock outlives a release of the workspace.)
+struct StreamLock {
+    std::shared_ptr<std::mutex> mu;
+    std::unique_lock<std::mutex> held;
+    StreamLock(int dev, cudaStream_t st) : mu(of(dev, st)), held(*mu) {}
+
+    static std::shared_ptr<std::mutex> of(int dev, cudaStream_t st) {
+        std::lock_guard<std::mutex> lock(g_mu);
+        Workspace& w = g_ws[std::make_pair(dev, st)];
+        if (!w.mu) w.mu = std::make_shared<std::mutex>();
+        return w.mu;
+    }
+};
 
 // Room in g_retired for one more block, made before the block that replaces it is
 // allocated: nothing throws in between.
@@ -126,6 +145,7 @@ pa_status get_workspace(int dev, cudaStream_t st, int num_seqs, int max_units, W
     nw.max_seqs = std::max(num_seqs, std::max(w.max_seqs, 64));
     nw.max_units = std::max(max_units, std::max(w.max_units, 4096));
     nw.bytes = ws_bytes(nw.max_seqs, nw.max_units);
+    nw.mu = w.mu;
     nw.captured = w.captured;
     nw.old_headers = w.old_headers;
     if (w.captured && w.ptr) nw.old_headers.push_back(w.ptr);
@@ -557,6 +577,7 @@ pa_status prefill_attn_varlen_ex(const void* q, const void* k, const void* v, co
     const int slots = sched == 1 ? 1 : pa::kSlots;
     const long long max_units_ll = unit_bound(total_q, num_seqs, n_heads, n_kv_heads, slots);
     if (max_units_ll >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
+    const StreamLock lock(dev, stream);
     Workspace* ws = nullptr;
     s = get_workspace(dev, stream, num_seqs, (int)max_units_ll, &ws);
     if (s != PA_OK) return s;
@@ -618,6 +639,7 @@ pa_status prefill_attn_device_status(pa_stream_t stream_, int32_t* flags) try {
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
+    const StreamLock own(dev, stream);  // (no call replaces the workspace meanwhile)
     std::vector<void*> words = {noalloc_scratch_if_set_up()};  // and the workspace, outgrown ones that graphs use included
     {
         std::lock_guard<std::mutex> lock(g_mu);
@@ -894,6 +916,7 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     const long long units =
         std::min(own_units * max_pieces + pre_units * std::max(1, max_prefix_pieces), own_units + pre_units + 4 * target);
     if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
+    const StreamLock lock(dev, stream);
     Workspace* ws = nullptr;
     s = get_workspace(dev, stream, num_seqs + 1, 0, &ws);
     if (s != PA_OK) return s;
@@ -1125,6 +1148,7 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
     const long long tiles = ((long long)max_cache_len + pa::kBlockN - 1) / pa::kBlockN + 1;
     const long long units = (long long)num_seqs * n_kv_heads * ((tiles + 1) / 2);
     if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
+    const StreamLock lock(dev, stream);
     Workspace* ws = nullptr;
     s = get_workspace(dev, stream, num_seqs, (int)units, &ws);
     if (s != PA_OK) return s;
@@ -1225,6 +1249,7 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     const int sms = sm_count(dev, &s);
     if (s != PA_OK) return s;
+    const StreamLock lock(dev, stream);
     Workspace* ws = nullptr;
     s = get_workspace(dev, stream, 0, 0, &ws);
     if (s != PA_OK) return s;
