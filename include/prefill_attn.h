@@ -270,7 +270,7 @@ pa_status prefill_attn_varlen_ex(
  * have been given back.  A few long rows are split along their keys and joined
  * by one more kernel; the partial results (fp32, at most 64 MiB) live in the
  * per-stream workspace.  Under graph capture the stream must already have run a
- * call of at least these sizes.  max_cache_len is at most 2^30.
+ * call of at least these sizes.  num_seqs and max_cache_len are at most 2^30.
  */
 pa_status prefill_attn_varlen_sinks(
     const void *q, const void *k, const void *v,
@@ -319,8 +319,8 @@ typedef struct pa_prefix {
  * up to 64 MiB for the own part and 256 MiB for the prefix's, and at least
  * total_q * n_heads * (head_dim + 1) * 4 bytes for each).  Every option of
  * pa_options applies but window and wait_timeout_test.  len = 0 is
- * prefill_attn_varlen_ex.  len and max_cache_len are at most 2^30.  A prefix
- * block outside the pool rejects the whole call on the device
+ * prefill_attn_varlen_ex.  len, num_seqs and max_cache_len are at most 2^30.  A
+ * prefix block outside the pool rejects the whole call on the device
  * (PA_DEVERR_METADATA, nothing written).  Under graph capture the stream must
  * already have run a call of at least these sizes.
  */
@@ -358,7 +358,8 @@ pa_status prefill_attn_varlen_prefix(
  * inputs give equal bits.  Sequences of a paged call must not share blocks that
  * hold cached keys their queries see: such a block's weights would be added to
  * by several thread blocks at once.  A sequence with inconsistent metadata is
- * skipped (PA_DEVERR_METADATA).  max_cache_len and prefix_len are at most 2^30.
+ * skipped (PA_DEVERR_METADATA).  num_seqs, max_cache_len and prefix_len are at
+ * most 2^30.
  * Other arguments as in prefill_attn_varlen.
  */
 pa_status prefill_attn_key_weights(

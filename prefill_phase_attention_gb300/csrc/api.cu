@@ -1008,11 +1008,13 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
 }
 
 // The kernels' position arithmetic stays within 32 bits: positions and spans are
-// at most kMaxTokens each, so the sum of two fits.  A window or sink count past
+// at most kMaxTokens each, so the sum of two fits, and so do the schedulers' loops
+// over as many sequences, which step 1024 at a time.  A window or sink count past
 // the cache's capacity says the same as the capacity.
 constexpr int kMaxTokens = 1 << 30;
 
-pa_status check_capacity(int max_cache_len, int prefix_len) {
+pa_status check_capacity(int num_seqs, int max_cache_len, int prefix_len) {
+    if (num_seqs > kMaxTokens) return fail(PA_ERR_UNSUPPORTED, "num_seqs (%d) must be at most 2^30", num_seqs);
     if (max_cache_len > kMaxTokens || prefix_len > kMaxTokens)
         return fail(PA_ERR_UNSUPPORTED, "max_cache_len (%d) and the prefix (%d tokens) must be at most 2^30",
                     max_cache_len, prefix_len);
@@ -1050,7 +1052,7 @@ pa_status prefill_attn_varlen_sinks(const void* q, const void* k, const void* v,
     if (s != PA_OK) return s;
     s = check_paged(o, max_cache_len, n_kv_heads);
     if (s != PA_OK) return s;
-    s = check_capacity(max_cache_len, 0);
+    s = check_capacity(num_seqs, max_cache_len, 0);
     if (s != PA_OK) return s;
     if (num_seqs == 0 || total_q == 0) return PA_OK;
     o.window = clamp_span(o.window, max_cache_len);
@@ -1084,7 +1086,7 @@ pa_status prefill_attn_varlen_prefix(const void* q, const void* k, const void* v
     Prefix pre;
     s = read_prefix(prefix, o, &pre);
     if (s != PA_OK) return s;
-    s = check_capacity(max_cache_len, pre.len);
+    s = check_capacity(num_seqs, max_cache_len, pre.len);
     if (s != PA_OK) return s;
     if (num_seqs == 0 || total_q == 0) return PA_OK;
     if (pre.k && (pre.k == out || pre.v == out || pre.k == cache_k || pre.k == cache_v || pre.v == cache_k ||
@@ -1132,7 +1134,7 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
     if (s != PA_OK) return s;
     s = check_paged(o, max_cache_len, n_kv_heads);
     if (s != PA_OK) return s;
-    s = check_capacity(max_cache_len, prefix_len);
+    s = check_capacity(num_seqs, max_cache_len, prefix_len);
     if (s != PA_OK) return s;
     if (num_seqs == 0 || total_q == 0) return PA_OK;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
@@ -1213,7 +1215,7 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
                     sink_tokens, recent_tokens, budget);
     s = check_paged(o, max_cache_len, n_kv_heads);
     if (s != PA_OK) return s;
-    s = check_capacity(max_cache_len, 0);
+    s = check_capacity(num_seqs, max_cache_len, 0);
     if (s != PA_OK) return s;
     const long long heads = (long long)num_seqs * n_kv_heads;
     if (heads >= (1LL << 24)) return fail(PA_ERR_UNSUPPORTED, "num_seqs * n_kv_heads must be < 2^24");

@@ -1,0 +1,47 @@
+"""More argument errors that the long-context calls report before touching a GPU (CPU tests)."""
+import ctypes
+
+import pytest
+
+from prefill_phase_attention_gb300 import binding, build
+from tests.test_long_context_abi import options, refused
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return binding.load()
+
+
+def attention(**kw):
+    """Arguments of an attention call from q on, up to the scale: tensors far from one another, one sequence."""
+    a = dict(q=1 << 30, k=2 << 30, v=3 << 30, cu_q=64, cu_k=256, ck=4 << 30, cv=5 << 30, off=512, out=6 << 30, lse=None,
+             num_seqs=1, total_q=4, cap=8, H=4, Hk=2, d=64, scale=0.125)
+    a.update(kw)
+    return list(a.values())
+
+
+def key_weights(**kw):
+    a = dict(q=1 << 30, k=2 << 30, cu_q=64, cu_k=256, ck=4 << 30, off=512, lse=7 << 30, weights=8 << 30, num_seqs=1,
+             total_q=4, cap=8, H=4, Hk=2, d=64, scale=0.125, causal=1, sinks=0, prefix=0)
+    a.update(kw)
+    return list(a.values())
+
+
+def prefix(**kw):
+    p = binding.PaPrefix(ctypes.sizeof(binding.PaPrefix), 5, 9 << 30, 10 << 30, 8, 0, None, None, None)
+    for name, v in kw.items():
+        setattr(p, name, v)
+    return ctypes.byref(p)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_more_sequences_than_the_schedulers_count(lib, paged):
+    """Their loops step 1024 sequences at a time in 32 bits: near 2^31 sequences a step would pass the end of int."""
+    n = 2 ** 30 + 1
+    o = dict(block_table=1 << 40, block_size=8, max_blocks_per_seq=1, num_blocks=4) if paged else {}
+    sizes = dict(num_seqs=n, total_q=1, H=1, Hk=1, cap=8 if paged else 1)
+    refused(lib, lib.prefill_attn_varlen_sinks(*attention(**sizes), 2, ctypes.byref(options(4, **o)), None), 2, "num_seqs")
+    p = prefix(block_table=1 << 41, len=1, capacity=1)
+    refused(lib, lib.prefill_attn_varlen_prefix(*attention(**sizes), 1, p, ctypes.byref(options(0, **o)), None), 2, "num_seqs")
+    refused(lib, lib.prefill_attn_key_weights(*key_weights(**sizes), ctypes.byref(options(0, **o)), None), 2, "num_seqs")
