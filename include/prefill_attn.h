@@ -389,12 +389,13 @@ pa_status prefill_attn_key_weights(
  *                 call must not share blocks.
  *   weights       one fp32 per cached row, laid out as in prefill_attn_key_weights.
  *   lengths       [num_seqs] int32: cached tokens.
- *   kept_lengths  [num_seqs] int32 out: min(lengths[b], budget); must not
- *                 overlap lengths.
+ *   kept_lengths  [num_seqs] int32 out: min(lengths[b], budget).
  *   kept_index    [num_seqs, n_kv_heads, budget] int32 out or NULL: the kept
  *                 positions, ascending, -1 past the last.
  *   kept_weights  out or NULL: the kept weights, moved like the rows; weights
  *                 itself, or memory that does not overlap it.
+ * What the call writes (the caches and their scales among it) must overlap no other
+ * buffer of it, kept_weights = weights apart.
  * A sequence whose length is outside [0, max_cache_len], or that names a block
  * outside the pool, is skipped (PA_DEVERR_METADATA, nothing of it written).
  * max_cache_len is at most 2^30.

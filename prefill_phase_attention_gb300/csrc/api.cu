@@ -1007,6 +1007,23 @@ bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
     return x < y + b_bytes && y < x + a_bytes;
 }
 
+// A buffer of a call, and whether the call writes it (at = nullptr: not given).
+struct Span {
+    const char* name;
+    const void* at;
+    size_t bytes;
+    bool written;
+};
+
+// What a call writes overlaps nothing else of it.
+pa_status check_disjoint(const Span* s, size_t n) {
+    for (size_t i = 0; i < n; ++i)
+        for (size_t j = i + 1; j < n; ++j)
+            if (s[i].at && s[j].at && (s[i].written || s[j].written) && overlap(s[i].at, s[i].bytes, s[j].at, s[j].bytes))
+                return fail(PA_ERR_INVALID_ARG, "%s must not overlap %s", s[i].name, s[j].name);
+    return PA_OK;
+}
+
 // The kernels' position arithmetic stays within 32 bits: positions and spans are
 // at most kMaxTokens each, so the sum of two fits, and so do the schedulers' loops
 // over as many sequences, which step 1024 at a time.  A window or sink count past
@@ -1231,20 +1248,25 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     }
     if ((reinterpret_cast<uintptr_t>(kept_index) | reinterpret_cast<uintptr_t>(kept_weights)) & 3u)
         return fail(PA_ERR_INVALID_ARG, "kept_index and kept_weights must be 4-byte aligned");
-    if (overlap(lengths, (size_t)num_seqs * 4, kept_lengths, (size_t)num_seqs * 4))
-        return fail(PA_ERR_INVALID_ARG, "kept_lengths must not overlap lengths");
     const size_t rows = o.block_table ? (size_t)o.num_blocks * n_kv_heads * o.block_size : (size_t)heads * max_cache_len;
     const size_t row_bytes = o.kv_quant ? head_dim : 2 * head_dim;
     const size_t index_bytes = (size_t)heads * budget * sizeof(int);
-    if (kept_index && (overlap(kept_index, index_bytes, weights, rows * 4) ||
-                       overlap(kept_index, index_bytes, lengths, (size_t)num_seqs * 4) ||
-                       overlap(kept_index, index_bytes, kept_lengths, (size_t)num_seqs * 4) ||
-                       (kept_weights && overlap(kept_index, index_bytes, kept_weights, rows * 4))))
-        return fail(PA_ERR_INVALID_ARG, "kept_index must not overlap the weights or the lengths");
-    if (kept_weights && kept_weights != weights && overlap(weights, rows * 4, kept_weights, rows * 4))
-        return fail(PA_ERR_INVALID_ARG, "kept_weights must be weights itself or not overlap it");
     if (overlap(cache_k, rows * row_bytes, cache_v, rows * row_bytes))
         return fail(PA_ERR_INVALID_ARG, "cache_k and cache_v must not overlap");
+    if (kept_weights && kept_weights != weights && overlap(weights, rows * 4, kept_weights, rows * 4))
+        return fail(PA_ERR_INVALID_ARG, "kept_weights must be weights itself or not overlap it");
+    const Span spans[] = {{"kept_index", kept_index, index_bytes, true},
+                          {"kept_lengths", kept_lengths, (size_t)num_seqs * 4, true},
+                          {"kept_weights", kept_weights == weights ? nullptr : kept_weights, rows * 4, true},
+                          {"cache_k", cache_k, rows * row_bytes, true},
+                          {"cache_v", cache_v, rows * row_bytes, true},
+                          {"cache_k_scale", o.scale_k, rows * 4, true},
+                          {"cache_v_scale", o.scale_v, rows * 4, true},
+                          {"weights", weights, rows * 4, kept_weights == weights},
+                          {"lengths", lengths, (size_t)num_seqs * 4, false},
+                          {"block_table", o.block_table, (size_t)num_seqs * o.max_blocks * 4, false}};
+    s = check_disjoint(spans, sizeof spans / sizeof *spans);
+    if (s != PA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

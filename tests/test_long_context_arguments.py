@@ -45,3 +45,30 @@ def test_more_sequences_than_the_schedulers_count(lib, paged):
     p = prefix(block_table=1 << 41, len=1, capacity=1)
     refused(lib, lib.prefill_attn_varlen_prefix(*attention(**sizes), 1, p, ctypes.byref(options(0, **o)), None), 2, "num_seqs")
     refused(lib, lib.prefill_attn_key_weights(*key_weights(**sizes), ctypes.byref(options(0, **o)), None), 2, "num_seqs")
+
+
+EVICT = dict(ck=1 << 25, cv=1 << 26, weights=1 << 24, lengths=1 << 20, new=1 << 21, index=1 << 22, kept_w=1 << 23,
+             num_seqs=2, cap=64, Hk=2, d=64, budget=6, sinks=1, recent=2)
+CODES = dict(kv_quant=1, cache_k_scale=1 << 27, cache_v_scale=1 << 28)
+
+
+# 256 rows of fp32 weights or scales (1024 bytes) and of 128 bytes of keys and values (32 KiB; int8: 16 KiB)
+@pytest.mark.parametrize("kw,o,msg", [
+    (dict(new=(1 << 24) + 1020), {}, "kept_lengths must not overlap weights"),
+    (dict(new=(1 << 23) + 4), {}, "kept_lengths must not overlap kept_weights"),
+    (dict(new=(1 << 25) + 32764), {}, "kept_lengths must not overlap cache_k"),
+    (dict(lengths=(1 << 26) + 32764), {}, "cache_v must not overlap lengths"),
+    (dict(lengths=(1 << 23) + 1020), {}, "kept_weights must not overlap lengths"),
+    (dict(index=(1 << 25) - 8), {}, "kept_index must not overlap cache_k"),
+    (dict(kept_w=(1 << 26) - 1020), {}, "kept_weights must not overlap cache_v"),
+    (dict(weights=(1 << 25) - 1020), {}, "cache_k must not overlap weights"),
+    (dict(index=(1 << 27) + 1020), CODES, "kept_index must not overlap cache_k_scale"),
+    (dict(kept_w=(1 << 28) + 1020), CODES, "kept_weights must not overlap cache_v_scale"),
+    (dict(), dict(CODES, cache_v_scale=(1 << 27) + 1020), "cache_k_scale must not overlap cache_v_scale"),
+    (dict(weights=(1 << 27) - 1020), CODES, "cache_k_scale must not overlap weights"),
+    (dict(new=1 << 30), dict(block_table=(1 << 30) + 4, block_size=8, max_blocks_per_seq=8, num_blocks=16),
+     "kept_lengths must not overlap block_table"),
+])
+def test_evict_refuses_overlapping_buffers(lib, kw, o, msg):
+    a = list({**EVICT, **kw}.values())
+    refused(lib, lib.prefill_attn_evict(*a, ctypes.byref(options(0, **o)), None), 1, msg)
