@@ -347,7 +347,7 @@ pa_status prefill_attn_varlen_prefix(
  *
  *   weights      one fp32 per cached (token, KV head): [num_seqs, n_kv_heads,
  *                max_cache_len], or [num_blocks, n_kv_heads, block_size] with a
- *                block_table; 4-byte aligned.
+ *                block_table; 4-byte aligned; overlaps no other buffer of the call.
  *   lse          [total_q, n_heads] fp32, not NULL.
  *   sink_tokens  as in prefill_attn_varlen_sinks (needs a window); 0: none.
  *   prefix_len   tokens of a shared prefix ahead of the sequences; it only moves

@@ -1015,6 +1015,11 @@ struct Span {
     bool written;
 };
 
+// Rows of a call's cache (and of its scales and weights).
+size_t cache_rows(const Options& o, int num_seqs, int max_cache_len, int n_kv_heads) {
+    return o.block_table ? (size_t)o.num_blocks * n_kv_heads * o.block_size : (size_t)num_seqs * n_kv_heads * max_cache_len;
+}
+
 // What a call writes overlaps nothing else of it.
 pa_status check_disjoint(const Span* s, size_t n) {
     for (size_t i = 0; i < n; ++i)
@@ -1154,6 +1159,20 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
     s = check_capacity(num_seqs, max_cache_len, prefix_len);
     if (s != PA_OK) return s;
     if (num_seqs == 0 || total_q == 0) return PA_OK;
+    const size_t rows = cache_rows(o, num_seqs, max_cache_len, n_kv_heads);
+    const size_t q_rows = (size_t)total_q * n_heads, k_rows = (size_t)total_q * n_kv_heads;
+    const Span spans[] = {{"weights", weights, rows * 4, true},
+                          {"q", q, q_rows * head_dim * 2, false},
+                          {"k", k, k_rows * head_dim * 2, false},
+                          {"cache_k", cache_k, rows * head_dim * (o.kv_quant ? 1 : 2), false},
+                          {"cache_k_scale", o.scale_k, rows * 4, false},
+                          {"lse", lse, q_rows * 4, false},
+                          {"cu_seqlens_q", cu_seqlens_q, ((size_t)num_seqs + 1) * 4, false},
+                          {"cu_seqlens_k", cu_seqlens_k, ((size_t)num_seqs + 1) * 4, false},
+                          {"cache_offsets", cache_offsets, (size_t)num_seqs * 4, false},
+                          {"block_table", o.block_table, (size_t)num_seqs * o.max_blocks * 4, false}};
+    s = check_disjoint(spans, sizeof spans / sizeof *spans);
+    if (s != PA_OK) return s;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1248,7 +1267,7 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     }
     if ((reinterpret_cast<uintptr_t>(kept_index) | reinterpret_cast<uintptr_t>(kept_weights)) & 3u)
         return fail(PA_ERR_INVALID_ARG, "kept_index and kept_weights must be 4-byte aligned");
-    const size_t rows = o.block_table ? (size_t)o.num_blocks * n_kv_heads * o.block_size : (size_t)heads * max_cache_len;
+    const size_t rows = cache_rows(o, num_seqs, max_cache_len, n_kv_heads);
     const size_t row_bytes = o.kv_quant ? head_dim : 2 * head_dim;
     const size_t index_bytes = (size_t)heads * budget * sizeof(int);
     if (overlap(cache_k, rows * row_bytes, cache_v, rows * row_bytes))

@@ -72,3 +72,22 @@ CODES = dict(kv_quant=1, cache_k_scale=1 << 27, cache_v_scale=1 << 28)
 def test_evict_refuses_overlapping_buffers(lib, kw, o, msg):
     a = list({**EVICT, **kw}.values())
     refused(lib, lib.prefill_attn_evict(*a, ctypes.byref(options(0, **o)), None), 1, msg)
+
+
+# q 4 x 4 heads x 128 bytes, k 4 x 2 x 128, lse 4 x 4 floats, weights 2 x 8 floats, cached keys 2 x 8 x 128 (int8: 64)
+@pytest.mark.parametrize("kw,o,msg", [
+    (dict(weights=(1 << 30) + 2044), {}, "weights must not overlap q"),
+    (dict(weights=(2 << 30) - 60), {}, "weights must not overlap k"),
+    (dict(weights=(4 << 30) + 2044), {}, "weights must not overlap cache_k"),
+    (dict(weights=(7 << 30) + 60), {}, "weights must not overlap lse"),
+    (dict(weights=(7 << 30) - 60), {}, "weights must not overlap lse"),
+    (dict(weights=68), {}, "weights must not overlap cu_seqlens_q"),
+    (dict(weights=260), {}, "weights must not overlap cu_seqlens_k"),
+    (dict(weights=512), {}, "weights must not overlap cache_offsets"),
+    (dict(weights=(11 << 30) + 60), dict(kv_quant=1, cache_k_scale=11 << 30, cache_v_scale=12 << 30),
+     "weights must not overlap cache_k_scale"),
+    (dict(weights=(11 << 30) - 124), dict(block_table=11 << 30, block_size=8, max_blocks_per_seq=1, num_blocks=2),
+     "weights must not overlap block_table"),
+])
+def test_key_weights_refuses_overlapping_buffers(lib, kw, o, msg):
+    refused(lib, lib.prefill_attn_key_weights(*key_weights(**kw), ctypes.byref(options(0, **o)), None), 1, msg)
