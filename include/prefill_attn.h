@@ -290,6 +290,7 @@ pa_status prefill_attn_varlen_sinks(
  *   paged cache (pa_options.block_table): block_table, a device array of int32
  *     [ceil(len / block_size)], names the prefix's blocks in the call's own
  *     pools (and scale pools); the other fields are ignored.
+ * What it names must not overlap out, lse or rows of the caches that the call writes.
  * Zero-initialise it and set struct_size = sizeof(pa_prefix).
  */
 typedef struct pa_prefix {

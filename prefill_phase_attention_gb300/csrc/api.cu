@@ -1114,6 +1114,22 @@ pa_status prefill_attn_varlen_prefix(const void* q, const void* k, const void* v
     if (pre.k && (pre.k == out || pre.v == out || pre.k == cache_k || pre.k == cache_v || pre.v == cache_k ||
                   pre.v == cache_v))
         return fail(PA_ERR_INVALID_ARG, "the prefix must not alias out or the caches");
+    if (pre.len > 0) {
+        // the rows that are read: [0, len) of every head
+        const size_t rows = pre.k ? (size_t)(n_kv_heads - 1) * pre.capacity + pre.len : 0;
+        const size_t row_bytes = o.kv_quant ? head_dim : 2 * head_dim;
+        const size_t blocks = pre.block_table ? ((size_t)pre.len + o.block_size - 1) / o.block_size : 0;
+        const size_t out_rows = (size_t)total_q * n_heads;
+        const Span spans[] = {{"out", out, out_rows * head_dim * 2, true},
+                              {"lse", lse, out_rows * 4, true},
+                              {"the prefix's k", pre.k, rows * row_bytes, false},
+                              {"the prefix's v", pre.v, rows * row_bytes, false},
+                              {"the prefix's k_scale", pre.scale_k, rows * 4, false},
+                              {"the prefix's v_scale", pre.scale_v, rows * 4, false},
+                              {"the prefix's block_table", pre.block_table, blocks * 4, false}};
+        s = check_disjoint(spans, sizeof spans / sizeof *spans);
+        if (s != PA_OK) return s;
+    }
     return enqueue_long(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs,
                         total_q, max_cache_len, n_heads, n_kv_heads, head_dim, scale, causal, 0, pre, o,
                         reinterpret_cast<cudaStream_t>(stream_));

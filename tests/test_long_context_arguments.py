@@ -91,3 +91,21 @@ def test_evict_refuses_overlapping_buffers(lib, kw, o, msg):
 ])
 def test_key_weights_refuses_overlapping_buffers(lib, kw, o, msg):
     refused(lib, lib.prefill_attn_key_weights(*key_weights(**kw), ctypes.byref(options(0, **o)), None), 1, msg)
+
+
+# out 4 x 4 heads x 128 bytes, lse 4 x 4 floats; of the prefix 8 + 5 rows of 128 bytes (int8: 64 and a scale)
+@pytest.mark.parametrize("kw,p,o,msg", [
+    (dict(), dict(k=(6 << 30) + 2032), {}, "out must not overlap the prefix's k"),
+    (dict(), dict(v=(6 << 30) - 13 * 128 + 16), {}, "out must not overlap the prefix's v"),
+    (dict(lse=(9 << 30) + 13 * 128 - 4), {}, {}, "lse must not overlap the prefix's k"),
+    (dict(lse=(10 << 30) - 60), {}, {}, "lse must not overlap the prefix's v"),
+    (dict(lse=13 << 30), dict(k_scale=(13 << 30) + 60, v_scale=14 << 30),
+     dict(kv_quant=1, cache_k_scale=11 << 30, cache_v_scale=12 << 30), "lse must not overlap the prefix's k_scale"),
+    (dict(), dict(k_scale=13 << 30, v_scale=(6 << 30) - 48),
+     dict(kv_quant=1, cache_k_scale=11 << 30, cache_v_scale=12 << 30), "out must not overlap the prefix's v_scale"),
+    (dict(), dict(block_table=(6 << 30) + 2044), dict(block_table=256, block_size=8, max_blocks_per_seq=1, num_blocks=4),
+     "out must not overlap the prefix's block_table"),
+])
+def test_prefix_refuses_overlapping_buffers(lib, kw, p, o, msg):
+    got = lib.prefill_attn_varlen_prefix(*attention(**kw), 1, prefix(**p), ctypes.byref(options(0, **o)), None)
+    refused(lib, got, 1, msg)
