@@ -1269,6 +1269,9 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     if (s != PA_OK) return s;
     s = check_capacity(num_seqs, max_cache_len, 0);
     if (s != PA_OK) return s;
+    // no sequence is longer than max_cache_len, so a larger budget says the same; only
+    // a caller's index has an entry for each of its tokens
+    if (!kept_index) budget = std::min(budget, max_cache_len);
     const long long heads = (long long)num_seqs * n_kv_heads;
     if (heads >= (1LL << 24)) return fail(PA_ERR_UNSUPPORTED, "num_seqs * n_kv_heads must be < 2^24");
     if (!o.block_table && heads * max_cache_len >= (1LL << 31))
