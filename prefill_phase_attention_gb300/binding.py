@@ -219,17 +219,19 @@ def prefill_attn_varlen_ex(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v
 # The long-context calls are often a few microseconds of GPU work, so their checks
 # read as few attributes as they need, as one expression where every call goes
 # through (0.3 us a tensor on the GPU's host; _check_tensors then names the
-# tensor that failed).  The shapes of q, k and the caches are checked as such;
-# the other tensors are dense in the layout their documentation states, so that
-# their element count says whether they fit.
+# tensor that failed).  Tensors have the shapes that their documentation states;
+# of the vectors of metadata the element count says whether they fit.
 _BF16, _I8, _F32, _I32 = torch.bfloat16, torch.int8, torch.float32, torch.int32
 
 
 def _check_tensors(device: int, *specs) -> None:
-    """Each spec (name, tensor or None, dtype, elements): contiguous, CUDA, on `device`, of that type and size."""
+    """Each spec (name, tensor or None, dtype, shape, or the elements of a vector): contiguous, CUDA, on `device`, of
+    that type and shape."""
     for name, t, dtype, n in specs:
-        if t is not None and (t.dtype is not dtype or t.get_device() != device or t.numel() != n or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of {n} elements on cuda:{device}, "
+        if t is not None and (t.dtype is not dtype or t.get_device() != device or not t.is_contiguous()
+                              or (t.numel() != n if type(n) is int else t.shape != n)):
+            size = f"of {n} elements" if type(n) is int else f"of shape {tuple(n)}"
+            raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {size} on cuda:{device}, "
                              f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
@@ -256,14 +258,14 @@ def _stream_on(stream, device: int) -> int:
 
 
 def _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d):
-    """Checks a call's cache tensors; returns (slot capacity, whether the cache is int8, rows of the cache)."""
+    """Checks a call's cache tensors; returns (slot capacity, whether the cache is int8, shape of the cache's rows)."""
     if cache_k.dim() != 4:
         raise ValueError("caches are [num_seqs, kv_heads, cap, head_dim], or [num_blocks, kv_heads, block_size, head_dim]")
     n, ck_heads, rows, ck_dim = cache_k.shape
     if ck_heads != hk or ck_dim != d or (block_table is None and n != b):
         raise ValueError(f"cache_k has shape {tuple(cache_k.shape)}: {hk} KV heads of {d}"
                          + ("" if block_table is not None else f" in {b} slots") + " are wanted")
-    dtype, quant, cap, total = _BF16, False, rows, n * hk * rows
+    dtype, quant, cap, total = _BF16, False, rows, (n, hk, rows)
     if block_table is not None:
         if block_table.dim() != 2 or block_table.shape[0] != b:
             raise ValueError(f"block_table must be [{b}, max_blocks_per_seq]")
@@ -276,34 +278,33 @@ def _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_
         _check_tensors(device, ("cache_k_scale", cache_k_scale, _F32, total), ("cache_v_scale", cache_v_scale, _F32, total))
     cv = cache_k if cache_v is None else cache_v
     if not (cache_k.dtype is dtype and cache_k.is_contiguous() and cache_k.get_device() == device
-            and cv.dtype is dtype and cv.numel() == total * d and cv.is_contiguous() and cv.get_device() == device):
-        _check_tensors(device, ("cache_k", cache_k, dtype, total * d), ("cache_v", cache_v, dtype, total * d))
+            and cv.dtype is dtype and cv.shape == cache_k.shape and cv.is_contiguous() and cv.get_device() == device):
+        _check_tensors(device, ("cache_k", cache_k, dtype, cache_k.shape), ("cache_v", cache_v, dtype, cache_k.shape))
     return cap, quant, total
 
 
 def _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, block_table,
                     cache_k_scale, cache_v_scale):
-    """Checks the tensors of a long-context call; returns (device, cache capacity, whether it is int8, cache rows)."""
+    """Checks the tensors of a long-context call; returns (device, cache capacity, whether it is int8, its rows' shape)."""
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q/k/v are [total_q, heads, head_dim]")
     device = _current_device(q)
     (t, h, d), (kt, hk, kd), b = q.shape, k.shape, cache_offsets.numel()
     if kt != t or kd != d:
         raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
-    nq, nk = t * h * d, t * hk * d
     vv, oo = k if v is None else v, q if out is None else out
     if not (q.dtype is _BF16 and k.dtype is _BF16 and q.is_contiguous() and k.is_contiguous() and k.get_device() == device
-            and vv.dtype is _BF16 and vv.numel() == nk and vv.is_contiguous() and vv.get_device() == device
-            and oo.dtype is _BF16 and oo.numel() == nq and oo.is_contiguous() and oo.get_device() == device
-            and (lse is None or lse.dtype is _F32 and lse.numel() == t * h and lse.is_contiguous()
+            and vv.dtype is _BF16 and vv.shape == k.shape and vv.is_contiguous() and vv.get_device() == device
+            and oo.dtype is _BF16 and oo.shape == q.shape and oo.is_contiguous() and oo.get_device() == device
+            and (lse is None or lse.dtype is _F32 and lse.shape == (t, h) and lse.is_contiguous()
                  and lse.get_device() == device)
             and cu_seqlens_q.dtype is _I32 and cu_seqlens_q.numel() == b + 1 and cu_seqlens_q.is_contiguous()
             and cu_seqlens_q.get_device() == device
             and cu_seqlens_k.dtype is _I32 and cu_seqlens_k.numel() == b + 1 and cu_seqlens_k.is_contiguous()
             and cu_seqlens_k.get_device() == device
             and cache_offsets.dtype is _I32 and cache_offsets.is_contiguous() and cache_offsets.get_device() == device):
-        _check_tensors(device, ("q", q, _BF16, nq), ("k", k, _BF16, nk), ("v", v, _BF16, nk), ("out", out, _BF16, nq),
-                       ("lse", lse, _F32, t * h), ("cu_seqlens_q", cu_seqlens_q, _I32, b + 1),
+        _check_tensors(device, ("q", q, _BF16, q.shape), ("k", k, _BF16, k.shape), ("v", v, _BF16, k.shape),
+                       ("out", out, _BF16, q.shape), ("lse", lse, _F32, (t, h)), ("cu_seqlens_q", cu_seqlens_q, _I32, b + 1),
                        ("cu_seqlens_k", cu_seqlens_k, _I32, b + 1), ("cache_offsets", cache_offsets, _I32, b))
     return device, *_cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d)
 
@@ -382,9 +383,8 @@ def prefill_attn_varlen_prefix(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cac
             raise ValueError("a contiguous cache needs prefix_k and prefix_v")
         if prefix_k.dim() != 3 or prefix_k.shape[0] != k.shape[1] or prefix_k.shape[2] != q.shape[2]:
             raise ValueError("prefix_k is [n_kv_heads, capacity, head_dim]")
-        rows, dtype = prefix_k.shape[0] * prefix_k.shape[1], _I8 if quant else _BF16
-        _check_tensors(device, ("prefix_k", prefix_k, dtype, rows * prefix_k.shape[2]),
-                       ("prefix_v", prefix_v, dtype, rows * prefix_k.shape[2]))
+        dtype = _I8 if quant else _BF16
+        _check_tensors(device, ("prefix_k", prefix_k, dtype, prefix_k.shape), ("prefix_v", prefix_v, dtype, prefix_k.shape))
         pre.k, pre.v, pre.capacity = prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_k.shape[1]
         if prefix_len is None:
             prefix_len = prefix_k.shape[1]
@@ -392,7 +392,7 @@ def prefill_attn_varlen_prefix(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cac
             for name, t in (("prefix_k_scale", prefix_k_scale), ("prefix_v_scale", prefix_v_scale)):
                 if t is None:
                     raise ValueError(f"an int8 cache needs {name}")
-                _check_tensors(device, (name, t, _F32, rows))
+                _check_tensors(device, (name, t, _F32, prefix_k.shape[:2]))
             pre.k_scale, pre.v_scale = prefix_k_scale.data_ptr(), prefix_v_scale.data_ptr()
     _int32(prefix_len=prefix_len)
     pre.len = prefix_len
@@ -445,7 +445,7 @@ def prefill_attn_evict(cache_k, cache_v, weights, lengths, kept_lengths, kept_in
     b, (_, hk, _, d) = lengths.numel(), cache_k.shape
     cap, _, rows = _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d)
     _check_tensors(device, ("weights", weights, _F32, rows), ("lengths", lengths, _I32, b),
-                   ("kept_lengths", kept_lengths, _I32, b), ("kept_index", kept_index, _I32, b * hk * budget),
+                   ("kept_lengths", kept_lengths, _I32, b), ("kept_index", kept_index, _I32, (b, hk, budget)),
                    ("kept_weights", kept_weights, _F32, rows))
     _check((_lib or load()).prefill_attn_evict(
         cache_k.data_ptr(), cache_v.data_ptr(), weights.data_ptr(), lengths.data_ptr(), kept_lengths.data_ptr(),

@@ -27,3 +27,48 @@ def test_evict_with_a_budget_past_the_cache_fills_the_index():
     c = Call(301, [0] * 3, [90, 0, 17], 64, 2, 1)
     evict(c, weights_for(c, 1, "plain"), 1000, 600, 300)
     ok()
+
+
+def swapped(t, a=-1, b=-2):
+    """A contiguous tensor of as many elements, two dimensions swapped."""
+    return torch.zeros_like(t.transpose(a, b).contiguous())
+
+
+@pytest.mark.parametrize("name", ["v", "cache_v", "out", "lse", "cache_k_scale", "cache_v_scale"])
+@pytest.mark.parametrize("call", ["sinks", "prefix"])
+def test_attention_refuses_other_shapes_of_as_many_elements(call, name):
+    c = Call(310, [3, 5], [20, 7], 64, 2, 2, int8="scale" in name, prefix=40 if call == "prefix" else 0)
+    names = ("q", "k", "v", "cu_seqlens_q", "cu_seqlens_k", "cache_k", "cache_v", "cache_offsets", "out", "lse")
+    t = {**dict(zip(names, c.tensors())), **c.scales}
+    t[name] = swapped(t[name])
+    kw = dict(window=9, sink_tokens=2) if call == "sinks" else c.pre
+    with pytest.raises(ValueError, match=name):
+        getattr(binding, f"prefill_attn_varlen_{call}")(**t, scale=c.scale, **kw)
+
+
+@pytest.mark.parametrize("name", ["prefix_v", "prefix_k_scale", "prefix_v_scale"])
+def test_prefix_refuses_other_shapes_of_as_many_elements(name):
+    c = Call(311, [3, 5], [20, 7], 64, 2, 2, int8="scale" in name, prefix=40)
+    c.pre[name] = swapped(c.pre[name])
+    with pytest.raises(ValueError, match=name):
+        c.prefix()
+
+
+@pytest.mark.parametrize("name", ["lse", "weights"])
+def test_key_weights_refuses_other_shapes_of_as_many_elements(name):
+    c = Call(312, [3, 5], [20, 7], 64, 2, 2)
+    t = dict(lse=torch.zeros((8, 4), device="cuda"), weights=c.weights.cuda())
+    t[name] = swapped(t[name])
+    with pytest.raises(ValueError, match=name):
+        binding.prefill_attn_key_weights(c.dev[0], c.dev[1], *c.meta, c.data[0][1], c.offsets, **t)
+
+
+@pytest.mark.parametrize("name", ["cache_v", "weights", "kept_index", "kept_weights"])
+def test_evict_refuses_other_shapes_of_as_many_elements(name):
+    c = Call(313, [0] * 3, [90, 20, 60], 64, 2, 1)
+    t = dict(cache_k=c.data[0][1], cache_v=c.data[1][1], weights=c.weights.cuda(), lengths=c.offsets,
+             kept_lengths=torch.zeros_like(c.offsets), kept_weights=c.weights.cuda(),
+             kept_index=torch.zeros((3, 2, 50), dtype=torch.int32, device="cuda"))
+    t[name] = swapped(t[name])
+    with pytest.raises(ValueError, match=name):
+        binding.prefill_attn_evict(**t, budget=50)
