@@ -65,40 +65,42 @@ struct Workspace {
     size_t aux_bytes = 0;
     bool captured = false;  // a captured graph holds these addresses: outgrown blocks are kept, not freed
     std::vector<void*> old_headers;  // headers of outgrown blocks that a graph may still write errors to
+    std::vector<void*> retired;      // outgrown blocks that a captured graph holds
 };
 
 std::mutex g_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;
-std::vector<std::pair<int, void*>> g_retired;  // (device, block) outgrown but held by a captured graph
 
-// Held by a call from its first look at its stream's workspace to its last launch.
-// A call's kernels hand data to one another through that workspace, and a call may
-// replace its blocks: two host threads that call on one stream must not mix their
-// launches.  (The lock outlives a release of the workspace.)
+// A stream's workspace and its lock, held by a call from its first look at the
+// workspace to its last launch.  A call's kernels hand data to one another through
+// that workspace, and a call may replace its blocks: two host threads that call on
+// one stream must not mix their launches.  (g_mu is for the map; the lock outlives a
+// release of the workspace.)
 struct StreamLock {
+    Workspace* ws;
     std::shared_ptr<std::mutex> mu;
     std::unique_lock<std::mutex> held;
-    StreamLock(int dev, cudaStream_t st) : mu(of(dev, st)), held(*mu) {}
+    StreamLock(int dev, cudaStream_t st) : ws(of(dev, st)), mu(ws->mu), held(*mu) {}
 
-    static std::shared_ptr<std::mutex> of(int dev, cudaStream_t st) {
+    static Workspace* of(int dev, cudaStream_t st) {
         std::lock_guard<std::mutex> lock(g_mu);
-        Workspace& w = g_ws[std::make_pair(dev, st)];
+        Workspace& w = g_ws[std::make_pair(dev, st)];  // (stays where it is)
         if (!w.mu) w.mu = std::make_shared<std::mutex>();
-        return w.mu;
+        return &w;
     }
 };
 
-// Room in g_retired for one more block, made before the block that replaces it is
+// Room in `retired` for one more block, made before the block that replaces it is
 // allocated: nothing throws in between.
-void prepare_drop(const Workspace& w) {
-    if (w.captured) g_retired.reserve(g_retired.size() + 1);
+void prepare_drop(Workspace& w) {
+    if (w.captured) w.retired.reserve(w.retired.size() + 1);
 }
 
 // Gives up a block of a workspace that has been replaced by a larger one.
-void drop_block(const Workspace& w, int dev, void* ptr, cudaStream_t st) {
+void drop_block(Workspace& w, void* ptr, cudaStream_t st) {
     if (!ptr) return;
     if (w.captured)
-        g_retired.emplace_back(dev, ptr);
+        w.retired.push_back(ptr);
     else
         cudaFreeAsync(ptr, st);
 }
@@ -125,15 +127,12 @@ bool capturing(cudaStream_t st) {
     return cudaStreamIsCapturing(st, &cs) == cudaSuccess && cs == cudaStreamCaptureStatusActive;
 }
 
-// Returns the workspace of (device, stream), growing it (stream-ordered) when
-// needed.  Under graph capture nothing is allocated: the stream must already
+// Grows the workspace of a stream (stream-ordered) when needed; its lock is held, as
+// in the next two.  Under graph capture nothing is allocated: the stream must already
 // hold a workspace big enough (from a call outside the capture).
-pa_status get_workspace(int dev, cudaStream_t st, int num_seqs, int max_units, Workspace** out) {
-    std::lock_guard<std::mutex> lock(g_mu);
-    Workspace& w = g_ws[std::make_pair(dev, st)];
+pa_status grow_workspace(Workspace& w, cudaStream_t st, int num_seqs, int max_units) {
     if (w.ptr && w.max_seqs >= num_seqs && w.max_units >= max_units) {
         if (!w.captured && capturing(st)) w.captured = true;
-        *out = &w;
         return PA_OK;
     }
     if (capturing(st))
@@ -141,37 +140,32 @@ pa_status get_workspace(int dev, cudaStream_t st, int num_seqs, int max_units, W
                     "graph capture: the stream's workspace would have to grow (%d sequences, %d work units); "
                     "run a call of at least these sizes on this stream before capturing",
                     num_seqs, max_units);
-    Workspace nw;
-    nw.max_seqs = std::max(num_seqs, std::max(w.max_seqs, 64));
-    nw.max_units = std::max(max_units, std::max(w.max_units, 4096));
-    nw.bytes = ws_bytes(nw.max_seqs, nw.max_units);
-    nw.mu = w.mu;
-    nw.captured = w.captured;
-    nw.old_headers = w.old_headers;
-    if (w.captured && w.ptr) nw.old_headers.push_back(w.ptr);
+    const int seqs = std::max(num_seqs, std::max(w.max_seqs, 64));
+    const int units = std::max(max_units, std::max(w.max_units, 4096));
+    const size_t bytes = ws_bytes(seqs, units);
     prepare_drop(w);
-    cudaError_t e = cudaMallocAsync(&nw.ptr, nw.bytes, st);
+    if (w.captured) w.old_headers.reserve(w.old_headers.size() + 1);
+    void* ptr = nullptr;
+    cudaError_t e = cudaMallocAsync(&ptr, bytes, st);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(workspace)");
-    e = cudaMemsetAsync(nw.ptr, 0, sizeof(pa::WorkspaceHeader), st);
+    e = cudaMemsetAsync(ptr, 0, sizeof(pa::WorkspaceHeader), st);
     if (e == cudaSuccess && w.ptr)  // keep sticky error bits across a regrow
-        e = cudaMemcpyAsync(nw.ptr, w.ptr, sizeof(int), cudaMemcpyDeviceToDevice, st);
+        e = cudaMemcpyAsync(ptr, w.ptr, sizeof(int), cudaMemcpyDeviceToDevice, st);
     if (e != cudaSuccess) {
-        cudaFreeAsync(nw.ptr, st);
+        cudaFreeAsync(ptr, st);
         return cuda_fail(e, "workspace init");
     }
-    drop_block(w, dev, w.ptr, st);
-    nw.rope = w.rope;  // the rotary and auxiliary scratch are grown on their own
-    nw.rope_bytes = w.rope_bytes;
-    nw.aux = w.aux;
-    nw.aux_bytes = w.aux_bytes;
-    w = std::move(nw);
-    *out = &w;
+    if (w.captured && w.ptr) w.old_headers.push_back(w.ptr);
+    drop_block(w, w.ptr, st);
+    w.ptr = ptr;
+    w.bytes = bytes;
+    w.max_seqs = seqs;
+    w.max_units = units;
     return PA_OK;
 }
 
 // Grows (stream-ordered) the rotated-q/k scratch of a workspace to `bytes`.
-pa_status get_rope_scratch(Workspace* w, int dev, cudaStream_t st, size_t bytes, void** out) {
-    std::lock_guard<std::mutex> lock(g_mu);
+pa_status get_rope_scratch(Workspace* w, cudaStream_t st, size_t bytes, void** out) {
     if (w->rope_bytes < bytes && capturing(st))
         return fail(PA_ERR_UNSUPPORTED,
                     "graph capture: the stream's rotary scratch would have to grow (%zu bytes); run a call with "
@@ -182,7 +176,7 @@ pa_status get_rope_scratch(Workspace* w, int dev, cudaStream_t st, size_t bytes,
         void* nptr = nullptr;
         cudaError_t e = cudaMallocAsync(&nptr, bytes, st);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(rotary scratch)");
-        drop_block(*w, dev, w->rope, st);
+        drop_block(*w, w->rope, st);
         w->rope = nptr;
         w->rope_bytes = bytes;
     }
@@ -191,8 +185,7 @@ pa_status get_rope_scratch(Workspace* w, int dev, cudaStream_t st, size_t bytes,
 }
 
 // Grows (stream-ordered) the auxiliary scratch of a workspace to `bytes`.
-pa_status get_aux_scratch(Workspace* w, int dev, cudaStream_t st, size_t bytes, void** out) {
-    std::lock_guard<std::mutex> lock(g_mu);
+pa_status get_aux_scratch(Workspace* w, cudaStream_t st, size_t bytes, void** out) {
     if (w->aux_bytes < bytes && capturing(st))
         return fail(PA_ERR_UNSUPPORTED,
                     "graph capture: the stream's auxiliary scratch would have to grow (%zu bytes); run a call of at "
@@ -203,7 +196,7 @@ pa_status get_aux_scratch(Workspace* w, int dev, cudaStream_t st, size_t bytes, 
         void* nptr = nullptr;
         cudaError_t e = cudaMallocAsync(&nptr, bytes, st);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(auxiliary scratch)");
-        drop_block(*w, dev, w->aux, st);
+        drop_block(*w, w->aux, st);
         w->aux = nptr;
         w->aux_bytes = bytes;
     }
@@ -578,13 +571,13 @@ pa_status prefill_attn_varlen_ex(const void* q, const void* k, const void* v, co
     const long long max_units_ll = unit_bound(total_q, num_seqs, n_heads, n_kv_heads, slots);
     if (max_units_ll >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
     const StreamLock lock(dev, stream);
-    Workspace* ws = nullptr;
-    s = get_workspace(dev, stream, num_seqs, (int)max_units_ll, &ws);
+    Workspace* const ws = lock.ws;
+    s = grow_workspace(*ws, stream, num_seqs, (int)max_units_ll);
     if (s != PA_OK) return s;
     Scratch scr{static_cast<pa::WorkspaceHeader*>(ws->ptr), ws_seqs(*ws), ws_units(*ws), ws->max_units,
                 ws_seq_scratch(*ws)};
     if (o.rope_theta > 0.f) {
-        s = get_rope_scratch(ws, dev, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
+        s = get_rope_scratch(ws, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
         if (s != PA_OK) return s;
     }
     return enqueue(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, num_seqs, total_q,
@@ -640,15 +633,10 @@ pa_status prefill_attn_device_status(pa_stream_t stream_, int32_t* flags) try {
     e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize");
     const StreamLock own(dev, stream);  // (no call replaces the workspace meanwhile)
-    std::vector<void*> words = {noalloc_scratch_if_set_up()};  // and the workspace, outgrown ones that graphs use included
-    {
-        std::lock_guard<std::mutex> lock(g_mu);
-        auto it = g_ws.find(std::make_pair(dev, stream));
-        if (it != g_ws.end()) {
-            words.push_back(it->second.ptr);
-            words.insert(words.end(), it->second.old_headers.begin(), it->second.old_headers.end());
-        }
-    }
+    // the workspace's word, outgrown ones that graphs use included
+    std::vector<void*> words = own.ws->old_headers;
+    words.push_back(own.ws->ptr);
+    words.push_back(noalloc_scratch_if_set_up());
     int32_t word = 0;
     for (void* ptr : words) {
         if (!ptr) continue;
@@ -672,16 +660,12 @@ void prefill_attn_release(void) try {
     int cur = 0;
     cudaGetDevice(&cur);
     for (auto& kv : g_ws) {
+        Workspace& w = kv.second;
         cudaSetDevice(kv.first.first);
-        if (kv.second.ptr) cudaFree(kv.second.ptr);
-        if (kv.second.rope) cudaFree(kv.second.rope);
-        if (kv.second.aux) cudaFree(kv.second.aux);
+        for (void* ptr : {w.ptr, w.rope, w.aux})
+            if (ptr) cudaFree(ptr);
+        for (void* ptr : w.retired) cudaFree(ptr);
     }
-    for (auto& r : g_retired) {
-        cudaSetDevice(r.first);
-        cudaFree(r.second);
-    }
-    g_retired.clear();
     cudaSetDevice(cur);
     g_ws.clear();
 } catch (...) {
@@ -917,8 +901,8 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
         std::min(own_units * max_pieces + pre_units * std::max(1, max_prefix_pieces), own_units + pre_units + 4 * target);
     if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
     const StreamLock lock(dev, stream);
-    Workspace* ws = nullptr;
-    s = get_workspace(dev, stream, num_seqs + 1, 0, &ws);
+    Workspace* const ws = lock.ws;
+    s = grow_workspace(*ws, stream, num_seqs + 1, 0);
     if (s != PA_OK) return s;
     const size_t list_bytes = align_up((size_t)units * sizeof(pa::UnitX), 256);
     const size_t seq_bytes = align_up(((size_t)num_seqs + 1 + pre_units) * sizeof(int), 256);
@@ -926,12 +910,12 @@ pa_status enqueue_long(const void* q, const void* k, const void* v, const int32_
     const size_t lse_bytes = align_up((size_t)(slabs * slab_rows) * sizeof(float), 256);
     const size_t o_bytes = (size_t)(slabs * slab_rows) * head_dim * sizeof(float);
     void* aux = nullptr;
-    s = get_aux_scratch(ws, dev, stream, list_bytes + seq_bytes + tok_bytes + lse_bytes + o_bytes, &aux);
+    s = get_aux_scratch(ws, stream, list_bytes + seq_bytes + tok_bytes + lse_bytes + o_bytes, &aux);
     if (s != PA_OK) return s;
     char* at = static_cast<char*>(aux);
     Scratch scr{static_cast<pa::WorkspaceHeader*>(ws->ptr), ws_seqs(*ws), nullptr, (int)units, ws_seq_scratch(*ws)};
     if (o.rope_theta > 0.f) {
-        s = get_rope_scratch(ws, dev, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
+        s = get_rope_scratch(ws, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
         if (s != PA_OK) return s;
     }
     const int grid = (int)std::min<long long>(sms, units);
@@ -1203,13 +1187,13 @@ pa_status prefill_attn_key_weights(const void* q, const void* k, const int32_t* 
     const long long units = (long long)num_seqs * n_kv_heads * ((tiles + 1) / 2);
     if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
     const StreamLock lock(dev, stream);
-    Workspace* ws = nullptr;
-    s = get_workspace(dev, stream, num_seqs, (int)units, &ws);
+    Workspace* const ws = lock.ws;
+    s = grow_workspace(*ws, stream, num_seqs, (int)units);
     if (s != PA_OK) return s;
     Scratch scr{static_cast<pa::WorkspaceHeader*>(ws->ptr), ws_seqs(*ws), ws_units(*ws), ws->max_units,
                 ws_seq_scratch(*ws)};
     if (o.rope_theta > 0.f) {
-        s = get_rope_scratch(ws, dev, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
+        s = get_rope_scratch(ws, stream, (size_t)total_q * (n_heads + n_kv_heads) * head_dim * 2, &scr.rope);
         if (s != PA_OK) return s;
     }
     const int grid = (int)std::min<long long>(sms, units);
@@ -1312,12 +1296,12 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     const int sms = sm_count(dev, &s);
     if (s != PA_OK) return s;
     const StreamLock lock(dev, stream);
-    Workspace* ws = nullptr;
-    s = get_workspace(dev, stream, 0, 0, &ws);
+    Workspace* const ws = lock.ws;
+    s = grow_workspace(*ws, stream, 0, 0);
     if (s != PA_OK) return s;
     void* aux = nullptr;
     if (!kept_index) {
-        s = get_aux_scratch(ws, dev, stream, index_bytes, &aux);
+        s = get_aux_scratch(ws, stream, index_bytes, &aux);
         if (s != PA_OK) return s;
     }
     pa::EvictArgs a;
