@@ -222,6 +222,7 @@ def prefill_attn_varlen_ex(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v
 # tensor that failed).  Tensors have the shapes that their documentation states;
 # of the vectors of metadata the element count says whether they fit.
 _BF16, _I8, _F32, _I32 = torch.bfloat16, torch.int8, torch.float32, torch.int32
+_INT = 0x7fffffff
 
 
 def _check_tensors(device: int, *specs) -> None:
@@ -261,7 +262,8 @@ def _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_
     """Checks a call's cache tensors; returns (slot capacity, whether the cache is int8, shape of the cache's rows)."""
     if cache_k.dim() != 4:
         raise ValueError("caches are [num_seqs, kv_heads, cap, head_dim], or [num_blocks, kv_heads, block_size, head_dim]")
-    n, ck_heads, rows, ck_dim = cache_k.shape
+    shape = cache_k.shape
+    n, ck_heads, rows, ck_dim = shape
     if ck_heads != hk or ck_dim != d or (block_table is None and n != b):
         raise ValueError(f"cache_k has shape {tuple(cache_k.shape)}: {hk} KV heads of {d}"
                          + ("" if block_table is not None else f" in {b} slots") + " are wanted")
@@ -278,8 +280,8 @@ def _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_
         _check_tensors(device, ("cache_k_scale", cache_k_scale, _F32, total), ("cache_v_scale", cache_v_scale, _F32, total))
     cv = cache_k if cache_v is None else cache_v
     if not (cache_k.dtype is dtype and cache_k.is_contiguous() and cache_k.get_device() == device
-            and cv.dtype is dtype and cv.shape == cache_k.shape and cv.is_contiguous() and cv.get_device() == device):
-        _check_tensors(device, ("cache_k", cache_k, dtype, cache_k.shape), ("cache_v", cache_v, dtype, cache_k.shape))
+            and cv.dtype is dtype and cv.shape == shape and cv.is_contiguous() and cv.get_device() == device):
+        _check_tensors(device, ("cache_k", cache_k, dtype, shape), ("cache_v", cache_v, dtype, shape))
     return cap, quant, total
 
 
@@ -289,13 +291,14 @@ def _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q/k/v are [total_q, heads, head_dim]")
     device = _current_device(q)
-    (t, h, d), (kt, hk, kd), b = q.shape, k.shape, cache_offsets.numel()
+    q_shape, k_shape, b = q.shape, k.shape, cache_offsets.numel()
+    (t, h, d), (kt, hk, kd) = q_shape, k_shape
     if kt != t or kd != d:
-        raise ValueError(f"k has shape {tuple(k.shape)}, q {tuple(q.shape)}")
+        raise ValueError(f"k has shape {tuple(k_shape)}, q {tuple(q_shape)}")
     vv, oo = k if v is None else v, q if out is None else out
     if not (q.dtype is _BF16 and k.dtype is _BF16 and q.is_contiguous() and k.is_contiguous() and k.get_device() == device
-            and vv.dtype is _BF16 and vv.shape == k.shape and vv.is_contiguous() and vv.get_device() == device
-            and oo.dtype is _BF16 and oo.shape == q.shape and oo.is_contiguous() and oo.get_device() == device
+            and vv.dtype is _BF16 and vv.shape == k_shape and vv.is_contiguous() and vv.get_device() == device
+            and oo.dtype is _BF16 and oo.shape == q_shape and oo.is_contiguous() and oo.get_device() == device
             and (lse is None or lse.dtype is _F32 and lse.shape == (t, h) and lse.is_contiguous()
                  and lse.get_device() == device)
             and cu_seqlens_q.dtype is _I32 and cu_seqlens_q.numel() == b + 1 and cu_seqlens_q.is_contiguous()
@@ -303,8 +306,8 @@ def _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache
             and cu_seqlens_k.dtype is _I32 and cu_seqlens_k.numel() == b + 1 and cu_seqlens_k.is_contiguous()
             and cu_seqlens_k.get_device() == device
             and cache_offsets.dtype is _I32 and cache_offsets.is_contiguous() and cache_offsets.get_device() == device):
-        _check_tensors(device, ("q", q, _BF16, q.shape), ("k", k, _BF16, k.shape), ("v", v, _BF16, k.shape),
-                       ("out", out, _BF16, q.shape), ("lse", lse, _F32, (t, h)), ("cu_seqlens_q", cu_seqlens_q, _I32, b + 1),
+        _check_tensors(device, ("q", q, _BF16, q_shape), ("k", k, _BF16, k_shape), ("v", v, _BF16, k_shape),
+                       ("out", out, _BF16, q_shape), ("lse", lse, _F32, (t, h)), ("cu_seqlens_q", cu_seqlens_q, _I32, b + 1),
                        ("cu_seqlens_k", cu_seqlens_k, _I32, b + 1), ("cache_offsets", cache_offsets, _I32, b))
     return device, *_cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d)
 
@@ -319,7 +322,7 @@ def _pointers(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offse
 def _int32(**values) -> None:
     """The C calls take 32-bit integers, and ctypes cuts larger ones off without a word."""
     for name, v in values.items():
-        if v > 0x7fffffff or v < -0x80000000:
+        if v > _INT or v < -_INT - 1:
             raise ValueError(f"{name} = {v} does not fit 32 bits")
 
 
@@ -344,7 +347,8 @@ def prefill_attn_varlen_sinks(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cach
     The query at absolute position p sees key j when j <= p and (j > p - window or
     j < sink_tokens).  Tensors and options as in prefill_attn_varlen_ex.
     """
-    _int32(window=window, sink_tokens=sink_tokens)
+    if not (-1 <= window <= _INT and -1 <= sink_tokens <= _INT):
+        _int32(window=window, sink_tokens=sink_tokens)
     device, cap, _, _ = _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse,
                                         block_table, cache_k_scale, cache_v_scale)
     _check((_lib or load()).prefill_attn_varlen_sinks(
@@ -415,10 +419,12 @@ def prefill_attn_key_weights(q, k, cu_seqlens_q, cu_seqlens_k, cache_k, cache_of
     """
     if lse is None:
         raise ValueError("prefill_attn_key_weights needs lse")
-    _int32(window=window, sink_tokens=sink_tokens, prefix_len=prefix_len)
+    if not (-1 <= window <= _INT and -1 <= sink_tokens <= _INT and -1 <= prefix_len <= _INT):
+        _int32(window=window, sink_tokens=sink_tokens, prefix_len=prefix_len)
     device, cap, _, rows = _attention_args(q, k, None, cu_seqlens_q, cu_seqlens_k, cache_k, None, cache_offsets, None, lse,
                                            block_table, cache_k_scale, cache_k_scale)
-    _check_tensors(device, ("weights", weights, _F32, rows))
+    if not (weights.dtype is _F32 and weights.shape == rows and weights.is_contiguous() and weights.get_device() == device):
+        _check_tensors(device, ("weights", weights, _F32, rows))
     t, h, d = q.shape
     hk, b = k.shape[1], cache_offsets.numel()
     _check((_lib or load()).prefill_attn_key_weights(
@@ -438,15 +444,25 @@ def prefill_attn_evict(cache_k, cache_v, weights, lengths, kept_lengths, kept_in
     lengths / kept_lengths int32 [num_seqs]; kept_index int32 [num_seqs, n_kv_heads, budget] or
     None; weights / kept_weights fp32 of shape cache_k.shape[:-1] (kept_weights may be weights).
     """
-    _int32(budget=budget, sink_tokens=sink_tokens, recent_tokens=recent_tokens)
+    if not (-1 <= budget <= _INT and -1 <= sink_tokens <= _INT and -1 <= recent_tokens <= _INT):
+        _int32(budget=budget, sink_tokens=sink_tokens, recent_tokens=recent_tokens)
     device = _current_device(cache_k)
     if cache_k.dim() != 4:
         raise ValueError("caches are [num_seqs, kv_heads, cap, head_dim]")
     b, (_, hk, _, d) = lengths.numel(), cache_k.shape
     cap, _, rows = _cache_specs(device, cache_k, cache_v, b, block_table, cache_k_scale, cache_v_scale, hk, d)
-    _check_tensors(device, ("weights", weights, _F32, rows), ("lengths", lengths, _I32, b),
-                   ("kept_lengths", kept_lengths, _I32, b), ("kept_index", kept_index, _I32, (b, hk, budget)),
-                   ("kept_weights", kept_weights, _F32, rows))
+    if not (weights.dtype is _F32 and weights.shape == rows and weights.is_contiguous() and weights.get_device() == device
+            and lengths.dtype is _I32 and lengths.is_contiguous() and lengths.get_device() == device
+            and kept_lengths.dtype is _I32 and kept_lengths.numel() == b and kept_lengths.is_contiguous()
+            and kept_lengths.get_device() == device
+            and (kept_index is None or kept_index.dtype is _I32 and kept_index.shape == (b, hk, budget)
+                 and kept_index.is_contiguous() and kept_index.get_device() == device)
+            and (kept_weights is None or kept_weights is weights
+                 or kept_weights.dtype is _F32 and kept_weights.shape == rows and kept_weights.is_contiguous()
+                 and kept_weights.get_device() == device)):
+        _check_tensors(device, ("weights", weights, _F32, rows), ("lengths", lengths, _I32, b),
+                       ("kept_lengths", kept_lengths, _I32, b), ("kept_index", kept_index, _I32, (b, hk, budget)),
+                       ("kept_weights", kept_weights, _F32, rows))
     _check((_lib or load()).prefill_attn_evict(
         cache_k.data_ptr(), cache_v.data_ptr(), weights.data_ptr(), lengths.data_ptr(), kept_lengths.data_ptr(),
         _ptr(kept_index), _ptr(kept_weights), b, cap, hk, d, budget, sink_tokens, recent_tokens,
