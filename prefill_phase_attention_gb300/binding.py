@@ -326,6 +326,12 @@ def _int32(**values) -> None:
             raise ValueError(f"{name} = {v} does not fit 32 bits")
 
 
+def _unread(why: str, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None:
+            raise ValueError(f"{why}: {name} would not be read")
+
+
 def _options(cache_k, block_table, cache_k_scale, cache_v_scale, window=0, rope_theta=0.0, schedule=0):
     """pa_options by position (struct_size, window, block_table, block_size, max_blocks_per_seq, num_blocks, ...)."""
     paged, quant = block_table is not None, cache_k_scale is not None
@@ -368,9 +374,17 @@ def prefill_attn_varlen_prefix(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cac
     keys and values in their first prefix_len rows (default: all of them), with fp32
     prefix_k_scale / prefix_v_scale [n_kv_heads, capacity] for an int8 cache.  Paged cache:
     prefix_table (int32 CUDA, one entry per block) names the prefix's blocks in the pools,
-    and prefix_len its tokens.  cu_seqlens_k and cache_offsets count each sequence's own
-    tokens, which follow the prefix.
+    and prefix_len its tokens.  A tensor of the other kind is refused.  cu_seqlens_k and
+    cache_offsets count each sequence's own tokens, which follow the prefix.
     """
+    paged = block_table is not None
+    if paged and not (prefix_k is prefix_v is prefix_k_scale is prefix_v_scale is None):
+        _unread("a paged cache's prefix is in its pools (prefix_table, prefix_len)", prefix_k=prefix_k, prefix_v=prefix_v,
+                prefix_k_scale=prefix_k_scale, prefix_v_scale=prefix_v_scale)
+    if not paged and prefix_table is not None:
+        _unread("a contiguous cache's prefix is prefix_k and prefix_v", prefix_table=prefix_table)
+    if cache_k_scale is None and not (prefix_k_scale is prefix_v_scale is None):
+        _unread("a bf16 cache's prefix has no scales", prefix_k_scale=prefix_k_scale, prefix_v_scale=prefix_v_scale)
     device, cap, quant, _ = _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out,
                                             lse, block_table, cache_k_scale, cache_v_scale)
     pre = PaPrefix()

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from prefill_phase_attention_gb300 import binding, build
 from tests.test_long_context_abi import options, refused
@@ -109,3 +110,21 @@ def test_key_weights_refuses_overlapping_buffers(lib, kw, o, msg):
 def test_prefix_refuses_overlapping_buffers(lib, kw, p, o, msg):
     got = lib.prefill_attn_varlen_prefix(*attention(**kw), 1, prefix(**p), ctypes.byref(options(0, **o)), None)
     refused(lib, got, 1, msg)
+
+
+@pytest.mark.parametrize("kw,msg", [
+    (dict(block_table="t", prefix_table="t", prefix_len=3, prefix_k="x"), "prefix_k"),
+    (dict(block_table="t", prefix_table="t", prefix_len=3, prefix_v="x"), "prefix_v"),
+    (dict(block_table="t", prefix_table="t", prefix_len=3, prefix_k_scale="x"), "prefix_k_scale"),
+    (dict(block_table="t", prefix_table="t", prefix_len=3, prefix_v_scale="x"), "prefix_v_scale"),
+    (dict(prefix_k="x", prefix_v="x", prefix_table="t"), "prefix_table"),
+    (dict(prefix_k="x", prefix_v="x", prefix_k_scale="x"), "prefix_k_scale"),
+    (dict(prefix_k="x", prefix_v="x", prefix_v_scale="x"), "prefix_v_scale"),
+])
+def test_binding_refuses_a_prefix_of_the_other_kind_of_cache(lib, kw, msg):
+    """A prefix tensor that the call would not read is an error, not ignored."""
+    x, t = torch.zeros(4, 2, 32, dtype=torch.bfloat16), torch.zeros((1, 2), dtype=torch.int32)
+    kw = {n: {"x": x, "t": t}.get(v, v) if isinstance(v, str) else v for n, v in kw.items()}
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match=msg):
+        binding.prefill_attn_varlen_prefix(x, x, x, i, i, x[None], x[None], i[:1], x, **kw)
