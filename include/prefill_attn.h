@@ -56,7 +56,9 @@
  *     Graphs captured on one stream share that stream's workspace, so their
  *     replays must not overlap each other or the stream's own calls.  A
  *     workspace that a captured call uses is kept until prefill_attn_release()
- *     even when a later call outgrows it.
+ *     even when a later call outgrows it; each that takes its place is then at
+ *     least twice as large (where memory allows), so that a stream keeps at most
+ *     about four times what its largest call needs.
  *     prefill_attn_varlen_noalloc allocates nothing at all.
  */
 #ifndef PREFILL_ATTN_H

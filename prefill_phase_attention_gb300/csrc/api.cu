@@ -127,6 +127,21 @@ bool capturing(cudaStream_t st) {
     return cudaStreamIsCapturing(st, &cs) == cudaSuccess && cs == cudaStreamCaptureStatusActive;
 }
 
+// Allocates (stream-ordered) a block of at least `need` bytes in place of one of
+// `old`.  Where that one stays for a captured graph, the new one is at least twice
+// its size (if there is room), so that all blocks which stay together are smaller
+// than the newest.
+cudaError_t alloc_block(const Workspace& w, size_t old, size_t need, cudaStream_t st, void** ptr, size_t* bytes) {
+    *bytes = w.captured ? std::max(need, 2 * old) : need;
+    cudaError_t e = cudaMallocAsync(ptr, *bytes, st);
+    if (e == cudaErrorMemoryAllocation && *bytes > need) {
+        cudaGetLastError();
+        *bytes = need;
+        e = cudaMallocAsync(ptr, need, st);
+    }
+    return e;
+}
+
 // Grows the workspace of a stream (stream-ordered) when needed; its lock is held, as
 // in the next two.  Under graph capture nothing is allocated: the stream must already
 // hold a workspace big enough (from a call outside the capture).
@@ -141,13 +156,15 @@ pa_status grow_workspace(Workspace& w, cudaStream_t st, int num_seqs, int max_un
                     "run a call of at least these sizes on this stream before capturing",
                     num_seqs, max_units);
     const int seqs = std::max(num_seqs, std::max(w.max_seqs, 64));
-    const int units = std::max(max_units, std::max(w.max_units, 4096));
-    const size_t bytes = ws_bytes(seqs, units);
+    int units = std::max(max_units, std::max(w.max_units, 4096));
+    size_t bytes = 0;
     prepare_drop(w);
     if (w.captured) w.old_headers.reserve(w.old_headers.size() + 1);
     void* ptr = nullptr;
-    cudaError_t e = cudaMallocAsync(&ptr, bytes, st);
+    cudaError_t e = alloc_block(w, w.bytes, ws_bytes(seqs, units), st, &ptr, &bytes);
     if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(workspace)");
+    // what is left of a larger block is room for units
+    units = (int)std::min<size_t>(INT_MAX, units + (bytes - ws_bytes(seqs, units)) / sizeof(pa::Unit));
     e = cudaMemsetAsync(ptr, 0, sizeof(pa::WorkspaceHeader), st);
     if (e == cudaSuccess && w.ptr)  // keep sticky error bits across a regrow
         e = cudaMemcpyAsync(ptr, w.ptr, sizeof(int), cudaMemcpyDeviceToDevice, st);
@@ -174,7 +191,7 @@ pa_status get_rope_scratch(Workspace* w, cudaStream_t st, size_t bytes, void** o
     if (w->rope_bytes < bytes) {
         prepare_drop(*w);
         void* nptr = nullptr;
-        cudaError_t e = cudaMallocAsync(&nptr, bytes, st);
+        cudaError_t e = alloc_block(*w, w->rope_bytes, bytes, st, &nptr, &bytes);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(rotary scratch)");
         drop_block(*w, w->rope, st);
         w->rope = nptr;
@@ -194,7 +211,7 @@ pa_status get_aux_scratch(Workspace* w, cudaStream_t st, size_t bytes, void** ou
     if (w->aux_bytes < bytes) {
         prepare_drop(*w);
         void* nptr = nullptr;
-        cudaError_t e = cudaMallocAsync(&nptr, bytes, st);
+        cudaError_t e = alloc_block(*w, w->aux_bytes, bytes, st, &nptr, &bytes);
         if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(auxiliary scratch)");
         drop_block(*w, w->aux, st);
         w->aux = nptr;
