@@ -402,7 +402,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, int b, int h, int 
     const int tid = threadIdx.x;
     const Rows row_of(a, b, h);
     uint8_t* const cache = static_cast<uint8_t*>(which ? a.cache_v : a.cache_k) + part * a.part_bytes;
-    const int log_pieces = a.part_bytes == 64 ? 2 : a.part_bytes == 32 ? 1 : 3;  // 16-byte pieces of a part
+    const int log_pieces = a.part_bytes == 64 ? 2 : 1;  // 16-byte pieces of a part (64 bytes, or a row of 32)
     const int rows = (kThreads * kVec) >> log_pieces;                           // of a chunk
     const int piece = tid & ((1 << log_pieces) - 1), row0 = tid >> log_pieces, step = kThreads >> log_pieces;
     auto sources = [&](int j0, int (&src)[kVec]) {
