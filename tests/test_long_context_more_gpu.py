@@ -72,3 +72,27 @@ def test_evict_refuses_other_shapes_of_as_many_elements(name):
     t[name] = swapped(t[name])
     with pytest.raises(ValueError, match=name):
         binding.prefill_attn_evict(**t, budget=50)
+
+
+# --------------------------------------------------------------------------- eviction: what a CTA selects from alone
+
+@pytest.mark.parametrize("kept", ["new", "same"])
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 1), (500, 4, 100), (2046, 0, 3), (2047, 3, 0), (2048, 4, 1000), (2049, 1, 1)])
+def test_evict_at_the_length_that_one_launch_selects_alone(budget, sinks, recent, kept):
+    """One launch: a CTA selects from up to 2048 tokens alone (its list is full at 2048 kept), its cluster from more."""
+    for d, int8, block in ((64, False, 0), (32, True, 16)):
+        c = Call(320, [0] * 3, [2047, 2048, 2049], d, 2, 1, block, int8)
+        evict(c, weights_for(c, 1, "ties" if d == 64 else "special"), budget, sinks, recent, kept=kept)
+        assert binding.prefill_attn_last_launch_count() == 1
+    ok()
+
+
+@pytest.mark.parametrize("kept", ["new", "same"])
+@pytest.mark.parametrize("budget,sinks,recent", [(1, 0, 1), (500, 4, 100), (4095, 0, 3), (4096, 4, 1000), (4097, 1, 1)])
+def test_evict_at_the_length_that_two_launches_select_alone(budget, sinks, recent, kept):
+    """Two launches: a CTA selects from up to 4096 tokens alone, its cluster from more; a capacity of 4096 has no cluster."""
+    for lens, slack in (([4095, 4096, 4097], 3), ([4096, 4095, 4096], 0)):
+        c = Call(321, [0] * 3, lens, 32, 60, 1, slack=slack)
+        evict(c, weights_for(c, 2, "special" if slack else "ties"), budget, sinks, recent, kept=kept)
+        assert binding.prefill_attn_last_launch_count() == 2
+    ok()
