@@ -3,6 +3,7 @@ import pytest
 import torch
 
 from prefill_phase_attention_gb300 import binding
+from tests import long_reference as R
 from tests.test_long_context_gpu import Call, evict, ok, weights_for
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +97,88 @@ def test_evict_at_the_length_that_two_launches_select_alone(budget, sinks, recen
         evict(c, weights_for(c, 2, "special" if slack else "ties"), budget, sinks, recent, kept=kept)
         assert binding.prefill_attn_last_launch_count() == 2
     ok()
+
+
+# --------------------------------------------------------------------------- what the attention calls leave in the cache
+
+def rows_written(c, skipped=()):
+    """[slots, heads, rows] of the cache: whether a sequence's new token has its row there; and the tokens of those rows
+    in the order that the mask picks them."""
+    at = torch.full(c.cache.shape[:-1], -1, dtype=torch.long)
+    for b, (n, p) in enumerate(zip(c.new, c.lens)):
+        if b in skipped:
+            continue
+        slot, row = c.cache.at(b, torch.arange(p, p + n))
+        at[slot, :, row] = torch.arange(c.cu[b], c.cu[b + 1])[:, None]
+    return at >= 0, at
+
+
+def check_cache(c, w, new, tol, skipped=()):
+    """K (w = 0) or V (1): the new tokens' rows within tol of `new` [tokens, heads, d] (None: the documented write, bit
+    for bit), every other row as it was."""
+    got, was = c.data[w][1].cpu(), c.cache.data[w]
+    here, token = rows_written(c, skipped)
+    assert torch.equal(R.bits(got)[~here], R.bits(was)[~here]), "a row that holds no new token was written"
+    sc = None if c.sc[w] is None else c.sc[w][1].cpu()
+    if sc is not None:
+        assert torch.equal(R.bits(sc)[~here], R.bits(c.cache.scale[w])[~here]), "a scale of no new token was written"
+    if tol is None:
+        data, scale = c.cache.written(w, new, c.cu)
+        assert torch.equal(R.bits(got)[here], R.bits(data)[here])
+        assert sc is None or torch.equal(R.bits(sc)[here], R.bits(scale)[here])
+        return
+    head = torch.arange(c.hk)[None, :, None].expand(here.shape)[here]
+    ref, tol = new[token[here], head].double(), tol[token[here], head].double()
+    x = got[here].double()
+    if sc is not None:
+        step = sc[here].double()[:, None]
+        most = ref.abs().amax(-1, keepdim=True)
+        assert ((step * 127 - most).abs() <= tol.amax(-1, keepdim=True) + most * 2.0 ** -22).all(), "scale"
+        x, tol = x * step, tol + step * (0.5 + 2.0 ** -10)  # and half a step of the code
+    err = (x - ref).abs()
+    assert (err <= tol).all(), f"off by {(err / tol).max():.2f} of the tolerance"
+
+
+@pytest.mark.parametrize("block", [0, 32])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("call,new,lens", [("sinks", [3, 40, 0, 1], [300, 0, 9, 77]), ("prefix", [2, 17, 0, 130], [100, 0, 9, 31]),
+                                           ("prefix", [1, 1], [64, 3])])
+def test_rotary_keys_in_the_cache(call, new, lens, int8, block):
+    """The cache gets the keys rotated to their absolute positions, behind the shared prefix's, and the values as given.
+
+    Tolerance: the library's angle is position * inv_freq in fp32, inv_freq by a division and a power that may each be
+    an ulp off the reference's, so an angle is within position * 2^-22 of it; a rotated value a cos - b sin moves by at
+    most (|a| + |b|) times that and by its own fp32 roundings, (|a| + |b|) 2^-21; then both round to bf16, where two
+    neighbours may be picked: a spacing, 2^-7 of the value.
+    """
+    theta, pre = 1e4, 150 if call == "prefix" else 0
+    c = Call(330, new, lens, 64, 2, 2, block, int8, pre)
+    c.sinks(90, 4, theta=theta) if call == "sinks" else c.prefix(theta=theta)
+    torch.cuda.synchronize()
+    c.guards()
+    pos = torch.cat([torch.arange(n) + p + pre for n, p in zip(new, lens)])
+    want = R.rotate(c.k, pos, theta)
+    a, b = c.k.double().abs().chunk(2, -1)
+    tol = 2.0 ** -7 * want.double().abs() + (a + b).repeat(1, 1, 2) * (pos.double()[:, None, None] * 2.0 ** -22 + 2.0 ** -21)
+    # the test can tell: neither the key as given nor the one at the position without the prefix would pass
+    for other in (c.k, R.rotate(c.k, pos - pre, theta) if pre else c.k, R.rotate(c.k, pos + 1, theta)):
+        moved = pos > 0
+        assert ((other.double() - want.double()).abs() > tol)[moved].any(-1).float().mean() > 0.9
+    check_cache(c, 0, want, tol)
+    check_cache(c, 1, c.v, None)
+    ok()
+
+
+@pytest.mark.parametrize("block", [0, 32])
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("call", ["sinks", "prefix"])
+def test_skipped_sequences_leave_the_other_caches_written(call, int8, block):
+    """One sequence's metadata is inconsistent: the others' new rows are written, and nothing else."""
+    c = Call(331, [1, 3, 40, 2], [20, 7, 200, 0], 64, 2, 2, block, int8, prefix=40 if call == "prefix" else 0)
+    c.offsets[1] = 8  # disagrees with cu_seqlens_k
+    c.sinks(64, 4) if call == "sinks" else c.prefix()
+    torch.cuda.synchronize()
+    c.guards()
+    for w, new in ((0, c.k), (1, c.v)):
+        check_cache(c, w, new, None, skipped=[1])
+    assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
