@@ -1,4 +1,6 @@
 """More GPU tests of the long-context calls: sizes, options and argument shapes at their edges."""
+import math
+
 import pytest
 import torch
 
@@ -182,3 +184,50 @@ def test_skipped_sequences_leave_the_other_caches_written(call, int8, block):
     for w, new in ((0, c.k), (1, c.v)):
         check_cache(c, w, new, None, skipped=[1])
     assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+
+
+# --------------------------------------------------------------------------- precision of the key weights
+
+@pytest.mark.parametrize("new,lens,d,group,block,int8", [
+    ([2000], [0], 128, 1, 0, False),                   # 16 Q tiles under one key
+    ([700, 90], [300, 0], 64, 4, 16, False),
+    ([700, 90], [300, 0], 64, 4, 0, True),
+    ([1] * 6, [900, 17, 0, 128, 300, 64], 128, 8, 0, False),
+    ([1, 2, 30], [900, 17, 300], 32, 4, 32, True),
+    ([150, 3], [40, 500], 64, 48, 0, False),           # 96 of a Q tile's 128 columns: bounds tested in every column
+])
+def test_key_weights_to_fp32(new, lens, d, group, block, int8):
+    """Scores that fp32 holds exactly (q and k of -1, 0 and 1, or int8 codes), so that what is left is the exponent's
+    argument, the exponential and the sum.
+
+    In units of 2^-24, relative to a term: the argument x - l (in powers of two) has the roundings of log2(e), of its
+    products with the scale, a row's scale and lse, and its own, at most 4 |x| + 3 |l| (of which ln 2 reaches the
+    term); ex2.approx is within 4 of its result.  The sum of positive terms: chains of at most 64 columns of a Q tile,
+    joined, then one addition per Q tile and at most three more: 70 + tiles.
+    """
+    c = Call(340, new, lens, d, 2, group, block, int8)
+    g = torch.Generator().manual_seed(9)
+    ints = lambda x: torch.randint(-1, 2, x.shape, generator=g).to(x.dtype)  # noqa: E731
+    c.q, c.k, c.scale = ints(c.q), ints(c.k), 0.125
+    c.dev[0].copy_(c.q), c.dev[1].copy_(c.k)
+    if not int8:
+        data = c.cache.data[0]
+        c.cache.data[0] = torch.where(data.isnan(), data, ints(data))
+        c.data[0][1].copy_(c.cache.data[0])
+    lse = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale)[1].float()
+    w = c.weights.cuda()
+    binding.prefill_attn_key_weights(c.dev[0], c.dev[1], *c.meta, c.data[0][1], c.offsets, lse.cuda(), w, scale=c.scale,
+                                     cache_k_scale=c.scales["cache_k_scale"], **c.opts)
+    ref = R.key_weights(c.cache, c.q, c.k, c.new, lse, c.scale, c.weights)
+    keys = c.k.double().norm(dim=-1).max()
+    for b in range(len(lens)):
+        if lens[b]:
+            keys = max(keys, c.cache.logical(0, b).norm(dim=-1).max())
+    x = math.log2(math.e) * c.scale * float(c.q.double().norm(dim=-1).max() * keys)  # |q . k| <= |q| |k|
+    l2 = math.log2(math.e) * float(lse.abs().max())
+    tiles = max(-(-n // (128 // group)) for n in new)
+    tol = 2.0 ** -24 * (math.log(2) * (4 * x + 3 * l2) + 4 + 70 + tiles) * ref.abs() + 1e-30
+    assert tol.max() / ref.abs().max() < 2.0 ** -14
+    err = (w.cpu().double() - ref).abs()
+    assert (err <= tol).all(), f"off by {(err / tol).max():.2f} of the tolerance"
+    ok()
