@@ -860,8 +860,10 @@ pa_status read_prefix(const pa_prefix* prefix, const Options& o, Prefix* out) {
     return PA_OK;
 }
 
-// Slabs of partial results are bounded by this many bytes for the sequences' own
-// keys (a few long rows: up to kMaxPieces pieces) and for the prefix's.
+// Rows are cut into as many pieces as have slabs of partial results within this many
+// bytes, at most kMaxPieces: one bound for the sequences' own keys, one for the
+// prefix's.  One slab (total_q rows of n_heads outputs) is the least that each part of a
+// prefix call has, however large: two of 0.54 GB for 32768 new tokens of 32 heads, D = 128.
 constexpr long long kPartialBytes = 64ll << 20, kPrefixPartialBytes = 256ll << 20;
 using pa::kMaxPieces;
 constexpr int kMinPieceTiles = 4;

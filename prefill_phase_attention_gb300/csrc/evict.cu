@@ -22,14 +22,21 @@
 // part (64 bytes where the row has them) of K or of V; parts never touch one
 // another's bytes, so no CTA waits for another.
 //
-// Two forms, picked by the launch's size.  A launch whose CTAs all run at once
-// is bound by latency: evict_kernel does both in one launch, a cluster of 2, 4
-// or 8 CTAs (its column parts) per (sequence, head).  A larger one is bound by
-// HBM, and a CTA that selects moves no bytes: select_kernel runs first, one CTA
-// (or a cluster) per (sequence, head), then move_kernel.  Measured (graph, 8 heads):
+// Two forms, picked by the number of CTAs.  While they all run at once, evict_kernel
+// does both in one launch, a cluster of 2, 4 or 8 CTAs (its column parts) per
+// (sequence, head).  With more of them a CTA that selects keeps one that moves from
+// running: select_kernel runs first, one CTA (or a cluster) per (sequence, head), then
+// move_kernel, which HBM bounds.  Measured (graph, 8 heads):
 // 4 sequences of about 510 tokens to 384 7.8 us in one launch, 10.1 in two; 16 of
 // 16384 to 4096 133 and 110 (select 19, move 85 at 6.3 TB/s); 64 of 700-4099 to
 // 1024 in int8 pages 97 and 62.6.
+// Few long caches take the first form too, and neither is near HBM there: a column
+// part of a head is one CTA's, whatever its length, 8 KB fetched while 8 KB are
+// written.
+// Single cold passes, D = 128 bf16, to a quarter, one launch and two: one cache of
+// 8192 tokens of 8 heads 34 and 38 us, of 32768 91 and 91 (0.75 TB/s), of 131072 333
+// and 351; of 32768 tokens of 2 heads 91 and 89 (0.19 TB/s); four of 16384 of 8
+// heads 59 and 67 (2.4 TB/s).
 #include <cooperative_groups.h>
 
 #include <cstdint>

@@ -253,7 +253,11 @@ __device__ __forceinline__ int wide_length(unsigned long long wide_tiles, int nu
 
 // Key tiles of a unit of a sequence whose queries fit one Q tile: about three
 // units per CTA of the `total` tiles of all of them (64 decode rows over 256-4096
-// cached tokens: 55.0 us; 55.9 with four, 60.9 with eight, 56.4 with two).
+// cached tokens, replayed: 55.0 us; 55.9 with four, 60.9 with eight, 56.4 with two).
+// Single cold passes with two, three, four and eight: those rows in int8 pages 79,
+// 79, 81 and 91 us; 8 rows over 16384 tokens 67, 65, 65 and 65; one row over 32768
+// 28, 28, 31 and 30; 32 rows of 4 heads over 2048-32768 116, 115, 114 and 114; 256 rows
+// over 128-1024 93 with each (a unit is a whole row of a head there).
 __device__ __forceinline__ int run_length(unsigned long long total, int num_ctas) {
     const unsigned long long per = total / (3u * (unsigned)num_ctas);
     return per >= kMaxRun ? kMaxRun : (per < 2 ? 2 : (int)per & ~1);
