@@ -387,33 +387,35 @@ def prefill_attn_varlen_prefix(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cac
         _unread("a bf16 cache's prefix has no scales", prefix_k_scale=prefix_k_scale, prefix_v_scale=prefix_v_scale)
     device, cap, quant, _ = _attention_args(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out,
                                             lse, block_table, cache_k_scale, cache_v_scale)
-    pre = PaPrefix()
-    pre.struct_size = _PREFIX_SIZE
-    if block_table is not None:
+    if paged:
         if prefix_table is None or prefix_len is None:
             raise ValueError("a paged cache needs prefix_table and prefix_len")
         _check_tensors(device, ("prefix_table", prefix_table, _I32, prefix_table.numel()))
         if prefix_len > prefix_table.numel() * cache_k.shape[2]:
             raise ValueError("prefix_table has fewer blocks than prefix_len needs")
-        pre.block_table = prefix_table.data_ptr()
+        _int32(prefix_len=prefix_len)
+        pre = PaPrefix(_PREFIX_SIZE, prefix_len, None, None, 0, 0, None, None, prefix_table.data_ptr())
     else:
         if prefix_k is None or prefix_v is None:
             raise ValueError("a contiguous cache needs prefix_k and prefix_v")
-        if prefix_k.dim() != 3 or prefix_k.shape[0] != k.shape[1] or prefix_k.shape[2] != q.shape[2]:
+        shape, dtype = prefix_k.shape, _I8 if quant else _BF16
+        if len(shape) != 3 or shape[0] != k.shape[1] or shape[2] != q.shape[2]:
             raise ValueError("prefix_k is [n_kv_heads, capacity, head_dim]")
-        dtype = _I8 if quant else _BF16
-        _check_tensors(device, ("prefix_k", prefix_k, dtype, prefix_k.shape), ("prefix_v", prefix_v, dtype, prefix_k.shape))
-        pre.k, pre.v, pre.capacity = prefix_k.data_ptr(), prefix_v.data_ptr(), prefix_k.shape[1]
-        if prefix_len is None:
-            prefix_len = prefix_k.shape[1]
+        if not (prefix_k.dtype is dtype and prefix_k.is_contiguous() and prefix_k.get_device() == device
+                and prefix_v.dtype is dtype and prefix_v.shape == shape and prefix_v.is_contiguous()
+                and prefix_v.get_device() == device):
+            _check_tensors(device, ("prefix_k", prefix_k, dtype, shape), ("prefix_v", prefix_v, dtype, shape))
         if quant:
             for name, t in (("prefix_k_scale", prefix_k_scale), ("prefix_v_scale", prefix_v_scale)):
                 if t is None:
                     raise ValueError(f"an int8 cache needs {name}")
-                _check_tensors(device, (name, t, _F32, prefix_k.shape[:2]))
-            pre.k_scale, pre.v_scale = prefix_k_scale.data_ptr(), prefix_v_scale.data_ptr()
-    _int32(prefix_len=prefix_len)
-    pre.len = prefix_len
+                _check_tensors(device, (name, t, _F32, shape[:2]))
+        if prefix_len is None:
+            prefix_len = shape[1]
+        if not -1 <= prefix_len <= _INT:
+            _int32(prefix_len=prefix_len)
+        pre = PaPrefix(_PREFIX_SIZE, prefix_len, prefix_k.data_ptr(), prefix_v.data_ptr(), shape[1], 0,
+                       _ptr(prefix_k_scale), _ptr(prefix_v_scale), None)
     _check((_lib or load()).prefill_attn_varlen_prefix(
         *_pointers(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse, cap, scale),
         1 if causal else 0, pre, _options(cache_k, block_table, cache_k_scale, cache_v_scale, 0, rope_theta, schedule),
