@@ -408,13 +408,13 @@ __device__ __noinline__ void zero_tile_rows(uint8_t* tile, int row0, int lane) {
 // upper half of a bf16 stage; this expands it in place into the swizzled bf16
 // tile the MMA reads (one warp): value = code * scale[row] rounded to bf16 when
 // kScale (sc[q] holds the scale of row 32 q + lane), else the code itself
-// (exact in bf16).  K's scales multiply the fp32 scores; V's belong to the rows that
-// P V sums over, so they have to be in an operand of that MMA: code * scale is rounded
-// to bf16 here (2^-8 at most, beside P's and the output's own roundings: 0.0028 of the
-// output in 2-norm against 0.0024 with a bf16 cache).  Scaling P before its rounding
-// instead would save this one; it is not done, the softmax warps would need V's scales
-// ahead of every tile.  Rows go in increasing order, kGroup batches of rows at a
-// time, each group read before it is written: the bf16 image of row r ends
+// (exact in bf16).  K's scales multiply the fp32 scores.  V's belong to the rows that
+// P V sums over, so they have to be in an operand of that MMA.  The long-context
+// variant has them in P, ahead of its rounding to bf16: P's and the output's are the
+// only roundings.  The other calls round the values here, a third one (2-norm errors
+// of the output 0.0023 and 0.0028), and keep the bits that they gave before.  Rows go
+// in increasing order, kGroup batches of rows at a time, each group read before it is
+// written: the bf16 image of row r ends
 // within the codes of rows <= r, so no code is overwritten unread.
 template <int D, bool kScale>
 __device__ __noinline__ void dequant_tile(uint8_t* stage, const float (&sc)[4], int lane) {
@@ -555,11 +555,20 @@ __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, Work
 // A CTA's own units when it plans for itself (FwdParamsX::direct), in list
 // order; u.b < 0: none.  The host takes this path only where a CTA gets a few.
 constexpr int kOwnUnits = 8;
-struct OwnUnits {
+struct __align__(16) OwnUnits {
     UnitX x[kOwnUnits];
     SeqInfo s[kOwnUnits];
     int next;
 };
+
+// Long-context variant over an int8 cache: the row scales of V's tiles, published by
+// K's cache writer beside those of K, for the softmax warps to multiply P by.  head_dim 32 and 64: a ring behind OwnUnits, as deep as K's
+// (Ctrl::kscale).  128: the tiles leave no room for it, so K's ring of four becomes two
+// slots of each.
+template <int D>
+constexpr int scale_ring_bytes() {
+    return D == 128 ? 0 : 4 * kBlockN * (int)sizeof(float);
+}
 
 // Claims the next unit that has tiles (the scheduler leaves holes in the list
 // where a query block has fewer tiles than its sequence has pieces).
@@ -603,7 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     // once its stage was released by the S of tile t + 4 - kStK, which the MMA
     // warp issues after the PV of tile t + 3 - kStK of every slot.  With at most
     // 3 stages that PV follows every slot's softmax of tile t: the ring slot is
-    // free.  (bf16 caches use no scale ring.)
+    // free.  (bf16 caches use no scale ring.)  A ring of two (long-context variant at
+    // head_dim 128): see its writer.
     constexpr int kStK = kQuant && C::kStagesK > 3 ? 3 : C::kStagesK;
     // paged bf16 cache, two column chunks: prefix tiles staged block by block
     constexpr bool kGrp = kPaged && !kQuant && C::kChunks == 2;
@@ -616,6 +626,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     uint8_t* v_smem = k_smem + C::kStagesK * C::kTileBytes;  // [kStagesV] tiles
     Ctrl* ctl = reinterpret_cast<Ctrl*>(v_smem + C::kStagesV * C::kTileBytes);
     OwnUnits* own = reinterpret_cast<OwnUnits*>(ctl + 1);  // kExt
+    // V's scales go into P (kVScale); slots of tile t in the rings of K's and V's scales
+    constexpr bool kVScale = kExt && kQuant;
+    constexpr int kScaleSlots = kVScale && D == 128 ? 2 : 4;
+    auto kscale_slot = [&](uint32_t t) -> float* { return ctl->kscale[t & (kScaleSlots - 1)]; };
+    auto vscale_slot = [&](uint32_t t) -> float* {
+        return kScaleSlots == 2 ? ctl->kscale[2 + (t & 1)] : reinterpret_cast<float*>(own + 1) + (t & 3) * kBlockN;
+    };
     bool direct = false;
     if constexpr (kExt) direct = p.direct != 0;
 
@@ -1221,6 +1238,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         uint64_t* empty = is_k ? ctl->k_empty : ctl->v_empty;
         __nv_bfloat16* cache = is_k ? p.cache_k : p.cache_v;
         uint32_t t = 0;
+        // K's writer, rings of two scale slots: waits until tile t - 2, the last one in
+        // tile t's slot, is through every slot's softmax.  Its PV was issued before the S
+        // of tile t - 1, whose end releases that tile's stage (its next use takes an
+        // arrival of this warp, so the phase cannot run on).  That end also lets the
+        // load of this warp's next tile begin, so the wait costs nothing.
+        auto scale_slot_free = [&](uint32_t t) -> bool {
+            if (kScaleSlots == 4 || t == 0) return true;
+            static_assert(kScaleSlots == 4 || kStK == 2, "the tile whose stage is waited for is the one before");
+            return warp_wait(&ctl->k_empty[(t - 1) % kStK], ((t - 1) / kStK) & 1, ctl, hdr);
+        };
         for (int u_it = 0;; ++u_it) {
             const int sl = u_it & 1;
             if (!warp_wait(&ctl->unit_full[sl], (u_it >> 1) & 1, ctl, hdr)) break;
@@ -1240,9 +1267,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     // int8 prefix tile: expand the codes for the MMA.  V rows
                     // become code * scale; K rows stay the (exact) codes and
                     // their scales go to the scale ring, folded into the scores.
+                    // kVScale: V rows stay codes too, K's writer publishes both scales.
                     const int kb = tile_key_base<kPaged>(j, us.s.P, np);
                     const float* scales = is_k ? p.scale_k : p.scale_v;
-                    float sc[4];
+                    float sc[4], sc_v[4];  // (sc_v: kVScale)
                     if (kPaged) {
                         // row scales through the block table; rows from P on (rest of the
                         // last block, stale rows) get scale 0 and so expand to zeros
@@ -1253,26 +1281,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const int pos = kb + 32 * q + lane;
-                            sc[q] = 0.f;
+                            sc[q] = sc_v[q] = 0.f;
+                            if (kVScale && !is_k) continue;
                             if (pos < us.s.P) {
                                 const int blk = __ldg(tab + (pos >> p.block_log2));
-                                if ((unsigned)blk < (unsigned)p.num_blocks)
-                                    sc[q] = __ldg(scales + ((((size_t)blk * p.n_kv_heads + us.u.kvh) << p.block_log2) +
-                                                            (pos & bmask)));
+                                if ((unsigned)blk < (unsigned)p.num_blocks) {
+                                    const size_t row = (((size_t)blk * p.n_kv_heads + us.u.kvh) << p.block_log2) + (pos & bmask);
+                                    sc[q] = __ldg(scales + row);
+                                    if (kVScale) sc_v[q] = __ldg(p.scale_v + row);
+                                }
                             }
                         }
                     } else {
-                        const float* srow = scales + ((size_t)us.u.b * p.n_kv_heads + us.u.kvh) * p.max_cache_len;
+                        size_t row0 = ((size_t)us.u.b * p.n_kv_heads + us.u.kvh) * p.max_cache_len;
+                        const float* scales_v = p.scale_v;
                         if constexpr (kExt)
-                            if (ug.pre)
-                                srow = (is_k ? p.prefix_scale_k : p.prefix_scale_v) + (size_t)us.u.kvh * p.prefix_cap;
+                            if (ug.pre) {
+                                scales = is_k ? p.prefix_scale_k : p.prefix_scale_v;
+                                scales_v = p.prefix_scale_v;
+                                row0 = (size_t)us.u.kvh * p.prefix_cap;
+                            }
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             const int row = kb + 32 * q + lane;  // rows below 0 are zero-filled codes
-                            sc[q] = row >= 0 ? __ldg(srow + row) : 0.f;
+                            sc[q] = sc_v[q] = 0.f;
+                            if (row < 0 || (kVScale && !is_k)) continue;
+                            sc[q] = __ldg(scales + row0 + row);
+                            if (kVScale) sc_v[q] = __ldg(scales_v + row0 + row);
                         }
                     }
                     if (!warp_wait(&full[st], (t / stages) & 1, ctl, hdr)) { ok = false; break; }
+                    if constexpr (kVScale) {
+                        dequant_tile<D, false>(ring + st * C::kTileBytes, sc, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(is_k ? &ctl->k_conv[st] : &ctl->v_conv[st]);
+                        if (is_k) {
+                            if (!scale_slot_free(t)) { ok = false; break; }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                kscale_slot(t)[32 * q + lane] = sc[q];
+                                vscale_slot(t)[32 * q + lane] = sc_v[q];
+                            }
+                            __syncwarp();
+                        }
+                        if (lane == 0) {
+                            if (is_k) mbar_arrive(&ctl->ks_full[t & 3]);
+                            mbar_arrive(&empty[st]);
+                        }
+                        continue;
+                    }
                     if (is_k) {
                         dequant_tile<D, false>(ring + st * C::kTileBytes, sc, lane);
 #pragma unroll
@@ -1729,11 +1787,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 }
                 const int jrel = ug.a[slot] + j;  // tile index in the unit's stream
                 const int jt = tile_at(ug, jrel);  // tile index in the sequence
+                const uint32_t tc = tg0 + jrel;
                 if (kQuant && jt < np) {
                     // int8 prefix tile: S holds q . code; scale column c by its row's scale
-                    const uint32_t tc = tg0 + jrel;
                     if (!warp_wait(&ctl->ks_full[tc & 3], (tc >> 2) & 1, ctl, hdr)) { ok = false; break; }
-                    const float4* ksc = reinterpret_cast<const float4*>(ctl->kscale[tc & 3]);
+                    const float4* ksc = reinterpret_cast<const float4*>(kscale_slot(tc));
 #pragma unroll
                     for (int c4 = 0; c4 < kBlockN / 4; ++c4) {
                         const float4 f = ksc[c4];
@@ -1796,16 +1854,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 // exponent arguments and the row sum on packed fp32 pairs
                 const float2 sl2v = make_float2(sl2, sl2), negm = make_float2(-m_use, -m_use);
                 float2 sum2 = make_float2(0.f, 0.f);
+                // kVScale: V's tile holds codes where it is of the cache, and P is multiplied
+                // by its scales (by 1 for new tokens: a prompt without cached keys takes 4 %
+                // more, 8192 tokens of 32 heads 935 us against 895; the loop twice, without
+                // the product for those, 930, and the others up to 3 % slower)
+                const float4* const vsc = reinterpret_cast<const float4*>(vscale_slot(tc));
+                const bool coded = jt < np;
 #pragma unroll
                 for (int c4 = 0; c4 < 4; ++c4) {
                     uint32_t pk[16];
+                    float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const float2 a = __ffma2_rn(make_float2(sv[c4 * 32 + 2 * i], sv[c4 * 32 + 2 * i + 1]), sl2v, negm);
                         const float p0 = ex2(a.x);
                         const float p1 = ex2(a.y);
                         sum2 = __fadd2_rn(sum2, make_float2(p0, p1));
-                        pk[i] = pack_bf16(p0, p1);
+                        if constexpr (kVScale) {
+                            if (i % 2 == 0 && coded) f = vsc[c4 * 8 + i / 2];
+                            const float2 ps =
+                                __fmul2_rn(make_float2(p0, p1), i % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
+                            pk[i] = pack_bf16(ps.x, ps.y);
+                        } else {
+                            pk[i] = pack_bf16(p0, p1);
+                        }
                     }
                     tmem_st16(s_col + c4 * 16, pk);
                 }
@@ -1944,7 +2016,7 @@ cudaError_t encode_pool_by_block(CUtensorMap* m, const void* ptr, uint64_t bs, u
 
 template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
 cudaError_t launch_d(const KernelParams<kExt>& p, int grid, cudaStream_t st) {
-    constexpr int kSmem = smem_bytes<D>(kExt ? (int)sizeof(OwnUnits) : 0);
+    constexpr int kSmem = smem_bytes<D>((kExt ? (int)sizeof(OwnUnits) : 0) + (kExt && kQuant ? scale_ring_bytes<D>() : 0));
     static_assert(kSmem <= 232448, "shared memory budget");
     static int configured_for[64] = {0};
     int dev = 0;

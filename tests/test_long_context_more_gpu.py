@@ -231,3 +231,28 @@ def test_key_weights_to_fp32(new, lens, d, group, block, int8):
     err = (w.cpu().double() - ref).abs()
     assert (err <= tol).all(), f"off by {(err / tol).max():.2f} of the tolerance"
     ok()
+
+
+# --------------------------------------------------------------------------- precision of the attention over int8 caches
+
+@pytest.mark.parametrize("block", [0, 16])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("call", ["sinks", "prefix"])
+def test_int8_attention_rounds_twice(call, d, block):
+    """P and the output are rounded to bf16, the values of an int8 cache are not.
+
+    Roundings are independent, so their squares add, in 2-norms relative to the output.  r is that of the output
+    alone, taken from the exact one; P's share is that of values spread over a binade, about 0.00153^2, against r^2 of
+    about 0.00165^2: two roundings come to 1.9 r^2, and a third of the values to 2.7 r^2.
+    """
+    new, lens = [40, 1, 3], [700, 1500, 333]
+    c = Call(350, new, lens, d, 2, 4, block, True, prefix=900 if call == "prefix" else 0)
+    kw = dict(window=600, sinks=70) if call == "sinks" else {}
+    c.sinks(600, 70) if call == "sinks" else c.prefix()
+    c.check(**kw)
+    ref, _, _ = R.attention(c.cache, c.q, c.k, c.v, c.new, c.scale, **kw)
+    r = ((ref.to(torch.bfloat16).double() - ref).norm() / ref.norm()).item()
+    err = ((c.out[1].cpu().double() - ref).norm() / ref.norm()).item()
+    assert 0.0013 < r < 0.0019
+    assert err ** 2 <= 2.3 * r ** 2, f"{err:.5f}: {(err / r) ** 2:.2f} of the output's rounding"
+    ok()
