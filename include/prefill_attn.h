@@ -415,6 +415,88 @@ pa_status prefill_attn_evict(
     const pa_options *opts, pa_stream_t stream);
 
 /*
+ * A KV cache in 4 bits.  A row (token, KV head) is cut into groups of 32, 64 or
+ * 128 channels; a group holds a scale s, a minimum m and a code 0 .. 15 per
+ * channel, and channel i stands for m + code_i * s.  Rows lie as in
+ * prefill_attn_varlen, contiguous [num_seqs, n_kv_heads, max_cache_len, .] or,
+ * with pa_options.block_table, as pools [num_blocks, n_kv_heads, block_size, .]:
+ *   k, v                head_dim / 2 bytes a row: byte j holds the codes of
+ *                       channels 2j (low 4 bits) and 2j + 1 (high).
+ *   k_params, v_params  head_dim / group pairs (s, m) of bf16 a row.
+ * All are 16-byte aligned.  A group x of bf16 values is stored as
+ *   m = min x;  s = bf16(fl(max x - m) * fl(1/15)), or 0 when that is < 2^-126;
+ *   code_i = min(15, rint(fl(fl(x_i - m) * r))), r = fl(1/s) (0 when s = 0),
+ * fl: to the nearest fp32; rint: to the nearest integer, ties to even.  max x - m must
+ * be finite in fp32.  d = 128 takes 68 bytes a row at group 128 and 80 at group
+ * 32, where bf16 takes 256 and int8 132.
+ * Zero-initialise it and set struct_size = sizeof(pa_cache4).
+ */
+typedef struct pa_cache4 {
+    uint32_t struct_size;
+    int32_t group;
+    void *k;
+    void *v;
+    void *k_params;
+    void *v_params;
+} pa_cache4;
+
+/*
+ * prefill_attn_varlen_cache4 -- attention over a 4-bit cache.
+ *
+ * prefill_attn_varlen_ex with the cache in 4 bits: every sequence's cached keys
+ * and values are what its codes stand for, the new tokens' are used at full
+ * precision and then quantised into the cache at cache_offsets[b] (after the
+ * rotary embedding, if any).  Of pa_options: window, block_table, rope_theta.
+ * Positions at or past cache_offsets[b] are not read.  What the call writes (out,
+ * lse, the cache) must overlap no other buffer of it.  Under graph capture the
+ * stream must already have run a call of at least these sizes.  num_seqs and
+ * max_cache_len are at most 2^30.
+ */
+pa_status prefill_attn_varlen_cache4(
+    const void *q, const void *k, const void *v,
+    const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+    const pa_cache4 *cache, const int32_t *cache_offsets,
+    void *out, float *lse,
+    int num_seqs, int total_q, int max_cache_len,
+    int n_heads, int n_kv_heads, int head_dim,
+    float scale, int causal, const pa_options *opts, pa_stream_t stream);
+
+/*
+ * prefill_attn_cache4_write -- quantises packed keys and values into a 4-bit cache.
+ *
+ *   k, v           [total, n_kv_heads, head_dim] bf16, sequences head to tail.
+ *   cu_seqlens     [num_seqs + 1] int32: sequence b owns rows cu_seqlens[b] ..
+ *                  cu_seqlens[b + 1] - 1 of k and v.
+ *   cache_offsets  [num_seqs] int32: position of its first one in the cache.
+ * Of pa_options: block_table, rope_theta (k is rotated to its position first, as
+ * in prefill_attn_varlen_ex).  Other rows of the cache are left as they were.  A
+ * sequence whose metadata is inconsistent, or whose tokens' table entries name a
+ * block outside the pool, is skipped (PA_DEVERR_METADATA).  The cache must
+ * overlap no other buffer of the call; num_seqs and max_cache_len are at most
+ * 2^30, total * n_kv_heads below that.
+ */
+pa_status prefill_attn_cache4_write(
+    const void *k, const void *v, const int32_t *cu_seqlens,
+    const pa_cache4 *cache, const int32_t *cache_offsets,
+    int num_seqs, int total, int max_cache_len, int n_kv_heads, int head_dim,
+    const pa_options *opts, pa_stream_t stream);
+
+/*
+ * prefill_attn_cache4_read -- the rows of a 4-bit cache as bf16, packed.
+ *
+ * The inverse of prefill_attn_cache4_write: positions cache_offsets[b] ..
+ * cache_offsets[b] + cu_seqlens[b + 1] - cu_seqlens[b] - 1 of every sequence
+ * into its rows of k and v, each value fl(m + code * s) rounded to bf16 (nearest even).
+ * Rows of skipped sequences are left as they were.  Of pa_options: block_table.
+ * k and v must overlap no other buffer of the call.
+ */
+pa_status prefill_attn_cache4_read(
+    const pa_cache4 *cache, const int32_t *cu_seqlens, const int32_t *cache_offsets,
+    void *k, void *v,
+    int num_seqs, int total, int max_cache_len, int n_kv_heads, int head_dim,
+    const pa_options *opts, pa_stream_t stream);
+
+/*
  * prefill_attn_varlen_noalloc -- prefill_attn_varlen that allocates nothing.
  * The pages have no counterpart to this call; it exists for integration.
  *

@@ -38,6 +38,12 @@ class PaPrefix(ctypes.Structure):
                 ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("block_table", ctypes.c_void_p)]
 
 
+class PaCache4(ctypes.Structure):
+    """pa_cache4 of include/prefill_attn.h."""
+    _fields_ = [("struct_size", ctypes.c_uint32), ("group", ctypes.c_int32), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("k_params", ctypes.c_void_p), ("v_params", ctypes.c_void_p)]
+
+
 # Entry points declared in include/prefill_attn.h: name -> (restype, argtypes)
 _P, _I, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 _VARLEN_ARGS = [_P] * 10 + [_I] * 6 + [_F, _I, _P]
@@ -52,6 +58,11 @@ SIGNATURES = {
                                                               ctypes.POINTER(PaOptions), _P]),
     "prefill_attn_key_weights": (_I, [_P] * 8 + [_I] * 6 + [_F, _I, _I, _I, ctypes.POINTER(PaOptions), _P]),
     "prefill_attn_evict": (_I, [_P] * 7 + [_I] * 7 + [ctypes.POINTER(PaOptions), _P]),
+    "prefill_attn_varlen_cache4": (_I, [_P] * 5 + [ctypes.POINTER(PaCache4)] + [_P] * 3 + [_I] * 6
+                                   + [_F, _I, ctypes.POINTER(PaOptions), _P]),
+    "prefill_attn_cache4_write": (_I, [_P] * 3 + [ctypes.POINTER(PaCache4), _P] + [_I] * 5
+                                  + [ctypes.POINTER(PaOptions), _P]),
+    "prefill_attn_cache4_read": (_I, [ctypes.POINTER(PaCache4)] + [_P] * 4 + [_I] * 5 + [ctypes.POINTER(PaOptions), _P]),
     "prefill_attn_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_int32)]),
     "prefill_attn_release": (None, []),
     "prefill_attn_status_string": (ctypes.c_char_p, [_I]),
@@ -483,6 +494,127 @@ def prefill_attn_evict(cache_k, cache_v, weights, lengths, kept_lengths, kept_in
         cache_k.data_ptr(), cache_v.data_ptr(), weights.data_ptr(), lengths.data_ptr(), kept_lengths.data_ptr(),
         _ptr(kept_index), _ptr(kept_weights), b, cap, hk, d, budget, sink_tokens, recent_tokens,
         _options(cache_k, block_table, cache_k_scale, cache_v_scale), _stream_on(stream, device)))
+
+
+def _cache4(device, b, cache_k, cache_v, cache_k_params, cache_v_params, block_table, hk, d):
+    """Checks a call's 4-bit cache; returns (its pa_cache4, slot capacity)."""
+    if cache_k.dim() != 4 or cache_k_params.dim() != 5:
+        raise ValueError("a 4-bit cache is [num_seqs, kv_heads, cap, head_dim / 2] codes, or [num_blocks, kv_heads, "
+                         "block_size, head_dim / 2], with [..., head_dim / group, 2] parameters")
+    shape = cache_k.shape
+    n, ck_heads, rows, half = shape
+    if ck_heads != hk or 2 * half != d or (block_table is None and n != b):
+        raise ValueError(f"cache_k has shape {tuple(shape)}: {hk} KV heads of {d} / 2 bytes"
+                         + ("" if block_table is not None else f" in {b} slots") + " are wanted")
+    groups = cache_k_params.shape[3]
+    if groups < 1 or d % groups:
+        raise ValueError(f"cache_k_params has shape {tuple(cache_k_params.shape)}: its groups do not divide {d} channels")
+    cap, params = rows, (n, hk, rows, groups, 2)
+    if block_table is not None:
+        if block_table.dim() != 2 or block_table.shape[0] != b:
+            raise ValueError(f"block_table must be [{b}, max_blocks_per_seq]")
+        cap = block_table.shape[1] * rows
+        if not (block_table.dtype is _I32 and block_table.is_contiguous() and block_table.get_device() == device):
+            _check_tensors(device, ("block_table", block_table, _I32, block_table.numel()))
+    if not (cache_k.dtype is _U8 and cache_k.is_contiguous() and cache_k.get_device() == device
+            and cache_v.dtype is _U8 and cache_v.shape == shape and cache_v.is_contiguous() and cache_v.get_device() == device
+            and cache_k_params.dtype is _BF16 and cache_k_params.shape == params and cache_k_params.is_contiguous()
+            and cache_k_params.get_device() == device
+            and cache_v_params.dtype is _BF16 and cache_v_params.shape == params and cache_v_params.is_contiguous()
+            and cache_v_params.get_device() == device):
+        _check_tensors(device, ("cache_k", cache_k, _U8, shape), ("cache_v", cache_v, _U8, shape),
+                       ("cache_k_params", cache_k_params, _BF16, params), ("cache_v_params", cache_v_params, _BF16, params))
+    return PaCache4(_CACHE4_SIZE, d // groups, cache_k.data_ptr(), cache_v.data_ptr(), cache_k_params.data_ptr(),
+                    cache_v_params.data_ptr()), cap
+
+
+_U8, _CACHE4_SIZE = torch.uint8, ctypes.sizeof(PaCache4)
+
+
+def prefill_attn_varlen_cache4(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out, lse=None, *,
+                               cache_k_params, cache_v_params, scale: Optional[float] = None, causal: bool = True,
+                               window: int = 0, block_table=None, rope_theta: float = 0.0, stream=None) -> None:
+    """prefill_attn_varlen_ex over a cache held in 4 bits.
+
+    cache_k/v: uint8 [num_seqs, n_kv_heads, max_cache_len, head_dim // 2], two codes to a byte (even
+    channel low); cache_k_params/cache_v_params: bf16 [num_seqs, n_kv_heads, max_cache_len,
+    head_dim // group, 2], scale and minimum of each group of 32, 64 or 128 channels: a channel
+    stands for minimum + code * scale.  With block_table both are pools [num_blocks, n_kv_heads,
+    block_size, ...].  The new tokens are attended at full precision and then stored in 4 bits.
+    """
+    if not -1 <= window <= _INT:
+        _int32(window=window)
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q/k/v are [total_q, heads, head_dim]")
+    device = _current_device(q)
+    q_shape, k_shape, b = q.shape, k.shape, cache_offsets.numel()
+    (t, h, d), (kt, hk, kd) = q_shape, k_shape
+    if kt != t or kd != d:
+        raise ValueError(f"k has shape {tuple(k_shape)}, q {tuple(q_shape)}")
+    if not (q.dtype is _BF16 and k.dtype is _BF16 and q.is_contiguous() and k.is_contiguous() and k.get_device() == device
+            and v.dtype is _BF16 and v.shape == k_shape and v.is_contiguous() and v.get_device() == device
+            and out.dtype is _BF16 and out.shape == q_shape and out.is_contiguous() and out.get_device() == device
+            and (lse is None or lse.dtype is _F32 and lse.shape == (t, h) and lse.is_contiguous()
+                 and lse.get_device() == device)
+            and cu_seqlens_q.dtype is _I32 and cu_seqlens_q.numel() == b + 1 and cu_seqlens_q.is_contiguous()
+            and cu_seqlens_q.get_device() == device
+            and cu_seqlens_k.dtype is _I32 and cu_seqlens_k.numel() == b + 1 and cu_seqlens_k.is_contiguous()
+            and cu_seqlens_k.get_device() == device
+            and cache_offsets.dtype is _I32 and cache_offsets.is_contiguous() and cache_offsets.get_device() == device):
+        _check_tensors(device, ("q", q, _BF16, q_shape), ("k", k, _BF16, k_shape), ("v", v, _BF16, k_shape),
+                       ("out", out, _BF16, q_shape), ("lse", lse, _F32, (t, h)), ("cu_seqlens_q", cu_seqlens_q, _I32, b + 1),
+                       ("cu_seqlens_k", cu_seqlens_k, _I32, b + 1), ("cache_offsets", cache_offsets, _I32, b))
+    cache, cap = _cache4(device, b, cache_k, cache_v, cache_k_params, cache_v_params, block_table, hk, d)
+    _check((_lib or load()).prefill_attn_varlen_cache4(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cache,
+        cache_offsets.data_ptr(), out.data_ptr(), _ptr(lse), b, t, cap, h, hk, d, d ** -0.5 if scale is None else scale,
+        1 if causal else 0, _options(cache_k, block_table, None, None, window, rope_theta), _stream_on(stream, device)))
+
+
+def _copy4_args(k, v, cu_seqlens, cache_k, cache_v, cache_offsets, cache_k_params, cache_v_params, block_table):
+    """Checks the tensors of a write or read of a 4-bit cache; returns (device, pa_cache4, capacity)."""
+    if k.dim() != 3:
+        raise ValueError("k/v are [total, kv_heads, head_dim]")
+    device = _current_device(k)
+    shape, b = k.shape, cache_offsets.numel()
+    if not (k.dtype is _BF16 and k.is_contiguous() and v.dtype is _BF16 and v.shape == shape and v.is_contiguous()
+            and v.get_device() == device and cu_seqlens.dtype is _I32 and cu_seqlens.numel() == b + 1
+            and cu_seqlens.is_contiguous() and cu_seqlens.get_device() == device and cache_offsets.dtype is _I32
+            and cache_offsets.is_contiguous() and cache_offsets.get_device() == device):
+        _check_tensors(device, ("k", k, _BF16, shape), ("v", v, _BF16, shape), ("cu_seqlens", cu_seqlens, _I32, b + 1),
+                       ("cache_offsets", cache_offsets, _I32, b))
+    return device, *_cache4(device, b, cache_k, cache_v, cache_k_params, cache_v_params, block_table, shape[1], shape[2])
+
+
+def prefill_attn_cache4_write(k, v, cu_seqlens, cache_k, cache_v, cache_offsets, *, cache_k_params, cache_v_params,
+                              block_table=None, rope_theta: float = 0.0, stream=None) -> None:
+    """Quantises packed k/v [total, n_kv_heads, head_dim] (bf16) into a 4-bit cache.
+
+    Sequence b owns rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1 and its first one goes to position
+    cache_offsets[b].  rope_theta > 0 rotates k to its positions first.  Caches as in
+    prefill_attn_varlen_cache4.
+    """
+    device, cache, cap = _copy4_args(k, v, cu_seqlens, cache_k, cache_v, cache_offsets, cache_k_params, cache_v_params,
+                                     block_table)
+    t, hk, d = k.shape
+    _check((_lib or load()).prefill_attn_cache4_write(
+        k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(), cache, cache_offsets.data_ptr(), cache_offsets.numel(), t, cap,
+        hk, d, _options(cache_k, block_table, None, None, 0, rope_theta), _stream_on(stream, device)))
+
+
+def prefill_attn_cache4_read(cache_k, cache_v, cu_seqlens, cache_offsets, k, v, *, cache_k_params, cache_v_params,
+                             block_table=None, stream=None) -> None:
+    """Reads rows of a 4-bit cache into packed k/v [total, n_kv_heads, head_dim] as bf16.
+
+    Positions cache_offsets[b], cache_offsets[b] + 1, ... of sequence b fill rows cu_seqlens[b] ..
+    cu_seqlens[b + 1] - 1: the inverse of prefill_attn_cache4_write.
+    """
+    device, cache, cap = _copy4_args(k, v, cu_seqlens, cache_k, cache_v, cache_offsets, cache_k_params, cache_v_params,
+                                     block_table)
+    t, hk, d = k.shape
+    _check((_lib or load()).prefill_attn_cache4_read(
+        cache, cu_seqlens.data_ptr(), cache_offsets.data_ptr(), k.data_ptr(), v.data_ptr(), cache_offsets.numel(), t, cap,
+        hk, d, _options(cache_k, block_table, None, None), _stream_on(stream, device)))
 
 
 def prefill_attn_varlen_noalloc(q, k, v, cu_seqlens_q, cu_seqlens_k, cache_k, cache_v, cache_offsets, out,

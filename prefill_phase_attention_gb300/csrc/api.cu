@@ -63,6 +63,7 @@ struct Workspace {
     size_t rope_bytes = 0;
     void* aux = nullptr;   // lists and partial results of the long-context calls (grown on demand)
     size_t aux_bytes = 0;
+    int* arrivals = nullptr;  // kArrivals counters of the 4-bit cache's row kernel, zero between calls
     bool captured = false;  // a captured graph holds these addresses: outgrown blocks are kept, not freed
     std::vector<void*> old_headers;  // headers of outgrown blocks that a graph may still write errors to
     std::vector<void*> retired;      // outgrown blocks that a captured graph holds
@@ -218,6 +219,29 @@ pa_status get_aux_scratch(Workspace* w, cudaStream_t st, size_t bytes, void** ou
         w->aux_bytes = bytes;
     }
     *out = w->aux;
+    return PA_OK;
+}
+
+// The counters by which CTAs that share a row block find the last of them (one per CTA).
+constexpr int kArrivals = 1024;
+
+pa_status get_arrivals(Workspace* w, cudaStream_t st, int** out) {
+    if (!w->arrivals) {
+        if (capturing(st))
+            return fail(PA_ERR_UNSUPPORTED,
+                        "graph capture: the stream has no counters yet; run a prefill_attn_varlen_cache4 call on this "
+                        "stream before capturing");
+        void* ptr = nullptr;
+        cudaError_t e = cudaMallocAsync(&ptr, kArrivals * sizeof(int), st);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaMallocAsync(counters)");
+        e = cudaMemsetAsync(ptr, 0, kArrivals * sizeof(int), st);
+        if (e != cudaSuccess) {
+            cudaFreeAsync(ptr, st);
+            return cuda_fail(e, "clearing the counters");
+        }
+        w->arrivals = static_cast<int*>(ptr);
+    }
+    *out = w->arrivals;
     return PA_OK;
 }
 
@@ -679,7 +703,7 @@ void prefill_attn_release(void) try {
     for (auto& kv : g_ws) {
         Workspace& w = kv.second;
         cudaSetDevice(kv.first.first);
-        for (void* ptr : {w.ptr, w.rope, w.aux})
+        for (void* ptr : {w.ptr, w.rope, w.aux, static_cast<void*>(w.arrivals)})
             if (ptr) cudaFree(ptr);
         for (void* ptr : w.retired) cudaFree(ptr);
     }
@@ -1349,6 +1373,265 @@ pa_status prefill_attn_evict(void* cache_k, void* cache_v, const float* weights,
     int launches = 0;
     e = pa::launch_evict(a, sms, &launches, stream);
     if (e != cudaSuccess) return cuda_fail(e, "eviction launch");
+    g_last_launches = launches;
+    return PA_OK;
+} catch (...) {
+    return caught();
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The 4-bit cache: attention over it, writing it, reading it back.
+// ---------------------------------------------------------------------------
+namespace {
+
+// The options that a 4-bit cache's calls share (kv_quant is the int8 cache's).
+pa_status read_options4(const pa_options* opts, int causal, const char* what, Options* o) {
+    pa_status s = read_options(opts, causal, o);
+    if (s != PA_OK) return s;
+    s = check_unused(*o, what);
+    if (s != PA_OK) return s;
+    if (o->kv_quant) return fail(PA_ERR_INVALID_ARG, "%s takes no kv_quant: the cache's parameters are in pa_cache4", what);
+    return PA_OK;
+}
+
+// Checks a 4-bit cache against the call's sizes and describes it to the kernels.
+pa_status read_cache4(const pa_cache4* cache, const Options& o, int head_dim, int n_kv_heads, int max_cache_len,
+                      bool pointers, pa::Cache4* out) {
+    if (!cache) return fail(PA_ERR_INVALID_ARG, "cache is NULL");
+    if (cache->struct_size < sizeof(pa_cache4))
+        return fail(PA_ERR_INVALID_ARG, "pa_cache4.struct_size %u is too small", (unsigned)cache->struct_size);
+    if ((cache->group != 32 && cache->group != 64 && cache->group != 128) || cache->group > head_dim)
+        return fail(PA_ERR_INVALID_ARG, "pa_cache4.group must be 32, 64 or 128 and at most head_dim (got %d)", cache->group);
+    if (pointers) {
+        const void* ptrs[] = {cache->k, cache->v, cache->k_params, cache->v_params};
+        const char* names[] = {"k", "v", "k_params", "v_params"};
+        for (int i = 0; i < 4; ++i) {
+            if (!ptrs[i]) return fail(PA_ERR_INVALID_ARG, "pa_cache4.%s is NULL", names[i]);
+            if (!aligned16(ptrs[i])) return fail(PA_ERR_INVALID_ARG, "pa_cache4.%s must be 16-byte aligned", names[i]);
+        }
+    }
+    out->k = static_cast<uint8_t*>(cache->k);
+    out->v = static_cast<uint8_t*>(cache->v);
+    out->kp = static_cast<uint32_t*>(cache->k_params);
+    out->vp = static_cast<uint32_t*>(cache->v_params);
+    out->groups = head_dim / cache->group;
+    out->n_kv_heads = n_kv_heads;
+    out->max_cache_len = max_cache_len;
+    out->block_table = o.block_table;
+    out->block_log2 = log2_of(o.block_size);
+    out->max_blocks = o.max_blocks;
+    out->num_blocks = o.num_blocks;
+    return PA_OK;
+}
+
+constexpr int kCacheSpans = 4;
+void cache_spans(const pa::Cache4& c, const Options& o, int num_seqs, int head_dim, bool written, Span* out) {
+    const size_t rows = cache_rows(o, num_seqs, c.max_cache_len, c.n_kv_heads);
+    out[0] = {"the cache's k", c.k, rows * (head_dim / 2), written};
+    out[1] = {"the cache's v", c.v, rows * (head_dim / 2), written};
+    out[2] = {"the cache's k_params", c.kp, rows * c.groups * 4, written};
+    out[3] = {"the cache's v_params", c.vp, rows * c.groups * 4, written};
+}
+
+// Writes packed tokens into the cache (k, v read), or reads them out of it (k, v written).
+pa_status copy_cache4(const void* k, const void* v, const int32_t* cu_seqlens, const pa_cache4* cache,
+                      const int32_t* cache_offsets, int num_seqs, int total, int max_cache_len, int n_kv_heads,
+                      int head_dim, const pa_options* opts, bool write, pa_stream_t stream_) {
+    g_last_error[0] = 0;
+    g_last_launches = 0;
+    g_last_schedule = 0;
+    Options o;
+    pa_status s = read_options4(opts, 1, write ? "prefill_attn_cache4_write" : "prefill_attn_cache4_read", &o);
+    if (s != PA_OK) return s;
+    if (o.window) return fail(PA_ERR_INVALID_ARG, "prefill_attn_cache4_write and _read take no window");
+    if (o.rope_theta > 0.f && !write) return fail(PA_ERR_INVALID_ARG, "prefill_attn_cache4_read takes no rope_theta");
+    if (num_seqs < 0) return fail(PA_ERR_INVALID_ARG, "num_seqs must be >= 0 (got %d)", num_seqs);
+    if (total < 0) return fail(PA_ERR_INVALID_ARG, "total must be >= 0 (got %d)", total);
+    if (max_cache_len < 1) return fail(PA_ERR_INVALID_ARG, "max_cache_len must be >= 1 (got %d)", max_cache_len);
+    if (n_kv_heads < 1) return fail(PA_ERR_INVALID_ARG, "n_kv_heads must be >= 1 (got %d)", n_kv_heads);
+    if (head_dim != 32 && head_dim != 64 && head_dim != 128)
+        return fail(PA_ERR_UNSUPPORTED, "head_dim must be 32, 64 or 128 (got %d)", head_dim);
+    s = check_paged(o, max_cache_len, n_kv_heads);
+    if (s != PA_OK) return s;
+    s = check_capacity(num_seqs, max_cache_len, 0);
+    if (s != PA_OK) return s;
+    const bool empty = num_seqs == 0 || total == 0;
+    pa::Copy4Params p;
+    s = read_cache4(cache, o, head_dim, n_kv_heads, max_cache_len, !empty, &p.cache);
+    if (s != PA_OK) return s;
+    if ((long long)total * n_kv_heads >= (1LL << 30))
+        return fail(PA_ERR_UNSUPPORTED, "total * n_kv_heads must be < 2^30");
+    if (!o.block_table && (long long)num_seqs * n_kv_heads * max_cache_len >= (1LL << 31))
+        return fail(PA_ERR_UNSUPPORTED, "num_seqs * n_kv_heads * max_cache_len must be < 2^31");
+    if (empty) return PA_OK;
+    const void* ptrs[] = {k, v, cu_seqlens, cache_offsets};
+    const char* names[] = {"k", "v", "cu_seqlens", "cache_offsets"};
+    for (int i = 0; i < 4; ++i) {
+        if (!ptrs[i]) return fail(PA_ERR_INVALID_ARG, "%s is NULL", names[i]);
+        if (i < 2 ? !aligned16(ptrs[i]) : (reinterpret_cast<uintptr_t>(ptrs[i]) & 3u) != 0)
+            return fail(PA_ERR_INVALID_ARG, "%s must be %d-byte aligned", names[i], i < 2 ? 16 : 4);
+    }
+    const size_t bytes = (size_t)total * n_kv_heads * head_dim * 2;
+    Span spans[kCacheSpans + 5] = {{"k", k, bytes, !write},
+                                   {"v", v, bytes, !write},
+                                   {"cu_seqlens", cu_seqlens, ((size_t)num_seqs + 1) * 4, false},
+                                   {"cache_offsets", cache_offsets, (size_t)num_seqs * 4, false},
+                                   {"block_table", o.block_table, (size_t)num_seqs * o.max_blocks * 4, false}};
+    cache_spans(p.cache, o, num_seqs, head_dim, write, spans + 5);
+    s = check_disjoint(spans, kCacheSpans + 5);
+    if (s != PA_OK) return s;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    const bool check = o.block_table || o.rope_theta > 0.f;  // by a kernel of its own
+    const StreamLock lock(dev, stream);
+    Workspace* const ws = lock.ws;
+    s = grow_workspace(*ws, stream, check ? num_seqs : 0, 0);
+    if (s != PA_OK) return s;
+    p.seqs = pa::Sequences4{cu_seqlens, nullptr, cache_offsets, num_seqs, total, check ? ws_seqs(*ws) : nullptr,
+                            static_cast<pa::WorkspaceHeader*>(ws->ptr)};
+    int launches = 1;
+    if (check) {
+        e = pa::launch_check_sequences4(p.seqs, p.cache, false, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "sequence check launch");
+        ++launches;
+    }
+    if (o.rope_theta > 0.f) {
+        void* rope = nullptr;
+        s = get_rope_scratch(ws, stream, bytes, &rope);
+        if (s != PA_OK) return s;
+        const void* no_q = nullptr;
+        e = rotate(no_q, k, cu_seqlens, p.seqs.checked, rope, total, num_seqs, 0, n_kv_heads, head_dim, o.rope_theta, 0,
+                   stream);
+        if (e != cudaSuccess) return cuda_fail(e, "rotary prologue launch");
+        ++launches;
+    }
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.k_out = write ? nullptr : static_cast<__nv_bfloat16*>(const_cast<void*>(k));
+    p.v_out = write ? nullptr : static_cast<__nv_bfloat16*>(const_cast<void*>(v));
+    e = write ? pa::launch_write_cache4(p, head_dim, stream) : pa::launch_read_cache4(p, head_dim, stream);
+    if (e != cudaSuccess) return cuda_fail(e, write ? "cache write launch" : "cache read launch");
+    g_last_launches = launches;
+    return PA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status prefill_attn_cache4_write(const void* k, const void* v, const int32_t* cu_seqlens, const pa_cache4* cache,
+                                    const int32_t* cache_offsets, int num_seqs, int total, int max_cache_len,
+                                    int n_kv_heads, int head_dim, const pa_options* opts, pa_stream_t stream) try {
+    return copy_cache4(k, v, cu_seqlens, cache, cache_offsets, num_seqs, total, max_cache_len, n_kv_heads, head_dim,
+                       opts, true, stream);
+} catch (...) {
+    return caught();
+}
+
+pa_status prefill_attn_cache4_read(const pa_cache4* cache, const int32_t* cu_seqlens, const int32_t* cache_offsets,
+                                   void* k, void* v, int num_seqs, int total, int max_cache_len, int n_kv_heads,
+                                   int head_dim, const pa_options* opts, pa_stream_t stream) try {
+    return copy_cache4(k, v, cu_seqlens, cache, cache_offsets, num_seqs, total, max_cache_len, n_kv_heads, head_dim,
+                       opts, false, stream);
+} catch (...) {
+    return caught();
+}
+
+pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v, const int32_t* cu_seqlens_q,
+                                     const int32_t* cu_seqlens_k, const pa_cache4* cache, const int32_t* cache_offsets,
+                                     void* out, float* lse, int num_seqs, int total_q, int max_cache_len, int n_heads,
+                                     int n_kv_heads, int head_dim, float scale, int causal, const pa_options* opts,
+                                     pa_stream_t stream_) try {
+    g_last_error[0] = 0;
+    g_last_launches = 0;
+    g_last_schedule = 0;
+    Options o;
+    pa_status s = read_options4(opts, causal, "prefill_attn_varlen_cache4", &o);
+    if (s != PA_OK) return s;
+    const bool empty = num_seqs == 0 || total_q == 0;
+    // stand-ins that satisfy the shared checks until the cache itself is checked
+    s = check_args(q, k, v, cu_seqlens_q, cu_seqlens_k, reinterpret_cast<const void*>(uintptr_t(16)),
+                   reinterpret_cast<const void*>(uintptr_t(32)), cache_offsets, out, lse, num_seqs, total_q,
+                   max_cache_len, n_heads, n_kv_heads, head_dim, scale, causal, o.block_table != nullptr);
+    if (s != PA_OK) return s;
+    s = check_paged(o, max_cache_len, n_kv_heads);
+    if (s != PA_OK) return s;
+    s = check_capacity(num_seqs, max_cache_len, 0);
+    if (s != PA_OK) return s;
+    pa::Cache4 c;
+    s = read_cache4(cache, o, head_dim, n_kv_heads, max_cache_len, !empty, &c);
+    if (s != PA_OK) return s;
+    if (empty) return PA_OK;
+    const size_t q_rows = (size_t)total_q * n_heads, k_rows = (size_t)total_q * n_kv_heads;
+    Span spans[kCacheSpans + 9] = {{"out", out, q_rows * head_dim * 2, true},
+                                   {"lse", lse, q_rows * 4, true},
+                                   {"q", q, q_rows * head_dim * 2, false},
+                                   {"k", k, k_rows * head_dim * 2, false},
+                                   {"v", v, k_rows * head_dim * 2, false},
+                                   {"cu_seqlens_q", cu_seqlens_q, ((size_t)num_seqs + 1) * 4, false},
+                                   {"cu_seqlens_k", cu_seqlens_k, ((size_t)num_seqs + 1) * 4, false},
+                                   {"cache_offsets", cache_offsets, (size_t)num_seqs * 4, false},
+                                   {"block_table", o.block_table, (size_t)num_seqs * o.max_blocks * 4, false}};
+    cache_spans(c, o, num_seqs, head_dim, true, spans + 9);
+    s = check_disjoint(spans, kCacheSpans + 9);
+    if (s != PA_OK) return s;
+    o.window = clamp_span(o.window, max_cache_len);
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    const int sms = sm_count(dev, &s);
+    if (s != PA_OK) return s;
+    const int grid = std::min(sms, kArrivals);
+    const int group = n_heads / n_kv_heads;
+    // row blocks of 16 where a sequence has more than 8 rows on average
+    const int row_tiles = (long long)total_q * group > 8LL * num_seqs ? 2 : 1;
+    const bool check = o.block_table || o.rope_theta > 0.f;
+    const StreamLock lock(dev, stream);
+    Workspace* const ws = lock.ws;
+    s = grow_workspace(*ws, stream, check ? num_seqs : 0, 0);
+    if (s != PA_OK) return s;
+    pa::Rows4Params p;
+    s = get_arrivals(ws, stream, &p.arrivals);
+    if (s != PA_OK) return s;
+    void* part = nullptr;
+    s = get_aux_scratch(ws, stream, (size_t)grid * 2 * 8 * row_tiles * (head_dim + 2) * sizeof(float), &part);
+    if (s != PA_OK) return s;
+    p.seqs = pa::Sequences4{cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q,
+                            check ? ws_seqs(*ws) : nullptr, static_cast<pa::WorkspaceHeader*>(ws->ptr)};
+    int launches = 1;
+    if (check) {
+        e = pa::launch_check_sequences4(p.seqs, c, true, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "sequence check launch");
+        ++launches;
+    }
+    if (o.rope_theta > 0.f) {
+        void* rope = nullptr;
+        s = get_rope_scratch(ws, stream, (q_rows + k_rows) * head_dim * 2, &rope);
+        if (s != PA_OK) return s;
+        e = rotate(q, k, cu_seqlens_q, p.seqs.checked, rope, total_q, num_seqs, n_heads, n_kv_heads, head_dim,
+                   o.rope_theta, 0, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "rotary prologue launch");
+        ++launches;
+    }
+    p.cache = c;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k);
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.n_heads = n_heads;
+    p.group = group;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.causal = causal;
+    p.window = o.window;
+    p.part = static_cast<float*>(part);
+    e = pa::launch_attn_rows4(p, head_dim, row_tiles, grid, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "attention launch");
     g_last_launches = launches;
     return PA_OK;
 } catch (...) {

@@ -1,0 +1,871 @@
+// attn_rows4.cuh -- attention of few query rows per sequence over the 4-bit cache:
+// decode rows, drafts, short chunks.
+//
+// A row block is 8 or 16 query rows (token, head of a KV head's group) of a sequence.
+// Its keys come in tiles: 32 cached rows, or 8 new tokens (bf16; as many bytes), which
+// follow them.  With a group's parameters (s, m) and codes c the score and output are
+//     q . k_j   = sum_g s_jg (q_g . (c_jg - 8)) + (m_jg + 8 s_jg) sum(q_g)
+//     sum_j p_j v_j = sum_j (p_j s_jg) (c_jg - 8) + sum_j p_j (m_jg + 8 s_jg)
+// so the products of codes run on the tensor cores with exact operands (c - 8 and q are
+// bf16 values), the parameters multiply in fp32, and the one rounding is that of p s to
+// bf16 for the second product.
+//
+// What bounds it is HBM: 68 bytes of key or value (d = 128, one group) feed 8 rows, where
+// 128-row MMA tiles would be 15/16 empty and want the codes expanded through shared
+// memory, twice its bandwidth at this rate (80 bytes written and 80 read per clock and SM
+// for 128).  So a warp keeps everything in registers: S^T = K Q^T and O^T = V^T P^T with
+// keys (channels) as the rows of mma.m16n8k16, 8 queries as its columns.  ldmatrix hands
+// out 4 codes as one 16-bit element: plain for K (a lane gets 8 channels of one key),
+// transposed for V (4 channels of two keys), and (x >> 4 i) & 0x000f000f is then an
+// operand's pair of codes; the channels' order inside an MMA is free, Q is laid out to
+// match.  P^T becomes an operand by movmatrix.
+//
+// All tiles of a call form one list (sequence, KV head, row block, tile); a CTA takes an
+// equal share of it, a warp an equal share of that, in a cp.async ring of its own that
+// runs on across row blocks: no barrier and no wait between warps until the end.  A row
+// block cut by a share's end leaves (maximum, sum, unnormalised output); the CTA joins
+// those of its warps, and the CTA that comes last joins those of the CTAs, in list order
+// whoever it is.
+#pragma once
+
+#include <cstdint>
+
+#include "cache4.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace pa {
+
+namespace rows4 {
+
+constexpr int kWarps = kRows4Warps;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTileKeys = 32;  // cached rows of a tile
+constexpr int kNewKeys = 8;    // new tokens of a tile
+
+template <int D, int NG, int NQ>
+struct Cfg {
+    static constexpr int kChunks = D / 32;
+    static constexpr int kRowBytes = D / 2;
+    static constexpr int kCodes = kTileKeys * kRowBytes;     // bytes of a tile's codes
+    static constexpr int kParams = kTileKeys * NG * 4;       // bytes of a tile's parameters
+    static constexpr int kTileBytes = 2 * (kCodes + kParams);
+    static constexpr int kStages = NQ == 2 && D == 128 ? 3 : 4;
+    static constexpr int kRows = 8 * NQ;
+    static constexpr int kRecord = kRows * D * 4;  // bytes of a partial output
+    static_assert(kStages * kTileBytes >= kRecord, "a warp's second record lies in its ring");
+};
+
+// What a warp needs to know of a tile in its ring.
+struct Tile {
+    int key;  // first position of a cached tile (row of the cache); new tokens: -1 - index of the first
+    int b, kvh, block;
+    SeqInfo s;
+    int flags;
+    int start_hi, start_lo;  // list position of the row block's first tile
+    int tiles;               // its tiles
+};
+enum : int {
+    kFirst = 1,      // of the row block, in this warp
+    kLast = 2,       // of the row block, in this warp
+    kFromBefore = 4, // the row block began before this warp's share
+    kGoesOn = 8,     // and ends after it
+};
+
+struct Record {
+    Tile t;
+    int valid;
+};
+
+// Tiles of the list that a sequence's row blocks have.
+struct Extent {
+    int first_tile;  // first cached tile that some query sees
+    int cached, fresh;
+    int blocks;  // row blocks
+    __device__ __forceinline__ int tiles() const { return cached + fresh; }
+};
+
+template <int NQ>
+__device__ __forceinline__ Extent extent(const Rows4Params& p, const SeqInfo& s) {
+    Extent e{0, 0, 0, 0};
+    if (s.n == 0) return e;
+    const int lo = p.causal && p.window > 0 ? max(0, s.P - p.window + 1) : 0;  // oldest key of the first token
+    e.first_tile = lo / kTileKeys;
+    e.cached = max(0, (s.P + kTileKeys - 1) / kTileKeys - e.first_tile);
+    e.fresh = (s.n + kNewKeys - 1) / kNewKeys;
+    e.blocks = (int)(((unsigned)s.n * (unsigned)p.group + 8 * NQ - 1) / (8 * NQ));  // n * group < 2^31
+    return e;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool read) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(read ? kBytes : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// 8x8 transpose of 16-bit elements held as a matrix fragment
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float log2_approx(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Codes i and i + 4 of a word (of each 16-bit half, code i), less 8, as a pair of bf16:
+// the code as the low mantissa bits of 128, less 136, both exact.
+template <int i>
+__device__ __forceinline__ uint32_t codes(uint32_t x) {
+    uint32_t y = ((x >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    const uint32_t c = 0x43084308u;  // 136, 136
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&c));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int D>
+__device__ __forceinline__ int swizzle(int key) {  // of a row's 16-byte parts
+    return D == 128 ? (key >> 1) & 3 : D == 64 ? (key >> 2) & 1 : 0;
+}
+
+// Partial result of a row block: rows [8 NQ] x (maximum, sum) and the unnormalised output.
+template <int D, int NQ>
+__device__ __forceinline__ void store_row(const Rows4Params& p, const Tile& t, int row, int d, float4 o) {
+    const int r = t.block * 8 * NQ + row;
+    if (r >= t.s.n * p.group) return;
+    const size_t at = ((size_t)(t.s.q_start + r / p.group) * p.n_heads + t.kvh * p.group + r % p.group) * D + d;
+    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
+}
+template <int NQ>
+__device__ __forceinline__ void store_lse(const Rows4Params& p, const Tile& t, int row, float m, float l) {
+    const int r = t.block * 8 * NQ + row;
+    if (!p.lse || r >= t.s.n * p.group) return;
+    p.lse[(size_t)(t.s.q_start + r / p.group) * p.n_heads + t.kvh * p.group + r % p.group] =
+        (m + log2_approx(l)) * 0.69314718055994530942f;
+}
+
+// Walks the tile list from a sequence on, and starts the copies of one tile at a time.
+template <int D, int NG, int NQ>
+struct Feeder {
+    using C = Cfg<D, NG, NQ>;
+    const Rows4Params& p;
+    const SeqInfo* table;  // in shared memory, or nullptr
+    uint32_t ring;
+    Tile* tiles;
+    int lane;
+    int b, item, j;  // sequence, row block of it (KV head major), tile of that
+    SeqInfo s;
+    Extent e;
+    long long at, end, block_start;  // list positions
+    int ids, next_ids;               // paged: blocks of the 8-row pieces of this and the next 256 positions
+
+    __device__ __forceinline__ SeqInfo seq(int i) const {
+        return table ? table[i] : sequence4(p.seqs, p.cache.max_cache_len, i);
+    }
+    // Puts the feeder at list position `first`; `start` is that of sequence b0.
+    __device__ __forceinline__ void seek(int b0, long long start, long long first, long long last) {
+        at = first;
+        end = last;
+        if (at >= end) return;
+        b = b0;
+        s = seq(b);
+        e = extent<NQ>(p, s);
+        for (;;) {
+            const long long all = (long long)e.tiles() * e.blocks * p.cache.n_kv_heads;
+            if (first < start + all) break;
+            start += all;
+            ++b;  // the list's total says that there is one
+            s = seq(b);
+            e = extent<NQ>(p, s);
+        }
+        const long long in = first - start;
+        item = (int)(in / e.tiles());
+        j = (int)(in % e.tiles());
+        block_start = first - j;
+        if (p.cache.block_table) load_ids(true);
+    }
+    __device__ __forceinline__ int id_of(int window) const {
+        const int pos = window * 256 + lane * 8;
+        if (pos >= s.P) return -1;
+        return __ldg(p.cache.block_table + (size_t)b * p.cache.max_blocks + (pos >> p.cache.block_log2));
+    }
+    __device__ __forceinline__ void load_ids(bool fresh) {
+        const int key = (e.first_tile + j) * kTileKeys, window = key >> 8;
+        if (fresh) {
+            ids = id_of(window);
+            next_ids = id_of(window + 1);
+        } else if ((key & 255) == 0) {
+            ids = next_ids;
+            next_ids = id_of(window + 1);
+        }
+    }
+    __device__ __forceinline__ void issue(int stage) {
+        if (at < end) {
+            const uint32_t dst = ring + stage * C::kTileBytes;
+            const int kvh = item / e.blocks, block = item % e.blocks;
+            const bool cached = j < e.cached;
+            if (lane == 0) {
+                Tile t;
+                t.key = cached ? (e.first_tile + j) * kTileKeys : -1 - (j - e.cached) * kNewKeys;
+                t.b = b;
+                t.kvh = kvh;
+                t.block = block;
+                t.s = s;
+                t.flags = 0;
+                t.start_hi = (int)(block_start >> 32);
+                t.start_lo = (int)block_start;
+                t.tiles = e.tiles();
+                tiles[stage] = t;
+            }
+            if (cached) {
+                const int key0 = (e.first_tile + j) * kTileKeys;
+                const size_t row0 = p.cache.block_table ? 0
+                                                        : ((size_t)b * p.cache.n_kv_heads + kvh) * p.cache.max_cache_len + key0;
+                const int bmask = (1 << p.cache.block_log2) - 1, piece0 = (key0 & 255) >> 3;
+                // row of the tile's key (0: none, `read` false)
+                auto row_of = [&](int key, bool& read) -> size_t {
+                    read = key0 + key < s.P;
+                    if (!p.cache.block_table) return read ? row0 + key : 0;
+                    const int id = __shfl_sync(0xffffffffu, ids, (piece0 + (key >> 3)) & 31);
+                    read = read && (unsigned)id < (unsigned)p.cache.num_blocks;
+                    return read ? (((size_t)id * p.cache.n_kv_heads + kvh) << p.cache.block_log2) + ((key0 + key) & bmask) : 0;
+                };
+                constexpr int kParts = C::kRowBytes / 16;
+#pragma unroll
+                for (int it = 0; it < kParts; ++it) {
+                    const int key = it * (32 / kParts) + lane / kParts, part = lane % kParts;
+                    bool read;
+                    const size_t row = row_of(key, read);
+                    const uint32_t to = dst + key * C::kRowBytes + (part ^ swizzle<D>(key)) * 16;
+                    const size_t from = row * C::kRowBytes + part * 16;
+                    cp_async16(to, p.cache.k + from, read);
+                    cp_async16(to + C::kCodes, p.cache.v + from, read);
+                }
+                bool read;
+                const size_t row = row_of(lane, read);
+                const uint32_t to = dst + 2 * C::kCodes + lane * NG * 4;
+                if constexpr (NG == 4) {
+                    cp_async16(to, p.cache.kp + row * NG, read);
+                    cp_async16(to + C::kParams, p.cache.vp + row * NG, read);
+                } else {
+                    cp_async_small<NG * 4>(to, p.cache.kp + row * NG, read);
+                    cp_async_small<NG * 4>(to + C::kParams, p.cache.vp + row * NG, read);
+                }
+            } else {
+                const int tok0 = (j - e.cached) * kNewKeys;
+                constexpr int kParts = D / 8;  // 16-byte parts of a bf16 row
+#pragma unroll
+                for (int it = 0; it < kParts * kNewKeys / 32; ++it) {
+                    const int at_ = it * 32 + lane, key = at_ / kParts, part = at_ % kParts;
+                    const bool read = tok0 + key < s.n;
+                    const size_t from = ((size_t)(s.q_start + (read ? tok0 + key : 0)) * p.cache.n_kv_heads + kvh) * D + part * 8;
+                    cp_async16(dst + at_ * 16, p.k + from, read);
+                    cp_async16(dst + C::kCodes + at_ * 16, p.v + from, read);
+                }
+            }
+            // onwards
+            ++at;
+            const bool block_ends = j + 1 == e.tiles();
+            if (lane == 0) {
+                int f = 0;
+                if (at - 1 == block_start || first_of_share) f |= kFirst;
+                if (first_of_share && at - 1 != block_start) started_before = true;
+                if (started_before) f |= kFromBefore;
+                if (block_ends || at == end) f |= kLast;
+                if (!block_ends && at == end) f |= kGoesOn;
+                tiles[stage].flags = f;
+                if (block_ends) started_before = false;
+            }
+            first_of_share = false;
+            if (!block_ends) {
+                ++j;
+                if (p.cache.block_table) load_ids(false);
+            } else if (at < end) {
+                j = 0;
+                block_start = at;
+                if (++item == e.blocks * p.cache.n_kv_heads) {
+                    item = 0;
+                    do {
+                        ++b;
+                        s = seq(b);
+                        e = extent<NQ>(p, s);
+                    } while (e.blocks == 0);
+                }
+                if (p.cache.block_table) load_ids(true);
+            }
+        }
+        cp_async_commit();
+    }
+    bool first_of_share = true, started_before = false;
+};
+
+template <int D, int NG, int NQ>
+__global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Params p) {
+    using C = Cfg<D, NG, NQ>;
+    constexpr int kGroupChunks = C::kChunks / NG;  // 32-channel chunks of a group
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ SeqInfo table[kRows4Seqs];
+    __shared__ Tile tile_info[kWarps][C::kStages];
+    __shared__ Record records[kWarps][2];
+    __shared__ float2 stats[kWarps][2][C::kRows];  // (maximum, sum) of a record's rows
+    __shared__ long long warp_sums[kWarps];
+    __shared__ long long start_of_first;
+    __shared__ int first_seq, arrived;
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
+    griddep_wait();
+
+    // ---- the list: its length, and the sequence that this CTA's share begins in
+    const bool in_table = p.seqs.num_seqs <= kRows4Seqs;
+    auto tiles_of = [&](int b) -> long long {
+        if (b >= p.seqs.num_seqs) return 0;
+        const SeqInfo s = sequence4(p.seqs, p.cache.max_cache_len, b);
+        if (in_table) table[b] = s;
+        const Extent e = extent<NQ>(p, s);
+        return (long long)e.tiles() * e.blocks * p.cache.n_kv_heads;
+    };
+    // exclusive prefix sum over the CTA; total: the sum
+    auto scan = [&](long long x, long long& total) -> long long {
+        long long inc = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        if (lane == 31) warp_sums[warp] = inc;
+        __syncthreads();
+        long long before = 0;
+        total = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += warp_sums[w];
+            total += warp_sums[w];
+        }
+        __syncthreads();
+        return before + inc - x;
+    };
+    long long all = 0, mine = 0, excl = 0;
+    for (int b0 = 0; b0 < p.seqs.num_seqs; b0 += kThreads) {
+        long long total;
+        mine = tiles_of(b0 + tid);
+        excl = all + scan(mine, total);
+        all += total;
+    }
+    if (!p.seqs.checked && blockIdx.x == 0)
+        for (int b = tid; b < p.seqs.num_seqs; b += kThreads)
+            if (stated_sequence(p.seqs, p.cache.max_cache_len, b).n < 0) atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
+    // shares of at least a tile per warp
+    const long long share = max((long long)kWarps, (all + gridDim.x - 1) / gridDim.x);
+    const long long from = min(all, share * blockIdx.x), to = min(all, from + share);
+    if (from >= to) return;  // (the whole CTA)
+    if (in_table) {
+        if (mine > 0 && excl <= from && from < excl + mine) first_seq = tid, start_of_first = excl;
+    } else {
+        long long before = 0;
+        for (int b0 = 0; b0 < p.seqs.num_seqs && before <= from; b0 += kThreads) {
+            long long total;
+            const long long x = tiles_of(b0 + tid), ex = before + scan(x, total);
+            if (x > 0 && ex <= from && from < ex + x) first_seq = b0 + tid, start_of_first = ex;
+            before += total;
+        }
+    }
+    if (tid < 2 * kWarps) records[tid / 2][tid % 2].valid = 0;
+    __syncthreads();
+
+    // ---- this warp's share
+    uint8_t* const ring = smem + warp * C::kStages * C::kTileBytes;
+    float* const kept = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kTileBytes + warp * C::kRecord);
+    const long long len = to - from;
+    Feeder<D, NG, NQ> feed{p, in_table ? table : nullptr, ptx::smem_u32(ring), tile_info[warp], lane};
+    const long long wfrom = from + len * warp / kWarps, wto = from + len * (warp + 1) / kWarps;
+    feed.seek(first_seq, start_of_first, wfrom, wto);
+    const int steps = (int)min(wto - wfrom, (long long)INT_MAX);
+#pragma unroll
+    for (int i = 0; i < C::kStages - 1; ++i) feed.issue(i);
+
+    uint32_t qf[NQ][C::kChunks][4];  // Q as the second operand: per chunk two 16-channel steps
+    float qsum[NQ][NG][2];           // sums of a group's channels of queries 2 t4, 2 t4 + 1
+    float o[NQ][C::kChunks][2][4];   // O^T: channels 32 c + 4 g + 2 e (+ 1), queries 2 t4, 2 t4 + 1
+    float om[NQ][NG][2];             // sum of p (m + 8 s) over this lane's keys
+    float m[NQ][2], l[NQ][2];        // running maximum (log2 units), sum over this lane's keys
+    int hi[NQ][2], lo[NQ][2];        // keys [lo, hi] are visible
+    int lo_most = 0;                 // largest lo
+
+    int stage = 0;
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+        cp_async_wait<C::kStages - 2>();
+        __syncwarp();
+        feed.issue(stage == 0 ? C::kStages - 1 : stage - 1);
+        const Tile& t = tile_info[warp][stage];
+        const int flags = t.flags, key = t.key;
+        const SeqInfo s = t.s;
+        const uint8_t* const tile = ring + stage * C::kTileBytes;
+        const uint32_t tile_u32 = ptx::smem_u32(tile);
+
+        if (flags & kFirst) {
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                const int r = t.block * C::kRows + 8 * n + g;
+                const bool there = r < s.n * p.group;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    p.q + ((size_t)(s.q_start + (there ? r / p.group : 0)) * p.n_heads + t.kvh * p.group + (there ? r % p.group : 0)) * D);
+                float sum[NG];
+#pragma unroll
+                for (int a = 0; a < NG; ++a) sum[a] = 0.f;
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c) {
+                    uint4 x = __ldg(src + 4 * c + t4);  // channels 32 c + 8 t4 ...
+                    if (!there) x = make_uint4(0, 0, 0, 0);
+                    qf[n][c][0] = __byte_perm(x.x, x.z, 0x5410);
+                    qf[n][c][1] = __byte_perm(x.x, x.z, 0x7632);
+                    qf[n][c][2] = __byte_perm(x.y, x.w, 0x5410);
+                    qf[n][c][3] = __byte_perm(x.y, x.w, 0x7632);
+                    sum[c / kGroupChunks] += bf16_lo(x.x) + bf16_hi(x.x) + bf16_lo(x.y) + bf16_hi(x.y) + bf16_lo(x.z) +
+                                             bf16_hi(x.z) + bf16_lo(x.w) + bf16_hi(x.w);
+                }
+#pragma unroll
+                for (int a = 0; a < NG; ++a) {
+                    sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 1);
+                    sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 2);  // of query g
+                    qsum[n][a][0] = __shfl_sync(0xffffffffu, sum[a], 8 * t4);
+                    qsum[n][a][1] = __shfl_sync(0xffffffffu, sum[a], 8 * t4 + 4);
+                    om[n][a][0] = om[n][a][1] = 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int tok = min((t.block * C::kRows + 8 * n + 2 * t4 + e) / p.group, s.n - 1);
+                    hi[n][e] = p.causal ? s.P + tok : s.P + s.n - 1;
+                    lo[n][e] = p.causal && p.window > 0 ? s.P + tok - p.window + 1 : 0;
+                    m[n][e] = -INFINITY;
+                    l[n][e] = 0.f;
+                }
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] = 0.f;
+            }
+            const int last_tok = min((t.block * C::kRows + C::kRows - 1) / p.group, s.n - 1);
+            lo_most = p.causal && p.window > 0 ? s.P + last_tok - p.window + 1 : 0;
+        }
+
+        // running maximum of the scores x (log2 units) of a tile's keys: raised, with what was
+        // summed under it scaled, only when it falls behind by more than 2^8
+        auto raise = [&](float (&top)[NQ][2]) {
+            bool behind = false;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) behind |= top[n][e] > m[n][e] + 8.f;
+            if (!__any_sync(0xffffffffu, behind)) return;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                float alpha[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = top[n][e];
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                    x = fmaxf(x, m[n][e]);
+                    alpha[e] = m[n][e] == -INFINITY ? 0.f : exp2_approx(m[n][e] - x);
+                    m[n][e] = x;
+                    l[n][e] *= alpha[e];
+#pragma unroll
+                    for (int a = 0; a < NG; ++a) om[n][a][e] *= alpha[e];
+                }
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] *= alpha[e & 1];
+            }
+        };
+
+        if (key >= 0) {
+            // ---- 32 cached keys: octet a of them in the matrix rows g of tile a / 2
+            float sc[NQ][4][2];  // scores of key 8 a + g, queries 2 t4 + e
+            const uint32_t row_addr = tile_u32 + lane * C::kRowBytes;
+            const uint32_t* kp = reinterpret_cast<const uint32_t*>(tile + 2 * C::kCodes) + g * NG;
+            const uint32_t* vp = kp + kTileKeys * NG;
+#pragma unroll
+            for (int a = 0; a < NG; ++a) {
+                float acc[NQ][2][4];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) acc[n][e / 4][e % 4] = 0.f;
+#pragma unroll
+                for (int cc = 0; cc < kGroupChunks; ++cc) {
+                    const int c = a * kGroupChunks + cc;
+                    uint32_t x[4];
+                    ldmatrix4(row_addr + (c ^ swizzle<D>(lane)) * 16, x);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t a0 = codes<0>(x[2 * h]), a1 = codes<0>(x[2 * h + 1]), a2 = codes<1>(x[2 * h]),
+                                       a3 = codes<1>(x[2 * h + 1]), b0 = codes<2>(x[2 * h]), b1 = codes<2>(x[2 * h + 1]),
+                                       b2 = codes<3>(x[2 * h]), b3 = codes<3>(x[2 * h + 1]);
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            mma(acc[n][h], a0, a1, a2, a3, qf[n][c][0], qf[n][c][1]);
+                            mma(acc[n][h], b0, b1, b2, b3, qf[n][c][2], qf[n][c][3]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t w = kp[8 * k * NG + a];
+                    const float sk = bf16_lo(w), mk = fmaf(8.f, sk, bf16_hi(w));
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float prev = a == 0 ? mk * qsum[n][a][e] : fmaf(mk, qsum[n][a][e], sc[n][k][e]);
+                            sc[n][k][e] = fmaf(sk, acc[n][k / 2][2 * (k & 1) + e], prev);
+                        }
+                }
+            }
+            float top[NQ][2];
+            const bool edge = key + kTileKeys > s.P || key < lo_most;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    top[n][e] = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int pos = key + 8 * k + g;
+                        float x = sc[n][k][e] * p.scale_log2;
+                        if (edge && (pos >= s.P || pos < lo[n][e])) x = -INFINITY;
+                        sc[n][k][e] = x;
+                        top[n][e] = fmaxf(top[n][e], x);
+                    }
+                }
+            raise(top);
+            uint32_t pt[NQ][NG][4];  // P^T scaled by the values' parameters, per octet
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float sv[NG], mv[NG];
+#pragma unroll
+                for (int a = 0; a < NG; ++a) {
+                    const uint32_t w = vp[8 * k * NG + a];
+                    sv[a] = bf16_lo(w);
+                    mv[a] = fmaf(8.f, sv[a], bf16_hi(w));
+                }
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    float pr[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        pr[e] = exp2_approx(sc[n][k][e] - (m[n][e] == -INFINITY ? 0.f : m[n][e]));
+                        l[n][e] += pr[e];
+#pragma unroll
+                        for (int a = 0; a < NG; ++a) om[n][a][e] = fmaf(pr[e], mv[a], om[n][a][e]);
+                    }
+#pragma unroll
+                    for (int a = 0; a < NG; ++a) pt[n][a][k] = movmatrix(pack(pr[0] * sv[a], pr[1] * sv[a]));
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c) {
+                const int a = c / kGroupChunks;
+                uint32_t x[4];
+                ldmatrix4_trans(row_addr + C::kCodes + (c ^ swizzle<D>(lane)) * 16, x);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t a0 = codes<0>(x[2 * h]), a1 = codes<1>(x[2 * h]), a2 = codes<0>(x[2 * h + 1]),
+                                   a3 = codes<1>(x[2 * h + 1]), b0 = codes<2>(x[2 * h]), b1 = codes<3>(x[2 * h]),
+                                   b2 = codes<2>(x[2 * h + 1]), b3 = codes<3>(x[2 * h + 1]);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        mma(o[n][c][0], a0, a1, a2, a3, pt[n][a][2 * h], pt[n][a][2 * h + 1]);
+                        mma(o[n][c][1], b0, b1, b2, b3, pt[n][a][2 * h], pt[n][a][2 * h + 1]);
+                    }
+                }
+            }
+        } else {
+            // ---- up to 8 new tokens, bf16: the matrix rows g of one tile
+            const int tok0 = -1 - key, tok = tok0 + g;
+            float acc[NQ][4];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c) {
+                const uint4 x = *reinterpret_cast<const uint4*>(tile + g * 2 * D + 64 * c + 16 * t4);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    mma(acc[n], __byte_perm(x.x, x.z, 0x5410), 0, __byte_perm(x.x, x.z, 0x7632), 0, qf[n][c][0], qf[n][c][1]);
+                    mma(acc[n], __byte_perm(x.y, x.w, 0x5410), 0, __byte_perm(x.y, x.w, 0x7632), 0, qf[n][c][2], qf[n][c][3]);
+                }
+            }
+            float top[NQ][2];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int pos = s.P + tok;
+                    const bool seen = tok < s.n && pos <= hi[n][e] && pos >= lo[n][e];
+                    acc[n][e] = top[n][e] = seen ? acc[n][e] * p.scale_log2 : -INFINITY;
+                }
+            raise(top);
+            uint32_t pt[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    acc[n][e] = exp2_approx(acc[n][e] - (m[n][e] == -INFINITY ? 0.f : m[n][e]));
+                    l[n][e] += acc[n][e];
+                }
+                pt[n] = movmatrix(pack(acc[n][0], acc[n][1]));
+            }
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c) {
+                const uint8_t* v = tile + C::kCodes + 64 * c + 8 * g;
+                const uint2 x = *reinterpret_cast<const uint2*>(v + 2 * t4 * 2 * D);
+                const uint2 y = *reinterpret_cast<const uint2*>(v + (2 * t4 + 1) * 2 * D);
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    mma(o[n][c][0], __byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), 0, 0, pt[n], 0);
+                    mma(o[n][c][1], __byte_perm(x.y, y.y, 0x5410), __byte_perm(x.y, y.y, 0x7632), 0, 0, pt[n], 0);
+                }
+            }
+            if (t.block == 0) {
+                // their rows go into the cache, once per KV head
+                constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+                constexpr int kGroupLanes = kLanes / NG;
+                const int part = lane % kLanes;
+                for (int r0 = 0; r0 < kNewKeys && tok0 + r0 < s.n; r0 += kStep) {
+                    const int r = r0 + lane / kLanes;
+                    uint32_t kw, vw;
+                    const uint32_t kc = quantise8(*reinterpret_cast<const uint4*>(tile + r * 2 * D + part * 16), kGroupLanes, &kw);
+                    const uint32_t vc =
+                        quantise8(*reinterpret_cast<const uint4*>(tile + C::kCodes + r * 2 * D + part * 16), kGroupLanes, &vw);
+                    if (tok0 + r >= s.n) continue;
+                    const size_t row = row4(p.cache, t.b, t.kvh, s.P + tok0 + r);
+                    if (row == ~size_t(0)) continue;
+                    reinterpret_cast<uint32_t*>(p.cache.k + row * C::kRowBytes)[part] = kc;
+                    reinterpret_cast<uint32_t*>(p.cache.v + row * C::kRowBytes)[part] = vc;
+                    if (part % kGroupLanes == 0) {
+                        p.cache.kp[row * NG + part / kGroupLanes] = kw;
+                        p.cache.vp[row * NG + part / kGroupLanes] = vw;
+                    }
+                }
+                __syncwarp();
+            }
+        }
+
+        if (flags & kLast) {
+            const bool whole = !(flags & (kFromBefore | kGoesOn));
+            const int slot = flags & kFromBefore ? 0 : 1;
+            // the second record is written when the ring is done with: its copies have landed
+            float* const rec = slot == 0 ? kept : reinterpret_cast<float*>(ring);
+            __syncwarp();
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float x = l[n][e];
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    l[n][e] = x;
+#pragma unroll
+                    for (int a = 0; a < NG; ++a) {
+                        float y = om[n][a][e];
+                        y += __shfl_xor_sync(0xffffffffu, y, 4);
+                        y += __shfl_xor_sync(0xffffffffu, y, 8);
+                        y += __shfl_xor_sync(0xffffffffu, y, 16);
+                        om[n][a][e] = y;
+                    }
+                    const int row = 8 * n + 2 * t4 + e;
+                    const float f = whole ? 1.f / x : 1.f;
+#pragma unroll
+                    for (int c = 0; c < C::kChunks; ++c) {
+                        const float add = om[n][c / kGroupChunks][e];
+                        const float4 v = make_float4((o[n][c][0][e] + add) * f, (o[n][c][0][2 + e] + add) * f,
+                                                     (o[n][c][1][e] + add) * f, (o[n][c][1][2 + e] + add) * f);
+                        if (whole)
+                            store_row<D, NQ>(p, t, row, 32 * c + 4 * g, v);
+                        else
+                            *reinterpret_cast<float4*>(rec + row * D + 32 * c + 4 * g) = v;
+                    }
+                    if (g == 0) {
+                        if (whole)
+                            store_lse<NQ>(p, t, row, m[n][e], x);
+                        else
+                            stats[warp][slot][row] = make_float2(m[n][e], x);
+                    }
+                }
+            }
+            if (!whole && lane == 0) {
+                Record r;
+                r.t = t;
+                r.valid = 1;
+                records[warp][slot] = r;
+            }
+        }
+        if (++stage == C::kStages) stage = 0;
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+
+    // ---- the CTA's records, in list order: neighbours of one row block are joined
+    auto record_data = [&](int i) -> const float* {
+        const uint8_t* base = i & 1 ? smem + (i / 2) * C::kStages * C::kTileBytes
+                                    : smem + kWarps * C::kStages * C::kTileBytes + (i / 2) * C::kRecord;
+        return reinterpret_cast<const float*>(base);
+    };
+    constexpr int kElems = C::kRows * D;
+    float* const part_stats = p.part + (size_t)gridDim.x * 2 * kElems;
+    int pending[2] = {-1, -1};  // records whose row block other CTAs share: began before, goes on
+    for (int i = 0; i < 2 * kWarps;) {
+        const Record& r = records[i / 2][i & 1];
+        if (!r.valid) {
+            ++i;
+            continue;
+        }
+        int end = i + 1;
+        for (int k = i + 1; k < 2 * kWarps; ++k) {
+            const Record& x = records[k / 2][k & 1];
+            if (!x.valid) continue;
+            if (x.t.start_lo != r.t.start_lo || x.t.start_hi != r.t.start_hi) break;
+            end = k + 1;
+        }
+        const long long b0 = ((long long)r.t.start_hi << 32) | (unsigned)r.t.start_lo;
+        const bool whole = b0 >= from && b0 + r.t.tiles <= to;
+        const int slot = b0 < from ? 0 : 1;  // of the partial results
+        for (int x = tid * 4; x < kElems; x += kThreads * 4) {
+            const int row = x / D;
+            float top = -INFINITY;
+            for (int k = i; k < end; ++k)
+                if (records[k / 2][k & 1].valid) top = fmaxf(top, stats[k / 2][k & 1][row].x);
+            float sum = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k = i; k < end; ++k) {
+                if (!records[k / 2][k & 1].valid) continue;
+                const float2 st = stats[k / 2][k & 1][row];
+                const float w = st.x == -INFINITY ? 0.f : exp2_approx(st.x - top);
+                const float4 y = *reinterpret_cast<const float4*>(record_data(k) + x);
+                sum = fmaf(w, st.y, sum);
+                v.x = fmaf(w, y.x, v.x), v.y = fmaf(w, y.y, v.y), v.z = fmaf(w, y.z, v.z), v.w = fmaf(w, y.w, v.w);
+            }
+            if (whole) {
+                const float f = 1.f / sum;
+                store_row<D, NQ>(p, r.t, row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+                if (x % D == 0) store_lse<NQ>(p, r.t, row, top, sum);
+            } else {
+                const size_t at = (size_t)blockIdx.x * 2 + slot;
+                __stcg(reinterpret_cast<float4*>(p.part + at * kElems + x), v);
+                if (x % D == 0) __stcg(reinterpret_cast<float2*>(part_stats) + at * C::kRows + row, make_float2(top, sum));
+            }
+        }
+        if (!whole) pending[slot] = i;
+        i = end;
+    }
+
+    // ---- row blocks that several CTAs share: the last to arrive joins them
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        if (pending[k] < 0) continue;  // (the whole CTA)
+        const Tile& t = records[pending[k] / 2][pending[k] & 1].t;
+        const long long b0 = ((long long)t.start_hi << 32) | (unsigned)t.start_lo;
+        const int c0 = (int)(b0 / share), c1 = (int)((b0 + t.tiles - 1) / share);
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            arrived = atomicAdd(p.arrivals + c0, 1);
+            __threadfence();
+        }
+        __syncthreads();
+        if (arrived != c1 - c0) continue;
+        if (tid == 0) p.arrivals[c0] = 0;
+        auto at = [&](int c) -> size_t { return (size_t)c * 2 + (c == c0 ? 1 : 0); };
+        for (int x = tid * 4; x < kElems; x += kThreads * 4) {
+            const int row = x / D;
+            float top = -INFINITY;
+#pragma unroll 8
+            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(part_stats) + at(c) * C::kRows + row).x);
+            float sum = 0.f;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+            for (int c = c0; c <= c1; ++c) {
+                const float2 st = __ldcg(reinterpret_cast<const float2*>(part_stats) + at(c) * C::kRows + row);
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + at(c) * kElems + x));
+                const float w = st.x == -INFINITY ? 0.f : exp2_approx(st.x - top);
+                sum = fmaf(w, st.y, sum);
+                v.x = fmaf(w, y.x, v.x), v.y = fmaf(w, y.y, v.y), v.z = fmaf(w, y.z, v.z), v.w = fmaf(w, y.w, v.w);
+            }
+            const float f = 1.f / sum;
+            store_row<D, NQ>(p, t, row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+            if (x % D == 0) store_lse<NQ>(p, t, row, top, sum);
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int NG, int NQ>
+cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
+    using C = Cfg<D, NG, NQ>;
+    constexpr int kSmem = kWarps * (C::kStages * C::kTileBytes + C::kRecord);
+    static_assert(kSmem <= 210 * 1024, "shared memory budget, beside the static part");
+    static int configured_for[64] = {0};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !configured_for[dev]) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(attn_rows4_kernel<D, NG, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) configured_for[dev] = 1;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_rows4_kernel<D, NG, NQ>, p);
+}
+
+}  // namespace rows4
+
+}  // namespace pa

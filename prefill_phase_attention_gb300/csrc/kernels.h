@@ -4,6 +4,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "cache4.cuh"
 #include "common.cuh"
 
 namespace pa {
@@ -180,5 +181,51 @@ struct EvictArgs {
     int block_log2, max_blocks, num_blocks;
 };
 cudaError_t launch_evict(const EvictArgs& a, int sms, int* launches, cudaStream_t stream);
+
+// ---- the 4-bit cache ----
+
+// Checks a call's sequences into a.checked (n = 0 for one that is skipped).  whole: every
+// table entry up to a sequence's last token counts, else only those of the call's tokens.
+cudaError_t launch_check_sequences4(const Sequences4& a, const Cache4& c, bool whole, cudaStream_t stream);
+
+// Rows of packed tokens [total_q, n_kv_heads, head_dim] into the cache, or back.
+struct Copy4Params {
+    Sequences4 seqs;
+    Cache4 cache;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    __nv_bfloat16* k_out;
+    __nv_bfloat16* v_out;
+};
+cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, cudaStream_t stream);
+
+// Attention of few query rows per sequence over the 4-bit cache (attn_rows4.cu).
+constexpr int kRows4Warps = 8;
+constexpr int kRows4Seqs = 256;  // sequences whose metadata a CTA keeps in shared memory
+struct Rows4Params {
+    Sequences4 seqs;
+    Cache4 cache;
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    __nv_bfloat16* out;
+    float* lse;
+    int n_heads, group;
+    float scale_log2;
+    int causal, window;
+    // partial results that CTAs hand one another: [grid][2] of 8 * row_tiles rows of D
+    // floats, then as many (maximum, sum) pairs; arrivals[grid] is zero between calls
+    float* part;
+    int* arrivals;
+};
+template <int D>
+cudaError_t launch_attn_rows4_d(const Rows4Params& p, int row_tiles, int grid, cudaStream_t stream);
+template <>
+cudaError_t launch_attn_rows4_d<64>(const Rows4Params& p, int row_tiles, int grid, cudaStream_t stream);
+template <>
+cudaError_t launch_attn_rows4_d<128>(const Rows4Params& p, int row_tiles, int grid, cudaStream_t stream);
+// row_tiles: query rows of a row block, in tiles of 8, 1 or 2.
+cudaError_t launch_attn_rows4(const Rows4Params& p, int head_dim, int row_tiles, int grid, cudaStream_t stream);
 
 }  // namespace pa

@@ -1,0 +1,388 @@
+"""GPU tests of the 4-bit cache: attention over it, writing it and reading it back, each against its plain 64-bit
+form (tests/cache4_reference.py, where the bounds are derived)."""
+import math
+
+import pytest
+import torch
+
+from prefill_phase_attention_gb300 import binding
+from tests import cache4_reference as R
+
+pytestmark = pytest.mark.gpu
+
+GUARD = 4096
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from prefill_phase_attention_gb300 import build
+    build.build()
+    binding.load()
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need CUDA")
+
+
+def cumulative(lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    return cu
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32).cuda()
+
+
+def guarded(x):
+    """(buffer with bands on both sides, the view that holds x)."""
+    n = x.numel() * x.element_size()
+    buf = torch.full((n + 2 * GUARD,), 0x5a, dtype=torch.uint8, device="cuda")
+    view = buf[GUARD:GUARD + n].view(x.dtype).view(x.shape)
+    view.copy_(x)
+    return buf, view
+
+
+def same_bits(a, b):
+    return torch.equal(a.contiguous().view(torch.uint8).cpu(), b.contiguous().view(torch.uint8).cpu())
+
+
+class Call:
+    """Inputs of one call on the CPU, their GPU copies, and what is written in guarded buffers."""
+
+    def __init__(self, seed, new, lens, d=128, hk=2, share=2, group=None, block=0, kind="normal", slack=3):
+        g = torch.Generator().manual_seed(seed)
+        self.new, self.lens, self.d, self.hk, self.share = new, lens, d, hk, share
+        cap = max(p + n for p, n in zip(lens, new)) + slack
+        self.cache = R.Cache(g, len(new), cap, hk, d, group or d, block, kind=kind)
+        t = sum(new)
+        size = 2.0 ** 40 if kind == "large" else 1.0
+        self.q = (torch.randn((t, hk * share, d), generator=g) / size).to(torch.bfloat16)
+        self.k = (torch.randn((t, hk, d), generator=g) * size).to(torch.bfloat16)
+        self.v = (torch.randn((t, hk, d), generator=g) * size).to(torch.bfloat16)
+        self.cu, self.scale = cumulative(new), d ** -0.5
+        self.meta = (i32(self.cu), i32(cumulative([p + n for p, n in zip(lens, new)])))
+        self.offsets = i32(lens)
+        self.dev = [x.cuda() for x in (self.q, self.k, self.v)]
+        self.cache.spoil(lens)
+        self.codes = [guarded(x) for x in self.cache.codes]
+        self.params = [guarded(x) for x in self.cache.params]
+        self.out = guarded(torch.full(self.q.shape, math.nan, dtype=torch.bfloat16))
+        self.lse = guarded(torch.full((t, hk * share), math.nan))
+        self.opts = dict(cache_k_params=self.params[0][1], cache_v_params=self.params[1][1],
+                         block_table=None if self.cache.table is None else self.cache.table.cuda())
+
+    def attend(self, **kw):
+        binding.prefill_attn_varlen_cache4(*self.dev, *self.meta, self.codes[0][1], self.codes[1][1], self.offsets,
+                                           self.out[1], self.lse[1], scale=self.scale, **self.opts, **kw)
+
+    def write(self, **kw):
+        binding.prefill_attn_cache4_write(*self.dev[1:], self.meta[0], self.codes[0][1], self.codes[1][1], self.offsets,
+                                          **self.opts, **kw)
+
+    def guards(self):
+        for buf, _ in self.codes + self.params + [self.out, self.lse]:
+            assert (buf[:GUARD] == 0x5a).all() and (buf[-GUARD:] == 0x5a).all(), "write outside a buffer"
+
+    def check_cache(self, k=None):
+        codes, params = self.cache.stored(self.k if k is None else k, self.v, self.cu, self.lens)
+        for which in range(2):
+            assert same_bits(self.codes[which][1], codes[which]), "codes"
+            assert same_bits(self.params[which][1], params[which]), "parameters"
+
+    def check(self, causal=True, window=0, tiles=False):
+        torch.cuda.synchronize()
+        assert binding.prefill_attn_device_status() == 0
+        out, lse, bound, lbound = R.attention(self.cache, self.q, self.k, self.v, self.cu, self.lens, self.scale, causal,
+                                              window, tiles)
+        got, glse = self.out[1].double().cpu(), self.lse[1].double().cpu()
+        assert got.isfinite().all() and glse.isfinite().all()
+        assert ((got - out).abs() <= bound).all(), ((got - out).abs() / bound).max()
+        assert ((glse - lse).abs() <= lbound).all(), ((glse - lse).abs() / lbound).max()
+        self.check_cache()
+        self.guards()
+
+
+DIMS = [(128, 128), (128, 64), (128, 32), (64, 64), (64, 32), (32, 32)]
+
+
+@pytest.mark.parametrize("block", [0, 8, 16, 128])
+@pytest.mark.parametrize("d,group", DIMS)
+def test_decode_rows(d, group, block):
+    c = Call(1, [1] * 9, [0, 1, 31, 32, 33, 255, 256, 257, 1000], d, group=group, block=block, share=4)
+    c.attend()
+    c.check()
+
+
+@pytest.mark.parametrize("hk,share", [(1, 1), (1, 8), (3, 5), (2, 16), (1, 48), (8, 1)])
+def test_head_layouts(hk, share):
+    c = Call(2, [1, 2, 1], [77, 500, 3], hk=hk, share=share, group=32)
+    c.attend()
+    c.check()
+
+
+@pytest.mark.parametrize("d,group", [(128, 64), (64, 64), (32, 32)])
+@pytest.mark.parametrize("new,lens", [([5, 1, 7], [100, 2000, 0]), ([9, 17, 1, 0], [31, 33, 64, 9]), ([8, 16], [0, 257])])
+def test_drafts(d, group, new, lens):
+    for block in (0, 16):
+        c = Call(3, new, lens, d, group=group, block=block, share=3)
+        c.attend()
+        c.check()
+
+
+@pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 100, 5000])
+@pytest.mark.parametrize("block", [0, 16])
+def test_windows(window, block):
+    c = Call(4, [1, 3, 1, 12], [1000, 257, 5, 40], group=64, block=block)
+    c.attend(window=window)
+    c.check(window=window)
+
+
+def test_all_keys_visible():
+    c = Call(5, [4, 1, 11], [64, 33, 0], group=32)
+    c.attend(causal=False)
+    c.check(causal=False)
+
+
+def test_one_long_row():
+    """Every CTA has a share of the same rows."""
+    c = Call(6, [1], [40000], hk=1, share=4)
+    c.attend()
+    c.check()
+
+
+def test_many_sequences():
+    """More sequences than a CTA keeps in shared memory."""
+    g = torch.Generator().manual_seed(0)
+    lens = torch.randint(0, 70, (700,), generator=g).tolist()
+    new = torch.randint(0, 3, (700,), generator=g).tolist()
+    c = Call(7, new, lens, d=32, hk=1, share=2)
+    c.attend()
+    c.check()
+
+
+def test_large_values():
+    """Scales far outside fp16's range."""
+    c = Call(8, [1, 6], [300, 45], group=64, kind="large")
+    c.attend()
+    c.check()
+
+
+def test_equal_inputs_give_equal_bits():
+    outs = []
+    for _ in range(3):
+        c = Call(9, [1] * 5, [5000, 3, 777, 12000, 64], hk=4, share=2)
+        c.attend()
+        outs.append((c.out[1].clone(), c.lse[1].clone()))
+    for o in outs[1:]:
+        assert same_bits(o[0], outs[0][0]) and same_bits(o[1], outs[0][1])
+
+
+@pytest.mark.parametrize("block", [0, 16])
+def test_rotary(block):
+    """The attention call's rotary embedding: q and the cached key as a call on rotated tensors has them."""
+    theta = 10000.0
+    c = Call(10, [1, 4, 1], [100, 257, 0], group=64, block=block)
+    c.attend(rope_theta=theta)
+    rot = [torch.empty_like(x) for x in (c.q, c.k)]
+    for b, p in enumerate(c.lens):
+        rows = slice(c.cu[b], c.cu[b + 1])
+        pos = p + torch.arange(c.new[b])
+        for x, y in zip((c.q, c.k), rot):
+            y[rows] = R.rotate(x[rows], pos, theta).to(torch.bfloat16)
+    e = Call(10, [1, 4, 1], [100, 257, 0], group=64, block=block)
+    e.q, e.k = rot
+    e.dev[:2] = [x.cuda() for x in rot]
+    e.attend()
+    torch.cuda.synchronize()
+    # a rotated value may round the other way (fp32 against 64 bits): one step of bf16 in few places,
+    # which moves a score by 2^-8 |q| |k| scale at those; the outputs agree within a bf16 step of the largest
+    a, b = c.out[1].double().cpu(), e.out[1].double().cpu()
+    assert (a - b).abs().max() <= 8 * R.U * b.abs().max()
+    # the call's own write and prefill_attn_cache4_write rotate alike
+    w = Call(10, [1, 4, 1], [100, 257, 0], group=64, block=block)
+    w.write(rope_theta=theta)
+    for which in range(2):
+        assert same_bits(w.codes[which][1], c.codes[which][1]) and same_bits(w.params[which][1], c.params[which][1])
+
+
+# ---------------------------------------------------------------------------
+# writing and reading
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("block", [0, 8, 64])
+@pytest.mark.parametrize("d,group", DIMS)
+def test_write(d, group, block):
+    c = Call(20, [1, 0, 33, 130, 2], [0, 7, 31, 5, 1000], d, hk=3, group=group, block=block)
+    c.write()
+    torch.cuda.synchronize()
+    assert binding.prefill_attn_device_status() == 0
+    c.check_cache()
+    c.guards()
+
+
+def edge_rows(d):
+    """Rows at the format's edges: constants, one outlier, ties, tiny and huge ranges, signed zeros."""
+    x = torch.zeros((12, 1, d))
+    x[1] = 3.25
+    x[2] = -1e-30
+    x[3, 0, 5] = 100.0
+    x[4] = torch.arange(d) % 16                               # codes without a rounding
+    x[5] = torch.arange(d) % 31 * 0.5                         # ties
+    x[6] = 1e-38 * (torch.arange(d) % 7)                      # a scale below the smallest normal number
+    x[7] = 2.0 ** -120 * (torch.arange(d) % 3)
+    x[8] = 1e38 * ((torch.arange(d) % 3) - 1)
+    x[9, 0, ::2] = -0.0
+    x[10] = 1000.0 + torch.arange(d) * 4
+    x[11, 0, -1] = -7.0
+    return x.to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("d,group", DIMS)
+def test_format_edges(d, group):
+    c = Call(21, [12], [4], d, hk=1, share=1, group=group)
+    c.k = edge_rows(d)
+    c.v = edge_rows(d).flip(0)
+    c.dev[1], c.dev[2] = c.k.cuda(), c.v.cuda()
+    c.write()
+    c.check_cache()
+    k, v = torch.empty_like(c.dev[1]), torch.empty_like(c.dev[2])
+    binding.prefill_attn_cache4_read(c.codes[0][1], c.codes[1][1], c.meta[0], c.offsets, k, v, **c.opts)
+    torch.cuda.synchronize()
+    for x, got in ((c.k, k), (c.v, v)):
+        codes, params = R.quantise(x, group)
+        assert same_bits(got, R.values(codes, params).float().to(torch.bfloat16))
+        # within half a step, the scale's own rounding over 15 steps, and the value's rounding
+        y = x.double().unflatten(-1, (-1, group))
+        span = (y.amax(-1) - y.amin(-1))[..., None]
+        bound = span / 30 + span * R.U + y.abs() * R.U + 15 * 2.0 ** -126
+        assert ((got.cpu().double().unflatten(-1, (-1, group)) - y).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("block", [0, 8, 64])
+@pytest.mark.parametrize("d,group", DIMS)
+def test_read(d, group, block):
+    g = torch.Generator().manual_seed(22)
+    starts, lens = [0, 3, 31, 100, 9], [1, 0, 129, 33, 2]
+    cache = R.Cache(g, 5, 160, 3, d, group, block)
+    t, cu = sum(lens), cumulative(lens)
+    codes, params = [x.cuda() for x in cache.codes], [x.cuda() for x in cache.params]
+    out = [guarded(torch.full((t, 3, d), math.nan, dtype=torch.bfloat16)) for _ in range(2)]
+    binding.prefill_attn_cache4_read(*codes, i32(cu), i32(starts), out[0][1], out[1][1], cache_k_params=params[0],
+                                     cache_v_params=params[1], block_table=None if cache.table is None else cache.table.cuda())
+    torch.cuda.synchronize()
+    assert binding.prefill_attn_device_status() == 0
+    for which in range(2):
+        want = torch.empty((t, 3, d), dtype=torch.bfloat16)
+        for b in range(5):
+            for h in range(3):
+                rows = cache.rows(which, b, h, starts[b] + lens[b], starts[b])
+                want[cu[b]:cu[b + 1], h] = R.values(*rows).float().to(torch.bfloat16)
+        assert same_bits(out[which][1], want)
+        assert (out[which][0][:GUARD] == 0x5a).all() and (out[which][0][-GUARD:] == 0x5a).all()
+
+
+# ---------------------------------------------------------------------------
+# metadata, streams, graphs, runs of calls
+# ---------------------------------------------------------------------------
+
+def test_bad_sequences_are_skipped():
+    """A sequence whose table names a block outside the pool, or whose lengths disagree: nothing of it is touched."""
+    c = Call(30, [1, 2, 1], [40, 20, 70], block=16)
+    table = c.opts["block_table"]
+    table[1, 1] = c.cache.codes[0].shape[0]
+    c.attend()
+    torch.cuda.synchronize()
+    assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+    out, lse, bound, _ = R.attention(c.cache, c.q, c.k, c.v, c.cu, c.lens, c.scale)
+    got = c.out[1].double().cpu()
+    assert got[1:3].isnan().all() and c.lse[1][1:3].isnan().all()
+    for rows in (slice(0, 1), slice(3, 4)):
+        assert ((got[rows] - out[rows]).abs() <= bound[rows]).all()
+    slot, row = c.cache.at(1, torch.arange(20, 22))
+    assert same_bits(c.codes[0][1][slot.cuda(), :, row.cuda()], c.cache.codes[0][slot, :, row])
+    for call in (c.write, c.attend):
+        table[1, 1] = -1
+        call()
+        assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+    e = Call(31, [1, 1], [40, 20])
+    e.meta[1][2] += 1
+    e.attend()
+    torch.cuda.synchronize()
+    assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+    assert e.out[1][1].isnan().all() and not e.out[1][0].isnan().any()
+
+
+def test_captured_calls_read_their_metadata_at_replay():
+    c = Call(32, [1] * 4, [300, 5, 64, 1000], hk=4, block=16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c.attend()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            c.attend()
+        want = c.out[1].clone()
+        c.out[1].fill_(math.nan)
+        for _ in range(3):
+            graph.replay()
+        side.synchronize()
+        assert same_bits(c.out[1], want)
+        lens = [17, 900, 0, 33]
+        c.cache.spoil([max(a, b) for a, b in zip(lens, c.lens)])
+        c.offsets.copy_(i32(lens))
+        c.meta[1].copy_(i32(cumulative([p + 1 for p in lens])))
+        d = Call(32, [1] * 4, lens, hk=4, block=16, slack=103)  # as many blocks
+        for a, b in zip(c.codes + c.params, d.codes + d.params):
+            a[1].copy_(b[1])
+        graph.replay()
+        side.synchronize()
+        d.attend()
+        side.synchronize()
+        assert same_bits(c.out[1], d.out[1]) and same_bits(c.lse[1], d.lse[1])
+
+
+def test_two_streams_at_once():
+    calls = [Call(33 + i, [1] * 3, [2000, 77, 500], hk=2) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for c, s in zip(calls, streams):
+            c.attend(stream=s)
+    for c in calls:
+        c.check()
+
+
+@pytest.mark.parametrize("block", [0, 16])
+def test_a_conversation(block):
+    """A prompt written from elsewhere, decode steps that append to the cache, and the cache read back: each step
+    attends what the one before stored."""
+    d, group, hk, share = 64, 32, 2, 4
+    c = Call(40, [50, 3], [0, 0], d, hk, share, group, block, slack=20)
+    c.write()
+    codes, params = c.cache.stored(c.k, c.v, c.cu, c.lens)
+    lens = [50, 3]
+    for step in range(4):
+        n = Call(41 + step, [1 + step, 1], lens, d, hk, share, group)
+        cache = c.cache
+        cache.codes, cache.params = codes, params
+        out, lse, bound, lbound = R.attention(cache, n.q, n.k, n.v, n.cu, lens, n.scale)
+        o, z = torch.empty_like(n.dev[0]), torch.empty_like(n.lse[1])
+        binding.prefill_attn_varlen_cache4(*n.dev, *n.meta, c.codes[0][1], c.codes[1][1], n.offsets, o, z, scale=n.scale,
+                                           **c.opts)
+        torch.cuda.synchronize()
+        assert ((o.double().cpu() - out).abs() <= bound).all() and ((z.double().cpu() - lse).abs() <= lbound).all()
+        codes, params = cache.stored(n.k, n.v, n.cu, lens)
+        lens = [p + m for p, m in zip(lens, n.new)]
+    for which in range(2):
+        assert same_bits(c.codes[which][1], codes[which]) and same_bits(c.params[which][1], params[which])
+    k, v = (torch.empty((sum(lens), hk, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    binding.prefill_attn_cache4_read(c.codes[0][1], c.codes[1][1], i32(cumulative(lens)), i32([0, 0]), k, v, **c.opts)
+    torch.cuda.synchronize()
+    c.cache.codes, c.cache.params = codes, params
+    cu = cumulative(lens)
+    for which, got in enumerate((k, v)):
+        for b in range(2):
+            for h in range(hk):
+                want = R.values(*c.cache.rows(which, b, h, lens[b])).float().to(torch.bfloat16)
+                assert same_bits(got[cu[b]:cu[b + 1], h], want)
