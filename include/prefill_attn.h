@@ -424,7 +424,7 @@ pa_status prefill_attn_evict(
  *                       channels 2j (low 4 bits) and 2j + 1 (high).
  *   k_params, v_params  head_dim / group pairs (s, m) of bf16 a row.
  * All are 16-byte aligned.  A group x of bf16 values is stored as
- *   m = min x;  s = bf16(fl(max x - m) * fl(1/15)), or 0 when that is < 2^-126;
+ *   m = min x (0 for -0);  s = bf16(fl(max x - m) * fl(1/15)), or 0 when that is < 2^-126;
  *   code_i = min(15, rint(fl(fl(x_i - m) * r))), r = fl(1/s) (0 when s = 0),
  * fl: to the nearest fp32; rint: to the nearest integer, ties to even.  max x - m must
  * be finite in fp32.  d = 128 takes 68 bytes a row at group 128 and 80 at group
@@ -473,7 +473,7 @@ pa_status prefill_attn_varlen_cache4(
  * sequence whose metadata is inconsistent, or whose tokens' table entries name a
  * block outside the pool, is skipped (PA_DEVERR_METADATA).  The cache must
  * overlap no other buffer of the call; num_seqs and max_cache_len are at most
- * 2^30, total * n_kv_heads below that.
+ * 2^30, total * n_kv_heads is below that and n_kv_heads below 2^15.
  */
 pa_status prefill_attn_cache4_write(
     const void *k, const void *v, const int32_t *cu_seqlens,

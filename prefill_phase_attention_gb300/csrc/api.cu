@@ -472,6 +472,8 @@ void fill_fwd(pa::FwdParams& p, const void* k, const void* v, void* cache_k, voi
     p.max_blocks = o.max_blocks;
     p.num_blocks = o.num_blocks;
     p.kv_quant = o.kv_quant;
+    p.params_k = p.params_v = nullptr;
+    p.groups = 0;
     p.wait_timeout_test = o.wait_timeout_test;
     p.alt = sched != 2;
     p.unit_slots = sched == 1 ? 1 : pa::kSlots;
@@ -502,6 +504,7 @@ void fill_schedule(pa::ScheduleArgs& sa, const int32_t* cu_seqlens_q, const int3
     sa.max_units = scr.max_units;
     sa.num_ctas = ctas;
     sa.unit_slots = slots;
+    sa.few_tokens = 0;
     sa.block_table = o.block_table;
     sa.block_size = o.block_size;
     sa.max_blocks = o.max_blocks;
@@ -1426,6 +1429,15 @@ pa_status read_cache4(const pa_cache4* cache, const Options& o, int head_dim, in
     return PA_OK;
 }
 
+// Attention over a 4-bit cache has two kernels.  The row kernel reads a sequence's cache
+// once per 16 query rows, at the rate of HBM; the tile kernel expands every cached tile to
+// bf16, which takes a unit as long as two such passes, for up to 256 rows.  So sequences
+// of up to 32 rows (of one token, if that has more) go to the row kernel and the others
+// to the tile kernel.  The host does not know the lengths: where all rows but one token of
+// each sequence are few, the row kernel takes every sequence, which costs less than the
+// other's launch and its scheduler's.
+constexpr int kRowsOfRowKernel = 32, kExcessRows = 256;
+
 constexpr int kCacheSpans = 4;
 void cache_spans(const pa::Cache4& c, const Options& o, int num_seqs, int head_dim, bool written, Span* out) {
     const size_t rows = cache_rows(o, num_seqs, c.max_cache_len, c.n_kv_heads);
@@ -1461,8 +1473,9 @@ pa_status copy_cache4(const void* k, const void* v, const int32_t* cu_seqlens, c
     pa::Copy4Params p;
     s = read_cache4(cache, o, head_dim, n_kv_heads, max_cache_len, !empty, &p.cache);
     if (s != PA_OK) return s;
-    if ((long long)total * n_kv_heads >= (1LL << 30))
-        return fail(PA_ERR_UNSUPPORTED, "total * n_kv_heads must be < 2^30");
+    // blocks of 8 heads of K and V at least where there are many (the grid's second dimension)
+    if ((long long)total * n_kv_heads >= (1LL << 30) || n_kv_heads > 32767)
+        return fail(PA_ERR_UNSUPPORTED, "total * n_kv_heads must be < 2^30 and n_kv_heads < 2^15");
     if (!o.block_table && (long long)num_seqs * n_kv_heads * max_cache_len >= (1LL << 31))
         return fail(PA_ERR_UNSUPPORTED, "num_seqs * n_kv_heads * max_cache_len must be < 2^31");
     if (empty) return PA_OK;
@@ -1486,7 +1499,9 @@ pa_status copy_cache4(const void* k, const void* v, const int32_t* cu_seqlens, c
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    const bool check = o.block_table || o.rope_theta > 0.f;  // by a kernel of its own
+    const int sms = sm_count(dev, &s);
+    if (s != PA_OK) return s;
+    const bool check = o.rope_theta > 0.f;  // the rotary prologue reads checked sequences
     const StreamLock lock(dev, stream);
     Workspace* const ws = lock.ws;
     s = grow_workspace(*ws, stream, check ? num_seqs : 0, 0);
@@ -1513,7 +1528,8 @@ pa_status copy_cache4(const void* k, const void* v, const int32_t* cu_seqlens, c
     p.v = static_cast<const __nv_bfloat16*>(v);
     p.k_out = write ? nullptr : static_cast<__nv_bfloat16*>(const_cast<void*>(k));
     p.v_out = write ? nullptr : static_cast<__nv_bfloat16*>(const_cast<void*>(v));
-    e = write ? pa::launch_write_cache4(p, head_dim, stream) : pa::launch_read_cache4(p, head_dim, stream);
+    e = write ? pa::launch_write_cache4(p, head_dim, sms, stream)
+              : pa::launch_read_cache4(p, head_dim, sms, stream);
     if (e != cudaSuccess) return cuda_fail(e, write ? "cache write launch" : "cache read launch");
     g_last_launches = launches;
     return PA_OK;
@@ -1586,38 +1602,80 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
     const int sms = sm_count(dev, &s);
     if (s != PA_OK) return s;
-    const int grid = std::min(sms, kArrivals);
     const int group = n_heads / n_kv_heads;
-    // row blocks of 16 where a sequence has more than 8 rows on average
-    const int row_tiles = (long long)total_q * group > 8LL * num_seqs ? 2 : 1;
-    const bool check = o.block_table || o.rope_theta > 0.f;
+    // Which kernels run: see kRowsOfRowKernel.
+    const int few = std::max(1, kRowsOfRowKernel / group);
+    const bool one = num_seqs == 1;
+    const bool tiles = one ? total_q > few : ((long long)total_q - num_seqs) * group > kExcessRows;
+    const bool rows = !(one && tiles);
+    // the row kernel's blocks have 16 rows where sequences have more than 8 on average (of
+    // those that it takes, if the tile kernel runs too)
+    const int row_tiles = group > 8 || (!tiles && (long long)total_q * group > 8LL * num_seqs) ? 2 : 1;
+    const int grid = std::min(sms, kArrivals);
+    const int sched = auto_schedule(total_q, num_seqs, n_heads, n_kv_heads, false, sms) == 1 ? 1 : 2;
+    const long long units = tiles ? unit_bound(total_q, num_seqs, n_heads, n_kv_heads, sched) : 0;
+    if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
+    const bool check = !tiles && (o.block_table || o.rope_theta > 0.f);
     const StreamLock lock(dev, stream);
     Workspace* const ws = lock.ws;
-    s = grow_workspace(*ws, stream, check ? num_seqs : 0, 0);
+    s = grow_workspace(*ws, stream, tiles || check ? num_seqs : 0, (int)units);
     if (s != PA_OK) return s;
     pa::Rows4Params p;
-    s = get_arrivals(ws, stream, &p.arrivals);
-    if (s != PA_OK) return s;
     void* part = nullptr;
-    s = get_aux_scratch(ws, stream, (size_t)grid * 2 * 8 * row_tiles * (head_dim + 2) * sizeof(float), &part);
-    if (s != PA_OK) return s;
+    if (rows) {
+        s = get_arrivals(ws, stream, &p.arrivals);
+        if (s != PA_OK) return s;
+        s = get_aux_scratch(ws, stream, (size_t)grid * 2 * 8 * row_tiles * (head_dim + 2) * sizeof(float), &part);
+        if (s != PA_OK) return s;
+    }
+    void* rope = nullptr;
+    if (o.rope_theta > 0.f) {
+        s = get_rope_scratch(ws, stream, (q_rows + k_rows) * head_dim * 2, &rope);
+        if (s != PA_OK) return s;
+    }
+    const Scratch scr{static_cast<pa::WorkspaceHeader*>(ws->ptr), ws_seqs(*ws), ws_units(*ws), ws->max_units,
+                      ws_seq_scratch(*ws)};
     p.seqs = pa::Sequences4{cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q,
-                            check ? ws_seqs(*ws) : nullptr, static_cast<pa::WorkspaceHeader*>(ws->ptr)};
-    int launches = 1;
-    if (check) {
+                            tiles || check ? scr.seqs : nullptr, scr.hdr};
+    int launches = 0;
+    const int tile_grid = (int)std::min<long long>(sms, units);
+    if (tiles) {
+        pa::ScheduleArgs sa;
+        fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, max_cache_len, n_heads, n_kv_heads,
+                      head_dim, causal, o, scr, sched, tile_grid);
+        sa.few_tokens = rows ? few : 0;
+        e = pa::launch_build_schedule(sa, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
+        ++launches;
+    } else if (check) {
         e = pa::launch_check_sequences4(p.seqs, c, true, stream);
         if (e != cudaSuccess) return cuda_fail(e, "sequence check launch");
         ++launches;
     }
-    if (o.rope_theta > 0.f) {
-        void* rope = nullptr;
-        s = get_rope_scratch(ws, stream, (q_rows + k_rows) * head_dim * 2, &rope);
-        if (s != PA_OK) return s;
+    if (rope) {
         e = rotate(q, k, cu_seqlens_q, p.seqs.checked, rope, total_q, num_seqs, n_heads, n_kv_heads, head_dim,
                    o.rope_theta, 0, stream);
         if (e != cudaSuccess) return cuda_fail(e, "rotary prologue launch");
         ++launches;
     }
+    if (tiles) {
+        pa::FwdParams fp;
+        fill_fwd(fp, k, v, c.k, c.v, out, lse, scr, max_cache_len, n_heads, n_kv_heads, scale, causal, o, sched);
+        fp.kv_quant = 2;
+        fp.params_k = c.kp;
+        fp.params_v = c.vp;
+        fp.groups = c.groups;
+        e = pa::encode_fwd_maps(fp, q, total_q, num_seqs, head_dim, o.num_blocks);
+        if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
+        e = head_dim == 32   ? pa::launch_attn_tiles4_d<32>(fp, tile_grid, stream)
+            : head_dim == 64 ? pa::launch_attn_tiles4_d<64>(fp, tile_grid, stream)
+                             : pa::launch_attn_tiles4_d<128>(fp, tile_grid, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+        ++launches;
+        g_last_schedule = sched;
+    }
+    g_last_launches = launches;
+    if (!rows) return PA_OK;
     p.cache = c;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k = static_cast<const __nv_bfloat16*>(k);
@@ -1629,10 +1687,11 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     p.scale_log2 = scale * 1.4426950408889634f;
     p.causal = causal;
     p.window = o.window;
+    p.most_tokens = tiles ? few : INT_MAX;
     p.part = static_cast<float*>(part);
     e = pa::launch_attn_rows4(p, head_dim, row_tiles, grid, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-    g_last_launches = launches;
+    ++g_last_launches;
     return PA_OK;
 } catch (...) {
     return caught();

@@ -88,7 +88,7 @@ struct Extent {
 template <int NQ>
 __device__ __forceinline__ Extent extent(const Rows4Params& p, const SeqInfo& s) {
     Extent e{0, 0, 0, 0};
-    if (s.n == 0) return e;
+    if (s.n == 0 || s.n > p.most_tokens) return e;
     const int lo = p.causal && p.window > 0 ? max(0, s.P - p.window + 1) : 0;  // oldest key of the first token
     e.first_tile = lo / kTileKeys;
     e.cached = max(0, (s.P + kTileKeys - 1) / kTileKeys - e.first_tile);
@@ -672,15 +672,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
                 const int part = lane % kLanes;
                 for (int r0 = 0; r0 < kNewKeys && tok0 + r0 < s.n; r0 += kStep) {
                     const int r = r0 + lane / kLanes;
-                    uint32_t kw, vw;
-                    const uint32_t kc = quantise8(*reinterpret_cast<const uint4*>(tile + r * 2 * D + part * 16), kGroupLanes, &kw);
-                    const uint32_t vc =
-                        quantise8(*reinterpret_cast<const uint4*>(tile + C::kCodes + r * 2 * D + part * 16), kGroupLanes, &vw);
+                    uint32_t kw, vw, kc[1], vc[1];
+                    const uint4 kx[1] = {*reinterpret_cast<const uint4*>(tile + r * 2 * D + part * 16)};
+                    const uint4 vx[1] = {*reinterpret_cast<const uint4*>(tile + C::kCodes + r * 2 * D + part * 16)};
+                    quantise(kx, kGroupLanes, kc, &kw);
+                    quantise(vx, kGroupLanes, vc, &vw);
                     if (tok0 + r >= s.n) continue;
                     const size_t row = row4(p.cache, t.b, t.kvh, s.P + tok0 + r);
                     if (row == ~size_t(0)) continue;
-                    reinterpret_cast<uint32_t*>(p.cache.k + row * C::kRowBytes)[part] = kc;
-                    reinterpret_cast<uint32_t*>(p.cache.v + row * C::kRowBytes)[part] = vc;
+                    reinterpret_cast<uint32_t*>(p.cache.k + row * C::kRowBytes)[part] = kc[0];
+                    reinterpret_cast<uint32_t*>(p.cache.v + row * C::kRowBytes)[part] = vc[0];
                     if (part % kGroupLanes == 0) {
                         p.cache.kp[row * NG + part / kGroupLanes] = kw;
                         p.cache.vp[row * NG + part / kGroupLanes] = vw;

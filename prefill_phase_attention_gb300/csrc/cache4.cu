@@ -1,10 +1,15 @@
 // cache4.cu -- writing keys and values into the 4-bit cache, reading them back, and
-// the check of a paged call's sequences.
+// the check of an attention call's sequences.
 //
-// Both are one pass over the rows: a lane takes 8 channels (16 bytes of bf16, 4 of
-// codes), head_dim / 8 lanes a row, and consecutive lanes of a warp take consecutive
-// tokens of one KV head, whose rows lie side by side in the cache.  The bytes bound
-// them; each thread has several rows in flight.
+// Both copies are one pass over the rows, which the bytes bound: a lane takes 16
+// channels (32 bytes of bf16, 8 of codes), head_dim / 16 lanes a row, and consecutive
+// rows of lanes take consecutive tokens of one KV head, whose rows lie side by side in
+// the cache.  A block takes 32 tokens and some heads of K and V; the tokens' sequences,
+// positions and table entries are looked up once a block, in shared memory.  A block
+// looks whether its sequences' tables are valid itself: a kernel ahead for that
+// costs a small call more than all of it.
+#include <algorithm>
+
 #include "cache4.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -16,123 +21,188 @@ namespace {
 constexpr int kCopyThreads = 256;
 constexpr int kCopyTokens = 32;  // of a block
 constexpr int kInFlight = 4;     // rows of a thread
+constexpr int kCuInSmem = 1024;  // sequences whose boundaries are searched in shared memory
 
-// Where the rows of a block's tokens are: the row of KV head 0 (~0: none); another
-// head's is `stride` rows on.
-__device__ __forceinline__ void locate_tokens(const Sequences4& a, const Cache4& c, long long t0, size_t* rows) {
-    for (int i = threadIdx.x; i < kCopyTokens; i += kCopyThreads) {
-        const long long t = t0 + i;
-        size_t row = ~size_t(0);
+struct Places {
+    int cu[kCuInSmem];
+    int seq[kCopyTokens], pos[kCopyTokens];
+    int last[kCopyTokens];        // of the token's sequence: its last position, its first token
+    int first[kCopyTokens];
+
+    size_t rows[kCopyTokens];     // row of KV head 0, ~0: none; another head's is `stride` rows on
+};
+
+// Where the rows of tokens [t0, t0 + kCopyTokens) are.  Ends with a barrier.
+__device__ __forceinline__ void locate_tokens(const Sequences4& a, const Cache4& c, int t0, Places& at) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool in_smem = a.num_seqs <= kCuInSmem;
+    if (in_smem) {
+        for (int b = tid; b < a.num_seqs; b += kCopyThreads) at.cu[b] = a.cu_seqlens_q[b];
+        __syncthreads();
+    }
+    if (tid < kCopyTokens) {
+        const int t = t0 + tid;
+        at.rows[tid] = ~size_t(0);
+        at.seq[tid] = -1;
+        
         if (t < a.total_q) {
             // the sequence owning token t: the last b with cu_seqlens_q[b] <= t
             int lo = 0, hi = a.num_seqs - 1;
             while (lo < hi) {
                 const int mid = lo + (hi - lo + 1) / 2;
-                if (a.cu_seqlens_q[mid] <= t)
+                if ((in_smem ? at.cu[mid] : a.cu_seqlens_q[mid]) <= t)
                     lo = mid;
                 else
                     hi = mid - 1;
             }
             const SeqInfo s = sequence4(a, c.max_cache_len, lo);
-            if (t >= s.q_start && t < (long long)s.q_start + s.n) row = row4(c, lo, 0, s.P + (int)(t - s.q_start));
+            if (t >= s.q_start && t < (long long)s.q_start + s.n) {
+                at.seq[tid] = lo;
+                at.pos[tid] = s.P + (t - s.q_start);
+                at.first[tid] = s.P;
+                at.last[tid] = s.P + s.n - 1;
+                at.rows[tid] = row4(c, lo, 0, at.pos[tid]);
+            }
         }
-        rows[i] = row;
     }
+    __syncthreads();
+    if (c.block_table && !a.checked) {
+        // a sequence with an entry outside the pool is skipped whole: the block's sequences,
+        // a warp each
+        for (int i = warp; i < kCopyTokens; i += kCopyThreads / 32) {
+            const int b = at.seq[i];
+            if (b < 0 || (i > 0 && at.seq[i - 1] == b)) continue;
+            const int32_t* table = c.block_table + (size_t)b * c.max_blocks;
+            const int end = (at.last[i] >> c.block_log2) + 1;
+            bool bad = false;
+#pragma unroll 8
+            for (int e = (at.first[i] >> c.block_log2) + lane; e < end; e += 32)
+                bad |= (unsigned)__ldg(table + e) >= (unsigned)c.num_blocks;
+            if (!__any_sync(0xffffffffu, bad)) continue;
+            if (lane == 0) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
+            if (i + lane < kCopyTokens && at.seq[i + lane] == b) at.rows[i + lane] = ~size_t(0);
+        }
+        __syncthreads();
+    }
+    if (!a.checked && blockIdx.x == 0 && blockIdx.y == 0)
+        for (int b = tid; b < a.num_seqs; b += kCopyThreads)
+            if (stated_sequence(a, c.max_cache_len, b).n < 0) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
 }
 
-// Sequences whose metadata is inconsistent are reported by block 0 where no kernel checked them.
-__device__ __forceinline__ void report_sequences(const Sequences4& a, int max_cache_len) {
-    if (a.checked || blockIdx.x != 0) return;
-    for (int b = threadIdx.x; b < a.num_seqs; b += blockDim.x)
-        if (stated_sequence(a, max_cache_len, b).n < 0) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
-}
+// Rows of a block: heads [h0, h1) of K then V, 32 tokens each; a thread takes every
+// kStep-th of them, `first` on, and channels [16 part, 16 part + 16).
+template <int D>
+struct Rows {
+    static constexpr int kLanes = D / 16;
+    static constexpr int kStep = kCopyThreads / kLanes;
+    static_assert(kStep % kCopyTokens == 0 || kCopyTokens % kStep == 0, "a pass is whole heads or part of one");
+    int part = threadIdx.x % kLanes, first = threadIdx.x / kLanes, h0, items;
+    __device__ __forceinline__ Rows(int n_kv_heads, int heads) {
+        h0 = blockIdx.y * heads;
+        items = (min(2 * n_kv_heads, h0 + heads) - h0) * kCopyTokens;
+    }
+    __device__ __forceinline__ int token(int it) const { return it % kCopyTokens; }
+    __device__ __forceinline__ int head(int it) const { return h0 + it / kCopyTokens; }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) write_cache4_kernel(const Copy4Params p) {
-    constexpr int kLanes = D / 8;  // of a row
-    __shared__ size_t rows[kCopyTokens];
-    const long long t0 = (long long)blockIdx.x * kCopyTokens;
-    griddep_wait();
-    locate_tokens(p.seqs, p.cache, t0, rows);
-    report_sequences(p.seqs, p.cache.max_cache_len);
-    __syncthreads();
-    const int Hk = p.cache.n_kv_heads, groups = p.cache.groups, group_lanes = kLanes / groups;
+    __shared__ Places at;
+    const int Hk = p.cache.n_kv_heads, groups = p.cache.groups, group_lanes = D / 16 / groups;
     const size_t stride = p.cache.block_table ? (size_t)1 << p.cache.block_log2 : (size_t)p.cache.max_cache_len;
-    const int part = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
-    constexpr int kStep = kCopyThreads / kLanes;  // rows of a pass
-    const int items = 2 * Hk * kCopyTokens;       // (k or v, head, token): a whole number of passes
-    for (int i0 = first; i0 < items; i0 += kInFlight * kStep) {
-        uint4 x[kInFlight];
+    const int t0 = blockIdx.x * kCopyTokens;
+    const Rows<D> r(Hk, p.heads);
+    constexpr int kStep = Rows<D>::kStep;
+    griddep_wait();
+    uint4 x[kInFlight][2];
+    auto load = [&](int i0) {
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
-            const int it = i0 + u * kStep, tt = it % kCopyTokens, h = it / kCopyTokens;
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (it < items && rows[tt] != ~size_t(0)) {
-                const __nv_bfloat16* src = h < Hk ? p.k : p.v;
-                x[u] = __ldg(reinterpret_cast<const uint4*>(src + ((t0 + tt) * Hk + (h < Hk ? h : h - Hk)) * D) + part);
+            const int it = i0 + u * kStep, t = t0 + r.token(it), h = r.head(it);
+            x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
+            if (it < r.items && t < p.seqs.total_q) {
+                const uint4* src =
+                    reinterpret_cast<const uint4*>((h < Hk ? p.k : p.v) + ((size_t)t * Hk + (h < Hk ? h : h - Hk)) * D) + 2 * r.part;
+                x[u][0] = __ldg(src);
+                x[u][1] = __ldg(src + 1);
             }
         }
+    };
+    load(r.first);  // in flight while the tokens are located
+    locate_tokens(p.seqs, p.cache, t0, at);
+    // (whole warps go round: items and the steps are multiples of a warp's rows)
+    for (int i0 = r.first; i0 < r.items; i0 += kInFlight * kStep) {
+        if (i0 != r.first) load(i0);
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
-            const int it = i0 + u * kStep, tt = it % kCopyTokens, h = it / kCopyTokens;
-            uint32_t word;
-            const uint32_t codes = quantise8(x[u], group_lanes, &word);
-            if (it >= items || rows[tt] == ~size_t(0)) continue;
-            const size_t row = rows[tt] + (h < Hk ? h : h - Hk) * stride;
-            reinterpret_cast<uint32_t*>((h < Hk ? p.cache.k : p.cache.v) + row * (D / 2))[part] = codes;
-            if (part % group_lanes == 0) (h < Hk ? p.cache.kp : p.cache.vp)[row * groups + part / group_lanes] = word;
+            const int it = i0 + u * kStep, h = r.head(it);
+            uint32_t codes[2], word;
+            quantise(x[u], group_lanes, codes, &word);
+            if (it >= r.items) continue;
+            size_t row = at.rows[r.token(it)];
+            if (row == ~size_t(0)) continue;
+            row += (h < Hk ? h : h - Hk) * stride;
+            reinterpret_cast<uint2*>((h < Hk ? p.cache.k : p.cache.v) + row * (D / 2))[r.part] = make_uint2(codes[0], codes[1]);
+            if (r.part % group_lanes == 0) (h < Hk ? p.cache.kp : p.cache.vp)[row * groups + r.part / group_lanes] = word;
         }
     }
 }
 
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) read_cache4_kernel(const Copy4Params p) {
-    constexpr int kLanes = D / 8;
-    __shared__ size_t rows[kCopyTokens];
-    const long long t0 = (long long)blockIdx.x * kCopyTokens;
-    griddep_wait();
-    locate_tokens(p.seqs, p.cache, t0, rows);
-    report_sequences(p.seqs, p.cache.max_cache_len);
-    __syncthreads();
-    const int Hk = p.cache.n_kv_heads, groups = p.cache.groups, group_lanes = kLanes / groups;
+    __shared__ Places at;
+    const int Hk = p.cache.n_kv_heads, groups = p.cache.groups, group_lanes = D / 16 / groups;
     const size_t stride = p.cache.block_table ? (size_t)1 << p.cache.block_log2 : (size_t)p.cache.max_cache_len;
-    const int part = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
-    constexpr int kStep = kCopyThreads / kLanes;
-    const int items = 2 * Hk * kCopyTokens;
-    for (int i0 = first; i0 < items; i0 += kInFlight * kStep) {
-        uint32_t codes[kInFlight], word[kInFlight];
+    const int t0 = blockIdx.x * kCopyTokens;
+    const Rows<D> r(Hk, p.heads);
+    constexpr int kStep = Rows<D>::kStep;
+    griddep_wait();
+    locate_tokens(p.seqs, p.cache, t0, at);
+    for (int i0 = r.first; i0 < r.items; i0 += kInFlight * kStep) {
+        uint2 codes[kInFlight];
+        uint32_t word[kInFlight];
+        bool there[kInFlight];
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
-            const int it = i0 + u * kStep, tt = it % kCopyTokens, h = it / kCopyTokens;
-            codes[u] = word[u] = 0;
-            if (it < items && rows[tt] != ~size_t(0)) {
-                const size_t row = rows[tt] + (h < Hk ? h : h - Hk) * stride;
-                codes[u] = reinterpret_cast<const uint32_t*>((h < Hk ? p.cache.k : p.cache.v) + row * (D / 2))[part];
-                word[u] = (h < Hk ? p.cache.kp : p.cache.vp)[row * groups + part / group_lanes];
+            const int it = i0 + u * kStep, h = r.head(it);
+            size_t row = it < r.items ? at.rows[r.token(it)] : ~size_t(0);
+            there[u] = row != ~size_t(0);
+            codes[u] = make_uint2(0, 0);
+            word[u] = 0;
+            if (there[u]) {
+                row += (h < Hk ? h : h - Hk) * stride;
+                codes[u] = __ldg(reinterpret_cast<const uint2*>((h < Hk ? p.cache.k : p.cache.v) + row * (D / 2)) + r.part);
+                word[u] = __ldg((h < Hk ? p.cache.kp : p.cache.vp) + row * groups + r.part / group_lanes);
             }
         }
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
-            const int it = i0 + u * kStep, tt = it % kCopyTokens, h = it / kCopyTokens;
-            if (it >= items || rows[tt] == ~size_t(0)) continue;
+            if (!there[u]) continue;
+            const int it = i0 + u * kStep, h = r.head(it);
             const float s = bf16_lo(word[u]), m = bf16_hi(word[u]);
-            uint32_t out[4];
+            uint4* dst = reinterpret_cast<uint4*>((h < Hk ? p.k_out : p.v_out) +
+                                                  ((size_t)(t0 + r.token(it)) * Hk + (h < Hk ? h : h - Hk)) * D) + 2 * r.part;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                // the product is exact, the sum rounds to fp32 and then once to bf16
-                const float a = fmaf((float)((codes[u] >> (8 * e)) & 15u), s, m);
-                const float b = fmaf((float)((codes[u] >> (8 * e + 4)) & 15u), s, m);
-                const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-                out[e] = *reinterpret_cast<const uint32_t*>(&v);
+            for (int half = 0; half < 2; ++half) {
+                const uint32_t c = half ? codes[u].y : codes[u].x;
+                uint32_t out[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // a code as the low bits of 2^23; the product with s is exact, the sum rounds
+                    // to fp32 and then once to bf16
+                    const float a = __uint_as_float(0x4b000000u | ((c >> (8 * e)) & 15u)) - 8388608.f;
+                    const float b = __uint_as_float(0x4b000000u | ((c >> (8 * e + 4)) & 15u)) - 8388608.f;
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(fmaf(a, s, m), fmaf(b, s, m));
+                    out[e] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                dst[half] = make_uint4(out[0], out[1], out[2], out[3]);
             }
-            __nv_bfloat16* dst = h < Hk ? p.k_out : p.v_out;
-            reinterpret_cast<uint4*>(dst + ((t0 + tt) * Hk + (h < Hk ? h : h - Hk)) * D)[part] =
-                make_uint4(out[0], out[1], out[2], out[3]);
         }
     }
 }
 
-// One block per sequence: its metadata, and the entries [first, end) of its table.
+// One block per sequence: its metadata, and the table entries of the call's tokens
+// (whole: of all tokens up to its last).
 __global__ void __launch_bounds__(128) check_sequences4_kernel(const Sequences4 a, const Cache4 c, bool whole) {
     const int b = blockIdx.x;
     griddep_launch();
@@ -140,7 +210,6 @@ __global__ void __launch_bounds__(128) check_sequences4_kernel(const Sequences4 
     const SeqInfo s = stated_sequence(a, c.max_cache_len, b);
     bool bad = s.n < 0;
     if (c.block_table && s.n > 0) {
-        // the blocks of the tokens it writes or reads; `whole`: of all tokens up to its last
         const int first = whole ? 0 : s.P >> c.block_log2, end = ((s.P + s.n - 1) >> c.block_log2) + 1;
         const int32_t* table = c.block_table + (size_t)b * c.max_blocks;
 #pragma unroll 4
@@ -154,9 +223,9 @@ __global__ void __launch_bounds__(128) check_sequences4_kernel(const Sequences4 
 }
 
 template <class Kernel, class... Args>
-cudaError_t launch_after(Kernel kernel, unsigned grid, unsigned threads, cudaStream_t stream, const Args&... args) {
+cudaError_t launch_after(Kernel kernel, dim3 grid, unsigned threads, cudaStream_t stream, const Args&... args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -170,24 +239,35 @@ cudaError_t launch_after(Kernel kernel, unsigned grid, unsigned threads, cudaStr
 }  // namespace
 
 cudaError_t launch_check_sequences4(const Sequences4& a, const Cache4& c, bool whole, cudaStream_t stream) {
-    return launch_after(check_sequences4_kernel, (unsigned)a.num_seqs, 128, stream, a, c, whole);
+    return launch_after(check_sequences4_kernel, dim3((unsigned)a.num_seqs), 128, stream, a, c, whole);
 }
 
-cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(((long long)p.seqs.total_q + kCopyTokens - 1) / kCopyTokens);
+namespace {
+
+// Heads of a block: enough blocks for the GPU first, then up to 8 heads to a block.
+template <class Kernel>
+cudaError_t launch_copy(Kernel kernel, Copy4Params p, int sms, cudaStream_t stream) {
+    const long long blocks = ((long long)p.seqs.total_q + kCopyTokens - 1) / kCopyTokens;
+    const long long heads = 2ll * p.cache.n_kv_heads;
+    p.heads = (int)std::max(1ll, std::min(8ll, blocks * heads / (8ll * sms)));
+    return launch_after(kernel, dim3((unsigned)blocks, (unsigned)((heads + p.heads - 1) / p.heads)), kCopyThreads, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream) {
     switch (head_dim) {
-        case 32: return launch_after(write_cache4_kernel<32>, grid, kCopyThreads, stream, p);
-        case 64: return launch_after(write_cache4_kernel<64>, grid, kCopyThreads, stream, p);
-        default: return launch_after(write_cache4_kernel<128>, grid, kCopyThreads, stream, p);
+        case 32: return launch_copy(write_cache4_kernel<32>, p, sms, stream);
+        case 64: return launch_copy(write_cache4_kernel<64>, p, sms, stream);
+        default: return launch_copy(write_cache4_kernel<128>, p, sms, stream);
     }
 }
 
-cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, cudaStream_t stream) {
-    const unsigned grid = (unsigned)(((long long)p.seqs.total_q + kCopyTokens - 1) / kCopyTokens);
+cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream) {
     switch (head_dim) {
-        case 32: return launch_after(read_cache4_kernel<32>, grid, kCopyThreads, stream, p);
-        case 64: return launch_after(read_cache4_kernel<64>, grid, kCopyThreads, stream, p);
-        default: return launch_after(read_cache4_kernel<128>, grid, kCopyThreads, stream, p);
+        case 32: return launch_copy(read_cache4_kernel<32>, p, sms, stream);
+        case 64: return launch_copy(read_cache4_kernel<64>, p, sms, stream);
+        default: return launch_copy(read_cache4_kernel<128>, p, sms, stream);
     }
 }
 

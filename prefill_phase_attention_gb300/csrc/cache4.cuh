@@ -5,7 +5,7 @@
 // channels.  A group's parameters are one 32-bit word, the scale s (low half) and the
 // minimum m (high half) as bf16; its codes are 4 bits per channel, two to a byte, the
 // even channel low.  A channel stands for m + code * s.  Of a group x of bf16 values
-//     m = min x                       (a bf16 already: exact)
+//     m = min x                       (a bf16 already: exact; 0 for -0)
 //     s = bf16(fl(max x - m) * fl(1/15)), 0 when that is below 2^-126
 //     code = min(15, rint(fl(fl(x - m) * r))), r = fl(1 / s), or 0 when s = 0
 // where fl rounds to fp32 and rint ties to even.  The error is at most s / 2 and a few
@@ -73,33 +73,51 @@ __device__ __forceinline__ size_t row4(const Cache4& c, int b, int kvh, int pos)
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// Quantises 8 channels (bf16 pairs x) of a row whose groups are spread over `lanes`
-// consecutive lanes each: returns the 8 codes, *params the group's word (the same in
-// its lanes).  All lanes of the warp.
-__device__ __forceinline__ uint32_t quantise8(const uint4& x, int lanes, uint32_t* params) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    float v[8];
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 v = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Quantises 8 kWords channels (bf16 pairs x) of a row whose groups are spread over
+// `lanes` consecutive lanes each: codes[w] holds those of channels 8 w ..., *params the
+// group's word (the same in its lanes).  All lanes of the warp.
+template <int kWords>
+__device__ __forceinline__ void quantise(const uint4 (&x)[kWords], int lanes, uint32_t (&codes)[kWords], uint32_t* params) {
+    // (minimum, -maximum) of the pairs, of the lane, of the group
+    uint32_t lo2 = x[0].x, hi2 = x[0].x ^ 0x80008000u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(w[i]), v[2 * i + 1] = bf16_hi(w[i]);
-    float lo = v[0], hi = v[0];
+    for (int w = 0; w < kWords; ++w) {
+        const uint32_t y[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
 #pragma unroll
-    for (int i = 1; i < 8; ++i) lo = fminf(lo, v[i]), hi = fmaxf(hi, v[i]);
-    for (int o = 1; o < lanes; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        for (int i = 0; i < 4; ++i) lo2 = min_bf16x2(lo2, y[i]), hi2 = min_bf16x2(hi2, y[i] ^ 0x80008000u);
     }
+    uint32_t ends = min_bf16x2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
+    for (int o = 1; o < lanes; o <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+    const float lo = __fadd_rn(bf16_lo(ends), 0.f), hi = -bf16_hi(ends);  // (a minimum of -0 is stored as 0)
     __nv_bfloat16 s = __float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f));
-    float sf = __bfloat162float(s);
-    const float r = sf >= 0x1p-126f ? __frcp_rn(sf) : 0.f;
-    if (!(sf >= 0x1p-126f)) s = __float2bfloat16_rn(0.f);
-    uint32_t codes = 0;
+    const bool normal = __bfloat162float(s) >= 0x1p-126f;
+    if (!normal) s = __float2bfloat16_rn(0.f);
+    const float r = normal ? __frcp_rn(__bfloat162float(s)) : 0.f;
+    // 2^23 + a value below 2^22 is rounded to an integer, ties to even; four codes then
+    // add up in the low 16 bits of such a sum, exactly
+    constexpr float kRound = 8388608.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = __float2int_rn(__fmul_rn(__fsub_rn(v[i], lo), r));
-        codes |= (uint32_t)(c < 15 ? c : 15) << (4 * i);
+    for (int w = 0; w < kWords; ++w) {
+        const uint32_t y[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
+        uint32_t half[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = i & 1 ? bf16_hi(y[2 * h + i / 2]) : bf16_lo(y[2 * h + i / 2]);
+                c[i] = __fsub_rn(__fadd_rn(fminf(__fmul_rn(__fsub_rn(v, lo), r), 15.f), kRound), kRound);
+            }
+            half[h] = __float_as_uint(__fadd_rn(fmaf(fmaf(c[3], 16.f, c[2]), 256.f, fmaf(c[1], 16.f, c[0])), kRound));
+        }
+        codes[w] = __byte_perm(half[0], half[1], 0x5410);
     }
     *params = (uint32_t)__bfloat16_as_ushort(s) | (__float_as_uint(lo) & 0xffff0000u);
-    return codes;
 }
 
 }  // namespace pa

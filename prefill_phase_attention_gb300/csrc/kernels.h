@@ -66,7 +66,11 @@ struct FwdParams {
     // scale of each cache row ([B, Hk, cap])
     float* scale_k;
     float* scale_v;
-    int kv_quant;
+    int kv_quant;  // 0: bf16, 1: int8, 2: 4 bits
+    // 4-bit cache: cache_k/cache_v hold its codes, these the parameters of each row's groups
+    uint32_t* params_k;
+    uint32_t* params_v;
+    int groups;
     int wait_timeout_test;  // test hook: CTA 0 waits on a barrier nothing completes
     // alternating variant (bf16 cache): units whose rows fit one Q tile split
     // their KV tiles between both softmax slots (even / odd) and merge the two
@@ -80,6 +84,16 @@ struct FwdParams {
 // num_blocks: blocks in the pool when p.block_table is set (else unused).
 cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_seqs, int head_dim, int num_blocks);
 cudaError_t launch_attn_fwd(const FwdParams& p, int head_dim, int grid, cudaStream_t st);
+
+// The same kernel over a 4-bit cache.
+template <int D>
+cudaError_t launch_attn_tiles4_d(const FwdParams& p, int grid, cudaStream_t st);
+template <>
+cudaError_t launch_attn_tiles4_d<32>(const FwdParams& p, int grid, cudaStream_t st);
+template <>
+cudaError_t launch_attn_tiles4_d<64>(const FwdParams& p, int grid, cudaStream_t st);
+template <>
+cudaError_t launch_attn_tiles4_d<128>(const FwdParams& p, int grid, cudaStream_t st);
 
 // Scheduler of the long-context variant.
 struct LongScheduleArgs : ScheduleArgs {
@@ -196,9 +210,10 @@ struct Copy4Params {
     const __nv_bfloat16* v;
     __nv_bfloat16* k_out;
     __nv_bfloat16* v_out;
+    int heads;  // of K and V that a block takes (set by the launch)
 };
-cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, cudaStream_t stream);
-cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, cudaStream_t stream);
+cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
+cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
 
 // Attention of few query rows per sequence over the 4-bit cache (attn_rows4.cu).
 constexpr int kRows4Warps = 8;
@@ -214,6 +229,7 @@ struct Rows4Params {
     int n_heads, group;
     float scale_log2;
     int causal, window;
+    int most_tokens;  // sequences with more new tokens are another kernel's
     // partial results that CTAs hand one another: [grid][2] of 8 * row_tiles rows of D
     // floats, then as many (maximum, sum) pairs; arrivals[grid] is zero between calls
     float* part;

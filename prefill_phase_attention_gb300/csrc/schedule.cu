@@ -36,6 +36,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
     const int tid = threadIdx.x;
     const int nthr = blockDim.x;
     const int tpu = a.unit_slots * (kBlockM / a.group);  // query tokens per unit
+    auto query_blocks = [&](int n) { return n > a.few_tokens ? (n + tpu - 1) / tpu : 0; };
     // the next kernel (launched with programmatic stream serialisation) may
     // start its prologue now; it waits for this kernel before reading the list
     griddep_launch();
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
             si.n = ok ? (int)n : 0;
             si.P = ok ? P : 0;
         }
-        const int nblk = (si.n + tpu - 1) / tpu;
+        const int nblk = query_blocks(si.n);
         int chunk_total;
         const int excl = block_exclusive_scan(nblk, warp_sums, &chunk_total);
         si.pad = blocks_before + excl;
@@ -111,7 +112,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
         const int lane = tid & 31, nwarps = nthr >> 5;
         for (int b = tid >> 5; b < a.num_seqs; b += nwarps) {
             const SeqInfo si = seqs[b];
-            const int nblk = (si.n + tpu - 1) / tpu;
+            const int nblk = query_blocks(si.n);
             long long c = 0;
             int mx = 0;
             for (int i = lane; i < nblk; i += 32) {
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
 
     // Pass 3: each sequence claims its range of the list from its bin ...
     for (int b = tid; b < a.num_seqs; b += nthr) {
-        const int nblk = (seqs[b].n + tpu - 1) / tpu;
+        const int nblk = query_blocks(seqs[b].n);
         if (nblk > 0) seq_scratch[b] = atomicAdd(&hist[seq_scratch[b]], nblk * a.n_kv_heads);
     }
     __threadfence_block();
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
         const int b = block_owner(seqs, a.num_seqs, i);
         const SeqInfo si = seqs[b];
         const int blk = i - si.pad;
-        const int nblk = (si.n + tpu - 1) / tpu;
+        const int nblk = query_blocks(si.n);
         const int hg = seq_group[b];
         const int g0 = kvh - kvh % hg;                 // first head of kvh's group
         const int gsize = min(hg, a.n_kv_heads - g0);  // heads in the group

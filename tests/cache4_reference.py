@@ -22,7 +22,7 @@ U = 2.0 ** -8
 def quantise(x, group):
     """(codes uint8 [..., d / 2], params bf16 [..., d / group, 2]) of bf16 rows x, by the format's steps in fp32."""
     y = x.float().unflatten(-1, (-1, group))
-    lo, hi = y.amin(-1), y.amax(-1)
+    lo, hi = y.amin(-1) + 0.0, y.amax(-1)                     # (0 for -0)
     s = ((hi - lo) * torch.tensor(1.0 / 15.0)).to(torch.bfloat16)
     s = torch.where(s.float() >= 2.0 ** -126, s, torch.zeros_like(s))
     r = torch.where(s > 0, torch.ones(()) / s.float(), torch.zeros(()))

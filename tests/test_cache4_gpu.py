@@ -129,6 +129,38 @@ def test_drafts(d, group, new, lens):
         c.check()
 
 
+@pytest.mark.parametrize("block", [0, 8, 128])
+@pytest.mark.parametrize("d,group", DIMS)
+def test_chunks(d, group, block):
+    """Chunks long enough for the tile kernel, decode rows and drafts beside them."""
+    c = Call(11, [300, 1, 129, 4, 0, 200], [0, 500, 127, 33, 9, 260], d, group=group, block=block, share=2)
+    c.attend()
+    c.check(tiles=True)
+
+
+@pytest.mark.parametrize("new,past,hk,share", [(9, 200, 2, 4), (40, 3, 1, 1), (64, 128, 1, 3), (513, 1000, 4, 4), (130, 0, 3, 16),
+                                               (257, 129, 2, 1)])
+@pytest.mark.parametrize("block", [0, 32])
+def test_one_chunk(new, past, hk, share, block):
+    c = Call(12, [new], [past], hk=hk, share=share, group=64, block=block)
+    c.attend()
+    c.check(tiles=True)
+
+
+@pytest.mark.parametrize("window", [1, 100, 128, 300])
+@pytest.mark.parametrize("block", [0, 16])
+def test_chunks_under_windows(window, block):
+    c = Call(13, [260, 1, 150], [400, 300, 10], group=32, block=block)
+    c.attend(window=window)
+    c.check(window=window, tiles=True)
+
+
+def test_chunks_with_all_keys_visible():
+    c = Call(14, [260, 1, 150], [100, 300, 10], group=128)
+    c.attend(causal=False)
+    c.check(causal=False, tiles=True)
+
+
 @pytest.mark.parametrize("window", [1, 2, 31, 32, 33, 100, 5000])
 @pytest.mark.parametrize("block", [0, 16])
 def test_windows(window, block):
@@ -178,10 +210,11 @@ def test_equal_inputs_give_equal_bits():
 
 
 @pytest.mark.parametrize("block", [0, 16])
-def test_rotary(block):
+@pytest.mark.parametrize("new", [[1, 4, 1], [1, 200, 140]])
+def test_rotary(block, new):
     """The attention call's rotary embedding: q and the cached key as a call on rotated tensors has them."""
     theta = 10000.0
-    c = Call(10, [1, 4, 1], [100, 257, 0], group=64, block=block)
+    c = Call(10, new, [100, 257, 0], group=64, block=block)
     c.attend(rope_theta=theta)
     rot = [torch.empty_like(x) for x in (c.q, c.k)]
     for b, p in enumerate(c.lens):
@@ -189,7 +222,7 @@ def test_rotary(block):
         pos = p + torch.arange(c.new[b])
         for x, y in zip((c.q, c.k), rot):
             y[rows] = R.rotate(x[rows], pos, theta).to(torch.bfloat16)
-    e = Call(10, [1, 4, 1], [100, 257, 0], group=64, block=block)
+    e = Call(10, new, [100, 257, 0], group=64, block=block)
     e.q, e.k = rot
     e.dev[:2] = [x.cuda() for x in rot]
     e.attend()
@@ -199,7 +232,7 @@ def test_rotary(block):
     a, b = c.out[1].double().cpu(), e.out[1].double().cpu()
     assert (a - b).abs().max() <= 8 * R.U * b.abs().max()
     # the call's own write and prefill_attn_cache4_write rotate alike
-    w = Call(10, [1, 4, 1], [100, 257, 0], group=64, block=block)
+    w = Call(10, new, [100, 257, 0], group=64, block=block)
     w.write(rope_theta=theta)
     for which in range(2):
         assert same_bits(w.codes[which][1], c.codes[which][1]) and same_bits(w.params[which][1], c.params[which][1])
@@ -310,6 +343,19 @@ def test_bad_sequences_are_skipped():
     torch.cuda.synchronize()
     assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
     assert e.out[1][1].isnan().all() and not e.out[1][0].isnan().any()
+
+
+def test_bad_chunks_are_skipped():
+    c = Call(35, [200, 150, 1], [40, 20, 70], block=16)
+    c.opts["block_table"][1, 1] = c.cache.codes[0].shape[0]
+    c.attend()
+    torch.cuda.synchronize()
+    assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+    out, _, bound, _ = R.attention(c.cache, c.q, c.k, c.v, c.cu, c.lens, c.scale, tiles=True)
+    got = c.out[1].double().cpu()
+    assert got[200:350].isnan().all()
+    for rows in (slice(0, 200), slice(350, 351)):
+        assert ((got[rows] - out[rows]).abs() <= bound[rows]).all()
 
 
 def test_captured_calls_read_their_metadata_at_replay():
