@@ -539,20 +539,23 @@ __device__ __forceinline__ void load_params4(const FwdParams& p, const uint32_t*
                                              int lane, uint32_t (&w)[Tile4<D>::kBatches]) {
     using T = Tile4<D>;
     const int group = (lane % T::kLanes) * p.groups / T::kLanes;
-    const int32_t* tab = p.block_table + (size_t)u.b * p.max_blocks;
-    const size_t row0 = ((size_t)u.b * p.n_kv_heads + u.kvh) * p.max_cache_len;
+    const size_t head0 = (size_t)u.b * p.n_kv_heads + u.kvh;
+    int id = -1;  // paged: the block of rows [8 lane, 8 lane + 8)
+    if (kPaged && lane < kBlockN / 8 && kb + 8 * lane < P)
+        id = __ldg(p.block_table + (size_t)u.b * p.max_blocks + ((kb + 8 * lane) >> p.block_log2));
 #pragma unroll
     for (int i = 0; i < T::kBatches; ++i) {
-        const int pos = kb + i * T::kRows + lane / T::kLanes;
-        w[i] = 0;
-        if (pos < 0 || pos >= P) continue;
-        size_t row = row0 + pos;
+        const int r = i * T::kRows + lane / T::kLanes, pos = kb + r;
+        bool there = pos >= 0 && pos < P;
+        size_t row;
         if (kPaged) {
-            const int blk = __ldg(tab + (pos >> p.block_log2));
-            if ((unsigned)blk >= (unsigned)p.num_blocks) continue;
+            const int blk = __shfl_sync(0xffffffffu, id, r >> 3);
+            there = there && (unsigned)blk < (unsigned)p.num_blocks;
             row = (((size_t)blk * p.n_kv_heads + u.kvh) << p.block_log2) + (pos & ((1 << p.block_log2) - 1));
+        } else {
+            row = head0 * p.max_cache_len + pos;
         }
-        w[i] = __ldg(params + row * p.groups + group);
+        w[i] = there ? __ldg(params + row * p.groups + group) : 0u;
     }
 }
 
@@ -564,14 +567,16 @@ __device__ __forceinline__ void load_params4(const FwdParams& p, const uint32_t*
 // at 2 D (r + 1) of the stage (its last column chunk's share of it), the codes of row r + 1
 // start at 1.5 D 128 + D (r + 1) / 2, never before it.
 template <int D>
-__device__ __forceinline__ void expand_tile4(uint8_t* stage, const uint32_t (&w)[Tile4<D>::kBatches], int lane) {
+__device__ __forceinline__ void expand_tile4(uint8_t* stage, uint32_t (&w)[Tile4<D>::kBatches], int lane) {
     using C = Cfg<D>;
     using T = Tile4<D>;
-    constexpr int kGroup = T::kBatches < 4 ? T::kBatches : 4;  // batches read before any is written
+    constexpr int kGroup = 4;  // batches read before any is written
     constexpr int kChunkGran = C::kChunkCols / 8;
     const uint8_t* codes = stage + C::kTileBytes - kBlockN * (D / 2);
     const int part = lane % T::kLanes;
-#pragma unroll
+    // a short loop (unrolled whole it takes five times as long: a warp that runs every
+    // instruction once waits for each to be fetched); the words move up by a group a pass
+#pragma unroll 1
     for (int i0 = 0; i0 < T::kBatches; i0 += kGroup) {
         uint4 x[kGroup];
 #pragma unroll
@@ -582,7 +587,7 @@ __device__ __forceinline__ void expand_tile4(uint8_t* stage, const uint32_t (&w)
         for (int b = 0; b < kGroup; ++b) {
             const int r = (i0 + b) * T::kRows + lane / T::kLanes;
             const uint32_t word[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
-            const uint32_t s2 = __byte_perm(w[i0 + b], 0, 0x1010), m2 = __byte_perm(w[i0 + b], 0, 0x3232);
+            const uint32_t s2 = __byte_perm(w[b], 0, 0x1010), m2 = __byte_perm(w[b], 0, 0x3232);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 // channels 32 part + 8 q ...: pairs (i, i + 4), put in order below
@@ -604,6 +609,8 @@ __device__ __forceinline__ void expand_tile4(uint8_t* stage, const uint32_t (&w)
                                __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
             }
         }
+#pragma unroll
+        for (int i = 0; i + kGroup < T::kBatches; ++i) w[i] = w[i + kGroup];
         __syncwarp();
     }
 }
@@ -1390,31 +1397,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             bool ok = true;
             // 4-bit cache: the parameters of the unit's next prefix tile, fetched while the one
             // before is expanded
-            uint32_t next4[kQ4 ? Tile4<D>::kBatches : 1];
+            uint32_t next4[kQ4 ? Tile4<D>::kBatches : 1] = {};
             auto fetch4 = [&](int j) {
                 if constexpr (kQ4)
                     if (j < np)
                         load_params4<D, kPaged>(p, is_k ? p.params_k : p.params_v, us.u, tile_key_base<kPaged>(j, us.s.P, np),
                                                 us.s.P, lane, next4);
             };
-            if (kQ4 && ug.ntiles > 0) fetch4(tile_at(ug, 0));
-            for (int jr = 0; jr < ug.ntiles; ++jr, ++t) {
-                const int j = tile_at(ug, jr);  // tile index in the sequence
+            for (int jr = kQ4 ? -1 : 0; jr < ug.ntiles; ++jr, ++t) {
+                const int j = jr < 0 ? 0 : tile_at(ug, jr);  // tile index in the sequence
                 const int st = t % stages;
-                if constexpr (kQ4) if (j < np) {
+                if constexpr (kQ4) {
                     uint32_t w[Tile4<D>::kBatches];
 #pragma unroll
                     for (int i = 0; i < Tile4<D>::kBatches; ++i) w[i] = next4[i];
                     if (jr + 1 < ug.ntiles) fetch4(tile_at(ug, jr + 1));
-                    if (!warp_wait(&full[st], (t / stages) & 1, ctl, hdr)) { ok = false; break; }
-                    expand_tile4<D>(ring + st * C::kTileBytes, w, lane);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(is_k ? &ctl->k_conv[st] : &ctl->v_conv[st]);
-                        mbar_arrive(&empty[st]);
+                    if (jr < 0) {
+                        --t;  // (no tile yet)
+                        continue;
                     }
-                    continue;
+                    if (j < np) {
+                        if (!warp_wait(&full[st], (t / stages) & 1, ctl, hdr)) { ok = false; break; }
+                        expand_tile4<D>(ring + st * C::kTileBytes, w, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(is_k ? &ctl->k_conv[st] : &ctl->v_conv[st]);
+                            mbar_arrive(&empty[st]);
+                        }
+                        continue;
+                    }
                 }
                 if (kQ8 && j < np) {
                     // int8 prefix tile: expand the codes for the MMA.  V rows
