@@ -38,42 +38,49 @@ namespace pa {
 
 namespace rows4 {
 
-constexpr int kWarps = kRows4Warps;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kTileKeys = 32;  // cached rows of a tile
 constexpr int kNewKeys = 8;    // new tokens of a tile
 
 template <int D, int NG, int NQ>
 struct Cfg {
+    // As many warps as registers (NQ = 1: 168 a thread) and shared memory allow: the
+    // instructions of a tile take most of the time that its bytes do, so the issue slots
+    // have to be filled.
+    static constexpr int kWarps = NQ == 2 ? 8 : NG == 4 ? 10 : 12;
+    static constexpr int kThreads = 32 * kWarps;
     static constexpr int kChunks = D / 32;
     static constexpr int kRowBytes = D / 2;
     static constexpr int kCodes = kTileKeys * kRowBytes;     // bytes of a tile's codes
     static constexpr int kParams = kTileKeys * NG * 4;       // bytes of a tile's parameters
     static constexpr int kTileBytes = 2 * (kCodes + kParams);
-    static constexpr int kStages = NQ == 2 && D == 128 ? 3 : 4;
+    static constexpr int kStages = D == 128 ? 3 : 4;
     static constexpr int kRows = 8 * NQ;
     static constexpr int kRecord = kRows * D * 4;  // bytes of a partial output
     static_assert(kStages * kTileBytes >= kRecord, "a warp's second record lies in its ring");
 };
 
-// What a warp needs to know of a tile in its ring.
-struct Tile {
-    int key;  // first position of a cached tile (row of the cache); new tokens: -1 - index of the first
-    int b, kvh, block;
+// A row block in a warp's share.
+struct Item {
     SeqInfo s;
-    int flags;
-    int start_hi, start_lo;  // list position of the row block's first tile
-    int tiles;               // its tiles
+    int b, kvh, block;
+    int tiles;                // of the row block
+    int start_hi, start_lo;   // list position of its first
+};
+// What a warp needs to know of a tile in its ring: the first position of a cached tile, or
+// -1 - the index of the first new token; its item's slot (bits 8 on) and the flags.
+struct Tile {
+    int key, flags;
 };
 enum : int {
     kFirst = 1,      // of the row block, in this warp
     kLast = 2,       // of the row block, in this warp
     kFromBefore = 4, // the row block began before this warp's share
     kGoesOn = 8,     // and ends after it
+    kSlot = 8,       // shift
 };
 
 struct Record {
-    Tile t;
+    Item t;
     int valid;
 };
 
@@ -97,6 +104,14 @@ __device__ __forceinline__ Extent extent(const Rows4Params& p, const SeqInfo& s)
     return e;
 }
 
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes) : "memory");
+}
+// The same, or zeros.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool read) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(read ? 16 : 0) : "memory");
 }
@@ -140,6 +155,13 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// max of three (one instruction on sm_100+)
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 __device__ __forceinline__ float log2_approx(float x) {
     float y;
     asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -167,14 +189,14 @@ __device__ __forceinline__ int swizzle(int key) {  // of a row's 16-byte parts
 
 // Partial result of a row block: rows [8 NQ] x (maximum, sum) and the unnormalised output.
 template <int D, int NQ>
-__device__ __forceinline__ void store_row(const Rows4Params& p, const Tile& t, int row, int d, float4 o) {
+__device__ __forceinline__ void store_row(const Rows4Params& p, const Item& t, int row, int d, float4 o) {
     const int r = t.block * 8 * NQ + row;
     if (r >= t.s.n * p.group) return;
     const size_t at = ((size_t)(t.s.q_start + r / p.group) * p.n_heads + t.kvh * p.group + r % p.group) * D + d;
     *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
 }
 template <int NQ>
-__device__ __forceinline__ void store_lse(const Rows4Params& p, const Tile& t, int row, float m, float l) {
+__device__ __forceinline__ void store_lse(const Rows4Params& p, const Item& t, int row, float m, float l) {
     const int r = t.block * 8 * NQ + row;
     if (!p.lse || r >= t.s.n * p.group) return;
     p.lse[(size_t)(t.s.q_start + r / p.group) * p.n_heads + t.kvh * p.group + r % p.group] =
@@ -185,25 +207,37 @@ __device__ __forceinline__ void store_lse(const Rows4Params& p, const Tile& t, i
 template <int D, int NG, int NQ>
 struct Feeder {
     using C = Cfg<D, NG, NQ>;
+    static constexpr int kParts = C::kRowBytes / 16;  // 16-byte parts of a row
+    static constexpr int kPassRows = 32 / kParts;     // rows that the lanes copy at once
     const Rows4Params& p;
     const SeqInfo* table;  // in shared memory, or nullptr
     uint32_t ring;
+    Item* items;
     Tile* tiles;
     int lane;
-    int b, item, j;  // sequence, row block of it (KV head major), tile of that
+    int left;            // tiles of the share that are still to come
+    int b, kvh, block;   // row block: sequence, KV head, block of rows
+    int key, cached_end; // next tile if it is cached; where those end
+    int fresh;           // new tokens' tiles of the row block that came
     SeqInfo s;
     Extent e;
-    long long at, end, block_start;  // list positions
-    int ids, next_ids;               // paged: blocks of the 8-row pieces of this and the next 256 positions
+    long long block_start;  // list position of the row block's first tile
+    // this lane's first part of the next cached tile (contiguous cache)
+    const uint8_t* kc;
+    const uint8_t* vc;
+    const uint32_t* kp;
+    const uint32_t* vp;
+    int ids, next_ids;  // paged: blocks of the 8-row pieces of this and the next 256 positions
+    int slot, flags;    // of the row block: its slot of `items`, kFirst and kFromBefore
 
     __device__ __forceinline__ SeqInfo seq(int i) const {
         return table ? table[i] : sequence4(p.seqs, p.cache.max_cache_len, i);
     }
     // Puts the feeder at list position `first`; `start` is that of sequence b0.
-    __device__ __forceinline__ void seek(int b0, long long start, long long first, long long last) {
-        at = first;
-        end = last;
-        if (at >= end) return;
+    __device__ __forceinline__ void seek(int b0, long long start, long long first, int count) {
+        left = count;
+        slot = -1;
+        if (left == 0) return;
         b = b0;
         s = seq(b);
         e = extent<NQ>(p, s);
@@ -216,133 +250,164 @@ struct Feeder {
             e = extent<NQ>(p, s);
         }
         const long long in = first - start;
-        item = (int)(in / e.tiles());
-        j = (int)(in % e.tiles());
+        const int item = (int)(in / e.tiles()), j = (int)(in % e.tiles());
+        kvh = item / e.blocks;
+        block = item % e.blocks;
         block_start = first - j;
-        if (p.cache.block_table) load_ids(true);
+        enter(j);
     }
-    __device__ __forceinline__ int id_of(int window) const {
-        const int pos = window * 256 + lane * 8;
-        if (pos >= s.P) return -1;
-        return __ldg(p.cache.block_table + (size_t)b * p.cache.max_blocks + (pos >> p.cache.block_log2));
-    }
-    __device__ __forceinline__ void load_ids(bool fresh) {
-        const int key = (e.first_tile + j) * kTileKeys, window = key >> 8;
-        if (fresh) {
-            ids = id_of(window);
-            next_ids = id_of(window + 1);
-        } else if ((key & 255) == 0) {
-            ids = next_ids;
-            next_ids = id_of(window + 1);
+    // Begins a row block at its tile j.
+    __device__ __forceinline__ void enter(int j) {
+        key = (e.first_tile + min(j, e.cached)) * kTileKeys;
+        cached_end = (e.first_tile + e.cached) * kTileKeys;
+        fresh = max(0, j - e.cached);
+        flags = kFirst | (j > 0 ? kFromBefore : 0);
+        slot = slot + 1 == C::kStages ? 0 : slot + 1;
+        if (lane == 0) items[slot] = Item{s, b, kvh, block, e.tiles(), (int)(block_start >> 32), (int)block_start};
+        if (p.cache.block_table) {
+            ids = id_of(key >> 8);
+            next_ids = id_of((key >> 8) + 1);
+        } else {
+            const size_t row = ((size_t)b * p.cache.n_kv_heads + kvh) * p.cache.max_cache_len + key;
+            const size_t at = (row + lane / kParts) * C::kRowBytes + lane % kParts * 16;
+            kc = p.cache.k + at;
+            vc = p.cache.v + at;
+            kp = p.cache.kp + (row + lane) * NG;
+            vp = p.cache.vp + (row + lane) * NG;
         }
     }
+    // The block of the lane's 8-row piece (of a checked table: the bounds keep a stray entry
+    // from becoming a stray read).
+    __device__ __forceinline__ int id_of(int window) const {
+        const int pos = window * 256 + lane * 8;
+        if (pos >= s.P) return 0;
+        const int id = __ldg(p.cache.block_table + (size_t)b * p.cache.max_blocks + (pos >> p.cache.block_log2));
+        return (int)min((unsigned)id, (unsigned)p.cache.num_blocks - 1);
+    }
+    // paged: the pool's row of the tile's row r
+    __device__ __forceinline__ size_t pool_row(int r) const {
+        const int id = __shfl_sync(0xffffffffu, ids, ((key & 255) >> 3) + (r >> 3));
+        return ((size_t)(unsigned)(id * p.cache.n_kv_heads + kvh) << p.cache.block_log2) +
+               ((key + r) & ((1 << p.cache.block_log2) - 1));
+    }
     __device__ __forceinline__ void issue(int stage) {
-        if (at < end) {
-            const uint32_t dst = ring + stage * C::kTileBytes;
-            const int kvh = item / e.blocks, block = item % e.blocks;
-            const bool cached = j < e.cached;
-            if (lane == 0) {
-                Tile t;
-                t.key = cached ? (e.first_tile + j) * kTileKeys : -1 - (j - e.cached) * kNewKeys;
-                t.b = b;
-                t.kvh = kvh;
-                t.block = block;
-                t.s = s;
-                t.flags = 0;
-                t.start_hi = (int)(block_start >> 32);
-                t.start_lo = (int)block_start;
-                t.tiles = e.tiles();
-                tiles[stage] = t;
-            }
-            if (cached) {
-                const int key0 = (e.first_tile + j) * kTileKeys;
-                const size_t row0 = p.cache.block_table ? 0
-                                                        : ((size_t)b * p.cache.n_kv_heads + kvh) * p.cache.max_cache_len + key0;
-                const int bmask = (1 << p.cache.block_log2) - 1, piece0 = (key0 & 255) >> 3;
-                // row of the tile's key (0: none, `read` false)
-                auto row_of = [&](int key, bool& read) -> size_t {
-                    read = key0 + key < s.P;
-                    if (!p.cache.block_table) return read ? row0 + key : 0;
-                    const int id = __shfl_sync(0xffffffffu, ids, (piece0 + (key >> 3)) & 31);
-                    read = read && (unsigned)id < (unsigned)p.cache.num_blocks;
-                    return read ? (((size_t)id * p.cache.n_kv_heads + kvh) << p.cache.block_log2) + ((key0 + key) & bmask) : 0;
-                };
-                constexpr int kParts = C::kRowBytes / 16;
+        if (left > 0) {
+            const uint32_t base = ring + stage * C::kTileBytes;
+            const uint32_t dst = base + lane / kParts * C::kRowBytes + (lane % kParts ^ swizzle<D>(lane / kParts)) * 16;
+            const uint32_t params = base + 2 * C::kCodes + lane * NG * 4;
+            const int at = key < cached_end ? key : -1 - fresh * kNewKeys;
+            if (at >= 0) {
+                // (the swizzle is the same for rows a pass apart)
+                if (key + kTileKeys <= s.P) {
+                    if (!p.cache.block_table) {
 #pragma unroll
-                for (int it = 0; it < kParts; ++it) {
-                    const int key = it * (32 / kParts) + lane / kParts, part = lane % kParts;
-                    bool read;
-                    const size_t row = row_of(key, read);
-                    const uint32_t to = dst + key * C::kRowBytes + (part ^ swizzle<D>(key)) * 16;
-                    const size_t from = row * C::kRowBytes + part * 16;
-                    cp_async16(to, p.cache.k + from, read);
-                    cp_async16(to + C::kCodes, p.cache.v + from, read);
-                }
-                bool read;
-                const size_t row = row_of(lane, read);
-                const uint32_t to = dst + 2 * C::kCodes + lane * NG * 4;
-                if constexpr (NG == 4) {
-                    cp_async16(to, p.cache.kp + row * NG, read);
-                    cp_async16(to + C::kParams, p.cache.vp + row * NG, read);
+                        for (int it = 0; it < kParts; ++it) {
+                            cp_async16(dst + it * 512, kc + it * 512);
+                            cp_async16(dst + C::kCodes + it * 512, vc + it * 512);
+                        }
+                        if constexpr (NG == 4) {
+                            cp_async16(params, kp);
+                            cp_async16(params + C::kParams, vp);
+                        } else {
+                            cp_async_small<NG * 4>(params, kp);
+                            cp_async_small<NG * 4>(params + C::kParams, vp);
+                        }
+                        kc += C::kCodes;
+                        vc += C::kCodes;
+                        kp += kTileKeys * NG;
+                        vp += kTileKeys * NG;
+                    } else {
+#pragma unroll
+                        for (int it = 0; it < kParts; ++it) {
+                            const size_t from = pool_row(it * kPassRows + lane / kParts) * C::kRowBytes + lane % kParts * 16;
+                            cp_async16(dst + it * 512, p.cache.k + from);
+                            cp_async16(dst + C::kCodes + it * 512, p.cache.v + from);
+                        }
+                        const size_t row = pool_row(lane) * NG;
+                        if constexpr (NG == 4) {
+                            cp_async16(params, p.cache.kp + row);
+                            cp_async16(params + C::kParams, p.cache.vp + row);
+                        } else {
+                            cp_async_small<NG * 4>(params, p.cache.kp + row);
+                            cp_async_small<NG * 4>(params + C::kParams, p.cache.vp + row);
+                        }
+                    }
                 } else {
-                    cp_async_small<NG * 4>(to, p.cache.kp + row * NG, read);
-                    cp_async_small<NG * 4>(to + C::kParams, p.cache.vp + row * NG, read);
+                    // the last cached tile: zeros past the sequence's cached rows
+                    const size_t row0 = ((size_t)b * p.cache.n_kv_heads + kvh) * p.cache.max_cache_len + key;
+#pragma unroll 1
+                    for (int it = 0; it < kParts; ++it) {
+                        const int r = it * kPassRows + lane / kParts;
+                        const bool read = key + r < s.P;
+                        const size_t row = p.cache.block_table ? pool_row(r) : row0 + r;
+                        const size_t from = (read ? row : 0) * C::kRowBytes + lane % kParts * 16;
+                        cp_async16(dst + it * 512, p.cache.k + from, read);
+                        cp_async16(dst + C::kCodes + it * 512, p.cache.v + from, read);
+                    }
+                    const bool read = key + lane < s.P;
+                    const size_t row = p.cache.block_table ? pool_row(lane) : row0 + lane;
+                    const size_t from = (read ? row : 0) * NG;
+                    if constexpr (NG == 4) {
+                        cp_async16(params, p.cache.kp + from, read);
+                        cp_async16(params + C::kParams, p.cache.vp + from, read);
+                    } else {
+                        cp_async_small<NG * 4>(params, p.cache.kp + from, read);
+                        cp_async_small<NG * 4>(params + C::kParams, p.cache.vp + from, read);
+                    }
+                }
+                key += kTileKeys;
+                if (p.cache.block_table && (key & 255) == 0) {
+                    ids = next_ids;
+                    next_ids = id_of((key >> 8) + 1);
                 }
             } else {
-                const int tok0 = (j - e.cached) * kNewKeys;
-                constexpr int kParts = D / 8;  // 16-byte parts of a bf16 row
-#pragma unroll
-                for (int it = 0; it < kParts * kNewKeys / 32; ++it) {
-                    const int at_ = it * 32 + lane, key = at_ / kParts, part = at_ % kParts;
-                    const bool read = tok0 + key < s.n;
-                    const size_t from = ((size_t)(s.q_start + (read ? tok0 + key : 0)) * p.cache.n_kv_heads + kvh) * D + part * 8;
-                    cp_async16(dst + at_ * 16, p.k + from, read);
-                    cp_async16(dst + C::kCodes + at_ * 16, p.v + from, read);
+                constexpr int kNewParts = D / 8;  // 16-byte parts of a bf16 row
+#pragma unroll 1
+                for (int it = 0; it < kNewParts * kNewKeys / 32; ++it) {
+                    const int x = it * 32 + lane, tok = fresh * kNewKeys + x / kNewParts;
+                    const bool read = tok < s.n;
+                    const size_t from =
+                        ((size_t)(s.q_start + (read ? tok : 0)) * p.cache.n_kv_heads + kvh) * D + x % kNewParts * 8;
+                    cp_async16(base + x * 16, p.k + from, read);
+                    cp_async16(base + C::kCodes + x * 16, p.v + from, read);
                 }
+                ++fresh;
             }
-            // onwards
-            ++at;
-            const bool block_ends = j + 1 == e.tiles();
-            if (lane == 0) {
-                int f = 0;
-                if (at - 1 == block_start || first_of_share) f |= kFirst;
-                if (first_of_share && at - 1 != block_start) started_before = true;
-                if (started_before) f |= kFromBefore;
-                if (block_ends || at == end) f |= kLast;
-                if (!block_ends && at == end) f |= kGoesOn;
-                tiles[stage].flags = f;
-                if (block_ends) started_before = false;
-            }
-            first_of_share = false;
-            if (!block_ends) {
-                ++j;
-                if (p.cache.block_table) load_ids(false);
-            } else if (at < end) {
-                j = 0;
-                block_start = at;
-                if (++item == e.blocks * p.cache.n_kv_heads) {
-                    item = 0;
-                    do {
-                        ++b;
-                        s = seq(b);
-                        e = extent<NQ>(p, s);
-                    } while (e.blocks == 0);
+            --left;
+            const bool ends = fresh == e.fresh;
+            int f = flags | slot << kSlot;
+            if (ends || left == 0) f |= ends ? kLast : kLast | kGoesOn;
+            if (lane == 0) tiles[stage] = Tile{at, f};
+            flags &= ~kFirst;
+            if (ends && left > 0) {
+                block_start += e.tiles();
+                if (++block == e.blocks) {
+                    block = 0;
+                    if (++kvh == p.cache.n_kv_heads) {
+                        kvh = 0;
+                        do {
+                            ++b;
+                            s = seq(b);
+                            e = extent<NQ>(p, s);
+                        } while (e.blocks == 0);
+                    }
                 }
-                if (p.cache.block_table) load_ids(true);
+                enter(0);
             }
         }
         cp_async_commit();
     }
-    bool first_of_share = true, started_before = false;
 };
 
 template <int D, int NG, int NQ>
-__global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Params p) {
+__global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel(const Rows4Params p) {
     using C = Cfg<D, NG, NQ>;
+    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     constexpr int kGroupChunks = C::kChunks / NG;  // 32-channel chunks of a group
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ SeqInfo table[kRows4Seqs];
-    __shared__ Tile tile_info[kWarps][C::kStages];
+    __shared__ Item items[kWarps][C::kStages];
+    __shared__ Tile tiles[kWarps][C::kStages];
     __shared__ Record records[kWarps][2];
     __shared__ float2 stats[kWarps][2][C::kRows];  // (maximum, sum) of a record's rows
     __shared__ long long warp_sums[kWarps];
@@ -411,34 +476,36 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
     uint8_t* const ring = smem + warp * C::kStages * C::kTileBytes;
     float* const kept = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kTileBytes + warp * C::kRecord);
     const long long len = to - from;
-    Feeder<D, NG, NQ> feed{p, in_table ? table : nullptr, ptx::smem_u32(ring), tile_info[warp], lane};
     const long long wfrom = from + len * warp / kWarps, wto = from + len * (warp + 1) / kWarps;
-    feed.seek(first_seq, start_of_first, wfrom, wto);
-    const int steps = (int)min(wto - wfrom, (long long)INT_MAX);
+    const int steps = (int)(wto - wfrom);  // (2^31 tiles of a warp would take an hour)
+    Feeder<D, NG, NQ> feed{p, in_table ? table : nullptr, ptx::smem_u32(ring), items[warp], tiles[warp], lane};
+    feed.seek(first_seq, start_of_first, wfrom, steps);
 #pragma unroll
     for (int i = 0; i < C::kStages - 1; ++i) feed.issue(i);
 
     uint32_t qf[NQ][C::kChunks][4];  // Q as the second operand: per chunk two 16-channel steps
-    float qsum[NQ][NG][2];           // sums of a group's channels of queries 2 t4, 2 t4 + 1
+    float2 qsum[NQ][NG];             // sums of a group's channels of queries 2 t4, 2 t4 + 1
     float o[NQ][C::kChunks][2][4];   // O^T: channels 32 c + 4 g + 2 e (+ 1), queries 2 t4, 2 t4 + 1
-    float om[NQ][NG][2];             // sum of p (m + 8 s) over this lane's keys
-    float m[NQ][2], l[NQ][2];        // running maximum (log2 units), sum over this lane's keys
-    int hi[NQ][2], lo[NQ][2];        // keys [lo, hi] are visible
-    int lo_most = 0;                 // largest lo
+    float2 om[NQ][NG];               // sum of p (m + 8 s) over this lane's keys
+    float2 l[NQ];                    // sum of p over this lane's keys
+    float2 neg[NQ], most[NQ];        // less the running maximum m (log2 units; 0 before any key), (m + 8) / scale
+    int P = 0, lo_most = 0;          // cached keys; the largest first visible key of a row
 
+    const float unscale = 1.f / p.scale_log2;
     int stage = 0;
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
         cp_async_wait<C::kStages - 2>();
         __syncwarp();
         feed.issue(stage == 0 ? C::kStages - 1 : stage - 1);
-        const Tile& t = tile_info[warp][stage];
-        const int flags = t.flags, key = t.key;
-        const SeqInfo s = t.s;
+        const int flags = tiles[warp][stage].flags, key = tiles[warp][stage].key;
+        const Item& t = items[warp][flags >> kSlot];
         const uint8_t* const tile = ring + stage * C::kTileBytes;
         const uint32_t tile_u32 = ptx::smem_u32(tile);
 
         if (flags & kFirst) {
+            const SeqInfo s = t.s;
+            P = s.P;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 const int r = t.block * C::kRows + 8 * n + g;
@@ -463,62 +530,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
                 for (int a = 0; a < NG; ++a) {
                     sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 1);
                     sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 2);  // of query g
-                    qsum[n][a][0] = __shfl_sync(0xffffffffu, sum[a], 8 * t4);
-                    qsum[n][a][1] = __shfl_sync(0xffffffffu, sum[a], 8 * t4 + 4);
-                    om[n][a][0] = om[n][a][1] = 0.f;
+                    qsum[n][a].x = __shfl_sync(0xffffffffu, sum[a], 8 * t4);
+                    qsum[n][a].y = __shfl_sync(0xffffffffu, sum[a], 8 * t4 + 4);
+                    om[n][a] = make_float2(0.f, 0.f);
                 }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int tok = min((t.block * C::kRows + 8 * n + 2 * t4 + e) / p.group, s.n - 1);
-                    hi[n][e] = p.causal ? s.P + tok : s.P + s.n - 1;
-                    lo[n][e] = p.causal && p.window > 0 ? s.P + tok - p.window + 1 : 0;
-                    m[n][e] = -INFINITY;
-                    l[n][e] = 0.f;
-                }
+                neg[n] = l[n] = make_float2(0.f, 0.f);
+                most[n] = both(-INFINITY);
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] = 0.f;
             }
-            const int last_tok = min((t.block * C::kRows + C::kRows - 1) / p.group, s.n - 1);
-            lo_most = p.causal && p.window > 0 ? s.P + last_tok - p.window + 1 : 0;
+            lo_most = 0;
+            if (p.causal && p.window > 0)
+                lo_most = s.P + min((t.block * C::kRows + C::kRows - 1) / p.group, s.n - 1) - p.window + 1;
         }
+        // keys [lo, hi] that row 8 n + 2 t4 + e sees
+        auto visible = [&](int n, int e, int& lo, int& hi) {
+            const int tok = min((t.block * C::kRows + 8 * n + 2 * t4 + e) / p.group, t.s.n - 1);
+            hi = p.causal ? P + tok : P + t.s.n - 1;
+            lo = p.causal && p.window > 0 ? P + tok - p.window + 1 : 0;
+        };
 
-        // running maximum of the scores x (log2 units) of a tile's keys: raised, with what was
-        // summed under it scaled, only when it falls behind by more than 2^8
-        auto raise = [&](float (&top)[NQ][2]) {
+        // The running maximum, from the largest score `top` of the lane's keys: it is raised, and
+        // what was summed under it scaled, only when it falls behind by more than 2^8.
+        auto raise = [&](const float2 (&top)[NQ]) {
             bool behind = false;
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) behind |= top[n][e] > m[n][e] + 8.f;
+            for (int n = 0; n < NQ; ++n) behind |= top[n].x > most[n].x || top[n].y > most[n].y;
             if (!__any_sync(0xffffffffu, behind)) return;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                float alpha[2];
+                float alpha[2], x[2] = {top[n].x, top[n].y};
+                const float was[2] = {most[n].x, most[n].y}, less[2] = {neg[n].x, neg[n].y};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float x = top[n][e];
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                    x = fmaxf(x, m[n][e]);
-                    alpha[e] = m[n][e] == -INFINITY ? 0.f : exp2_approx(m[n][e] - x);
-                    m[n][e] = x;
-                    l[n][e] *= alpha[e];
-#pragma unroll
-                    for (int a = 0; a < NG; ++a) om[n][a][e] *= alpha[e];
+                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 4));
+                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 8));
+                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16));
+                    x[e] *= p.scale_log2;
+                    const bool none = was[e] == -INFINITY;  // no key before
+                    if (!none) x[e] = fmaxf(x[e], -less[e]);
+                    alpha[e] = none || x[e] == -INFINITY ? 0.f : exp2_approx(-less[e] - x[e]);
                 }
+                l[n].x *= alpha[0], l[n].y *= alpha[1];
+#pragma unroll
+                for (int a = 0; a < NG; ++a) om[n][a].x *= alpha[0], om[n][a].y *= alpha[1];
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] *= alpha[e & 1];
+                if (x[0] != -INFINITY) neg[n].x = -x[0], most[n].x = (x[0] + 8.f) * unscale;
+                if (x[1] != -INFINITY) neg[n].y = -x[1], most[n].y = (x[1] + 8.f) * unscale;
             }
         };
 
         if (key >= 0) {
-            // ---- 32 cached keys: octet a of them in the matrix rows g of tile a / 2
-            float sc[NQ][4][2];  // scores of key 8 a + g, queries 2 t4 + e
+            // ---- 32 cached keys: octet k of them in the matrix rows g of half k / 2
+            float2 sc[NQ][4];  // scores of key 8 k + g, queries 2 t4 and 2 t4 + 1
             const uint32_t row_addr = tile_u32 + lane * C::kRowBytes;
             const uint32_t* kp = reinterpret_cast<const uint32_t*>(tile + 2 * C::kCodes) + g * NG;
             const uint32_t* vp = kp + kTileKeys * NG;
@@ -551,53 +620,55 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
                     const uint32_t w = kp[8 * k * NG + a];
                     const float sk = bf16_lo(w), mk = fmaf(8.f, sk, bf16_hi(w));
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const float prev = a == 0 ? mk * qsum[n][a][e] : fmaf(mk, qsum[n][a][e], sc[n][k][e]);
-                            sc[n][k][e] = fmaf(sk, acc[n][k / 2][2 * (k & 1) + e], prev);
-                        }
+                    for (int n = 0; n < NQ; ++n) {
+                        const float2 qc = make_float2(acc[n][k / 2][2 * (k & 1)], acc[n][k / 2][2 * (k & 1) + 1]);
+                        sc[n][k] = __ffma2_rn(both(sk), qc, a == 0 ? __fmul2_rn(both(mk), qsum[n][a])
+                                                                   : __ffma2_rn(both(mk), qsum[n][a], sc[n][k]));
+                    }
                 }
             }
-            float top[NQ][2];
-            const bool edge = key + kTileKeys > s.P || key < lo_most;
+            if (key + kTileKeys > P || key < lo_most) {
+                // an edge of the cached keys, or of a window
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    top[n][e] = -INFINITY;
+                for (int n = 0; n < NQ; ++n) {
+                    int lo[2], hi;
+                    visible(n, 0, lo[0], hi);
+                    visible(n, 1, lo[1], hi);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const int pos = key + 8 * k + g;
-                        float x = sc[n][k][e] * p.scale_log2;
-                        if (edge && (pos >= s.P || pos < lo[n][e])) x = -INFINITY;
-                        sc[n][k][e] = x;
-                        top[n][e] = fmaxf(top[n][e], x);
+                        if (pos >= P || pos < lo[0]) sc[n][k].x = -INFINITY;
+                        if (pos >= P || pos < lo[1]) sc[n][k].y = -INFINITY;
                     }
                 }
+            }
+            float2 top[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                top[n].x = fmaxf(max3(sc[n][0].x, sc[n][1].x, sc[n][2].x), sc[n][3].x);
+                top[n].y = fmaxf(max3(sc[n][0].y, sc[n][1].y, sc[n][2].y), sc[n][3].y);
+            }
             raise(top);
             uint32_t pt[NQ][NG][4];  // P^T scaled by the values' parameters, per octet
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float sv[NG], mv[NG];
+                float2 pr[NQ];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    const float2 x = __ffma2_rn(sc[n][k], both(p.scale_log2), neg[n]);
+                    pr[n] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                    l[n] = __fadd2_rn(l[n], pr[n]);
+                }
 #pragma unroll
                 for (int a = 0; a < NG; ++a) {
                     const uint32_t w = vp[8 * k * NG + a];
-                    sv[a] = bf16_lo(w);
-                    mv[a] = fmaf(8.f, sv[a], bf16_hi(w));
-                }
+                    const float sv = bf16_lo(w), mv = fmaf(8.f, sv, bf16_hi(w));
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    float pr[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        pr[e] = exp2_approx(sc[n][k][e] - (m[n][e] == -INFINITY ? 0.f : m[n][e]));
-                        l[n][e] += pr[e];
-#pragma unroll
-                        for (int a = 0; a < NG; ++a) om[n][a][e] = fmaf(pr[e], mv[a], om[n][a][e]);
+                    for (int n = 0; n < NQ; ++n) {
+                        om[n][a] = __ffma2_rn(pr[n], both(mv), om[n][a]);
+                        const float2 x = __fmul2_rn(pr[n], both(sv));
+                        pt[n][a][k] = movmatrix(pack(x.x, x.y));
                     }
-#pragma unroll
-                    for (int a = 0; a < NG; ++a) pt[n][a][k] = movmatrix(pack(pr[0] * sv[a], pr[1] * sv[a]));
                 }
             }
 #pragma unroll
@@ -619,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
             }
         } else {
             // ---- up to 8 new tokens, bf16: the matrix rows g of one tile
-            const int tok0 = -1 - key, tok = tok0 + g;
+            const int tok0 = -1 - key, tok = tok0 + g, many = t.s.n;
             float acc[NQ][4];
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -634,25 +705,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
                     mma(acc[n], __byte_perm(x.y, x.w, 0x5410), 0, __byte_perm(x.y, x.w, 0x7632), 0, qf[n][c][2], qf[n][c][3]);
                 }
             }
-            float top[NQ][2];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int pos = s.P + tok;
-                    const bool seen = tok < s.n && pos <= hi[n][e] && pos >= lo[n][e];
-                    acc[n][e] = top[n][e] = seen ? acc[n][e] * p.scale_log2 : -INFINITY;
-                }
-            raise(top);
-            uint32_t pt[NQ];
+            float2 top[NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    acc[n][e] = exp2_approx(acc[n][e] - (m[n][e] == -INFINITY ? 0.f : m[n][e]));
-                    l[n][e] += acc[n][e];
+                    int lo, hi;
+                    visible(n, e, lo, hi);
+                    if (tok >= many || P + tok > hi || P + tok < lo) acc[n][e] = -INFINITY;
                 }
-                pt[n] = movmatrix(pack(acc[n][0], acc[n][1]));
+                top[n] = make_float2(acc[n][0], acc[n][1]);
+            }
+            raise(top);
+            uint32_t pt[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                const float2 x = __ffma2_rn(top[n], both(p.scale_log2), neg[n]);
+                const float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                l[n] = __fadd2_rn(l[n], pr);
+                pt[n] = movmatrix(pack(pr.x, pr.y));
             }
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c) {
@@ -670,15 +741,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
                 constexpr int kLanes = D / 8, kStep = 32 / kLanes;
                 constexpr int kGroupLanes = kLanes / NG;
                 const int part = lane % kLanes;
-                for (int r0 = 0; r0 < kNewKeys && tok0 + r0 < s.n; r0 += kStep) {
+                for (int r0 = 0; r0 < kNewKeys && tok0 + r0 < many; r0 += kStep) {
                     const int r = r0 + lane / kLanes;
                     uint32_t kw, vw, kc[1], vc[1];
                     const uint4 kx[1] = {*reinterpret_cast<const uint4*>(tile + r * 2 * D + part * 16)};
                     const uint4 vx[1] = {*reinterpret_cast<const uint4*>(tile + C::kCodes + r * 2 * D + part * 16)};
                     quantise(kx, kGroupLanes, kc, &kw);
                     quantise(vx, kGroupLanes, vc, &vw);
-                    if (tok0 + r >= s.n) continue;
-                    const size_t row = row4(p.cache, t.b, t.kvh, s.P + tok0 + r);
+                    if (tok0 + r >= many) continue;
+                    const size_t row = row4(p.cache, t.b, t.kvh, P + tok0 + r);
                     if (row == ~size_t(0)) continue;
                     reinterpret_cast<uint32_t*>(p.cache.k + row * C::kRowBytes)[part] = kc[0];
                     reinterpret_cast<uint32_t*>(p.cache.v + row * C::kRowBytes)[part] = vc[0];
@@ -701,26 +772,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
             for (int n = 0; n < NQ; ++n) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float x = l[n][e];
+                    float x = e ? l[n].y : l[n].x;
                     x += __shfl_xor_sync(0xffffffffu, x, 4);
                     x += __shfl_xor_sync(0xffffffffu, x, 8);
                     x += __shfl_xor_sync(0xffffffffu, x, 16);
-                    l[n][e] = x;
+                    float add[NG];
 #pragma unroll
                     for (int a = 0; a < NG; ++a) {
-                        float y = om[n][a][e];
+                        float y = e ? om[n][a].y : om[n][a].x;
                         y += __shfl_xor_sync(0xffffffffu, y, 4);
                         y += __shfl_xor_sync(0xffffffffu, y, 8);
                         y += __shfl_xor_sync(0xffffffffu, y, 16);
-                        om[n][a][e] = y;
+                        add[a] = y;
                     }
                     const int row = 8 * n + 2 * t4 + e;
                     const float f = whole ? 1.f / x : 1.f;
+                    // (-inf where the share's keys are all hidden from the row)
+                    const float m = (e ? most[n].y : most[n].x) == -INFINITY ? -INFINITY : -(e ? neg[n].y : neg[n].x);
 #pragma unroll
                     for (int c = 0; c < C::kChunks; ++c) {
-                        const float add = om[n][c / kGroupChunks][e];
-                        const float4 v = make_float4((o[n][c][0][e] + add) * f, (o[n][c][0][2 + e] + add) * f,
-                                                     (o[n][c][1][e] + add) * f, (o[n][c][1][2 + e] + add) * f);
+                        const float y = add[c / kGroupChunks];
+                        const float4 v = make_float4((o[n][c][0][e] + y) * f, (o[n][c][0][2 + e] + y) * f,
+                                                     (o[n][c][1][e] + y) * f, (o[n][c][1][2 + e] + y) * f);
                         if (whole)
                             store_row<D, NQ>(p, t, row, 32 * c + 4 * g, v);
                         else
@@ -728,9 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
                     }
                     if (g == 0) {
                         if (whole)
-                            store_lse<NQ>(p, t, row, m[n][e], x);
+                            store_lse<NQ>(p, t, row, m, x);
                         else
-                            stats[warp][slot][row] = make_float2(m[n][e], x);
+                            stats[warp][slot][row] = make_float2(m, x);
                     }
                 }
             }
@@ -804,7 +877,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         if (pending[k] < 0) continue;  // (the whole CTA)
-        const Tile& t = records[pending[k] / 2][pending[k] & 1].t;
+        const Item& t = records[pending[k] / 2][pending[k] & 1].t;
         const long long b0 = ((long long)t.start_hi << 32) | (unsigned)t.start_lo;
         const int c0 = (int)(b0 / share), c1 = (int)((b0 + t.tiles - 1) / share);
         __threadfence();
@@ -843,8 +916,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows4_kernel(const Rows4Para
 template <int D, int NG, int NQ>
 cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     using C = Cfg<D, NG, NQ>;
-    constexpr int kSmem = kWarps * (C::kStages * C::kTileBytes + C::kRecord);
-    static_assert(kSmem <= 210 * 1024, "shared memory budget, beside the static part");
+    constexpr int kSmem = C::kWarps * (C::kStages * C::kTileBytes + C::kRecord);
+    static_assert(kSmem <= 215 * 1024, "shared memory budget, beside the static part");
     static int configured_for[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
@@ -856,7 +929,7 @@ cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

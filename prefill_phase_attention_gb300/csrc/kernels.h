@@ -216,7 +216,6 @@ cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, int sms, cud
 cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
 
 // Attention of few query rows per sequence over the 4-bit cache (attn_rows4.cu).
-constexpr int kRows4Warps = 8;
 constexpr int kRows4Seqs = 256;  // sequences whose metadata a CTA keeps in shared memory
 struct Rows4Params {
     Sequences4 seqs;
