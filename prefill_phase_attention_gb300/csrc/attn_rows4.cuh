@@ -4,11 +4,17 @@
 // A row block is 8 or 16 query rows (token, head of a KV head's group) of a sequence.
 // Its keys come in tiles: 32 cached rows, or 8 new tokens (bf16; as many bytes), which
 // follow them.  With a group's parameters (s, m) and codes c the score and output are
-//     q . k_j   = sum_g s_jg (q_g . (c_jg - 8)) + (m_jg + 8 s_jg) sum(q_g)
-//     sum_j p_j v_j = sum_j (p_j s_jg) (c_jg - 8) + sum_j p_j (m_jg + 8 s_jg)
-// so the products of codes run on the tensor cores with exact operands (c - 8 and q are
-// bf16 values), the parameters multiply in fp32, and the one rounding is that of p s to
-// bf16 for the second product.
+//     q . k_j   = sum_g s_jg (q_g . c_jg) + m_jg sum(q_g)
+//     sum_j p_j v_j = sum_j (p_j s_jg) c_jg + sum_j p_j m_jg
+// so the products of codes run on the tensor cores, in fp16 with exact codes, and the
+// parameters multiply in fp32.  A code in the low bits of an fp16 number is c 2^-24, in the
+// next four 16 c 2^-24, both subnormal and exact: one instruction a pair of codes, and
+// one shift for every four.  (With bf16 operands it is a shift, a mask and a
+// subtraction: 64 decode rows of 1024 to 16384 tokens 235 us.)  fp16's range is met by powers
+// of two: a query is scaled so that its largest channel is in [2^14, 2^15), what falls
+// below fp16 then is 2^-38 of that; and p s by a factor T per query that keeps its
+// running maximum within 2^15 (see `shrink`), and its rounding to fp16 is the one
+// that there is.
 //
 // What bounds it is HBM: 68 bytes of key or value (d = 128, one group) feed 8 rows, where
 // 128-row MMA tiles would be 15/16 empty and want the codes expanded through shared
@@ -27,6 +33,8 @@
 // those of its warps, and the CTA that comes last joins those of the CTAs, in list order
 // whoever it is.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include <cstdint>
 
@@ -138,6 +146,19 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4])
                  : "r"(addr)
                  : "memory");
 }
+// the same of fp16, and without a sum before
+__device__ __forceinline__ void mma_half(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_half_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 // 8x8 transpose of 16-bit elements held as a matrix fragment
 __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
     uint32_t y;
@@ -172,15 +193,20 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Codes i and i + 4 of a word (of each 16-bit half, code i), less 8, as a pair of bf16:
-// the code as the low mantissa bits of 128, less 136, both exact.
-template <int i>
-__device__ __forceinline__ uint32_t codes(uint32_t x) {
-    uint32_t y = ((x >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const uint32_t c = 0x43084308u;  // 136, 136
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y), *reinterpret_cast<const __nv_bfloat162*>(&c));
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+
+// Codes i and i + 4 of a word (of each 16-bit half, code i) as a pair of fp16: times 2^-24
+// for even i, 2^-20 for odd.
+template <int i>
+__device__ __forceinline__ uint32_t codes(uint32_t x) {
+    return (i >= 2 ? x >> 8 : x) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
+}
+constexpr float kCode = 0x1p-24f;    // unit of a code
+constexpr float kMostT = 0x1p100f;   // largest factor of the weights
+constexpr float kMostWeight = 0x1p15f;
 
 template <int D>
 __device__ __forceinline__ int swizzle(int key) {  // of a row's 16-byte parts
@@ -486,12 +512,13 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     uint32_t qf[NQ][C::kChunks][4];  // Q as the second operand: per chunk two 16-channel steps
     float2 qsum[NQ][NG];             // sums of a group's channels of queries 2 t4, 2 t4 + 1
     float o[NQ][C::kChunks][2][4];   // O^T: channels 32 c + 4 g + 2 e (+ 1), queries 2 t4, 2 t4 + 1
-    float2 om[NQ][NG];               // sum of p (m + 8 s) over this lane's keys
+    float2 om[NQ][NG];               // sum of p m over this lane's keys
     float2 l[NQ];                    // sum of p over this lane's keys
+    float2 scale[NQ];                // from scores as they are accumulated to log2 units
     float2 neg[NQ], most[NQ];        // less the running maximum m (log2 units; 0 before any key), (m + 8) / scale
+    float2 T[NQ];                    // factor of p s in the second product, and of O with it
     int P = 0, lo_most = 0;          // cached keys; the largest first visible key of a row
 
-    const float unscale = 1.f / p.scale_log2;
     int stage = 0;
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
@@ -512,30 +539,50 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 const bool there = r < s.n * p.group;
                 const uint4* src = reinterpret_cast<const uint4*>(
                     p.q + ((size_t)(s.q_start + (there ? r / p.group : 0)) * p.n_heads + t.kvh * p.group + (there ? r % p.group : 0)) * D);
+                uint4 x[C::kChunks];  // channels 32 c + 8 t4 ...
+                uint32_t top2 = 0;    // largest magnitude, of pairs
+#pragma unroll
+                for (int c = 0; c < C::kChunks; ++c) {
+                    x[c] = there ? __ldg(src + 4 * c + t4) : make_uint4(0, 0, 0, 0);
+                    const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top2 = __vmaxu2(top2, y[i] & 0x7fff7fffu);
+                }
+                uint32_t top1 = max(top2 & 0xffffu, top2 >> 16);
+                top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+                top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
+                // its largest channel goes to [2^14, 2^15)
+                const int up = min(268 - (int)(top1 >> 7), 253);
+                const float f = __int_as_float(up << 23);
+                const float un = __int_as_float((254 - up) << 23) * (p.scale_log2 / kCode);
                 float sum[NG];
 #pragma unroll
                 for (int a = 0; a < NG; ++a) sum[a] = 0.f;
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c) {
-                    uint4 x = __ldg(src + 4 * c + t4);  // channels 32 c + 8 t4 ...
-                    if (!there) x = make_uint4(0, 0, 0, 0);
-                    qf[n][c][0] = __byte_perm(x.x, x.z, 0x5410);
-                    qf[n][c][1] = __byte_perm(x.x, x.z, 0x7632);
-                    qf[n][c][2] = __byte_perm(x.y, x.w, 0x5410);
-                    qf[n][c][3] = __byte_perm(x.y, x.w, 0x7632);
-                    sum[c / kGroupChunks] += bf16_lo(x.x) + bf16_hi(x.x) + bf16_lo(x.y) + bf16_hi(x.y) + bf16_lo(x.z) +
-                                             bf16_hi(x.z) + bf16_lo(x.w) + bf16_hi(x.w);
+                    const float y[8] = {bf16_lo(x[c].x) * f, bf16_hi(x[c].x) * f, bf16_lo(x[c].y) * f, bf16_hi(x[c].y) * f,
+                                        bf16_lo(x[c].z) * f, bf16_hi(x[c].z) * f, bf16_lo(x[c].w) * f, bf16_hi(x[c].w) * f};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float w = i & 1 ? 0.0625f : 1.f;  // odd codes come 16 times as large
+                        qf[n][c][i] = pack_half(y[i] * w, y[i + 4] * w);
+                        sum[c / kGroupChunks] += y[i] + y[i + 4];
+                    }
                 }
 #pragma unroll
                 for (int a = 0; a < NG; ++a) {
                     sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 1);
                     sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 2);  // of query g
+                    sum[a] *= kCode;
                     qsum[n][a].x = __shfl_sync(0xffffffffu, sum[a], 8 * t4);
                     qsum[n][a].y = __shfl_sync(0xffffffffu, sum[a], 8 * t4 + 4);
                     om[n][a] = make_float2(0.f, 0.f);
                 }
+                scale[n].x = __shfl_sync(0xffffffffu, un, 8 * t4);
+                scale[n].y = __shfl_sync(0xffffffffu, un, 8 * t4 + 4);
                 neg[n] = l[n] = make_float2(0.f, 0.f);
                 most[n] = both(-INFINITY);
+                T[n] = both(kMostT);
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
@@ -553,7 +600,14 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
         };
 
         // The running maximum, from the largest score `top` of the lane's keys: it is raised, and
-        // what was summed under it scaled, only when it falls behind by more than 2^8.
+        // what was summed under it scaled, only when it falls behind by more than 2^8.  O keeps
+        // its size, T is what grows.
+        auto scale_o = [&](int n, float x, float y) {
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] *= e & 1 ? y : x;
+        };
         auto raise = [&](const float2 (&top)[NQ]) {
             bool behind = false;
 #pragma unroll
@@ -561,27 +615,47 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
             if (!__any_sync(0xffffffffu, behind)) return;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                float alpha[2], x[2] = {top[n].x, top[n].y};
+                float alpha[2], t[2], x[2] = {top[n].x, top[n].y};
                 const float was[2] = {most[n].x, most[n].y}, less[2] = {neg[n].x, neg[n].y};
+                const float sc[2] = {scale[n].x, scale[n].y}, t0[2] = {T[n].x, T[n].y};
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 4));
                     x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 8));
                     x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16));
-                    x[e] *= p.scale_log2;
+                    x[e] *= sc[e];
                     const bool none = was[e] == -INFINITY;  // no key before
                     if (!none) x[e] = fmaxf(x[e], -less[e]);
-                    alpha[e] = none || x[e] == -INFINITY ? 0.f : exp2_approx(-less[e] - x[e]);
+                    alpha[e] = none ? 0.f : exp2_approx(-less[e] - x[e]);
+                    t[e] = fminf(__fdividef(t0[e], alpha[e]), kMostT);
+                    if (none || !(alpha[e] > 0x1p-100f)) t[e] = kMostT;
                 }
+                scale_o(n, alpha[0] * (t[0] / t0[0]), alpha[1] * (t[1] / t0[1]));
+                T[n] = make_float2(t[0], t[1]);
                 l[n].x *= alpha[0], l[n].y *= alpha[1];
 #pragma unroll
                 for (int a = 0; a < NG; ++a) om[n][a].x *= alpha[0], om[n][a].y *= alpha[1];
+                if (x[0] != -INFINITY) neg[n].x = -x[0], most[n].x = (x[0] + 8.f) / sc[0];
+                if (x[1] != -INFINITY) neg[n].y = -x[1], most[n].y = (x[1] + 8.f) / sc[1];
+            }
+        };
+        // The factor T of weights that reach `top` without it: where a weight would pass kMostWeight,
+        // the largest goes to [2^7, 2^8).
+        auto shrink = [&](const float2 (&top)[NQ]) {
 #pragma unroll
-                for (int c = 0; c < C::kChunks; ++c)
+            for (int n = 0; n < NQ; ++n) {
+                float t[2], x[2] = {top[n].x, top[n].y};
+                const float t0[2] = {T[n].x, T[n].y};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] *= alpha[e & 1];
-                if (x[0] != -INFINITY) neg[n].x = -x[0], most[n].x = (x[0] + 8.f) * unscale;
-                if (x[1] != -INFINITY) neg[n].y = -x[1], most[n].y = (x[1] + 8.f) * unscale;
+                for (int e = 0; e < 2; ++e) {
+                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 4));
+                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 8));
+                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16));
+                    x[e] = fminf(x[e], 0x1p127f);
+                    t[e] = x[e] * t0[e] > kMostWeight ? __int_as_float(min(261 - (__float_as_int(x[e]) >> 23), 227) << 23) : t0[e];
+                }
+                scale_o(n, t[0] / t0[0], t[1] / t0[1]);
+                T[n] = make_float2(t[0], t[1]);
             }
         };
 
@@ -595,10 +669,6 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
             for (int a = 0; a < NG; ++a) {
                 float acc[NQ][2][4];
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[n][e / 4][e % 4] = 0.f;
-#pragma unroll
                 for (int cc = 0; cc < kGroupChunks; ++cc) {
                     const int c = a * kGroupChunks + cc;
                     uint32_t x[4];
@@ -610,20 +680,24 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                                        b2 = codes<3>(x[2 * h]), b3 = codes<3>(x[2 * h + 1]);
 #pragma unroll
                         for (int n = 0; n < NQ; ++n) {
-                            mma(acc[n][h], a0, a1, a2, a3, qf[n][c][0], qf[n][c][1]);
-                            mma(acc[n][h], b0, b1, b2, b3, qf[n][c][2], qf[n][c][3]);
+                            if (cc == 0)
+                                mma_half_first(acc[n][h], a0, a1, a2, a3, qf[n][c][0], qf[n][c][1]);
+                            else
+                                mma_half(acc[n][h], a0, a1, a2, a3, qf[n][c][0], qf[n][c][1]);
+                            mma_half(acc[n][h], b0, b1, b2, b3, qf[n][c][2], qf[n][c][3]);
                         }
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t w = kp[8 * k * NG + a];
-                    const float sk = bf16_lo(w), mk = fmaf(8.f, sk, bf16_hi(w));
+                    const float sk = bf16_lo(w), mk = bf16_hi(w);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        const float2 qc = make_float2(acc[n][k / 2][2 * (k & 1)], acc[n][k / 2][2 * (k & 1) + 1]);
-                        sc[n][k] = __ffma2_rn(both(sk), qc, a == 0 ? __fmul2_rn(both(mk), qsum[n][a])
-                                                                   : __ffma2_rn(both(mk), qsum[n][a], sc[n][k]));
+                        const float* const qc = acc[n][k / 2] + 2 * (k & 1);
+                        const float2 x = a == 0 ? make_float2(mk * qsum[n][a].x, mk * qsum[n][a].y)
+                                                : make_float2(fmaf(mk, qsum[n][a].x, sc[n][k].x), fmaf(mk, qsum[n][a].y, sc[n][k].y));
+                        sc[n][k] = make_float2(fmaf(sk, qc[0], x.x), fmaf(sk, qc[1], x.y));
                     }
                 }
             }
@@ -649,28 +723,64 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 top[n].y = fmaxf(max3(sc[n][0].y, sc[n][1].y, sc[n][2].y), sc[n][3].y);
             }
             raise(top);
-            uint32_t pt[NQ][NG][4];  // P^T scaled by the values' parameters, per octet
+            float sv[4][NG];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float2 pr[NQ];
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
-                    const float2 x = __ffma2_rn(sc[n][k], both(p.scale_log2), neg[n]);
+                    const float2 x = __ffma2_rn(sc[n][k], scale[n], neg[n]);
                     pr[n] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
                     l[n] = __fadd2_rn(l[n], pr[n]);
+                    sc[n][k] = pr[n];
                 }
 #pragma unroll
                 for (int a = 0; a < NG; ++a) {
                     const uint32_t w = vp[8 * k * NG + a];
-                    const float sv = bf16_lo(w), mv = fmaf(8.f, sv, bf16_hi(w));
+                    const float mv = bf16_hi(w);
+                    sv[k][a] = bf16_lo(w);
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        om[n][a] = __ffma2_rn(pr[n], both(mv), om[n][a]);
-                        const float2 x = __fmul2_rn(pr[n], both(sv));
-                        pt[n][a][k] = movmatrix(pack(x.x, x.y));
-                    }
+                    for (int n = 0; n < NQ; ++n)
+                        om[n][a] = make_float2(fmaf(pr[n].x, mv, om[n][a].x), fmaf(pr[n].y, mv, om[n][a].y));
                 }
             }
+            uint32_t pt[NQ][NG][4];  // P^T times the values' scales and T, per octet
+#pragma unroll 1
+            for (int pass = 0;; ++pass) {
+                float most_w = 0.f;
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 x = __fmul2_rn(sc[n][k], T[n]);
+#pragma unroll
+                        for (int a = 0; a < NG; ++a) {
+                            const float wx = x.x * sv[k][a], wy = x.y * sv[k][a];
+                            most_w = max3(most_w, wx, wy);
+                            pt[n][a][k] = pack_half(wx, wy);
+                        }
+                    }
+                if (pass > 0 || !__any_sync(0xffffffffu, most_w > kMostWeight)) break;
+                float2 top_w[NQ];
+#pragma unroll
+                for (int n = 0; n < NQ; ++n) {
+                    top_w[n] = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int a = 0; a < NG; ++a) {
+                            top_w[n].x = fmaxf(top_w[n].x, sc[n][k].x * sv[k][a]);
+                            top_w[n].y = fmaxf(top_w[n].y, sc[n][k].y * sv[k][a]);
+                        }
+                }
+                shrink(top_w);
+            }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int a = 0; a < NG; ++a)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) pt[n][a][k] = movmatrix(pt[n][a][k]);
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c) {
                 const int a = c / kGroupChunks;
@@ -683,13 +793,18 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                                    b2 = codes<2>(x[2 * h + 1]), b3 = codes<3>(x[2 * h + 1]);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        mma(o[n][c][0], a0, a1, a2, a3, pt[n][a][2 * h], pt[n][a][2 * h + 1]);
-                        mma(o[n][c][1], b0, b1, b2, b3, pt[n][a][2 * h], pt[n][a][2 * h + 1]);
+                        mma_half(o[n][c][0], a0, a1, a2, a3, pt[n][a][2 * h], pt[n][a][2 * h + 1]);
+                        mma_half(o[n][c][1], b0, b1, b2, b3, pt[n][a][2 * h], pt[n][a][2 * h + 1]);
                     }
                 }
             }
         } else {
-            // ---- up to 8 new tokens, bf16: the matrix rows g of one tile
+            // ---- up to 8 new tokens, bf16: the matrix rows g of one tile.  Q goes back to bf16;
+            // scores and outputs keep the units of the codes' products.
+            auto as_bf16 = [](uint32_t h, float w) -> uint32_t {
+                const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+                return pack(x.x * w, x.y * w);
+            };
             const int tok0 = -1 - key, tok = tok0 + g, many = t.s.n;
             float acc[NQ][4];
 #pragma unroll
@@ -701,8 +816,10 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 const uint4 x = *reinterpret_cast<const uint4*>(tile + g * 2 * D + 64 * c + 16 * t4);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
-                    mma(acc[n], __byte_perm(x.x, x.z, 0x5410), 0, __byte_perm(x.x, x.z, 0x7632), 0, qf[n][c][0], qf[n][c][1]);
-                    mma(acc[n], __byte_perm(x.y, x.w, 0x5410), 0, __byte_perm(x.y, x.w, 0x7632), 0, qf[n][c][2], qf[n][c][3]);
+                    mma(acc[n], __byte_perm(x.x, x.z, 0x5410), 0, __byte_perm(x.x, x.z, 0x7632), 0, as_bf16(qf[n][c][0], 1.f),
+                        as_bf16(qf[n][c][1], 16.f));
+                    mma(acc[n], __byte_perm(x.y, x.w, 0x5410), 0, __byte_perm(x.y, x.w, 0x7632), 0, as_bf16(qf[n][c][2], 1.f),
+                        as_bf16(qf[n][c][3], 16.f));
                 }
             }
             float2 top[NQ];
@@ -712,7 +829,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 for (int e = 0; e < 2; ++e) {
                     int lo, hi;
                     visible(n, e, lo, hi);
-                    if (tok >= many || P + tok > hi || P + tok < lo) acc[n][e] = -INFINITY;
+                    acc[n][e] = tok >= many || P + tok > hi || P + tok < lo ? -INFINITY : acc[n][e] * kCode;
                 }
                 top[n] = make_float2(acc[n][0], acc[n][1]);
             }
@@ -720,20 +837,23 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
             uint32_t pt[NQ];
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-                const float2 x = __ffma2_rn(top[n], both(p.scale_log2), neg[n]);
+                const float2 x = __ffma2_rn(top[n], scale[n], neg[n]);
                 const float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
                 l[n] = __fadd2_rn(l[n], pr);
-                pt[n] = movmatrix(pack(pr.x, pr.y));
+                pt[n] = movmatrix(pack(pr.x * T[n].x * kCode, pr.y * T[n].y * kCode));
             }
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c) {
                 const uint8_t* v = tile + C::kCodes + 64 * c + 8 * g;
                 const uint2 x = *reinterpret_cast<const uint2*>(v + 2 * t4 * 2 * D);
                 const uint2 y = *reinterpret_cast<const uint2*>(v + (2 * t4 + 1) * 2 * D);
+                // odd channels 16 times as large, as the codes' are
+                auto odd = [](uint32_t lo, uint32_t hi) -> uint32_t { return pack(bf16_hi(lo) * 16.f, bf16_hi(hi) * 16.f); };
+                const uint32_t v1 = odd(x.x, y.x), v3 = odd(x.y, y.y);
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
-                    mma(o[n][c][0], __byte_perm(x.x, y.x, 0x5410), __byte_perm(x.x, y.x, 0x7632), 0, 0, pt[n], 0);
-                    mma(o[n][c][1], __byte_perm(x.y, y.y, 0x5410), __byte_perm(x.y, y.y, 0x7632), 0, 0, pt[n], 0);
+                    mma(o[n][c][0], __byte_perm(x.x, y.x, 0x5410), v1, 0, 0, pt[n], 0);
+                    mma(o[n][c][1], __byte_perm(x.y, y.y, 0x5410), v3, 0, 0, pt[n], 0);
                 }
             }
             if (t.block == 0) {
@@ -787,13 +907,14 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                     }
                     const int row = 8 * n + 2 * t4 + e;
                     const float f = whole ? 1.f / x : 1.f;
+                    const float un = f / (kCode * (e ? T[n].y : T[n].x)), odd = 0.0625f * un;
                     // (-inf where the share's keys are all hidden from the row)
                     const float m = (e ? most[n].y : most[n].x) == -INFINITY ? -INFINITY : -(e ? neg[n].y : neg[n].x);
 #pragma unroll
                     for (int c = 0; c < C::kChunks; ++c) {
-                        const float y = add[c / kGroupChunks];
-                        const float4 v = make_float4((o[n][c][0][e] + y) * f, (o[n][c][0][2 + e] + y) * f,
-                                                     (o[n][c][1][e] + y) * f, (o[n][c][1][2 + e] + y) * f);
+                        const float y = add[c / kGroupChunks] * f;
+                        const float4 v = make_float4(fmaf(o[n][c][0][e], un, y), fmaf(o[n][c][0][2 + e], odd, y),
+                                                     fmaf(o[n][c][1][e], un, y), fmaf(o[n][c][1][2 + e], odd, y));
                         if (whole)
                             store_row<D, NQ>(p, t, row, 32 * c + 4 * g, v);
                         else

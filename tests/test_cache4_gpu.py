@@ -199,6 +199,25 @@ def test_large_values():
     c.check()
 
 
+@pytest.mark.parametrize("new", [[1, 1, 1], [3, 2, 60]])
+def test_values_of_very_different_size(new):
+    """Rows of V whose scales differ by 2^60, and queries so large that the weights differ as much: what a row adds
+    may be the product of a tiny weight and a huge value."""
+    c = Call(15, new, [600, 64, 40], group=64)
+    g = torch.Generator().manual_seed(1)
+    for which in range(2):
+        size = torch.randint(-30, 31, c.cache.params[1].shape[:3], generator=g).double()
+        if which == 0:
+            size *= 0.1
+        x = c.cache.params[which].double() * torch.exp2(size)[..., None, None]
+        c.cache.params[which] = x.to(torch.bfloat16)
+        c.params[which][1].copy_(c.cache.params[which])
+    c.q *= 6
+    c.dev[0].copy_(c.q)
+    c.attend()
+    c.check(tiles=max(new) > 16)
+
+
 def test_equal_inputs_give_equal_bits():
     outs = []
     for _ in range(3):
