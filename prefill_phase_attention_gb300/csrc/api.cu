@@ -1622,10 +1622,13 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     if (s != PA_OK) return s;
     pa::Rows4Params p;
     void* part = nullptr;
+    size_t part_floats = 0;
     if (rows) {
         s = get_arrivals(ws, stream, &p.arrivals);
         if (s != PA_OK) return s;
-        s = get_aux_scratch(ws, stream, (size_t)grid * 2 * 8 * row_tiles * (head_dim + 2) * sizeof(float), &part);
+        part_floats = (size_t)grid * 2 * 8 * row_tiles * (head_dim + 2);
+        const size_t kept = (size_t)grid * pa::kRows4Warps * 8 * row_tiles * head_dim;
+        s = get_aux_scratch(ws, stream, (part_floats + kept) * sizeof(float), &part);
         if (s != PA_OK) return s;
     }
     void* rope = nullptr;
@@ -1689,6 +1692,7 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     p.window = o.window;
     p.most_tokens = tiles ? few : INT_MAX;
     p.part = static_cast<float*>(part);
+    p.kept = p.part + part_floats;
     e = pa::launch_attn_rows4(p, head_dim, row_tiles, grid, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
     ++g_last_launches;

@@ -51,10 +51,10 @@ constexpr int kNewKeys = 8;    // new tokens of a tile
 
 template <int D, int NG, int NQ>
 struct Cfg {
-    // As many warps as registers (NQ = 1: 168 a thread) and shared memory allow: the
+    // As many warps as registers (16: 128 a thread, 12: 168) and shared memory allow: the
     // instructions of a tile take most of the time that its bytes do, so the issue slots
     // have to be filled.
-    static constexpr int kWarps = NQ == 2 ? 8 : NG == 4 ? 10 : 12;
+    static constexpr int kWarps = NQ == 2 ? 8 : NG > 1 ? 12 : 16;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kChunks = D / 32;
     static constexpr int kRowBytes = D / 2;
@@ -84,6 +84,7 @@ enum : int {
     kLast = 2,       // of the row block, in this warp
     kFromBefore = 4, // the row block began before this warp's share
     kGoesOn = 8,     // and ends after it
+    kEdge = 16,      // some of the tile's keys are hidden from some row
     kSlot = 8,       // shift
 };
 
@@ -229,6 +230,17 @@ __device__ __forceinline__ void store_lse(const Rows4Params& p, const Item& t, i
         (m + log2_approx(l)) * 0.69314718055994530942f;
 }
 
+// Where a warp is in the tile list; in shared memory, read and written where it is not
+// simply at the next whole cached tile of its row block.
+struct Walk {
+    SeqInfo s;
+    Extent e;
+    long long block_start;  // list position of the row block's first tile
+    int b, kvh, block;      // row block: sequence, KV head, block of rows
+    int fresh;              // tiles of new tokens that came
+    int lo_most;            // largest first visible key of a row
+};
+
 // Walks the tile list from a sequence on, and starts the copies of one tile at a time.
 template <int D, int NG, int NQ>
 struct Feeder {
@@ -237,24 +249,18 @@ struct Feeder {
     static constexpr int kPassRows = 32 / kParts;     // rows that the lanes copy at once
     const Rows4Params& p;
     const SeqInfo* table;  // in shared memory, or nullptr
-    uint32_t ring;
+    Walk* walk;
     Item* items;
     Tile* tiles;
+    uint32_t ring;    // this lane's place in the first stage
+    uint32_t params;  // and its parameters'
     int lane;
-    int left;            // tiles of the share that are still to come
-    int b, kvh, block;   // row block: sequence, KV head, block of rows
-    int key, cached_end; // next tile if it is cached; where those end
-    int fresh;           // new tokens' tiles of the row block that came
-    SeqInfo s;
-    Extent e;
-    long long block_start;  // list position of the row block's first tile
-    // this lane's first part of the next cached tile (contiguous cache)
-    const uint8_t* kc;
-    const uint8_t* vc;
-    const uint32_t* kp;
-    const uint32_t* vp;
+    int left;         // tiles of the share that are still to come
+    int key;          // next tile if it is cached
+    int whole_until;  // tiles below are whole and have no edge
+    unsigned row;     // contiguous cache: row of the next cached tile
+    int flags;        // of the next tile: its item's slot, kFirst and kFromBefore
     int ids, next_ids;  // paged: blocks of the 8-row pieces of this and the next 256 positions
-    int slot, flags;    // of the row block: its slot of `items`, kFirst and kFromBefore
 
     __device__ __forceinline__ SeqInfo seq(int i) const {
         return table ? table[i] : sequence4(p.seqs, p.cache.max_cache_len, i);
@@ -262,166 +268,187 @@ struct Feeder {
     // Puts the feeder at list position `first`; `start` is that of sequence b0.
     __device__ __forceinline__ void seek(int b0, long long start, long long first, int count) {
         left = count;
-        slot = -1;
+        key = whole_until = 0;
+        flags = (C::kStages - 1) << kSlot;
         if (left == 0) return;
-        b = b0;
-        s = seq(b);
-        e = extent<NQ>(p, s);
+        Walk w;
+        w.b = b0;
+        w.s = seq(w.b);
+        w.e = extent<NQ>(p, w.s);
         for (;;) {
-            const long long all = (long long)e.tiles() * e.blocks * p.cache.n_kv_heads;
+            const long long all = (long long)w.e.tiles() * w.e.blocks * p.cache.n_kv_heads;
             if (first < start + all) break;
             start += all;
-            ++b;  // the list's total says that there is one
-            s = seq(b);
-            e = extent<NQ>(p, s);
+            ++w.b;  // the list's total says that there is one
+            w.s = seq(w.b);
+            w.e = extent<NQ>(p, w.s);
         }
         const long long in = first - start;
-        const int item = (int)(in / e.tiles()), j = (int)(in % e.tiles());
-        kvh = item / e.blocks;
-        block = item % e.blocks;
-        block_start = first - j;
-        enter(j);
+        const int item = (int)(in / w.e.tiles()), j = (int)(in % w.e.tiles());
+        w.kvh = item / w.e.blocks;
+        w.block = item % w.e.blocks;
+        w.block_start = first - j;
+        enter(w, j);
+        if (lane == 0) *walk = w;
+        __syncwarp();
     }
     // Begins a row block at its tile j.
-    __device__ __forceinline__ void enter(int j) {
-        key = (e.first_tile + min(j, e.cached)) * kTileKeys;
-        cached_end = (e.first_tile + e.cached) * kTileKeys;
-        fresh = max(0, j - e.cached);
-        flags = kFirst | (j > 0 ? kFromBefore : 0);
-        slot = slot + 1 == C::kStages ? 0 : slot + 1;
-        if (lane == 0) items[slot] = Item{s, b, kvh, block, e.tiles(), (int)(block_start >> 32), (int)block_start};
+    __device__ __forceinline__ void enter(Walk& w, int j) {
+        key = (w.e.first_tile + min(j, w.e.cached)) * kTileKeys;
+        w.fresh = max(0, j - w.e.cached);
+        w.lo_most = 0;
+        if (p.causal && p.window > 0)
+            w.lo_most = w.s.P + min((w.block * C::kRows + C::kRows - 1) / p.group, w.s.n - 1) - p.window + 1;
+        const int slot = (flags >> kSlot) + 1 == C::kStages ? 0 : (flags >> kSlot) + 1;
+        flags = slot << kSlot | kFirst | (j > 0 ? kFromBefore : 0);
+        if (lane == 0)
+            items[slot] = Item{w.s, w.b, w.kvh, w.block, w.e.tiles(), (int)(w.block_start >> 32), (int)w.block_start};
         if (p.cache.block_table) {
-            ids = id_of(key >> 8);
-            next_ids = id_of((key >> 8) + 1);
+            ids = id_of(w.b, w.s.P, key >> 8);
+            next_ids = id_of(w.b, w.s.P, (key >> 8) + 1);
         } else {
-            const size_t row = ((size_t)b * p.cache.n_kv_heads + kvh) * p.cache.max_cache_len + key;
-            const size_t at = (row + lane / kParts) * C::kRowBytes + lane % kParts * 16;
-            kc = p.cache.k + at;
-            vc = p.cache.v + at;
-            kp = p.cache.kp + (row + lane) * NG;
-            vp = p.cache.vp + (row + lane) * NG;
+            row = (unsigned)((w.b * p.cache.n_kv_heads + w.kvh) * p.cache.max_cache_len + key);  // < 2^31
         }
+        whole_until = key < w.lo_most ? 0 : w.s.P / kTileKeys * kTileKeys;
     }
     // The block of the lane's 8-row piece (of a checked table: the bounds keep a stray entry
     // from becoming a stray read).
-    __device__ __forceinline__ int id_of(int window) const {
+    __device__ __forceinline__ int id_of(int b, int P, int window) const {
         const int pos = window * 256 + lane * 8;
-        if (pos >= s.P) return 0;
+        if (pos >= P) return 0;
         const int id = __ldg(p.cache.block_table + (size_t)b * p.cache.max_blocks + (pos >> p.cache.block_log2));
         return (int)min((unsigned)id, (unsigned)p.cache.num_blocks - 1);
     }
     // paged: the pool's row of the tile's row r
-    __device__ __forceinline__ size_t pool_row(int r) const {
+    __device__ __forceinline__ size_t pool_row(int kvh, int r) const {
         const int id = __shfl_sync(0xffffffffu, ids, ((key & 255) >> 3) + (r >> 3));
         return ((size_t)(unsigned)(id * p.cache.n_kv_heads + kvh) << p.cache.block_log2) +
                ((key + r) & ((1 << p.cache.block_log2) - 1));
     }
+    __device__ __forceinline__ void advance(int b, int P) {
+        key += kTileKeys;
+        row += kTileKeys;
+        if (p.cache.block_table && (key & 255) == 0) {
+            ids = next_ids;
+            next_ids = id_of(b, P, (key >> 8) + 1);
+        }
+    }
     __device__ __forceinline__ void issue(int stage) {
         if (left > 0) {
-            const uint32_t base = ring + stage * C::kTileBytes;
-            const uint32_t dst = base + lane / kParts * C::kRowBytes + (lane % kParts ^ swizzle<D>(lane / kParts)) * 16;
-            const uint32_t params = base + 2 * C::kCodes + lane * NG * 4;
-            const int at = key < cached_end ? key : -1 - fresh * kNewKeys;
-            if (at >= 0) {
-                // (the swizzle is the same for rows a pass apart)
-                if (key + kTileKeys <= s.P) {
-                    if (!p.cache.block_table) {
-#pragma unroll
-                        for (int it = 0; it < kParts; ++it) {
-                            cp_async16(dst + it * 512, kc + it * 512);
-                            cp_async16(dst + C::kCodes + it * 512, vc + it * 512);
-                        }
-                        if constexpr (NG == 4) {
-                            cp_async16(params, kp);
-                            cp_async16(params + C::kParams, vp);
-                        } else {
-                            cp_async_small<NG * 4>(params, kp);
-                            cp_async_small<NG * 4>(params + C::kParams, vp);
-                        }
-                        kc += C::kCodes;
-                        vc += C::kCodes;
-                        kp += kTileKeys * NG;
-                        vp += kTileKeys * NG;
-                    } else {
-#pragma unroll
-                        for (int it = 0; it < kParts; ++it) {
-                            const size_t from = pool_row(it * kPassRows + lane / kParts) * C::kRowBytes + lane % kParts * 16;
-                            cp_async16(dst + it * 512, p.cache.k + from);
-                            cp_async16(dst + C::kCodes + it * 512, p.cache.v + from);
-                        }
-                        const size_t row = pool_row(lane) * NG;
-                        if constexpr (NG == 4) {
-                            cp_async16(params, p.cache.kp + row);
-                            cp_async16(params + C::kParams, p.cache.vp + row);
-                        } else {
-                            cp_async_small<NG * 4>(params, p.cache.kp + row);
-                            cp_async_small<NG * 4>(params + C::kParams, p.cache.vp + row);
-                        }
-                    }
-                } else {
-                    // the last cached tile: zeros past the sequence's cached rows
-                    const size_t row0 = ((size_t)b * p.cache.n_kv_heads + kvh) * p.cache.max_cache_len + key;
-#pragma unroll 1
-                    for (int it = 0; it < kParts; ++it) {
-                        const int r = it * kPassRows + lane / kParts;
-                        const bool read = key + r < s.P;
-                        const size_t row = p.cache.block_table ? pool_row(r) : row0 + r;
-                        const size_t from = (read ? row : 0) * C::kRowBytes + lane % kParts * 16;
-                        cp_async16(dst + it * 512, p.cache.k + from, read);
-                        cp_async16(dst + C::kCodes + it * 512, p.cache.v + from, read);
-                    }
-                    const bool read = key + lane < s.P;
-                    const size_t row = p.cache.block_table ? pool_row(lane) : row0 + lane;
-                    const size_t from = (read ? row : 0) * NG;
-                    if constexpr (NG == 4) {
-                        cp_async16(params, p.cache.kp + from, read);
-                        cp_async16(params + C::kParams, p.cache.vp + from, read);
-                    } else {
-                        cp_async_small<NG * 4>(params, p.cache.kp + from, read);
-                        cp_async_small<NG * 4>(params + C::kParams, p.cache.vp + from, read);
-                    }
-                }
-                key += kTileKeys;
-                if (p.cache.block_table && (key & 255) == 0) {
-                    ids = next_ids;
-                    next_ids = id_of((key >> 8) + 1);
-                }
-            } else {
-                constexpr int kNewParts = D / 8;  // 16-byte parts of a bf16 row
-#pragma unroll 1
-                for (int it = 0; it < kNewParts * kNewKeys / 32; ++it) {
-                    const int x = it * 32 + lane, tok = fresh * kNewKeys + x / kNewParts;
-                    const bool read = tok < s.n;
-                    const size_t from =
-                        ((size_t)(s.q_start + (read ? tok : 0)) * p.cache.n_kv_heads + kvh) * D + x % kNewParts * 8;
-                    cp_async16(base + x * 16, p.k + from, read);
-                    cp_async16(base + C::kCodes + x * 16, p.v + from, read);
-                }
-                ++fresh;
-            }
-            --left;
-            const bool ends = fresh == e.fresh;
-            int f = flags | slot << kSlot;
-            if (ends || left == 0) f |= ends ? kLast : kLast | kGoesOn;
-            if (lane == 0) tiles[stage] = Tile{at, f};
-            flags &= ~kFirst;
-            if (ends && left > 0) {
-                block_start += e.tiles();
-                if (++block == e.blocks) {
-                    block = 0;
-                    if (++kvh == p.cache.n_kv_heads) {
-                        kvh = 0;
-                        do {
-                            ++b;
-                            s = seq(b);
-                            e = extent<NQ>(p, s);
-                        } while (e.blocks == 0);
-                    }
-                }
-                enter(0);
-            }
+            if (key < whole_until)
+                issue_whole(stage);
+            else
+                issue_any(stage);
         }
         cp_async_commit();
+    }
+    // (the swizzle is the same for rows a pass apart)
+    __device__ __forceinline__ void issue_whole(int stage) {
+        const uint32_t dst = ring + stage * C::kTileBytes, par = params + stage * C::kTileBytes;
+        if (lane == 0) tiles[stage] = Tile{key, flags | (left == 1 ? kLast | kGoesOn : 0)};
+        flags &= ~kFirst;
+        --left;
+        if (!p.cache.block_table) {
+            const size_t from = (size_t)row * C::kRowBytes + lane * 16;
+#pragma unroll
+            for (int it = 0; it < kParts; ++it) {
+                cp_async16(dst + it * 512, p.cache.k + from + it * 512);
+                cp_async16(dst + C::kCodes + it * 512, p.cache.v + from + it * 512);
+            }
+            const size_t at = (size_t)(row + lane) * NG;
+            if constexpr (NG == 4) {
+                cp_async16(par, p.cache.kp + at);
+                cp_async16(par + C::kParams, p.cache.vp + at);
+            } else {
+                cp_async_small<NG * 4>(par, p.cache.kp + at);
+                cp_async_small<NG * 4>(par + C::kParams, p.cache.vp + at);
+            }
+            advance(0, 0);
+        } else {
+            const int kvh = walk->kvh;
+#pragma unroll
+            for (int it = 0; it < kParts; ++it) {
+                const size_t from = pool_row(kvh, it * kPassRows + lane / kParts) * C::kRowBytes + lane % kParts * 16;
+                cp_async16(dst + it * 512, p.cache.k + from);
+                cp_async16(dst + C::kCodes + it * 512, p.cache.v + from);
+            }
+            const size_t at = pool_row(kvh, lane) * NG;
+            if constexpr (NG == 4) {
+                cp_async16(par, p.cache.kp + at);
+                cp_async16(par + C::kParams, p.cache.vp + at);
+            } else {
+                cp_async_small<NG * 4>(par, p.cache.kp + at);
+                cp_async_small<NG * 4>(par + C::kParams, p.cache.vp + at);
+            }
+            advance(walk->b, walk->s.P);
+        }
+    }
+    // A cached tile at an edge, with zeros past the sequence's cached rows, or new tokens.
+    __device__ __forceinline__ void issue_any(int stage) {
+        Walk w = *walk;
+        const uint32_t dst = ring + stage * C::kTileBytes, par = params + stage * C::kTileBytes;
+        const bool cached = w.fresh == 0 && key < (w.e.first_tile + w.e.cached) * kTileKeys;
+        const int at = cached ? key : -1 - w.fresh * kNewKeys;
+        if (cached) {
+#pragma unroll 1
+            for (int it = 0; it < kParts; ++it) {
+                const int r = it * kPassRows + lane / kParts;
+                const bool read = key + r < w.s.P;
+                const size_t from_row = p.cache.block_table ? pool_row(w.kvh, r) : row + r;
+                const size_t from = (read ? from_row : 0) * C::kRowBytes + lane % kParts * 16;
+                cp_async16(dst + it * 512, p.cache.k + from, read);
+                cp_async16(dst + C::kCodes + it * 512, p.cache.v + from, read);
+            }
+            const bool read = key + lane < w.s.P;
+            const size_t from_row = p.cache.block_table ? pool_row(w.kvh, lane) : row + lane;
+            const size_t from = (read ? from_row : 0) * NG;
+            if constexpr (NG == 4) {
+                cp_async16(par, p.cache.kp + from, read);
+                cp_async16(par + C::kParams, p.cache.vp + from, read);
+            } else {
+                cp_async_small<NG * 4>(par, p.cache.kp + from, read);
+                cp_async_small<NG * 4>(par + C::kParams, p.cache.vp + from, read);
+            }
+            advance(w.b, w.s.P);
+            if (key >= w.lo_most) whole_until = w.s.P / kTileKeys * kTileKeys;
+        } else {
+            const uint32_t base = params + stage * C::kTileBytes - lane * NG * 4 - 2 * C::kCodes;
+            constexpr int kNewParts = D / 8;  // 16-byte parts of a bf16 row
+#pragma unroll 1
+            for (int it = 0; it < kNewParts * kNewKeys / 32; ++it) {
+                const int x = it * 32 + lane, tok = w.fresh * kNewKeys + x / kNewParts;
+                const bool read = tok < w.s.n;
+                const size_t from =
+                    ((size_t)(w.s.q_start + (read ? tok : 0)) * p.cache.n_kv_heads + w.kvh) * D + x % kNewParts * 8;
+                cp_async16(base + x * 16, p.k + from, read);
+                cp_async16(base + C::kCodes + x * 16, p.v + from, read);
+            }
+            ++w.fresh;
+        }
+        --left;
+        const bool ends = w.fresh == w.e.fresh;
+        int f = flags | kEdge;
+        if (ends || left == 0) f |= ends ? kLast : kLast | kGoesOn;
+        if (lane == 0) tiles[stage] = Tile{at, f};
+        flags &= ~kFirst;
+        if (ends && left > 0) {
+            w.block_start += w.e.tiles();
+            if (++w.block == w.e.blocks) {
+                w.block = 0;
+                if (++w.kvh == p.cache.n_kv_heads) {
+                    w.kvh = 0;
+                    do {
+                        ++w.b;
+                        w.s = seq(w.b);
+                        w.e = extent<NQ>(p, w.s);
+                    } while (w.e.blocks == 0);
+                }
+            }
+            enter(w, 0);
+        }
+        __syncwarp();
+        if (lane == 0) *walk = w;
+        __syncwarp();
     }
 };
 
@@ -434,6 +461,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     __shared__ SeqInfo table[kRows4Seqs];
     __shared__ Item items[kWarps][C::kStages];
     __shared__ Tile tiles[kWarps][C::kStages];
+    __shared__ Walk walks[kWarps];
     __shared__ Record records[kWarps][2];
     __shared__ float2 stats[kWarps][2][C::kRows];  // (maximum, sum) of a record's rows
     __shared__ long long warp_sums[kWarps];
@@ -500,15 +528,16 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
 
     // ---- this warp's share
     uint8_t* const ring = smem + warp * C::kStages * C::kTileBytes;
-    float* const kept = reinterpret_cast<float*>(smem + kWarps * C::kStages * C::kTileBytes + warp * C::kRecord);
+    // a warp's first record: in global memory, its second one: in its ring
+    float* const kept = p.kept + ((size_t)blockIdx.x * kWarps + warp) * C::kRows * D;
     const long long len = to - from;
     const long long wfrom = from + len * warp / kWarps, wto = from + len * (warp + 1) / kWarps;
     const int steps = (int)(wto - wfrom);  // (2^31 tiles of a warp would take an hour)
-    Feeder<D, NG, NQ> feed{p, in_table ? table : nullptr, ptx::smem_u32(ring), items[warp], tiles[warp], lane};
+    constexpr int kParts = C::kRowBytes / 16;
+    Feeder<D, NG, NQ> feed{p, in_table ? table : nullptr, &walks[warp], items[warp], tiles[warp],
+                           ptx::smem_u32(ring) + lane / kParts * C::kRowBytes + (lane % kParts ^ swizzle<D>(lane / kParts)) * 16,
+                           ptx::smem_u32(ring) + 2 * C::kCodes + lane * NG * 4, lane};
     feed.seek(first_seq, start_of_first, wfrom, steps);
-#pragma unroll
-    for (int i = 0; i < C::kStages - 1; ++i) feed.issue(i);
-
     uint32_t qf[NQ][C::kChunks][4];  // Q as the second operand: per chunk two 16-channel steps
     float2 qsum[NQ][NG];             // sums of a group's channels of queries 2 t4, 2 t4 + 1
     float o[NQ][C::kChunks][2][4];   // O^T: channels 32 c + 4 g + 2 e (+ 1), queries 2 t4, 2 t4 + 1
@@ -517,14 +546,14 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     float2 scale[NQ];                // from scores as they are accumulated to log2 units
     float2 neg[NQ], most[NQ];        // less the running maximum m (log2 units; 0 before any key), (m + 8) / scale
     float2 T[NQ];                    // factor of p s in the second product, and of O with it
-    int P = 0, lo_most = 0;          // cached keys; the largest first visible key of a row
 
-    int stage = 0;
+    int stage = 1;  // (the first pass fills stage 0)
 #pragma unroll 1
-    for (int i = 0; i < steps; ++i) {
-        cp_async_wait<C::kStages - 2>();
-        __syncwarp();
+    for (int i = 1 - C::kStages; i < steps; ++i, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
         feed.issue(stage == 0 ? C::kStages - 1 : stage - 1);
+        if (i < 0) continue;
+        cp_async_wait<C::kStages - 1>();
+        __syncwarp();
         const int flags = tiles[warp][stage].flags, key = tiles[warp][stage].key;
         const Item& t = items[warp][flags >> kSlot];
         const uint8_t* const tile = ring + stage * C::kTileBytes;
@@ -532,7 +561,6 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
 
         if (flags & kFirst) {
             const SeqInfo s = t.s;
-            P = s.P;
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
                 const int r = t.block * C::kRows + 8 * n + g;
@@ -588,15 +616,12 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
 #pragma unroll
                     for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] = 0.f;
             }
-            lo_most = 0;
-            if (p.causal && p.window > 0)
-                lo_most = s.P + min((t.block * C::kRows + C::kRows - 1) / p.group, s.n - 1) - p.window + 1;
         }
         // keys [lo, hi] that row 8 n + 2 t4 + e sees
         auto visible = [&](int n, int e, int& lo, int& hi) {
             const int tok = min((t.block * C::kRows + 8 * n + 2 * t4 + e) / p.group, t.s.n - 1);
-            hi = p.causal ? P + tok : P + t.s.n - 1;
-            lo = p.causal && p.window > 0 ? P + tok - p.window + 1 : 0;
+            hi = p.causal ? t.s.P + tok : t.s.P + t.s.n - 1;
+            lo = p.causal && p.window > 0 ? t.s.P + tok - p.window + 1 : 0;
         };
 
         // The running maximum, from the largest score `top` of the lane's keys: it is raised, and
@@ -667,7 +692,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
             const uint32_t* vp = kp + kTileKeys * NG;
 #pragma unroll
             for (int a = 0; a < NG; ++a) {
-                float acc[NQ][2][4];
+                // (even and odd steps apart: two chains of dependent products instead of one)
+                float acc[NQ][2][4], odd[NQ][2][4];
 #pragma unroll
                 for (int cc = 0; cc < kGroupChunks; ++cc) {
                     const int c = a * kGroupChunks + cc;
@@ -680,11 +706,13 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                                        b2 = codes<3>(x[2 * h]), b3 = codes<3>(x[2 * h + 1]);
 #pragma unroll
                         for (int n = 0; n < NQ; ++n) {
-                            if (cc == 0)
+                            if (cc == 0) {
                                 mma_half_first(acc[n][h], a0, a1, a2, a3, qf[n][c][0], qf[n][c][1]);
-                            else
+                                mma_half_first(odd[n][h], b0, b1, b2, b3, qf[n][c][2], qf[n][c][3]);
+                            } else {
                                 mma_half(acc[n][h], a0, a1, a2, a3, qf[n][c][0], qf[n][c][1]);
-                            mma_half(acc[n][h], b0, b1, b2, b3, qf[n][c][2], qf[n][c][3]);
+                                mma_half(odd[n][h], b0, b1, b2, b3, qf[n][c][2], qf[n][c][3]);
+                            }
                         }
                     }
                 }
@@ -694,15 +722,18 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                     const float sk = bf16_lo(w), mk = bf16_hi(w);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
-                        const float* const qc = acc[n][k / 2] + 2 * (k & 1);
+                        const int i = 2 * (k & 1);
+                        const float2 qc = __fadd2_rn(make_float2(acc[n][k / 2][i], acc[n][k / 2][i + 1]),
+                                                     make_float2(odd[n][k / 2][i], odd[n][k / 2][i + 1]));
                         const float2 x = a == 0 ? make_float2(mk * qsum[n][a].x, mk * qsum[n][a].y)
                                                 : make_float2(fmaf(mk, qsum[n][a].x, sc[n][k].x), fmaf(mk, qsum[n][a].y, sc[n][k].y));
-                        sc[n][k] = make_float2(fmaf(sk, qc[0], x.x), fmaf(sk, qc[1], x.y));
+                        sc[n][k] = make_float2(fmaf(sk, qc.x, x.x), fmaf(sk, qc.y, x.y));
                     }
                 }
             }
-            if (key + kTileKeys > P || key < lo_most) {
-                // an edge of the cached keys, or of a window
+            if (flags & kEdge) {
+                // the end of the cached keys, or an edge of a window
+                const int P = t.s.P;
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
                     int lo[2], hi;
@@ -805,7 +836,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
                 return pack(x.x * w, x.y * w);
             };
-            const int tok0 = -1 - key, tok = tok0 + g, many = t.s.n;
+            const int tok0 = -1 - key, tok = tok0 + g, many = t.s.n, P = t.s.P;
             float acc[NQ][4];
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
@@ -935,16 +966,15 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 records[warp][slot] = r;
             }
         }
-        if (++stage == C::kStages) stage = 0;
+        __syncwarp();
     }
     cp_async_wait<0>();
     __syncthreads();
 
     // ---- the CTA's records, in list order: neighbours of one row block are joined
     auto record_data = [&](int i) -> const float* {
-        const uint8_t* base = i & 1 ? smem + (i / 2) * C::kStages * C::kTileBytes
-                                    : smem + kWarps * C::kStages * C::kTileBytes + (i / 2) * C::kRecord;
-        return reinterpret_cast<const float*>(base);
+        return i & 1 ? reinterpret_cast<const float*>(smem + (i / 2) * C::kStages * C::kTileBytes)
+                     : p.kept + ((size_t)blockIdx.x * kWarps + i / 2) * C::kRows * D;
     };
     constexpr int kElems = C::kRows * D;
     float* const part_stats = p.part + (size_t)gridDim.x * 2 * kElems;
@@ -1037,7 +1067,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
 template <int D, int NG, int NQ>
 cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     using C = Cfg<D, NG, NQ>;
-    constexpr int kSmem = C::kWarps * (C::kStages * C::kTileBytes + C::kRecord);
+    constexpr int kSmem = C::kWarps * C::kStages * C::kTileBytes;
     static_assert(kSmem <= 215 * 1024, "shared memory budget, beside the static part");
     static int configured_for[64] = {0};
     int dev = 0;
