@@ -223,7 +223,7 @@ pa_status get_aux_scratch(Workspace* w, cudaStream_t st, size_t bytes, void** ou
 }
 
 // The counters by which CTAs that share a row block find the last of them (one per CTA).
-constexpr int kArrivals = 1024;
+constexpr int kArrivals = pa::kRows4Grid;
 
 pa_status get_arrivals(Workspace* w, cudaStream_t st, int** out) {
     if (!w->arrivals) {

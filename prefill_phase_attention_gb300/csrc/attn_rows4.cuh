@@ -48,6 +48,10 @@ namespace rows4 {
 
 constexpr int kTileKeys = 32;  // cached rows of a tile
 constexpr int kNewKeys = 8;    // new tokens of a tile
+// Beginning and ending a row block costs a warp about as much as two tiles, so the list has
+// as many places ahead of a row block's tiles that hold none: equal shares of places are equal
+// shares of time.
+constexpr int kBlockCost = 2;
 
 template <int D, int NG, int NQ>
 struct Cfg {
@@ -61,10 +65,11 @@ struct Cfg {
     static constexpr int kCodes = kTileKeys * kRowBytes;     // bytes of a tile's codes
     static constexpr int kParams = kTileKeys * NG * 4;       // bytes of a tile's parameters
     static constexpr int kTileBytes = 2 * (kCodes + kParams);
-    static constexpr int kStages = D == 128 ? 3 : 4;
+    static constexpr int kStages = D == 128 && NQ == 1 ? 3 : 4;
     static constexpr int kRows = 8 * NQ;
     static constexpr int kRecord = kRows * D * 4;  // bytes of a partial output
-    static_assert(kStages * kTileBytes >= kRecord, "a warp's second record lies in its ring");
+    static_assert(kStages * kTileBytes >= 2 * kRecord, "a warp's records end up in its ring");
+    static_assert(2 * kWarps <= 32, "a lane per record");
 };
 
 // A row block in a warp's share.
@@ -99,7 +104,18 @@ struct Extent {
     int cached, fresh;
     int blocks;  // row blocks
     __device__ __forceinline__ int tiles() const { return cached + fresh; }
+    __device__ __forceinline__ int places() const { return blocks > 0 ? tiles() + kBlockCost : 0; }
 };
+
+// x / y and the remainder; 32 bits of x are enough nearly always.
+__device__ __forceinline__ int divide(long long x, int y, int& rest) {
+    if ((x >> 32) == 0) {
+        rest = (int)((unsigned)x % (unsigned)y);
+        return (int)((unsigned)x / (unsigned)y);
+    }
+    rest = (int)(x % y);
+    return (int)(x / y);
+}
 
 template <int NQ>
 __device__ __forceinline__ Extent extent(const Rows4Params& p, const SeqInfo& s) {
@@ -255,7 +271,8 @@ struct Feeder {
     uint32_t ring;    // this lane's place in the first stage
     uint32_t params;  // and its parameters'
     int lane;
-    int left;         // tiles of the share that are still to come
+    int left;         // places of the share that are still to come
+    int count;        // tiles that came
     int key;          // next tile if it is cached
     int whole_until;  // tiles below are whole and have no edge
     unsigned row;     // contiguous cache: row of the next cached tile
@@ -266,9 +283,9 @@ struct Feeder {
         return table ? table[i] : sequence4(p.seqs, p.cache.max_cache_len, i);
     }
     // Puts the feeder at list position `first`; `start` is that of sequence b0.
-    __device__ __forceinline__ void seek(int b0, long long start, long long first, int count) {
-        left = count;
-        key = whole_until = 0;
+    __device__ __forceinline__ void seek(int b0, long long start, long long first, int places) {
+        left = places;
+        count = key = whole_until = 0;
         flags = (C::kStages - 1) << kSlot;
         if (left == 0) return;
         Walk w;
@@ -276,19 +293,20 @@ struct Feeder {
         w.s = seq(w.b);
         w.e = extent<NQ>(p, w.s);
         for (;;) {
-            const long long all = (long long)w.e.tiles() * w.e.blocks * p.cache.n_kv_heads;
+            const long long all = (long long)w.e.places() * w.e.blocks * p.cache.n_kv_heads;
             if (first < start + all) break;
             start += all;
             ++w.b;  // the list's total says that there is one
             w.s = seq(w.b);
             w.e = extent<NQ>(p, w.s);
         }
-        const long long in = first - start;
-        const int item = (int)(in / w.e.tiles()), j = (int)(in % w.e.tiles());
+        int place;
+        const int item = divide(first - start, w.e.places(), place);
         w.kvh = item / w.e.blocks;
         w.block = item % w.e.blocks;
-        w.block_start = first - j;
-        enter(w, j);
+        w.block_start = first - place + kBlockCost;
+        if (place < kBlockCost) left -= kBlockCost - place;
+        if (left > 0) enter(w, max(0, place - kBlockCost));
         if (lane == 0) *walk = w;
         __syncwarp();
     }
@@ -348,6 +366,7 @@ struct Feeder {
         if (lane == 0) tiles[stage] = Tile{key, flags | (left == 1 ? kLast | kGoesOn : 0)};
         flags &= ~kFirst;
         --left;
+        ++count;
         if (!p.cache.block_table) {
             const size_t from = (size_t)row * C::kRowBytes + lane * 16;
 #pragma unroll
@@ -426,13 +445,14 @@ struct Feeder {
             ++w.fresh;
         }
         --left;
+        ++count;
         const bool ends = w.fresh == w.e.fresh;
         int f = flags | kEdge;
         if (ends || left == 0) f |= ends ? kLast : kLast | kGoesOn;
         if (lane == 0) tiles[stage] = Tile{at, f};
         flags &= ~kFirst;
         if (ends && left > 0) {
-            w.block_start += w.e.tiles();
+            w.block_start += w.e.places();
             if (++w.block == w.e.blocks) {
                 w.block = 0;
                 if (++w.kvh == p.cache.n_kv_heads) {
@@ -444,7 +464,8 @@ struct Feeder {
                     } while (w.e.blocks == 0);
                 }
             }
-            enter(w, 0);
+            left -= kBlockCost;
+            if (left > 0) enter(w, 0);
         }
         __syncwarp();
         if (lane == 0) *walk = w;
@@ -477,7 +498,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
         const SeqInfo s = sequence4(p.seqs, p.cache.max_cache_len, b);
         if (in_table) table[b] = s;
         const Extent e = extent<NQ>(p, s);
-        return (long long)e.tiles() * e.blocks * p.cache.n_kv_heads;
+        return (long long)e.places() * e.blocks * p.cache.n_kv_heads;
     };
     // exclusive prefix sum over the CTA; total: the sum
     auto scan = [&](long long x, long long& total) -> long long {
@@ -508,7 +529,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     if (!p.seqs.checked && blockIdx.x == 0)
         for (int b = tid; b < p.seqs.num_seqs; b += kThreads)
             if (stated_sequence(p.seqs, p.cache.max_cache_len, b).n < 0) atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
-    // shares of at least a tile per warp
+    // shares of at least a place per warp
     const long long share = max((long long)kWarps, (all + gridDim.x - 1) / gridDim.x);
     const long long from = min(all, share * blockIdx.x), to = min(all, from + share);
     if (from >= to) return;  // (the whole CTA)
@@ -532,12 +553,11 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     float* const kept = p.kept + ((size_t)blockIdx.x * kWarps + warp) * C::kRows * D;
     const long long len = to - from;
     const long long wfrom = from + len * warp / kWarps, wto = from + len * (warp + 1) / kWarps;
-    const int steps = (int)(wto - wfrom);  // (2^31 tiles of a warp would take an hour)
     constexpr int kParts = C::kRowBytes / 16;
     Feeder<D, NG, NQ> feed{p, in_table ? table : nullptr, &walks[warp], items[warp], tiles[warp],
                            ptx::smem_u32(ring) + lane / kParts * C::kRowBytes + (lane % kParts ^ swizzle<D>(lane / kParts)) * 16,
                            ptx::smem_u32(ring) + 2 * C::kCodes + lane * NG * 4, lane};
-    feed.seek(first_seq, start_of_first, wfrom, steps);
+    feed.seek(first_seq, start_of_first, wfrom, (int)(wto - wfrom));  // (2^31 tiles of a warp would take an hour)
     uint32_t qf[NQ][C::kChunks][4];  // Q as the second operand: per chunk two 16-channel steps
     float2 qsum[NQ][NG];             // sums of a group's channels of queries 2 t4, 2 t4 + 1
     float o[NQ][C::kChunks][2][4];   // O^T: channels 32 c + 4 g + 2 e (+ 1), queries 2 t4, 2 t4 + 1
@@ -549,9 +569,10 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
 
     int stage = 1;  // (the first pass fills stage 0)
 #pragma unroll 1
-    for (int i = 1 - C::kStages; i < steps; ++i, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
+    for (int i = 1 - C::kStages;; ++i, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
         feed.issue(stage == 0 ? C::kStages - 1 : stage - 1);
         if (i < 0) continue;
+        if (i >= feed.count) break;  // (the feeder is ahead)
         cp_async_wait<C::kStages - 1>();
         __syncwarp();
         const int flags = tiles[warp][stage].flags, key = tiles[warp][stage].key;
@@ -969,41 +990,51 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
         __syncwarp();
     }
     cp_async_wait<0>();
+    constexpr int kElems = C::kRows * D;
+    __syncwarp();
+    if (records[warp][0].valid) {
+        // the first record joins the second one in the ring
+        float4* const to = reinterpret_cast<float4*>(ring) + kElems / 4;
+#pragma unroll
+        for (int x = 0; x < kElems / 128; ++x) to[32 * x + lane] = __ldcg(reinterpret_cast<const float4*>(kept) + 32 * x + lane);
+    }
     __syncthreads();
 
-    // ---- the CTA's records, in list order: neighbours of one row block are joined
+    // ---- the CTA's records (one per lane), in list order: neighbours of one row block are joined
     auto record_data = [&](int i) -> const float* {
-        return i & 1 ? reinterpret_cast<const float*>(smem + (i / 2) * C::kStages * C::kTileBytes)
-                     : p.kept + ((size_t)blockIdx.x * kWarps + i / 2) * C::kRows * D;
+        return reinterpret_cast<const float*>(smem + i / 2 * C::kStages * C::kTileBytes) + (i & 1 ? 0 : kElems);
     };
-    constexpr int kElems = C::kRows * D;
-    float* const part_stats = p.part + (size_t)gridDim.x * 2 * kElems;
-    int pending[2] = {-1, -1};  // records whose row block other CTAs share: began before, goes on
-    for (int i = 0; i < 2 * kWarps;) {
-        const Record& r = records[i / 2][i & 1];
-        if (!r.valid) {
-            ++i;
-            continue;
-        }
-        int end = i + 1;
-        for (int k = i + 1; k < 2 * kWarps; ++k) {
-            const Record& x = records[k / 2][k & 1];
-            if (!x.valid) continue;
-            if (x.t.start_lo != r.t.start_lo || x.t.start_hi != r.t.start_hi) break;
-            end = k + 1;
-        }
-        const long long b0 = ((long long)r.t.start_hi << 32) | (unsigned)r.t.start_lo;
-        const bool whole = b0 >= from && b0 + r.t.tiles <= to;
+    float2* const part_stats = reinterpret_cast<float2*>(p.part + (size_t)gridDim.x * 2 * kElems);
+    unsigned valid, begins;  // of the records; where a row block's first one is
+    {
+        const bool have = lane < 2 * kWarps && records[lane / 2][lane & 1].valid;
+        valid = __ballot_sync(0xffffffffu, have);
+        const int hi = have ? records[lane / 2][lane & 1].t.start_hi : 0, lo = have ? records[lane / 2][lane & 1].t.start_lo : 0;
+        const unsigned before = valid & ((1u << lane) - 1);
+        const int prev = before ? 31 - __clz(before) : lane;
+        const int prev_hi = __shfl_sync(0xffffffffu, hi, prev), prev_lo = __shfl_sync(0xffffffffu, lo, prev);
+        begins = __ballot_sync(0xffffffffu, have && !(before != 0 && prev_hi == hi && prev_lo == lo));
+    }
+    int pending[2] = {-1, -1};  // records whose row block other CTAs share: it began before, it goes on
+    for (unsigned left = begins; left != 0; left &= left - 1) {
+        const int i = __ffs(left) - 1;
+        const unsigned others = left & (left - 1);
+        const unsigned members = valid & ~((1u << i) - 1) & (others ? (others & -others) - 1 : 0xffffffffu);
+        const Item& t = records[i / 2][i & 1].t;
+        const long long b0 = ((long long)t.start_hi << 32) | (unsigned)t.start_lo;
+        const bool whole = b0 >= from && b0 + t.tiles <= to;
         const int slot = b0 < from ? 0 : 1;  // of the partial results
         for (int x = tid * 4; x < kElems; x += kThreads * 4) {
             const int row = x / D;
             float top = -INFINITY;
-            for (int k = i; k < end; ++k)
-                if (records[k / 2][k & 1].valid) top = fmaxf(top, stats[k / 2][k & 1][row].x);
+            for (unsigned m = members; m != 0; m &= m - 1) {
+                const int k = __ffs(m) - 1;
+                top = fmaxf(top, stats[k / 2][k & 1][row].x);
+            }
             float sum = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = i; k < end; ++k) {
-                if (!records[k / 2][k & 1].valid) continue;
+            for (unsigned m = members; m != 0; m &= m - 1) {
+                const int k = __ffs(m) - 1;
                 const float2 st = stats[k / 2][k & 1][row];
                 const float w = st.x == -INFINITY ? 0.f : exp2_approx(st.x - top);
                 const float4 y = *reinterpret_cast<const float4*>(record_data(k) + x);
@@ -1012,28 +1043,27 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
             }
             if (whole) {
                 const float f = 1.f / sum;
-                store_row<D, NQ>(p, r.t, row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-                if (x % D == 0) store_lse<NQ>(p, r.t, row, top, sum);
+                store_row<D, NQ>(p, t, row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+                if (x % D == 0) store_lse<NQ>(p, t, row, top, sum);
             } else {
                 const size_t at = (size_t)blockIdx.x * 2 + slot;
                 __stcg(reinterpret_cast<float4*>(p.part + at * kElems + x), v);
-                if (x % D == 0) __stcg(reinterpret_cast<float2*>(part_stats) + at * C::kRows + row, make_float2(top, sum));
+                if (x % D == 0) __stcg(part_stats + at * C::kRows + row, make_float2(top, sum));
             }
         }
         if (!whole) pending[slot] = i;
-        i = end;
     }
 
-    // ---- row blocks that several CTAs share: the last to arrive joins them
+    // ---- row blocks that several CTAs share: the last to arrive joins them, in list order
 #pragma unroll 1
     for (int k = 0; k < 2; ++k) {
         if (pending[k] < 0) continue;  // (the whole CTA)
         const Item& t = records[pending[k] / 2][pending[k] & 1].t;
         const long long b0 = ((long long)t.start_hi << 32) | (unsigned)t.start_lo;
         const int c0 = (int)(b0 / share), c1 = (int)((b0 + t.tiles - 1) / share);
-        __threadfence();
         __syncthreads();
         if (tid == 0) {
+            __threadfence();  // (what the CTA wrote, by way of the barrier)
             arrived = atomicAdd(p.arrivals + c0, 1);
             __threadfence();
         }
@@ -1041,19 +1071,23 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
         if (arrived != c1 - c0) continue;
         if (tid == 0) p.arrivals[c0] = 0;
         auto at = [&](int c) -> size_t { return (size_t)c * 2 + (c == c0 ? 1 : 0); };
+        float2* const st = reinterpret_cast<float2*>(smem);  // (the records are done with)
+        const int pieces = c1 - c0 + 1;
+        for (int x = tid; x < pieces * C::kRows; x += kThreads)
+            st[x] = __ldcg(part_stats + at(c0 + x / C::kRows) * C::kRows + x % C::kRows);
+        __syncthreads();
         for (int x = tid * 4; x < kElems; x += kThreads * 4) {
             const int row = x / D;
             float top = -INFINITY;
-#pragma unroll 8
-            for (int c = c0; c <= c1; ++c) top = fmaxf(top, __ldcg(reinterpret_cast<const float2*>(part_stats) + at(c) * C::kRows + row).x);
+            for (int c = 0; c < pieces; ++c) top = fmaxf(top, st[c * C::kRows + row].x);
             float sum = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-            for (int c = c0; c <= c1; ++c) {
-                const float2 st = __ldcg(reinterpret_cast<const float2*>(part_stats) + at(c) * C::kRows + row);
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + at(c) * kElems + x));
-                const float w = st.x == -INFINITY ? 0.f : exp2_approx(st.x - top);
-                sum = fmaf(w, st.y, sum);
+            for (int c = 0; c < pieces; ++c) {
+                const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + at(c0 + c) * kElems + x));
+                const float2 one = st[c * C::kRows + row];
+                const float w = one.x == -INFINITY ? 0.f : exp2_approx(one.x - top);
+                sum = fmaf(w, one.y, sum);
                 v.x = fmaf(w, y.x, v.x), v.y = fmaf(w, y.y, v.y), v.z = fmaf(w, y.z, v.z), v.w = fmaf(w, y.w, v.w);
             }
             const float f = 1.f / sum;
@@ -1068,6 +1102,7 @@ template <int D, int NG, int NQ>
 cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     using C = Cfg<D, NG, NQ>;
     constexpr int kSmem = C::kWarps * C::kStages * C::kTileBytes;
+    static_assert(kSmem >= kRows4Grid * C::kRows * (int)sizeof(float2), "statistics of the partial results to be joined");
     static_assert(kSmem <= 215 * 1024, "shared memory budget, beside the static part");
     static int configured_for[64] = {0};
     int dev = 0;

@@ -235,7 +235,7 @@ struct Rows4Params {
     int* arrivals;
     float* kept;  // [grid][kRows4Warps] of 8 * row_tiles rows of D floats: records of a CTA's warps
 };
-constexpr int kRows4Warps = 16;  // at most
+constexpr int kRows4Warps = 16, kRows4Grid = 256;  // at most
 template <int D>
 cudaError_t launch_attn_rows4_d(const Rows4Params& p, int row_tiles, int grid, cudaStream_t stream);
 template <>
