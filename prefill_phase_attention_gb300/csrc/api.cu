@@ -1438,6 +1438,9 @@ pa_status read_cache4(const pa_cache4* cache, const Options& o, int head_dim, in
 // other's launch and its scheduler's.
 constexpr int kRowsOfRowKernel = 32, kExcessRows = 256;
 
+// Entries of a block table that every CTA of the row kernel reads whole.
+constexpr int kOwnTable = 32768;
+
 constexpr int kCacheSpans = 4;
 void cache_spans(const pa::Cache4& c, const Options& o, int num_seqs, int head_dim, bool written, Span* out) {
     const size_t rows = cache_rows(o, num_seqs, c.max_cache_len, c.n_kv_heads);
@@ -1615,7 +1618,10 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     const int sched = auto_schedule(total_q, num_seqs, n_heads, n_kv_heads, false, sms) == 1 ? 1 : 2;
     const long long units = tiles ? unit_bound(total_q, num_seqs, n_heads, n_kv_heads, sched) : 0;
     if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
-    const bool check = !tiles && (o.block_table || o.rope_theta > 0.f);
+    // The row kernel's CTAs check small tables themselves, each all of them; for larger ones,
+    // and for the rotary prologue, a kernel ahead does.
+    const bool check = !tiles && (o.rope_theta > 0.f || (o.block_table && (num_seqs > pa::kRows4Seqs ||
+                                                                           (long long)num_seqs * o.max_blocks > kOwnTable)));
     const StreamLock lock(dev, stream);
     Workspace* const ws = lock.ws;
     s = grow_workspace(*ws, stream, tiles || check ? num_seqs : 0, (int)units);

@@ -108,13 +108,13 @@ struct Extent {
 };
 
 // x / y and the remainder; 32 bits of x are enough nearly always.
-__device__ __forceinline__ int divide(long long x, int y, int& rest) {
+__device__ __forceinline__ long long divide(long long x, int y, int& rest) {
     if ((x >> 32) == 0) {
         rest = (int)((unsigned)x % (unsigned)y);
-        return (int)((unsigned)x / (unsigned)y);
+        return (long long)((unsigned)x / (unsigned)y);
     }
     rest = (int)(x % y);
-    return (int)(x / y);
+    return x / y;
 }
 
 template <int NQ>
@@ -301,7 +301,7 @@ struct Feeder {
             w.e = extent<NQ>(p, w.s);
         }
         int place;
-        const int item = divide(first - start, w.e.places(), place);
+        const int item = (int)divide(first - start, w.e.places(), place);
         w.kvh = item / w.e.blocks;
         w.block = item % w.e.blocks;
         w.block_start = first - place + kBlockCost;
@@ -488,16 +488,53 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     __shared__ long long warp_sums[kWarps];
     __shared__ long long start_of_first;
     __shared__ int first_seq, arrived;
+    __shared__ bool joins[2];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
     griddep_wait();
 
     // ---- the list: its length, and the sequence that this CTA's share begins in
     const bool in_table = p.seqs.num_seqs <= kRows4Seqs;
-    auto tiles_of = [&](int b) -> long long {
+    if (in_table) {
+        if (tid < p.seqs.num_seqs) {
+            SeqInfo s = p.seqs.checked ? p.seqs.checked[tid] : stated_sequence(p.seqs, p.cache.max_cache_len, tid);
+            if (s.n < 0) s.pad = 1, s.n = 0;  // (pad: to be reported)
+            table[tid] = s;
+        }
+        if (p.cache.block_table && !p.seqs.checked) {
+            // a sequence with a table entry outside the pool is skipped whole: 16 entries a thread
+            // at a time
+            constexpr int kChunk = 16;
+            if (tid == 0) arrived = 0;
+            __syncthreads();
+            if (tid < p.seqs.num_seqs && table[tid].n > 0)
+                atomicMax(&arrived, ((table[tid].P + table[tid].n - 1) >> p.cache.block_log2) / kChunk + 1);
+            __syncthreads();
+            const unsigned chunks = (unsigned)arrived;  // of the longest sequence
+            for (unsigned x = tid; x < chunks * (unsigned)p.seqs.num_seqs; x += kThreads) {
+                const int b = x / chunks, i0 = x % chunks * kChunk;
+                const SeqInfo s = table[b];
+                const int end = s.n > 0 ? ((s.P + s.n - 1) >> p.cache.block_log2) + 1 : 0;
+                const int32_t* entries = p.cache.block_table + (size_t)b * p.cache.max_blocks;
+                int id[kChunk];
+                bool bad = false;
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) id[i] = i0 + i < end ? __ldg(entries + i0 + i) : 0;
+#pragma unroll
+                for (int i = 0; i < kChunk; ++i) bad |= (unsigned)id[i] >= (unsigned)p.cache.num_blocks;
+                if (bad) table[b].pad = 1;  // (several threads, one value)
+            }
+            __syncthreads();
+            if (tid < p.seqs.num_seqs && table[tid].pad) table[tid].n = 0;
+        }
+        if (!p.seqs.checked && blockIdx.x == 0 && tid < p.seqs.num_seqs && table[tid].pad)
+            atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
+    } else if (!p.seqs.checked && blockIdx.x == 0) {
+        for (int b = tid; b < p.seqs.num_seqs; b += kThreads)
+            if (stated_sequence(p.seqs, p.cache.max_cache_len, b).n < 0) atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
+    }
+    auto places_of = [&](int b) -> long long {
         if (b >= p.seqs.num_seqs) return 0;
-        const SeqInfo s = sequence4(p.seqs, p.cache.max_cache_len, b);
-        if (in_table) table[b] = s;
-        const Extent e = extent<NQ>(p, s);
+        const Extent e = extent<NQ>(p, in_table ? table[b] : sequence4(p.seqs, p.cache.max_cache_len, b));
         return (long long)e.places() * e.blocks * p.cache.n_kv_heads;
     };
     // exclusive prefix sum over the CTA; total: the sum
@@ -512,9 +549,11 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
         __syncthreads();
         long long before = 0;
         total = 0;
+#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += warp_sums[w];
-            total += warp_sums[w];
+            const long long y = warp_sums[w];
+            if (w < warp) before += y;
+            total += y;
         }
         __syncthreads();
         return before + inc - x;
@@ -522,15 +561,13 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     long long all = 0, mine = 0, excl = 0;
     for (int b0 = 0; b0 < p.seqs.num_seqs; b0 += kThreads) {
         long long total;
-        mine = tiles_of(b0 + tid);
+        mine = places_of(b0 + tid);
         excl = all + scan(mine, total);
         all += total;
     }
-    if (!p.seqs.checked && blockIdx.x == 0)
-        for (int b = tid; b < p.seqs.num_seqs; b += kThreads)
-            if (stated_sequence(p.seqs, p.cache.max_cache_len, b).n < 0) atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
     // shares of at least a place per warp
-    const long long share = max((long long)kWarps, (all + gridDim.x - 1) / gridDim.x);
+    int rest;
+    const long long share = max((long long)kWarps, (long long)divide(all + gridDim.x - 1, gridDim.x, rest));
     const long long from = min(all, share * blockIdx.x), to = min(all, from + share);
     if (from >= to) return;  // (the whole CTA)
     if (in_table) {
@@ -539,7 +576,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
         long long before = 0;
         for (int b0 = 0; b0 < p.seqs.num_seqs && before <= from; b0 += kThreads) {
             long long total;
-            const long long x = tiles_of(b0 + tid), ex = before + scan(x, total);
+            const long long x = places_of(b0 + tid), ex = before + scan(x, total);
             if (x > 0 && ex <= from && from < ex + x) first_seq = b0 + tid, start_of_first = ex;
             before += total;
         }
@@ -1055,46 +1092,72 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     }
 
     // ---- row blocks that several CTAs share: the last to arrive joins them, in list order
-#pragma unroll 1
+    if (pending[0] < 0 && pending[1] < 0) return;  // (the whole CTA)
+    int c0[2], pieces[2];
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
-        if (pending[k] < 0) continue;  // (the whole CTA)
+        if (pending[k] < 0) continue;
         const Item& t = records[pending[k] / 2][pending[k] & 1].t;
         const long long b0 = ((long long)t.start_hi << 32) | (unsigned)t.start_lo;
-        const int c0 = (int)(b0 / share), c1 = (int)((b0 + t.tiles - 1) / share);
-        __syncthreads();
-        if (tid == 0) {
-            __threadfence();  // (what the CTA wrote, by way of the barrier)
-            arrived = atomicAdd(p.arrivals + c0, 1);
-            __threadfence();
+        c0[k] = (int)(b0 / share);
+        pieces[k] = (int)((b0 + t.tiles - 1) / share) - c0[k] + 1;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        __threadfence();  // (what the CTA wrote, by way of the barrier)
+        int old[2] = {-1, -1};
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (pending[k] >= 0) old[k] = atomicAdd(p.arrivals + c0[k], 1);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            joins[k] = pending[k] >= 0 && old[k] == pieces[k] - 1;
+            if (joins[k]) p.arrivals[c0[k]] = 0;
         }
-        __syncthreads();
-        if (arrived != c1 - c0) continue;
-        if (tid == 0) p.arrivals[c0] = 0;
-        auto at = [&](int c) -> size_t { return (size_t)c * 2 + (c == c0 ? 1 : 0); };
-        float2* const st = reinterpret_cast<float2*>(smem);  // (the records are done with)
-        const int pieces = c1 - c0 + 1;
-        for (int x = tid; x < pieces * C::kRows; x += kThreads)
-            st[x] = __ldcg(part_stats + at(c0 + x / C::kRows) * C::kRows + x % C::kRows);
-        __syncthreads();
+        __threadfence();
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < 2; ++k) {
+        if (!joins[k]) continue;
+        const Item& t = records[pending[k] / 2][pending[k] & 1].t;
         for (int x = tid * 4; x < kElems; x += kThreads * 4) {
             const int row = x / D;
-            float top = -INFINITY;
-            for (int c = 0; c < pieces; ++c) top = fmaxf(top, st[c * C::kRows + row].x);
-            float sum = 0.f;
+            float top = -INFINITY, sum = 0.f;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-            for (int c = 0; c < pieces; ++c) {
-                const float4 y = __ldcg(reinterpret_cast<const float4*>(p.part + at(c0 + c) * kElems + x));
-                const float2 one = st[c * C::kRows + row];
-                const float w = one.x == -INFINITY ? 0.f : exp2_approx(one.x - top);
-                sum = fmaf(w, one.y, sum);
-                v.x = fmaf(w, y.x, v.x), v.y = fmaf(w, y.y, v.y), v.z = fmaf(w, y.z, v.z), v.w = fmaf(w, y.w, v.w);
+            constexpr int kAtOnce = 8;
+            for (int c = 0; c < pieces[k]; c += kAtOnce) {
+                float4 y[kAtOnce];
+                float2 st[kAtOnce];
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    st[i] = make_float2(-INFINITY, 0.f);
+                    y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c + i < pieces[k]) {
+                        const size_t at = (size_t)(c0[k] + c + i) * 2 + (c + i == 0 ? 1 : 0);
+                        st[i] = __ldcg(part_stats + at * C::kRows + row);
+                        y[i] = __ldcg(reinterpret_cast<const float4*>(p.part + at * kElems + x));
+                    }
+                }
+                float most_here = top;
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) most_here = fmaxf(most_here, st[i].x);
+                const float use = most_here == -INFINITY ? 0.f : most_here;  // (no key yet: the weights are 0)
+                const float f = exp2_approx(top - use);
+                top = most_here;
+                sum *= f;
+                v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const float w = exp2_approx(st[i].x - use);
+                    sum = fmaf(w, st[i].y, sum);
+                    v.x = fmaf(w, y[i].x, v.x), v.y = fmaf(w, y[i].y, v.y), v.z = fmaf(w, y[i].z, v.z), v.w = fmaf(w, y[i].w, v.w);
+                }
             }
             const float f = 1.f / sum;
             store_row<D, NQ>(p, t, row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
             if (x % D == 0) store_lse<NQ>(p, t, row, top, sum);
         }
-        __syncthreads();
     }
 }
 
@@ -1102,7 +1165,6 @@ template <int D, int NG, int NQ>
 cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     using C = Cfg<D, NG, NQ>;
     constexpr int kSmem = C::kWarps * C::kStages * C::kTileBytes;
-    static_assert(kSmem >= kRows4Grid * C::kRows * (int)sizeof(float2), "statistics of the partial results to be joined");
     static_assert(kSmem <= 215 * 1024, "shared memory budget, beside the static part");
     static int configured_for[64] = {0};
     int dev = 0;
