@@ -472,8 +472,6 @@ void fill_fwd(pa::FwdParams& p, const void* k, const void* v, void* cache_k, voi
     p.max_blocks = o.max_blocks;
     p.num_blocks = o.num_blocks;
     p.kv_quant = o.kv_quant;
-    p.params_k = p.params_v = nullptr;
-    p.groups = 0;
     p.wait_timeout_test = o.wait_timeout_test;
     p.alt = sched != 2;
     p.unit_slots = sched == 1 ? 1 : pa::kSlots;
@@ -504,7 +502,7 @@ void fill_schedule(pa::ScheduleArgs& sa, const int32_t* cu_seqlens_q, const int3
     sa.max_units = scr.max_units;
     sa.num_ctas = ctas;
     sa.unit_slots = slots;
-    sa.few_tokens = 0;
+    sa.taken = nullptr;
     sa.block_table = o.block_table;
     sa.block_size = o.block_size;
     sa.max_blocks = o.max_blocks;
@@ -1429,14 +1427,17 @@ pa_status read_cache4(const pa_cache4* cache, const Options& o, int head_dim, in
     return PA_OK;
 }
 
-// Attention over a 4-bit cache has two kernels.  The row kernel reads a sequence's cache
-// once per 16 query rows, at the rate of HBM; the tile kernel expands every cached tile to
-// bf16, which takes a unit as long as two such passes, for up to 256 rows.  So sequences
-// of up to 32 rows (of one token, if that has more) go to the row kernel and the others
-// to the tile kernel.  The host does not know the lengths: where all rows but one token of
-// each sequence are few, the row kernel takes every sequence, which costs less than the
-// other's launch and its scheduler's.
-constexpr int kRowsOfRowKernel = 32, kExcessRows = 256;
+// Attention over a 4-bit cache takes two ways.  The row kernel reads a sequence's cache once
+// per 16 query rows, a part of it in every CTA.  The other way, for long chunks, expands
+// the sequence's cache to bf16 once (a pool of blocks in the workspace) and runs the
+// tensor-core kernel over it.  Sequences of up to kRowsOfRowKernel rows go the first way, the
+// others the second as far as the pool reaches.  The host does not know the lengths: where
+// all rows but one token of each sequence are at most kExcessRows, the row kernel takes every
+// sequence, which costs less than the other way's launches.
+constexpr int kRowsOfRowKernel = 256, kExcessRows = 1024;
+
+// The pool holds at least one sequence of max_cache_len tokens, and up to this many bytes of more.
+constexpr long long kPoolBytes = 1ll << 30;
 
 // Entries of a block table that every CTA of the row kernel reads whole.
 constexpr int kOwnTable = 32768;
@@ -1606,11 +1607,10 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     const int sms = sm_count(dev, &s);
     if (s != PA_OK) return s;
     const int group = n_heads / n_kv_heads;
-    // Which kernels run: see kRowsOfRowKernel.
+    // Which way sequences go: see kRowsOfRowKernel.
     const int few = std::max(1, kRowsOfRowKernel / group);
     const bool one = num_seqs == 1;
     const bool tiles = one ? total_q > few : ((long long)total_q - num_seqs) * group > kExcessRows;
-    const bool rows = !(one && tiles);
     // the row kernel's blocks have 16 rows where sequences have more than 8 on average (of
     // those that it takes, if the tile kernel runs too)
     const int row_tiles = group > 8 || (!tiles && (long long)total_q * group > 8LL * num_seqs) ? 2 : 1;
@@ -1622,21 +1622,38 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     // and for the rotary prologue, a kernel ahead does.
     const bool check = !tiles && (o.rope_theta > 0.f || (o.block_table && (num_seqs > pa::kRows4Seqs ||
                                                                            (long long)num_seqs * o.max_blocks > kOwnTable)));
+    // the pool of expanded blocks
+    const long long seq_blocks = ((long long)max_cache_len + pa::kBlock4 - 1) / pa::kBlock4;
+    const size_t block_bytes = (size_t)n_kv_heads * pa::kBlock4 * head_dim * 2;  // of K or V
+    long long pool_blocks = 0;
+    if (tiles) {
+        const long long most = std::min<long long>(num_seqs, total_q / (few + 1)) * seq_blocks;
+        pool_blocks = std::max(seq_blocks, std::min(most, kPoolBytes / (long long)(2 * block_bytes)));
+        if (pool_blocks * n_kv_heads >= (1LL << 31) || num_seqs * seq_blocks >= (1LL << 31))
+            return fail(PA_ERR_UNSUPPORTED, "max_cache_len * n_kv_heads or num_seqs * max_cache_len is too large for a long chunk");
+    }
     const StreamLock lock(dev, stream);
     Workspace* const ws = lock.ws;
     s = grow_workspace(*ws, stream, tiles || check ? num_seqs : 0, (int)units);
     if (s != PA_OK) return s;
     pa::Rows4Params p;
-    void* part = nullptr;
-    size_t part_floats = 0;
-    if (rows) {
-        s = get_arrivals(ws, stream, &p.arrivals);
-        if (s != PA_OK) return s;
-        part_floats = (size_t)grid * 2 * 8 * row_tiles * (head_dim + 2);
-        const size_t kept = (size_t)grid * pa::kRows4Warps * 8 * row_tiles * head_dim;
-        s = get_aux_scratch(ws, stream, (part_floats + kept) * sizeof(float), &part);
-        if (s != PA_OK) return s;
-    }
+    s = get_arrivals(ws, stream, &p.arrivals);
+    if (s != PA_OK) return s;
+    const size_t part_bytes = align_up((size_t)grid * 2 * 8 * row_tiles * (head_dim + 2) * sizeof(float), 256);
+    const size_t kept_bytes = align_up((size_t)grid * pa::kRows4Warps * 8 * row_tiles * head_dim * sizeof(float), 256);
+    const size_t seq_bytes = tiles ? align_up((size_t)num_seqs * sizeof(pa::SeqInfo), 256) : 0;
+    const size_t taken_bytes = tiles ? align_up(((size_t)num_seqs + 1) * sizeof(int), 256) : 0;
+    const size_t table_bytes = tiles ? align_up((size_t)num_seqs * seq_blocks * sizeof(int), 256) : 0;
+    const size_t owner_bytes = align_up((size_t)pool_blocks * sizeof(int2), 256);
+    const size_t pool_bytes = align_up((size_t)pool_blocks * block_bytes, 256);
+    void* aux = nullptr;
+    s = get_aux_scratch(ws, stream, part_bytes + kept_bytes + seq_bytes + taken_bytes + table_bytes + owner_bytes +
+                                        2 * pool_bytes, &aux);
+    if (s != PA_OK) return s;
+    char* at = static_cast<char*>(aux);
+    auto take = [&](size_t bytes) { char* const x = at; at += bytes; return x; };
+    p.part = reinterpret_cast<float*>(take(part_bytes));
+    p.kept = reinterpret_cast<float*>(take(kept_bytes));
     void* rope = nullptr;
     if (o.rope_theta > 0.f) {
         s = get_rope_scratch(ws, stream, (q_rows + k_rows) * head_dim * 2, &rope);
@@ -1644,17 +1661,27 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     }
     const Scratch scr{static_cast<pa::WorkspaceHeader*>(ws->ptr), ws_seqs(*ws), ws_units(*ws), ws->max_units,
                       ws_seq_scratch(*ws)};
-    p.seqs = pa::Sequences4{cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q,
-                            tiles || check ? scr.seqs : nullptr, scr.hdr};
+    p.seqs = pa::Sequences4{cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, check ? scr.seqs : nullptr, scr.hdr};
+    p.taken = nullptr;
     int launches = 0;
-    const int tile_grid = (int)std::min<long long>(sms, units);
+    pa::Expand4Params x;
     if (tiles) {
-        pa::ScheduleArgs sa;
-        fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, max_cache_len, n_heads, n_kv_heads,
-                      head_dim, causal, o, scr, sched, tile_grid);
-        sa.few_tokens = rows ? few : 0;
-        e = pa::launch_build_schedule(sa, stream);
-        if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
+        p.seqs.checked = reinterpret_cast<pa::SeqInfo*>(take(seq_bytes));
+        x.seqs = p.seqs;
+        x.cache = c;
+        x.few_tokens = few;
+        x.window = causal ? o.window : 0;
+        x.pool_blocks = (int)pool_blocks;
+        x.table_blocks = (int)seq_blocks;
+        x.taken = reinterpret_cast<int*>(take(taken_bytes));
+        x.blocks = x.taken + num_seqs;
+        x.table = reinterpret_cast<int32_t*>(take(table_bytes));
+        x.owners = reinterpret_cast<int2*>(take(owner_bytes));
+        x.k = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
+        x.v = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
+        p.taken = x.taken;
+        e = pa::launch_plan_expand4(x, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "plan launch");
         ++launches;
     } else if (check) {
         e = pa::launch_check_sequences4(p.seqs, c, true, stream);
@@ -1668,23 +1695,41 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         ++launches;
     }
     if (tiles) {
+        Options po = o;  // the pool, as a paged bf16 cache
+        po.block_table = x.table;
+        po.block_size = pa::kBlock4;
+        po.max_blocks = (int)seq_blocks;
+        po.num_blocks = (int)pool_blocks;
+        const int pool_len = (int)std::min<long long>(seq_blocks * pa::kBlock4, kMaxTokens);
+        const int tile_grid = (int)std::min<long long>(sms, units);
+        pa::ScheduleArgs sa;
+        fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, pool_len, n_heads, n_kv_heads,
+                      head_dim, causal, po, scr, sched, tile_grid);
+        sa.taken = x.taken;
+        e = pa::launch_build_schedule(sa, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
+        e = pa::launch_expand4(x, head_dim, sms, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "expansion launch");
         pa::FwdParams fp;
-        fill_fwd(fp, k, v, c.k, c.v, out, lse, scr, max_cache_len, n_heads, n_kv_heads, scale, causal, o, sched);
-        fp.kv_quant = 2;
-        fp.params_k = c.kp;
-        fp.params_v = c.vp;
-        fp.groups = c.groups;
-        e = pa::encode_fwd_maps(fp, q, total_q, num_seqs, head_dim, o.num_blocks);
+        fill_fwd(fp, k, v, x.k, x.v, out, lse, scr, pool_len, n_heads, n_kv_heads, scale, causal, po, sched);
+        e = pa::encode_fwd_maps(fp, q, total_q, num_seqs, head_dim, po.num_blocks);
         if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
-        e = head_dim == 32   ? pa::launch_attn_tiles4_d<32>(fp, tile_grid, stream)
-            : head_dim == 64 ? pa::launch_attn_tiles4_d<64>(fp, tile_grid, stream)
-                             : pa::launch_attn_tiles4_d<128>(fp, tile_grid, stream);
+        e = pa::launch_attn_fwd(fp, head_dim, tile_grid, stream);
         if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-        ++launches;
+        // the new tokens into the cache (the row kernel writes those of its sequences itself)
+        pa::Copy4Params w;
+        w.seqs = p.seqs;
+        w.cache = c;
+        w.k = static_cast<const __nv_bfloat16*>(k);
+        w.v = static_cast<const __nv_bfloat16*>(v);
+        w.k_out = w.v_out = nullptr;
+        e = pa::launch_write_cache4(w, head_dim, sms, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
+        launches += 4;
         g_last_schedule = sched;
     }
     g_last_launches = launches;
-    if (!rows) return PA_OK;
+    if (one && tiles) return PA_OK;  // (the pool has room for it)
     p.cache = c;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.k = static_cast<const __nv_bfloat16*>(k);
@@ -1696,9 +1741,6 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     p.scale_log2 = scale * 1.4426950408889634f;
     p.causal = causal;
     p.window = o.window;
-    p.most_tokens = tiles ? few : INT_MAX;
-    p.part = static_cast<float*>(part);
-    p.kept = p.part + part_floats;
     e = pa::launch_attn_rows4(p, head_dim, row_tiles, grid, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
     ++g_last_launches;

@@ -517,137 +517,12 @@ __device__ __noinline__ void quant_tile_rows(const uint8_t* tile, int8_t* codes,
     }
 }
 
-// Bytes of a row of codes of a quantised cache (1: int8, 2: 4 bits).
-template <int D, int kQuant>
-constexpr int code_row_bytes() {
-    return kQuant == 2 ? D / 2 : D;
-}
-
-// 4-bit cache, prefix tile: a lane's 32 channels of kRows rows at a time -- the row, the
-// lane's part of it, and the words of parameters it needs of the tile's rows.
-template <int D>
-struct Tile4 {
-    static constexpr int kLanes = D / 32;        // of a row
-    static constexpr int kRows = 32 / kLanes;    // of a batch
-    static constexpr int kBatches = kBlockN / kRows;
-};
-
-// Parameters of the lane's batches of rows [kb, kb + 128) of a sequence's prefix; rows
-// outside [0, P) get 0, 0 and so expand to zeros.
-template <int D, bool kPaged>
-__device__ __forceinline__ void load_params4(const FwdParams& p, const uint32_t* params, const Unit& u, int kb, int P,
-                                             int lane, uint32_t (&w)[Tile4<D>::kBatches]) {
-    using T = Tile4<D>;
-    const int group = (lane % T::kLanes) * p.groups / T::kLanes;
-    const size_t head0 = (size_t)u.b * p.n_kv_heads + u.kvh;
-    int id = -1;  // paged: the block of rows [8 lane, 8 lane + 8)
-    if (kPaged && lane < kBlockN / 8 && kb + 8 * lane < P)
-        id = __ldg(p.block_table + (size_t)u.b * p.max_blocks + ((kb + 8 * lane) >> p.block_log2));
-#pragma unroll
-    for (int i = 0; i < T::kBatches; ++i) {
-        const int r = i * T::kRows + lane / T::kLanes, pos = kb + r;
-        bool there = pos >= 0 && pos < P;
-        size_t row;
-        if (kPaged) {
-            const int blk = __shfl_sync(0xffffffffu, id, r >> 3);
-            there = there && (unsigned)blk < (unsigned)p.num_blocks;
-            row = (((size_t)blk * p.n_kv_heads + u.kvh) << p.block_log2) + (pos & ((1 << p.block_log2) - 1));
-        } else {
-            row = head0 * p.max_cache_len + pos;
-        }
-        w[i] = there ? __ldg(params + row * p.groups + group) : 0u;
-    }
-}
-
-// Expands a tile of 4-bit codes in place (one warp): the box of codes (row r = D / 2
-// bytes) lies in the upper quarter of the stage, m + code s goes into the swizzled bf16
-// tile, rounded once.  code + 128 is a bf16 whose low mantissa bits are the code; less
-// 128 it is the code, and one fused multiply-add of bf16 pairs rounds the value.  Rows go in
-// increasing order, each batch read before it is written: the bf16 image of row r ends
-// at 2 D (r + 1) of the stage (its last column chunk's share of it), the codes of row r + 1
-// start at 1.5 D 128 + D (r + 1) / 2, never before it.
-template <int D>
-__device__ __forceinline__ void expand_tile4(uint8_t* stage, uint32_t (&w)[Tile4<D>::kBatches], int lane) {
-    using C = Cfg<D>;
-    using T = Tile4<D>;
-    constexpr int kGroup = 4;  // batches read before any is written
-    constexpr int kChunkGran = C::kChunkCols / 8;
-    const uint8_t* codes = stage + C::kTileBytes - kBlockN * (D / 2);
-    const int part = lane % T::kLanes;
-    // a short loop (unrolled whole it takes five times as long: a warp that runs every
-    // instruction once waits for each to be fetched); the words move up by a group a pass
-#pragma unroll 1
-    for (int i0 = 0; i0 < T::kBatches; i0 += kGroup) {
-        uint4 x[kGroup];
-#pragma unroll
-        for (int b = 0; b < kGroup; ++b)
-            x[b] = *reinterpret_cast<const uint4*>(codes + ((i0 + b) * 32 + lane) * 16);
-        __syncwarp();
-#pragma unroll
-        for (int b = 0; b < kGroup; ++b) {
-            const int r = (i0 + b) * T::kRows + lane / T::kLanes;
-            const uint32_t word[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
-            const uint32_t s2 = __byte_perm(w[b], 0, 0x1010), m2 = __byte_perm(w[b], 0, 0x3232);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                // channels 32 part + 8 q ...: pairs (i, i + 4), put in order below
-                uint32_t v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t y = ((word[q] >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-                    const uint32_t c128 = 0x43004300u;
-                    const __nv_bfloat162 c = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&y),
-                                                     *reinterpret_cast<const __nv_bfloat162*>(&c128));
-                    const __nv_bfloat162 o = __hfma2(c, *reinterpret_cast<const __nv_bfloat162*>(&s2),
-                                                     *reinterpret_cast<const __nv_bfloat162*>(&m2));
-                    v[i] = *reinterpret_cast<const uint32_t*>(&o);
-                }
-                const int g = part * 4 + q, c = g / kChunkGran, gg = g % kChunkGran;
-                const int phys = D >= 64 ? (gg ^ (r & 7)) : (gg ^ ((r >> 1) & 3));
-                *reinterpret_cast<uint4*>(stage + c * C::kChunkBytes + r * C::kRowBytes + phys * 16) =
-                    make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410),
-                               __byte_perm(v[0], v[1], 0x7632), __byte_perm(v[2], v[3], 0x7632));
-            }
-        }
-#pragma unroll
-        for (int i = 0; i + kGroup < T::kBatches; ++i) w[i] = w[i + kGroup];
-        __syncwarp();
-    }
-}
-
-// 4-bit cache write: rows [lo_row, lo_row + nrows) of a staged bf16 tile, in the cache's
-// format, to the rows row_index(i) (~0: skip).
-template <int D, class RowIndex>
-__device__ __noinline__ void quant4_tile_rows(const uint8_t* tile, uint8_t* codes, uint32_t* params, int groups,
-                                              RowIndex row_index, int lo_row, int nrows, int lane) {
-    using C = Cfg<D>;
-    constexpr int kGran = D / 8;  // lanes per row
-    constexpr int kRows = 32 / kGran;
-    constexpr int kChunkGran = C::kChunkCols / 8;
-    const int g = lane % kGran, group_lanes = kGran / groups;
-    const int c = g / kChunkGran, gg = g % kChunkGran;
-    for (int i0 = 0; i0 < nrows; i0 += kRows) {
-        const int i = i0 + lane / kGran;
-        const bool valid = i < nrows;
-        const int r = lo_row + (valid ? i : 0);
-        const int phys = D >= 64 ? (gg ^ (r & 7)) : (gg ^ ((r >> 1) & 3));
-        const uint4 x[1] = {*reinterpret_cast<const uint4*>(tile + c * C::kChunkBytes + r * C::kRowBytes + phys * 16)};
-        uint32_t code[1], word;
-        quantise(x, group_lanes, code, &word);
-        if (!valid) continue;
-        const size_t row = row_index(i);
-        if (row == ~size_t(0)) continue;
-        reinterpret_cast<uint32_t*>(codes + row * (D / 2))[g] = code[0];
-        if (g % group_lanes == 0) params[row * groups + g / group_lanes] = word;
-    }
-}
-
 // Contiguous cache, one KV ring (K or V): waits for the stage, then
 // TMA-loads tile j (index in the sequence) of unit u from the cache (prefix
 // tiles; z = its [slot, head] plane) or from the new tokens' k/v.  Out of line: the K and the V loader
 // share one copy of this code, which keeps the kernel's hot code within the
 // instruction caches.
-template <int D, int kQuant>
+template <int D, bool kQuant>
 __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, WorkspaceHeader* hdr, uint8_t* ring,
                                           int stages, uint64_t* full, uint64_t* empty, const CUtensorMap* tm_cache,
                                           const CUtensorMap* tm_new, int* last_parity, uint32_t t, int j,
@@ -658,11 +533,10 @@ __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, Work
     const int kb = tile_key_base<false>(j, s.P, np);
     if (!wait_bar(&empty[st], ph ^ 1, ctl, hdr)) return false;
     if (kQuant && j < np) {
-        // codes of the prefix tile into the stage's upper half (4 bits: upper quarter; one
-        // box of 128 rows), expanded to bf16 by the cache writer
-        constexpr int kCodeBytes = kBlockN * code_row_bytes<D, kQuant>();
-        mbar_arrive_expect_tx(&full[st], kCodeBytes);
-        tma_load_3d(ring + (st + 1) * C::kTileBytes - kCodeBytes, tm_cache, &full[st], 0, kb, z);
+        // int8 codes of the prefix tile into the stage's upper half (one box of
+        // 128 rows x D bytes), expanded to bf16 by the cache writer
+        mbar_arrive_expect_tx(&full[st], kBlockN * D);
+        tma_load_3d(ring + st * C::kTileBytes + C::kTileBytes / 2, tm_cache, &full[st], 0, kb, z);
         last_parity[st] = (int)ph;
         return true;
     }
@@ -728,13 +602,10 @@ __device__ __forceinline__ void claim_unit_ext(const FwdParamsX& p, WorkspaceHea
 template <bool kExt>
 using KernelParams = std::conditional_t<kExt, FwdParamsX, FwdParams>;
 
-// kQuant: the cache is bf16 (0), int8 (1) or in 4 bits (2).
-template <int D, bool kPaged, int kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
+template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ KernelParams<kExt> p) {
     using C = Cfg<D>;
-    constexpr bool kQ8 = kQuant == 1, kQ4 = kQuant == 2;
-    static_assert(!(kAlt && kQ8), "the merge exchange shares storage with the int8 scale ring");
-    static_assert(!(kExt && kQ4), "no long-context variant over a 4-bit cache");
+    static_assert(!(kAlt && kQuant), "the merge exchange shares storage with the int8 scale ring");
     // K stages in use.  With an int8 cache the K writer publishes each tile's row
     // scales in a 4-deep ring (Ctrl::kscale) that the softmax warps read after
     // S; it writes the scales of tile t + 4 only once that tile has landed, i.e.
@@ -743,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     // 3 stages that PV follows every slot's softmax of tile t: the ring slot is
     // free.  (bf16 caches use no scale ring.)  A ring of two (long-context variant at
     // head_dim 128): see its writer.
-    constexpr int kStK = kQ8 && C::kStagesK > 3 ? 3 : C::kStagesK;
+    constexpr int kStK = kQuant && C::kStagesK > 3 ? 3 : C::kStagesK;
     // paged bf16 cache, two column chunks: prefix tiles staged block by block
     constexpr bool kGrp = kPaged && !kQuant && C::kChunks == 2;
     const int unit_slots = kAlt ? p.unit_slots : kSlots;  // Q tiles of a unit
@@ -756,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     Ctrl* ctl = reinterpret_cast<Ctrl*>(v_smem + C::kStagesV * C::kTileBytes);
     OwnUnits* own = reinterpret_cast<OwnUnits*>(ctl + 1);  // kExt
     // V's scales go into P (kVScale); slots of tile t in the rings of K's and V's scales
-    constexpr bool kVScale = kExt && kQ8;
+    constexpr bool kVScale = kExt && kQuant;
     constexpr int kScaleSlots = kVScale && D == 128 ? 2 : 4;
     auto kscale_slot = [&](uint32_t t) -> float* { return ctl->kscale[t & (kScaleSlots - 1)]; };
     auto vscale_slot = [&](uint32_t t) -> float* {
@@ -1013,17 +884,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         const int kb = tile_key_base<true>(jj, s.P, ug.np);
                         uint8_t* stage = ring + st * C::kTileBytes;
                         if (kQuant && jj < ug.np) {
-                            // codes, one box of br rows per block, into the stage's upper half
-                            // (4 bits: quarter; expanded to bf16 by the cache writer)
-                            constexpr int kRow = code_row_bytes<D, kQuant>();
+                            // int8 codes, one box of br rows x D bytes per block, into the
+                            // stage's upper half (expanded to bf16 by the cache writer)
                             const int boxes = (min(kBlockN, s.P - kb) + br - 1) >> br_log2;
-                            if (gleader) mbar_arrive_expect_tx(&full[st], boxes * br * kRow);
+                            if (gleader) mbar_arrive_expect_tx(&full[st], boxes * br * D);
                             __syncwarp(gmask);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int box = gl + 16 * h;
                                 if (box < boxes)
-                                    tma_load_3d(stage + C::kTileBytes - kBlockN * kRow + box * br * kRow, tm_cache, &full[st], 0,
+                                    tma_load_3d(stage + C::kTileBytes / 2 + box * br * D, tm_cache, &full[st], 0,
                                                 (kb + box * br) & bmask, (h ? id1 : id0) * p.n_kv_heads + u.kvh);
                             }
                         } else if (kGrp && jj < ug.np) {
@@ -1237,14 +1107,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             const int ntiles = ug.ntiles;
             if (!warp_wait(&ctl->q_full, u_it & 1, ctl, hdr)) break;
             if constexpr (kAlt) if (ug.alt) {
-                // (bf16 and 4-bit caches) V tile tj, index jt in the sequence, ready for PV
+                // (bf16 cache only) V tile tj, index jt in the sequence, ready for PV
                 auto wait_v = [&](uint32_t tj, int jt) -> bool {
                     const int vst = tj % C::kStagesV;
-                    if (kQ4 && jt < ug.np) {
-                        const bool got = warp_wait(&ctl->v_conv[vst], (vcpar >> vst) & 1, ctl, hdr);
-                        vcpar ^= 1u << vst;
-                        return got;
-                    }
                     if (kPaged && paged_tail_tile(jt, s.P, ug.np)) {
                         const bool got = warp_wait(&ctl->v_fix[vst], (fixpar >> vst) & 1, ctl, hdr);
                         fixpar ^= 1u << vst;
@@ -1395,40 +1260,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             const int np = ug.np;
             const int q_end = min(us.u.q0 + unit_slots * tps, us.s.n);
             bool ok = true;
-            // 4-bit cache: the parameters of the unit's next prefix tile, fetched while the one
-            // before is expanded
-            uint32_t next4[kQ4 ? Tile4<D>::kBatches : 1] = {};
-            auto fetch4 = [&](int j) {
-                if constexpr (kQ4)
-                    if (j < np)
-                        load_params4<D, kPaged>(p, is_k ? p.params_k : p.params_v, us.u, tile_key_base<kPaged>(j, us.s.P, np),
-                                                us.s.P, lane, next4);
-            };
-            for (int jr = kQ4 ? -1 : 0; jr < ug.ntiles; ++jr, ++t) {
-                const int j = jr < 0 ? 0 : tile_at(ug, jr);  // tile index in the sequence
+            for (int jr = 0; jr < ug.ntiles; ++jr, ++t) {
+                const int j = tile_at(ug, jr);  // tile index in the sequence
                 const int st = t % stages;
-                if constexpr (kQ4) {
-                    uint32_t w[Tile4<D>::kBatches];
-#pragma unroll
-                    for (int i = 0; i < Tile4<D>::kBatches; ++i) w[i] = next4[i];
-                    if (jr + 1 < ug.ntiles) fetch4(tile_at(ug, jr + 1));
-                    if (jr < 0) {
-                        --t;  // (no tile yet)
-                        continue;
-                    }
-                    if (j < np) {
-                        if (!warp_wait(&full[st], (t / stages) & 1, ctl, hdr)) { ok = false; break; }
-                        expand_tile4<D>(ring + st * C::kTileBytes, w, lane);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(is_k ? &ctl->k_conv[st] : &ctl->v_conv[st]);
-                            mbar_arrive(&empty[st]);
-                        }
-                        continue;
-                    }
-                }
-                if (kQ8 && j < np) {
+                if (kQuant && j < np) {
                     // int8 prefix tile: expand the codes for the MMA.  V rows
                     // become code * scale; K rows stay the (exact) codes and
                     // their scales go to the scale ring, folded into the scores.
@@ -1516,22 +1351,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 int lo_row, nrows;
                 if (own_rows(j, np, us.u.q0, q_end, lo_row, nrows)) {
                     const int first_tok = (j - np) * kBlockN + lo_row;  // token index within the sequence
-                    if constexpr (kQ4) {
-                        const int32_t* tab = p.block_table + (size_t)us.u.b * p.max_blocks;
-                        const int pos0 = us.s.P + first_tok, lg = p.block_log2, Hk = p.n_kv_heads, kvh = us.u.kvh;
-                        const int nb = p.num_blocks;
-                        const size_t row0 = ((size_t)us.u.b * Hk + kvh) * p.max_cache_len + pos0;
-                        quant4_tile_rows<D>(ring + st * C::kTileBytes, reinterpret_cast<uint8_t*>(cache),
-                                            is_k ? p.params_k : p.params_v, p.groups,
-                                            [=](int i) -> size_t {
-                                                if (!kPaged) return row0 + i;
-                                                const int pos = pos0 + i;
-                                                const int blk = __ldg(tab + (pos >> lg));
-                                                if ((unsigned)blk >= (unsigned)nb) return ~size_t(0);
-                                                return (((size_t)blk * Hk + kvh) << lg) + (pos & ((1 << lg) - 1));
-                                            },
-                                            lo_row, nrows, lane);
-                    } else if (kQ8 && kPaged) {
+                    if (kQuant && kPaged) {
                         const int32_t* tab = p.block_table + (size_t)us.u.b * p.max_blocks;
                         const int pos0 = us.s.P + first_tok, lg = p.block_log2, Hk = p.n_kv_heads, kvh = us.u.kvh;
                         const int nb = p.num_blocks;
@@ -1544,7 +1364,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                                                return (((size_t)blk * Hk + kvh) << lg) + (pos & ((1 << lg) - 1));
                                            },
                                            lo_row, nrows, lane);
-                    } else if (kQ8) {
+                    } else if (kQuant) {
                         const size_t row0 = ((size_t)us.u.b * p.n_kv_heads + us.u.kvh) * p.max_cache_len +
                                             us.s.P + first_tok;
                         quant_tile_rows<D>(ring + st * C::kTileBytes, reinterpret_cast<int8_t*>(cache),
@@ -1572,7 +1392,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     // int8 cache: one ks_full phase per K tile (none for this one's
                     // scales), only after the tile landed, so that the ring never
                     // runs two phases ahead of a softmax warp
-                    if (kQ8 && is_k) mbar_arrive(&ctl->ks_full[t & 3]);
+                    if (kQuant && is_k) mbar_arrive(&ctl->ks_full[t & 3]);
                     mbar_arrive(&empty[st]);
                 }
             }
@@ -1968,7 +1788,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 const int jrel = ug.a[slot] + j;  // tile index in the unit's stream
                 const int jt = tile_at(ug, jrel);  // tile index in the sequence
                 const uint32_t tc = tg0 + jrel;
-                if (kQ8 && jt < np) {
+                if (kQuant && jt < np) {
                     // int8 prefix tile: S holds q . code; scale column c by its row's scale
                     if (!warp_wait(&ctl->ks_full[tc & 3], (tc >> 2) & 1, ctl, hdr)) { ok = false; break; }
                     const float4* ksc = reinterpret_cast<const float4*>(kscale_slot(tc));
@@ -2145,7 +1965,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-#if !defined(PA_ATTN_LONG) && !defined(PA_ATTN_TILES4)
+#ifndef PA_ATTN_LONG
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -2192,11 +2012,11 @@ cudaError_t encode_pool_by_block(CUtensorMap* m, const void* ptr, uint64_t bs, u
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-#endif
+#endif  // PA_ATTN_LONG
 
-template <int D, bool kPaged, int kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
+template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
 cudaError_t launch_d(const KernelParams<kExt>& p, int grid, cudaStream_t st) {
-    constexpr int kSmem = smem_bytes<D>((kExt ? (int)sizeof(OwnUnits) : 0) + (kExt && kQuant == 1 ? scale_ring_bytes<D>() : 0));
+    constexpr int kSmem = smem_bytes<D>((kExt ? (int)sizeof(OwnUnits) : 0) + (kExt && kQuant ? scale_ring_bytes<D>() : 0));
     static_assert(kSmem <= 232448, "shared memory budget");
     static int configured_for[64] = {0};
     int dev = 0;
@@ -2224,7 +2044,7 @@ cudaError_t launch_d(const KernelParams<kExt>& p, int grid, cudaStream_t st) {
 
 }  // namespace
 
-#if !defined(PA_ATTN_LONG) && !defined(PA_ATTN_TILES4)
+#ifndef PA_ATTN_LONG
 cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_seqs, int head_dim, int num_blocks) {
     const uint32_t cc = head_dim >= 64 ? 64 : 32;
     const CUtensorMapSwizzle sw = head_dim >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -2237,15 +2057,13 @@ cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_se
     if (e != cudaSuccess) return e;
     e = encode3d(&p.tm_v, p.v, D, Hk, T, D * 2, Hk * D * 2, cc, 1, kBlockN, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     if (e != cudaSuccess) return e;
-    // bytes of a quantised row: int8 codes, or 4-bit codes two to a byte
-    const uint64_t row = p.kv_quant == 2 ? D / 2 : D;
     if (p.block_table && p.kv_quant) {
-        // pools [num_blocks, Hk, bs, row] viewed (row, bs, num_blocks * Hk), box (row, min(bs, 128), 1)
+        // int8 pools [num_blocks, Hk, bs, D] viewed (D, bs, num_blocks * Hk), box (D, min(bs, 128), 1)
         const uint64_t bs = 1ull << p.block_log2, Z = (uint64_t)num_blocks * Hk;
-        e = encode3d(&p.tm_ck, p.cache_k, row, bs, Z, row, bs * row, (uint32_t)row, p.box_rows, 1, CU_TENSOR_MAP_SWIZZLE_NONE,
+        e = encode3d(&p.tm_ck, p.cache_k, D, bs, Z, D, bs * D, (uint32_t)D, p.box_rows, 1, CU_TENSOR_MAP_SWIZZLE_NONE,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_DATA_TYPE_UINT8);
         if (e != cudaSuccess) return e;
-        return encode3d(&p.tm_cv, p.cache_v, row, bs, Z, row, bs * row, (uint32_t)row, p.box_rows, 1, CU_TENSOR_MAP_SWIZZLE_NONE,
+        return encode3d(&p.tm_cv, p.cache_v, D, bs, Z, D, bs * D, (uint32_t)D, p.box_rows, 1, CU_TENSOR_MAP_SWIZZLE_NONE,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_DATA_TYPE_UINT8);
     }
     if (p.block_table && D == 128) {
@@ -2265,11 +2083,11 @@ cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_se
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
     }
     if (p.kv_quant) {
-        // codes [B, Hk, cap, row] viewed (row, cap, B*Hk), box (row, 128, 1), no swizzle
-        e = encode3d(&p.tm_ck, p.cache_k, row, cap, (uint64_t)num_seqs * Hk, row, cap * row, (uint32_t)row, kBlockN, 1,
+        // int8 codes [B, Hk, cap, D] viewed (D, cap, B*Hk), box (D, 128, 1), no swizzle
+        e = encode3d(&p.tm_ck, p.cache_k, D, cap, (uint64_t)num_seqs * Hk, D, cap * D, (uint32_t)D, kBlockN, 1,
                      CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_DATA_TYPE_UINT8);
         if (e != cudaSuccess) return e;
-        return encode3d(&p.tm_cv, p.cache_v, row, cap, (uint64_t)num_seqs * Hk, row, cap * row, (uint32_t)row, kBlockN, 1,
+        return encode3d(&p.tm_cv, p.cache_v, D, cap, (uint64_t)num_seqs * Hk, D, cap * D, (uint32_t)D, kBlockN, 1,
                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_DATA_TYPE_UINT8);
     }
     e = encode3d(&p.tm_ck, p.cache_k, D, cap, (uint64_t)num_seqs * Hk, D * 2, cap * D * 2, cc, kBlockN, 1, sw,
@@ -2325,15 +2143,6 @@ cudaError_t launch_attn_fwd(const FwdParams& p, int head_dim, int grid, cudaStre
         case 128: return launch_dim<128>(p, grid, st);
         default: return cudaErrorInvalidValue;
     }
-}
-#elif defined(PA_ATTN_TILES4)
-// attn_tiles4_*.cu include this file with PA_ATTN_TILES4 = the head_dim they compile the
-// kernel over a 4-bit cache for.
-template <>
-cudaError_t launch_attn_tiles4_d<PA_ATTN_TILES4>(const FwdParams& p, int grid, cudaStream_t st) {
-    constexpr int D = PA_ATTN_TILES4;
-    if (p.block_table) return p.alt ? launch_d<D, true, 2, true>(p, grid, st) : launch_d<D, true, 2>(p, grid, st);
-    return p.alt ? launch_d<D, false, 2, true>(p, grid, st) : launch_d<D, false, 2>(p, grid, st);
 }
 #else
 // attn_long_*.cu include this file with PA_ATTN_LONG = the head_dim they compile

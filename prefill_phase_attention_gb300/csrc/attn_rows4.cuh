@@ -107,6 +107,13 @@ struct Extent {
     __device__ __forceinline__ int places() const { return blocks > 0 ? tiles() + kBlockCost : 0; }
 };
 
+// A sequence of this kernel's (n = 0: another kernel's, or skipped).
+__device__ __forceinline__ SeqInfo sequence_of(const Rows4Params& p, int b) {
+    SeqInfo s = sequence4(p.seqs, p.cache.max_cache_len, b);
+    if (p.taken && p.taken[b]) s.n = 0;
+    return s;
+}
+
 // x / y and the remainder; 32 bits of x are enough nearly always.
 __device__ __forceinline__ long long divide(long long x, int y, int& rest) {
     if ((x >> 32) == 0) {
@@ -120,7 +127,7 @@ __device__ __forceinline__ long long divide(long long x, int y, int& rest) {
 template <int NQ>
 __device__ __forceinline__ Extent extent(const Rows4Params& p, const SeqInfo& s) {
     Extent e{0, 0, 0, 0};
-    if (s.n == 0 || s.n > p.most_tokens) return e;
+    if (s.n == 0) return e;
     const int lo = p.causal && p.window > 0 ? max(0, s.P - p.window + 1) : 0;  // oldest key of the first token
     e.first_tile = lo / kTileKeys;
     e.cached = max(0, (s.P + kTileKeys - 1) / kTileKeys - e.first_tile);
@@ -280,7 +287,7 @@ struct Feeder {
     int ids, next_ids;  // paged: blocks of the 8-row pieces of this and the next 256 positions
 
     __device__ __forceinline__ SeqInfo seq(int i) const {
-        return table ? table[i] : sequence4(p.seqs, p.cache.max_cache_len, i);
+        return table ? table[i] : sequence_of(p, i);
     }
     // Puts the feeder at list position `first`; `start` is that of sequence b0.
     __device__ __forceinline__ void seek(int b0, long long start, long long first, int places) {
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     const bool in_table = p.seqs.num_seqs <= kRows4Seqs;
     if (in_table) {
         if (tid < p.seqs.num_seqs) {
-            SeqInfo s = p.seqs.checked ? p.seqs.checked[tid] : stated_sequence(p.seqs, p.cache.max_cache_len, tid);
+            SeqInfo s = p.seqs.checked ? sequence_of(p, tid) : stated_sequence(p.seqs, p.cache.max_cache_len, tid);
             if (s.n < 0) s.pad = 1, s.n = 0;  // (pad: to be reported)
             table[tid] = s;
         }
@@ -534,7 +541,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     }
     auto places_of = [&](int b) -> long long {
         if (b >= p.seqs.num_seqs) return 0;
-        const Extent e = extent<NQ>(p, in_table ? table[b] : sequence4(p.seqs, p.cache.max_cache_len, b));
+        const Extent e = extent<NQ>(p, in_table ? table[b] : sequence_of(p, b));
         return (long long)e.places() * e.blocks * p.cache.n_kv_heads;
     };
     // exclusive prefix sum over the CTA; total: the sum

@@ -148,6 +148,25 @@ __global__ void __launch_bounds__(kCopyThreads) write_cache4_kernel(const Copy4P
     }
 }
 
+// The values of 16 channels: a code as the low bits of 2^23; the product with s is exact, the sum
+// rounds to fp32 and then once to bf16.
+__device__ __forceinline__ void expand16(const uint2& codes, uint32_t word, uint4 (&out)[2]) {
+    const float s = bf16_lo(word), m = bf16_hi(word);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t c = half ? codes.y : codes.x;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = __uint_as_float(0x4b000000u | ((c >> (8 * e)) & 15u)) - 8388608.f;
+            const float b = __uint_as_float(0x4b000000u | ((c >> (8 * e + 4)) & 15u)) - 8388608.f;
+            const __nv_bfloat162 v = __floats2bfloat162_rn(fmaf(a, s, m), fmaf(b, s, m));
+            w[e] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        out[half] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) read_cache4_kernel(const Copy4Params p) {
     __shared__ Places at;
@@ -179,26 +198,19 @@ __global__ void __launch_bounds__(kCopyThreads) read_cache4_kernel(const Copy4Pa
         for (int u = 0; u < kInFlight; ++u) {
             if (!there[u]) continue;
             const int it = i0 + u * kStep, h = r.head(it);
-            const float s = bf16_lo(word[u]), m = bf16_hi(word[u]);
             uint4* dst = reinterpret_cast<uint4*>((h < Hk ? p.k_out : p.v_out) +
                                                   ((size_t)(t0 + r.token(it)) * Hk + (h < Hk ? h : h - Hk)) * D) + 2 * r.part;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t c = half ? codes[u].y : codes[u].x;
-                uint32_t out[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    // a code as the low bits of 2^23; the product with s is exact, the sum rounds
-                    // to fp32 and then once to bf16
-                    const float a = __uint_as_float(0x4b000000u | ((c >> (8 * e)) & 15u)) - 8388608.f;
-                    const float b = __uint_as_float(0x4b000000u | ((c >> (8 * e + 4)) & 15u)) - 8388608.f;
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(fmaf(a, s, m), fmaf(b, s, m));
-                    out[e] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-                dst[half] = make_uint4(out[0], out[1], out[2], out[3]);
-            }
+            uint4 out[2];
+            expand16(codes[u], word[u], out);
+            dst[0] = out[0];
+            dst[1] = out[1];
         }
     }
+}
+
+// The first block of a sequence that its queries see.
+__device__ __forceinline__ int first_block(const Expand4Params& p, const SeqInfo& s) {
+    return p.window > 0 ? max(0, s.P - p.window + 1) / kBlock4 : 0;
 }
 
 // One block per sequence: its metadata, and the table entries of the call's tokens
@@ -219,6 +231,111 @@ __global__ void __launch_bounds__(128) check_sequences4_kernel(const Sequences4 
     if (threadIdx.x == 0) {
         a.checked[b] = bad ? SeqInfo{0, 0, 0, 0} : s;
         if (bad) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
+    }
+}
+
+// One block: checks the sequences, and lays out the pool.
+__global__ void __launch_bounds__(1024) plan_expand4_kernel(const Expand4Params p) {
+    __shared__ int warp_sums[32], in_use;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const Cache4& c = p.cache;
+    if (tid == 0) in_use = 0;
+    griddep_wait();
+    // a warp per sequence
+    for (int b = warp; b < p.seqs.num_seqs; b += 32) {
+        const SeqInfo s = stated_sequence(p.seqs, c.max_cache_len, b);
+        bool bad = s.n < 0;
+        if (c.block_table && s.n > 0) {
+            const int end = ((s.P + s.n - 1) >> c.block_log2) + 1;
+            const int32_t* table = c.block_table + (size_t)b * c.max_blocks;
+#pragma unroll 8
+            for (int i = lane; i < end; i += 32) bad |= (unsigned)__ldg(table + i) >= (unsigned)c.num_blocks;
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) {
+            p.seqs.checked[b] = bad ? SeqInfo{0, 0, 0, 0} : s;
+            if (bad) atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
+        }
+    }
+    __syncthreads();
+    int base = 0;  // blocks of the sequences before
+    for (int b0 = 0; b0 < p.seqs.num_seqs; b0 += 1024) {
+        const int b = b0 + tid;
+        SeqInfo s{0, 0, 0, 0};
+        if (b < p.seqs.num_seqs) s = p.seqs.checked[b];
+        const bool wanted = s.n > p.few_tokens;
+        const int first = first_block(p, s);
+        // (sums past the pool saturate: a sequence's blocks are at most 2^23)
+        int need = wanted ? (s.P + s.n + kBlock4 - 1) / kBlock4 - first : 0, inc = need;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc = min(inc + y, 1 << 29);
+        }
+        if (lane == 31) warp_sums[warp] = inc;
+        __syncthreads();
+        int before = base;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) before = min(before + warp_sums[w], 1 << 29);
+            base = min(base + warp_sums[w], 1 << 29);
+        }
+        const int at = min(before + inc, 1 << 29) - need;
+        const bool fits = wanted && before + inc < 1 << 29 && at + need <= p.pool_blocks;
+        if (b < p.seqs.num_seqs) p.taken[b] = fits ? at + 1 : 0;
+        if (fits) atomicMax(&in_use, at + need);  // (those that fit are the first ones: no gaps)
+        __syncthreads();
+    }
+    if (tid == 0) *p.blocks = in_use;
+    for (int b = warp; b < p.seqs.num_seqs; b += 32) {
+        const int at = p.taken[b] - 1;
+        if (at < 0) continue;
+        const SeqInfo s = p.seqs.checked[b];
+        const int first = first_block(p, s), end = (s.P + s.n + kBlock4 - 1) / kBlock4;
+        for (int i = lane; i < end; i += 32) {
+            p.table[(size_t)b * p.table_blocks + i] = i < first ? 0 : at + i - first;
+            if (i >= first) p.owners[at + i - first] = make_int2(b, i * kBlock4);
+        }
+    }
+}
+
+// A block takes 128 rows (a block of the pool, one head of K or V) at a time.
+template <int D>
+__global__ void __launch_bounds__(kCopyThreads) expand4_kernel(const Expand4Params p) {
+    constexpr int kLanes = D / 16, kStep = kCopyThreads / kLanes;
+    constexpr int kPasses = kBlock4 / kStep > 0 ? kBlock4 / kStep : 1;
+    const Cache4& c = p.cache;
+    const int Hk = c.n_kv_heads, group_lanes = kLanes / c.groups;
+    const int part = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
+    griddep_wait();
+    const long long units = 2ll * Hk * *p.blocks;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+        const int block = (int)(u / (2 * Hk)), h = (int)(u % (2 * Hk)), kvh = h < Hk ? h : h - Hk;
+        const int2 owner = p.owners[block];
+        const int P = p.seqs.checked[owner.x].P;
+        uint2 codes[kPasses];
+        uint32_t word[kPasses];
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int pos = owner.y + i * kStep + first;
+            codes[i] = make_uint2(0, 0);
+            word[i] = 0;
+            if (i * kStep + first < kBlock4 && pos < P) {
+                const size_t row = row4(c, owner.x, kvh, pos);
+                if (row == ~size_t(0)) continue;
+                codes[i] = __ldg(reinterpret_cast<const uint2*>((h < Hk ? c.k : c.v) + row * (D / 2)) + part);
+                word[i] = __ldg((h < Hk ? c.kp : c.vp) + row * c.groups + part / group_lanes);
+            }
+        }
+        __nv_bfloat16* const pool = (h < Hk ? p.k : p.v) + ((size_t)block * Hk + kvh) * kBlock4 * D;
+#pragma unroll
+        for (int i = 0; i < kPasses; ++i) {
+            const int r = i * kStep + first;
+            if (r >= kBlock4 || owner.y + r >= P) continue;
+            uint4 out[2];
+            expand16(codes[i], word[i], out);
+            uint4* dst = reinterpret_cast<uint4*>(pool + (size_t)r * D) + 2 * part;
+            dst[0] = out[0];
+            dst[1] = out[1];
+        }
     }
 }
 
@@ -268,6 +385,19 @@ cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cuda
         case 32: return launch_copy(read_cache4_kernel<32>, p, sms, stream);
         case 64: return launch_copy(read_cache4_kernel<64>, p, sms, stream);
         default: return launch_copy(read_cache4_kernel<128>, p, sms, stream);
+    }
+}
+
+cudaError_t launch_plan_expand4(const Expand4Params& p, cudaStream_t stream) {
+    return launch_after(plan_expand4_kernel, dim3(1), 1024, stream, p);
+}
+
+cudaError_t launch_expand4(const Expand4Params& p, int head_dim, int sms, cudaStream_t stream) {
+    const dim3 grid((unsigned)std::min((long long)sms * 6, 2ll * p.cache.n_kv_heads * p.pool_blocks));
+    switch (head_dim) {
+        case 32: return launch_after(expand4_kernel<32>, grid, kCopyThreads, stream, p);
+        case 64: return launch_after(expand4_kernel<64>, grid, kCopyThreads, stream, p);
+        default: return launch_after(expand4_kernel<128>, grid, kCopyThreads, stream, p);
     }
 }
 

@@ -74,7 +74,7 @@ struct ScheduleArgs {
     int max_units;  // capacity of the unit list
     int num_ctas;   // CTAs of the attention launch (persistent: at most one per SM)
     int unit_slots; // Q tiles per unit: 2 (plain kernel) or 1 (alternating variant)
-    int few_tokens; // sequences of up to as many new tokens get no units (0: all do)
+    const int* taken;  // sequences with 0 get no units; nullptr: all do
     // paged cache (block_table == nullptr: contiguous slots)
     const int32_t* block_table;  // [num_seqs][max_blocks]
     int block_size, max_blocks, num_blocks;

@@ -66,11 +66,7 @@ struct FwdParams {
     // scale of each cache row ([B, Hk, cap])
     float* scale_k;
     float* scale_v;
-    int kv_quant;  // 0: bf16, 1: int8, 2: 4 bits
-    // 4-bit cache: cache_k/cache_v hold its codes, these the parameters of each row's groups
-    uint32_t* params_k;
-    uint32_t* params_v;
-    int groups;
+    int kv_quant;
     int wait_timeout_test;  // test hook: CTA 0 waits on a barrier nothing completes
     // alternating variant (bf16 cache): units whose rows fit one Q tile split
     // their KV tiles between both softmax slots (even / odd) and merge the two
@@ -84,16 +80,6 @@ struct FwdParams {
 // num_blocks: blocks in the pool when p.block_table is set (else unused).
 cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_seqs, int head_dim, int num_blocks);
 cudaError_t launch_attn_fwd(const FwdParams& p, int head_dim, int grid, cudaStream_t st);
-
-// The same kernel over a 4-bit cache.
-template <int D>
-cudaError_t launch_attn_tiles4_d(const FwdParams& p, int grid, cudaStream_t st);
-template <>
-cudaError_t launch_attn_tiles4_d<32>(const FwdParams& p, int grid, cudaStream_t st);
-template <>
-cudaError_t launch_attn_tiles4_d<64>(const FwdParams& p, int grid, cudaStream_t st);
-template <>
-cudaError_t launch_attn_tiles4_d<128>(const FwdParams& p, int grid, cudaStream_t st);
 
 // Scheduler of the long-context variant.
 struct LongScheduleArgs : ScheduleArgs {
@@ -202,6 +188,29 @@ cudaError_t launch_evict(const EvictArgs& a, int sms, int* launches, cudaStream_
 // table entry up to a sequence's last token counts, else only those of the call's tokens.
 cudaError_t launch_check_sequences4(const Sequences4& a, const Cache4& c, bool whole, cudaStream_t stream);
 
+// Long chunks: their sequences' cached rows expanded to bf16, in a pool of blocks of
+// kBlock4 tokens [pool_blocks][n_kv_heads][kBlock4][head_dim] that the attention kernel reads as
+// a paged cache.
+constexpr int kBlock4 = 128;
+struct Expand4Params {
+    Sequences4 seqs;  // checked: where the plan writes them
+    Cache4 cache;
+    int few_tokens;   // sequences of up to as many new tokens are not taken
+    int window;
+    int pool_blocks;
+    int table_blocks;  // of a sequence
+    int* taken;        // [num_seqs] 1 + the sequence's first block of the pool, 0: not taken
+    int32_t* table;    // [num_seqs][table_blocks]
+    int2* owners;      // [pool_blocks] sequence and first position
+    int* blocks;       // in use
+    __nv_bfloat16* k;
+    __nv_bfloat16* v;
+};
+// Checks the sequences (like launch_check_sequences4, whole) and gives those that are taken their
+// blocks, in order, until the pool is full.
+cudaError_t launch_plan_expand4(const Expand4Params& p, cudaStream_t stream);
+cudaError_t launch_expand4(const Expand4Params& p, int head_dim, int sms, cudaStream_t stream);
+
 // Rows of packed tokens [total_q, n_kv_heads, head_dim] into the cache, or back.
 struct Copy4Params {
     Sequences4 seqs;
@@ -228,7 +237,7 @@ struct Rows4Params {
     int n_heads, group;
     float scale_log2;
     int causal, window;
-    int most_tokens;  // sequences with more new tokens are another kernel's
+    const int* taken;  // sequences that another kernel takes (not 0); nullptr: none
     // partial results that CTAs hand one another: [grid][2] of 8 * row_tiles rows of D
     // floats, then as many (maximum, sum) pairs; arrivals[grid] is zero between calls
     float* part;

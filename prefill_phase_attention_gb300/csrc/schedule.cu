@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
     const int tid = threadIdx.x;
     const int nthr = blockDim.x;
     const int tpu = a.unit_slots * (kBlockM / a.group);  // query tokens per unit
-    auto query_blocks = [&](int n) { return n > a.few_tokens ? (n + tpu - 1) / tpu : 0; };
+    auto query_blocks = [&](int b, int n) { return !a.taken || a.taken[b] ? (n + tpu - 1) / tpu : 0; };
     // the next kernel (launched with programmatic stream serialisation) may
     // start its prologue now; it waits for this kernel before reading the list
     griddep_launch();
@@ -57,7 +57,8 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
         const int lane = tid & 31, nwarps = nthr >> 5;
         for (int b = tid >> 5; b < a.num_seqs; b += nwarps) {
             const long long lk = (long long)a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
-            const long long used = lk > 0 ? (lk + a.block_size - 1) / a.block_size : 0;
+            const bool taken = !a.taken || a.taken[b];  // (another has no table here)
+            const long long used = lk > 0 && taken ? (lk + a.block_size - 1) / a.block_size : 0;
             const int nb = used < a.max_blocks ? (int)used : a.max_blocks;
             bool bad = false;
             for (int L = lane; L < nb; L += 32) {
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
             si.n = ok ? (int)n : 0;
             si.P = ok ? P : 0;
         }
-        const int nblk = query_blocks(si.n);
+        const int nblk = b < a.num_seqs ? query_blocks(b, si.n) : 0;
         int chunk_total;
         const int excl = block_exclusive_scan(nblk, warp_sums, &chunk_total);
         si.pad = blocks_before + excl;
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
         const int lane = tid & 31, nwarps = nthr >> 5;
         for (int b = tid >> 5; b < a.num_seqs; b += nwarps) {
             const SeqInfo si = seqs[b];
-            const int nblk = query_blocks(si.n);
+            const int nblk = query_blocks(b, si.n);
             long long c = 0;
             int mx = 0;
             for (int i = lane; i < nblk; i += 32) {
@@ -153,7 +154,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
 
     // Pass 3: each sequence claims its range of the list from its bin ...
     for (int b = tid; b < a.num_seqs; b += nthr) {
-        const int nblk = query_blocks(seqs[b].n);
+        const int nblk = query_blocks(b, seqs[b].n);
         if (nblk > 0) seq_scratch[b] = atomicAdd(&hist[seq_scratch[b]], nblk * a.n_kv_heads);
     }
     __threadfence_block();
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
         const int b = block_owner(seqs, a.num_seqs, i);
         const SeqInfo si = seqs[b];
         const int blk = i - si.pad;
-        const int nblk = query_blocks(si.n);
+        const int nblk = query_blocks(b, si.n);
         const int hg = seq_group[b];
         const int g0 = kvh - kvh % hg;                 // first head of kvh's group
         const int gsize = min(hg, a.n_kv_heads - g0);  // heads in the group
