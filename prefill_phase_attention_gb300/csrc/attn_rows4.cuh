@@ -58,7 +58,7 @@ struct Cfg {
     // As many warps as registers (16: 128 a thread, 12: 168) and shared memory allow: the
     // instructions of a tile take most of the time that its bytes do, so the issue slots
     // have to be filled.
-    static constexpr int kWarps = NQ == 2 ? 8 : NG > 1 ? 12 : 16;
+    static constexpr int kWarps = NQ == 2 ? (D == 128 ? 8 : 12) : NG > 1 ? 12 : 16;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kChunks = D / 32;
     static constexpr int kRowBytes = D / 2;

@@ -77,20 +77,25 @@ __device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
     const __nv_bfloat162 v = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
     return *reinterpret_cast<const uint32_t*>(&v);
 }
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 v = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 // Quantises 8 kWords channels (bf16 pairs x) of a row whose groups are spread over
 // `lanes` consecutive lanes each: codes[w] holds those of channels 8 w ..., *params the
 // group's word (the same in its lanes).  All lanes of the warp.
 template <int kWords>
 __device__ __forceinline__ void quantise(const uint4 (&x)[kWords], int lanes, uint32_t (&codes)[kWords], uint32_t* params) {
-    // (minimum, -maximum) of the pairs, of the lane, of the group
-    uint32_t lo2 = x[0].x, hi2 = x[0].x ^ 0x80008000u;
+    uint32_t lo2 = x[0].x, hi2 = x[0].x;
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
         const uint32_t y[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lo2 = min_bf16x2(lo2, y[i]), hi2 = min_bf16x2(hi2, y[i] ^ 0x80008000u);
+        for (int i = w == 0 ? 1 : 0; i < 4; ++i) lo2 = min_bf16x2(lo2, y[i]), hi2 = max_bf16x2(hi2, y[i]);
     }
+    // (minimum, -maximum) of the lane, of the group
+    hi2 ^= 0x80008000u;
     uint32_t ends = min_bf16x2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
     for (int o = 1; o < lanes; o <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
     const float lo = __fadd_rn(bf16_lo(ends), 0.f), hi = -bf16_hi(ends);  // (a minimum of -0 is stored as 0)
@@ -98,24 +103,23 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[kWords], int lanes, ui
     const bool normal = __bfloat162float(s) >= 0x1p-126f;
     if (!normal) s = __float2bfloat16_rn(0.f);
     const float r = normal ? __frcp_rn(__bfloat162float(s)) : 0.f;
-    // 2^23 + a value below 2^22 is rounded to an integer, ties to even; four codes then
-    // add up in the low 16 bits of such a sum, exactly
+    // 2^23 + a value below 2^22 is rounded to an integer, ties to even, in the low bits.  None is
+    // above 15: s is at least (1 - 2^-8) (hi - lo) / 15, so the largest is below 15.1.
     constexpr float kRound = 8388608.f;
+    const float2 less = make_float2(-lo, -lo), times = make_float2(r, r);
+    constexpr uint32_t kUnits = 0x4b000000u * 0x11111111u;  // what the eight numbers' upper bits add up to
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
         const uint32_t y[4] = {x[w].x, x[w].y, x[w].z, x[w].w};
-        uint32_t half[2];
+        uint32_t sum = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float c[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float v = i & 1 ? bf16_hi(y[2 * h + i / 2]) : bf16_lo(y[2 * h + i / 2]);
-                c[i] = __fsub_rn(__fadd_rn(fminf(__fmul_rn(__fsub_rn(v, lo), r), 15.f), kRound), kRound);
-            }
-            half[h] = __float_as_uint(__fadd_rn(fmaf(fmaf(c[3], 16.f, c[2]), 256.f, fmaf(c[1], 16.f, c[0])), kRound));
+        for (int i = 3; i >= 0; --i) {
+            // (the last sum by halves: a product and a sum of pairs are fused, which rounds once)
+            const float2 c = __fmul2_rn(__fadd2_rn(make_float2(bf16_lo(y[i]), bf16_hi(y[i])), less), times);
+            sum = sum * 16 + __float_as_uint(__fadd_rn(c.y, kRound));
+            sum = sum * 16 + __float_as_uint(__fadd_rn(c.x, kRound));
         }
-        codes[w] = __byte_perm(half[0], half[1], 0x5410);
+        codes[w] = sum - kUnits;
     }
     *params = (uint32_t)__bfloat16_as_ushort(s) | (__float_as_uint(lo) & 0xffff0000u);
 }
