@@ -1439,9 +1439,6 @@ constexpr int kRowsOfRowKernel = 256, kExcessRows = 1024;
 // The pool holds at least one sequence of max_cache_len tokens, and up to this many bytes of more.
 constexpr long long kPoolBytes = 1ll << 30;
 
-// Entries of a block table that every CTA of the row kernel reads whole.
-constexpr int kOwnTable = 32768;
-
 constexpr int kCacheSpans = 4;
 void cache_spans(const pa::Cache4& c, const Options& o, int num_seqs, int head_dim, bool written, Span* out) {
     const size_t rows = cache_rows(o, num_seqs, c.max_cache_len, c.n_kv_heads);
@@ -1618,10 +1615,9 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     const int sched = auto_schedule(total_q, num_seqs, n_heads, n_kv_heads, false, sms) == 1 ? 1 : 2;
     const long long units = tiles ? unit_bound(total_q, num_seqs, n_heads, n_kv_heads, sched) : 0;
     if (units >= (1LL << 31)) return fail(PA_ERR_UNSUPPORTED, "too many work units");
-    // The row kernel's CTAs check small tables themselves, each all of them; for larger ones,
-    // and for the rotary prologue, a kernel ahead does.
-    const bool check = !tiles && (o.rope_theta > 0.f || (o.block_table && (num_seqs > pa::kRows4Seqs ||
-                                                                           (long long)num_seqs * o.max_blocks > kOwnTable)));
+    // The row kernel's CTAs check metadata and tables themselves; a kernel ahead does for the
+    // rotary prologue, and for more sequences than a CTA keeps at hand.
+    const bool check = !tiles && (o.rope_theta > 0.f || (o.block_table && num_seqs > pa::kRows4Seqs));
     // the pool of expanded blocks
     const long long seq_blocks = ((long long)max_cache_len + pa::kBlock4 - 1) / pa::kBlock4;
     const size_t block_bytes = (size_t)n_kv_heads * pa::kBlock4 * head_dim * 2;  // of K or V

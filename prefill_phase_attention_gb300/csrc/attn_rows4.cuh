@@ -237,18 +237,18 @@ __device__ __forceinline__ int swizzle(int key) {  // of a row's 16-byte parts
     return D == 128 ? (key >> 1) & 3 : D == 64 ? (key >> 2) & 1 : 0;
 }
 
-// Partial result of a row block: rows [8 NQ] x (maximum, sum) and the unnormalised output.
+// One row's four channels, and its log-sum-exp; nothing of a sequence whose table is bad.
 template <int D, int NQ>
-__device__ __forceinline__ void store_row(const Rows4Params& p, const Item& t, int row, int d, float4 o) {
+__device__ __forceinline__ void store_row(const Rows4Params& p, const Item& t, bool bad, int row, int d, float4 o) {
     const int r = t.block * 8 * NQ + row;
-    if (r >= t.s.n * p.group) return;
+    if (bad || r >= t.s.n * p.group) return;
     const size_t at = ((size_t)(t.s.q_start + r / p.group) * p.n_heads + t.kvh * p.group + r % p.group) * D + d;
     *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
 }
 template <int NQ>
-__device__ __forceinline__ void store_lse(const Rows4Params& p, const Item& t, int row, float m, float l) {
+__device__ __forceinline__ void store_lse(const Rows4Params& p, const Item& t, bool bad, int row, float m, float l) {
     const int r = t.block * 8 * NQ + row;
-    if (!p.lse || r >= t.s.n * p.group) return;
+    if (bad || !p.lse || r >= t.s.n * p.group) return;
     p.lse[(size_t)(t.s.q_start + r / p.group) * p.n_heads + t.kvh * p.group + r % p.group] =
         (m + log2_approx(l)) * 0.69314718055994530942f;
 }
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     __shared__ float2 stats[kWarps][2][C::kRows];  // (maximum, sum) of a record's rows
     __shared__ long long warp_sums[kWarps];
     __shared__ long long start_of_first;
-    __shared__ int first_seq, arrived;
+    __shared__ int first_seq, last_seq;
     __shared__ bool joins[2];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, t4 = lane % 4;
     griddep_wait();
@@ -504,37 +504,13 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     if (in_table) {
         if (tid < p.seqs.num_seqs) {
             SeqInfo s = p.seqs.checked ? sequence_of(p, tid) : stated_sequence(p.seqs, p.cache.max_cache_len, tid);
-            if (s.n < 0) s.pad = 1, s.n = 0;  // (pad: to be reported)
+            s.pad = s.n < 0;  // (to be reported)
+            s.n = max(s.n, 0);
             table[tid] = s;
-        }
-        if (p.cache.block_table && !p.seqs.checked) {
-            // a sequence with a table entry outside the pool is skipped whole: 16 entries a thread
-            // at a time
-            constexpr int kChunk = 16;
-            if (tid == 0) arrived = 0;
-            __syncthreads();
-            if (tid < p.seqs.num_seqs && table[tid].n > 0)
-                atomicMax(&arrived, ((table[tid].P + table[tid].n - 1) >> p.cache.block_log2) / kChunk + 1);
-            __syncthreads();
-            const unsigned chunks = (unsigned)arrived;  // of the longest sequence
-            for (unsigned x = tid; x < chunks * (unsigned)p.seqs.num_seqs; x += kThreads) {
-                const int b = x / chunks, i0 = x % chunks * kChunk;
-                const SeqInfo s = table[b];
-                const int end = s.n > 0 ? ((s.P + s.n - 1) >> p.cache.block_log2) + 1 : 0;
-                const int32_t* entries = p.cache.block_table + (size_t)b * p.cache.max_blocks;
-                int id[kChunk];
-                bool bad = false;
-#pragma unroll
-                for (int i = 0; i < kChunk; ++i) id[i] = i0 + i < end ? __ldg(entries + i0 + i) : 0;
-#pragma unroll
-                for (int i = 0; i < kChunk; ++i) bad |= (unsigned)id[i] >= (unsigned)p.cache.num_blocks;
-                if (bad) table[b].pad = 1;  // (several threads, one value)
-            }
-            __syncthreads();
-            if (tid < p.seqs.num_seqs && table[tid].pad) table[tid].n = 0;
         }
         if (!p.seqs.checked && blockIdx.x == 0 && tid < p.seqs.num_seqs && table[tid].pad)
             atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
+        // from here on pad says that a sequence of this CTA's share has a bad block table
     } else if (!p.seqs.checked && blockIdx.x == 0) {
         for (int b = tid; b < p.seqs.num_seqs; b += kThreads)
             if (stated_sequence(p.seqs, p.cache.max_cache_len, b).n < 0) atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
@@ -577,8 +553,10 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     const long long share = max((long long)kWarps, (long long)divide(all + gridDim.x - 1, gridDim.x, rest));
     const long long from = min(all, share * blockIdx.x), to = min(all, from + share);
     if (from >= to) return;  // (the whole CTA)
+    const bool check_tables = in_table && p.cache.block_table && !p.seqs.checked;
     if (in_table) {
         if (mine > 0 && excl <= from && from < excl + mine) first_seq = tid, start_of_first = excl;
+        if (mine > 0 && excl < to && to <= excl + mine) last_seq = tid;
     } else {
         long long before = 0;
         for (int b0 = 0; b0 < p.seqs.num_seqs && before <= from; b0 += kThreads) {
@@ -611,13 +589,32 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     float2 neg[NQ], most[NQ];        // less the running maximum m (log2 units; 0 before any key), (m + 8) / scale
     float2 T[NQ];                    // factor of p s in the second product, and of O with it
 
+    // Whether a sequence is to be skipped whole because its table names a block outside the pool: the
+    // CTA looks through the tables of the sequences in its share while the first tiles
+    // come (a block id is clamped where it is used, so nothing faults meanwhile).
+    auto bad_table = [&](int b) -> bool { return check_tables && table[b].pad != 0; };
+
     int stage = 1;  // (the first pass fills stage 0)
 #pragma unroll 1
     for (int i = 1 - C::kStages;; ++i, stage = stage + 1 == C::kStages ? 0 : stage + 1) {
         feed.issue(stage == 0 ? C::kStages - 1 : stage - 1);
         if (i < 0) continue;
+        if (i == 0 && check_tables) {
+            for (int b = first_seq; b <= last_seq; ++b) {
+                const SeqInfo s = table[b];
+                const int end = s.n > 0 ? ((s.P + s.n - 1) >> p.cache.block_log2) + 1 : 0;
+                const int32_t* entries = p.cache.block_table + (size_t)b * p.cache.max_blocks;
+                bool bad = false;
+#pragma unroll 4
+                for (int x = tid; x < end; x += kThreads) bad |= (unsigned)__ldg(entries + x) >= (unsigned)p.cache.num_blocks;
+                if (bad) {
+                    table[b].pad = 1;  // (several threads, one value)
+                    atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
+                }
+            }
+            __syncthreads();
+        }
         if (i >= feed.count) break;  // (the feeder is ahead)
-        cp_async_wait<C::kStages - 1>();
         __syncwarp();
         const int flags = tiles[warp][stage].flags, key = tiles[warp][stage].key;
         const Item& t = items[warp][flags >> kSlot];
@@ -682,6 +679,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                     for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] = 0.f;
             }
         }
+        cp_async_wait<C::kStages - 1>();  // (after the queries' loads: both come at once)
+        __syncwarp();
         // keys [lo, hi] that row 8 n + 2 t4 + e sees
         auto visible = [&](int n, int e, int& lo, int& hi) {
             const int tok = min((t.block * C::kRows + 8 * n + 2 * t4 + e) / p.group, t.s.n - 1);
@@ -952,7 +951,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                     mma(o[n][c][1], __byte_perm(x.y, y.y, 0x5410), v3, 0, 0, pt[n], 0);
                 }
             }
-            if (t.block == 0) {
+            if (t.block == 0 && !bad_table(t.b)) {
                 // their rows go into the cache, once per KV head
                 constexpr int kLanes = D / 8, kStep = 32 / kLanes;
                 constexpr int kGroupLanes = kLanes / NG;
@@ -1012,13 +1011,13 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                         const float4 v = make_float4(fmaf(o[n][c][0][e], un, y), fmaf(o[n][c][0][2 + e], odd, y),
                                                      fmaf(o[n][c][1][e], un, y), fmaf(o[n][c][1][2 + e], odd, y));
                         if (whole)
-                            store_row<D, NQ>(p, t, row, 32 * c + 4 * g, v);
+                            store_row<D, NQ>(p, t, bad_table(t.b), row, 32 * c + 4 * g, v);
                         else
                             *reinterpret_cast<float4*>(rec + row * D + 32 * c + 4 * g) = v;
                     }
                     if (g == 0) {
                         if (whole)
-                            store_lse<NQ>(p, t, row, m, x);
+                            store_lse<NQ>(p, t, bad_table(t.b), row, m, x);
                         else
                             stats[warp][slot][row] = make_float2(m, x);
                     }
@@ -1087,8 +1086,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
             }
             if (whole) {
                 const float f = 1.f / sum;
-                store_row<D, NQ>(p, t, row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-                if (x % D == 0) store_lse<NQ>(p, t, row, top, sum);
+                store_row<D, NQ>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+                if (x % D == 0) store_lse<NQ>(p, t, bad_table(t.b), row, top, sum);
             } else {
                 const size_t at = (size_t)blockIdx.x * 2 + slot;
                 __stcg(reinterpret_cast<float4*>(p.part + at * kElems + x), v);
@@ -1162,8 +1161,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 }
             }
             const float f = 1.f / sum;
-            store_row<D, NQ>(p, t, row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-            if (x % D == 0) store_lse<NQ>(p, t, row, top, sum);
+            store_row<D, NQ>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+            if (x % D == 0) store_lse<NQ>(p, t, bad_table(t.b), row, top, sum);
         }
     }
 }

@@ -361,12 +361,14 @@ cudaError_t launch_check_sequences4(const Sequences4& a, const Cache4& c, bool w
 
 namespace {
 
-// Heads of a block: enough blocks for the GPU first, then up to 8 heads to a block.
+// Heads of a block: enough blocks for the GPU first, then up to kMostRows channels of rows to a
+// block, so that finding its tokens is little of its time.
+constexpr long long kMostRows = 65536;
 template <class Kernel>
-cudaError_t launch_copy(Kernel kernel, Copy4Params p, int sms, cudaStream_t stream) {
+cudaError_t launch_copy(Kernel kernel, Copy4Params p, int head_dim, int sms, cudaStream_t stream) {
     const long long blocks = ((long long)p.seqs.total_q + kCopyTokens - 1) / kCopyTokens;
     const long long heads = 2ll * p.cache.n_kv_heads;
-    p.heads = (int)std::max(1ll, std::min(8ll, blocks * heads / (8ll * sms)));
+    p.heads = (int)std::max(1ll, std::min(kMostRows / head_dim / kCopyTokens, blocks * heads / (8ll * sms)));
     return launch_after(kernel, dim3((unsigned)blocks, (unsigned)((heads + p.heads - 1) / p.heads)), kCopyThreads, stream, p);
 }
 
@@ -374,17 +376,17 @@ cudaError_t launch_copy(Kernel kernel, Copy4Params p, int sms, cudaStream_t stre
 
 cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream) {
     switch (head_dim) {
-        case 32: return launch_copy(write_cache4_kernel<32>, p, sms, stream);
-        case 64: return launch_copy(write_cache4_kernel<64>, p, sms, stream);
-        default: return launch_copy(write_cache4_kernel<128>, p, sms, stream);
+        case 32: return launch_copy(write_cache4_kernel<32>, p, 32, sms, stream);
+        case 64: return launch_copy(write_cache4_kernel<64>, p, 64, sms, stream);
+        default: return launch_copy(write_cache4_kernel<128>, p, 128, sms, stream);
     }
 }
 
 cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream) {
     switch (head_dim) {
-        case 32: return launch_copy(read_cache4_kernel<32>, p, sms, stream);
-        case 64: return launch_copy(read_cache4_kernel<64>, p, sms, stream);
-        default: return launch_copy(read_cache4_kernel<128>, p, sms, stream);
+        case 32: return launch_copy(read_cache4_kernel<32>, p, 32, sms, stream);
+        case 64: return launch_copy(read_cache4_kernel<64>, p, 64, sms, stream);
+        default: return launch_copy(read_cache4_kernel<128>, p, 128, sms, stream);
     }
 }
 
