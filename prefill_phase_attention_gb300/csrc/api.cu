@@ -1661,6 +1661,9 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     p.taken = nullptr;
     int launches = 0;
     pa::Expand4Params x;
+    Options po;
+    const int pool_len = (int)std::min<long long>(seq_blocks * pa::kBlock4, kMaxTokens);
+    const int tile_grid = (int)std::min<long long>(sms, units);
     if (tiles) {
         p.seqs.checked = reinterpret_cast<pa::SeqInfo*>(take(seq_bytes));
         x.seqs = p.seqs;
@@ -1671,13 +1674,22 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         x.table_blocks = (int)seq_blocks;
         x.taken = reinterpret_cast<int*>(take(taken_bytes));
         x.blocks = x.taken + num_seqs;
-        x.table = reinterpret_cast<int32_t*>(take(table_bytes));
+        x.table = one ? nullptr : reinterpret_cast<int32_t*>(take(table_bytes));
         x.owners = reinterpret_cast<int2*>(take(owner_bytes));
         x.k = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
         x.v = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
         p.taken = x.taken;
-        e = pa::launch_plan_expand4(x, stream);
-        if (e != cudaSuccess) return cuda_fail(e, "plan launch");
+        po = o;  // the pool, as a bf16 cache
+        po.block_table = x.table;
+        po.block_size = one ? 0 : pa::kBlock4;
+        po.max_blocks = one ? 0 : (int)seq_blocks;
+        po.num_blocks = one ? 0 : (int)pool_blocks;
+        pa::ScheduleArgs sa;
+        fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, pool_len, n_heads, n_kv_heads,
+                      head_dim, causal, po, scr, sched, tile_grid);
+        sa.taken = x.taken;
+        e = pa::launch_build_schedule4(sa, x, stream);
+        if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
         ++launches;
     } else if (check) {
         e = pa::launch_check_sequences4(p.seqs, c, true, stream);
@@ -1691,19 +1703,11 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         ++launches;
     }
     if (tiles) {
-        Options po = o;  // the pool, as a paged bf16 cache
-        po.block_table = x.table;
-        po.block_size = pa::kBlock4;
-        po.max_blocks = (int)seq_blocks;
-        po.num_blocks = (int)pool_blocks;
-        const int pool_len = (int)std::min<long long>(seq_blocks * pa::kBlock4, kMaxTokens);
-        const int tile_grid = (int)std::min<long long>(sms, units);
-        pa::ScheduleArgs sa;
-        fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, pool_len, n_heads, n_kv_heads,
-                      head_dim, causal, po, scr, sched, tile_grid);
-        sa.taken = x.taken;
-        e = pa::launch_build_schedule(sa, stream);
-        if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
+        x.write.seqs = p.seqs;
+        x.write.cache = c;
+        x.write.k = static_cast<const __nv_bfloat16*>(k);
+        x.write.v = static_cast<const __nv_bfloat16*>(v);
+        x.write.k_out = x.write.v_out = nullptr;
         e = pa::launch_expand4(x, head_dim, sms, stream);
         if (e != cudaSuccess) return cuda_fail(e, "expansion launch");
         pa::FwdParams fp;
@@ -1712,16 +1716,7 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
         e = pa::launch_attn_fwd(fp, head_dim, tile_grid, stream);
         if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-        // the new tokens into the cache (the row kernel writes those of its sequences itself)
-        pa::Copy4Params w;
-        w.seqs = p.seqs;
-        w.cache = c;
-        w.k = static_cast<const __nv_bfloat16*>(k);
-        w.v = static_cast<const __nv_bfloat16*>(v);
-        w.k_out = w.v_out = nullptr;
-        e = pa::launch_write_cache4(w, head_dim, sms, stream);
-        if (e != cudaSuccess) return cuda_fail(e, "cache write launch");
-        launches += 4;
+        launches += 2;
         g_last_schedule = sched;
     }
     g_last_launches = launches;

@@ -33,7 +33,7 @@ struct Places {
 };
 
 // Where the rows of tokens [t0, t0 + kCopyTokens) are.  Ends with a barrier.
-__device__ __forceinline__ void locate_tokens(const Sequences4& a, const Cache4& c, int t0, Places& at) {
+__device__ __forceinline__ void locate_tokens(const Sequences4& a, const Cache4& c, int t0, Places& at, bool report) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool in_smem = a.num_seqs <= kCuInSmem;
     if (in_smem) {
@@ -84,7 +84,7 @@ __device__ __forceinline__ void locate_tokens(const Sequences4& a, const Cache4&
         }
         __syncthreads();
     }
-    if (!a.checked && blockIdx.x == 0 && blockIdx.y == 0)
+    if (!a.checked && report)
         for (int b = tid; b < a.num_seqs; b += kCopyThreads)
             if (stated_sequence(a, c.max_cache_len, b).n < 0) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
 }
@@ -97,23 +97,22 @@ struct Rows {
     static constexpr int kStep = kCopyThreads / kLanes;
     static_assert(kStep % kCopyTokens == 0 || kCopyTokens % kStep == 0, "a pass is whole heads or part of one");
     int part = threadIdx.x % kLanes, first = threadIdx.x / kLanes, h0, items;
-    __device__ __forceinline__ Rows(int n_kv_heads, int heads) {
-        h0 = blockIdx.y * heads;
+    __device__ __forceinline__ Rows(int n_kv_heads, int heads, int heads_at) {
+        h0 = heads_at * heads;
         items = (min(2 * n_kv_heads, h0 + heads) - h0) * kCopyTokens;
     }
     __device__ __forceinline__ int token(int it) const { return it % kCopyTokens; }
     __device__ __forceinline__ int head(int it) const { return h0 + it / kCopyTokens; }
 };
 
+// Tokens [32 tokens_at, ...) and heads [heads_at * p.heads, ...) of k and v into the cache.
 template <int D>
-__global__ void __launch_bounds__(kCopyThreads) write_cache4_kernel(const Copy4Params p) {
-    __shared__ Places at;
+__device__ __forceinline__ void write_rows4(const Copy4Params& p, Places& at, int tokens_at, int heads_at) {
     const int Hk = p.cache.n_kv_heads, groups = p.cache.groups, group_lanes = D / 16 / groups;
     const size_t stride = p.cache.block_table ? (size_t)1 << p.cache.block_log2 : (size_t)p.cache.max_cache_len;
-    const int t0 = blockIdx.x * kCopyTokens;
-    const Rows<D> r(Hk, p.heads);
+    const int t0 = tokens_at * kCopyTokens;
+    const Rows<D> r(Hk, p.heads, heads_at);
     constexpr int kStep = Rows<D>::kStep;
-    griddep_wait();
     uint4 x[kInFlight][2];
     auto load = [&](int i0) {
 #pragma unroll
@@ -129,7 +128,7 @@ __global__ void __launch_bounds__(kCopyThreads) write_cache4_kernel(const Copy4P
         }
     };
     load(r.first);  // in flight while the tokens are located
-    locate_tokens(p.seqs, p.cache, t0, at);
+    locate_tokens(p.seqs, p.cache, t0, at, tokens_at == 0 && heads_at == 0);
     // (whole warps go round: items and the steps are multiples of a warp's rows)
     for (int i0 = r.first; i0 < r.items; i0 += kInFlight * kStep) {
         if (i0 != r.first) load(i0);
@@ -146,6 +145,13 @@ __global__ void __launch_bounds__(kCopyThreads) write_cache4_kernel(const Copy4P
             if (r.part % group_lanes == 0) (h < Hk ? p.cache.kp : p.cache.vp)[row * groups + r.part / group_lanes] = word;
         }
     }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kCopyThreads) write_cache4_kernel(const Copy4Params p) {
+    __shared__ Places at;
+    griddep_wait();
+    write_rows4<D>(p, at, blockIdx.x, blockIdx.y);
 }
 
 // The values of 16 channels: a code as the low bits of 2^23; the product with s is exact, the sum
@@ -173,10 +179,10 @@ __global__ void __launch_bounds__(kCopyThreads) read_cache4_kernel(const Copy4Pa
     const int Hk = p.cache.n_kv_heads, groups = p.cache.groups, group_lanes = D / 16 / groups;
     const size_t stride = p.cache.block_table ? (size_t)1 << p.cache.block_log2 : (size_t)p.cache.max_cache_len;
     const int t0 = blockIdx.x * kCopyTokens;
-    const Rows<D> r(Hk, p.heads);
+    const Rows<D> r(Hk, p.heads, blockIdx.y);
     constexpr int kStep = Rows<D>::kStep;
     griddep_wait();
-    locate_tokens(p.seqs, p.cache, t0, at);
+    locate_tokens(p.seqs, p.cache, t0, at, blockIdx.x == 0 && blockIdx.y == 0);
     for (int i0 = r.first; i0 < r.items; i0 += kInFlight * kStep) {
         uint2 codes[kInFlight];
         uint32_t word[kInFlight];
@@ -208,11 +214,6 @@ __global__ void __launch_bounds__(kCopyThreads) read_cache4_kernel(const Copy4Pa
     }
 }
 
-// The first block of a sequence that its queries see.
-__device__ __forceinline__ int first_block(const Expand4Params& p, const SeqInfo& s) {
-    return p.window > 0 ? max(0, s.P - p.window + 1) / kBlock4 : 0;
-}
-
 // One block per sequence: its metadata, and the table entries of the call's tokens
 // (whole: of all tokens up to its last).
 __global__ void __launch_bounds__(128) check_sequences4_kernel(const Sequences4 a, const Cache4 c, bool whole) {
@@ -234,80 +235,24 @@ __global__ void __launch_bounds__(128) check_sequences4_kernel(const Sequences4 
     }
 }
 
-// One block: checks the sequences, and lays out the pool.
-__global__ void __launch_bounds__(1024) plan_expand4_kernel(const Expand4Params p) {
-    __shared__ int warp_sums[32], in_use;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Cache4& c = p.cache;
-    if (tid == 0) in_use = 0;
-    griddep_wait();
-    // a warp per sequence
-    for (int b = warp; b < p.seqs.num_seqs; b += 32) {
-        const SeqInfo s = stated_sequence(p.seqs, c.max_cache_len, b);
-        bool bad = s.n < 0;
-        if (c.block_table && s.n > 0) {
-            const int end = ((s.P + s.n - 1) >> c.block_log2) + 1;
-            const int32_t* table = c.block_table + (size_t)b * c.max_blocks;
-#pragma unroll 8
-            for (int i = lane; i < end; i += 32) bad |= (unsigned)__ldg(table + i) >= (unsigned)c.num_blocks;
-        }
-        bad = __any_sync(0xffffffffu, bad);
-        if (lane == 0) {
-            p.seqs.checked[b] = bad ? SeqInfo{0, 0, 0, 0} : s;
-            if (bad) atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
-        }
-    }
-    __syncthreads();
-    int base = 0;  // blocks of the sequences before
-    for (int b0 = 0; b0 < p.seqs.num_seqs; b0 += 1024) {
-        const int b = b0 + tid;
-        SeqInfo s{0, 0, 0, 0};
-        if (b < p.seqs.num_seqs) s = p.seqs.checked[b];
-        const bool wanted = s.n > p.few_tokens;
-        const int first = first_block(p, s);
-        // (sums past the pool saturate: a sequence's blocks are at most 2^23)
-        int need = wanted ? (s.P + s.n + kBlock4 - 1) / kBlock4 - first : 0, inc = need;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc = min(inc + y, 1 << 29);
-        }
-        if (lane == 31) warp_sums[warp] = inc;
-        __syncthreads();
-        int before = base;
-        for (int w = 0; w < 32; ++w) {
-            if (w < warp) before = min(before + warp_sums[w], 1 << 29);
-            base = min(base + warp_sums[w], 1 << 29);
-        }
-        const int at = min(before + inc, 1 << 29) - need;
-        const bool fits = wanted && before + inc < 1 << 29 && at + need <= p.pool_blocks;
-        if (b < p.seqs.num_seqs) p.taken[b] = fits ? at + 1 : 0;
-        if (fits) atomicMax(&in_use, at + need);  // (those that fit are the first ones: no gaps)
-        __syncthreads();
-    }
-    if (tid == 0) *p.blocks = in_use;
-    for (int b = warp; b < p.seqs.num_seqs; b += 32) {
-        const int at = p.taken[b] - 1;
-        if (at < 0) continue;
-        const SeqInfo s = p.seqs.checked[b];
-        const int first = first_block(p, s), end = (s.P + s.n + kBlock4 - 1) / kBlock4;
-        for (int i = lane; i < end; i += 32) {
-            p.table[(size_t)b * p.table_blocks + i] = i < first ? 0 : at + i - first;
-            if (i >= first) p.owners[at + i - first] = make_int2(b, i * kBlock4);
-        }
-    }
-}
-
-// A block takes 128 rows (a block of the pool, one head of K or V) at a time.
+// The first p.expanders blocks take 128 rows (a block of the pool, one head of K or V) at a time;
+// the others write the call's new tokens into the cache, which nothing else of the call reads.
 template <int D>
 __global__ void __launch_bounds__(kCopyThreads) expand4_kernel(const Expand4Params p) {
+    __shared__ Places places;
+    griddep_wait();
+    if ((int)blockIdx.x >= p.expanders) {
+        const int x = blockIdx.x - p.expanders;
+        write_rows4<D>(p.write, places, x % p.write_blocks, x / p.write_blocks);
+        return;
+    }
     constexpr int kLanes = D / 16, kStep = kCopyThreads / kLanes;
     constexpr int kPasses = kBlock4 / kStep > 0 ? kBlock4 / kStep : 1;
     const Cache4& c = p.cache;
     const int Hk = c.n_kv_heads, group_lanes = kLanes / c.groups;
     const int part = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
-    griddep_wait();
     const long long units = 2ll * Hk * *p.blocks;
-    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    for (long long u = blockIdx.x; u < units; u += p.expanders) {
         const int block = (int)(u / (2 * Hk)), h = (int)(u % (2 * Hk)), kvh = h < Hk ? h : h - Hk;
         const int2 owner = p.owners[block];
         const int P = p.seqs.checked[owner.x].P;
@@ -325,7 +270,10 @@ __global__ void __launch_bounds__(kCopyThreads) expand4_kernel(const Expand4Para
                 word[i] = __ldg((h < Hk ? c.kp : c.vp) + row * c.groups + part / group_lanes);
             }
         }
-        __nv_bfloat16* const pool = (h < Hk ? p.k : p.v) + ((size_t)block * Hk + kvh) * kBlock4 * D;
+        // row of the pool: its blocks' (a paged cache), or its one sequence's (contiguous)
+        const size_t row0 = p.table ? ((size_t)block * Hk + kvh) * kBlock4
+                                    : (size_t)kvh * p.table_blocks * kBlock4 + owner.y;
+        __nv_bfloat16* const pool = (h < Hk ? p.k : p.v) + row0 * D;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int r = i * kStep + first;
@@ -364,11 +312,15 @@ namespace {
 // Heads of a block: enough blocks for the GPU first, then up to kMostRows channels of rows to a
 // block, so that finding its tokens is little of its time.
 constexpr long long kMostRows = 65536;
+int heads_of_block(long long blocks, long long heads, int head_dim, int sms) {
+    return (int)std::max(1ll, std::min(kMostRows / head_dim / kCopyTokens, blocks * heads / (8ll * sms)));
+}
+
 template <class Kernel>
 cudaError_t launch_copy(Kernel kernel, Copy4Params p, int head_dim, int sms, cudaStream_t stream) {
     const long long blocks = ((long long)p.seqs.total_q + kCopyTokens - 1) / kCopyTokens;
     const long long heads = 2ll * p.cache.n_kv_heads;
-    p.heads = (int)std::max(1ll, std::min(kMostRows / head_dim / kCopyTokens, blocks * heads / (8ll * sms)));
+    p.heads = heads_of_block(blocks, heads, head_dim, sms);
     return launch_after(kernel, dim3((unsigned)blocks, (unsigned)((heads + p.heads - 1) / p.heads)), kCopyThreads, stream, p);
 }
 
@@ -390,12 +342,13 @@ cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cuda
     }
 }
 
-cudaError_t launch_plan_expand4(const Expand4Params& p, cudaStream_t stream) {
-    return launch_after(plan_expand4_kernel, dim3(1), 1024, stream, p);
-}
-
-cudaError_t launch_expand4(const Expand4Params& p, int head_dim, int sms, cudaStream_t stream) {
-    const dim3 grid((unsigned)std::min((long long)sms * 6, 2ll * p.cache.n_kv_heads * p.pool_blocks));
+cudaError_t launch_expand4(Expand4Params p, int head_dim, int sms, cudaStream_t stream) {
+    const long long blocks = ((long long)p.write.seqs.total_q + kCopyTokens - 1) / kCopyTokens;
+    const long long heads = 2ll * p.cache.n_kv_heads;
+    p.write.heads = heads_of_block(blocks, heads, head_dim, sms);
+    p.write_blocks = (int)blocks;
+    p.expanders = (int)std::min((long long)sms * 4, heads * p.pool_blocks);
+    const dim3 grid((unsigned)(p.expanders + blocks * ((heads + p.write.heads - 1) / p.write.heads)));
     switch (head_dim) {
         case 32: return launch_after(expand4_kernel<32>, grid, kCopyThreads, stream, p);
         case 64: return launch_after(expand4_kernel<64>, grid, kCopyThreads, stream, p);

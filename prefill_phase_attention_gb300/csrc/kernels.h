@@ -188,9 +188,22 @@ cudaError_t launch_evict(const EvictArgs& a, int sms, int* launches, cudaStream_
 // table entry up to a sequence's last token counts, else only those of the call's tokens.
 cudaError_t launch_check_sequences4(const Sequences4& a, const Cache4& c, bool whole, cudaStream_t stream);
 
-// Long chunks: their sequences' cached rows expanded to bf16, in a pool of blocks of
-// kBlock4 tokens [pool_blocks][n_kv_heads][kBlock4][head_dim] that the attention kernel reads as
-// a paged cache.
+// Rows of packed tokens [total_q, n_kv_heads, head_dim] into the cache, or back.
+struct Copy4Params {
+    Sequences4 seqs;
+    Cache4 cache;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    __nv_bfloat16* k_out;
+    __nv_bfloat16* v_out;
+    int heads;  // of K and V that a block takes (set by the launch)
+};
+cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
+cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
+
+// Long chunks: their sequences' cached rows expanded to bf16, for the attention kernel to read as
+// a paged cache, a pool of blocks of kBlock4 tokens [pool_blocks][n_kv_heads][kBlock4][head_dim],
+// or, with one sequence (table == nullptr), as a contiguous one.
 constexpr int kBlock4 = 128;
 struct Expand4Params {
     Sequences4 seqs;  // checked: where the plan writes them
@@ -205,24 +218,13 @@ struct Expand4Params {
     int* blocks;       // in use
     __nv_bfloat16* k;
     __nv_bfloat16* v;
+    Copy4Params write;            // the call's new tokens, written by the same launch
+    int expanders, write_blocks;  // blocks that expand, blocks of tokens to write (set by the launch)
 };
-// Checks the sequences (like launch_check_sequences4, whole) and gives those that are taken their
-// blocks, in order, until the pool is full.
-cudaError_t launch_plan_expand4(const Expand4Params& p, cudaStream_t stream);
-cudaError_t launch_expand4(const Expand4Params& p, int head_dim, int sms, cudaStream_t stream);
-
-// Rows of packed tokens [total_q, n_kv_heads, head_dim] into the cache, or back.
-struct Copy4Params {
-    Sequences4 seqs;
-    Cache4 cache;
-    const __nv_bfloat16* k;
-    const __nv_bfloat16* v;
-    __nv_bfloat16* k_out;
-    __nv_bfloat16* v_out;
-    int heads;  // of K and V that a block takes (set by the launch)
-};
-cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
-cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
+// Checks the sequences (like launch_check_sequences4, whole), gives those that are taken their
+// blocks, in order, until the pool is full, and builds the list of their work units.
+cudaError_t launch_build_schedule4(const ScheduleArgs& a, const Expand4Params& x, cudaStream_t stream);
+cudaError_t launch_expand4(Expand4Params p, int head_dim, int sms, cudaStream_t stream);
 
 // Attention of few query rows per sequence over the 4-bit cache (attn_rows4.cu).
 constexpr int kRows4Seqs = 256;  // sequences whose metadata a CTA keeps in shared memory

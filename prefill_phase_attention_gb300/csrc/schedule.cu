@@ -23,12 +23,13 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "plan4.cuh"
 #include "prefill_attn.h"
 #include "schedule.cuh"
 
 namespace pa {
 
-__global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
+__device__ __forceinline__ void build_schedule(const ScheduleArgs& a) {
     __shared__ int hist[kCostBins];
     __shared__ int warp_sums[32];
     __shared__ SeqInfo s_seqs[kSmemSeqs];
@@ -183,6 +184,19 @@ __global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) {
             a.units[pos] = u;
         }
     }
+}
+
+__global__ void __launch_bounds__(1024) build_schedule_kernel(ScheduleArgs a) { build_schedule(a); }
+
+// Over a 4-bit cache: the expanded sequences first (which the list is of).
+__global__ void __launch_bounds__(1024) build_schedule4_kernel(ScheduleArgs a, Expand4Params x) {
+    plan_expand4(x);
+    build_schedule(a);
+}
+
+cudaError_t launch_build_schedule4(const ScheduleArgs& a, const Expand4Params& x, cudaStream_t stream) {
+    build_schedule4_kernel<<<1, 1024, 0, stream>>>(a, x);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_build_schedule(const ScheduleArgs& a, cudaStream_t stream) {
