@@ -1427,14 +1427,16 @@ pa_status read_cache4(const pa_cache4* cache, const Options& o, int head_dim, in
     return PA_OK;
 }
 
-// Attention over a 4-bit cache takes two ways.  The row kernel reads a sequence's cache once
-// per 16 query rows, a part of it in every CTA.  The other way, for long chunks, expands
-// the sequence's cache to bf16 once (a pool of blocks in the workspace) and runs the
-// tensor-core kernel over it.  Sequences of up to kRowsOfRowKernel rows go the first way, the
-// others the second as far as the pool reaches.  The host does not know the lengths: where
-// all rows but one token of each sequence are at most kExcessRows, the row kernel takes every
-// sequence, which costs less than the other way's launches.
-constexpr int kRowsOfRowKernel = 256, kExcessRows = 1024;
+// Attention over a 4-bit cache takes two ways.  The row kernel reads a sequence's cache once per
+// 8 query rows (from L2 after the first time), a part of it in every CTA.  The other way, for
+// long chunks, expands the sequence's cache to bf16 once (into the workspace) and runs the
+// tensor-core kernel over it.  Sequences of few new tokens go the first way, the others the
+// second as far as that room reaches; few: up to kFewRows rows over all heads (one sequence,
+// D = 128, 32 heads, over 1024 / 8192 / 32768 cached tokens, us: 64 tokens 38 / 70 / 160 and 29 /
+// 80 / 268, 128 tokens 65 / 130 / 310 and 29 / 80 / 264).  The host does not know the lengths:
+// where all rows but one token of each sequence are at most kExcessRows, the row kernel takes
+// every sequence, which costs less than the other way's launches.
+constexpr int kFewRows = 2048, kExcessRows = 8192;
 
 // The pool holds at least one sequence of max_cache_len tokens, and up to this many bytes of more.
 constexpr long long kPoolBytes = 1ll << 30;
@@ -1604,13 +1606,10 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     const int sms = sm_count(dev, &s);
     if (s != PA_OK) return s;
     const int group = n_heads / n_kv_heads;
-    // Which way sequences go: see kRowsOfRowKernel.
-    const int few = std::max(1, kRowsOfRowKernel / group);
+    // Which way sequences go: see kFewRows.
+    const int few = std::max(1, kFewRows / n_heads);
     const bool one = num_seqs == 1;
-    const bool tiles = one ? total_q > few : ((long long)total_q - num_seqs) * group > kExcessRows;
-    // the row kernel's blocks have 16 rows where sequences have more than 8 on average (of
-    // those that it takes, if the tile kernel runs too)
-    const int row_tiles = group > 8 || (!tiles && (long long)total_q * group > 8LL * num_seqs) ? 2 : 1;
+    const bool tiles = one ? total_q > few : ((long long)total_q - num_seqs) * n_heads > kExcessRows;
     const int grid = std::min(sms, kArrivals);
     const int sched = auto_schedule(total_q, num_seqs, n_heads, n_kv_heads, false, sms) == 1 ? 1 : 2;
     const long long units = tiles ? unit_bound(total_q, num_seqs, n_heads, n_kv_heads, sched) : 0;
@@ -1635,8 +1634,8 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     pa::Rows4Params p;
     s = get_arrivals(ws, stream, &p.arrivals);
     if (s != PA_OK) return s;
-    const size_t part_bytes = align_up((size_t)grid * 2 * 8 * row_tiles * (head_dim + 2) * sizeof(float), 256);
-    const size_t kept_bytes = align_up((size_t)grid * pa::kRows4Warps * 8 * row_tiles * head_dim * sizeof(float), 256);
+    const size_t part_bytes = align_up((size_t)grid * 2 * 8 * (head_dim + 2) * sizeof(float), 256);
+    const size_t kept_bytes = align_up((size_t)grid * pa::kRows4Warps * 8 * head_dim * sizeof(float), 256);
     const size_t seq_bytes = tiles ? align_up((size_t)num_seqs * sizeof(pa::SeqInfo), 256) : 0;
     const size_t taken_bytes = tiles ? align_up(((size_t)num_seqs + 1) * sizeof(int), 256) : 0;
     const size_t table_bytes = tiles ? align_up((size_t)num_seqs * seq_blocks * sizeof(int), 256) : 0;
@@ -1732,7 +1731,7 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     p.scale_log2 = scale * 1.4426950408889634f;
     p.causal = causal;
     p.window = o.window;
-    e = pa::launch_attn_rows4(p, head_dim, row_tiles, grid, stream);
+    e = pa::launch_attn_rows4(p, head_dim, grid, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
     ++g_last_launches;
     return PA_OK;

@@ -1,7 +1,9 @@
 // attn_rows4.cuh -- attention of few query rows per sequence over the 4-bit cache:
 // decode rows, drafts, short chunks.
 //
-// A row block is 8 or 16 query rows (token, head of a KV head's group) of a sequence.
+// A row block is 8 query rows (token, head of a KV head's group) of a sequence.  (16 rows, which
+// share the expansion of the codes, leave registers for 8 warps: one row of 8192 keys by
+// 64 tokens of 32 heads took 80 us so, 70 with blocks of 8.)
 // Its keys come in tiles: 32 cached rows, or 8 new tokens (bf16; as many bytes), which
 // follow them.  With a group's parameters (s, m) and codes c the score and output are
 //     q . k_j   = sum_g s_jg (q_g . c_jg) + m_jg sum(q_g)
@@ -48,26 +50,26 @@ namespace rows4 {
 
 constexpr int kTileKeys = 32;  // cached rows of a tile
 constexpr int kNewKeys = 8;    // new tokens of a tile
+constexpr int kRows = 8;       // query rows of a row block: the columns of an MMA
 // Beginning and ending a row block costs a warp about as much as two tiles, so the list has
 // as many places ahead of a row block's tiles that hold none: equal shares of places are equal
 // shares of time.
 constexpr int kBlockCost = 2;
 
-template <int D, int NG, int NQ>
+template <int D, int NG>
 struct Cfg {
-    // As many warps as registers (16: 128 a thread, 12: 168) and shared memory allow: the
+    // As many warps as registers (16: 128 a thread, 12: 168) allow: the
     // instructions of a tile take most of the time that its bytes do, so the issue slots
     // have to be filled.
-    static constexpr int kWarps = NQ == 2 ? (D == 128 ? 8 : 12) : NG > 1 ? 12 : 16;
+    static constexpr int kWarps = NG > 1 ? 12 : 16;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kChunks = D / 32;
     static constexpr int kRowBytes = D / 2;
     static constexpr int kCodes = kTileKeys * kRowBytes;     // bytes of a tile's codes
     static constexpr int kParams = kTileKeys * NG * 4;       // bytes of a tile's parameters
     static constexpr int kTileBytes = 2 * (kCodes + kParams);
-    static constexpr int kStages = D == 128 && NQ == 1 ? 3 : 4;
-    static constexpr int kRows = 8 * NQ;
-    static constexpr int kRecord = kRows * D * 4;  // bytes of a partial output
+    static constexpr int kStages = D == 128 ? 3 : 4;
+        static constexpr int kRecord = kRows * D * 4;  // bytes of a partial output
     static_assert(kStages * kTileBytes >= 2 * kRecord, "a warp's records end up in its ring");
     static_assert(2 * kWarps <= 32, "a lane per record");
 };
@@ -124,7 +126,6 @@ __device__ __forceinline__ long long divide(long long x, int y, int& rest) {
     return x / y;
 }
 
-template <int NQ>
 __device__ __forceinline__ Extent extent(const Rows4Params& p, const SeqInfo& s) {
     Extent e{0, 0, 0, 0};
     if (s.n == 0) return e;
@@ -132,7 +133,7 @@ __device__ __forceinline__ Extent extent(const Rows4Params& p, const SeqInfo& s)
     e.first_tile = lo / kTileKeys;
     e.cached = max(0, (s.P + kTileKeys - 1) / kTileKeys - e.first_tile);
     e.fresh = (s.n + kNewKeys - 1) / kNewKeys;
-    e.blocks = (int)(((unsigned)s.n * (unsigned)p.group + 8 * NQ - 1) / (8 * NQ));  // n * group < 2^31
+    e.blocks = (int)(((unsigned)s.n * (unsigned)p.group + kRows - 1) / kRows);  // n * group < 2^31
     return e;
 }
 
@@ -238,16 +239,15 @@ __device__ __forceinline__ int swizzle(int key) {  // of a row's 16-byte parts
 }
 
 // One row's four channels, and its log-sum-exp; nothing of a sequence whose table is bad.
-template <int D, int NQ>
+template <int D>
 __device__ __forceinline__ void store_row(const Rows4Params& p, const Item& t, bool bad, int row, int d, float4 o) {
-    const int r = t.block * 8 * NQ + row;
+    const int r = t.block * kRows + row;
     if (bad || r >= t.s.n * p.group) return;
     const size_t at = ((size_t)(t.s.q_start + r / p.group) * p.n_heads + t.kvh * p.group + r % p.group) * D + d;
     *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack(o.x, o.y), pack(o.z, o.w));
 }
-template <int NQ>
 __device__ __forceinline__ void store_lse(const Rows4Params& p, const Item& t, bool bad, int row, float m, float l) {
-    const int r = t.block * 8 * NQ + row;
+    const int r = t.block * kRows + row;
     if (bad || !p.lse || r >= t.s.n * p.group) return;
     p.lse[(size_t)(t.s.q_start + r / p.group) * p.n_heads + t.kvh * p.group + r % p.group] =
         (m + log2_approx(l)) * 0.69314718055994530942f;
@@ -265,9 +265,9 @@ struct Walk {
 };
 
 // Walks the tile list from a sequence on, and starts the copies of one tile at a time.
-template <int D, int NG, int NQ>
+template <int D, int NG>
 struct Feeder {
-    using C = Cfg<D, NG, NQ>;
+    using C = Cfg<D, NG>;
     static constexpr int kParts = C::kRowBytes / 16;  // 16-byte parts of a row
     static constexpr int kPassRows = 32 / kParts;     // rows that the lanes copy at once
     const Rows4Params& p;
@@ -298,14 +298,14 @@ struct Feeder {
         Walk w;
         w.b = b0;
         w.s = seq(w.b);
-        w.e = extent<NQ>(p, w.s);
+        w.e = extent(p, w.s);
         for (;;) {
             const long long all = (long long)w.e.places() * w.e.blocks * p.cache.n_kv_heads;
             if (first < start + all) break;
             start += all;
             ++w.b;  // the list's total says that there is one
             w.s = seq(w.b);
-            w.e = extent<NQ>(p, w.s);
+            w.e = extent(p, w.s);
         }
         int place;
         const int item = (int)divide(first - start, w.e.places(), place);
@@ -323,7 +323,7 @@ struct Feeder {
         w.fresh = max(0, j - w.e.cached);
         w.lo_most = 0;
         if (p.causal && p.window > 0)
-            w.lo_most = w.s.P + min((w.block * C::kRows + C::kRows - 1) / p.group, w.s.n - 1) - p.window + 1;
+            w.lo_most = w.s.P + min((w.block * kRows + kRows - 1) / p.group, w.s.n - 1) - p.window + 1;
         const int slot = (flags >> kSlot) + 1 == C::kStages ? 0 : (flags >> kSlot) + 1;
         flags = slot << kSlot | kFirst | (j > 0 ? kFromBefore : 0);
         if (lane == 0)
@@ -467,7 +467,7 @@ struct Feeder {
                     do {
                         ++w.b;
                         w.s = seq(w.b);
-                        w.e = extent<NQ>(p, w.s);
+                        w.e = extent(p, w.s);
                     } while (w.e.blocks == 0);
                 }
             }
@@ -480,9 +480,9 @@ struct Feeder {
     }
 };
 
-template <int D, int NG, int NQ>
-__global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel(const Rows4Params p) {
-    using C = Cfg<D, NG, NQ>;
+template <int D, int NG>
+__global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(const Rows4Params p) {
+    using C = Cfg<D, NG>;
     constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     constexpr int kGroupChunks = C::kChunks / NG;  // 32-channel chunks of a group
     extern __shared__ __align__(16) uint8_t smem[];
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     __shared__ Tile tiles[kWarps][C::kStages];
     __shared__ Walk walks[kWarps];
     __shared__ Record records[kWarps][2];
-    __shared__ float2 stats[kWarps][2][C::kRows];  // (maximum, sum) of a record's rows
+    __shared__ float2 stats[kWarps][2][kRows];  // (maximum, sum) of a record's rows
     __shared__ long long warp_sums[kWarps];
     __shared__ long long start_of_first;
     __shared__ int first_seq, last_seq;
@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     }
     auto places_of = [&](int b) -> long long {
         if (b >= p.seqs.num_seqs) return 0;
-        const Extent e = extent<NQ>(p, in_table ? table[b] : sequence_of(p, b));
+        const Extent e = extent(p, in_table ? table[b] : sequence_of(p, b));
         return (long long)e.places() * e.blocks * p.cache.n_kv_heads;
     };
     // exclusive prefix sum over the CTA; total: the sum
@@ -572,22 +572,22 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
     // ---- this warp's share
     uint8_t* const ring = smem + warp * C::kStages * C::kTileBytes;
     // a warp's first record: in global memory, its second one: in its ring
-    float* const kept = p.kept + ((size_t)blockIdx.x * kWarps + warp) * C::kRows * D;
+    float* const kept = p.kept + ((size_t)blockIdx.x * kWarps + warp) * kRows * D;
     const long long len = to - from;
     const long long wfrom = from + len * warp / kWarps, wto = from + len * (warp + 1) / kWarps;
     constexpr int kParts = C::kRowBytes / 16;
-    Feeder<D, NG, NQ> feed{p, in_table ? table : nullptr, &walks[warp], items[warp], tiles[warp],
+    Feeder<D, NG> feed{p, in_table ? table : nullptr, &walks[warp], items[warp], tiles[warp],
                            ptx::smem_u32(ring) + lane / kParts * C::kRowBytes + (lane % kParts ^ swizzle<D>(lane / kParts)) * 16,
                            ptx::smem_u32(ring) + 2 * C::kCodes + lane * NG * 4, lane};
     feed.seek(first_seq, start_of_first, wfrom, (int)(wto - wfrom));  // (2^31 tiles of a warp would take an hour)
-    uint32_t qf[NQ][C::kChunks][4];  // Q as the second operand: per chunk two 16-channel steps
-    float2 qsum[NQ][NG];             // sums of a group's channels of queries 2 t4, 2 t4 + 1
-    float o[NQ][C::kChunks][2][4];   // O^T: channels 32 c + 4 g + 2 e (+ 1), queries 2 t4, 2 t4 + 1
-    float2 om[NQ][NG];               // sum of p m over this lane's keys
-    float2 l[NQ];                    // sum of p over this lane's keys
-    float2 scale[NQ];                // from scores as they are accumulated to log2 units
-    float2 neg[NQ], most[NQ];        // less the running maximum m (log2 units; 0 before any key), (m + 8) / scale
-    float2 T[NQ];                    // factor of p s in the second product, and of O with it
+    uint32_t qf[C::kChunks][4];  // Q as the second operand: per chunk two 16-channel steps
+    float2 qsum[NG];             // sums of a group's channels of queries 2 t4, 2 t4 + 1
+    float o[C::kChunks][2][4];   // O^T: channels 32 c + 4 g + 2 e (+ 1), queries 2 t4, 2 t4 + 1
+    float2 om[NG];               // sum of p m over this lane's keys
+    float2 l;                    // sum of p over this lane's keys
+    float2 scale;                // from scores as they are accumulated to log2 units
+    float2 neg, most;            // less the running maximum m (log2 units; 0 before any key), (m + 8) / scale
+    float2 T;                    // factor of p s in the second product, and of O with it
 
     // Whether a sequence is to be skipped whole because its table names a block outside the pool: the
     // CTA looks through the tables of the sequences in its share while the first tiles
@@ -623,67 +623,64 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
 
         if (flags & kFirst) {
             const SeqInfo s = t.s;
+            const int r = t.block * kRows + g;
+            const bool there = r < s.n * p.group;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.q + ((size_t)(s.q_start + (there ? r / p.group : 0)) * p.n_heads + t.kvh * p.group + (there ? r % p.group : 0)) * D);
+            uint4 x[C::kChunks];  // channels 32 c + 8 t4 ...
+            uint32_t top2 = 0;    // largest magnitude, of pairs
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                const int r = t.block * C::kRows + 8 * n + g;
-                const bool there = r < s.n * p.group;
-                const uint4* src = reinterpret_cast<const uint4*>(
-                    p.q + ((size_t)(s.q_start + (there ? r / p.group : 0)) * p.n_heads + t.kvh * p.group + (there ? r % p.group : 0)) * D);
-                uint4 x[C::kChunks];  // channels 32 c + 8 t4 ...
-                uint32_t top2 = 0;    // largest magnitude, of pairs
+            for (int c = 0; c < C::kChunks; ++c) {
+                x[c] = there ? __ldg(src + 4 * c + t4) : make_uint4(0, 0, 0, 0);
+                const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-                for (int c = 0; c < C::kChunks; ++c) {
-                    x[c] = there ? __ldg(src + 4 * c + t4) : make_uint4(0, 0, 0, 0);
-                    const uint32_t y[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top2 = __vmaxu2(top2, y[i] & 0x7fff7fffu);
-                }
-                uint32_t top1 = max(top2 & 0xffffu, top2 >> 16);
-                top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
-                top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
-                // its largest channel goes to [2^14, 2^15)
-                const int up = min(268 - (int)(top1 >> 7), 253);
-                const float f = __int_as_float(up << 23);
-                const float un = __int_as_float((254 - up) << 23) * (p.scale_log2 / kCode);
-                float sum[NG];
-#pragma unroll
-                for (int a = 0; a < NG; ++a) sum[a] = 0.f;
-#pragma unroll
-                for (int c = 0; c < C::kChunks; ++c) {
-                    const float y[8] = {bf16_lo(x[c].x) * f, bf16_hi(x[c].x) * f, bf16_lo(x[c].y) * f, bf16_hi(x[c].y) * f,
-                                        bf16_lo(x[c].z) * f, bf16_hi(x[c].z) * f, bf16_lo(x[c].w) * f, bf16_hi(x[c].w) * f};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float w = i & 1 ? 0.0625f : 1.f;  // odd codes come 16 times as large
-                        qf[n][c][i] = pack_half(y[i] * w, y[i + 4] * w);
-                        sum[c / kGroupChunks] += y[i] + y[i + 4];
-                    }
-                }
-#pragma unroll
-                for (int a = 0; a < NG; ++a) {
-                    sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 1);
-                    sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 2);  // of query g
-                    sum[a] *= kCode;
-                    qsum[n][a].x = __shfl_sync(0xffffffffu, sum[a], 8 * t4);
-                    qsum[n][a].y = __shfl_sync(0xffffffffu, sum[a], 8 * t4 + 4);
-                    om[n][a] = make_float2(0.f, 0.f);
-                }
-                scale[n].x = __shfl_sync(0xffffffffu, un, 8 * t4);
-                scale[n].y = __shfl_sync(0xffffffffu, un, 8 * t4 + 4);
-                neg[n] = l[n] = make_float2(0.f, 0.f);
-                most[n] = both(-INFINITY);
-                T[n] = both(kMostT);
-#pragma unroll
-                for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] = 0.f;
+                for (int i = 0; i < 4; ++i) top2 = __vmaxu2(top2, y[i] & 0x7fff7fffu);
             }
+            uint32_t top1 = max(top2 & 0xffffu, top2 >> 16);
+            top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 1));
+            top1 = max(top1, __shfl_xor_sync(0xffffffffu, top1, 2));
+            // its largest channel goes to [2^14, 2^15)
+            const int up = min(268 - (int)(top1 >> 7), 253);
+            const float f = __int_as_float(up << 23);
+            const float un = __int_as_float((254 - up) << 23) * (p.scale_log2 / kCode);
+            float sum[NG];
+#pragma unroll
+            for (int a = 0; a < NG; ++a) sum[a] = 0.f;
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c) {
+                const float y[8] = {bf16_lo(x[c].x) * f, bf16_hi(x[c].x) * f, bf16_lo(x[c].y) * f, bf16_hi(x[c].y) * f,
+                                    bf16_lo(x[c].z) * f, bf16_hi(x[c].z) * f, bf16_lo(x[c].w) * f, bf16_hi(x[c].w) * f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w = i & 1 ? 0.0625f : 1.f;  // odd codes come 16 times as large
+                    qf[c][i] = pack_half(y[i] * w, y[i + 4] * w);
+                    sum[c / kGroupChunks] += y[i] + y[i + 4];
+                }
+            }
+#pragma unroll
+            for (int a = 0; a < NG; ++a) {
+                sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 1);
+                sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 2);  // of query g
+                sum[a] *= kCode;
+                qsum[a].x = __shfl_sync(0xffffffffu, sum[a], 8 * t4);
+                qsum[a].y = __shfl_sync(0xffffffffu, sum[a], 8 * t4 + 4);
+                om[a] = make_float2(0.f, 0.f);
+            }
+            scale.x = __shfl_sync(0xffffffffu, un, 8 * t4);
+            scale.y = __shfl_sync(0xffffffffu, un, 8 * t4 + 4);
+            neg = l = make_float2(0.f, 0.f);
+            most = both(-INFINITY);
+            T = both(kMostT);
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[c][e / 4][e % 4] = 0.f;
         }
         cp_async_wait<C::kStages - 1>();  // (after the queries' loads: both come at once)
         __syncwarp();
-        // keys [lo, hi] that row 8 n + 2 t4 + e sees
-        auto visible = [&](int n, int e, int& lo, int& hi) {
-            const int tok = min((t.block * C::kRows + 8 * n + 2 * t4 + e) / p.group, t.s.n - 1);
+        // keys [lo, hi] that row 2 t4 + e sees
+        auto visible = [&](int e, int& lo, int& hi) {
+            const int tok = min((t.block * kRows + 2 * t4 + e) / p.group, t.s.n - 1);
             hi = p.causal ? t.s.P + tok : t.s.P + t.s.n - 1;
             lo = p.causal && p.window > 0 ? t.s.P + tok - p.window + 1 : 0;
         };
@@ -691,73 +688,64 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
         // The running maximum, from the largest score `top` of the lane's keys: it is raised, and
         // what was summed under it scaled, only when it falls behind by more than 2^8.  O keeps
         // its size, T is what grows.
-        auto scale_o = [&](int n, float x, float y) {
+        auto scale_o = [&](float x, float y) {
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[n][c][e / 4][e % 4] *= e & 1 ? y : x;
+                for (int e = 0; e < 8; ++e) o[c][e / 4][e % 4] *= e & 1 ? y : x;
         };
-        auto raise = [&](const float2 (&top)[NQ]) {
-            bool behind = false;
+        auto raise = [&](const float2& top) {
+            if (!__any_sync(0xffffffffu, top.x > most.x || top.y > most.y)) return;
+            float alpha[2], t[2], x[2] = {top.x, top.y};
+            const float was[2] = {most.x, most.y}, less[2] = {neg.x, neg.y};
+            const float sc[2] = {scale.x, scale.y}, t0[2] = {T.x, T.y};
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) behind |= top[n].x > most[n].x || top[n].y > most[n].y;
-            if (!__any_sync(0xffffffffu, behind)) return;
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                float alpha[2], t[2], x[2] = {top[n].x, top[n].y};
-                const float was[2] = {most[n].x, most[n].y}, less[2] = {neg[n].x, neg[n].y};
-                const float sc[2] = {scale[n].x, scale[n].y}, t0[2] = {T[n].x, T[n].y};
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 4));
-                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 8));
-                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16));
-                    x[e] *= sc[e];
-                    const bool none = was[e] == -INFINITY;  // no key before
-                    if (!none) x[e] = fmaxf(x[e], -less[e]);
-                    alpha[e] = none ? 0.f : exp2_approx(-less[e] - x[e]);
-                    t[e] = fminf(__fdividef(t0[e], alpha[e]), kMostT);
-                    if (none || !(alpha[e] > 0x1p-100f)) t[e] = kMostT;
-                }
-                scale_o(n, alpha[0] * (t[0] / t0[0]), alpha[1] * (t[1] / t0[1]));
-                T[n] = make_float2(t[0], t[1]);
-                l[n].x *= alpha[0], l[n].y *= alpha[1];
-#pragma unroll
-                for (int a = 0; a < NG; ++a) om[n][a].x *= alpha[0], om[n][a].y *= alpha[1];
-                if (x[0] != -INFINITY) neg[n].x = -x[0], most[n].x = (x[0] + 8.f) / sc[0];
-                if (x[1] != -INFINITY) neg[n].y = -x[1], most[n].y = (x[1] + 8.f) / sc[1];
+            for (int e = 0; e < 2; ++e) {
+                x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 4));
+                x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 8));
+                x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16));
+                x[e] *= sc[e];
+                const bool none = was[e] == -INFINITY;  // no key before
+                if (!none) x[e] = fmaxf(x[e], -less[e]);
+                alpha[e] = none ? 0.f : exp2_approx(-less[e] - x[e]);
+                t[e] = fminf(__fdividef(t0[e], alpha[e]), kMostT);
+                if (none || !(alpha[e] > 0x1p-100f)) t[e] = kMostT;
             }
+            scale_o(alpha[0] * (t[0] / t0[0]), alpha[1] * (t[1] / t0[1]));
+            T = make_float2(t[0], t[1]);
+            l.x *= alpha[0], l.y *= alpha[1];
+#pragma unroll
+            for (int a = 0; a < NG; ++a) om[a].x *= alpha[0], om[a].y *= alpha[1];
+            if (x[0] != -INFINITY) neg.x = -x[0], most.x = (x[0] + 8.f) / sc[0];
+            if (x[1] != -INFINITY) neg.y = -x[1], most.y = (x[1] + 8.f) / sc[1];
         };
         // The factor T of weights that reach `top` without it: where a weight would pass kMostWeight,
         // the largest goes to [2^7, 2^8).
-        auto shrink = [&](const float2 (&top)[NQ]) {
+        auto shrink = [&](const float2& top) {
+            float t[2], x[2] = {top.x, top.y};
+            const float t0[2] = {T.x, T.y};
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                float t[2], x[2] = {top[n].x, top[n].y};
-                const float t0[2] = {T[n].x, T[n].y};
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 4));
-                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 8));
-                    x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16));
-                    x[e] = fminf(x[e], 0x1p127f);
-                    t[e] = x[e] * t0[e] > kMostWeight ? __int_as_float(min(261 - (__float_as_int(x[e]) >> 23), 227) << 23) : t0[e];
-                }
-                scale_o(n, t[0] / t0[0], t[1] / t0[1]);
-                T[n] = make_float2(t[0], t[1]);
+            for (int e = 0; e < 2; ++e) {
+                x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 4));
+                x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 8));
+                x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16));
+                x[e] = fminf(x[e], 0x1p127f);
+                t[e] = x[e] * t0[e] > kMostWeight ? __int_as_float(min(261 - (__float_as_int(x[e]) >> 23), 227) << 23) : t0[e];
             }
+            scale_o(t[0] / t0[0], t[1] / t0[1]);
+            T = make_float2(t[0], t[1]);
         };
 
         if (key >= 0) {
             // ---- 32 cached keys: octet k of them in the matrix rows g of half k / 2
-            float2 sc[NQ][4];  // scores of key 8 k + g, queries 2 t4 and 2 t4 + 1
+            float2 sc[4];  // scores of key 8 k + g, queries 2 t4 and 2 t4 + 1
             const uint32_t row_addr = tile_u32 + lane * C::kRowBytes;
             const uint32_t* kp = reinterpret_cast<const uint32_t*>(tile + 2 * C::kCodes) + g * NG;
             const uint32_t* vp = kp + kTileKeys * NG;
 #pragma unroll
             for (int a = 0; a < NG; ++a) {
                 // (even and odd steps apart: two chains of dependent products instead of one)
-                float acc[NQ][2][4], odd[NQ][2][4];
+                float acc[2][4], odd[2][4];
 #pragma unroll
                 for (int cc = 0; cc < kGroupChunks; ++cc) {
                     const int c = a * kGroupChunks + cc;
@@ -768,15 +756,12 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                         const uint32_t a0 = codes<0>(x[2 * h]), a1 = codes<0>(x[2 * h + 1]), a2 = codes<1>(x[2 * h]),
                                        a3 = codes<1>(x[2 * h + 1]), b0 = codes<2>(x[2 * h]), b1 = codes<2>(x[2 * h + 1]),
                                        b2 = codes<3>(x[2 * h]), b3 = codes<3>(x[2 * h + 1]);
-#pragma unroll
-                        for (int n = 0; n < NQ; ++n) {
-                            if (cc == 0) {
-                                mma_half_first(acc[n][h], a0, a1, a2, a3, qf[n][c][0], qf[n][c][1]);
-                                mma_half_first(odd[n][h], b0, b1, b2, b3, qf[n][c][2], qf[n][c][3]);
-                            } else {
-                                mma_half(acc[n][h], a0, a1, a2, a3, qf[n][c][0], qf[n][c][1]);
-                                mma_half(odd[n][h], b0, b1, b2, b3, qf[n][c][2], qf[n][c][3]);
-                            }
+                        if (cc == 0) {
+                            mma_half_first(acc[h], a0, a1, a2, a3, qf[c][0], qf[c][1]);
+                            mma_half_first(odd[h], b0, b1, b2, b3, qf[c][2], qf[c][3]);
+                        } else {
+                            mma_half(acc[h], a0, a1, a2, a3, qf[c][0], qf[c][1]);
+                            mma_half(odd[h], b0, b1, b2, b3, qf[c][2], qf[c][3]);
                         }
                     }
                 }
@@ -784,98 +769,75 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 for (int k = 0; k < 4; ++k) {
                     const uint32_t w = kp[8 * k * NG + a];
                     const float sk = bf16_lo(w), mk = bf16_hi(w);
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        const int i = 2 * (k & 1);
-                        const float2 qc = __fadd2_rn(make_float2(acc[n][k / 2][i], acc[n][k / 2][i + 1]),
-                                                     make_float2(odd[n][k / 2][i], odd[n][k / 2][i + 1]));
-                        const float2 x = a == 0 ? make_float2(mk * qsum[n][a].x, mk * qsum[n][a].y)
-                                                : make_float2(fmaf(mk, qsum[n][a].x, sc[n][k].x), fmaf(mk, qsum[n][a].y, sc[n][k].y));
-                        sc[n][k] = make_float2(fmaf(sk, qc.x, x.x), fmaf(sk, qc.y, x.y));
-                    }
+                    const int i = 2 * (k & 1);
+                    const float2 qc = __fadd2_rn(make_float2(acc[k / 2][i], acc[k / 2][i + 1]),
+                                                 make_float2(odd[k / 2][i], odd[k / 2][i + 1]));
+                    const float2 x = a == 0 ? make_float2(mk * qsum[a].x, mk * qsum[a].y)
+                                            : make_float2(fmaf(mk, qsum[a].x, sc[k].x), fmaf(mk, qsum[a].y, sc[k].y));
+                    sc[k] = make_float2(fmaf(sk, qc.x, x.x), fmaf(sk, qc.y, x.y));
                 }
             }
             if (flags & kEdge) {
                 // the end of the cached keys, or an edge of a window
                 const int P = t.s.P;
+                int lo[2], hi;
+                visible(0, lo[0], hi);
+                visible(1, lo[1], hi);
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    int lo[2], hi;
-                    visible(n, 0, lo[0], hi);
-                    visible(n, 1, lo[1], hi);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int pos = key + 8 * k + g;
-                        if (pos >= P || pos < lo[0]) sc[n][k].x = -INFINITY;
-                        if (pos >= P || pos < lo[1]) sc[n][k].y = -INFINITY;
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const int pos = key + 8 * k + g;
+                    if (pos >= P || pos < lo[0]) sc[k].x = -INFINITY;
+                    if (pos >= P || pos < lo[1]) sc[k].y = -INFINITY;
                 }
             }
-            float2 top[NQ];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                top[n].x = fmaxf(max3(sc[n][0].x, sc[n][1].x, sc[n][2].x), sc[n][3].x);
-                top[n].y = fmaxf(max3(sc[n][0].y, sc[n][1].y, sc[n][2].y), sc[n][3].y);
-            }
+            float2 top;
+            top.x = fmaxf(max3(sc[0].x, sc[1].x, sc[2].x), sc[3].x);
+            top.y = fmaxf(max3(sc[0].y, sc[1].y, sc[2].y), sc[3].y);
             raise(top);
             float sv[4][NG];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float2 pr[NQ];
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    const float2 x = __ffma2_rn(sc[n][k], scale[n], neg[n]);
-                    pr[n] = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-                    l[n] = __fadd2_rn(l[n], pr[n]);
-                    sc[n][k] = pr[n];
-                }
+                const float2 x = __ffma2_rn(sc[k], scale, neg);
+                const float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+                l = __fadd2_rn(l, pr);
+                sc[k] = pr;
 #pragma unroll
                 for (int a = 0; a < NG; ++a) {
                     const uint32_t w = vp[8 * k * NG + a];
                     const float mv = bf16_hi(w);
                     sv[k][a] = bf16_lo(w);
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-                        om[n][a] = make_float2(fmaf(pr[n].x, mv, om[n][a].x), fmaf(pr[n].y, mv, om[n][a].y));
+                    om[a] = make_float2(fmaf(pr.x, mv, om[a].x), fmaf(pr.y, mv, om[a].y));
                 }
             }
-            uint32_t pt[NQ][NG][4];  // P^T times the values' scales and T, per octet
+            uint32_t pt[NG][4];  // P^T times the values' scales and T, per octet
 #pragma unroll 1
             for (int pass = 0;; ++pass) {
                 float most_w = 0.f;
 #pragma unroll
-                for (int n = 0; n < NQ; ++n)
+                for (int k = 0; k < 4; ++k) {
+                    const float2 x = __fmul2_rn(sc[k], T);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 x = __fmul2_rn(sc[n][k], T[n]);
-#pragma unroll
-                        for (int a = 0; a < NG; ++a) {
-                            const float wx = x.x * sv[k][a], wy = x.y * sv[k][a];
-                            most_w = max3(most_w, wx, wy);
-                            pt[n][a][k] = pack_half(wx, wy);
-                        }
+                    for (int a = 0; a < NG; ++a) {
+                        const float wx = x.x * sv[k][a], wy = x.y * sv[k][a];
+                        most_w = max3(most_w, wx, wy);
+                        pt[a][k] = pack_half(wx, wy);
                     }
-                if (pass > 0 || !__any_sync(0xffffffffu, most_w > kMostWeight)) break;
-                float2 top_w[NQ];
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    top_w[n] = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-#pragma unroll
-                        for (int a = 0; a < NG; ++a) {
-                            top_w[n].x = fmaxf(top_w[n].x, sc[n][k].x * sv[k][a]);
-                            top_w[n].y = fmaxf(top_w[n].y, sc[n][k].y * sv[k][a]);
-                        }
                 }
+                if (pass > 0 || !__any_sync(0xffffffffu, most_w > kMostWeight)) break;
+                float2 top_w = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int a = 0; a < NG; ++a) {
+                        top_w.x = fmaxf(top_w.x, sc[k].x * sv[k][a]);
+                        top_w.y = fmaxf(top_w.y, sc[k].y * sv[k][a]);
+                    }
                 shrink(top_w);
             }
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+            for (int a = 0; a < NG; ++a)
 #pragma unroll
-                for (int a = 0; a < NG; ++a)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) pt[n][a][k] = movmatrix(pt[n][a][k]);
+                for (int k = 0; k < 4; ++k) pt[a][k] = movmatrix(pt[a][k]);
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c) {
                 const int a = c / kGroupChunks;
@@ -886,11 +848,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                     const uint32_t a0 = codes<0>(x[2 * h]), a1 = codes<1>(x[2 * h]), a2 = codes<0>(x[2 * h + 1]),
                                    a3 = codes<1>(x[2 * h + 1]), b0 = codes<2>(x[2 * h]), b1 = codes<3>(x[2 * h]),
                                    b2 = codes<2>(x[2 * h + 1]), b3 = codes<3>(x[2 * h + 1]);
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n) {
-                        mma_half(o[n][c][0], a0, a1, a2, a3, pt[n][a][2 * h], pt[n][a][2 * h + 1]);
-                        mma_half(o[n][c][1], b0, b1, b2, b3, pt[n][a][2 * h], pt[n][a][2 * h + 1]);
-                    }
+                    mma_half(o[c][0], a0, a1, a2, a3, pt[a][2 * h], pt[a][2 * h + 1]);
+                    mma_half(o[c][1], b0, b1, b2, b3, pt[a][2 * h], pt[a][2 * h + 1]);
                 }
             }
         } else {
@@ -901,42 +860,36 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 return pack(x.x * w, x.y * w);
             };
             const int tok0 = -1 - key, tok = tok0 + g, many = t.s.n, P = t.s.P;
-            float acc[NQ][4];
+            float acc[4];
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
+            for (int e = 0; e < 4; ++e) acc[e] = 0.f;
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c) {
                 const uint4 x = *reinterpret_cast<const uint4*>(tile + g * 2 * D + 64 * c + 16 * t4);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    mma(acc[n], __byte_perm(x.x, x.z, 0x5410), 0, __byte_perm(x.x, x.z, 0x7632), 0, as_bf16(qf[n][c][0], 1.f),
-                        as_bf16(qf[n][c][1], 16.f));
-                    mma(acc[n], __byte_perm(x.y, x.w, 0x5410), 0, __byte_perm(x.y, x.w, 0x7632), 0, as_bf16(qf[n][c][2], 1.f),
-                        as_bf16(qf[n][c][3], 16.f));
-                }
+                mma(acc, __byte_perm(x.x, x.z, 0x5410), 0, __byte_perm(x.x, x.z, 0x7632), 0, as_bf16(qf[c][0], 1.f),
+                    as_bf16(qf[c][1], 16.f));
+                mma(acc, __byte_perm(x.y, x.w, 0x5410), 0, __byte_perm(x.y, x.w, 0x7632), 0, as_bf16(qf[c][2], 1.f),
+                    as_bf16(qf[c][3], 16.f));
             }
-            float2 top[NQ];
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    int lo, hi;
-                    visible(n, e, lo, hi);
-                    acc[n][e] = tok >= many || P + tok > hi || P + tok < lo ? -INFINITY : acc[n][e] * kCode;
-                }
-                top[n] = make_float2(acc[n][0], acc[n][1]);
+            for (int e = 0; e < 2; ++e) {
+                int lo, hi;
+                visible(e, lo, hi);
+                acc[e] = tok >= many || P + tok > hi || P + tok < lo ? -INFINITY : acc[e] * kCode;
             }
+            const float2 top = make_float2(acc[0], acc[1]);
             raise(top);
-            uint32_t pt[NQ];
-#pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                const float2 x = __ffma2_rn(top[n], scale[n], neg[n]);
-                const float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-                l[n] = __fadd2_rn(l[n], pr);
-                pt[n] = movmatrix(pack(pr.x * T[n].x * kCode, pr.y * T[n].y * kCode));
+            // the weights here are p itself, at most: T is what scaled it to fp16's range so far
+            constexpr float kOwn = 1.f / kCode;
+            if (__any_sync(0xffffffffu, T.x > kOwn || T.y > kOwn)) {
+                const float2 t1 = make_float2(fminf(T.x, kOwn), fminf(T.y, kOwn));
+                scale_o(t1.x / T.x, t1.y / T.y);
+                T = t1;
             }
+            const float2 x = __ffma2_rn(top, scale, neg);
+            const float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
+            l = __fadd2_rn(l, pr);
+            const uint32_t pt = movmatrix(pack(pr.x * T.x * kCode, pr.y * T.y * kCode));
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c) {
                 const uint8_t* v = tile + C::kCodes + 64 * c + 8 * g;
@@ -945,11 +898,8 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 // odd channels 16 times as large, as the codes' are
                 auto odd = [](uint32_t lo, uint32_t hi) -> uint32_t { return pack(bf16_hi(lo) * 16.f, bf16_hi(hi) * 16.f); };
                 const uint32_t v1 = odd(x.x, y.x), v3 = odd(x.y, y.y);
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) {
-                    mma(o[n][c][0], __byte_perm(x.x, y.x, 0x5410), v1, 0, 0, pt[n], 0);
-                    mma(o[n][c][1], __byte_perm(x.y, y.y, 0x5410), v3, 0, 0, pt[n], 0);
-                }
+                mma(o[c][0], __byte_perm(x.x, y.x, 0x5410), v1, 0, 0, pt, 0);
+                mma(o[c][1], __byte_perm(x.y, y.y, 0x5410), v3, 0, 0, pt, 0);
             }
             if (t.block == 0 && !bad_table(t.b)) {
                 // their rows go into the cache, once per KV head
@@ -984,43 +934,40 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
             float* const rec = slot == 0 ? kept : reinterpret_cast<float*>(ring);
             __syncwarp();
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
+            for (int e = 0; e < 2; ++e) {
+                float x = e ? l.y : l.x;
+                x += __shfl_xor_sync(0xffffffffu, x, 4);
+                x += __shfl_xor_sync(0xffffffffu, x, 8);
+                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                float add[NG];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = e ? l[n].y : l[n].x;
-                    x += __shfl_xor_sync(0xffffffffu, x, 4);
-                    x += __shfl_xor_sync(0xffffffffu, x, 8);
-                    x += __shfl_xor_sync(0xffffffffu, x, 16);
-                    float add[NG];
+                for (int a = 0; a < NG; ++a) {
+                    float y = e ? om[a].y : om[a].x;
+                    y += __shfl_xor_sync(0xffffffffu, y, 4);
+                    y += __shfl_xor_sync(0xffffffffu, y, 8);
+                    y += __shfl_xor_sync(0xffffffffu, y, 16);
+                    add[a] = y;
+                }
+                const int row = 2 * t4 + e;
+                const float f = whole ? 1.f / x : 1.f;
+                const float un = f / (kCode * (e ? T.y : T.x)), odd = 0.0625f * un;
+                // (-inf where the share's keys are all hidden from the row)
+                const float m = (e ? most.y : most.x) == -INFINITY ? -INFINITY : -(e ? neg.y : neg.x);
 #pragma unroll
-                    for (int a = 0; a < NG; ++a) {
-                        float y = e ? om[n][a].y : om[n][a].x;
-                        y += __shfl_xor_sync(0xffffffffu, y, 4);
-                        y += __shfl_xor_sync(0xffffffffu, y, 8);
-                        y += __shfl_xor_sync(0xffffffffu, y, 16);
-                        add[a] = y;
-                    }
-                    const int row = 8 * n + 2 * t4 + e;
-                    const float f = whole ? 1.f / x : 1.f;
-                    const float un = f / (kCode * (e ? T[n].y : T[n].x)), odd = 0.0625f * un;
-                    // (-inf where the share's keys are all hidden from the row)
-                    const float m = (e ? most[n].y : most[n].x) == -INFINITY ? -INFINITY : -(e ? neg[n].y : neg[n].x);
-#pragma unroll
-                    for (int c = 0; c < C::kChunks; ++c) {
-                        const float y = add[c / kGroupChunks] * f;
-                        const float4 v = make_float4(fmaf(o[n][c][0][e], un, y), fmaf(o[n][c][0][2 + e], odd, y),
-                                                     fmaf(o[n][c][1][e], un, y), fmaf(o[n][c][1][2 + e], odd, y));
-                        if (whole)
-                            store_row<D, NQ>(p, t, bad_table(t.b), row, 32 * c + 4 * g, v);
-                        else
-                            *reinterpret_cast<float4*>(rec + row * D + 32 * c + 4 * g) = v;
-                    }
-                    if (g == 0) {
-                        if (whole)
-                            store_lse<NQ>(p, t, bad_table(t.b), row, m, x);
-                        else
-                            stats[warp][slot][row] = make_float2(m, x);
-                    }
+                for (int c = 0; c < C::kChunks; ++c) {
+                    const float y = add[c / kGroupChunks] * f;
+                    const float4 v = make_float4(fmaf(o[c][0][e], un, y), fmaf(o[c][0][2 + e], odd, y),
+                                                 fmaf(o[c][1][e], un, y), fmaf(o[c][1][2 + e], odd, y));
+                    if (whole)
+                        store_row<D>(p, t, bad_table(t.b), row, 32 * c + 4 * g, v);
+                    else
+                        *reinterpret_cast<float4*>(rec + row * D + 32 * c + 4 * g) = v;
+                }
+                if (g == 0) {
+                    if (whole)
+                        store_lse(p, t, bad_table(t.b), row, m, x);
+                    else
+                        stats[warp][slot][row] = make_float2(m, x);
                 }
             }
             if (!whole && lane == 0) {
@@ -1033,7 +980,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
         __syncwarp();
     }
     cp_async_wait<0>();
-    constexpr int kElems = C::kRows * D;
+    constexpr int kElems = kRows * D;
     __syncwarp();
     if (records[warp][0].valid) {
         // the first record joins the second one in the ring
@@ -1086,12 +1033,12 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
             }
             if (whole) {
                 const float f = 1.f / sum;
-                store_row<D, NQ>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-                if (x % D == 0) store_lse<NQ>(p, t, bad_table(t.b), row, top, sum);
+                store_row<D>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+                if (x % D == 0) store_lse(p, t, bad_table(t.b), row, top, sum);
             } else {
                 const size_t at = (size_t)blockIdx.x * 2 + slot;
                 __stcg(reinterpret_cast<float4*>(p.part + at * kElems + x), v);
-                if (x % D == 0) __stcg(part_stats + at * C::kRows + row, make_float2(top, sum));
+                if (x % D == 0) __stcg(part_stats + at * kRows + row, make_float2(top, sum));
             }
         }
         if (!whole) pending[slot] = i;
@@ -1141,7 +1088,7 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                     y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
                     if (c + i < pieces[k]) {
                         const size_t at = (size_t)(c0[k] + c + i) * 2 + (c + i == 0 ? 1 : 0);
-                        st[i] = __ldcg(part_stats + at * C::kRows + row);
+                        st[i] = __ldcg(part_stats + at * kRows + row);
                         y[i] = __ldcg(reinterpret_cast<const float4*>(p.part + at * kElems + x));
                     }
                 }
@@ -1161,15 +1108,15 @@ __global__ void __launch_bounds__(Cfg<D, NG, NQ>::kThreads, 1) attn_rows4_kernel
                 }
             }
             const float f = 1.f / sum;
-            store_row<D, NQ>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-            if (x % D == 0) store_lse<NQ>(p, t, bad_table(t.b), row, top, sum);
+            store_row<D>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+            if (x % D == 0) store_lse(p, t, bad_table(t.b), row, top, sum);
         }
     }
 }
 
-template <int D, int NG, int NQ>
+template <int D, int NG>
 cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
-    using C = Cfg<D, NG, NQ>;
+    using C = Cfg<D, NG>;
     constexpr int kSmem = C::kWarps * C::kStages * C::kTileBytes;
     static_assert(kSmem <= 215 * 1024, "shared memory budget, beside the static part");
     static int configured_for[64] = {0};
@@ -1177,7 +1124,7 @@ cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     cudaGetDevice(&dev);
     if (dev >= 64 || !configured_for[dev]) {
         const cudaError_t e =
-            cudaFuncSetAttribute(attn_rows4_kernel<D, NG, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+            cudaFuncSetAttribute(attn_rows4_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) configured_for[dev] = 1;
     }
@@ -1191,7 +1138,7 @@ cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_rows4_kernel<D, NG, NQ>, p);
+    return cudaLaunchKernelEx(&cfg, attn_rows4_kernel<D, NG>, p);
 }
 
 }  // namespace rows4

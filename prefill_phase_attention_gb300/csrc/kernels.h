@@ -240,20 +240,14 @@ struct Rows4Params {
     float scale_log2;
     int causal, window;
     const int* taken;  // sequences that another kernel takes (not 0); nullptr: none
-    // partial results that CTAs hand one another: [grid][2] of 8 * row_tiles rows of D
+    // partial results that CTAs hand one another: [grid][2] of 8 rows of D
     // floats, then as many (maximum, sum) pairs; arrivals[grid] is zero between calls
     float* part;
     int* arrivals;
-    float* kept;  // [grid][kRows4Warps] of 8 * row_tiles rows of D floats: records of a CTA's warps
+    float* kept;  // [grid][kRows4Warps] of 8 rows of D floats: records of a CTA's warps
 };
 constexpr int kRows4Warps = 16, kRows4Grid = 256;  // at most
-template <int D>
-cudaError_t launch_attn_rows4_d(const Rows4Params& p, int row_tiles, int grid, cudaStream_t stream);
-template <>
-cudaError_t launch_attn_rows4_d<64>(const Rows4Params& p, int row_tiles, int grid, cudaStream_t stream);
-template <>
-cudaError_t launch_attn_rows4_d<128>(const Rows4Params& p, int row_tiles, int grid, cudaStream_t stream);
-// row_tiles: query rows of a row block, in tiles of 8, 1 or 2.
-cudaError_t launch_attn_rows4(const Rows4Params& p, int head_dim, int row_tiles, int grid, cudaStream_t stream);
+cudaError_t launch_attn_rows4(const Rows4Params& p, int head_dim, int grid, cudaStream_t stream);
+cudaError_t launch_attn_rows4_128(const Rows4Params& p, int grid, cudaStream_t stream);
 
 }  // namespace pa

@@ -59,7 +59,7 @@ class Cache:
         for which in range(2):
             x = torch.randn((slots, hk, rows, d), generator=g) + (offset if which == 0 else 0)
             if kind == "large":
-                x *= 2.0 ** 40
+                x *= 2.0 ** 60
             c, p = quantise(x.to(torch.bfloat16), group)
             self.codes.append(c)
             self.params.append(p)

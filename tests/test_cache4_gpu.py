@@ -55,7 +55,7 @@ class Call:
         cap = max(p + n for p, n in zip(lens, new)) + slack
         self.cache = R.Cache(g, len(new), cap, hk, d, group or d, block, kind=kind)
         t = sum(new)
-        size = 2.0 ** 40 if kind == "large" else 1.0
+        size = 2.0 ** 60 if kind == "large" else 1.0
         self.q = (torch.randn((t, hk * share, d), generator=g) / size).to(torch.bfloat16)
         self.k = (torch.randn((t, hk, d), generator=g) * size).to(torch.bfloat16)
         self.v = (torch.randn((t, hk, d), generator=g) * size).to(torch.bfloat16)
@@ -230,9 +230,10 @@ def test_many_sequences():
     c.check()
 
 
-def test_large_values():
-    """Scales far outside fp16's range."""
-    c = Call(8, [1, 6], [300, 45], group=64, kind="large")
+@pytest.mark.parametrize("new,lens", [([1, 6], [300, 45]), ([3, 1, 9], [0, 0, 0])])
+def test_large_values(new, lens):
+    """Keys and values (and their scales) far outside fp16's range."""
+    c = Call(8, new, lens, group=64, kind="large")
     c.attend()
     c.check()
 
