@@ -577,8 +577,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     const long long wfrom = from + len * warp / kWarps, wto = from + len * (warp + 1) / kWarps;
     constexpr int kParts = C::kRowBytes / 16;
     Feeder<D, NG> feed{p, in_table ? table : nullptr, &walks[warp], items[warp], tiles[warp],
-                           ptx::smem_u32(ring) + lane / kParts * C::kRowBytes + (lane % kParts ^ swizzle<D>(lane / kParts)) * 16,
-                           ptx::smem_u32(ring) + 2 * C::kCodes + lane * NG * 4, lane};
+                       ptx::smem_u32(ring) + lane / kParts * C::kRowBytes + (lane % kParts ^ swizzle<D>(lane / kParts)) * 16,
+                       ptx::smem_u32(ring) + 2 * C::kCodes + lane * NG * 4, lane};
     feed.seek(first_seq, start_of_first, wfrom, (int)(wto - wfrom));  // (2^31 tiles of a warp would take an hour)
     uint32_t qf[C::kChunks][4];  // Q as the second operand: per chunk two 16-channel steps
     float2 qsum[NG];             // sums of a group's channels of queries 2 t4, 2 t4 + 1
@@ -1005,55 +1005,61 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
         const int prev_hi = __shfl_sync(0xffffffffu, hi, prev), prev_lo = __shfl_sync(0xffffffffu, lo, prev);
         begins = __ballot_sync(0xffffffffu, have && !(before != 0 && prev_hi == hi && prev_lo == lo));
     }
-    int pending[2] = {-1, -1};  // records whose row block other CTAs share: it began before, it goes on
-    for (unsigned left = begins; left != 0; left &= left - 1) {
-        const int i = __ffs(left) - 1;
-        const unsigned others = left & (left - 1);
-        const unsigned members = valid & ~((1u << i) - 1) & (others ? (others & -others) - 1 : 0xffffffffu);
+    // the first record's row block may have begun in a CTA before, the last one's may go on
+    auto start_of = [&](int i) -> long long {
         const Item& t = records[i / 2][i & 1].t;
-        const long long b0 = ((long long)t.start_hi << 32) | (unsigned)t.start_lo;
-        const bool whole = b0 >= from && b0 + t.tiles <= to;
-        const int slot = b0 < from ? 0 : 1;  // of the partial results
-        for (int x = tid * 4; x < kElems; x += kThreads * 4) {
-            const int row = x / D;
-            float top = -INFINITY;
-            for (unsigned m = members; m != 0; m &= m - 1) {
-                const int k = __ffs(m) - 1;
-                top = fmaxf(top, stats[k / 2][k & 1][row].x);
-            }
-            float sum = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (unsigned m = members; m != 0; m &= m - 1) {
-                const int k = __ffs(m) - 1;
-                const float2 st = stats[k / 2][k & 1][row];
-                const float w = st.x == -INFINITY ? 0.f : exp2_approx(st.x - top);
-                const float4 y = *reinterpret_cast<const float4*>(record_data(k) + x);
-                sum = fmaf(w, st.y, sum);
-                v.x = fmaf(w, y.x, v.x), v.y = fmaf(w, y.y, v.y), v.z = fmaf(w, y.z, v.z), v.w = fmaf(w, y.w, v.w);
-            }
-            if (whole) {
-                const float f = 1.f / sum;
-                store_row<D>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-                if (x % D == 0) store_lse(p, t, bad_table(t.b), row, top, sum);
-            } else {
-                const size_t at = (size_t)blockIdx.x * 2 + slot;
-                __stcg(reinterpret_cast<float4*>(p.part + at * kElems + x), v);
-                if (x % D == 0) __stcg(part_stats + at * kRows + row, make_float2(top, sum));
-            }
+        return ((long long)t.start_hi << 32) | (unsigned)t.start_lo;
+    };
+    if (begins == 0) return;  // (the whole CTA)
+    int shared[2];            // records of the row blocks that other CTAs share: it began before, it goes on
+    {
+        const int i = __ffs(begins) - 1, k = 31 - __clz(begins);
+        shared[0] = start_of(i) < from ? i : -1;
+        shared[1] = start_of(k) >= from && start_of(k) + records[k / 2][k & 1].t.tiles > to ? k : -1;
+    }
+    // a warp takes 128 channels of a row block at a time
+    constexpr int kUnits = kElems / 128;
+    const int rank = __popc(begins & ((1u << lane) - 1)), row_blocks = __popc(begins);
+    for (int u = warp; u < row_blocks * kUnits; u += kWarps) {
+        const int i = __ffs(__ballot_sync(0xffffffffu, (begins >> lane & 1) && rank == u / kUnits)) - 1;
+        const unsigned later = begins & ~((2u << i) - 1);
+        unsigned members = valid & ~((1u << i) - 1) & (later ? (later & -later) - 1 : 0xffffffffu);
+        const int x = u % kUnits * 128 + lane * 4, row = x / D;
+        float top = -INFINITY;
+        for (unsigned m = members; m != 0; m &= m - 1) {
+            const int k = __ffs(m) - 1;
+            top = fmaxf(top, stats[k / 2][k & 1][row].x);
         }
-        if (!whole) pending[slot] = i;
+        float sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (; members != 0; members &= members - 1) {
+            const int k = __ffs(members) - 1;
+            const float2 st = stats[k / 2][k & 1][row];
+            const float w = st.x == -INFINITY ? 0.f : exp2_approx(st.x - top);
+            const float4 y = *reinterpret_cast<const float4*>(record_data(k) + x);
+            sum = fmaf(w, st.y, sum);
+            v.x = fmaf(w, y.x, v.x), v.y = fmaf(w, y.y, v.y), v.z = fmaf(w, y.z, v.z), v.w = fmaf(w, y.w, v.w);
+        }
+        if (i != shared[0] && i != shared[1]) {
+            const Item& t = records[i / 2][i & 1].t;
+            const float f = 1.f / sum;
+            store_row<D>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+            if (x % D == 0) store_lse(p, t, bad_table(t.b), row, top, sum);
+        } else {
+            const size_t at = (size_t)blockIdx.x * 2 + (i == shared[0] ? 0 : 1);
+            __stcg(reinterpret_cast<float4*>(p.part + at * kElems + x), v);
+            if (x % D == 0) __stcg(part_stats + at * kRows + row, make_float2(top, sum));
+        }
     }
 
     // ---- row blocks that several CTAs share: the last to arrive joins them, in list order
-    if (pending[0] < 0 && pending[1] < 0) return;  // (the whole CTA)
+    if (shared[0] < 0 && shared[1] < 0) return;  // (the whole CTA)
     int c0[2], pieces[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        if (pending[k] < 0) continue;
-        const Item& t = records[pending[k] / 2][pending[k] & 1].t;
-        const long long b0 = ((long long)t.start_hi << 32) | (unsigned)t.start_lo;
-        c0[k] = (int)(b0 / share);
-        pieces[k] = (int)((b0 + t.tiles - 1) / share) - c0[k] + 1;
+        if (shared[k] < 0) continue;
+        c0[k] = (int)(start_of(shared[k]) / share);
+        pieces[k] = (int)((start_of(shared[k]) + records[shared[k] / 2][shared[k] & 1].t.tiles - 1) / share) - c0[k] + 1;
     }
     __syncthreads();
     if (tid == 0) {
@@ -1061,56 +1067,54 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
         int old[2] = {-1, -1};
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            if (pending[k] >= 0) old[k] = atomicAdd(p.arrivals + c0[k], 1);
+            if (shared[k] >= 0) old[k] = atomicAdd(p.arrivals + c0[k], 1);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            joins[k] = pending[k] >= 0 && old[k] == pieces[k] - 1;
+            joins[k] = shared[k] >= 0 && old[k] == pieces[k] - 1;
             if (joins[k]) p.arrivals[c0[k]] = 0;
         }
         __threadfence();
     }
     __syncthreads();
-#pragma unroll 1
-    for (int k = 0; k < 2; ++k) {
+    for (int u = warp; u < 2 * kUnits; u += kWarps) {
+        const int k = u / kUnits, x = u % kUnits * 128 + lane * 4, row = x / D;
         if (!joins[k]) continue;
-        const Item& t = records[pending[k] / 2][pending[k] & 1].t;
-        for (int x = tid * 4; x < kElems; x += kThreads * 4) {
-            const int row = x / D;
-            float top = -INFINITY, sum = 0.f;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-            constexpr int kAtOnce = 8;
-            for (int c = 0; c < pieces[k]; c += kAtOnce) {
-                float4 y[kAtOnce];
-                float2 st[kAtOnce];
+        const int i = k == 0 ? shared[0] : shared[1], first = k == 0 ? c0[0] : c0[1], count = k == 0 ? pieces[0] : pieces[1];
+        float top = -INFINITY, sum = 0.f;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int kAtOnce = 8;
+        for (int c = 0; c < count; c += kAtOnce) {
+            float4 y[kAtOnce];
+            float2 st[kAtOnce];
 #pragma unroll
-                for (int i = 0; i < kAtOnce; ++i) {
-                    st[i] = make_float2(-INFINITY, 0.f);
-                    y[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (c + i < pieces[k]) {
-                        const size_t at = (size_t)(c0[k] + c + i) * 2 + (c + i == 0 ? 1 : 0);
-                        st[i] = __ldcg(part_stats + at * kRows + row);
-                        y[i] = __ldcg(reinterpret_cast<const float4*>(p.part + at * kElems + x));
-                    }
-                }
-                float most_here = top;
-#pragma unroll
-                for (int i = 0; i < kAtOnce; ++i) most_here = fmaxf(most_here, st[i].x);
-                const float use = most_here == -INFINITY ? 0.f : most_here;  // (no key yet: the weights are 0)
-                const float f = exp2_approx(top - use);
-                top = most_here;
-                sum *= f;
-                v.x *= f, v.y *= f, v.z *= f, v.w *= f;
-#pragma unroll
-                for (int i = 0; i < kAtOnce; ++i) {
-                    const float w = exp2_approx(st[i].x - use);
-                    sum = fmaf(w, st[i].y, sum);
-                    v.x = fmaf(w, y[i].x, v.x), v.y = fmaf(w, y[i].y, v.y), v.z = fmaf(w, y[i].z, v.z), v.w = fmaf(w, y[i].w, v.w);
+            for (int e = 0; e < kAtOnce; ++e) {
+                st[e] = make_float2(-INFINITY, 0.f);
+                y[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c + e < count) {
+                    const size_t at = (size_t)(first + c + e) * 2 + (c + e == 0 ? 1 : 0);
+                    st[e] = __ldcg(part_stats + at * kRows + row);
+                    y[e] = __ldcg(reinterpret_cast<const float4*>(p.part + at * kElems + x));
                 }
             }
-            const float f = 1.f / sum;
-            store_row<D>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
-            if (x % D == 0) store_lse(p, t, bad_table(t.b), row, top, sum);
+            float most_here = top;
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) most_here = fmaxf(most_here, st[e].x);
+            const float use = most_here == -INFINITY ? 0.f : most_here;  // (no key yet: the weights are 0)
+            const float f = exp2_approx(top - use);
+            top = most_here;
+            sum *= f;
+            v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+#pragma unroll
+            for (int e = 0; e < kAtOnce; ++e) {
+                const float w = exp2_approx(st[e].x - use);
+                sum = fmaf(w, st[e].y, sum);
+                v.x = fmaf(w, y[e].x, v.x), v.y = fmaf(w, y[e].y, v.y), v.z = fmaf(w, y[e].z, v.z), v.w = fmaf(w, y[e].w, v.w);
+            }
         }
+        const Item& t = records[i / 2][i & 1].t;
+        const float f = 1.f / sum;
+        store_row<D>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+        if (x % D == 0) store_lse(p, t, bad_table(t.b), row, top, sum);
     }
 }
 
