@@ -61,7 +61,7 @@ struct Cfg {
     // As many warps as registers (16: 128 a thread, 12: 168) allow: the
     // instructions of a tile take most of the time that its bytes do, so the issue slots
     // have to be filled.
-    static constexpr int kWarps = NG > 1 ? 12 : 16;
+    static constexpr int kWarps = NG == 4 ? 12 : 16;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kChunks = D / 32;
     static constexpr int kRowBytes = D / 2;
@@ -178,6 +178,12 @@ __device__ __forceinline__ void mma_half(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_half_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                                uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
@@ -232,6 +238,8 @@ __device__ __forceinline__ uint32_t codes(uint32_t x) {
 constexpr float kCode = 0x1p-24f;    // unit of a code
 constexpr float kMostT = 0x1p100f;   // largest factor of the weights
 constexpr float kMostWeight = 0x1p15f;
+
+__device__ __forceinline__ float to_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
 template <int D>
 __device__ __forceinline__ int swizzle(int key) {  // of a row's 16-byte parts
@@ -581,7 +589,9 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                        ptx::smem_u32(ring) + 2 * C::kCodes + lane * NG * 4, lane};
     feed.seek(first_seq, start_of_first, wfrom, (int)(wto - wfrom));  // (2^31 tiles of a warp would take an hour)
     uint32_t qf[C::kChunks][4];  // Q as the second operand: per chunk two 16-channel steps
-    float2 qsum[NG];             // sums of a group's channels of queries 2 t4, 2 t4 + 1
+    // sums of query g's channels by group, each as three bf16 terms, as the second operand of
+    // the minima's product: places 0 .. NG - 1 the first terms, then the second, then the third
+    uint32_t qsum[2];
     float o[C::kChunks][2][4];   // O^T: channels 32 c + 4 g + 2 e (+ 1), queries 2 t4, 2 t4 + 1
     float2 om[NG];               // sum of p m over this lane's keys
     float2 l;                    // sum of p over this lane's keys
@@ -662,9 +672,25 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 1);
                 sum[a] += __shfl_xor_sync(0xffffffffu, sum[a], 2);  // of query g
                 sum[a] *= kCode;
-                qsum[a].x = __shfl_sync(0xffffffffu, sum[a], 8 * t4);
-                qsum[a].y = __shfl_sync(0xffffffffu, sum[a], 8 * t4 + 4);
                 om[a] = make_float2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float term[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int place = 8 * h + 2 * t4 + e;
+                    float x = 0.f;
+#pragma unroll
+                    for (int a = 0; a < NG; ++a) {
+                        const float first = to_bf16(sum[a]), second = to_bf16(sum[a] - first);
+                        if (place == a) x = first;
+                        if (place == NG + a) x = second;
+                        if (place == 2 * NG + a) x = sum[a] - first - second;
+                    }
+                    term[e] = x;
+                }
+                qsum[h] = pack(term[0], term[1]);
             }
             scale.x = __shfl_sync(0xffffffffu, un, 8 * t4);
             scale.y = __shfl_sync(0xffffffffu, un, 8 * t4 + 4);
@@ -738,14 +764,25 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
 
         if (key >= 0) {
             // ---- 32 cached keys: octet k of them in the matrix rows g of half k / 2
-            float2 sc[4];  // scores of key 8 k + g, queries 2 t4 and 2 t4 + 1
+            // scores of key 8 k + g (accumulators 2 (k % 2) of half k / 2), queries 2 t4 and 2 t4 + 1:
+            // first what the minima add
+            float score[2][4];
             const uint32_t row_addr = tile_u32 + lane * C::kRowBytes;
             const uint32_t* kp = reinterpret_cast<const uint32_t*>(tile + 2 * C::kCodes) + g * NG;
             const uint32_t* vp = kp + kTileKeys * NG;
+            constexpr int kPair = NG > 1 ? 2 : 1;  // groups of a lane's two places
+            const uint32_t* const km = kp + kPair * (NG == 4 ? t4 & 1 : 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t a0 = __byte_perm(km[16 * h * NG], km[16 * h * NG + kPair - 1], 0x7632);
+                const uint32_t a1 = __byte_perm(km[(16 * h + 8) * NG], km[(16 * h + 8) * NG + kPair - 1], 0x7632);
+                mma_first(score[h], a0, a1, a0, a1, qsum[0], qsum[1]);
+            }
 #pragma unroll
             for (int a = 0; a < NG; ++a) {
-                // (even and odd steps apart: two chains of dependent products instead of one)
-                float acc[2][4], odd[2][4];
+                // (one group: even and odd steps apart, two chains of dependent products for one)
+                constexpr int kChains = NG == 1 && kGroupChunks > 1 ? 2 : 1;
+                float acc[kChains][2][4];
 #pragma unroll
                 for (int cc = 0; cc < kGroupChunks; ++cc) {
                     const int c = a * kGroupChunks + cc;
@@ -756,27 +793,29 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                         const uint32_t a0 = codes<0>(x[2 * h]), a1 = codes<0>(x[2 * h + 1]), a2 = codes<1>(x[2 * h]),
                                        a3 = codes<1>(x[2 * h + 1]), b0 = codes<2>(x[2 * h]), b1 = codes<2>(x[2 * h + 1]),
                                        b2 = codes<3>(x[2 * h]), b3 = codes<3>(x[2 * h + 1]);
-                        if (cc == 0) {
-                            mma_half_first(acc[h], a0, a1, a2, a3, qf[c][0], qf[c][1]);
-                            mma_half_first(odd[h], b0, b1, b2, b3, qf[c][2], qf[c][3]);
-                        } else {
-                            mma_half(acc[h], a0, a1, a2, a3, qf[c][0], qf[c][1]);
-                            mma_half(odd[h], b0, b1, b2, b3, qf[c][2], qf[c][3]);
-                        }
+                        if (cc == 0)
+                            mma_half_first(acc[0][h], a0, a1, a2, a3, qf[c][0], qf[c][1]);
+                        else
+                            mma_half(acc[0][h], a0, a1, a2, a3, qf[c][0], qf[c][1]);
+                        if (cc == 0 && kChains == 2)
+                            mma_half_first(acc[kChains - 1][h], b0, b1, b2, b3, qf[c][2], qf[c][3]);
+                        else
+                            mma_half(acc[kChains - 1][h], b0, b1, b2, b3, qf[c][2], qf[c][3]);
                     }
                 }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const uint32_t w = kp[8 * k * NG + a];
-                    const float sk = bf16_lo(w), mk = bf16_hi(w);
-                    const int i = 2 * (k & 1);
-                    const float2 qc = __fadd2_rn(make_float2(acc[k / 2][i], acc[k / 2][i + 1]),
-                                                 make_float2(odd[k / 2][i], odd[k / 2][i + 1]));
-                    const float2 x = a == 0 ? make_float2(mk * qsum[a].x, mk * qsum[a].y)
-                                            : make_float2(fmaf(mk, qsum[a].x, sc[k].x), fmaf(mk, qsum[a].y, sc[k].y));
-                    sc[k] = make_float2(fmaf(sk, qc.x, x.x), fmaf(sk, qc.y, x.y));
+                    const float sk = bf16_lo(kp[8 * k * NG + a]);
+                    const int h = k / 2, i = 2 * (k & 1);
+                    float2 qc = make_float2(acc[0][h][i], acc[0][h][i + 1]);
+                    if (kChains == 2) qc = __fadd2_rn(qc, make_float2(acc[kChains - 1][h][i], acc[kChains - 1][h][i + 1]));
+                    score[h][i] = fmaf(sk, qc.x, score[h][i]);
+                    score[h][i + 1] = fmaf(sk, qc.y, score[h][i + 1]);
                 }
             }
+            float2 sc[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) sc[k] = make_float2(score[k / 2][2 * (k & 1)], score[k / 2][2 * (k & 1) + 1]);
             if (flags & kEdge) {
                 // the end of the cached keys, or an edge of a window
                 const int P = t.s.P;
@@ -1122,7 +1161,7 @@ template <int D, int NG>
 cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     using C = Cfg<D, NG>;
     constexpr int kSmem = C::kWarps * C::kStages * C::kTileBytes;
-    static_assert(kSmem <= 215 * 1024, "shared memory budget, beside the static part");
+    static_assert(kSmem <= 216 * 1024, "shared memory budget, beside the static part");
     static int configured_for[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
