@@ -1531,6 +1531,7 @@ pa_status copy_cache4(const void* k, const void* v, const int32_t* cu_seqlens, c
     p.v = static_cast<const __nv_bfloat16*>(v);
     p.k_out = write ? nullptr : static_cast<__nv_bfloat16*>(const_cast<void*>(k));
     p.v_out = write ? nullptr : static_cast<__nv_bfloat16*>(const_cast<void*>(v));
+    p.aligned32 = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0;
     e = write ? pa::launch_write_cache4(p, head_dim, sms, stream)
               : pa::launch_read_cache4(p, head_dim, sms, stream);
     if (e != cudaSuccess) return cuda_fail(e, write ? "cache write launch" : "cache read launch");
@@ -1707,6 +1708,7 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         x.write.k = static_cast<const __nv_bfloat16*>(k);
         x.write.v = static_cast<const __nv_bfloat16*>(v);
         x.write.k_out = x.write.v_out = nullptr;
+        x.write.aligned32 = false;
         e = pa::launch_expand4(x, head_dim, sms, stream);
         if (e != cudaSuccess) return cuda_fail(e, "expansion launch");
         pa::FwdParams fp;

@@ -950,8 +950,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                     uint32_t kw, vw, kc[1], vc[1];
                     const uint4 kx[1] = {*reinterpret_cast<const uint4*>(tile + r * 2 * D + part * 16)};
                     const uint4 vx[1] = {*reinterpret_cast<const uint4*>(tile + C::kCodes + r * 2 * D + part * 16)};
-                    quantise(kx, kGroupLanes, kc, &kw);
-                    quantise(vx, kGroupLanes, vc, &vw);
+                    quantise<kGroupLanes>(kx, kc, &kw);
+                    quantise<kGroupLanes>(vx, vc, &vw);
                     if (tok0 + r >= many) continue;
                     const size_t row = row4(p.cache, t.b, t.kvh, P + tok0 + r);
                     if (row == ~size_t(0)) continue;

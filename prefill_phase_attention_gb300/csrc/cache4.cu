@@ -89,69 +89,77 @@ __device__ __forceinline__ void locate_tokens(const Sequences4& a, const Cache4&
             if (stated_sequence(a, c.max_cache_len, b).n < 0) atomicOr(&a.hdr->error, PA_DEVERR_METADATA);
 }
 
-// Rows of a block: heads [h0, h1) of K then V, 32 tokens each; a thread takes every
-// kStep-th of them, `first` on, and channels [16 part, 16 part + 16).
+// A thread's rows: its token of the block's, heads first, first + kHeadStep, ... below end, and
+// channels [16 part, 16 part + 16).
 template <int D>
 struct Rows {
     static constexpr int kLanes = D / 16;
-    static constexpr int kStep = kCopyThreads / kLanes;
-    static_assert(kStep % kCopyTokens == 0 || kCopyTokens % kStep == 0, "a pass is whole heads or part of one");
-    int part = threadIdx.x % kLanes, first = threadIdx.x / kLanes, h0, items;
-    __device__ __forceinline__ Rows(int n_kv_heads, int heads, int heads_at) {
-        h0 = heads_at * heads;
-        items = (min(2 * n_kv_heads, h0 + heads) - h0) * kCopyTokens;
+    static constexpr int kHeadStep = kCopyThreads / kLanes / kCopyTokens;
+    static_assert(kHeadStep >= 1 && kCopyThreads % (kLanes * kCopyTokens) == 0, "a pass is whole heads");
+    int part = threadIdx.x % kLanes, token = threadIdx.x / kLanes % kCopyTokens, first, end;
+    __device__ __forceinline__ Rows(int n_kv_heads, int heads, int slice) {
+        first = slice * heads + threadIdx.x / (kLanes * kCopyTokens);
+        end = min(n_kv_heads, (slice + 1) * heads);
     }
-    __device__ __forceinline__ int token(int it) const { return it % kCopyTokens; }
-    __device__ __forceinline__ int head(int it) const { return h0 + it / kCopyTokens; }
 };
 
-// Tokens [32 tokens_at, ...) and heads [heads_at * p.heads, ...) of k and v into the cache.
-template <int D>
-__device__ __forceinline__ void write_rows4(const Copy4Params& p, Places& at, int tokens_at, int heads_at) {
-    const int Hk = p.cache.n_kv_heads, groups = p.cache.groups, group_lanes = D / 16 / groups;
-    const size_t stride = p.cache.block_table ? (size_t)1 << p.cache.block_log2 : (size_t)p.cache.max_cache_len;
-    const int t0 = tokens_at * kCopyTokens;
-    const Rows<D> r(Hk, p.heads, heads_at);
-    constexpr int kStep = Rows<D>::kStep;
+// Rows of the cache from one KV head to the next.
+__device__ __forceinline__ size_t head_stride(const Cache4& c) {
+    return c.block_table ? (size_t)1 << c.block_log2 : (size_t)c.max_cache_len;
+}
+
+// Tokens [32 tokens_at, ...) of a slice of the heads of k, or of v (the slices after those), into the
+// cache.
+template <int D, int kGroups>
+__device__ __forceinline__ void write_rows4(const Copy4Params& p, Places& at, int tokens_at, int slice) {
+    constexpr int kGroupLanes = D / 16 / kGroups, kStep = Rows<D>::kHeadStep;
+    const int Hk = p.cache.n_kv_heads, t = tokens_at * kCopyTokens;
+    const int slices = (Hk + p.heads - 1) / p.heads;
+    const bool keys = slice < slices;
+    const Rows<D> r(Hk, p.heads, keys ? slice : slice - slices);
+    const bool there = t + r.token < p.seqs.total_q;
+    const uint4* src = reinterpret_cast<const uint4*>((keys ? p.k : p.v) + ((size_t)(t + r.token) * Hk + r.first) * D) + 2 * r.part;
     uint4 x[kInFlight][2];
-    auto load = [&](int i0) {
+    auto load = [&](int h) {
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
-            const int it = i0 + u * kStep, t = t0 + r.token(it), h = r.head(it);
             x[u][0] = x[u][1] = make_uint4(0, 0, 0, 0);
-            if (it < r.items && t < p.seqs.total_q) {
-                const uint4* src =
-                    reinterpret_cast<const uint4*>((h < Hk ? p.k : p.v) + ((size_t)t * Hk + (h < Hk ? h : h - Hk)) * D) + 2 * r.part;
-                x[u][0] = __ldg(src);
-                x[u][1] = __ldg(src + 1);
+            if (there && h + u * kStep < r.end) {
+                x[u][0] = __ldg(src + u * kStep * (D / 8));
+                x[u][1] = __ldg(src + u * kStep * (D / 8) + 1);
             }
         }
+        src += kInFlight * kStep * (D / 8);
     };
     load(r.first);  // in flight while the tokens are located
-    locate_tokens(p.seqs, p.cache, t0, at, tokens_at == 0 && heads_at == 0);
-    // (whole warps go round: items and the steps are multiples of a warp's rows)
-    for (int i0 = r.first; i0 < r.items; i0 += kInFlight * kStep) {
-        if (i0 != r.first) load(i0);
+    locate_tokens(p.seqs, p.cache, t, at, tokens_at == 0 && slice == 0);
+    const size_t row = at.rows[r.token], stride = head_stride(p.cache) * kStep;
+    const bool wanted = row != ~size_t(0);
+    const size_t row0 = wanted ? row + r.first * head_stride(p.cache) : 0;
+    uint2* codes_at = reinterpret_cast<uint2*>((keys ? p.cache.k : p.cache.v) + row0 * (D / 2)) + r.part;
+    uint32_t* params_at = (keys ? p.cache.kp : p.cache.vp) + row0 * kGroups + r.part / kGroupLanes;
+    // (whole warps go round: a warp's rows are of one head)
+    for (int h = r.first; h < r.end; h += kInFlight * kStep) {
+        if (h != r.first) load(h);
 #pragma unroll
         for (int u = 0; u < kInFlight; ++u) {
-            const int it = i0 + u * kStep, h = r.head(it);
             uint32_t codes[2], word;
-            quantise(x[u], group_lanes, codes, &word);
-            if (it >= r.items) continue;
-            size_t row = at.rows[r.token(it)];
-            if (row == ~size_t(0)) continue;
-            row += (h < Hk ? h : h - Hk) * stride;
-            reinterpret_cast<uint2*>((h < Hk ? p.cache.k : p.cache.v) + row * (D / 2))[r.part] = make_uint2(codes[0], codes[1]);
-            if (r.part % group_lanes == 0) (h < Hk ? p.cache.kp : p.cache.vp)[row * groups + r.part / group_lanes] = word;
+            quantise<kGroupLanes>(x[u], codes, &word);
+            if (wanted && h + u * kStep < r.end) {
+                *codes_at = make_uint2(codes[0], codes[1]);
+                if (r.part % kGroupLanes == 0) *params_at = word;
+            }
+            codes_at += stride * (D / 16);
+            params_at += stride * kGroups;
         }
     }
 }
 
-template <int D>
-__global__ void __launch_bounds__(kCopyThreads) write_cache4_kernel(const Copy4Params p) {
+template <int D, int kGroups>
+__global__ void __launch_bounds__(kCopyThreads, 4) write_cache4_kernel(const Copy4Params p) {
     __shared__ Places at;
     griddep_wait();
-    write_rows4<D>(p, at, blockIdx.x, blockIdx.y);
+    write_rows4<D, kGroups>(p, at, blockIdx.x, blockIdx.y);
 }
 
 // The values of 16 channels: a code as the low bits of 2^23; the product with s is exact, the sum
@@ -173,43 +181,54 @@ __device__ __forceinline__ void expand16(const uint2& codes, uint32_t word, uint
     }
 }
 
-template <int D>
+// 32 bytes, as one store where the tensor's alignment allows: of two stores each would fill half of
+// every 32-byte sector that a warp touches.
+__device__ __forceinline__ void store32(uint4* to, const uint4 (&x)[2], bool aligned) {
+    if (aligned)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(x[0].x), "r"(x[0].y),
+                     "r"(x[0].z), "r"(x[0].w), "r"(x[1].x), "r"(x[1].y), "r"(x[1].z), "r"(x[1].w)
+                     : "memory");
+    else
+        to[0] = x[0], to[1] = x[1];
+}
+
+template <int D, int kGroups>
 __global__ void __launch_bounds__(kCopyThreads) read_cache4_kernel(const Copy4Params p) {
+    constexpr int kGroupLanes = D / 16 / kGroups, kStep = Rows<D>::kHeadStep;
     __shared__ Places at;
-    const int Hk = p.cache.n_kv_heads, groups = p.cache.groups, group_lanes = D / 16 / groups;
-    const size_t stride = p.cache.block_table ? (size_t)1 << p.cache.block_log2 : (size_t)p.cache.max_cache_len;
-    const int t0 = blockIdx.x * kCopyTokens;
+    const int Hk = p.cache.n_kv_heads, t = blockIdx.x * kCopyTokens;
     const Rows<D> r(Hk, p.heads, blockIdx.y);
-    constexpr int kStep = Rows<D>::kStep;
     griddep_wait();
-    locate_tokens(p.seqs, p.cache, t0, at, blockIdx.x == 0 && blockIdx.y == 0);
-    for (int i0 = r.first; i0 < r.items; i0 += kInFlight * kStep) {
-        uint2 codes[kInFlight];
-        uint32_t word[kInFlight];
-        bool there[kInFlight];
+    locate_tokens(p.seqs, p.cache, t, at, blockIdx.x == 0 && blockIdx.y == 0);
+    if (at.rows[r.token] == ~size_t(0)) return;
+    const size_t row0 = at.rows[r.token] + r.first * head_stride(p.cache), stride = head_stride(p.cache) * kStep;
+    const size_t to = ((size_t)(t + r.token) * Hk + r.first) * (D / 8) + 2 * r.part;
+#pragma unroll 1
+    for (int v = 0; v < 2; ++v) {  // K, then V: finding the tokens takes a block as long as either
+        const uint2* codes_at = reinterpret_cast<const uint2*>((v ? p.cache.v : p.cache.k) + row0 * (D / 2)) + r.part;
+        const uint32_t* params_at = (v ? p.cache.vp : p.cache.kp) + row0 * kGroups + r.part / kGroupLanes;
+        uint4* dst = reinterpret_cast<uint4*>(v ? p.v_out : p.k_out) + to;
+        for (int h = r.first; h < r.end; h += kInFlight * kStep) {
+            uint2 codes[kInFlight];
+            uint32_t word[kInFlight];
 #pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            const int it = i0 + u * kStep, h = r.head(it);
-            size_t row = it < r.items ? at.rows[r.token(it)] : ~size_t(0);
-            there[u] = row != ~size_t(0);
-            codes[u] = make_uint2(0, 0);
-            word[u] = 0;
-            if (there[u]) {
-                row += (h < Hk ? h : h - Hk) * stride;
-                codes[u] = __ldg(reinterpret_cast<const uint2*>((h < Hk ? p.cache.k : p.cache.v) + row * (D / 2)) + r.part);
-                word[u] = __ldg((h < Hk ? p.cache.kp : p.cache.vp) + row * groups + r.part / group_lanes);
+            for (int u = 0; u < kInFlight; ++u) {
+                codes[u] = make_uint2(0, 0);
+                word[u] = 0;
+                if (h + u * kStep < r.end) {
+                    codes[u] = __ldg(codes_at);
+                    word[u] = __ldg(params_at);
+                }
+                codes_at += stride * (D / 16);
+                params_at += stride * kGroups;
             }
-        }
 #pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            if (!there[u]) continue;
-            const int it = i0 + u * kStep, h = r.head(it);
-            uint4* dst = reinterpret_cast<uint4*>((h < Hk ? p.k_out : p.v_out) +
-                                                  ((size_t)(t0 + r.token(it)) * Hk + (h < Hk ? h : h - Hk)) * D) + 2 * r.part;
-            uint4 out[2];
-            expand16(codes[u], word[u], out);
-            dst[0] = out[0];
-            dst[1] = out[1];
+            for (int u = 0; u < kInFlight; ++u) {
+                uint4 out[2];
+                expand16(codes[u], word[u], out);
+                if (h + u * kStep < r.end) store32(dst, out, p.aligned32);
+                dst += kStep * (D / 8);
+            }
         }
     }
 }
@@ -237,19 +256,20 @@ __global__ void __launch_bounds__(128) check_sequences4_kernel(const Sequences4 
 
 // The first p.expanders blocks take 128 rows (a block of the pool, one head of K or V) at a time;
 // the others write the call's new tokens into the cache, which nothing else of the call reads.
-template <int D>
-__global__ void __launch_bounds__(kCopyThreads) expand4_kernel(const Expand4Params p) {
+template <int D, int kGroups>
+__global__ void __launch_bounds__(kCopyThreads, 4) expand4_kernel(const Expand4Params p) {
     __shared__ Places places;
     griddep_wait();
     if ((int)blockIdx.x >= p.expanders) {
         const int x = blockIdx.x - p.expanders;
-        write_rows4<D>(p.write, places, x % p.write_blocks, x / p.write_blocks);
+        write_rows4<D, kGroups>(p.write, places, x % p.write_blocks, x / p.write_blocks);
         return;
     }
     constexpr int kLanes = D / 16, kStep = kCopyThreads / kLanes;
     constexpr int kPasses = kBlock4 / kStep > 0 ? kBlock4 / kStep : 1;
     const Cache4& c = p.cache;
-    const int Hk = c.n_kv_heads, group_lanes = kLanes / c.groups;
+    constexpr int kGroupLanes = kLanes / kGroups;
+    const int Hk = c.n_kv_heads;
     const int part = threadIdx.x % kLanes, first = threadIdx.x / kLanes;
     const long long units = 2ll * Hk * *p.blocks;
     for (long long u = blockIdx.x; u < units; u += p.expanders) {
@@ -267,7 +287,7 @@ __global__ void __launch_bounds__(kCopyThreads) expand4_kernel(const Expand4Para
                 const size_t row = row4(c, owner.x, kvh, pos);
                 if (row == ~size_t(0)) continue;
                 codes[i] = __ldg(reinterpret_cast<const uint2*>((h < Hk ? c.k : c.v) + row * (D / 2)) + part);
-                word[i] = __ldg((h < Hk ? c.kp : c.vp) + row * c.groups + part / group_lanes);
+                word[i] = __ldg((h < Hk ? c.kp : c.vp) + row * kGroups + part / kGroupLanes);
             }
         }
         // row of the pool: its blocks' (a paged cache), or its one sequence's (contiguous)
@@ -281,8 +301,7 @@ __global__ void __launch_bounds__(kCopyThreads) expand4_kernel(const Expand4Para
             uint4 out[2];
             expand16(codes[i], word[i], out);
             uint4* dst = reinterpret_cast<uint4*>(pool + (size_t)r * D) + 2 * part;
-            dst[0] = out[0];
-            dst[1] = out[1];
+            store32(dst, out, true);  // (the pool is the workspace's)
         }
     }
 }
@@ -309,51 +328,52 @@ cudaError_t launch_check_sequences4(const Sequences4& a, const Cache4& c, bool w
 
 namespace {
 
-// Heads of a block: enough blocks for the GPU first, then up to kMostRows channels of rows to a
-// block, so that finding its tokens is little of its time.
-constexpr long long kMostRows = 65536;
-int heads_of_block(long long blocks, long long heads, int head_dim, int sms) {
-    return (int)std::max(1ll, std::min(kMostRows / head_dim / kCopyTokens, blocks * heads / (8ll * sms)));
+// Heads of a block: enough blocks for the GPU first, then up to kMostChannels of a token to a block,
+// so that finding its tokens is little of its time.
+constexpr long long kMostChannels = 2048;
+
+// kinds: 2 where K and V have blocks of their own.
+int heads_of_block(long long blocks, int n_kv_heads, int head_dim, int kinds, int sms) {
+    const long long wanted = blocks * kinds * n_kv_heads / (8ll * sms);
+    const int most = (int)std::max(1ll, std::min({wanted, kMostChannels / head_dim, (long long)n_kv_heads}));
+    const int slices = (n_kv_heads + most - 1) / most;
+    return (n_kv_heads + slices - 1) / slices;
 }
 
 template <class Kernel>
-cudaError_t launch_copy(Kernel kernel, Copy4Params p, int head_dim, int sms, cudaStream_t stream) {
+cudaError_t launch_copy(Kernel kernel, Copy4Params p, int head_dim, int kinds, int sms, cudaStream_t stream) {
     const long long blocks = ((long long)p.seqs.total_q + kCopyTokens - 1) / kCopyTokens;
-    const long long heads = 2ll * p.cache.n_kv_heads;
-    p.heads = heads_of_block(blocks, heads, head_dim, sms);
-    return launch_after(kernel, dim3((unsigned)blocks, (unsigned)((heads + p.heads - 1) / p.heads)), kCopyThreads, stream, p);
+    p.heads = heads_of_block(blocks, p.cache.n_kv_heads, head_dim, kinds, sms);
+    const int slices = kinds * ((p.cache.n_kv_heads + p.heads - 1) / p.heads);
+    return launch_after(kernel, dim3((unsigned)blocks, (unsigned)slices), kCopyThreads, stream, p);
 }
+
+// f<head_dim, groups of a row>
+#define PA_CACHE4_VARIANT(head_dim, groups, f)                    \
+    head_dim == 32                    ? f<32, 1>                  \
+    : head_dim == 64                  ? groups == 1 ? f<64, 1> : f<64, 2> \
+    : groups == 1                     ? f<128, 1>                 \
+    : groups == 2                     ? f<128, 2>                 \
+                                      : f<128, 4>
 
 }  // namespace
 
 cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream) {
-    switch (head_dim) {
-        case 32: return launch_copy(write_cache4_kernel<32>, p, 32, sms, stream);
-        case 64: return launch_copy(write_cache4_kernel<64>, p, 64, sms, stream);
-        default: return launch_copy(write_cache4_kernel<128>, p, 128, sms, stream);
-    }
+    return launch_copy(PA_CACHE4_VARIANT(head_dim, p.cache.groups, write_cache4_kernel), p, head_dim, 2, sms, stream);
 }
 
 cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream) {
-    switch (head_dim) {
-        case 32: return launch_copy(read_cache4_kernel<32>, p, 32, sms, stream);
-        case 64: return launch_copy(read_cache4_kernel<64>, p, 64, sms, stream);
-        default: return launch_copy(read_cache4_kernel<128>, p, 128, sms, stream);
-    }
+    return launch_copy(PA_CACHE4_VARIANT(head_dim, p.cache.groups, read_cache4_kernel), p, head_dim, 1, sms, stream);
 }
 
 cudaError_t launch_expand4(Expand4Params p, int head_dim, int sms, cudaStream_t stream) {
     const long long blocks = ((long long)p.write.seqs.total_q + kCopyTokens - 1) / kCopyTokens;
-    const long long heads = 2ll * p.cache.n_kv_heads;
-    p.write.heads = heads_of_block(blocks, heads, head_dim, sms);
+    const int Hk = p.cache.n_kv_heads;
+    p.write.heads = heads_of_block(blocks, Hk, head_dim, 2, sms);
     p.write_blocks = (int)blocks;
-    p.expanders = (int)std::min((long long)sms * 4, heads * p.pool_blocks);
-    const dim3 grid((unsigned)(p.expanders + blocks * ((heads + p.write.heads - 1) / p.write.heads)));
-    switch (head_dim) {
-        case 32: return launch_after(expand4_kernel<32>, grid, kCopyThreads, stream, p);
-        case 64: return launch_after(expand4_kernel<64>, grid, kCopyThreads, stream, p);
-        default: return launch_after(expand4_kernel<128>, grid, kCopyThreads, stream, p);
-    }
+    p.expanders = (int)std::min((long long)sms * 4, 2ll * Hk * p.pool_blocks);
+    const dim3 grid((unsigned)(p.expanders + blocks * 2 * ((Hk + p.write.heads - 1) / p.write.heads)));
+    return launch_after(PA_CACHE4_VARIANT(head_dim, p.cache.groups, expand4_kernel), grid, kCopyThreads, stream, p);
 }
 
 }  // namespace pa

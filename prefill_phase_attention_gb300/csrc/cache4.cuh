@@ -83,10 +83,10 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // Quantises 8 kWords channels (bf16 pairs x) of a row whose groups are spread over
-// `lanes` consecutive lanes each: codes[w] holds those of channels 8 w ..., *params the
+// kLanes consecutive lanes each: codes[w] holds those of channels 8 w ..., *params the
 // group's word (the same in its lanes).  All lanes of the warp.
-template <int kWords>
-__device__ __forceinline__ void quantise(const uint4 (&x)[kWords], int lanes, uint32_t (&codes)[kWords], uint32_t* params) {
+template <int kLanes, int kWords>
+__device__ __forceinline__ void quantise(const uint4 (&x)[kWords], uint32_t (&codes)[kWords], uint32_t* params) {
     uint32_t lo2 = x[0].x, hi2 = x[0].x;
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
@@ -97,7 +97,8 @@ __device__ __forceinline__ void quantise(const uint4 (&x)[kWords], int lanes, ui
     // (minimum, -maximum) of the lane, of the group
     hi2 ^= 0x80008000u;
     uint32_t ends = min_bf16x2(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
-    for (int o = 1; o < lanes; o <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) ends = min_bf16x2(ends, __shfl_xor_sync(0xffffffffu, ends, o));
     const float lo = __fadd_rn(bf16_lo(ends), 0.f), hi = -bf16_hi(ends);  // (a minimum of -0 is stored as 0)
     __nv_bfloat16 s = __float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), 1.0f / 15.0f));
     const bool normal = __bfloat162float(s) >= 0x1p-126f;

@@ -196,7 +196,8 @@ struct Copy4Params {
     const __nv_bfloat16* v;
     __nv_bfloat16* k_out;
     __nv_bfloat16* v_out;
-    int heads;  // of K and V that a block takes (set by the launch)
+    bool aligned32;  // k_out and v_out are 32-byte aligned
+    int heads;       // of K and V that a block takes (set by the launch)
 };
 cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
 cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
