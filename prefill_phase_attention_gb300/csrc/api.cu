@@ -1413,6 +1413,8 @@ pa_status read_cache4(const pa_cache4* cache, const Options& o, int head_dim, in
             if (!aligned16(ptrs[i])) return fail(PA_ERR_INVALID_ARG, "pa_cache4.%s must be 16-byte aligned", names[i]);
         }
     }
+    if (o.block_table && (long long)o.num_blocks * n_kv_heads * o.block_size >= (1LL << 32))
+        return fail(PA_ERR_UNSUPPORTED, "num_blocks * n_kv_heads * block_size must be < 2^32");
     out->k = static_cast<uint8_t*>(cache->k);
     out->v = static_cast<uint8_t*>(cache->v);
     out->kp = static_cast<uint32_t*>(cache->k_params);

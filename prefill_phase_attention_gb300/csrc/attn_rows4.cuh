@@ -97,7 +97,7 @@ enum : int {
 
 struct Record {
     Item t;
-    int valid;
+    int valid;  // 0: none; 1: kept in global memory; 2: in the ring
 };
 
 // Tiles of the list that a sequence's row blocks have.
@@ -292,7 +292,7 @@ struct Feeder {
     int whole_until;  // tiles below are whole and have no edge
     unsigned row;     // contiguous cache: row of the next cached tile
     int flags;        // of the next tile: its item's slot, kFirst and kFromBefore
-    int ids, next_ids;  // paged: blocks of the 8-row pieces of this and the next 256 positions
+    unsigned rows, next_rows;  // paged: the pool's row of the lane's 8-row piece of this and the next 256 positions
 
     __device__ __forceinline__ SeqInfo seq(int i) const {
         return table ? table[i] : sequence_of(p, i);
@@ -337,33 +337,33 @@ struct Feeder {
         if (lane == 0)
             items[slot] = Item{w.s, w.b, w.kvh, w.block, w.e.tiles(), (int)(w.block_start >> 32), (int)w.block_start};
         if (p.cache.block_table) {
-            ids = id_of(w.b, w.s.P, key >> 8);
-            next_ids = id_of(w.b, w.s.P, (key >> 8) + 1);
+            rows = piece(w.b, w.kvh, w.s.P, key >> 8);
+            next_rows = piece(w.b, w.kvh, w.s.P, (key >> 8) + 1);
         } else {
             row = (unsigned)((w.b * p.cache.n_kv_heads + w.kvh) * p.cache.max_cache_len + key);  // < 2^31
         }
         whole_until = key < w.lo_most ? 0 : w.s.P / kTileKeys * kTileKeys;
     }
-    // The block of the lane's 8-row piece (of a checked table: the bounds keep a stray entry
-    // from becoming a stray read).
-    __device__ __forceinline__ int id_of(int b, int P, int window) const {
+    // The pool's row of the lane's 8-row piece.  (The bounds keep an entry that names no block of the
+    // pool, which the CTA's check of the tables finds meanwhile, from becoming a stray read; a
+    // pool has less than 2^32 rows.)
+    __device__ __forceinline__ unsigned piece(int b, int kvh, int P, int window) const {
         const int pos = window * 256 + lane * 8;
         if (pos >= P) return 0;
         const int id = __ldg(p.cache.block_table + (size_t)b * p.cache.max_blocks + (pos >> p.cache.block_log2));
-        return (int)min((unsigned)id, (unsigned)p.cache.num_blocks - 1);
+        const unsigned block = min((unsigned)id, (unsigned)p.cache.num_blocks - 1);
+        return ((block * p.cache.n_kv_heads + kvh) << p.cache.block_log2) + (pos & ((1 << p.cache.block_log2) - 1));
     }
     // paged: the pool's row of the tile's row r
-    __device__ __forceinline__ size_t pool_row(int kvh, int r) const {
-        const int id = __shfl_sync(0xffffffffu, ids, ((key & 255) >> 3) + (r >> 3));
-        return ((size_t)(unsigned)(id * p.cache.n_kv_heads + kvh) << p.cache.block_log2) +
-               ((key + r) & ((1 << p.cache.block_log2) - 1));
+    __device__ __forceinline__ unsigned pool_row(int r) const {
+        return __shfl_sync(0xffffffffu, rows, ((key & 255) >> 3) + (r >> 3)) + (r & 7);
     }
-    __device__ __forceinline__ void advance(int b, int P) {
+    __device__ __forceinline__ void advance() {
         key += kTileKeys;
         row += kTileKeys;
         if (p.cache.block_table && (key & 255) == 0) {
-            ids = next_ids;
-            next_ids = id_of(b, P, (key >> 8) + 1);
+            rows = next_rows;
+            next_rows = piece(walk->b, walk->kvh, walk->s.P, (key >> 8) + 1);
         }
     }
     __device__ __forceinline__ void issue(int stage) {
@@ -397,16 +397,14 @@ struct Feeder {
                 cp_async_small<NG * 4>(par, p.cache.kp + at);
                 cp_async_small<NG * 4>(par + C::kParams, p.cache.vp + at);
             }
-            advance(0, 0);
         } else {
-            const int kvh = walk->kvh;
 #pragma unroll
             for (int it = 0; it < kParts; ++it) {
-                const size_t from = pool_row(kvh, it * kPassRows + lane / kParts) * C::kRowBytes + lane % kParts * 16;
+                const size_t from = (size_t)pool_row(it * kPassRows + lane / kParts) * C::kRowBytes + lane % kParts * 16;
                 cp_async16(dst + it * 512, p.cache.k + from);
                 cp_async16(dst + C::kCodes + it * 512, p.cache.v + from);
             }
-            const size_t at = pool_row(kvh, lane) * NG;
+            const size_t at = (size_t)pool_row(lane) * NG;
             if constexpr (NG == 4) {
                 cp_async16(par, p.cache.kp + at);
                 cp_async16(par + C::kParams, p.cache.vp + at);
@@ -414,8 +412,8 @@ struct Feeder {
                 cp_async_small<NG * 4>(par, p.cache.kp + at);
                 cp_async_small<NG * 4>(par + C::kParams, p.cache.vp + at);
             }
-            advance(walk->b, walk->s.P);
         }
+        advance();
     }
     // A cached tile at an edge, with zeros past the sequence's cached rows, or new tokens.
     __device__ __forceinline__ void issue_any(int stage) {
@@ -428,13 +426,13 @@ struct Feeder {
             for (int it = 0; it < kParts; ++it) {
                 const int r = it * kPassRows + lane / kParts;
                 const bool read = key + r < w.s.P;
-                const size_t from_row = p.cache.block_table ? pool_row(w.kvh, r) : row + r;
+                const size_t from_row = p.cache.block_table ? pool_row(r) : row + r;
                 const size_t from = (read ? from_row : 0) * C::kRowBytes + lane % kParts * 16;
                 cp_async16(dst + it * 512, p.cache.k + from, read);
                 cp_async16(dst + C::kCodes + it * 512, p.cache.v + from, read);
             }
             const bool read = key + lane < w.s.P;
-            const size_t from_row = p.cache.block_table ? pool_row(w.kvh, lane) : row + lane;
+            const size_t from_row = p.cache.block_table ? pool_row(lane) : row + lane;
             const size_t from = (read ? from_row : 0) * NG;
             if constexpr (NG == 4) {
                 cp_async16(par, p.cache.kp + from, read);
@@ -443,7 +441,7 @@ struct Feeder {
                 cp_async_small<NG * 4>(par, p.cache.kp + from, read);
                 cp_async_small<NG * 4>(par + C::kParams, p.cache.vp + from, read);
             }
-            advance(w.b, w.s.P);
+            advance();
             if (key >= w.lo_most) whole_until = w.s.P / kTileKeys * kTileKeys;
         } else {
             const uint32_t base = params + stage * C::kTileBytes - lane * NG * 4 - 2 * C::kCodes;
@@ -579,7 +577,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
 
     // ---- this warp's share
     uint8_t* const ring = smem + warp * C::kStages * C::kTileBytes;
-    // a warp's first record: in global memory, its second one: in its ring
+    // a warp's first record, where its share goes on after it (at the end the ring has room)
     float* const kept = p.kept + ((size_t)blockIdx.x * kWarps + warp) * kRows * D;
     const long long len = to - from;
     const long long wfrom = from + len * warp / kWarps, wto = from + len * (warp + 1) / kWarps;
@@ -969,8 +967,9 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
         if (flags & kLast) {
             const bool whole = !(flags & (kFromBefore | kGoesOn));
             const int slot = flags & kFromBefore ? 0 : 1;
-            // the second record is written when the ring is done with: its copies have landed
-            float* const rec = slot == 0 ? kept : reinterpret_cast<float*>(ring);
+            // where the share ends the ring is done with: its copies have landed
+            const bool at_end = i + 1 >= feed.count;
+            float* const rec = !at_end ? kept : reinterpret_cast<float*>(ring) + (slot == 0 ? kRows * D : 0);
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -1012,7 +1011,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
             if (!whole && lane == 0) {
                 Record r;
                 r.t = t;
-                r.valid = 1;
+                r.valid = at_end ? 2 : 1;
                 records[warp][slot] = r;
             }
         }
@@ -1021,7 +1020,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     cp_async_wait<0>();
     constexpr int kElems = kRows * D;
     __syncwarp();
-    if (records[warp][0].valid) {
+    if (records[warp][0].valid == 1) {
         // the first record joins the second one in the ring
         float4* const to = reinterpret_cast<float4*>(ring) + kElems / 4;
 #pragma unroll
