@@ -51,10 +51,11 @@ namespace rows4 {
 constexpr int kTileKeys = 32;  // cached rows of a tile
 constexpr int kNewKeys = 8;    // new tokens of a tile
 constexpr int kRows = 8;       // query rows of a row block: the columns of an MMA
-// Beginning and ending a row block costs a warp about as much as two tiles, so the list has
+// Beginning and ending a row block costs a warp as much as several tiles, so the list has
 // as many places ahead of a row block's tiles that hold none: equal shares of places are equal
-// shares of time.
-constexpr int kBlockCost = 2;
+// shares of time.  (64 decode rows of 256 to 4096 tokens over pages, us, with 1 / 2 / 3 / 4 / 6
+// places: 62 / 62 / 60 / 58 / 58.)
+constexpr int kBlockCost = 4;
 
 template <int D, int NG>
 struct Cfg {
