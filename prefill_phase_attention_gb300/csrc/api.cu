@@ -1620,15 +1620,15 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     // The row kernel's CTAs check metadata and tables themselves; a kernel ahead does for the
     // rotary prologue, and for more sequences than a CTA keeps at hand.
     const bool check = !tiles && (o.rope_theta > 0.f || (o.block_table && num_seqs > pa::kRows4Seqs));
-    // the pool of expanded blocks
-    const long long seq_blocks = ((long long)max_cache_len + pa::kBlock4 - 1) / pa::kBlock4;
-    const size_t block_bytes = (size_t)n_kv_heads * pa::kBlock4 * head_dim * 2;  // of K or V
+    // the pool of expanded blocks (a sequence has up to one more than its positions: see FwdParamsTwo)
+    const long long seq_blocks = ((long long)max_cache_len + pa::kBlock4 - 1) / pa::kBlock4 + 1;
+    const size_t block_bytes = (size_t)n_kv_heads * pa::kBlock4 * head_dim * 2;  // of a term of K, or of V
     long long pool_blocks = 0;
     if (tiles) {
         const long long most = std::min<long long>(num_seqs, total_q / (few + 1)) * seq_blocks;
-        pool_blocks = std::max(seq_blocks, std::min(most, kPoolBytes / (long long)(2 * block_bytes)));
-        if (pool_blocks * n_kv_heads >= (1LL << 31) || num_seqs * seq_blocks >= (1LL << 31))
-            return fail(PA_ERR_UNSUPPORTED, "max_cache_len * n_kv_heads or num_seqs * max_cache_len is too large for a long chunk");
+        pool_blocks = std::max(seq_blocks, std::min(most, kPoolBytes / (long long)(3 * block_bytes)));
+        if (pool_blocks * pa::kBlock4 * n_kv_heads >= (1LL << 31))
+            return fail(PA_ERR_UNSUPPORTED, "max_cache_len * n_kv_heads is too large for a long chunk");
     }
     const StreamLock lock(dev, stream);
     Workspace* const ws = lock.ws;
@@ -1640,13 +1640,12 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     const size_t part_bytes = align_up((size_t)grid * 2 * 8 * (head_dim + 2) * sizeof(float), 256);
     const size_t kept_bytes = align_up((size_t)grid * pa::kRows4Warps * 8 * head_dim * sizeof(float), 256);
     const size_t seq_bytes = tiles ? align_up((size_t)num_seqs * sizeof(pa::SeqInfo), 256) : 0;
-    const size_t taken_bytes = tiles ? align_up(((size_t)num_seqs + 1) * sizeof(int), 256) : 0;
-    const size_t table_bytes = tiles ? align_up((size_t)num_seqs * seq_blocks * sizeof(int), 256) : 0;
+    const size_t taken_bytes = tiles ? align_up((2 * (size_t)num_seqs + 1) * sizeof(int), 256) : 0;
     const size_t owner_bytes = align_up((size_t)pool_blocks * sizeof(int2), 256);
     const size_t pool_bytes = align_up((size_t)pool_blocks * block_bytes, 256);
     void* aux = nullptr;
-    s = get_aux_scratch(ws, stream, part_bytes + kept_bytes + seq_bytes + taken_bytes + table_bytes + owner_bytes +
-                                        2 * pool_bytes, &aux);
+    s = get_aux_scratch(ws, stream, part_bytes + kept_bytes + seq_bytes + taken_bytes + owner_bytes + 3 * pool_bytes,
+                        &aux);
     if (s != PA_OK) return s;
     char* at = static_cast<char*>(aux);
     auto take = [&](size_t bytes) { char* const x = at; at += bytes; return x; };
@@ -1663,8 +1662,6 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     p.taken = nullptr;
     int launches = 0;
     pa::Expand4Params x;
-    Options po;
-    const int pool_len = (int)std::min<long long>(seq_blocks * pa::kBlock4, kMaxTokens);
     const int tile_grid = (int)std::min<long long>(sms, units);
     if (tiles) {
         p.seqs.checked = reinterpret_cast<pa::SeqInfo*>(take(seq_bytes));
@@ -1673,22 +1670,19 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         x.few_tokens = few;
         x.window = causal ? o.window : 0;
         x.pool_blocks = (int)pool_blocks;
-        x.table_blocks = (int)seq_blocks;
         x.taken = reinterpret_cast<int*>(take(taken_bytes));
-        x.blocks = x.taken + num_seqs;
-        x.table = one ? nullptr : reinterpret_cast<int32_t*>(take(table_bytes));
+        x.base = x.taken + num_seqs;
+        x.blocks = x.base + num_seqs;
         x.owners = reinterpret_cast<int2*>(take(owner_bytes));
         x.k = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
+        x.k2 = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
         x.v = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
         p.taken = x.taken;
-        po = o;  // the pool, as a bf16 cache
-        po.block_table = x.table;
-        po.block_size = one ? 0 : pa::kBlock4;
-        po.max_blocks = one ? 0 : (int)seq_blocks;
-        po.num_blocks = one ? 0 : (int)pool_blocks;
+        Options contiguous = o;  // (the pool is; the plan checks the cache's own table)
+        contiguous.block_table = nullptr;
         pa::ScheduleArgs sa;
-        fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, pool_len, n_heads, n_kv_heads,
-                      head_dim, causal, po, scr, sched, tile_grid);
+        fill_schedule(sa, cu_seqlens_q, cu_seqlens_k, cache_offsets, num_seqs, total_q, max_cache_len, n_heads, n_kv_heads,
+                      head_dim, causal, contiguous, scr, sched, tile_grid);
         sa.taken = x.taken;
         e = pa::launch_build_schedule4(sa, x, stream);
         if (e != cudaSuccess) return cuda_fail(e, "schedule launch");
@@ -1713,11 +1707,18 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         x.write.aligned32 = false;
         e = pa::launch_expand4(x, head_dim, sms, stream);
         if (e != cudaSuccess) return cuda_fail(e, "expansion launch");
-        pa::FwdParams fp;
-        fill_fwd(fp, k, v, x.k, x.v, out, lse, scr, pool_len, n_heads, n_kv_heads, scale, causal, po, sched);
-        e = pa::encode_fwd_maps(fp, q, total_q, num_seqs, head_dim, po.num_blocks);
+        Options contiguous = o;
+        contiguous.block_table = nullptr;
+        pa::FwdParamsTwo fp;
+        fill_fwd(fp, k, v, x.k, x.v, out, lse, scr, max_cache_len, n_heads, n_kv_heads, scale, causal, contiguous, sched);
+        fp.base = x.base;
+        // (the maps of q, k and v; those of the cache are replaced by the pool's)
+        e = pa::encode_fwd_maps(fp, q, total_q, 1, head_dim, 0);
+        if (e == cudaSuccess) e = pa::encode_pool_maps(fp, head_dim, x.k, x.k2, x.v, pool_blocks * pa::kBlock4);
         if (e != cudaSuccess) return cuda_fail(e, "tensor map encoding");
-        e = pa::launch_attn_fwd(fp, head_dim, tile_grid, stream);
+        e = head_dim == 32   ? pa::launch_attn_two_d<32>(fp, tile_grid, stream)
+            : head_dim == 64 ? pa::launch_attn_two_d<64>(fp, tile_grid, stream)
+                             : pa::launch_attn_two_d<128>(fp, tile_grid, stream);
         if (e != cudaSuccess) return cuda_fail(e, "attention launch");
         launches += 2;
         g_last_schedule = sched;

@@ -58,6 +58,7 @@
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -526,7 +527,7 @@ template <int D, bool kQuant>
 __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, WorkspaceHeader* hdr, uint8_t* ring,
                                           int stages, uint64_t* full, uint64_t* empty, const CUtensorMap* tm_cache,
                                           const CUtensorMap* tm_new, int* last_parity, uint32_t t, int j,
-                                          const Unit& u, const SeqInfo& s, int np, int z) {
+                                          const Unit& u, const SeqInfo& s, int np, int z, int row0 = 0) {
     using C = Cfg<D>;
     const int st = t % stages;
     const uint32_t ph = (t / stages) & 1;
@@ -544,7 +545,7 @@ __device__ __forceinline__ bool load_kv_tile(const FwdParams& p, Ctrl* ctl, Work
     for (int c = 0; c < C::kChunks; ++c) {
         uint8_t* dst = ring + st * C::kTileBytes + c * C::kChunkBytes;
         if (j < np)
-            tma_load_3d(dst, tm_cache, &full[st], c * C::kChunkCols, kb, z);
+            tma_load_3d(dst, tm_cache, &full[st], c * C::kChunkCols, row0 + kb, z);
         else
             tma_load_3d(dst, tm_new, &full[st], c * C::kChunkCols, u.kvh, s.q_start + kb - s.P);
     }
@@ -599,12 +600,17 @@ __device__ __forceinline__ void claim_unit_ext(const FwdParamsX& p, WorkspaceHea
 
 // kExt: the long-context variant (sink tokens, a prefix the batch shares, units
 // whose tiles are split between CTAs).
-template <bool kExt>
-using KernelParams = std::conditional_t<kExt, FwdParamsX, FwdParams>;
+// kTwo: cached keys in two bf16 terms, of the sequences' rows of one pool (FwdParamsTwo).  A
+// cached tile is two entries of the K ring, and S their products' sum; nothing is
+// written to the pool.
+template <bool kExt, bool kTwo>
+using KernelParams = std::conditional_t<kTwo, FwdParamsTwo, std::conditional_t<kExt, FwdParamsX, FwdParams>>;
 
-template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
-__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ KernelParams<kExt> p) {
+template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false, bool kTwo = false>
+__global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ KernelParams<kExt, kTwo> p) {
     using C = Cfg<D>;
+    static_assert(!kTwo || (!kPaged && !kQuant && !kHook && !kExt), "keys in two terms: plain calls only");
+    constexpr int kReleasers = kTwo ? 1 : 2;  // of a ring's stage: MMA commit, cache writer
     static_assert(!(kAlt && kQuant), "the merge exchange shares storage with the int8 scale ring");
     // K stages in use.  With an int8 cache the K writer publishes each tile's row
     // scales in a 4-deep ring (Ctrl::kscale) that the softmax warps read after
@@ -614,7 +620,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     // 3 stages that PV follows every slot's softmax of tile t: the ring slot is
     // free.  (bf16 caches use no scale ring.)  A ring of two (long-context variant at
     // head_dim 128): see its writer.
-    constexpr int kStK = kQuant && C::kStagesK > 3 ? 3 : C::kStagesK;
+    // Keys in two terms at head_dim 128, units whose slots alternate: three of the five tiles that
+    // the rings have, so that one term of the next tile comes while a tile's two are used
+    // (512 tokens over 4096 cached ones, 32/8 heads: with two 95 us, with three 78).  Where both
+    // slots use every tile, V's third one is worth more (4096 over 4096, 32 heads: 474 and 494).
+    constexpr bool kMoreK = kTwo && kAlt && D == 128;
+    constexpr int kRingK = C::kStagesK + (kMoreK ? 1 : 0), kStV = C::kStagesV - (kMoreK ? 1 : 0);
+    constexpr int kStK = kQuant && C::kStagesK > 3 ? 3 : kRingK;
     // paged bf16 cache, two column chunks: prefix tiles staged block by block
     constexpr bool kGrp = kPaged && !kQuant && C::kChunks == 2;
     const int unit_slots = kAlt ? p.unit_slots : kSlots;  // Q tiles of a unit
@@ -622,9 +634,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     // swizzled TMA/UMMA tiles need 1024-byte alignment (reported below)
     const bool misaligned = (smem_u32(smem_raw) & 1023u) != 0;
     uint8_t* q_smem = smem_raw;                              // [kSlots] tiles
-    uint8_t* k_smem = q_smem + kSlots * C::kTileBytes;       // [kStagesK] tiles
-    uint8_t* v_smem = k_smem + C::kStagesK * C::kTileBytes;  // [kStagesV] tiles
-    Ctrl* ctl = reinterpret_cast<Ctrl*>(v_smem + C::kStagesV * C::kTileBytes);
+    uint8_t* k_smem = q_smem + kSlots * C::kTileBytes;       // [kRingK] tiles
+    uint8_t* v_smem = k_smem + kRingK * C::kTileBytes;       // [kStV] tiles
+    Ctrl* ctl = reinterpret_cast<Ctrl*>(v_smem + kStV * C::kTileBytes);
     OwnUnits* own = reinterpret_cast<OwnUnits*>(ctl + 1);  // kExt
     // V's scales go into P (kVScale); slots of tile t in the rings of K's and V's scales
     constexpr bool kVScale = kExt && kQuant;
@@ -650,11 +662,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         mbar_init(&ctl->q_empty, 1);
         for (int s = 0; s < kStK; ++s) {
             mbar_init(&ctl->k_full[s], 1);
-            mbar_init(&ctl->k_empty[s], 2);  // MMA commit + cache writer
+            mbar_init(&ctl->k_empty[s], kReleasers);
         }
-        for (int s = 0; s < C::kStagesV; ++s) {
+        for (int s = 0; s < kStV; ++s) {
             mbar_init(&ctl->v_full[s], 1);
-            mbar_init(&ctl->v_empty[s], 2);
+            mbar_init(&ctl->v_empty[s], kReleasers);
             mbar_init(&ctl->v_fix[s], 1);  // V cache writer
             mbar_init(&ctl->v_conv[s], 1);
         }
@@ -686,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 prefetch_tmap(&p.tm_pv);
             }
         }
+        if constexpr (kTwo) prefetch_tmap(&p.tm_ck2);
     }
     if (!misaligned && warp == 1) {
         tmem_alloc(&ctl->tmem_base, 512);
@@ -765,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const int src = lane & 16;  // the group's leader lane
         const bool gleader = gl == 0;
         uint8_t* ring = is_v ? v_smem : k_smem;
-        const int stages = is_v ? C::kStagesV : kStK;
+        const int stages = is_v ? kStV : kStK;
         uint64_t* full = is_v ? ctl->v_full : ctl->k_full;
         uint64_t* empty = is_v ? ctl->v_empty : ctl->k_empty;
         const CUtensorMap* tm_cache = is_v ? &p.tm_cv : &p.tm_ck;
@@ -987,9 +1000,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 if constexpr (kExt)
                     if (ug.pre) tm_c = &p.tm_pk, z = u.kvh;
                 bool ok = true;
-                for (int j = 0; j < ug.ntiles && ok; ++j, ++t)
-                    ok = load_kv_tile<D, kQuant>(p, ctl, hdr, k_smem, kStK, ctl->k_full, ctl->k_empty, tm_c, &p.tm_k,
-                                                 last_k_parity, t, tile_at(ug, j), u, s, ug.np, z);
+                if constexpr (kTwo) {
+                    const int row0 = p.base[u.b];
+                    for (int j = 0; j < ug.ntiles && ok; ++j, ++t) {
+                        ok = load_kv_tile<D, kQuant>(p, ctl, hdr, k_smem, kStK, ctl->k_full, ctl->k_empty, &p.tm_ck, &p.tm_k,
+                                                     last_k_parity, t, tile_at(ug, j), u, s, ug.np, u.kvh, row0);
+                        if (ok && tile_at(ug, j) < ug.np)
+                            ok = load_kv_tile<D, kQuant>(p, ctl, hdr, k_smem, kStK, ctl->k_full, ctl->k_empty, &p.tm_ck2,
+                                                         &p.tm_k, last_k_parity, ++t, tile_at(ug, j), u, s, ug.np, u.kvh, row0);
+                    }
+                } else {
+                    for (int j = 0; j < ug.ntiles && ok; ++j, ++t)
+                        ok = load_kv_tile<D, kQuant>(p, ctl, hdr, k_smem, kStK, ctl->k_full, ctl->k_empty, tm_c, &p.tm_k,
+                                                     last_k_parity, t, tile_at(ug, j), u, s, ug.np, z);
+                }
                 if (!ok) break;
             }
             if (aborted(ctl)) {
@@ -1013,13 +1037,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 int z = us.u.b * p.n_kv_heads + us.u.kvh;
                 if constexpr (kExt)
                     if (ug.pre) tm_c = &p.tm_pv, z = us.u.kvh;
+                int row0 = 0;
+                if constexpr (kTwo) row0 = p.base[us.u.b], z = us.u.kvh;
                 bool ok = true;
                 for (int j = 0; j < ug.ntiles && ok; ++j, ++t)
-                    ok = load_kv_tile<D, kQuant>(p, ctl, hdr, v_smem, C::kStagesV, ctl->v_full, ctl->v_empty, tm_c,
-                                                 &p.tm_v, last_v_parity, t, tile_at(ug, j), us.u, us.s, ug.np, z);
+                    ok = load_kv_tile<D, kQuant>(p, ctl, hdr, v_smem, kStV, ctl->v_full, ctl->v_empty, tm_c,
+                                                 &p.tm_v, last_v_parity, t, tile_at(ug, j), us.u, us.s, ug.np, z, row0);
                 if (!ok) break;
             }
-            if (aborted(ctl)) drain(ctl->v_full, last_v_parity, C::kStagesV);
+            if (aborted(ctl)) drain(ctl->v_full, last_v_parity, kStV);
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------- MMA issuer
@@ -1038,6 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         const uint64_t k_desc_g = smem_desc(k_addr, 16, C::kGrpSbo, C::kSw);
         const uint64_t v_desc_g = smem_desc(v_addr, C::kSbo, C::kGrpSbo, C::kSw);
         uint32_t t = 0;                // KV tiles of this CTA so far
+        uint32_t tk = 0;               // kTwo: entries of the K ring so far
         uint32_t ns[kSlots] = {0, 0};  // tiles processed per slot so far
         uint32_t no[kSlots] = {0, 0};  // units with the slot active so far
         uint32_t fixpar = 0;           // paged: parity bit per V stage of v_fix
@@ -1074,9 +1101,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             }
             __syncwarp();
         };
+        // kTwo: S of slot i from Q tile qi and `entries` (one or two) of the K ring from e on
+        auto issue_s_two = [&](int i, uint32_t e, int entries, int qi) {
+            if (leader) {
+                for (int h = 0; h < entries; ++h) {
+                    const uint32_t koff = ((e + h) % kStK) * C::kTileBytes, qoff = qi * C::kTileBytes;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = ((kk * 16) / C::kChunkCols) * C::kChunkBytes + ((kk * 16) % C::kChunkCols) * 2;
+                        mma_ss(tmem + i * kColSlot, q_desc + ((qoff + off) >> 4), k_desc + ((koff + off) >> 4), C::kIdescS,
+                               h > 0 || kk > 0 ? 1u : 0u);
+                    }
+                }
+                mma_commit(&ctl->s_full[i]);
+            }
+            __syncwarp();
+        };
         auto issue_pv = [&](int i, uint32_t tt, bool first, bool grp) {
             if (leader) {
-                const uint32_t voff = (tt % C::kStagesV) * C::kTileBytes;
+                const uint32_t voff = (tt % kStV) * C::kTileBytes;
                 // V operand: descriptor template and 16-key step of the tile's staging
                 const bool g = kGrp && grp;
                 const uint64_t vd = g ? v_desc_g : v_desc;
@@ -1105,28 +1148,52 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             const auto ug = geo(std::bool_constant<kAlt>(), u, s, s0);
             auto at = [&](int j) { return tile_at(ug, j); };
             const int ntiles = ug.ntiles;
+            // the K ring's entries of tile j: waits for them, computes S from them, frees them
+            const int cached = kTwo ? max(0, min(ug.np - at(0), ntiles)) : 0;
+            auto entry = [&](int j) -> uint32_t { return tk + (j < cached ? 2 * j : cached + j); };
+            auto wait_tile = [&](int j) -> bool {
+                if constexpr (!kTwo) return wait_k(t + j, at(j), ug.np);
+                const uint32_t e = entry(j);
+                if (!warp_wait(&ctl->k_full[e % kStK], (e / kStK) & 1, ctl, hdr)) return false;
+                return j >= cached || warp_wait(&ctl->k_full[(e + 1) % kStK], ((e + 1) / kStK) & 1, ctl, hdr);
+            };
+            auto issue_tile = [&](int i, int j, int qi) {
+                if constexpr (kTwo)
+                    issue_s_two(i, entry(j), j < cached ? 2 : 1, qi);
+                else
+                    issue_s(i, t + j, qi, at(j) < ug.np);
+            };
+            auto free_tile = [&](int j) {
+                if constexpr (kTwo) {
+                    const uint32_t e = entry(j);
+                    commit(&ctl->k_empty[e % kStK]);
+                    if (j < cached) commit(&ctl->k_empty[(e + 1) % kStK]);
+                } else {
+                    commit(&ctl->k_empty[(t + j) % kStK]);
+                }
+            };
             if (!warp_wait(&ctl->q_full, u_it & 1, ctl, hdr)) break;
             if constexpr (kAlt) if (ug.alt) {
                 // (bf16 cache only) V tile tj, index jt in the sequence, ready for PV
                 auto wait_v = [&](uint32_t tj, int jt) -> bool {
-                    const int vst = tj % C::kStagesV;
+                    const int vst = tj % kStV;
                     if (kPaged && paged_tail_tile(jt, s.P, ug.np)) {
                         const bool got = warp_wait(&ctl->v_fix[vst], (fixpar >> vst) & 1, ctl, hdr);
                         fixpar ^= 1u << vst;
                         return got;
                     }
-                    return warp_wait(&ctl->v_full[vst], (tj / C::kStagesV) & 1, ctl, hdr);
+                    return warp_wait(&ctl->v_full[vst], (tj / kStV) & 1, ctl, hdr);
                 };
                 // slot i takes the tiles j with j % 2 == i, both from Q tile 0:
                 // S_0(0), S_1(1), then per tile j: PV_i(j), S_i(j + 2)
-                if (!wait_k(t, at(0), ug.np)) break;
+                if (!wait_tile(0)) break;
                 tc_fence_after();
-                issue_s(0, t, 0, at(0) < ug.np);
-                commit(&ctl->k_empty[t % kStK]);
-                if (!wait_k(t + 1, at(1), ug.np)) break;
+                issue_tile(0, 0, 0);
+                free_tile(0);
+                if (!wait_tile(1)) break;
                 tc_fence_after();
-                issue_s(1, t + 1, 0, at(1) < ug.np);
-                commit(&ctl->k_empty[(t + 1) % kStK]);
+                issue_tile(1, 1, 0);
+                free_tile(1);
                 if (ntiles == 2) commit(&ctl->q_empty);
                 for (int j = 0; j < ntiles && ok; ++j) {
                     const uint32_t tj = t + j;
@@ -1137,27 +1204,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     tc_fence_after();
                     issue_pv(i, tj, kth == 0, at(j) < ug.np);
                     if (j + 2 < ntiles) {
-                        if (!wait_k(tj + 2, at(j + 2), ug.np)) { ok = false; break; }
+                        if (!wait_tile(j + 2)) { ok = false; break; }
                         tc_fence_after();
-                        issue_s(i, tj + 2, 0, at(j + 2) < ug.np);
-                        commit(&ctl->k_empty[(tj + 2) % kStK]);
+                        issue_tile(i, j + 2, 0);
+                        free_tile(j + 2);
                         if (j + 3 == ntiles) commit(&ctl->q_empty);
                     }
-                    commit(&ctl->v_empty[tj % C::kStagesV]);
+                    commit(&ctl->v_empty[tj % kStV]);
                 }
                 ns[0] += (ntiles + 1) / 2;
                 ns[1] += ntiles / 2;
                 no[0] += 1;
                 no[1] += 1;
                 t += ntiles;
+                tk += ntiles + cached;
                 continue;
             }
             // prologue: S of tile 0 for the slots that start there
-            if (!wait_k(t, at(0), ug.np)) break;
+            if (!wait_tile(0)) break;
             tc_fence_after();
             for (int i = 0; i < kSlots; ++i)
-                if (ug.a[i] == 0 && ug.b[i] > 0) issue_s(i, t, i, at(0) < ug.np);
-            commit(&ctl->k_empty[t % kStK]);
+                if (ug.a[i] == 0 && ug.b[i] > 0) issue_tile(i, 0, i);
+            free_tile(0);
             if (ntiles == 1) commit(&ctl->q_empty);
             for (int j = 0; j < ntiles && ok; ++j) {
                 const uint32_t tj = t + j;
@@ -1168,7 +1236,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                         if (!warp_wait(&ctl->p_full[i], (ns[i] + j - ug.a[i]) & 1, ctl, hdr)) { ok = false; break; }
                         if (j == ug.a[i] && !warp_wait(&ctl->o_empty[i], (no[i] & 1) ^ 1, ctl, hdr)) { ok = false; break; }
                         if (!v_ready) {
-                            const int vst = tj % C::kStagesV;
+                            const int vst = tj % kStV;
                             bool got;
                             if (kQuant && at(j) < ug.np) {
                                 // int8 prefix tile (a paged tail included: its rows past P
@@ -1179,7 +1247,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                                 got = warp_wait(&ctl->v_fix[vst], (fixpar >> vst) & 1, ctl, hdr);
                                 fixpar ^= 1u << vst;
                             } else {
-                                got = warp_wait(&ctl->v_full[vst], (tj / C::kStagesV) & 1, ctl, hdr);
+                                got = warp_wait(&ctl->v_full[vst], (tj / kStV) & 1, ctl, hdr);
                             }
                             if (!got) {
                                 ok = false;
@@ -1193,28 +1261,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     if (j + 1 >= ug.a[i] && j + 1 < ug.b[i]) {
                         // S_i(j+1) overwrites P_i(j): issued after PV_i(j) on the in-order tensor pipe
                         if (!k_ready) {
-                            if (!wait_k(tj + 1, at(j + 1), ug.np)) {
+                            if (!wait_tile(j + 1)) {
                                 ok = false;
                                 break;
                             }
                             k_ready = true;
                             tc_fence_after();
                         }
-                        issue_s(i, tj + 1, i, at(j + 1) < ug.np);
+                        issue_tile(i, j + 1, i);
                     }
                 }
                 if (!ok) break;
                 if (j + 1 < ntiles) {
-                    commit(&ctl->k_empty[(tj + 1) % kStK]);
+                    free_tile(j + 1);
                     if (j + 2 == ntiles) commit(&ctl->q_empty);
                 }
-                commit(&ctl->v_empty[tj % C::kStagesV]);
+                commit(&ctl->v_empty[tj % kStV]);
             }
             for (int i = 0; i < kSlots; ++i) {
                 ns[i] += ug.b[i] - ug.a[i];
                 no[i] += ug.b[i] > ug.a[i] ? 1 : 0;
             }
             t += ntiles;
+            tk += ntiles + cached;
         }
         // every MMA this warp issued has finished before TMEM is released
         if (leader) {
@@ -1232,7 +1301,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
         // behind; on the tiles holding the unit's own tokens it first copies
         // those rows from shared memory into the cache.
         const bool is_k = warp == 3;
-        const int stages = is_k ? kStK : C::kStagesV;
+        const int stages = is_k ? kStK : kStV;
         uint8_t* ring = is_k ? k_smem : v_smem;
         uint64_t* full = is_k ? ctl->k_full : ctl->v_full;
         uint64_t* empty = is_k ? ctl->k_empty : ctl->v_empty;
@@ -1256,6 +1325,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->unit_empty[sl]);
             if (us.u.b < 0) break;
+            if constexpr (kTwo) continue;  // (nothing to write)
             const auto ug = geo(std::bool_constant<kAlt>(), us.u, us.s, s0);
             const int np = ug.np;
             const int q_end = min(us.u.q0 + unit_slots * tps, us.s.n);
@@ -1965,7 +2035,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-#ifndef PA_ATTN_LONG
+#if !defined(PA_ATTN_LONG) && !defined(PA_ATTN_TWO)
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -2014,15 +2084,15 @@ cudaError_t encode_pool_by_block(CUtensorMap* m, const void* ptr, uint64_t bs, u
 
 #endif  // PA_ATTN_LONG
 
-template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false>
-cudaError_t launch_d(const KernelParams<kExt>& p, int grid, cudaStream_t st) {
+template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false, bool kTwo = false>
+cudaError_t launch_d(const KernelParams<kExt, kTwo>& p, int grid, cudaStream_t st) {
     constexpr int kSmem = smem_bytes<D>((kExt ? (int)sizeof(OwnUnits) : 0) + (kExt && kQuant ? scale_ring_bytes<D>() : 0));
     static_assert(kSmem <= 232448, "shared memory budget");
     static int configured_for[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && !configured_for[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<D, kPaged, kQuant, kAlt, kHook, kExt>,
+        cudaError_t e = cudaFuncSetAttribute(attn_fwd_kernel<D, kPaged, kQuant, kAlt, kHook, kExt, kTwo>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         configured_for[dev] = 1;
@@ -2039,12 +2109,12 @@ cudaError_t launch_d(const KernelParams<kExt>& p, int grid, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, kPaged, kQuant, kAlt, kHook, kExt>, p);
+    return cudaLaunchKernelEx(&cfg, attn_fwd_kernel<D, kPaged, kQuant, kAlt, kHook, kExt, kTwo>, p);
 }
 
 }  // namespace
 
-#ifndef PA_ATTN_LONG
+#if !defined(PA_ATTN_LONG) && !defined(PA_ATTN_TWO)
 cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_seqs, int head_dim, int num_blocks) {
     const uint32_t cc = head_dim >= 64 ? 64 : 32;
     const CUtensorMapSwizzle sw = head_dim >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
@@ -2097,6 +2167,20 @@ cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_se
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+// Tensor maps of a pool [n_kv_heads][rows][head_dim] of expanded keys (two terms) and values.
+cudaError_t encode_pool_maps(FwdParamsTwo& p, int head_dim, const __nv_bfloat16* k, const __nv_bfloat16* k2,
+                             const __nv_bfloat16* v, long long rows) {
+    const uint32_t cc = head_dim >= 64 ? 64 : 32;
+    const CUtensorMapSwizzle sw = head_dim >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    const uint64_t D = head_dim, n = rows;
+    cudaError_t e = cudaSuccess;
+    for (auto [map, ptr] : {std::make_pair(&p.tm_ck, k), std::make_pair(&p.tm_ck2, k2), std::make_pair(&p.tm_cv, v)}) {
+        if (e == cudaSuccess)
+            e = encode3d(map, ptr, D, n, p.n_kv_heads, D * 2, n * D * 2, cc, kBlockN, 1, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    }
+    return e;
+}
+
 // Tensor maps of a contiguous shared prefix [Hk, prefix_cap, D] (a paged one is read through tm_ck / tm_cv).
 cudaError_t encode_prefix_maps(FwdParamsX& p, int head_dim, const void* prefix_k, const void* prefix_v) {
     const uint32_t cc = head_dim >= 64 ? 64 : 32;
@@ -2143,6 +2227,15 @@ cudaError_t launch_attn_fwd(const FwdParams& p, int head_dim, int grid, cudaStre
         case 128: return launch_dim<128>(p, grid, st);
         default: return cudaErrorInvalidValue;
     }
+}
+#elif defined(PA_ATTN_TWO)
+// attn_two_*.cu include this file with PA_ATTN_TWO = the head_dim they compile the variant with
+// keys in two terms for.
+template <>
+cudaError_t launch_attn_two_d<PA_ATTN_TWO>(const FwdParamsTwo& p, int grid, cudaStream_t st) {
+    constexpr int D = PA_ATTN_TWO;
+    return p.alt ? launch_d<D, false, false, true, false, false, true>(p, grid, st)
+                 : launch_d<D, false, false, false, false, false, true>(p, grid, st);
 }
 #else
 // attn_long_*.cu include this file with PA_ATTN_LONG = the head_dim they compile

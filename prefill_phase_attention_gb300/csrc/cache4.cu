@@ -192,6 +192,28 @@ __device__ __forceinline__ void store32(uint4* to, const uint4 (&x)[2], bool ali
         to[0] = x[0], to[1] = x[1];
 }
 
+// The values of 16 channels as sums of two bf16 terms (to 2^-17 of their size: keys, whose scores
+// go through an exponential).
+__device__ __forceinline__ void expand16_two(const uint2& codes, uint32_t word, uint4 (&one)[2], uint4 (&two)[2]) {
+    const float s = bf16_lo(word), m = bf16_hi(word);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t c = half ? codes.y : codes.x;
+        uint32_t w[4], x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = fmaf(__uint_as_float(0x4b000000u | ((c >> (8 * e)) & 15u)) - 8388608.f, s, m);
+            const float b = fmaf(__uint_as_float(0x4b000000u | ((c >> (8 * e + 4)) & 15u)) - 8388608.f, s, m);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+            w[e] = *reinterpret_cast<const uint32_t*>(&v);
+            const __nv_bfloat162 r = __floats2bfloat162_rn(a - bf16_lo(w[e]), b - bf16_hi(w[e]));
+            x[e] = *reinterpret_cast<const uint32_t*>(&r);
+        }
+        one[half] = make_uint4(w[0], w[1], w[2], w[3]);
+        two[half] = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+}
+
 template <int D, int kGroups>
 __global__ void __launch_bounds__(kCopyThreads) read_cache4_kernel(const Copy4Params p) {
     constexpr int kGroupLanes = D / 16 / kGroups, kStep = Rows<D>::kHeadStep;
@@ -283,25 +305,28 @@ __global__ void __launch_bounds__(kCopyThreads, 4) expand4_kernel(const Expand4P
             const int pos = owner.y + i * kStep + first;
             codes[i] = make_uint2(0, 0);
             word[i] = 0;
-            if (i * kStep + first < kBlock4 && pos < P) {
+            if (i * kStep + first < kBlock4 && pos >= 0 && pos < P) {
                 const size_t row = row4(c, owner.x, kvh, pos);
                 if (row == ~size_t(0)) continue;
                 codes[i] = __ldg(reinterpret_cast<const uint2*>((h < Hk ? c.k : c.v) + row * (D / 2)) + part);
                 word[i] = __ldg((h < Hk ? c.kp : c.vp) + row * kGroups + part / kGroupLanes);
             }
         }
-        // row of the pool: its blocks' (a paged cache), or its one sequence's (contiguous)
-        const size_t row0 = p.table ? ((size_t)block * Hk + kvh) * kBlock4
-                                    : (size_t)kvh * p.table_blocks * kBlock4 + owner.y;
-        __nv_bfloat16* const pool = (h < Hk ? p.k : p.v) + row0 * D;
+        const size_t at = ((size_t)kvh * p.pool_blocks + block) * kBlock4 * D;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int r = i * kStep + first;
-            if (r >= kBlock4 || owner.y + r >= P) continue;
-            uint4 out[2];
-            expand16(codes[i], word[i], out);
-            uint4* dst = reinterpret_cast<uint4*>(pool + (size_t)r * D) + 2 * part;
-            store32(dst, out, true);  // (the pool is the workspace's)
+            if (r >= kBlock4 || owner.y + r >= P) continue;  // (positions below 0 expand to zeros)
+            const size_t to = at + (size_t)r * D + 16 * part;
+            uint4 one[2], two[2];
+            if (h < Hk) {
+                expand16_two(codes[i], word[i], one, two);
+                store32(reinterpret_cast<uint4*>(p.k + to), one, true);  // (the pool is the workspace's)
+                store32(reinterpret_cast<uint4*>(p.k2 + to), two, true);
+            } else {
+                expand16(codes[i], word[i], one);
+                store32(reinterpret_cast<uint4*>(p.v + to), one, true);
+            }
         }
     }
 }

@@ -81,6 +81,24 @@ struct FwdParams {
 cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_seqs, int head_dim, int num_blocks);
 cudaError_t launch_attn_fwd(const FwdParams& p, int head_dim, int grid, cudaStream_t st);
 
+// Cached keys in two bf16 terms (k + k2 to 2^-17 of their size) and values, expanded from a 4-bit
+// cache: position x of sequence b is row base[b] + x of a pool [n_kv_heads][rows][head_dim] (base[b]
+// - 128 .. base[b] - 1 are zeros where tiles that end at its last position begin below 0).
+struct FwdParamsTwo : FwdParams {
+    CUtensorMap tm_ck2;  // as tm_ck
+    const int* base;
+};
+cudaError_t encode_pool_maps(FwdParamsTwo& p, int head_dim, const __nv_bfloat16* k, const __nv_bfloat16* k2,
+                             const __nv_bfloat16* v, long long rows);
+template <int D>
+cudaError_t launch_attn_two_d(const FwdParamsTwo& p, int grid, cudaStream_t st);
+template <>
+cudaError_t launch_attn_two_d<32>(const FwdParamsTwo& p, int grid, cudaStream_t st);
+template <>
+cudaError_t launch_attn_two_d<64>(const FwdParamsTwo& p, int grid, cudaStream_t st);
+template <>
+cudaError_t launch_attn_two_d<128>(const FwdParamsTwo& p, int grid, cudaStream_t st);
+
 // Scheduler of the long-context variant.
 struct LongScheduleArgs : ScheduleArgs {
     UnitX* xunits;
@@ -202,9 +220,8 @@ struct Copy4Params {
 cudaError_t launch_write_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
 cudaError_t launch_read_cache4(const Copy4Params& p, int head_dim, int sms, cudaStream_t stream);
 
-// Long chunks: their sequences' cached rows expanded to bf16, for the attention kernel to read as
-// a paged cache, a pool of blocks of kBlock4 tokens [pool_blocks][n_kv_heads][kBlock4][head_dim],
-// or, with one sequence (table == nullptr), as a contiguous one.
+// Long chunks: their sequences' cached rows expanded for the attention kernel, in blocks of kBlock4
+// rows of a pool [n_kv_heads][pool_blocks * kBlock4][head_dim] (FwdParamsTwo).
 constexpr int kBlock4 = 128;
 struct Expand4Params {
     Sequences4 seqs;  // checked: where the plan writes them
@@ -212,12 +229,12 @@ struct Expand4Params {
     int few_tokens;   // sequences of up to as many new tokens are not taken
     int window;
     int pool_blocks;
-    int table_blocks;  // of a sequence
-    int* taken;        // [num_seqs] 1 + the sequence's first block of the pool, 0: not taken
-    int32_t* table;    // [num_seqs][table_blocks]
-    int2* owners;      // [pool_blocks] sequence and first position
-    int* blocks;       // in use
+    int* taken;       // [num_seqs] 0: not taken
+    int* base;        // [num_seqs] the pool's row of a taken sequence's position 0
+    int2* owners;     // [pool_blocks] sequence and first position
+    int* blocks;      // in use
     __nv_bfloat16* k;
+    __nv_bfloat16* k2;
     __nv_bfloat16* v;
     Copy4Params write;            // the call's new tokens, written by the same launch
     int expanders, write_blocks;  // blocks that expand, blocks of tokens to write (set by the launch)

@@ -6,11 +6,14 @@
 
 namespace pa {
 
-// The first block of the pool that the attention kernel reads of a sequence: it reads whole tiles,
-// which end at P in a contiguous cache, so from up to 127 positions ahead of a window on.
+// The blocks [first, end) of a sequence's positions that the attention kernel reads: whole tiles that
+// end at its last cached one, so from up to 127 positions ahead of a window on, or from below 0:
+// block -1 is of zeros.
 __device__ __forceinline__ int first_block(const Expand4Params& p, const SeqInfo& s) {
-    return p.window > 0 ? max(0, s.P - p.window + 2 - kBlock4) / kBlock4 : 0;
+    const int first = p.window > 0 ? max(0, s.P - p.window + 2 - kBlock4) / kBlock4 : 0;
+    return first > 0 ? first : -1;
 }
+__device__ __forceinline__ int end_block(const SeqInfo& s) { return s.P > 0 ? (s.P + kBlock4 - 1) / kBlock4 : -1; }
 
 // Checks the sequences, and lays out the pool (one block of 1024 threads; ends with a barrier).
 __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
@@ -43,7 +46,7 @@ __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
         const bool wanted = s.n > p.few_tokens;
         const int first = first_block(p, s);
         // (sums past the pool saturate: a sequence's blocks are at most 2^23)
-        int need = wanted ? (s.P + s.n + kBlock4 - 1) / kBlock4 - first : 0, inc = need;
+        int need = wanted ? max(0, end_block(s) - first) : 0, inc = need;
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc = min(inc + y, 1 << 29);
@@ -57,20 +60,19 @@ __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
         }
         const int at = min(before + inc, 1 << 29) - need;
         const bool fits = wanted && before + inc < 1 << 29 && at + need <= p.pool_blocks;
-        if (b < p.seqs.num_seqs) p.taken[b] = fits ? at + 1 : 0;
+        if (b < p.seqs.num_seqs) {
+            p.taken[b] = fits;
+            p.base[b] = (at - first) * kBlock4;
+        }
         if (fits) atomicMax(&in_use, at + need);  // (those that fit are the first ones: no gaps)
         __syncthreads();
     }
     if (tid == 0) *p.blocks = in_use;
     for (int b = warp; b < p.seqs.num_seqs; b += 32) {
-        const int at = p.taken[b] - 1;
-        if (at < 0) continue;
+        if (!p.taken[b]) continue;
         const SeqInfo s = p.seqs.checked[b];
-        const int first = first_block(p, s), end = (s.P + s.n + kBlock4 - 1) / kBlock4;
-        for (int i = lane; i < end; i += 32) {
-            if (p.table) p.table[(size_t)b * p.table_blocks + i] = i < first ? 0 : at + i - first;
-            if (i >= first) p.owners[at + i - first] = make_int2(b, i * kBlock4);
-        }
+        const int first = first_block(p, s), end = end_block(s), at = p.base[b] / kBlock4 + first;
+        for (int i = first + lane; i < end; i += 32) p.owners[at + i - first] = make_int2(b, i * kBlock4);
     }
     __threadfence_block();
     __syncthreads();

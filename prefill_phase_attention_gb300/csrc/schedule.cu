@@ -58,8 +58,7 @@ __device__ __forceinline__ void build_schedule(const ScheduleArgs& a) {
         const int lane = tid & 31, nwarps = nthr >> 5;
         for (int b = tid >> 5; b < a.num_seqs; b += nwarps) {
             const long long lk = (long long)a.cu_seqlens_k[b + 1] - a.cu_seqlens_k[b];
-            const bool taken = !a.taken || a.taken[b];  // (another has no table here)
-            const long long used = lk > 0 && taken ? (lk + a.block_size - 1) / a.block_size : 0;
+            const long long used = lk > 0 ? (lk + a.block_size - 1) / a.block_size : 0;
             const int nb = used < a.max_blocks ? (int)used : a.max_blocks;
             bool bad = false;
             for (int L = lane; L < nb; L += 32) {
