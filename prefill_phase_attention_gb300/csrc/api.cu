@@ -1434,8 +1434,8 @@ pa_status read_cache4(const pa_cache4* cache, const Options& o, int head_dim, in
 // long chunks, expands the sequence's cache to bf16 once (into the workspace) and runs the
 // tensor-core kernel over it.  Sequences of few new tokens go the first way, the others the
 // second as far as that room reaches; few: up to kFewRows rows over all heads (one sequence,
-// D = 128, 32 heads, over 1024 / 8192 / 32768 cached tokens, us: 64 tokens 38 / 70 / 160 and 29 /
-// 80 / 268, 128 tokens 65 / 130 / 310 and 29 / 80 / 264).  The host does not know the lengths:
+// D = 128, 32 heads, over 1024 / 8192 / 32768 cached tokens, us: 64 tokens 35 / 78 / 201 and 33 /
+// 111 / 448, 128 tokens 60 / 141 / 391 and 33 / 111 / 434).  The host does not know the lengths:
 // where all rows but one token of each sequence are at most kExcessRows, the row kernel takes
 // every sequence, which costs less than the other way's launches.
 constexpr int kFewRows = 2048, kExcessRows = 8192;
@@ -1667,7 +1667,7 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         p.seqs.checked = reinterpret_cast<pa::SeqInfo*>(take(seq_bytes));
         x.seqs = p.seqs;
         x.cache = c;
-        x.few_tokens = few;
+        x.few_tokens = one ? 0 : few;  // (the row kernel is not launched for one, whatever its length now)
         x.window = causal ? o.window : 0;
         x.pool_blocks = (int)pool_blocks;
         x.taken = reinterpret_cast<int*>(take(taken_bytes));

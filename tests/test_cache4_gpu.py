@@ -1,5 +1,6 @@
 """GPU tests of the 4-bit cache: attention over it, writing it and reading it back, each against its plain 64-bit
 form (tests/cache4_reference.py, where the bounds are derived)."""
+import concurrent.futures
 import math
 
 import pytest
@@ -49,12 +50,12 @@ def same_bits(a, b):
 class Call:
     """Inputs of one call on the CPU, their GPU copies, and what is written in guarded buffers."""
 
-    def __init__(self, seed, new, lens, d=128, hk=2, share=2, group=None, block=0, kind="normal", slack=3):
+    def __init__(self, seed, new, lens, d=128, hk=2, share=2, group=None, block=0, kind="normal", slack=3, pad=0):
         g = torch.Generator().manual_seed(seed)
         self.new, self.lens, self.d, self.hk, self.share = new, lens, d, hk, share
         cap = max(p + n for p, n in zip(lens, new)) + slack
         self.cache = R.Cache(g, len(new), cap, hk, d, group or d, block, kind=kind)
-        t = sum(new)
+        t = sum(new) + pad
         size = 2.0 ** 60 if kind == "large" else 1.0
         self.q = (torch.randn((t, hk * share, d), generator=g) / size).to(torch.bfloat16)
         self.k = (torch.randn((t, hk, d), generator=g) * size).to(torch.bfloat16)
@@ -94,7 +95,10 @@ class Call:
         assert binding.prefill_attn_device_status() == 0
         out, lse, bound, lbound = R.attention(self.cache, self.q, self.k, self.v, self.cu, self.lens, self.scale, causal,
                                               window, tiles)
-        got, glse = self.out[1].double().cpu(), self.lse[1].double().cpu()
+        t = self.cu[-1]
+        assert self.out[1][t:].isnan().all() and self.lse[1][t:].isnan().all(), "rows behind the last sequence"
+        got, glse = self.out[1][:t].double().cpu(), self.lse[1][:t].double().cpu()
+        out, lse, bound, lbound = out[:t], lse[:t], bound[:t], lbound[:t]
         assert got.isfinite().all() and glse.isfinite().all()
         assert ((got - out).abs() <= bound).all(), ((got - out).abs() / bound).max()
         assert ((glse - lse).abs() <= lbound).all(), ((glse - lse).abs() / lbound).max()
@@ -176,19 +180,42 @@ def test_more_long_chunks_than_the_pool_holds():
     largest = max(v.double().abs().max(), R.values(cache.codes[1], cache.params[1]).abs().max())
     for i in range(b):
         alone, e = attend(slice(i * n, (i + 1) * n), [i])
-        # each is off by less than 3 u of the largest value where scores are exact; a score's error from
-        # keys rounded to bf16, u |q| |k| scale per channel at most, in the mean over channels
-        # 2^-9 sqrt(128) 3 / sqrt(128) of a key's size: below 2^-6, which moves weights by 2^-5
-        assert ((together[i * n:(i + 1) * n] - alone).abs() <= (6 * R.U + 2.0 ** -5) * largest).all()
+        # off by 2 u (values, p) and 2^-11 (p s) of the largest value, new tokens' weights by u, and each out's own rounding u
+        assert ((together[i * n:(i + 1) * n] - alone).abs() <= 6 * R.U * largest).all()
         blocks = table[i, -fresh:].long()
         for x, y in zip(c, e):
             assert same_bits(x[blocks], y[blocks])
+
+
+@pytest.mark.parametrize("new,pad", [([1, 3], 7), ([5], 600), ([130], 70), ([0], 300), ([300, 1, 129], 200), ([2, 3, 1], 900)])
+def test_rows_behind_the_last_sequence(new, pad):
+    """What a replayed call over fewer tokens than it was captured for has: they are left as they were."""
+    c = Call(18, new, [100, 257, 31][:len(new)], group=64, pad=pad)
+    c.attend()
+    c.check(tiles=True)
+    w = Call(19, new, [100, 257, 31][:len(new)], group=64, pad=pad)
+    w.write()
+    w.check_cache()
+    k = torch.full(w.k.shape, math.nan, dtype=torch.bfloat16, device="cuda")
+    v = k.clone()
+    binding.prefill_attn_cache4_read(w.codes[0][1], w.codes[1][1], w.meta[0], w.offsets, k, v, **w.opts)
+    t = w.cu[-1]
+    for got, x in ((k, w.k), (v, w.v)):
+        assert got[t:].isnan().all()
+        assert same_bits(got[:t], R.values(*R.quantise(x[:t], 64)).float().to(torch.bfloat16))
 
 
 @pytest.mark.parametrize("window", [1, 100, 128, 300])
 @pytest.mark.parametrize("block", [0, 16])
 def test_chunks_under_windows(window, block):
     c = Call(13, [460, 1, 150], [400, 300, 10], group=32, block=block)
+    c.attend(window=window)
+    c.check(window=window, tiles=True)
+
+
+@pytest.mark.parametrize("window,past", [(129, 1000), (130, 1024), (257, 1025), (385, 1151), (5000, 1023)])
+def test_one_chunk_under_a_window(window, past):
+    c = Call(16, [200], [past], hk=1, share=4, group=64, block=32)
     c.attend(window=window)
     c.check(window=window, tiles=True)
 
@@ -446,15 +473,94 @@ def test_captured_calls_read_their_metadata_at_replay():
         assert same_bits(c.out[1], d.out[1]) and same_bits(c.lse[1], d.lse[1])
 
 
-def test_two_streams_at_once():
-    calls = [Call(33 + i, [1] * 3, [2000, 77, 500], hk=2) for i in range(2)]
+@pytest.mark.parametrize("new", [[600], [300, 1, 129]])
+def test_captured_chunks_read_their_metadata_at_replay(new):
+    c = Call(36, new, [300, 5, 64][:len(new)], block=16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c.attend()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            c.attend()
+    # other lengths of the same total, and fewer tokens
+    for seed, fewer, lens in ((37, new[::-1], [129, 0, 300][:len(new)]), (38, [5, 2, 1][:len(new)], [200, 9, 300][:len(new)]),
+                              (39, [400, 0, 1][:len(new)], [37, 300, 5][:len(new)])):
+        pad = sum(new) - sum(fewer)
+        cap = c.cache.table.shape[1] * 16
+        d = Call(seed, fewer, lens, block=16, pad=pad, slack=cap - max(p + n for p, n in zip(lens, fewer)))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            for a, b in zip(c.codes + c.params + [c.out, c.lse], d.codes + d.params + [d.out, d.lse]):
+                a[1].copy_(b[1])
+            for a, b in zip([*c.dev, *c.meta, c.offsets, c.opts["block_table"]],
+                            [*d.dev, *d.meta, d.offsets, d.opts["block_table"]]):
+                a.copy_(b)
+            graph.replay()
+        side.synchronize()
+        d.codes, d.params, d.out, d.lse = c.codes, c.params, c.out, c.lse
+        d.check(tiles=True)
+
+
+def test_many_paged_sequences():
+    """More than a CTA keeps at hand, in blocks; one sequence's table names a block outside the pool."""
+    g = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 90, (400,), generator=g).tolist()
+    for bad in (None, 257):
+        c = Call(50, [1] * 400, lens, d=64, hk=1, share=2, group=32, block=8)
+        if bad is None:
+            c.attend()
+            c.check()
+            continue
+        c.opts["block_table"][bad, 0] = -5
+        c.attend()
+        torch.cuda.synchronize()
+        assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+        out, _, bound, _ = R.attention(c.cache, c.q, c.k, c.v, c.cu, c.lens, c.scale)
+        got = c.out[1].double().cpu()
+        there = torch.arange(400) != bad
+        assert got[bad].isnan().all() and ((got - out).abs() <= bound)[there].all()
+
+
+def test_read_into_tensors_that_are_16_byte_aligned():
+    g = torch.Generator().manual_seed(23)
+    cache = R.Cache(g, 1, 200, 2, 128, 128)
+    codes, params = [x.cuda() for x in cache.codes], [x.cuda() for x in cache.params]
+    buf = [torch.full((70 * 256 + 16,), math.nan, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    k, v = buf[0][8:8 + 70 * 256].view(70, 2, 128), buf[1][:70 * 256].view(70, 2, 128)
+    assert k.data_ptr() % 32 == 16
+    binding.prefill_attn_cache4_read(*codes, i32([0, 70]), i32([100]), k, v, cache_k_params=params[0], cache_v_params=params[1])
+    for which, got in enumerate((k, v)):
+        for h in range(2):
+            assert same_bits(got[:, h], R.values(*cache.rows(which, 0, h, 170, 100)).float().to(torch.bfloat16))
+    assert buf[0][:8].isnan().all() and buf[0][-8:].isnan().all() and buf[1][-16:].isnan().all()
+
+
+def test_threads_on_one_stream():
+    """Calls of several host threads at once on one stream run one after the other."""
+    calls = [Call(60 + i, new, lens, hk=2, block=16)
+             for i, (new, lens) in enumerate([([1] * 3, [2000, 77, 500]), ([300, 1, 129], [400, 5, 64]), ([600], [100])])]
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    with concurrent.futures.ThreadPoolExecutor(3) as pool:
+        for _ in range(5):
+            list(pool.map(lambda c: c.attend(stream=stream), calls))
+    stream.synchronize()
+    for c in calls:
+        c.check(tiles=max(c.new) > 16)
+
+
+@pytest.mark.parametrize("new", [[1] * 3, [300, 1, 129], [500]])
+def test_two_streams_at_once(new):
+    calls = [Call(33 + i, new, [2000, 77, 500][:len(new)], hk=2) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in calls]
     torch.cuda.synchronize()
     for _ in range(10):
         for c, s in zip(calls, streams):
             c.attend(stream=s)
     for c in calls:
-        c.check()
+        c.check(tiles=max(new) > 16)
 
 
 @pytest.mark.parametrize("block", [0, 16])
