@@ -1,16 +1,22 @@
 """Plain 64-bit forms of the 4-bit cache's calls, and the error bounds their tests use.
 
-A rounding to bf16 is off by at most u = 2^-8 of the value, one to fp32 by 2^-24.
+A rounding to bf16 is off by at most u = 2^-8 of the value, one to fp16 by 2^-11, one to fp32 by 2^-24.
 
-Attention.  Let P be the exact softmax weights.  The row kernel rounds p s (s: a value's scale) to
-bf16 ahead of the product with the codes less 8, and a new token's p ahead of the product with its
-value, so O is off by at most  u sum_j P_j a_j,  a_j = s_j |c_j - 8| for a cached key, |v_j| for a
-new one.  The tile kernel rounds cached keys and values to bf16, and p: the scores are off by
-at most  x = u scale sum_i |q_i| |k_i|  (cached keys only), which moves each P by a factor within e^(+-2x)
-(its own score and the sum's), and O by  u sum_j P_j |v_j| (values) + u sum_j P_j |v_j| (p).  Both round
-out once.  fp32: a score is a sum of d products and d / 32 parameter terms, each within 2^-20 of
-sum |q| |k| (the codes' sums are cancelled by the offset's, at most 16 times as large), and
-exponentials and sums add 2^-18 of the weights.
+Attention.  Let P be the exact softmax weights, s, m, c a cached key's or value's scale, minimum and code.
+
+The row kernel rounds p s to fp16 ahead of the product with c, and a new token's p to bf16 ahead of the
+product with its value, so O is off by at most  sum_j P_j a_j,  a_j = 2^-11 s_j c_j for a cached key and
+u |v_j| for a new one.  Weights are scaled so that a row's largest is at least 2^7: those below fp16's normal
+range are off by 2^-25 absolutely, 2^-32 of the largest p s, 15 times as much in O, each.
+
+The tile kernel's cached keys are sums of two bf16 terms, off by at most 2^-16, which is as much of
+scale sum_i |q_i| |k_i| in a score; it rounds cached values and p to bf16, and O is off by u sum_j P_j |v_j| for
+each.
+
+Both round out once.  fp32: a score is a sum of d / 16 products of 16 channels and d / 32 parameter terms,
+each sum off by at most 2^-22 of what it sums up: together 2^-18 of A = scale sum_i |q_i| (|m_i| + c_i s_i), which
+covers its product with the scale and the difference to the maximum too.  Exponentials and sums add 2^-18 of
+the weights, and O's sums 2^-18 of  sum_j P_j (|m_j| + c_j s_j).  A score off by x moves every P by a factor within e^(+-2x).
 """
 import math
 
@@ -124,29 +130,33 @@ def attention(cache, q, k, v, cu, lens, scale, causal=True, window=0, tiles=Fals
         if window:
             see = see & (j > pos - window)
         for h in range(hk):
-            kc = values(*cache.rows(0, b, h, p))
+            kc, ks, km = split(*cache.rows(0, b, h, p))
             vc, vs, vm = split(*cache.rows(1, b, h, p))
-            kk = torch.cat([kc, k[rows, h].double()])
-            val = torch.cat([vm + vc * vs, v[rows, h].double()])
-            step = torch.cat([vs * (vc - 8).abs(), v[rows, h].double().abs()])
+            kn, vn = k[rows, h].double(), v[rows, h].double()
+            kk, kparts = torch.cat([km + kc * ks, kn]), torch.cat([km.abs() + kc * ks, kn.abs()])
+            val, vparts = torch.cat([vm + vc * vs, vn]), torch.cat([vm.abs() + vc * vs, vn.abs()])
+            step = torch.cat([2.0 ** -11 * vc * vs, U * vn.abs()])
+            least = torch.cat([vs, torch.zeros_like(vn)])
             qq = q[rows, h * g:(h + 1) * g].double()
             x = torch.einsum("igd,jd->igj", qq, kk) * scale
             x = torch.where(see[:, None], x, -math.inf)
             z = torch.logsumexp(x, -1)
             w = torch.exp(x - z[..., None])
             ab = torch.einsum("igd,jd->igj", qq.abs(), kk.abs()) * scale
-            ab = torch.where(see[:, None], ab, 0.0)
-            fp32 = ab * 2.0 ** -16 + 2.0 ** -18
-            cached = (j < p).double()
-            ex = torch.where(see[:, None], (U * ab * cached if tiles else 0.0) + fp32, 0.0).amax(-1)
+            parts = torch.einsum("igd,jd->igj", qq.abs(), kparts) * scale
+            x_err = parts * 2.0 ** -18 + (ab * 2.0 ** -16 if tiles else 0.0) + 2.0 ** -18
+            ex = torch.where(see[:, None], x_err, 0.0).amax(-1)
             o = torch.einsum("igj,jd->igd", w, val)
             mean = torch.einsum("igj,jd->igd", w, val.abs())
-            r = torch.einsum("igj,jd->igd", w, step) if not tiles else 2 * mean
+            r = torch.einsum("igj,jd->igd", w, step) + 2.0 ** -18 * torch.einsum("igj,jd->igd", w, vparts)
+            r = r + 15 * 2.0 ** -32 * (p + n) * (w[..., None] * least).amax(2)
+            if tiles:
+                r = r + 2 * U * mean
             out[rows, h * g:(h + 1) * g] = o
             lse[rows, h * g:(h + 1) * g] = z
             grown = torch.expm1(2 * ex)[..., None] * mean
             # out itself may be off by what precedes its own rounding
-            err = (U + 2.0 ** -18) * r * (1 + torch.expm1(2 * ex)[..., None]) + grown
+            err = r * (1 + torch.expm1(2 * ex)[..., None]) + grown
             bound[rows, h * g:(h + 1) * g] = err + U * (o.abs() + err)
             lbound[rows, h * g:(h + 1) * g] = ex + z.abs() * 2.0 ** -20 + 2.0 ** -20
     return out, lse, bound, lbound

@@ -66,6 +66,7 @@ SHARED = [
     (dict(o=dict(wait_timeout_test=1)), 1, "wait_timeout_test"),
     (dict(o=dict(PAGED, block_size=16)), 1, "max_cache_len"),
     (dict(o=dict(PAGED, block_size=12), cap=12), 2, "block_size"),
+    (dict(o=dict(PAGED, num_blocks=2 ** 28)), 2, "2^32"),
 ]
 
 
