@@ -1620,8 +1620,8 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     // The row kernel's CTAs check metadata and tables themselves; a kernel ahead does for the
     // rotary prologue, and for more sequences than a CTA keeps at hand.
     const bool check = !tiles && (o.rope_theta > 0.f || (o.block_table && num_seqs > pa::kRows4Seqs));
-    // the pool of expanded blocks (a sequence has up to one more than its positions: see FwdParamsTwo)
-    const long long seq_blocks = ((long long)max_cache_len + pa::kBlock4 - 1) / pa::kBlock4 + 1;
+    // the pool of expanded blocks
+    const long long seq_blocks = ((long long)max_cache_len + pa::kBlock4 - 1) / pa::kBlock4;
     const size_t block_bytes = (size_t)n_kv_heads * pa::kBlock4 * head_dim * 2;  // of a term of K, or of V
     long long pool_blocks = 0;
     if (tiles) {
@@ -1642,10 +1642,11 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
     const size_t seq_bytes = tiles ? align_up((size_t)num_seqs * sizeof(pa::SeqInfo), 256) : 0;
     const size_t taken_bytes = tiles ? align_up((2 * (size_t)num_seqs + 1) * sizeof(int), 256) : 0;
     const size_t owner_bytes = align_up((size_t)pool_blocks * sizeof(int2), 256);
+    const size_t halves_bytes = align_up((size_t)pool_blocks * n_kv_heads, 256);
     const size_t pool_bytes = align_up((size_t)pool_blocks * block_bytes, 256);
     void* aux = nullptr;
-    s = get_aux_scratch(ws, stream, part_bytes + kept_bytes + seq_bytes + taken_bytes + owner_bytes + 3 * pool_bytes,
-                        &aux);
+    s = get_aux_scratch(ws, stream,
+                        part_bytes + kept_bytes + seq_bytes + taken_bytes + owner_bytes + halves_bytes + 3 * pool_bytes, &aux);
     if (s != PA_OK) return s;
     char* at = static_cast<char*>(aux);
     auto take = [&](size_t bytes) { char* const x = at; at += bytes; return x; };
@@ -1674,6 +1675,7 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         x.base = x.taken + num_seqs;
         x.blocks = x.base + num_seqs;
         x.owners = reinterpret_cast<int2*>(take(owner_bytes));
+        x.halves = reinterpret_cast<uint8_t*>(take(halves_bytes));
         x.k = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
         x.k2 = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
         x.v = reinterpret_cast<__nv_bfloat16*>(take(pool_bytes));
@@ -1712,6 +1714,8 @@ pa_status prefill_attn_varlen_cache4(const void* q, const void* k, const void* v
         pa::FwdParamsTwo fp;
         fill_fwd(fp, k, v, x.k, x.v, out, lse, scr, max_cache_len, n_heads, n_kv_heads, scale, causal, contiguous, sched);
         fp.base = x.base;
+        fp.halves = x.halves;
+        fp.pool_blocks = (int)pool_blocks;
         // (the maps of q, k and v; those of the cache are replaced by the pool's)
         e = pa::encode_fwd_maps(fp, q, total_q, 1, head_dim, 0);
         if (e == cudaSuccess) e = pa::encode_pool_maps(fp, head_dim, x.k, x.k2, x.v, pool_blocks * pa::kBlock4);

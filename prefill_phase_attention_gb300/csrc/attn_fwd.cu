@@ -48,10 +48,13 @@
 // sink tokens and batches that share a prefix.  Its units are pieces of a query
 // block's tiles (UnitX); a piece writes fp32 partial results, which merge_kernel
 // joins.  Few units: no scheduler runs, every CTA plans for itself first.
+// The variant for 4-bit caches (kTwo; compiled by attn_two_*.cu) reads cached tiles from a pool that a
+// kernel before expanded them into; its units never have two Q tiles where their slots alternate.
 // Every wait is bounded in time; on timeout the CTA records PA_DEVERR_TIMEOUT,
 // drains its in-flight copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cudaTypedefs.h>
 
 #include <climits>
@@ -94,6 +97,7 @@ struct Cfg {
     static constexpr int kStagesV = D == 128 ? 3 : 4;
     static constexpr uint32_t kIdescS = idesc_bf16_f32(kBlockM, kBlockN, 0, 0);
     static constexpr uint32_t kIdescO = idesc_bf16_f32(kBlockM, D, 0, 1);
+    static constexpr uint32_t kIdescOHalf = idesc_f16_f32(kBlockM, D, 0, 1);
 };
 
 struct UnitSlot {
@@ -207,6 +211,11 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // First key (absolute position in the sequence) of KV tile j of a unit whose
@@ -602,15 +611,35 @@ __device__ __forceinline__ void claim_unit_ext(const FwdParamsX& p, WorkspaceHea
 // whose tiles are split between CTAs).
 // kTwo: cached keys in two bf16 terms, of the sequences' rows of one pool (FwdParamsTwo).  A
 // cached tile is two entries of the K ring, and S their products' sum; nothing is
-// written to the pool.
+// written to the pool.  Cached values are fp16 where the pool says so (of the tile), and P is too
+// there: 512 tokens over 4096 cached ones are off by 0.0028 of the output with both in bf16, by
+// 0.0017 so, which is the output's own rounding (and take 81 us in place of 79).
 template <bool kExt, bool kTwo>
 using KernelParams = std::conditional_t<kTwo, FwdParamsTwo, std::conditional_t<kExt, FwdParamsX, FwdParams>>;
+
+// Whether the pool holds a tile's values in fp16: its place in the flags is that of the unit plus the
+// tile's index.
+template <class Params>
+__device__ __forceinline__ int value_flags(const Params& p, const Unit& u, const SeqInfo& s, int np) {
+    if constexpr (std::is_same_v<Params, FwdParamsTwo>)  // (a whole number of blocks)
+        return u.kvh * p.pool_blocks + (p.base[u.b] + s.P - np * kBlockN) / kBlockN;
+    return 0;
+}
+template <class Params>
+__device__ __forceinline__ bool value_half(const Params& p, int flags, int jt, int np) {
+    if constexpr (std::is_same_v<Params, FwdParamsTwo>) return jt < np && __ldg(p.halves + flags + jt) != 0;
+    return false;
+}
 
 template <int D, bool kPaged, bool kQuant, bool kAlt = false, bool kHook = false, bool kExt = false, bool kTwo = false>
 __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_constant__ KernelParams<kExt, kTwo> p) {
     using C = Cfg<D>;
     static_assert(!kTwo || (!kPaged && !kQuant && !kHook && !kExt), "keys in two terms: plain calls only");
     constexpr int kReleasers = kTwo ? 1 : 2;  // of a ring's stage: MMA commit, cache writer
+    // What the running maximum is kept below the largest score by (log2 units), so that weights are
+    // larger by as much: up to 2^15 with the 2^8 that it may fall behind, and exact in fp16 from 2^-21
+    // of the largest on.
+    constexpr float kLead = kTwo ? 7.f : 0.f;
     static_assert(!(kAlt && kQuant), "the merge exchange shares storage with the int8 scale ring");
     // K stages in use.  With an int8 cache the K writer publishes each tile's row
     // scales in a 4-deep ring (Ctrl::kscale) that the softmax warps read after
@@ -620,21 +649,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
     // 3 stages that PV follows every slot's softmax of tile t: the ring slot is
     // free.  (bf16 caches use no scale ring.)  A ring of two (long-context variant at
     // head_dim 128): see its writer.
-    // Keys in two terms at head_dim 128, units whose slots alternate: three of the five tiles that
-    // the rings have, so that one term of the next tile comes while a tile's two are used
-    // (512 tokens over 4096 cached ones, 32/8 heads: with two 95 us, with three 78).  Where both
-    // slots use every tile, V's third one is worth more (4096 over 4096, 32 heads: 474 and 494).
-    constexpr bool kMoreK = kTwo && kAlt && D == 128;
-    constexpr int kRingK = C::kStagesK + (kMoreK ? 1 : 0), kStV = C::kStagesV - (kMoreK ? 1 : 0);
+    // Keys in two terms at head_dim 128, units of one Q tile: the second one's place is a third
+    // stage of K, so that one term of the next tile comes while a tile's two are used (512 tokens
+    // over 4096 cached ones, 32/8 heads: with two 97 us, with three 81).
+    constexpr bool kOneQ = kTwo && kAlt && D == 128;
+    constexpr int kRingQ = kOneQ ? 1 : kSlots, kRingK = C::kStagesK + (kOneQ ? 1 : 0), kStV = C::kStagesV;
     constexpr int kStK = kQuant && C::kStagesK > 3 ? 3 : kRingK;
     // paged bf16 cache, two column chunks: prefix tiles staged block by block
     constexpr bool kGrp = kPaged && !kQuant && C::kChunks == 2;
-    const int unit_slots = kAlt ? p.unit_slots : kSlots;  // Q tiles of a unit
+    const int unit_slots = kTwo && kAlt ? 1 : kAlt ? p.unit_slots : kSlots;  // Q tiles of a unit
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // swizzled TMA/UMMA tiles need 1024-byte alignment (reported below)
     const bool misaligned = (smem_u32(smem_raw) & 1023u) != 0;
     uint8_t* q_smem = smem_raw;                              // [kSlots] tiles
-    uint8_t* k_smem = q_smem + kSlots * C::kTileBytes;       // [kRingK] tiles
+    uint8_t* k_smem = q_smem + kRingQ * C::kTileBytes;       // [kRingK] tiles
     uint8_t* v_smem = k_smem + kRingK * C::kTileBytes;       // [kStV] tiles
     Ctrl* ctl = reinterpret_cast<Ctrl*>(v_smem + kStV * C::kTileBytes);
     OwnUnits* own = reinterpret_cast<OwnUnits*>(ctl + 1);  // kExt
@@ -1117,8 +1145,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             }
             __syncwarp();
         };
-        auto issue_pv = [&](int i, uint32_t tt, bool first, bool grp) {
+        auto issue_pv = [&](int i, uint32_t tt, bool first, bool grp, bool half) {
             if (leader) {
+                const uint32_t idesc = kTwo && half ? C::kIdescOHalf : C::kIdescO;
                 const uint32_t voff = (tt % kStV) * C::kTileBytes;
                 // V operand: descriptor template and 16-key step of the tile's staging
                 const bool g = kGrp && grp;
@@ -1127,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
 #pragma unroll
                 for (int kk = 0; kk < kBlockN / 16; ++kk)
                     mma_ts(tmem + i * kColSlot + kColO, tmem + i * kColSlot + kk * 8,
-                           vd + ((voff + kk * vstep) >> 4), C::kIdescO, (!first || kk > 0) ? 1u : 0u);
+                           vd + ((voff + kk * vstep) >> 4), idesc, (!first || kk > 0) ? 1u : 0u);
                 mma_commit(&ctl->pv_done[i]);
             }
             __syncwarp();
@@ -1148,6 +1177,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             const auto ug = geo(std::bool_constant<kAlt>(), u, s, s0);
             auto at = [&](int j) { return tile_at(ug, j); };
             const int ntiles = ug.ntiles;
+            const int flags = kTwo ? value_flags(p, u, s, ug.np) : 0;
             // the K ring's entries of tile j: waits for them, computes S from them, frees them
             const int cached = kTwo ? max(0, min(ug.np - at(0), ntiles)) : 0;
             auto entry = [&](int j) -> uint32_t { return tk + (j < cached ? 2 * j : cached + j); };
@@ -1195,14 +1225,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 issue_tile(1, 1, 0);
                 free_tile(1);
                 if (ntiles == 2) commit(&ctl->q_empty);
+                bool next_half = kTwo && value_half(p, flags, at(0), ug.np);
                 for (int j = 0; j < ntiles && ok; ++j) {
                     const uint32_t tj = t + j;
+                    const bool half = next_half;
+                    next_half = kTwo && value_half(p, flags, at(j + 1), ug.np);
                     const int i = j & 1, kth = j >> 1;
                     if (!warp_wait(&ctl->p_full[i], (ns[i] + kth) & 1, ctl, hdr)) { ok = false; break; }
                     if (kth == 0 && !warp_wait(&ctl->o_empty[i], (no[i] & 1) ^ 1, ctl, hdr)) { ok = false; break; }
                     if (!wait_v(tj, at(j))) { ok = false; break; }
                     tc_fence_after();
-                    issue_pv(i, tj, kth == 0, at(j) < ug.np);
+                    issue_pv(i, tj, kth == 0, at(j) < ug.np, half);
                     if (j + 2 < ntiles) {
                         if (!wait_tile(j + 2)) { ok = false; break; }
                         tc_fence_after();
@@ -1227,8 +1260,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 if (ug.a[i] == 0 && ug.b[i] > 0) issue_tile(i, 0, i);
             free_tile(0);
             if (ntiles == 1) commit(&ctl->q_empty);
+            bool next_half = kTwo && value_half(p, flags, at(0), ug.np);
             for (int j = 0; j < ntiles && ok; ++j) {
                 const uint32_t tj = t + j;
+                const bool half = next_half;
+                next_half = kTwo && value_half(p, flags, at(j + 1), ug.np);
                 bool v_ready = false, k_ready = false;
                 for (int i = 0; i < kSlots; ++i) {
                     if (j >= ug.a[i] && j < ug.b[i]) {
@@ -1256,7 +1292,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                             v_ready = true;
                         }
                         tc_fence_after();
-                        issue_pv(i, tj, j == ug.a[i], at(j) < ug.np);
+                        issue_pv(i, tj, j == ug.a[i], at(j) < ug.np, half);
                     }
                     if (j + 1 >= ug.a[i] && j + 1 < ug.b[i]) {
                         // S_i(j+1) overwrites P_i(j): issued after PV_i(j) on the in-order tensor pipe
@@ -1537,10 +1573,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 slot_lo[i] = (causal && p.window > 0) ? s.P + qe - p.window : INT_MIN / 2;
             }
             const int hrow = u.kvh * G + r % G;
+            const int flags = kTwo ? value_flags(p, u, s, np) : 0;
             float m[kSlots] = {-INFINITY, -INFINITY}, l[kSlots] = {0.f, 0.f};
             int cnt[kSlots] = {0, 0};  // this unit's tiles per slot
             bool ok = true;
+            bool next_half = kTwo && value_half(p, flags, tile_at(ug, 0), np);
             for (int j = 0; j < ug.ntiles && ok; ++j) {
+                const bool half_v = next_half;
+                next_half = kTwo && value_half(p, flags, tile_at(ug, j + 1), np);
 #pragma unroll
                 for (int i = 0; i < kSlots; ++i) {
                     const bool in = alt ? (j & 1) == i : (j >= ug.a[i] && j < ug.b[i]);
@@ -1606,13 +1646,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     float alpha = 1.f;
                     bool rescale = false;
                     if (cnt[i] == 0) {
-                        m[i] = m_new;
+                        m[i] = m_new - kLead;
                     } else {
-                        const bool need = m_new > m[i] + 8.f;
+                        const bool need = m_new > m[i] + (8.f + kLead);
                         rescale = __any_sync(0xffffffffu, need);
                         if (need) {
-                            alpha = ex2(m[i] - m_new);
-                            m[i] = m_new;
+                            const float m_next = m_new - kLead;
+                            alpha = ex2(m[i] - m_next);
+                            m[i] = m_next;
                         }
                     }
                     const float m_use = m[i] == -INFINITY ? 0.f : m[i];
@@ -1620,20 +1661,27 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                     // columns at 32 h (over S columns the pair has read)
                     const float2 sl2v = make_float2(sl2, sl2), negm = make_float2(-m_use, -m_use);
                     float2 sum2 = make_float2(0.f, 0.f);
+                    // (two loops: a choice in one takes 10 us of 80 more)
+                    auto weights = [&](auto as_half) {
 #pragma unroll
-                    for (int c4 = 0; c4 < 2; ++c4) {
-                        uint32_t pk[16];
+                        for (int c4 = 0; c4 < 2; ++c4) {
+                            uint32_t pk[16];
 #pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            const float2 a =
-                                __ffma2_rn(make_float2(sv[c4 * 32 + 2 * q], sv[c4 * 32 + 2 * q + 1]), sl2v, negm);
-                            const float p0 = ex2(a.x);
-                            const float p1 = ex2(a.y);
-                            sum2 = __fadd2_rn(sum2, make_float2(p0, p1));
-                            pk[q] = pack_bf16(p0, p1);
+                            for (int q = 0; q < 16; ++q) {
+                                const float2 a =
+                                    __ffma2_rn(make_float2(sv[c4 * 32 + 2 * q], sv[c4 * 32 + 2 * q + 1]), sl2v, negm);
+                                const float p0 = ex2(a.x);
+                                const float p1 = ex2(a.y);
+                                sum2 = __fadd2_rn(sum2, make_float2(p0, p1));
+                                pk[q] = decltype(as_half)::value ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+                            }
+                            tmem_st16(s_col + half * (kHalfCols / 2) + c4 * 16, pk);
                         }
-                        tmem_st16(s_col + half * (kHalfCols / 2) + c4 * 16, pk);
-                    }
+                    };
+                    if (kTwo && half_v)
+                        weights(std::true_type());
+                    else
+                        weights(std::false_type());
                     l[i] = l[i] * alpha + (sum2.x + sum2.y);
                     if (rescale) {
                         if constexpr (kHalfD >= 32) {
@@ -1828,9 +1876,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
             const int row_lo = (causal && p.window > 0) ? s.P + tok - p.window + 1 : INT_MIN / 2;
             const int slot_lo = (causal && p.window > 0) ? s.P + qe - p.window : INT_MIN / 2;
             const int np = ug.np;
+            const int flags = kTwo ? value_flags(p, u, s, np) : 0;
             float m = -INFINITY, l = 0.f;
             bool ok = true;
+            bool next_half = kTwo && value_half(p, flags, tile_at(ug, ug.a[slot]), np);
             for (int j = 0; j < nt; ++j) {
+                const bool half_v = next_half;
+                next_half = kTwo && value_half(p, flags, tile_at(ug, ug.a[slot] + j + 1), np);
                 if (!warp_wait(&ctl->s_full[slot], (ns + j) & 1, ctl, hdr)) { ok = false; break; }
                 tc_fence_after();
                 // S_slot(j) is complete, and with it every earlier MMA of this
@@ -1909,13 +1961,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 float alpha = 1.f;
                 bool rescale = false;
                 if (j == 0) {
-                    m = m_new;
+                    m = m_new - kLead;
                 } else {
-                    const bool need = m_new > m + 8.f;
+                    const bool need = m_new > m + (8.f + kLead);
                     rescale = __any_sync(0xffffffffu, need);
                     if (need) {
-                        alpha = ex2(m - m_new);
-                        m = m_new;
+                        const float m_next = m_new - kLead;
+                        alpha = ex2(m - m_next);
+                        m = m_next;
                     }
                 }
                 const float m_use = m == -INFINITY ? 0.f : m;
@@ -1930,27 +1983,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_fwd_kernel(const __grid_cons
                 // the product for those, 930, and the others up to 3 % slower)
                 const float4* const vsc = reinterpret_cast<const float4*>(vscale_slot(tc));
                 const bool coded = jt < np;
+                auto weights = [&](auto as_half) {
 #pragma unroll
-                for (int c4 = 0; c4 < 4; ++c4) {
-                    uint32_t pk[16];
-                    float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
+                    for (int c4 = 0; c4 < 4; ++c4) {
+                        uint32_t pk[16];
+                        float4 f = make_float4(1.f, 1.f, 1.f, 1.f);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 a = __ffma2_rn(make_float2(sv[c4 * 32 + 2 * i], sv[c4 * 32 + 2 * i + 1]), sl2v, negm);
-                        const float p0 = ex2(a.x);
-                        const float p1 = ex2(a.y);
-                        sum2 = __fadd2_rn(sum2, make_float2(p0, p1));
-                        if constexpr (kVScale) {
-                            if (i % 2 == 0 && coded) f = vsc[c4 * 8 + i / 2];
-                            const float2 ps =
-                                __fmul2_rn(make_float2(p0, p1), i % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
-                            pk[i] = pack_bf16(ps.x, ps.y);
-                        } else {
-                            pk[i] = pack_bf16(p0, p1);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 a = __ffma2_rn(make_float2(sv[c4 * 32 + 2 * i], sv[c4 * 32 + 2 * i + 1]), sl2v, negm);
+                            const float p0 = ex2(a.x);
+                            const float p1 = ex2(a.y);
+                            sum2 = __fadd2_rn(sum2, make_float2(p0, p1));
+                            if constexpr (kVScale) {
+                                if (i % 2 == 0 && coded) f = vsc[c4 * 8 + i / 2];
+                                const float2 ps =
+                                    __fmul2_rn(make_float2(p0, p1), i % 2 ? make_float2(f.z, f.w) : make_float2(f.x, f.y));
+                                pk[i] = pack_bf16(ps.x, ps.y);
+                            } else {
+                                pk[i] = decltype(as_half)::value ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+                            }
                         }
+                        tmem_st16(s_col + c4 * 16, pk);
                     }
-                    tmem_st16(s_col + c4 * 16, pk);
-                }
+                };
+                if (kTwo && half_v)
+                    weights(std::true_type());
+                else
+                    weights(std::false_type());
                 l = l * alpha + (sum2.x + sum2.y);
                 if (rescale) {
 #pragma unroll

@@ -8,6 +8,8 @@
 // positions and table entries are looked up once a block, in shared memory.  A block
 // looks whether its sequences' tables are valid itself: a kernel ahead for that
 // costs a small call more than all of it.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "cache4.cuh"
@@ -192,6 +194,24 @@ __device__ __forceinline__ void store32(uint4* to, const uint4 (&x)[2], bool ali
         to[0] = x[0], to[1] = x[1];
 }
 
+// The values of 16 channels in fp16.
+__device__ __forceinline__ void expand16_half(const uint2& codes, uint32_t word, uint4 (&out)[2]) {
+    const float s = bf16_lo(word), m = bf16_hi(word);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t c = half ? codes.y : codes.x;
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float a = __uint_as_float(0x4b000000u | ((c >> (8 * e)) & 15u)) - 8388608.f;
+            const float b = __uint_as_float(0x4b000000u | ((c >> (8 * e + 4)) & 15u)) - 8388608.f;
+            const __half2 v = __floats2half2_rn(fmaf(a, s, m), fmaf(b, s, m));
+            w[e] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        out[half] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 // The values of 16 channels as sums of two bf16 terms (to 2^-17 of their size: keys, whose scores
 // go through an exponential).
 __device__ __forceinline__ void expand16_two(const uint2& codes, uint32_t word, uint4 (&one)[2], uint4 (&two)[2]) {
@@ -313,10 +333,24 @@ __global__ void __launch_bounds__(kCopyThreads, 4) expand4_kernel(const Expand4P
             }
         }
         const size_t at = ((size_t)kvh * p.pool_blocks + block) * kBlock4 * D;
+        // Values are rounded to fp16, an eighth of bf16's error, where the block's largest are within
+        // its range with room for smaller ones (below 2^-14 they are off by 2^-25).
+        bool half = false;
+        if (h >= Hk) {
+            bool fits = true, large = false;
+#pragma unroll
+            for (int i = 0; i < kPasses; ++i) {
+                const float top = fabsf(bf16_hi(word[i])) + 15.f * bf16_lo(word[i]);
+                fits = fits && top <= 0x1p15f;
+                large = large || top >= 0x1p-6f;
+            }
+            half = __syncthreads_and(fits) && __syncthreads_or(large);
+            if (threadIdx.x == 0) p.halves[(size_t)kvh * p.pool_blocks + block] = half;
+        }
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
             const int r = i * kStep + first;
-            if (r >= kBlock4 || owner.y + r >= P) continue;  // (positions below 0 expand to zeros)
+            if (r >= kBlock4) continue;  // (positions below 0 expand to zeros)
             const size_t to = at + (size_t)r * D + 16 * part;
             uint4 one[2], two[2];
             if (h < Hk) {
@@ -324,7 +358,10 @@ __global__ void __launch_bounds__(kCopyThreads, 4) expand4_kernel(const Expand4P
                 store32(reinterpret_cast<uint4*>(p.k + to), one, true);  // (the pool is the workspace's)
                 store32(reinterpret_cast<uint4*>(p.k2 + to), two, true);
             } else {
-                expand16(codes[i], word[i], one);
+                if (half)
+                    expand16_half(codes[i], word[i], one);
+                else
+                    expand16(codes[i], word[i], one);
                 store32(reinterpret_cast<uint4*>(p.v + to), one, true);
             }
         }

@@ -82,11 +82,14 @@ cudaError_t encode_fwd_maps(FwdParams& p, const void* q, int total_q, int num_se
 cudaError_t launch_attn_fwd(const FwdParams& p, int head_dim, int grid, cudaStream_t st);
 
 // Cached keys in two bf16 terms (k + k2 to 2^-17 of their size) and values, expanded from a 4-bit
-// cache: position x of sequence b is row base[b] + x of a pool [n_kv_heads][rows][head_dim] (base[b]
-// - 128 .. base[b] - 1 are zeros where tiles that end at its last position begin below 0).
+// cache: position x of sequence b is row base[b] + x of a pool [n_kv_heads][pool_blocks * 128][head_dim],
+// where the tiles that end at its last position are whole blocks (zeros below position 0).  A block's
+// values are fp16 where halves[kv head][block] is not 0, else bf16.
 struct FwdParamsTwo : FwdParams {
     CUtensorMap tm_ck2;  // as tm_ck
     const int* base;
+    const uint8_t* halves;
+    int pool_blocks;
 };
 cudaError_t encode_pool_maps(FwdParamsTwo& p, int head_dim, const __nv_bfloat16* k, const __nv_bfloat16* k2,
                              const __nv_bfloat16* v, long long rows);
@@ -230,12 +233,13 @@ struct Expand4Params {
     int window;
     int pool_blocks;
     int* taken;       // [num_seqs] 0: not taken
-    int* base;        // [num_seqs] the pool's row of a taken sequence's position 0
+    int* base;        // [num_seqs] the pool's row of a taken sequence's position 0 (below 0 where the pool begins later)
     int2* owners;     // [pool_blocks] sequence and first position
     int* blocks;      // in use
     __nv_bfloat16* k;
     __nv_bfloat16* k2;
-    __nv_bfloat16* v;
+    __nv_bfloat16* v;  // or fp16:
+    uint8_t* halves;   // [n_kv_heads][pool_blocks] whether a block's values are
     Copy4Params write;            // the call's new tokens, written by the same launch
     int expanders, write_blocks;  // blocks that expand, blocks of tokens to write (set by the launch)
 };

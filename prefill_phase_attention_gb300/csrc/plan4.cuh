@@ -6,14 +6,14 @@
 
 namespace pa {
 
-// The blocks [first, end) of a sequence's positions that the attention kernel reads: whole tiles that
-// end at its last cached one, so from up to 127 positions ahead of a window on, or from below 0:
-// block -1 is of zeros.
+// The attention kernel's tiles of a sequence's cached positions, which are the pool's blocks: [first,
+// end) of them, the last one ends at position P - 1, so that block 0 may begin below 0.
+__device__ __forceinline__ int end_block(const SeqInfo& s) { return (s.P + kBlock4 - 1) / kBlock4; }
+__device__ __forceinline__ int block_start(const SeqInfo& s, int i) { return s.P - (end_block(s) - i) * kBlock4; }
 __device__ __forceinline__ int first_block(const Expand4Params& p, const SeqInfo& s) {
-    const int first = p.window > 0 ? max(0, s.P - p.window + 2 - kBlock4) / kBlock4 : 0;
-    return first > 0 ? first : -1;
+    const int oldest = p.window > 0 ? max(0, s.P - p.window + 1) : 0;  // key that a query sees
+    return (oldest - block_start(s, 0)) / kBlock4;
 }
-__device__ __forceinline__ int end_block(const SeqInfo& s) { return s.P > 0 ? (s.P + kBlock4 - 1) / kBlock4 : -1; }
 
 // Checks the sequences, and lays out the pool (one block of 1024 threads; ends with a barrier).
 __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
@@ -46,7 +46,7 @@ __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
         const bool wanted = s.n > p.few_tokens;
         const int first = first_block(p, s);
         // (sums past the pool saturate: a sequence's blocks are at most 2^23)
-        int need = wanted ? max(0, end_block(s) - first) : 0, inc = need;
+        int need = wanted ? end_block(s) - first : 0, inc = need;
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc = min(inc + y, 1 << 29);
@@ -62,7 +62,7 @@ __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
         const bool fits = wanted && before + inc < 1 << 29 && at + need <= p.pool_blocks;
         if (b < p.seqs.num_seqs) {
             p.taken[b] = fits;
-            p.base[b] = (at - first) * kBlock4;
+            p.base[b] = at * kBlock4 - block_start(s, first);
         }
         if (fits) atomicMax(&in_use, at + need);  // (those that fit are the first ones: no gaps)
         __syncthreads();
@@ -71,8 +71,8 @@ __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
     for (int b = warp; b < p.seqs.num_seqs; b += 32) {
         if (!p.taken[b]) continue;
         const SeqInfo s = p.seqs.checked[b];
-        const int first = first_block(p, s), end = end_block(s), at = p.base[b] / kBlock4 + first;
-        for (int i = first + lane; i < end; i += 32) p.owners[at + i - first] = make_int2(b, i * kBlock4);
+        const int first = first_block(p, s), end = end_block(s), at = (p.base[b] + block_start(s, first)) / kBlock4;
+        for (int i = first + lane; i < end; i += 32) p.owners[at + i - first] = make_int2(b, block_start(s, i));
     }
     __threadfence_block();
     __syncthreads();

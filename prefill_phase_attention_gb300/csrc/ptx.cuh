@@ -246,6 +246,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn, in
            | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
            | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
 }
+// The same with A and B fp16 (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+    return idesc_bf16_f32(M, N, a_mn, b_mn) & ~(1u << 7 | 1u << 10);
+}
 
 }  // namespace ptx
 // Programmatic dependent launch (sm_90+): a kernel launched with programmatic

@@ -10,8 +10,9 @@ u |v_j| for a new one.  Weights are scaled so that a row's largest is at least 2
 range are off by 2^-25 absolutely, 2^-32 of the largest p s, 15 times as much in O, each.
 
 The tile kernel's cached keys are sums of two bf16 terms, off by at most 2^-16, which is as much of
-scale sum_i |q_i| |k_i| in a score; it rounds cached values and p to bf16, and O is off by u sum_j P_j |v_j| for
-each.
+scale sum_i |q_i| |k_i| in a score.  Cached values and their p are rounded to fp16, 2^-11 each, where a tile's values
+are within its range, else to bf16 like a new token's p; values below 2^-14 are off by 2^-25.  A bound of a call
+says which (halves); weights below 2^-14 are 2^-21 of the largest at least, off by 2^-32 of it.
 
 Both round out once.  fp32: a score is a sum of d / 16 products of 16 channels and d / 32 parameter terms,
 each sum off by at most 2^-22 of what it sums up: together 2^-18 of A = scale sum_i |q_i| (|m_i| + c_i s_i), which
@@ -112,8 +113,9 @@ def rotate(x, pos, theta):
     return torch.cat([lo * c - hi * s, hi * c + lo * s], -1)
 
 
-def attention(cache, q, k, v, cu, lens, scale, causal=True, window=0, tiles=False):
-    """(out, lse, bound on out's error, bound on lse's) in 64 bits.  tiles: the bounds of the tile kernel too."""
+def attention(cache, q, k, v, cu, lens, scale, causal=True, window=0, tiles=False, halves=True):
+    """(out, lse, bound on out's error, bound on lse's) in 64 bits.  tiles: the bounds of the tile kernel too; halves:
+    every tile's cached values are within fp16's range."""
     t, heads, d = q.shape
     hk = k.shape[1]
     g = heads // hk
@@ -150,7 +152,10 @@ def attention(cache, q, k, v, cu, lens, scale, causal=True, window=0, tiles=Fals
             mean = torch.einsum("igj,jd->igd", w, val.abs())
             r = torch.einsum("igj,jd->igd", w, step) + 2.0 ** -18 * torch.einsum("igj,jd->igd", w, vparts)
             r = r + 15 * 2.0 ** -32 * (p + n) * (w[..., None] * least).amax(2)
-            if tiles:
+            if tiles and halves:
+                fine = torch.where(j[:, None] < p, 2 * 2.0 ** -11 * val.abs() + 2.0 ** -25, U * val.abs())
+                r = r + torch.einsum("igj,jd->igd", w, fine) + 2.0 ** -32 * (p + n) * val.abs().amax() * w.amax(-1)[..., None]
+            elif tiles:
                 r = r + 2 * U * mean
             out[rows, h * g:(h + 1) * g] = o
             lse[rows, h * g:(h + 1) * g] = z

@@ -90,11 +90,11 @@ class Call:
             assert same_bits(self.codes[which][1], codes[which]), "codes"
             assert same_bits(self.params[which][1], params[which]), "parameters"
 
-    def check(self, causal=True, window=0, tiles=False):
+    def check(self, causal=True, window=0, tiles=False, halves=True):
         torch.cuda.synchronize()
         assert binding.prefill_attn_device_status() == 0
         out, lse, bound, lbound = R.attention(self.cache, self.q, self.k, self.v, self.cu, self.lens, self.scale, causal,
-                                              window, tiles)
+                                              window, tiles, halves)
         t = self.cu[-1]
         assert self.out[1][t:].isnan().all() and self.lse[1][t:].isnan().all(), "rows behind the last sequence"
         got, glse = self.out[1][:t].double().cpu(), self.lse[1][:t].double().cpu()
@@ -220,6 +220,22 @@ def test_one_chunk_under_a_window(window, past):
     c.check(window=window, tiles=True)
 
 
+@pytest.mark.parametrize("block", [0, 16])
+def test_chunks_over_values_of_any_size(block):
+    """Tiles whose values are outside fp16's range (large, or all tiny) beside such as are inside it, in each sequence."""
+    c = Call(15, [300, 129, 400], [700, 129, 128], d=64, group=32, block=block)
+    slots = torch.arange(c.cache.codes[1].shape[0])
+    size = torch.exp2(torch.tensor([0.0, 20.0, -20.0, 90.0, -9.0])[slots % 5 if block else slots % 2 * 2])
+    x = c.cache.params[1].double() * size[:, None, None, None, None]
+    if not block:
+        x[0, :, 200:400] *= 2.0 ** 30
+        x[2, :, :1] *= 2.0 ** 30
+    c.cache.params[1] = x.to(torch.bfloat16)
+    c.params[1][1].copy_(c.cache.params[1])
+    c.attend()
+    c.check(tiles=True, halves=False)
+
+
 def test_chunks_with_all_keys_visible():
     c = Call(14, [460, 1, 150], [100, 300, 10], group=128)
     c.attend(causal=False)
@@ -281,7 +297,7 @@ def test_values_of_very_different_size(new):
     c.q *= 6
     c.dev[0].copy_(c.q)
     c.attend()
-    c.check(tiles=max(new) > 16)
+    c.check(tiles=max(new) > 16, halves=False)
 
 
 def test_equal_inputs_give_equal_bits():
