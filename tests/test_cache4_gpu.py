@@ -75,6 +75,7 @@ class Call:
     def attend(self, **kw):
         binding.prefill_attn_varlen_cache4(*self.dev, *self.meta, self.codes[0][1], self.codes[1][1], self.offsets,
                                            self.out[1], self.lse[1], scale=self.scale, **self.opts, **kw)
+        self.expanded = binding.load().prefill_attn_last_schedule() != 0  # (the row kernel has no schedule)
 
     def write(self, **kw):
         binding.prefill_attn_cache4_write(*self.dev[1:], self.meta[0], self.codes[0][1], self.codes[1][1], self.offsets,
@@ -137,18 +138,19 @@ def test_drafts(d, group, new, lens):
 @pytest.mark.parametrize("d,group", DIMS)
 def test_chunks(d, group, block):
     """Chunks long enough for the tile kernel, decode rows and drafts beside them."""
-    c = Call(11, [300, 1, 129, 4, 0, 200], [0, 500, 127, 33, 9, 260], d, group=group, block=block, share=2)
+    c = Call(11, [300, 1, 129, 4, 0, 200], [0, 500, 127, 33, 9, 260], d, hk=1, group=group, block=block, share=16)
     c.attend()
+    assert c.expanded
     c.check(tiles=True)
 
 
 @pytest.mark.parametrize("new,past,hk,share", [(9, 200, 2, 4), (40, 3, 1, 1), (64, 128, 1, 3), (513, 1000, 4, 4), (130, 0, 3, 16),
-                                               (257, 129, 2, 1)])
+                                               (257, 129, 2, 1), (300, 200, 8, 1), (70, 250, 1, 48)])
 @pytest.mark.parametrize("block", [0, 32])
 def test_one_chunk(new, past, hk, share, block):
     c = Call(12, [new], [past], hk=hk, share=share, group=64, block=block)
     c.attend()
-    c.check(tiles=True)
+    c.check(tiles=c.expanded)
 
 
 def test_more_long_chunks_than_the_pool_holds():
@@ -190,9 +192,9 @@ def test_more_long_chunks_than_the_pool_holds():
 @pytest.mark.parametrize("new,pad", [([1, 3], 7), ([5], 600), ([130], 70), ([0], 300), ([300, 1, 129], 200), ([2, 3, 1], 900)])
 def test_rows_behind_the_last_sequence(new, pad):
     """What a replayed call over fewer tokens than it was captured for has: they are left as they were."""
-    c = Call(18, new, [100, 257, 31][:len(new)], group=64, pad=pad)
+    c = Call(18, new, [100, 257, 31][:len(new)], share=8, group=64, pad=pad)
     c.attend()
-    c.check(tiles=True)
+    c.check(tiles=c.expanded)
     w = Call(19, new, [100, 257, 31][:len(new)], group=64, pad=pad)
     w.write()
     w.check_cache()
@@ -208,22 +210,24 @@ def test_rows_behind_the_last_sequence(new, pad):
 @pytest.mark.parametrize("window", [1, 100, 128, 300])
 @pytest.mark.parametrize("block", [0, 16])
 def test_chunks_under_windows(window, block):
-    c = Call(13, [460, 1, 150], [400, 300, 10], group=32, block=block)
+    c = Call(13, [460, 1, 150], [400, 300, 10], hk=1, share=16, group=32, block=block)
     c.attend(window=window)
+    assert c.expanded
     c.check(window=window, tiles=True)
 
 
 @pytest.mark.parametrize("window,past", [(129, 1000), (130, 1024), (257, 1025), (385, 1151), (5000, 1023)])
 def test_one_chunk_under_a_window(window, past):
-    c = Call(16, [200], [past], hk=1, share=4, group=64, block=32)
+    c = Call(16, [200], [past], hk=1, share=16, group=64, block=32)
     c.attend(window=window)
+    assert c.expanded
     c.check(window=window, tiles=True)
 
 
 @pytest.mark.parametrize("block", [0, 16])
 def test_chunks_over_values_of_any_size(block):
     """Tiles whose values are outside fp16's range (large, or all tiny) beside such as are inside it, in each sequence."""
-    c = Call(15, [300, 129, 400], [700, 129, 128], d=64, group=32, block=block)
+    c = Call(15, [300, 129, 400], [700, 129, 128], d=64, hk=1, share=16, group=32, block=block)
     slots = torch.arange(c.cache.codes[1].shape[0])
     size = torch.exp2(torch.tensor([0.0, 20.0, -20.0, 90.0, -9.0])[slots % 5 if block else slots % 2 * 2])
     x = c.cache.params[1].double() * size[:, None, None, None, None]
@@ -233,12 +237,14 @@ def test_chunks_over_values_of_any_size(block):
     c.cache.params[1] = x.to(torch.bfloat16)
     c.params[1][1].copy_(c.cache.params[1])
     c.attend()
+    assert c.expanded
     c.check(tiles=True, halves=False)
 
 
 def test_chunks_with_all_keys_visible():
-    c = Call(14, [460, 1, 150], [100, 300, 10], group=128)
+    c = Call(14, [460, 1, 150], [100, 300, 10], hk=1, share=16, group=128)
     c.attend(causal=False)
+    assert c.expanded
     c.check(causal=False, tiles=True)
 
 
@@ -300,6 +306,61 @@ def test_values_of_very_different_size(new):
     c.check(tiles=max(new) > 16, halves=False)
 
 
+@pytest.mark.parametrize("new", [[1, 3], [1100, 1]])
+def test_pools_past_4_gib(new):
+    """Blocks whose codes begin past 2^32 bytes: the same bits as in a small pool."""
+    c = Call(70, new, [700, 40], hk=8, share=1, block=16)
+    blocks = 2 ** 32 // (8 * 16 * 64) + 5
+    small = [x[1].clone() for x in c.codes + c.params]
+    big = [torch.empty((blocks + x.shape[0], *x.shape[1:]), dtype=x.dtype, device="cuda") for x in small]
+    for x, y in zip(big, small):
+        x[blocks:] = y
+    c.attend()
+    out, lse = c.out[1].clone(), c.lse[1].clone()
+    c.opts.update(cache_k_params=big[2], cache_v_params=big[3], block_table=c.opts["block_table"] + blocks)
+    c.codes[:2] = [(None, big[0]), (None, big[1])]
+    c.attend()
+    torch.cuda.synchronize()
+    assert binding.prefill_attn_device_status() == 0
+    assert same_bits(c.out[1], out) and same_bits(c.lse[1], lse)
+    codes, params = c.cache.stored(c.k, c.v, c.cu, c.lens)
+    for which in range(2):
+        assert same_bits(big[which][blocks:], codes[which]) and same_bits(big[2 + which][blocks:], params[which])
+    k, v = torch.empty_like(c.dev[1]), torch.empty_like(c.dev[2])
+    c.write()
+    binding.prefill_attn_cache4_read(big[0], big[1], c.meta[0], c.offsets, k, v, **c.opts)
+    for which, (got, x) in enumerate(((k, c.k), (v, c.v))):
+        assert same_bits(big[which][blocks:], codes[which])
+        assert same_bits(got, R.values(*R.quantise(x, 128)).float().to(torch.bfloat16))
+
+
+def test_slots_past_4_gib():
+    """The same of contiguous slots."""
+    cap = 5 * 2 ** 20
+    c = Call(71, [1, 3], [0, 700], hk=8, share=1)
+    big = [torch.empty((2, 8, cap, *x[1].shape[3:]), dtype=x[1].dtype, device="cuda") for x in c.codes + c.params]
+    for x, y in zip(big, c.codes + c.params):
+        x[:, :, :y[1].shape[2]] = y[1]
+    c.attend()
+    out, lse = c.out[1].clone(), c.lse[1].clone()
+    codes, params = c.cache.stored(c.k, c.v, c.cu, c.lens)
+    c.opts.update(cache_k_params=big[2], cache_v_params=big[3])
+    c.codes[:2] = [(None, big[0]), (None, big[1])]
+    for call in (c.attend, c.write):
+        for x, y in zip(big, c.cache.codes + c.cache.params):
+            x[:, :, :y.shape[2]] = y.cuda()
+        call()
+        torch.cuda.synchronize()
+        for which in range(2):
+            n = codes[which].shape[2]
+            assert same_bits(big[which][:, :, :n], codes[which]) and same_bits(big[2 + which][:, :, :n], params[which])
+    assert same_bits(c.out[1], out) and same_bits(c.lse[1], lse)
+    k, v = torch.empty_like(c.dev[1]), torch.empty_like(c.dev[2])
+    binding.prefill_attn_cache4_read(big[0], big[1], c.meta[0], c.offsets, k, v, **c.opts)
+    for got, x in ((k, c.k), (v, c.v)):
+        assert same_bits(got, R.values(*R.quantise(x, 128)).float().to(torch.bfloat16))
+
+
 def test_equal_inputs_give_equal_bits():
     outs = []
     for _ in range(3):
@@ -315,15 +376,16 @@ def test_equal_inputs_give_equal_bits():
 def test_rotary(block, new):
     """The attention call's rotary embedding: q and the cached key as a call on rotated tensors has them."""
     theta = 10000.0
-    c = Call(10, new, [100, 257, 0], group=64, block=block)
+    c = Call(10, new, [100, 257, 0], hk=1, share=16, group=64, block=block)
     c.attend(rope_theta=theta)
+    assert c.expanded == (max(new) > 100)
     rot = [torch.empty_like(x) for x in (c.q, c.k)]
     for b, p in enumerate(c.lens):
         rows = slice(c.cu[b], c.cu[b + 1])
         pos = p + torch.arange(c.new[b])
         for x, y in zip((c.q, c.k), rot):
             y[rows] = R.rotate(x[rows], pos, theta).to(torch.bfloat16)
-    e = Call(10, new, [100, 257, 0], group=64, block=block)
+    e = Call(10, new, [100, 257, 0], hk=1, share=16, group=64, block=block)
     e.q, e.k = rot
     e.dev[:2] = [x.cuda() for x in rot]
     e.attend()
@@ -333,7 +395,7 @@ def test_rotary(block, new):
     a, b = c.out[1].double().cpu(), e.out[1].double().cpu()
     assert (a - b).abs().max() <= 8 * R.U * b.abs().max()
     # the call's own write and prefill_attn_cache4_write rotate alike
-    w = Call(10, new, [100, 257, 0], group=64, block=block)
+    w = Call(10, new, [100, 257, 0], hk=1, share=16, group=64, block=block)
     w.write(rope_theta=theta)
     for which in range(2):
         assert same_bits(w.codes[which][1], c.codes[which][1]) and same_bits(w.params[which][1], c.params[which][1])
@@ -447,11 +509,12 @@ def test_bad_sequences_are_skipped():
 
 
 def test_bad_chunks_are_skipped():
-    c = Call(35, [400, 250, 1], [40, 20, 70], block=16)
+    c = Call(35, [400, 250, 1], [40, 20, 70], hk=1, share=16, block=16)
     c.opts["block_table"][1, 1] = c.cache.codes[0].shape[0]
     c.attend()
     torch.cuda.synchronize()
     assert binding.prefill_attn_device_status() == binding.DEVERR_METADATA
+    assert c.expanded
     out, _, bound, _ = R.attention(c.cache, c.q, c.k, c.v, c.cu, c.lens, c.scale, tiles=True)
     got = c.out[1].double().cpu()
     assert got[400:650].isnan().all()
@@ -491,7 +554,7 @@ def test_captured_calls_read_their_metadata_at_replay():
 
 @pytest.mark.parametrize("new", [[600], [300, 1, 129]])
 def test_captured_chunks_read_their_metadata_at_replay(new):
-    c = Call(36, new, [300, 5, 64][:len(new)], block=16)
+    c = Call(36, new, [300, 5, 64][:len(new)], hk=1, share=24, block=16)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
@@ -500,12 +563,13 @@ def test_captured_chunks_read_their_metadata_at_replay(new):
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
             c.attend()
+    assert c.expanded
     # other lengths of the same total, and fewer tokens
     for seed, fewer, lens in ((37, new[::-1], [129, 0, 300][:len(new)]), (38, [5, 2, 1][:len(new)], [200, 9, 300][:len(new)]),
                               (39, [400, 0, 1][:len(new)], [37, 300, 5][:len(new)])):
         pad = sum(new) - sum(fewer)
         cap = c.cache.table.shape[1] * 16
-        d = Call(seed, fewer, lens, block=16, pad=pad, slack=cap - max(p + n for p, n in zip(lens, fewer)))
+        d = Call(seed, fewer, lens, hk=1, share=24, block=16, pad=pad, slack=cap - max(p + n for p, n in zip(lens, fewer)))
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
             for a, b in zip(c.codes + c.params + [c.out, c.lse], d.codes + d.params + [d.out, d.lse]):
@@ -555,7 +619,7 @@ def test_read_into_tensors_that_are_16_byte_aligned():
 
 def test_threads_on_one_stream():
     """Calls of several host threads at once on one stream run one after the other."""
-    calls = [Call(60 + i, new, lens, hk=2, block=16)
+    calls = [Call(60 + i, new, lens, hk=2, share=16, block=16)
              for i, (new, lens) in enumerate([([1] * 3, [2000, 77, 500]), ([300, 1, 129], [400, 5, 64]), ([600], [100])])]
     torch.cuda.synchronize()
     stream = torch.cuda.Stream()
@@ -569,7 +633,7 @@ def test_threads_on_one_stream():
 
 @pytest.mark.parametrize("new", [[1] * 3, [300, 1, 129], [500]])
 def test_two_streams_at_once(new):
-    calls = [Call(33 + i, new, [2000, 77, 500][:len(new)], hk=2) for i in range(2)]
+    calls = [Call(33 + i, new, [2000, 77, 500][:len(new)], hk=2, share=16) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in calls]
     torch.cuda.synchronize()
     for _ in range(10):
