@@ -447,10 +447,19 @@ typedef struct pa_cache4 {
  * and values are what its codes stand for, the new tokens' are used at full
  * precision and then quantised into the cache at cache_offsets[b] (after the
  * rotary embedding, if any).  Of pa_options: window, block_table, rope_theta.
+ * q, k, v and what the cache stands for are finite and below 2^100 in magnitude.
+ * Scores are exact to fp32's rounding; cached values' weights are rounded to fp16
+ * (2^-11), and so are the values themselves in long chunks, where the largest
+ * of 128 positions' lies in [2^-6, 2^15], else to bf16; new tokens' weights are rounded to bf16.
  * Positions at or past cache_offsets[b] are not read.  What the call writes (out,
  * lse, the cache) must overlap no other buffer of it.  Under graph capture the
  * stream must already have run a call of at least these sizes.  num_seqs and
- * max_cache_len are at most 2^30.
+ * max_cache_len are at most 2^30, and a pool has less than 2^32 rows (num_blocks *
+ * n_kv_heads * block_size).
+ * Sequences of more than 2048 / n_heads new tokens may be expanded into the stream's
+ * workspace: 1 GiB, or less where max_cache_len * num_seqs needs less, or what one
+ * sequence of max_cache_len tokens takes where that is more (6 * n_kv_heads *
+ * head_dim bytes a token; max_cache_len * n_kv_heads < 2^31 then).
  */
 pa_status prefill_attn_varlen_cache4(
     const void *q, const void *k, const void *v,
