@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kCopyThreads, 4) expand4_kernel(const Expand4P
             for (int i = 0; i < kPasses; ++i) {
                 const float top = fabsf(bf16_hi(word[i])) + 15.f * bf16_lo(word[i]);
                 fits = fits && top <= 0x1p15f;
-                large = large || top >= 0x1p-6f;
+                large = large || top >= 0x1p-12f;
             }
             half = __syncthreads_and(fits) && __syncthreads_or(large);
             if (threadIdx.x == 0) p.halves[(size_t)kvh * p.pool_blocks + block] = half;
