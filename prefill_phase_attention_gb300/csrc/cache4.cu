@@ -442,4 +442,6 @@ cudaError_t launch_expand4(Expand4Params p, int head_dim, int sms, cudaStream_t 
     return launch_after(PA_CACHE4_VARIANT(head_dim, p.cache.groups, expand4_kernel), grid, kCopyThreads, stream, p);
 }
 
+#undef PA_CACHE4_VARIANT
+
 }  // namespace pa

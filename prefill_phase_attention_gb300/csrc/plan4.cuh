@@ -62,7 +62,7 @@ __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
         const bool fits = wanted && before + inc < 1 << 29 && at + need <= p.pool_blocks;
         if (b < p.seqs.num_seqs) {
             p.taken[b] = fits;
-            p.base[b] = at * kBlock4 - block_start(s, first);
+            p.base[b] = fits ? at * kBlock4 - block_start(s, first) : 0;
         }
         if (fits) atomicMax(&in_use, at + need);  // (those that fit are the first ones: no gaps)
         __syncthreads();

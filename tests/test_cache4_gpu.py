@@ -118,7 +118,7 @@ def test_decode_rows(d, group, block):
     c.check()
 
 
-@pytest.mark.parametrize("hk,share", [(1, 1), (1, 8), (3, 5), (2, 16), (1, 48), (8, 1)])
+@pytest.mark.parametrize("hk,share", [(1, 1), (1, 8), (3, 5), (2, 16), (1, 48), (1, 128), (8, 1)])
 def test_head_layouts(hk, share):
     c = Call(2, [1, 2, 1], [77, 500, 3], hk=hk, share=share, group=32)
     c.attend()
@@ -145,7 +145,7 @@ def test_chunks(d, group, block):
 
 
 @pytest.mark.parametrize("new,past,hk,share", [(9, 200, 2, 4), (40, 3, 1, 1), (64, 128, 1, 3), (513, 1000, 4, 4), (130, 0, 3, 16),
-                                               (257, 129, 2, 1), (300, 200, 8, 1), (70, 250, 1, 48)])
+                                               (257, 129, 2, 1), (300, 200, 8, 1), (70, 250, 1, 48), (40, 100, 1, 128)])
 @pytest.mark.parametrize("block", [0, 32])
 def test_one_chunk(new, past, hk, share, block):
     c = Call(12, [new], [past], hk=hk, share=share, group=64, block=block)
