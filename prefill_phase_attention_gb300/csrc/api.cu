@@ -1435,7 +1435,7 @@ pa_status read_cache4(const pa_cache4* cache, const Options& o, int head_dim, in
 // tensor-core kernel over it.  Sequences of few new tokens go the first way, the others the
 // second as far as that room reaches; few: up to kFewRows rows over all heads (one sequence,
 // D = 128, 32 heads, over 1024 / 8192 / 32768 cached tokens, us: 64 tokens 35 / 78 / 201 and 33 /
-// 111 / 448, 128 tokens 60 / 141 / 391 and 33 / 111 / 434).  The host does not know the lengths:
+// 113 / 432, 128 tokens 60 / 141 / 391 and 33 / 113 / 465).  The host does not know the lengths:
 // where all rows but one token of each sequence are at most kExcessRows, the row kernel takes
 // every sequence, which costs less than the other way's launches.
 constexpr int kFewRows = 2048, kExcessRows = 8192;
