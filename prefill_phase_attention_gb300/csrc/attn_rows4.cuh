@@ -79,9 +79,14 @@ struct Cfg {
     static_assert(2 * kWarps <= 32, "a lane per record");
 };
 
+// A sequence (n = 0: another kernel's, or skipped).
+struct Seq {
+    int q_start, n, P;  // as in SeqInfo
+};
+
 // A row block in a warp's share.
 struct Item {
-    SeqInfo s;
+    Seq s;
     int b, kvh, block;
     int tiles;                // of the row block
     int start_hi, start_lo;   // list position of its first
@@ -114,11 +119,9 @@ struct Extent {
     __device__ __forceinline__ int places() const { return blocks > 0 ? tiles() + kBlockCost : 0; }
 };
 
-// A sequence of this kernel's (n = 0: another kernel's, or skipped).
-__device__ __forceinline__ SeqInfo sequence_of(const Rows4Params& p, int b) {
-    SeqInfo s = sequence4(p.seqs, p.cache.max_cache_len, b);
-    if (p.taken && p.taken[b]) s.n = 0;
-    return s;
+__device__ __forceinline__ Seq sequence_of(const Rows4Params& p, int b) {
+    const SeqInfo s = sequence4(p.seqs, p.cache.max_cache_len, b);
+    return Seq{s.q_start, p.taken && p.taken[b] ? 0 : s.n, s.P};
 }
 
 // x / y and the remainder; 32 bits of x are enough nearly always.
@@ -131,7 +134,7 @@ __device__ __forceinline__ long long divide(long long x, int y, int& rest) {
     return x / y;
 }
 
-__device__ __forceinline__ Extent extent(const Rows4Params& p, const SeqInfo& s) {
+__device__ __forceinline__ Extent extent(const Rows4Params& p, const Seq& s) {
     Extent e{0, 0, 0, 0};
     if (s.n == 0) return e;
     const int lo = p.causal && p.window > 0 ? max(0, s.P - p.window + 1) : 0;  // oldest key of the first token
@@ -269,7 +272,7 @@ __device__ __forceinline__ void store_lse(const Rows4Params& p, const Item& t, b
 // Where a warp is in the tile list; in shared memory, read and written where it is not
 // simply at the next whole cached tile of its row block.
 struct Walk {
-    SeqInfo s;
+    Seq s;
     Extent e;
     long long block_start;  // list position of the row block's first tile
     int b, kvh, block;      // row block: sequence, KV head, block of rows
@@ -284,7 +287,7 @@ struct Feeder {
     static constexpr int kParts = C::kRowBytes / 16;  // 16-byte parts of a row
     static constexpr int kPassRows = 32 / kParts;     // rows that the lanes copy at once
     const Rows4Params& p;
-    const SeqInfo* table;  // in shared memory, or nullptr
+    const Seq* table;  // in shared memory, or nullptr
     Walk* walk;
     Item* items;
     Tile* tiles;
@@ -299,7 +302,7 @@ struct Feeder {
     int flags;        // of the next tile: its item's slot, kFirst and kFromBefore
     unsigned rows, next_rows;  // paged: the pool's row of the lane's 8-row piece of this and the next 256 positions
 
-    __device__ __forceinline__ SeqInfo seq(int i) const {
+    __device__ __forceinline__ Seq seq(int i) const {
         return table ? table[i] : sequence_of(p, i);
     }
     // Puts the feeder at list position `first`; `start` is that of sequence b0.
@@ -497,7 +500,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     constexpr int kGroupChunks = C::kChunks / NG;  // 32-channel chunks of a group
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ SeqInfo table[kRows4Seqs];
+    __shared__ Seq table[kRows4Seqs];
+    __shared__ unsigned bad_tables[kRows4Seqs / 32];  // a bit per sequence of this CTA's share
     __shared__ Item items[kWarps][C::kStages];
     __shared__ Tile tiles[kWarps][C::kStages];
     __shared__ Walk walks[kWarps];
@@ -514,14 +518,17 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     const bool in_table = p.seqs.num_seqs <= kRows4Seqs;
     if (in_table) {
         if (tid < p.seqs.num_seqs) {
-            SeqInfo s = p.seqs.checked ? sequence_of(p, tid) : stated_sequence(p.seqs, p.cache.max_cache_len, tid);
-            s.pad = s.n < 0;  // (to be reported)
-            s.n = max(s.n, 0);
+            Seq s;
+            if (p.seqs.checked) {
+                s = sequence_of(p, tid);
+            } else {
+                const SeqInfo stated = stated_sequence(p.seqs, p.cache.max_cache_len, tid);
+                if (blockIdx.x == 0 && stated.n < 0) atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
+                s = Seq{stated.q_start, max(stated.n, 0), stated.P};
+            }
             table[tid] = s;
         }
-        if (!p.seqs.checked && blockIdx.x == 0 && tid < p.seqs.num_seqs && table[tid].pad)
-            atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
-        // from here on pad says that a sequence of this CTA's share has a bad block table
+        if (tid < kRows4Seqs / 32) bad_tables[tid] = 0;
     } else if (!p.seqs.checked && blockIdx.x == 0) {
         for (int b = tid; b < p.seqs.num_seqs; b += kThreads)
             if (stated_sequence(p.seqs, p.cache.max_cache_len, b).n < 0) atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
@@ -605,7 +612,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     // Whether a sequence is to be skipped whole because its table names a block outside the pool: the
     // CTA looks through the tables of the sequences in its share while the first tiles
     // come (a block id is clamped where it is used, so nothing faults meanwhile).
-    auto bad_table = [&](int b) -> bool { return check_tables && table[b].pad != 0; };
+    auto bad_table = [&](int b) -> bool { return check_tables && (bad_tables[b / 32] >> b % 32 & 1) != 0; };
 
     int stage = 1;  // (the first pass fills stage 0)
 #pragma unroll 1
@@ -614,14 +621,14 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
         if (i < 0) continue;
         if (i == 0 && check_tables) {
             for (int b = first_seq; b <= last_seq; ++b) {
-                const SeqInfo s = table[b];
+                const Seq s = table[b];
                 const int end = s.n > 0 ? ((s.P + s.n - 1) >> p.cache.block_log2) + 1 : 0;
                 const int32_t* entries = p.cache.block_table + (size_t)b * p.cache.max_blocks;
                 bool bad = false;
 #pragma unroll 4
                 for (int x = tid; x < end; x += kThreads) bad |= (unsigned)__ldg(entries + x) >= (unsigned)p.cache.num_blocks;
                 if (bad) {
-                    table[b].pad = 1;  // (several threads, one value)
+                    atomicOr(&bad_tables[b / 32], 1u << b % 32);
                     atomicOr(&p.seqs.hdr->error, PA_DEVERR_METADATA);
                 }
             }
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
         const uint32_t tile_u32 = ptx::smem_u32(tile);
 
         if (flags & kFirst) {
-            const SeqInfo s = t.s;
+            const Seq s = t.s;
             const int r = t.block * kRows + g;
             const bool there = r < s.n * p.group;
             const uint4* src = reinterpret_cast<const uint4*>(
