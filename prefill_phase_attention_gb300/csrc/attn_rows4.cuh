@@ -74,6 +74,9 @@ struct Cfg {
     static constexpr int kParams = kTileKeys * NG * 4;       // bytes of a tile's parameters
     static constexpr int kTileBytes = 2 * (kCodes + kParams);
     static constexpr int kStages = D == 128 ? 3 : 4;
+    // Places of a warp's row blocks: one per tile in the ring, which may each be a row block, and one
+    // for the next row block, which the feeder enters as soon as it has issued a last tile.
+    static constexpr int kItems = kStages + 1;
     static constexpr int kRecord = kRows * D * 4;  // bytes of a partial output
     static_assert(kStages * kTileBytes >= 2 * kRecord, "a warp's records end up in its ring");
     static_assert(2 * kWarps <= 32, "a lane per record");
@@ -309,7 +312,7 @@ struct Feeder {
     __device__ __forceinline__ void seek(int b0, long long start, long long first, int places) {
         left = places;
         count = key = whole_until = 0;
-        flags = (C::kStages - 1) << kSlot;
+        flags = (C::kItems - 1) << kSlot;
         if (left == 0) return;
         Walk w;
         w.b = b0;
@@ -340,7 +343,7 @@ struct Feeder {
         w.lo_most = 0;
         if (p.causal && p.window > 0)
             w.lo_most = w.s.P + min((w.block * kRows + kRows - 1) / p.group, w.s.n - 1) - p.window + 1;
-        const int slot = (flags >> kSlot) + 1 == C::kStages ? 0 : (flags >> kSlot) + 1;
+        const int slot = (flags >> kSlot) + 1 == C::kItems ? 0 : (flags >> kSlot) + 1;
         flags = slot << kSlot | kFirst | (j > 0 ? kFromBefore : 0);
         if (lane == 0)
             items[slot] = Item{w.s, w.b, w.kvh, w.block, w.e.tiles(), (int)(w.block_start >> 32), (int)w.block_start};
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ Seq table[kRows4Seqs];
     __shared__ unsigned bad_tables[kRows4Seqs / 32];  // a bit per sequence of this CTA's share
-    __shared__ Item items[kWarps][C::kStages];
+    __shared__ Item items[kWarps][C::kItems];
     __shared__ Tile tiles[kWarps][C::kStages];
     __shared__ Walk walks[kWarps];
     __shared__ Record records[kWarps][2];
@@ -1172,7 +1175,7 @@ template <int D, int NG>
 cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     using C = Cfg<D, NG>;
     constexpr int kSmem = C::kWarps * C::kStages * C::kTileBytes;
-    static_assert(kSmem <= 216 * 1024, "shared memory budget, beside the static part");
+    static_assert(kSmem <= 216 * 1024, "shared memory budget, beside the static part (11 KB)");
     static int configured_for[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);
