@@ -735,7 +735,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
         };
         auto raise = [&](const float2& top) {
             if (!__any_sync(0xffffffffu, top.x > most.x || top.y > most.y)) return;
-            float alpha[2], t[2], x[2] = {top.x, top.y};
+            float alpha[2], t[2], less_o[2], x[2] = {top.x, top.y};
             const float was[2] = {most.x, most.y}, less[2] = {neg.x, neg.y};
             const float sc[2] = {scale.x, scale.y}, t0[2] = {T.x, T.y};
 #pragma unroll
@@ -747,10 +747,11 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 const bool none = was[e] == -INFINITY;  // no key before
                 if (!none) x[e] = fmaxf(x[e], -less[e]);
                 alpha[e] = none ? 0.f : exp2_approx(-less[e] - x[e]);
-                t[e] = fminf(__fdividef(t0[e], alpha[e]), kMostT);
-                if (none || !(alpha[e] > 0x1p-100f)) t[e] = kMostT;
+                // (t / t0 is 1 / alpha at most, which is finite: alpha is 2^-126 at least, or 0)
+                t[e] = alpha[e] == 0.f ? kMostT : fminf(__fdividef(t0[e], alpha[e]), kMostT);
+                less_o[e] = alpha[e] == 0.f ? 0.f : alpha[e] * (t[e] / t0[e]);
             }
-            scale_o(alpha[0] * (t[0] / t0[0]), alpha[1] * (t[1] / t0[1]));
+            scale_o(less_o[0], less_o[1]);
             T = make_float2(t[0], t[1]);
             l.x *= alpha[0], l.y *= alpha[1];
 #pragma unroll

@@ -45,3 +45,48 @@ def test_many_rows_without_cached_keys(d, group, seqs, block, past, window):
     c.attend(window=window)
     assert not c.expanded
     c.check(window=window)
+
+
+# ---------------------------------------------------------------------------
+# magnitudes
+# ---------------------------------------------------------------------------
+
+def shared_rows(seed, d=128, group=128, past=8192, seqs=16):
+    """A call whose warps have shares of some 27 tiles: what one tile of a row block leaves meets the next ones."""
+    return Call(seed, [1] * seqs, [past] * seqs, d, hk=2, share=64, group=group)
+
+
+def scaled(c, which, factor):
+    """Multiplies the parameters of a call's cached keys (0) or values (1)."""
+    c.cache.params[which] = (c.cache.params[which].double() * factor).to(torch.bfloat16)
+    c.params[which][1].copy_(c.cache.params[which])
+
+
+def raised(c, nats):
+    """Every 8th tile of 32 keys scores `nats` higher on average: queries are positive, the keys' minima grow by one
+    number."""
+    c.q = c.q.abs()
+    c.dev[0].copy_(c.q)
+    up = nats / (c.q.double().sum(-1).mean() * c.scale)
+    later = torch.arange(c.cache.cap) // 32 % 8 == 7
+    c.cache.params[0][..., 1] = (c.cache.params[0][..., 1].double() + up * later[:, None]).to(torch.bfloat16)
+    c.params[0][1].copy_(c.cache.params[0])
+    return later
+
+
+@pytest.mark.parametrize("d,group", DIMS)
+@pytest.mark.parametrize("nats,early,late", [
+    (140, 45, 0),    # what came before the jump is 2^-157 of what comes after it
+    (80, 60, 0),     # 2^-55
+    (80, 90, -20),   # about as much
+    (75, 90, 90),
+    (80, -60, 40),
+])
+def test_jumps_of_the_maximum_between_values_of_any_size(d, group, nats, early, late):
+    """The score rises by more than 100 in log2 units within a warp's share, values before and after differ by powers of 2."""
+    c = shared_rows(3, d, group)
+    later = raised(c, nats)
+    scaled(c, 1, torch.where(later, 2.0 ** late, 2.0 ** early)[:, None, None].double())
+    c.attend()
+    assert not c.expanded
+    c.check()
