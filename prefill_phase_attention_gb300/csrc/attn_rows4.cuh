@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
             // its largest channel goes to [2^14, 2^15)
             const int up = min(268 - (int)(top1 >> 7), 253);
             const float f = __int_as_float(up << 23);
-            const float un = __int_as_float((254 - up) << 23) * (p.scale_log2 / kCode);
+            // (never 0: hidden keys' scores are -inf, and a query of zeros or a tiny scale leaves them so)
+            const float un = fmaxf(__int_as_float((254 - up) << 23) * (p.scale_log2 / kCode), 0x1p-126f);
             float sum[NG];
 #pragma unroll
             for (int a = 0; a < NG; ++a) sum[a] = 0.f;

@@ -90,3 +90,14 @@ def test_jumps_of_the_maximum_between_values_of_any_size(d, group, nats, early, 
     c.attend()
     assert not c.expanded
     c.check()
+
+
+@pytest.mark.parametrize("past", [7, 40, 257])
+def test_a_query_of_zeros_under_any_scale(past):
+    """scale is any finite number above 0: a query of zeros weighs every visible key alike."""
+    c = Call(4, [3, 1, 1], [past, 0, 1], hk=2, share=5, group=64)
+    c.q[:, ::2] = 0
+    c.dev[0].copy_(c.q)
+    c.scale = 1e-20
+    c.attend()
+    c.check()
