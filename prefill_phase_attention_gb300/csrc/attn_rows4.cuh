@@ -14,9 +14,9 @@
 // one shift for every four.  (With bf16 operands it is a shift, a mask and a
 // subtraction: 64 decode rows of 1024 to 16384 tokens 235 us.)  fp16's range is met by powers
 // of two: a query is scaled so that its largest channel is in [2^14, 2^15), what falls
-// below fp16 then is 2^-38 of that; and p s by a factor T per query that keeps its
-// running maximum within 2^15 (see `shrink`), and its rounding to fp16 is the one
-// that there is.
+// below fp16 then is 2^-38 of that (2^-34 for odd codes' channels); and p s by a factor T per
+// query and group that keeps its running maximum within 2^15 (see `shrink`): its rounding to fp16,
+// 2^-11 or 2^-32 of the largest p s of the group so far, is the one that there is.
 //
 // What bounds it is HBM: 68 bytes of key or value (d = 128, one group) feed 8 rows, where
 // 128-row MMA tiles would be 15/16 empty and want the codes expanded through shared
@@ -108,10 +108,7 @@ enum : int {
     kSlot = 8,       // shift
 };
 
-struct Record {
-    Item t;
-    int valid;  // 0: none; 1: kept in global memory; 2: in the ring
-};
+enum : uint8_t { kNoRecord, kKept, kInRing };  // a warp's record: none, in global memory, in the ring
 
 // Tiles of the list that a sequence's row blocks have.
 struct Extent {
@@ -508,8 +505,10 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     __shared__ Item items[kWarps][C::kItems];
     __shared__ Tile tiles[kWarps][C::kStages];
     __shared__ Walk walks[kWarps];
-    __shared__ Record records[kWarps][2];
+    __shared__ Item records[kWarps][2];
+    __shared__ uint8_t record_kinds[kWarps][2];
     __shared__ float2 stats[kWarps][2][kRows];  // (maximum, sum) of a record's rows
+    __shared__ __align__(16) float2 factors[NG > 1 ? kWarps : 1][4][NG];
     __shared__ long long warp_sums[kWarps];
     __shared__ long long start_of_first;
     __shared__ int first_seq, last_seq;
@@ -587,7 +586,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
             before += total;
         }
     }
-    if (tid < 2 * kWarps) records[tid / 2][tid % 2].valid = 0;
+    if (tid < 2 * kWarps) record_kinds[tid / 2][tid % 2] = kNoRecord;
     __syncthreads();
 
     // ---- this warp's share
@@ -610,7 +609,29 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     float2 l;                    // sum of p over this lane's keys
     float2 scale;                // from scores as they are accumulated to log2 units
     float2 neg, most;            // less the running maximum m (log2 units; 0 before any key), (m + 8) / scale
-    float2 T;                    // factor of p s in the second product, and of O with it
+    // Factor T of p s in the second product, and of O with it, of each group: one for all would leave the
+    // weights of a group whose scales are 2^-20 of another's few bits.  They change seldom, so those
+    // of more than one group are in shared memory (64 rows over 1024 to 16384 tokens, groups of 32: 154 us;
+    // in registers, which spill, 185; one factor for all groups 157).
+    float2 T_one;
+    auto factor = [&](int a) -> float2 { return NG > 1 ? factors[NG > 1 ? warp : 0][t4][a] : T_one; };
+    auto set_factor = [&](int a, const float2& t) {  // (between two meetings of the warp)
+        if (NG == 1)
+            T_one = t;
+        else if (g == 0)
+            factors[NG > 1 ? warp : 0][t4][a] = t;
+    };
+    auto all_factors = [&](float2 (&T)[NG]) {
+        if constexpr (NG == 1) {
+            T[0] = T_one;
+        } else {
+#pragma unroll
+            for (int a = 0; a < NG; a += 2) {
+                const float4 x = *reinterpret_cast<const float4*>(&factors[warp][t4][a]);
+                T[a] = make_float2(x.x, x.y), T[a + 1] = make_float2(x.z, x.w);
+            }
+        }
+    };
 
     // Whether a sequence is to be skipped whole because its table names a block outside the pool: the
     // CTA looks through the tables of the sequences in its share while the first tiles
@@ -710,7 +731,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
             scale.y = __shfl_sync(0xffffffffu, un, 8 * t4 + 4);
             neg = l = make_float2(0.f, 0.f);
             most = both(-INFINITY);
-            T = both(kMostT);
+#pragma unroll
+            for (int a = 0; a < NG; ++a) set_factor(a, both(kMostT));
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c)
 #pragma unroll
@@ -728,17 +750,16 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
         // The running maximum, from the largest score `top` of the lane's keys: it is raised, and
         // what was summed under it scaled, only when it falls behind by more than 2^8.  O keeps
         // its size, T is what grows.
-        auto scale_o = [&](float x, float y) {
+        auto scale_o = [&](int a, float x, float y) {  // of a group's channels
 #pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
+            for (int c = 0; c < kGroupChunks; ++c)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[c][e / 4][e % 4] *= e & 1 ? y : x;
+                for (int e = 0; e < 8; ++e) o[a * kGroupChunks + c][e / 4][e % 4] *= e & 1 ? y : x;
         };
         auto raise = [&](const float2& top) {
             if (!__any_sync(0xffffffffu, top.x > most.x || top.y > most.y)) return;
-            float alpha[2], t[2], less_o[2], x[2] = {top.x, top.y};
-            const float was[2] = {most.x, most.y}, less[2] = {neg.x, neg.y};
-            const float sc[2] = {scale.x, scale.y}, t0[2] = {T.x, T.y};
+            float alpha[2], x[2] = {top.x, top.y};
+            const float was[2] = {most.x, most.y}, less[2] = {neg.x, neg.y}, sc[2] = {scale.x, scale.y};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 4));
@@ -748,23 +769,34 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 const bool none = was[e] == -INFINITY;  // no key before
                 if (!none) x[e] = fmaxf(x[e], -less[e]);
                 alpha[e] = none ? 0.f : exp2_approx(-less[e] - x[e]);
-                // (t / t0 is 1 / alpha at most, which is finite: alpha is 2^-126 at least, or 0)
-                t[e] = alpha[e] == 0.f ? kMostT : fminf(__fdividef(t0[e], alpha[e]), kMostT);
-                less_o[e] = alpha[e] == 0.f ? 0.f : alpha[e] * (t[e] / t0[e]);
             }
-            scale_o(less_o[0], less_o[1]);
-            T = make_float2(t[0], t[1]);
-            l.x *= alpha[0], l.y *= alpha[1];
 #pragma unroll
-            for (int a = 0; a < NG; ++a) om[a].x *= alpha[0], om[a].y *= alpha[1];
+            for (int a = 0; a < NG; ++a) {
+                const float2 was_t = factor(a);
+                const float t0[2] = {was_t.x, was_t.y};
+                float t[2], less_o[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    // (t / t0 is 1 / alpha at most, which is finite: alpha is 2^-126 at least, or 0)
+                    t[e] = alpha[e] == 0.f ? kMostT : fminf(__fdividef(t0[e], alpha[e]), kMostT);
+                    less_o[e] = alpha[e] == 0.f ? 0.f : alpha[e] * (t[e] / t0[e]);
+                }
+                scale_o(a, less_o[0], less_o[1]);
+                __syncwarp();
+                set_factor(a, make_float2(t[0], t[1]));
+                om[a].x *= alpha[0], om[a].y *= alpha[1];
+            }
+            __syncwarp();
+            l.x *= alpha[0], l.y *= alpha[1];
             if (x[0] != -INFINITY) neg.x = -x[0], most.x = (x[0] + 8.f) / sc[0];
             if (x[1] != -INFINITY) neg.y = -x[1], most.y = (x[1] + 8.f) / sc[1];
         };
-        // The factor T of weights that reach `top` without it: where a weight would pass kMostWeight,
+        // The factor of a group's weights that reach `top` without it: where one would pass kMostWeight,
         // the largest goes to [2^7, 2^8).
-        auto shrink = [&](const float2& top) {
+        auto shrink = [&](int a, const float2& top) {
             float t[2], x[2] = {top.x, top.y};
-            const float t0[2] = {T.x, T.y};
+            const float2 was = factor(a);
+            const float t0[2] = {was.x, was.y};
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 4));
@@ -773,8 +805,9 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 x[e] = fminf(x[e], 0x1p127f);
                 t[e] = x[e] * t0[e] > kMostWeight ? __int_as_float(min(261 - (__float_as_int(x[e]) >> 23), 227) << 23) : t0[e];
             }
-            scale_o(t[0] / t0[0], t[1] / t0[1]);
-            T = make_float2(t[0], t[1]);
+            scale_o(a, t[0] / t0[0], t[1] / t0[1]);
+            __syncwarp();
+            set_factor(a, make_float2(t[0], t[1]));
         };
 
         if (key >= 0) {
@@ -848,6 +881,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
             top.x = fmaxf(max3(sc[0].x, sc[1].x, sc[2].x), sc[3].x);
             top.y = fmaxf(max3(sc[0].y, sc[1].y, sc[2].y), sc[3].y);
             raise(top);
+            float2 T[NG];
+            all_factors(T);
             float sv[4][NG];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -869,24 +904,27 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 float most_w = 0.f;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float2 x = __fmul2_rn(sc[k], T);
 #pragma unroll
                     for (int a = 0; a < NG; ++a) {
-                        const float wx = x.x * sv[k][a], wy = x.y * sv[k][a];
-                        most_w = max3(most_w, wx, wy);
-                        pt[a][k] = pack_half(wx, wy);
+                        const float2 x = __fmul2_rn(sc[k], T[a]);
+                        const float2 w = make_float2(x.x * sv[k][a], x.y * sv[k][a]);
+                        most_w = max3(most_w, w.x, w.y);
+                        pt[a][k] = pack_half(w.x, w.y);
                     }
                 }
                 if (pass > 0 || !__any_sync(0xffffffffu, most_w > kMostWeight)) break;
-                float2 top_w = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int a = 0; a < NG; ++a) {
+                    float2 top_w = make_float2(0.f, 0.f);
 #pragma unroll
-                    for (int a = 0; a < NG; ++a) {
+                    for (int k = 0; k < 4; ++k) {
                         top_w.x = fmaxf(top_w.x, sc[k].x * sv[k][a]);
                         top_w.y = fmaxf(top_w.y, sc[k].y * sv[k][a]);
                     }
-                shrink(top_w);
+                    shrink(a, top_w);
+                }
+                __syncwarp();
+                all_factors(T);
             }
 #pragma unroll
             for (int a = 0; a < NG; ++a)
@@ -935,15 +973,25 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
             raise(top);
             // the weights here are p itself, at most: T is what scaled it to fp16's range so far
             constexpr float kOwn = 1.f / kCode;
-            if (__any_sync(0xffffffffu, T.x > kOwn || T.y > kOwn)) {
-                const float2 t1 = make_float2(fminf(T.x, kOwn), fminf(T.y, kOwn));
-                scale_o(t1.x / T.x, t1.y / T.y);
-                T = t1;
+#pragma unroll
+            for (int a = 0; a < NG; ++a) {
+                const float2 T = factor(a);
+                if (__any_sync(0xffffffffu, T.x > kOwn || T.y > kOwn)) {
+                    const float2 t1 = make_float2(fminf(T.x, kOwn), fminf(T.y, kOwn));
+                    scale_o(a, t1.x / T.x, t1.y / T.y);
+                    set_factor(a, t1);  // (the lanes have met)
+                }
             }
+            __syncwarp();
             const float2 x = __ffma2_rn(top, scale, neg);
             const float2 pr = make_float2(exp2_approx(x.x), exp2_approx(x.y));
             l = __fadd2_rn(l, pr);
-            const uint32_t pt = movmatrix(pack(pr.x * T.x * kCode, pr.y * T.y * kCode));
+            uint32_t pt[NG];
+#pragma unroll
+            for (int a = 0; a < NG; ++a) {
+                const float2 T = factor(a);
+                pt[a] = movmatrix(pack(pr.x * T.x * kCode, pr.y * T.y * kCode));
+            }
 #pragma unroll
             for (int c = 0; c < C::kChunks; ++c) {
                 const uint8_t* v = tile + C::kCodes + 64 * c + 8 * g;
@@ -952,8 +1000,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 // odd channels 16 times as large, as the codes' are
                 auto odd = [](uint32_t lo, uint32_t hi) -> uint32_t { return pack(bf16_hi(lo) * 16.f, bf16_hi(hi) * 16.f); };
                 const uint32_t v1 = odd(x.x, y.x), v3 = odd(x.y, y.y);
-                mma(o[c][0], __byte_perm(x.x, y.x, 0x5410), v1, 0, 0, pt, 0);
-                mma(o[c][1], __byte_perm(x.y, y.y, 0x5410), v3, 0, 0, pt, 0);
+                mma(o[c][0], __byte_perm(x.x, y.x, 0x5410), v1, 0, 0, pt[c / kGroupChunks], 0);
+                mma(o[c][1], __byte_perm(x.y, y.y, 0x5410), v3, 0, 0, pt[c / kGroupChunks], 0);
             }
             if (t.block == 0 && !bad_table(t.b)) {
                 // their rows go into the cache, once per KV head
@@ -1005,11 +1053,12 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 }
                 const int row = 2 * t4 + e;
                 const float f = whole ? 1.f / x : 1.f;
-                const float un = f / (kCode * (e ? T.y : T.x)), odd = 0.0625f * un;
                 // (-inf where the share's keys are all hidden from the row)
                 const float m = (e ? most.y : most.x) == -INFINITY ? -INFINITY : -(e ? neg.y : neg.x);
 #pragma unroll
                 for (int c = 0; c < C::kChunks; ++c) {
+                    const float2 T = factor(c / kGroupChunks);
+                    const float un = f / (kCode * (e ? T.y : T.x)), odd = 0.0625f * un;
                     const float y = add[c / kGroupChunks] * f;
                     const float4 v = make_float4(fmaf(o[c][0][e], un, y), fmaf(o[c][0][2 + e], odd, y),
                                                  fmaf(o[c][1][e], un, y), fmaf(o[c][1][2 + e], odd, y));
@@ -1026,10 +1075,8 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 }
             }
             if (!whole && lane == 0) {
-                Record r;
-                r.t = t;
-                r.valid = at_end ? 2 : 1;
-                records[warp][slot] = r;
+                records[warp][slot] = t;
+                record_kinds[warp][slot] = at_end ? kInRing : kKept;
             }
         }
         __syncwarp();
@@ -1037,7 +1084,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     cp_async_wait<0>();
     constexpr int kElems = kRows * D;
     __syncwarp();
-    if (records[warp][0].valid == 1) {
+    if (record_kinds[warp][0] == kKept) {
         // the first record joins the second one in the ring
         float4* const to = reinterpret_cast<float4*>(ring) + kElems / 4;
 #pragma unroll
@@ -1052,9 +1099,9 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     float2* const part_stats = reinterpret_cast<float2*>(p.part + (size_t)gridDim.x * 2 * kElems);
     unsigned valid, begins;  // of the records; where a row block's first one is
     {
-        const bool have = lane < 2 * kWarps && records[lane / 2][lane & 1].valid;
+        const bool have = lane < 2 * kWarps && record_kinds[lane / 2][lane & 1] != kNoRecord;
         valid = __ballot_sync(0xffffffffu, have);
-        const int hi = have ? records[lane / 2][lane & 1].t.start_hi : 0, lo = have ? records[lane / 2][lane & 1].t.start_lo : 0;
+        const int hi = have ? records[lane / 2][lane & 1].start_hi : 0, lo = have ? records[lane / 2][lane & 1].start_lo : 0;
         const unsigned before = valid & ((1u << lane) - 1);
         const int prev = before ? 31 - __clz(before) : lane;
         const int prev_hi = __shfl_sync(0xffffffffu, hi, prev), prev_lo = __shfl_sync(0xffffffffu, lo, prev);
@@ -1062,7 +1109,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     }
     // the first record's row block may have begun in a CTA before, the last one's may go on
     auto start_of = [&](int i) -> long long {
-        const Item& t = records[i / 2][i & 1].t;
+        const Item& t = records[i / 2][i & 1];
         return ((long long)t.start_hi << 32) | (unsigned)t.start_lo;
     };
     if (begins == 0) return;  // (the whole CTA)
@@ -1070,7 +1117,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     {
         const int i = __ffs(begins) - 1, k = 31 - __clz(begins);
         shared[0] = start_of(i) < from ? i : -1;
-        shared[1] = start_of(k) >= from && start_of(k) + records[k / 2][k & 1].t.tiles > to ? k : -1;
+        shared[1] = start_of(k) >= from && start_of(k) + records[k / 2][k & 1].tiles > to ? k : -1;
     }
     // a warp takes 128 channels of a row block at a time
     constexpr int kUnits = kElems / 128;
@@ -1096,7 +1143,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
             v.x = fmaf(w, y.x, v.x), v.y = fmaf(w, y.y, v.y), v.z = fmaf(w, y.z, v.z), v.w = fmaf(w, y.w, v.w);
         }
         if (i != shared[0] && i != shared[1]) {
-            const Item& t = records[i / 2][i & 1].t;
+            const Item& t = records[i / 2][i & 1];
             const float f = 1.f / sum;
             store_row<D>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
             if (x % D == 0) store_lse(p, t, bad_table(t.b), row, top, sum);
@@ -1114,7 +1161,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
     for (int k = 0; k < 2; ++k) {
         if (shared[k] < 0) continue;
         c0[k] = (int)(start_of(shared[k]) / share);
-        pieces[k] = (int)((start_of(shared[k]) + records[shared[k] / 2][shared[k] & 1].t.tiles - 1) / share) - c0[k] + 1;
+        pieces[k] = (int)((start_of(shared[k]) + records[shared[k] / 2][shared[k] & 1].tiles - 1) / share) - c0[k] + 1;
     }
     __syncthreads();
     if (tid == 0) {
@@ -1166,7 +1213,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 v.x = fmaf(w, y[e].x, v.x), v.y = fmaf(w, y[e].y, v.y), v.z = fmaf(w, y[e].z, v.z), v.w = fmaf(w, y[e].w, v.w);
             }
         }
-        const Item& t = records[i / 2][i & 1].t;
+        const Item& t = records[i / 2][i & 1];
         const float f = 1.f / sum;
         store_row<D>(p, t, bad_table(t.b), row, x % D, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
         if (x % D == 0) store_lse(p, t, bad_table(t.b), row, top, sum);
@@ -1177,7 +1224,7 @@ template <int D, int NG>
 cudaError_t launch(const Rows4Params& p, int grid, cudaStream_t stream) {
     using C = Cfg<D, NG>;
     constexpr int kSmem = C::kWarps * C::kStages * C::kTileBytes;
-    static_assert(kSmem <= 216 * 1024, "shared memory budget, beside the static part (11 KB)");
+    static_assert(kSmem <= 216 * 1024, "shared memory budget, beside the static part (11 KB at most)");
     static int configured_for[64] = {0};
     int dev = 0;
     cudaGetDevice(&dev);

@@ -101,3 +101,18 @@ def test_a_query_of_zeros_under_any_scale(past):
     c.scale = 1e-20
     c.attend()
     c.check()
+
+
+@pytest.mark.parametrize("d,group", [(128, 64), (128, 32), (64, 32)])
+@pytest.mark.parametrize("power", [-60, -30, -22, 22, 30, 60])
+def test_groups_of_very_different_size(d, group, power):
+    """Values of one group of channels 2^power the size of the others': each group's weights keep their bits."""
+    c = Call(5, [1, 3, 1], [1000, 70, 300], d, hk=2, share=3, group=group)
+    factor = torch.ones(d // group, 1, dtype=torch.float64)
+    factor[-1] = 2.0 ** power
+    scaled(c, 1, factor)
+    c.v[..., -group:] = (c.v[..., -group:].double() * 2.0 ** power).to(torch.bfloat16)
+    c.dev[2].copy_(c.v)
+    c.attend()
+    assert not c.expanded
+    c.check()
