@@ -337,18 +337,18 @@ __global__ void __launch_bounds__(kCopyThreads, 4) expand4_kernel(const Expand4P
             }
         }
         const size_t at = ((size_t)kvh * p.pool_blocks + block) * kBlock4 * D;
-        // Values are rounded to fp16, an eighth of bf16's error, where the block's largest are within
-        // its range with room for smaller ones (below 2^-14 they are off by 2^-25).
+        // Values are rounded to fp16, an eighth of bf16's error, where the largest of every row and group of
+        // the block is within its range, with room for smaller ones (below 2^-14 they are off by 2^-25, which
+        // is 2^-13 of their group's largest then), or 0.
         bool half = false;
         if (h >= Hk) {
-            bool fits = true, large = false;
+            bool fits = true;
 #pragma unroll
             for (int i = 0; i < kPasses; ++i) {
-                const float top = fabsf(bf16_hi(word[i])) + 15.f * bf16_lo(word[i]);
-                fits = fits && top <= 0x1p15f;
-                large = large || top >= 0x1p-12f;
+                const float m = bf16_hi(word[i]), top = fmaxf(fabsf(m), fabsf(fmaf(15.f, bf16_lo(word[i]), m)));
+                fits = fits && (top == 0.f || (top >= 0x1p-12f && top <= 0x1p15f));
             }
-            half = __syncthreads_and(fits) && __syncthreads_or(large);
+            half = __syncthreads_and(fits);
             if (threadIdx.x == 0) p.halves[(size_t)kvh * p.pool_blocks + block] = half;
         }
 #pragma unroll

@@ -116,3 +116,38 @@ def test_groups_of_very_different_size(d, group, power):
     c.attend()
     assert not c.expanded
     c.check()
+
+
+@pytest.mark.parametrize("d,group", [(128, 64), (128, 32), (64, 32)])
+@pytest.mark.parametrize("power", [-40, -26, -22, -12])
+@pytest.mark.parametrize("block", [0, 16])
+def test_chunks_over_groups_of_very_different_size(d, group, power, block):
+    """The tile kernel: values near 1 beside a group near 2^power, which keeps at least bf16's bits.  Queries are
+    large: few keys weigh at all, so that errors do not cancel."""
+    c = Call(6, [400, 1, 129], [700, 129, 128], d, hk=1, share=16, group=group, block=block)
+    factor = torch.ones(d // group, 1, dtype=torch.float64)
+    factor[-1] = 2.0 ** power
+    scaled(c, 1, factor)
+    c.v[..., -group:] = (c.v[..., -group:].double() * 2.0 ** power).to(torch.bfloat16)
+    c.dev[2].copy_(c.v)
+    c.q *= 4
+    c.dev[0].copy_(c.q)
+    c.attend()
+    assert c.expanded
+    c.check(tiles=True, halves=False)
+
+
+@pytest.mark.parametrize("block", [0, 16])
+def test_chunks_over_rows_of_very_different_size(block):
+    """One position in 16 holds values near 2^-26 and scores highest."""
+    c = Call(7, [400, 1, 129], [700, 129, 128], hk=1, share=16, group=32, block=block)
+    rows = torch.arange(c.cache.codes[0].shape[2]) % 16 == 3
+    scaled(c, 1, torch.where(rows, 2.0 ** -26, 1.0)[:, None, None].double())
+    c.q = c.q.abs()
+    c.dev[0].copy_(c.q)
+    up = 30 / (c.q.double().sum(-1).mean() * c.scale)
+    c.cache.params[0][..., 1] = (c.cache.params[0][..., 1].double() + up * rows[:, None]).to(torch.bfloat16)
+    c.params[0][1].copy_(c.cache.params[0])
+    c.attend()
+    assert c.expanded
+    c.check(tiles=True, halves=False)
