@@ -448,10 +448,13 @@ typedef struct pa_cache4 {
  * precision and then quantised into the cache at cache_offsets[b] (after the
  * rotary embedding, if any).  Of pa_options: window, block_table, rope_theta.
  * q, k, v and what the cache stands for are finite and below 2^100 in magnitude.
- * Scores are exact to fp32's rounding; cached values' weights are rounded to fp16
- * (2^-11), and so are the values themselves in long chunks, in tiles of 128 positions in
- * which the largest of every row's groups is 0 or in [2^-12, 2^15] (values below 2^-14 are
- * off by 2^-25 then), else to bf16 (2^-8); new tokens' weights are rounded to bf16.
+ * Sums are fp32.  Few new tokens: scores are exact to fp32's rounding; products of a cached
+ * value's weight and its scale are rounded to fp16, 2^-11 or 2^-32 of the largest of its query
+ * and group of channels so far.  Long chunks: cached keys are rounded to a sum of two bf16 numbers
+ * (2^-17); cached values and their weights to fp16 (2^-11 each, weights or 2^-32 of the query's
+ * largest so far) in tiles of 128 positions in which the largest of every row's groups is 0 or in
+ * [2^-12, 2^15] (values below 2^-14 are off by 2^-25 then), else to bf16 (2^-8 each).  New
+ * tokens' weights are rounded to bf16 (2^-8).  out is rounded once.
  * Positions at or past cache_offsets[b] are not read.  What the call writes (out,
  * lse, the cache) must overlap no other buffer of it.  Under graph capture the
  * stream must already have run a call of at least these sizes.  num_seqs and
