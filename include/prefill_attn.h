@@ -460,10 +460,12 @@ typedef struct pa_cache4 {
  * stream must already have run a call of at least these sizes.  num_seqs and
  * max_cache_len are at most 2^30, and a pool has less than 2^32 rows (num_blocks *
  * n_kv_heads * block_size).
- * Sequences of more than 2048 / n_heads new tokens may be expanded into the stream's
- * workspace: 1 GiB, or less where max_cache_len * num_seqs needs less, or what one
- * sequence of max_cache_len tokens takes where that is more (6 * n_kv_heads *
- * head_dim bytes a token; max_cache_len * n_kv_heads < 2^31 then).
+ * In a call of more than 8192 / n_heads + num_seqs new tokens (2048 / n_heads where num_seqs is 1) the
+ * sequences of more than 2048 / n_heads new tokens are expanded into the stream's workspace, in
+ * order, each that fits in what the ones before leave of it; the others take longer.  Such a call
+ * reserves 1 GiB, or less where max_cache_len * num_seqs needs less, or what one sequence of
+ * max_cache_len tokens takes where that is more (6 * n_kv_heads * head_dim bytes a
+ * token; max_cache_len * n_kv_heads < 2^31 then), whatever its sequences' lengths are.
  */
 pa_status prefill_attn_varlen_cache4(
     const void *q, const void *k, const void *v,

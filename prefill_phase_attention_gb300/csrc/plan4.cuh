@@ -17,10 +17,9 @@ __device__ __forceinline__ int first_block(const Expand4Params& p, const SeqInfo
 
 // Checks the sequences, and lays out the pool (one block of 1024 threads; ends with a barrier).
 __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
-    __shared__ int warp_sums[32], in_use;
+    __shared__ int warp_sums[32], first_out, base_there;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Cache4& c = p.cache;
-    if (tid == 0) in_use = 0;
     // a warp per sequence
     for (int b = warp; b < p.seqs.num_seqs; b += 32) {
         const SeqInfo s = stated_sequence(p.seqs, c.max_cache_len, b);
@@ -38,36 +37,51 @@ __device__ __forceinline__ void plan_expand4(const Expand4Params& p) {
         }
     }
     __syncthreads();
-    int base = 0;  // blocks of the sequences before
+    // In order, each sequence that fits in what is left of the pool: passes over 1024 of them, each of which
+    // takes those before the first that does not fit, and leaves that one out.  (One pass where all fit.)
+    int base = 0;  // blocks given away
     for (int b0 = 0; b0 < p.seqs.num_seqs; b0 += 1024) {
         const int b = b0 + tid;
         SeqInfo s{0, 0, 0, 0};
         if (b < p.seqs.num_seqs) s = p.seqs.checked[b];
-        const bool wanted = s.n > p.few_tokens;
+        bool open = s.n > p.few_tokens, fits = false;
         const int first = first_block(p, s);
-        // (sums past the pool saturate: a sequence's blocks are at most 2^23)
-        int need = wanted ? end_block(s) - first : 0, inc = need;
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc = min(inc + y, 1 << 29);
+        const int need = end_block(s) - first;  // (0: a first prompt)
+        int at = 0;
+        for (;;) {
+            open = open && need <= p.pool_blocks - base;
+            // (sums past the pool saturate: a sequence's blocks are at most 2^23)
+            int end = open ? need : 0;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, end, o);
+                if (lane >= o) end = min(end + y, 1 << 29);
+            }
+            if (lane == 31) warp_sums[warp] = end;
+            if (tid == 0) first_out = 1024;
+            __syncthreads();
+            int before = base;
+            int all = base;
+            for (int w = 0; w < 32; ++w) {
+                if (w < warp) before = min(before + warp_sums[w], 1 << 29);
+                all = min(all + warp_sums[w], 1 << 29);
+            }
+            end = min(before + end, 1 << 29);
+            if (open && end > p.pool_blocks) atomicMin(&first_out, tid);
+            __syncthreads();
+            const int out = first_out;
+            if (open && tid < out) open = false, fits = true, at = end - need;
+            if (tid == out) open = false, base_there = end - need;
+            __syncthreads();
+            base = out < 1024 ? base_there : all;
+            if (out == 1024) break;
         }
-        if (lane == 31) warp_sums[warp] = inc;
-        __syncthreads();
-        int before = base;
-        for (int w = 0; w < 32; ++w) {
-            if (w < warp) before = min(before + warp_sums[w], 1 << 29);
-            base = min(base + warp_sums[w], 1 << 29);
-        }
-        const int at = min(before + inc, 1 << 29) - need;
-        const bool fits = wanted && before + inc < 1 << 29 && at + need <= p.pool_blocks;
         if (b < p.seqs.num_seqs) {
             p.taken[b] = fits;
             p.base[b] = fits ? at * kBlock4 - block_start(s, first) : 0;
         }
-        if (fits) atomicMax(&in_use, at + need);  // (those that fit are the first ones: no gaps)
-        __syncthreads();
     }
-    if (tid == 0) *p.blocks = in_use;
+    if (tid == 0) *p.blocks = base;
+    __syncthreads();
     for (int b = warp; b < p.seqs.num_seqs; b += 32) {
         if (!p.taken[b]) continue;
         const SeqInfo s = p.seqs.checked[b];

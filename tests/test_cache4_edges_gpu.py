@@ -151,3 +151,53 @@ def test_chunks_over_rows_of_very_different_size(block):
     c.attend()
     assert c.expanded
     c.check(tiles=True, halves=False)
+
+
+# ---------------------------------------------------------------------------
+# which way sequences go
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("lens,fit", [
+    ([131000, 131000, 1000, 0], [0, 2, 3]),
+    ([131000, 50000, 131000, 40000, 5000, 3000, 0], [0, 3, 5, 6]),
+    ([0, 131000, 0, 44000, 43000, 600, 500, 0], [0, 1, 2, 4, 5, 7]),  # 1365 - 1024 - 336 - 5 = 0 blocks for the 500
+])
+def test_what_fits_is_expanded_whatever_stands_before_it(lens, fit):
+    """The 1 GiB of expanded blocks holds 1365 of 128 positions of 8 heads: sequences are taken in order as long as
+    they fit in what is left, and a first prompt needs no room.  The tile kernel's bits for a sequence are the
+    same whatever its neighbours; the row kernel's differ.  (Cached positions are 64 blocks over and over.)"""
+    g = torch.Generator().manual_seed(18)
+    hk, d, bs, n, seqs = 8, 128, 16, 400, len(lens)
+    per, own = -(-(max(lens) + n) // bs), n // bs + 2
+    cache = R.Cache(g, 1, (64 + 2 * seqs * own) * bs, hk, d, 128, bs, spare=0)
+    codes, params = [x.cuda() for x in cache.codes], [x.cuda() for x in cache.params]
+    q, k, v = ((torch.randn((seqs * n, hk, d), generator=g) * s).to(torch.bfloat16).cuda() for s in (3, 1, 1))
+    short = [p if b in fit else 0 for b, p in enumerate(lens)]  # (which needs no room)
+    table = torch.randint(0, 64, (seqs, per), generator=g)
+    for b in range(seqs):                        # blocks of its own for what a call writes
+        for i, p in enumerate((short[b], lens[b])):
+            at = torch.arange(p // bs, min(p // bs + own, per))
+            table[b, at] = 64 + (2 * b + i) * own + torch.arange(len(at))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = table.to(**i32)
+
+    def attend(lens):
+        cu, cu_k = [0], [0]
+        for p in lens:
+            cu.append(cu[-1] + n)
+            cu_k.append(cu_k[-1] + n + p)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        c = [x.clone() for x in codes + params]
+        binding.prefill_attn_varlen_cache4(q, k, v, torch.tensor(cu, **i32), torch.tensor(cu_k, **i32), c[0], c[1],
+                                           torch.tensor(lens, **i32), out, lse, cache_k_params=c[2], cache_v_params=c[3],
+                                           block_table=table)
+        assert binding.load().prefill_attn_last_schedule() != 0
+        torch.cuda.synchronize()
+        assert binding.prefill_attn_device_status() == 0
+        return out, lse
+
+    crowded, roomy = attend(lens), attend(short)
+    for got, want in zip(crowded, roomy):
+        assert got.isfinite().all()
+        for b in fit:
+            assert torch.equal(got[b * n:(b + 1) * n], want[b * n:(b + 1) * n]), b
