@@ -1437,7 +1437,10 @@ pa_status read_cache4(const pa_cache4* cache, const Options& o, int head_dim, in
 // D = 128, 32 heads, over 1024 / 8192 / 32768 cached tokens, us: 64 tokens 35 / 78 / 201 and 33 /
 // 113 / 432, 128 tokens 60 / 141 / 391 and 33 / 113 / 465).  The host does not know the lengths:
 // where all rows but one token of each sequence are at most kExcessRows, the row kernel takes
-// every sequence, which costs less than the other way's launches.
+// every sequence.  Past that the rows may be one chunk or many drafts, and a chunk loses more by the row
+// kernel than drafts by the other way's three launches (over 2048 cached tokens, 32/8 heads, us, the
+// row kernel alone and the rule): 64 decode rows and a chunk of 261 tokens 192 and 125, 255
+// and one of 1025 945 and 228; 65 x 5 drafts 99 and 120, 256 x 5 319 and 353.
 constexpr int kFewRows = 2048, kExcessRows = 8192;
 
 // The pool holds at least one sequence of max_cache_len tokens, and up to this many bytes of more.

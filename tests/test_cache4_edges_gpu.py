@@ -1,13 +1,11 @@
 """GPU tests of the 4-bit cache at the edges of its calls' documented range, against the plain 64-bit forms and error
 bounds of tests/cache4_reference.py."""
-import math
-
 import pytest
 import torch
 
 from prefill_phase_attention_gb300 import binding
 from tests import cache4_reference as R
-from tests.test_cache4_gpu import Call, DIMS
+from tests.test_cache4_gpu import Call, DIMS, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -201,3 +199,55 @@ def test_what_fits_is_expanded_whatever_stands_before_it(lens, fit):
         assert got.isfinite().all()
         for b in fit:
             assert torch.equal(got[b * n:(b + 1) * n], want[b * n:(b + 1) * n]), b
+
+
+# ---------------------------------------------------------------------------
+# copies
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("block", [0, 8])
+def test_copies_of_many_sequences(block):
+    """More sequences than a block searches in shared memory, empty ones among them."""
+    g = torch.Generator().manual_seed(19)
+    new = torch.randint(0, 3, (1500,), generator=g).tolist()
+    lens = torch.randint(0, 20, (1500,), generator=g).tolist()
+    c = Call(20, new, lens, 32, hk=2, group=32, block=block)
+    c.write()
+    k, v = torch.empty_like(c.dev[1]), torch.empty_like(c.dev[2])
+    binding.prefill_attn_cache4_read(c.codes[0][1], c.codes[1][1], c.meta[0], c.offsets, k, v, **c.opts)
+    torch.cuda.synchronize()
+    assert binding.prefill_attn_device_status() == 0
+    c.check_cache()
+    c.guards()
+    for got, x in ((k, c.k), (v, c.v)):
+        assert same_bits(got, R.values(*R.quantise(x, 32)).float().to(torch.bfloat16))
+
+
+def test_captured_copies_read_their_metadata_at_replay():
+    c = Call(21, [40, 0, 90, 3], [7, 0, 64, 1], group=64, block=16)
+    k, v = torch.empty_like(c.dev[1]), torch.empty_like(c.dev[2])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def copies():
+        c.write()
+        binding.prefill_attn_cache4_read(c.codes[0][1], c.codes[1][1], c.meta[0], c.offsets, k, v, **c.opts)
+
+    with torch.cuda.stream(side):
+        copies()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            copies()
+        d = Call(22, [1, 90, 2, 40], [100, 0, 31, 64], group=64, block=16, slack=154 + 3 - 104)
+        for a, b in zip(c.codes + c.params, d.codes + d.params):
+            a[1].copy_(b[1])
+        for a, b in zip([*c.dev, *c.meta, c.offsets, c.opts["block_table"]],
+                        [*d.dev, *d.meta, d.offsets, d.opts["block_table"]]):
+            a.copy_(b)
+        graph.replay()
+    side.synchronize()
+    d.codes, d.params = c.codes, c.params
+    d.check_cache()
+    for got, x in ((k, d.k), (v, d.v)):
+        assert same_bits(got, R.values(*R.quantise(x, 64)).float().to(torch.bfloat16))
