@@ -244,7 +244,10 @@ __device__ __forceinline__ uint32_t codes(uint32_t x) {
     return (i >= 2 ? x >> 8 : x) & (i & 1 ? 0x00f000f0u : 0x000f000fu);
 }
 constexpr float kCode = 0x1p-24f;    // unit of a code
-constexpr float kMostT = 0x1p100f;   // largest factor of the weights
+// Largest factor of the weights: scales down to 2^-126 come to 2^-8, and it times a weight of up to
+// 2^9 is finite (infinity times a scale of 0 would be NaN).
+constexpr int kMostLogT = 118;
+constexpr float kMostT = 0x1p118f;
 constexpr float kMostWeight = 0x1p15f;
 
 __device__ __forceinline__ float to_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
@@ -803,7 +806,7 @@ __global__ void __launch_bounds__(Cfg<D, NG>::kThreads, 1) attn_rows4_kernel(con
                 x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 8));
                 x[e] = fmaxf(x[e], __shfl_xor_sync(0xffffffffu, x[e], 16));
                 x[e] = fminf(x[e], 0x1p127f);
-                t[e] = x[e] * t0[e] > kMostWeight ? __int_as_float(min(261 - (__float_as_int(x[e]) >> 23), 227) << 23) : t0[e];
+                t[e] = x[e] * t0[e] > kMostWeight ? __int_as_float(min(261 - (__float_as_int(x[e]) >> 23), 127 + kMostLogT) << 23) : t0[e];
             }
             scale_o(a, t[0] / t0[0], t[1] / t0[1]);
             __syncwarp();

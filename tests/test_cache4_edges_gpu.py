@@ -116,6 +116,44 @@ def test_groups_of_very_different_size(d, group, power):
     c.check()
 
 
+@pytest.mark.parametrize("d,group", DIMS)
+@pytest.mark.parametrize("power", [60, 92])
+def test_new_tokens_of_small_weight_beside_large_cached_values(d, group, power):
+    """Cached keys outweigh the new tokens by 2^-14 to 2^-20 and hold 0 in every group's first channel, which is the new
+    tokens' alone: their weights keep their bits under the factor of the cached ones'."""
+    c = Call(8, [6, 1, 40], [300, 65, 32], d, hk=2, share=2, group=group)
+    c.cache.codes[1][..., ::group // 2] &= 0xf0
+    c.codes[1][1].copy_(c.cache.codes[1])
+    c.cache.params[1][..., 1] = 0
+    scaled(c, 1, 2.0 ** power)
+    c.v = (c.v.double() * 2.0 ** power).to(torch.bfloat16)
+    c.dev[2].copy_(c.v)
+    c.q = c.q.abs()
+    c.dev[0].copy_(c.q)
+    up = 12 / (c.q.double().sum(-1).mean() * c.scale)
+    c.cache.params[0][..., 1] = (c.cache.params[0][..., 1].double() + up).to(torch.bfloat16)
+    c.params[0][1].copy_(c.cache.params[0])
+    c.attend()
+    assert not c.expanded
+    c.check()
+
+
+@pytest.mark.parametrize("d,group", [(128, 128), (128, 32), (32, 32)])
+@pytest.mark.parametrize("new", [[1, 1], [1, 3]])
+@pytest.mark.parametrize("power", [-90, -110, -118])
+def test_tiny_values(d, group, new, power):
+    """Cached values whose scales are near the smallest normal number."""
+    c = Call(9, new, [500, 40], d, hk=2, share=3, group=group)
+    scaled(c, 1, 2.0 ** power)
+    c.v = (c.v.double() * 2.0 ** power).to(torch.bfloat16)
+    c.dev[2].copy_(c.v)
+    c.q *= 4
+    c.dev[0].copy_(c.q)
+    c.attend()
+    assert not c.expanded
+    c.check()
+
+
 @pytest.mark.parametrize("d,group", [(128, 64), (128, 32), (64, 32)])
 @pytest.mark.parametrize("power", [-40, -26, -22, -12])
 @pytest.mark.parametrize("block", [0, 16])
