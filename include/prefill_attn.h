@@ -447,7 +447,8 @@ typedef struct pa_cache4 {
  * and values are what its codes stand for, the new tokens' are used at full
  * precision and then quantised into the cache at cache_offsets[b] (after the
  * rotary embedding, if any).  Of pa_options: window, block_table, rope_theta.
- * q, k, v and what the cache stands for are finite and below 2^100 in magnitude.
+ * q, k, v and what the cache stands for are finite and below 2^80 in magnitude, and products
+ * q . k below 2^100 (weights are up to 2^15 here and sums of up to 2^30 of them fp32).
  * Sums are fp32.  Few new tokens: scores are exact to fp32's rounding; products of a cached
  * value's weight and its scale are rounded to fp16, 2^-11 or 2^-32 of the largest of its query
  * and group of channels so far.  Long chunks: cached keys are rounded to a sum of two bf16 numbers

@@ -189,6 +189,27 @@ def test_chunks_over_rows_of_very_different_size(block):
     c.check(tiles=True, halves=False)
 
 
+
+@pytest.mark.parametrize("nats", [4, 10, 60])
+def test_chunks_over_large_values_of_one_sign(nats):
+    """Values near the largest allowed, all positive, under scores that rise over the maximum of the first tiles: by
+    less than it may fall behind, and by more."""
+    c = Call(10, [700], [9000], 32, hk=1, share=16, group=32)
+    c.q = c.q.abs()
+    c.dev[0].copy_(c.q)
+    up = nats / (c.q.double().sum(-1).mean() * c.scale)
+    later = torch.arange(c.cache.cap) >= 256
+    c.cache.params[0][..., 1] = (c.cache.params[0][..., 1].double() + up * later[:, None]).to(torch.bfloat16)
+    c.params[0][1].copy_(c.cache.params[0])
+    c.cache.params[1][..., 1] = 0
+    scaled(c, 1, 2.0 ** 76)
+    c.v = (c.v.double().abs() * 2.0 ** 76).to(torch.bfloat16)
+    c.dev[2].copy_(c.v)
+    c.attend()
+    assert c.expanded
+    c.check(tiles=True, halves=False)
+
+
 # ---------------------------------------------------------------------------
 # which way sequences go
 # ---------------------------------------------------------------------------
