@@ -2,8 +2,8 @@
 // decode rows, drafts, short chunks.
 //
 // A row block is 8 query rows (token, head of a KV head's group) of a sequence.  (16 rows, which
-// share the expansion of the codes, leave registers for 8 warps: one row of 8192 keys by
-// 64 tokens of 32 heads took 80 us so, 70 with blocks of 8.)
+// share the expansion of the codes, leave registers for 8 warps at d = 128: 8192 keys by 64 tokens
+// of 32 heads took 80 us so, 70 with blocks of 8.)
 // Its keys come in tiles: 32 cached rows, or 8 new tokens (bf16; as many bytes), which
 // follow them.  With a group's parameters (s, m) and codes c the score and output are
 //     q . k_j   = sum_g s_jg (q_g . c_jg) + m_jg sum(q_g)
@@ -35,9 +35,9 @@
 // those of its warps, and the CTA that comes last joins those of the CTAs, in list order
 // whoever it is.
 //
-// 64 rows over 1024 to 16384 tokens (32/8 heads, d = 128, group 32): 146 us, 5.0 TB/s: about
-// 88 % of the copy rate between the list's making, the first tiles' way, the spread of the ends and
-// the joins, which take some 20 us.
+// 64 rows over 1024 to 16384 tokens (32/8 heads, d = 128, group 32): 144 us, 5.0 TB/s: about
+// 88 % of the copy rate between the launch (4 us), the list's making (3), the first tiles' way (5), the
+// spread of the ends (6) and the joins (7).
 #pragma once
 
 #include <cuda_fp16.h>

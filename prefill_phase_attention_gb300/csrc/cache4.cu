@@ -8,7 +8,7 @@
 // positions and table entries are looked up once a block, in shared memory.  A block
 // looks whether its sequences' tables are valid itself: a kernel ahead for that
 // costs a small call more than all of it.  32768 tokens of 32 heads, d = 128, group 128: written in
-// 114 us, read in 114 (6.0 TB/s; the floor at the copy rate is 101).  A lane that finds its rows by
+// 115 us, read in 115 (6.0 TB/s; the floor at the copy rate is 101).  A lane that finds its rows by
 // adding strides, and not anew, brought the first from 164; both 16-byte halves of 32 bytes in one
 // store brought reading 16 x 16384 tokens of 8 heads, group 64, from 236 to 212 (floor 205).
 #include <cuda_fp16.h>
